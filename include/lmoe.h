@@ -442,6 +442,50 @@ int lmoe_backward(const lmoe_dims *dims, const void *packed, const void *packed_
 int lmoe_quantize_e4m3(const void *x, long long rows, int cols, uint8_t *codes, float *scales,
                        void *stream);
 
+/* Element types of the calls below. */
+enum lmoe_type {
+  LMOE_BF16 = 0,
+  LMOE_E4M3 = 1, /* one-byte codes with fp32 scales, the recipe stated at lmoe_dims */
+  LMOE_F32 = 2
+};
+
+/* Residual addition with RMSNorm: the pre-norm of the decoder block that the layer sits in
+ * ([IK3] baseline decoder passage: each sub-layer is wrapped in a residual connection; the
+ * pages give no formula for the block's norm -- this is the one the layer itself uses, over the
+ * hidden width).  For each of `rows` rows of `cols` elements, in fp32:
+ *   total = x + residual;  rstd = 1 / sqrt(mean(total^2) + eps);  y = gamma * total * rstd
+ * with y from the unrounded total.
+ *   x, residual [rows, cols] bf16 (residual NULL: total = x), gamma [cols] fp32;
+ *   y [rows, cols]: y_type LMOE_BF16, or LMOE_E4M3: codes with y_scales [rows] fp32, by the
+ *     recipe of lmoe_quantize_e4m3 from the fp32 y;
+ *   total [rows, cols] bf16 (rounded to nearest) and rstd [rows] fp32: outputs, or NULL.
+ *   ld*: distance between rows in elements (>= cols), any value.  total may be x or residual
+ *   itself, and so may a bf16 y; outputs must not overlap inputs in any other way, nor each other.
+ * Any cols and any alignment to the element size are accepted; 16-byte-aligned rows (8 bytes for
+ * codes) of a multiple of 8 columns, at most 16384, take the fast path.  A row that is not finite
+ * gives what the formulas give.  rows == 0 is a no-op.
+ * Errors: INVALID_ARG (null pointers, sizes, strides, type, misaligned), UNSUPPORTED (rows >= 2^31). */
+int lmoe_add_rmsnorm(const void *x, long long ldx, const void *residual, long long ldr,
+                     const float *gamma, long long rows, int cols, float eps, void *y,
+                     long long ldy, int y_type, float *y_scales, void *total, long long ldt,
+                     float *rstd, void *stream);
+
+/* Its gradients, from dy = dLoss/dy (the bf16 y) and the forward's total and rstd: with
+ * xh = total * rstd and g = dy * gamma,
+ *   dx = rstd * (g - xh * mean(g * xh)) + dtotal     (the gradient of x, and of residual)
+ *   dgamma = sum over the rows of dy * xh
+ * in fp32, dgamma added in a fixed order.
+ *   dy, total, dtotal (NULL: none) [rows, cols] bf16, gamma [cols] and rstd [rows] fp32 in;
+ *   dx [rows, cols] bf16 out (it may be dy or dtotal itself), dgamma [cols] fp32 out, or NULL
+ *   (not wanted; ws is then unused); ws: lmoe_add_rmsnorm_backward_workspace_bytes of device
+ *   scratch, 16-byte aligned.  Strides, widths and alignment as above.  rows == 0 sets dgamma to 0.
+ * Errors: INVALID_ARG, UNSUPPORTED (rows >= 2^31), WORKSPACE_TOO_SMALL. */
+size_t lmoe_add_rmsnorm_backward_workspace_bytes(long long rows, int cols);
+int lmoe_add_rmsnorm_backward(const void *dy, long long ldy, const void *total, long long ldt,
+                              const float *gamma, const float *rstd, const void *dtotal,
+                              long long ldd, long long rows, int cols, void *dx, long long ldx,
+                              float *dgamma, void *ws, size_t ws_bytes, void *stream);
+
 /* Size in bytes of the fixed device array that lmoe_forward_noalloc uses as its workspace. */
 #define LMOE_NOALLOC_SCRATCH_BYTES (24u << 20)
 

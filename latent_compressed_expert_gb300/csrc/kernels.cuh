@@ -219,6 +219,8 @@ int launch_quantize_rows(const __nv_bfloat16* x, int64_t rows, int cols, int64_t
 int launch_pack_tiled_e4m3(uint8_t* dst, float* scales, const __nv_bfloat16* w,
                            const __nv_bfloat16* w_g, const __nv_bfloat16* w_v, int glu, int E,
                            int M_w, int Kd, cudaStream_t stream);
+// out[c] = sum over p < parts of part[p * cols + c], in a fixed order.
+int launch_column_sum(const float* part, int parts, int cols, float* out, cudaStream_t stream);
 int launch_pack(const lmoe_dims& D, const lmoe_weights& w, const PackedLayout& P, uint8_t* base,
                 cudaStream_t stream);
 

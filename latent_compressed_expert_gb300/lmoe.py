@@ -24,6 +24,7 @@ LMOE_ERR_WORKSPACE_TOO_SMALL = 5
 
 # Every symbol the header declares, with its ctypes signature.
 _vp, _i, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+_ll = ctypes.c_longlong
 
 
 class Dims(ctypes.Structure):
@@ -58,6 +59,9 @@ class HostPipe(ctypes.Structure):
                 ("computed", _vp * HOST_PIPE_MAX_DEPTH),
                 ("downloaded", _vp * HOST_PIPE_MAX_DEPTH), ("calls", ctypes.c_ulonglong)]
 
+# enum lmoe_type
+BF16, E4M3, F32 = 0, 1, 2
+
 # enum lmoe_phase
 PHASE_ALL, PHASE_ROUTER, PHASE_EXPERTS = 0, 1, 2
 
@@ -90,6 +94,11 @@ SIGNATURES = {
     "lmoe_ep_dispatch": (_i, [_vp, _i, _i, _i, _i, _vp, _i, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     "lmoe_ep_combine": (_i, [_vp, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _i, _vp, _vp,
                              _vp, _vp]),
+    "lmoe_add_rmsnorm": (_i, [_vp, _ll, _vp, _ll, _vp, _ll, _i, _f, _vp, _ll, _i, _vp, _vp, _ll,
+                              _vp, _vp]),
+    "lmoe_add_rmsnorm_backward_workspace_bytes": (_sz, [_ll, _i]),
+    "lmoe_add_rmsnorm_backward": (_i, [_vp, _ll, _vp, _ll, _vp, _vp, _vp, _ll, _ll, _i, _vp, _ll,
+                                       _vp, _vp, _sz, _vp]),
     "lmoe_load_stats_update": (_i, [_vp, _i, _vp, _vp]),
     "lmoe_route": (_i, [_vp, _vp, _i, _i, _i, _vp, _vp, _vp, _vp]),
     "lmoe_forward": (_i, [ctypes.POINTER(Dims), _vp, _vp, _vp, _vp, _vp, _sz, ctypes.POINTER(IO),
@@ -404,6 +413,103 @@ def gemm_wgrad_bf16(A: torch.Tensor, B: torch.Tensor, stream=None) -> torch.Tens
 
 def last_device_error(workspace: torch.Tensor) -> int:
     return int(load().lmoe_last_device_error(_ptr(workspace)))
+
+
+def _rows(t, dtype, shape, name):
+    """(address, distance between rows) of a 2-D device tensor whose rows are contiguous."""
+    if t.dtype != dtype or tuple(t.shape) != shape:
+        _expect(t, dtype, shape, name)
+    if not t.is_cuda:
+        raise ValueError("lmoe: tensors must be CUDA device tensors")
+    rs, cs = t.stride()
+    if cs != 1 and shape[1] > 1:
+        raise ValueError(f"lmoe: the rows of {name} must be contiguous")
+    return t.data_ptr(), rs if shape[0] > 1 else max(rs, shape[1])
+
+
+def _same_device(dev, *tensors):
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"lmoe: tensors on {dev} and on {t.device}")
+
+
+def _on(dev):
+    """The device's current stream; its device must be the current one."""
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"lmoe: tensors on {dev}, but the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    return torch.cuda.current_stream().cuda_stream
+
+
+def _add_rmsnorm(x, gamma, residual, eps, fp8, train, y, total, stream):
+    rows, cols = x.shape
+    bf, dev = torch.bfloat16, x.device
+    px, ldx = _rows(x, bf, (rows, cols), "x")
+    pr, ldr = (None, 0) if residual is None else _rows(residual, bf, (rows, cols), "residual")
+    _expect(gamma, torch.float32, (cols,), "gamma")
+    if total is None and residual is not None:
+        total = torch.empty((rows, cols), dtype=bf, device=dev)
+    pt, ldt = (None, 0) if total is None else _rows(total, bf, (rows, cols), "total")
+    yt = torch.uint8 if fp8 else bf
+    if y is None:
+        y = torch.empty((rows, cols), dtype=yt, device=dev)
+    py, ldy = _rows(y, yt, (rows, cols), "y")
+    scales = torch.empty(rows, dtype=torch.float32, device=dev) if fp8 else None
+    rstd = torch.empty(rows, dtype=torch.float32, device=dev) if train else None
+    _same_device(dev, gamma, residual, total, y)
+    st = _on(dev) if stream is None else stream.cuda_stream
+    _check(load().lmoe_add_rmsnorm(px, ldx, pr, ldr, _ptr(gamma), rows, cols, eps, py, ldy,
+                                   E4M3 if fp8 else BF16, _ptr(scales), pt, ldt, _ptr(rstd), st),
+           "lmoe_add_rmsnorm")
+    return y, scales, x if total is None else total, rstd
+
+
+def add_rmsnorm(x: torch.Tensor, gamma: torch.Tensor, residual: torch.Tensor | None = None,
+                eps: float = 1e-6, train: bool = False, y=None, total=None, stream=None):
+    """Residual addition with RMSNorm (lmoe_add_rmsnorm): x and residual [rows, cols] bf16
+    (rows contiguous, at any stride), gamma [cols] fp32 -> (y, total), or with train
+    (y, total, rstd) for add_rmsnorm_backward.  total is x + residual in bf16 (x itself
+    without a residual); ``y`` and ``total`` may be given, and may be x or residual."""
+    y, _, total, rstd = _add_rmsnorm(x, gamma, residual, eps, False, train, y, total, stream)
+    return (y, total, rstd) if train else (y, total)
+
+
+def add_rmsnorm_e4m3(x: torch.Tensor, gamma: torch.Tensor, residual: torch.Tensor | None = None,
+                     eps: float = 1e-6, total=None, stream=None):
+    """add_rmsnorm with y as e4m3 codes (uint8) and one fp32 scale per row:
+    (codes, scales, total)."""
+    return _add_rmsnorm(x, gamma, residual, eps, True, False, None, total, stream)[:3]
+
+
+def add_rmsnorm_backward(dy: torch.Tensor, total: torch.Tensor, gamma: torch.Tensor,
+                         rstd: torch.Tensor, dtotal: torch.Tensor | None = None,
+                         want_dgamma: bool = True, dx=None, stream=None):
+    """Gradients of add_rmsnorm (lmoe_add_rmsnorm_backward): dy, and dtotal (the gradient that
+    reaches total itself, or None), [rows, cols] bf16 -> (dx bf16, dgamma fp32 or None); dx is
+    the gradient of x and of residual."""
+    rows, cols = dy.shape
+    bf, f, dev = torch.bfloat16, torch.float32, dy.device
+    pd, ldy = _rows(dy, bf, (rows, cols), "dy")
+    pt, ldt = _rows(total, bf, (rows, cols), "total")
+    pe, lde = (None, 0) if dtotal is None else _rows(dtotal, bf, (rows, cols), "dtotal")
+    _expect(gamma, f, (cols,), "gamma")
+    _expect(rstd, f, (rows,), "rstd")
+    if dx is None:
+        dx = torch.empty((rows, cols), dtype=bf, device=dev)
+    po, ldo = _rows(dx, bf, (rows, cols), "dx")
+    lib = load()
+    dgamma = ws = None
+    nb = 0
+    if want_dgamma:
+        dgamma = torch.empty(cols, dtype=f, device=dev)
+        nb = lib.lmoe_add_rmsnorm_backward_workspace_bytes(rows, cols)
+        ws = torch.empty(nb, dtype=torch.uint8, device=dev)
+    _same_device(dev, total, gamma, rstd, dtotal, dx)
+    st = _on(dev) if stream is None else stream.cuda_stream
+    _check(lib.lmoe_add_rmsnorm_backward(pd, ldy, pt, ldt, _ptr(gamma), _ptr(rstd), pe, lde, rows,
+                                         cols, po, ldo, _ptr(dgamma), _ptr(ws), nb, st),
+           "lmoe_add_rmsnorm_backward")
+    return dx, dgamma
 
 
 class Layer:
