@@ -486,6 +486,61 @@ int lmoe_add_rmsnorm_backward(const void *dy, long long ldy, const void *total, 
                               long long ldd, long long rows, int cols, void *dx, long long ldx,
                               float *dgamma, void *ws, size_t ws_bytes, void *stream);
 
+/* Linear layers with a fused epilogue, for the dense projections around the layer ([IK3]
+ * baseline decoder passage: the dense FFN that the experts replace, and the block's other
+ * projections; the pages give no formulas):
+ *   p = x . w^T (times x_scales[m] * w_scales[n] for e4m3) + bias;   y = act(p) + residual
+ * with fp32 accumulation in TMEM and one rounding of y to bf16.
+ *   act  LMOE_ACT_NONE; _SILU p * sigmoid(p); _GELU p * Phi(p), Phi the normal distribution
+ *        function; _SITU the layer's gated activation: w [2N, K] and bias [2N] hold the N gate
+ *        rows, then the N value rows, and y = SiTU(p[:, n], p[:, N + n]) with cap c.
+ * Below, rows = N, or 2N with LMOE_ACT_SITU. */
+enum lmoe_act { LMOE_ACT_NONE = 0, LMOE_ACT_SILU = 1, LMOE_ACT_GELU = 2, LMOE_ACT_SITU = 3 };
+
+typedef struct lmoe_linear {
+  int M, N, K;            /* rows of x, output features, input features */
+  int act;                /* enum lmoe_act */
+  int type;               /* of x and w: LMOE_BF16, or LMOE_E4M3 codes (forward only) */
+  float c;                /* SiTU-GLU cap (LMOE_ACT_SITU) */
+  const void *x;          /* [M, K], rows ldx elements apart */
+  long long ldx;
+  const float *x_scales;  /* [M] (e4m3) */
+  const void *w;          /* [rows, K], rows ldw elements apart */
+  long long ldw;
+  const float *w_scales;  /* [rows] (e4m3) */
+  const float *bias;      /* [rows] fp32, or NULL */
+  const void *residual;   /* [M, N] bf16, rows ldr elements apart, or NULL */
+  long long ldr;
+  void *y;                /* [M, N] bf16 out, rows ldy elements apart; may be residual itself */
+  long long ldy;
+  void *pre;              /* [M, rows] bf16: the pre-activations p, rounded, rows ldp elements
+                             apart: written by the forward (NULL: not kept), read by the backward */
+  long long ldp;
+  uint32_t *dev_flag;     /* one caller-owned device word, zeroed before its first use; receives
+                             the error bits of a device-side wait that ran out */
+} lmoe_linear;
+
+/* The layer's output y (and pre).  N a multiple of 8, K of 8 (16 for e4m3); x, w, residual, y and
+ * pre 16-byte aligned with row distances in whole 16 bytes.  y and pre overlap no input (y may be
+ * residual itself).  M == 0 is a no-op.
+ * Errors: INVALID_ARG, UNSUPPORTED (N, K; 2^27 or more 64 x 64 tiles), CUDA. */
+int lmoe_linear_forward(const lmoe_linear *p, void *stream);
+
+/* Its gradients, given dy = dLoss/dy [M, N] bf16 (rows lddy elements apart) and the forward's
+ * x, w and (unless act is LMOE_ACT_NONE) pre; y, residual and bias are not read:
+ *   dp = dy * act'(pre), rounded to bf16 as the products' operand (act NONE: dp = dy, exact);
+ *   dx [M, K] bf16 = dp . w;  dw [rows, K] = dp^T . x, dw_type LMOE_BF16 or LMOE_F32;
+ *   dbias [rows] fp32 = column sums of dp before its rounding, in a fixed order.
+ * The residual's gradient is dy.  Any of dx, dw, dbias may be NULL (not wanted).  bf16 layers
+ * only.  ws: lmoe_linear_backward_workspace_bytes(p) of device scratch, 16-byte aligned; not
+ * needed when act is LMOE_ACT_NONE and dbias is NULL.  M == 0 zeroes dw and dbias.  Alignment as
+ * above; dw rows are K apart.
+ * Errors: INVALID_ARG, UNSUPPORTED (also LMOE_E4M3), WORKSPACE_TOO_SMALL, CUDA. */
+size_t lmoe_linear_backward_workspace_bytes(const lmoe_linear *p);
+int lmoe_linear_backward(const lmoe_linear *p, const void *dy, long long lddy, void *dx,
+                         long long lddx, void *dw, int dw_type, float *dbias, void *ws,
+                         size_t ws_bytes, void *stream);
+
 /* Size in bytes of the fixed device array that lmoe_forward_noalloc uses as its workspace. */
 #define LMOE_NOALLOC_SCRATCH_BYTES (24u << 20)
 

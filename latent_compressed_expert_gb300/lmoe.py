@@ -59,6 +59,16 @@ class HostPipe(ctypes.Structure):
                 ("computed", _vp * HOST_PIPE_MAX_DEPTH),
                 ("downloaded", _vp * HOST_PIPE_MAX_DEPTH), ("calls", ctypes.c_ulonglong)]
 
+class LinearDesc(ctypes.Structure):
+    _fields_ = [("M", _i), ("N", _i), ("K", _i), ("act", _i), ("type", _i), ("c", _f),
+                ("x", _vp), ("ldx", _ll), ("x_scales", _vp), ("w", _vp), ("ldw", _ll),
+                ("w_scales", _vp), ("bias", _vp), ("residual", _vp), ("ldr", _ll), ("y", _vp),
+                ("ldy", _ll), ("pre", _vp), ("ldp", _ll), ("dev_flag", _vp)]
+
+
+# enum lmoe_act
+ACTS = {"none": 0, "silu": 1, "gelu": 2, "situ": 3}
+
 # enum lmoe_type
 BF16, E4M3, F32 = 0, 1, 2
 
@@ -99,6 +109,9 @@ SIGNATURES = {
     "lmoe_add_rmsnorm_backward_workspace_bytes": (_sz, [_ll, _i]),
     "lmoe_add_rmsnorm_backward": (_i, [_vp, _ll, _vp, _ll, _vp, _vp, _vp, _ll, _ll, _i, _vp, _ll,
                                        _vp, _vp, _sz, _vp]),
+    "lmoe_linear_forward": (_i, [_vp, _vp]),
+    "lmoe_linear_backward_workspace_bytes": (_sz, [_vp]),
+    "lmoe_linear_backward": (_i, [_vp, _vp, _ll, _vp, _ll, _vp, _i, _vp, _vp, _sz, _vp]),
     "lmoe_load_stats_update": (_i, [_vp, _i, _vp, _vp]),
     "lmoe_route": (_i, [_vp, _vp, _i, _i, _i, _vp, _vp, _vp, _vp]),
     "lmoe_forward": (_i, [ctypes.POINTER(Dims), _vp, _vp, _vp, _vp, _vp, _sz, ctypes.POINTER(IO),
@@ -424,7 +437,7 @@ def _rows(t, dtype, shape, name):
     rs, cs = t.stride()
     if cs != 1 and shape[1] > 1:
         raise ValueError(f"lmoe: the rows of {name} must be contiguous")
-    return t.data_ptr(), rs if shape[0] > 1 else max(rs, shape[1])
+    return t.data_ptr(), rs if shape[0] > 1 else shape[1]
 
 
 def _same_device(dev, *tensors):
@@ -510,6 +523,112 @@ def add_rmsnorm_backward(dy: torch.Tensor, total: torch.Tensor, gamma: torch.Ten
                                          cols, po, ldo, _ptr(dgamma), _ptr(ws), nb, st),
            "lmoe_add_rmsnorm_backward")
     return dx, dgamma
+
+
+class Linear:
+    """A linear layer with a fused epilogue (lmoe_linear_forward / _backward):
+    y = act(x w^T + bias) + residual.
+
+    w [N, K] bf16, or e4m3 codes (uint8) with fp32 ``w_scales`` [N] (forward only); bias [N] fp32
+    or None; act "none", "silu", "gelu" or "situ" (then w, bias and w_scales hold the N gate rows,
+    then the N value rows, and c is the cap).  The layer keeps references, not copies: an
+    optimizer may update w and bias in place.  N must be a multiple of 8, K of 8 (e4m3: 16)."""
+
+    def __init__(self, w: torch.Tensor, bias: torch.Tensor | None = None, act: str = "none",
+                 w_scales: torch.Tensor | None = None, c: float = 100.0):
+        if act not in ACTS:
+            raise ValueError(f"lmoe: unknown activation {act!r}")
+        rows, K = w.shape
+        if act == "situ" and rows % 2:
+            raise ValueError("lmoe: a gated layer needs as many value rows as gate rows")
+        self.fp8 = w.dtype == torch.uint8
+        if self.fp8 != (w_scales is not None):
+            raise ValueError("lmoe: e4m3 codes (uint8) and w_scales go together")
+        self.w, self.bias, self.w_scales, self.act, self.c = w, bias, w_scales, act, c
+        self.rows, self.K, self.N = rows, K, rows // 2 if act == "situ" else rows
+        self.device = w.device
+        self._dtype = torch.uint8 if self.fp8 else torch.bfloat16
+        self._pw, self._ldw = _rows(w, self._dtype, (rows, K), "w")
+        f = torch.float32
+        for t, name in ((bias, "bias"), (w_scales, "w_scales")):
+            if t is not None:
+                _expect(t, f, (rows,), name)
+        self._pb, self._pws = _ptr(bias), _ptr(w_scales)
+        _same_device(w.device, bias, w_scales)
+        self.flag = torch.zeros(1, dtype=torch.int32, device=w.device)
+        self._pflag = self.flag.data_ptr()
+
+    def _desc(self, M, px, ldx):
+        return LinearDesc(M, self.N, self.K, ACTS[self.act], E4M3 if self.fp8 else BF16, self.c,
+                          px, ldx, None, self._pw, self._ldw, self._pws, self._pb, None, 0, None,
+                          0, None, 0, self._pflag)
+
+    def forward(self, x: torch.Tensor, residual: torch.Tensor | None = None,
+                x_scales: torch.Tensor | None = None, train: bool = False, y=None, stream=None):
+        """x [M, K] bf16 (or e4m3 codes with x_scales [M]), residual [M, N] bf16 -> y [M, N] bf16;
+        with train, (y, pre), the bf16 pre-activations that ``backward`` needs (None without an
+        activation).  Rows at any stride of whole 16 bytes.  ``y`` may be given (or be residual)."""
+        M = x.shape[0]
+        bf = torch.bfloat16
+        px, ldx = _rows(x, self._dtype, (M, self.K), "x")
+        d = self._desc(M, px, ldx)
+        if self.fp8:
+            if x_scales is None:
+                raise ValueError("lmoe: e4m3 rows need x_scales")
+            _expect(x_scales, torch.float32, (M,), "x_scales")
+            d.x_scales = _ptr(x_scales)
+        elif x_scales is not None:
+            raise ValueError("lmoe: x_scales belong to e4m3 rows")
+        if residual is not None:
+            d.residual, d.ldr = _rows(residual, bf, (M, self.N), "residual")
+        if y is None:
+            y = torch.empty((M, self.N), dtype=bf, device=self.device)
+        d.y, d.ldy = _rows(y, bf, (M, self.N), "y")
+        pre = None
+        if train and self.act != "none":
+            pre = torch.empty((M, self.rows), dtype=bf, device=self.device)
+            d.pre, d.ldp = pre.data_ptr(), self.rows
+        _same_device(self.device, x, residual, x_scales, y)
+        st = _on(self.device) if stream is None else stream.cuda_stream
+        _check(load().lmoe_linear_forward(ctypes.byref(d), st), "lmoe_linear_forward")
+        return (y, pre) if train else y
+
+    def backward(self, x: torch.Tensor, dy: torch.Tensor, pre: torch.Tensor | None = None,
+                 dw_dtype=torch.float32, want_dx: bool = True, want_dw: bool = True,
+                 stream=None) -> dict:
+        """Gradients for the x and pre of a ``forward(train=True)``: dy [M, N] bf16 -> dx [M, K]
+        bf16, dw (fp32, or bf16 with dw_dtype) and, when the layer has a bias, dbias fp32.  The
+        residual's gradient is dy itself."""
+        M = dy.shape[0]
+        bf, f, dev = torch.bfloat16, torch.float32, self.device
+        if self.fp8:
+            raise LmoeError(LMOE_ERR_UNSUPPORTED, "lmoe_linear_backward")
+        if dw_dtype not in (bf, f):
+            raise ValueError("lmoe: dw_dtype must be torch.float32 or torch.bfloat16")
+        px, ldx = _rows(x, bf, (M, self.K), "x")
+        pd, ldd = _rows(dy, bf, (M, self.N), "dy")
+        d = self._desc(M, px, ldx)
+        if self.act != "none":
+            if pre is None:
+                raise ValueError("lmoe: this layer's backward needs the forward's pre")
+            d.pre, d.ldp = _rows(pre, bf, (M, self.rows), "pre")
+        dx = torch.empty((M, self.K), dtype=bf, device=dev) if want_dx else None
+        dw = torch.empty((self.rows, self.K), dtype=dw_dtype, device=dev) if want_dw else None
+        db = None if self.bias is None else torch.empty(self.rows, dtype=f, device=dev)
+        lib = load()
+        nb = lib.lmoe_linear_backward_workspace_bytes(ctypes.byref(d))
+        ws = torch.empty(nb, dtype=torch.uint8, device=dev)
+        _same_device(dev, x, dy, pre)
+        st = _on(dev) if stream is None else stream.cuda_stream
+        _check(lib.lmoe_linear_backward(ctypes.byref(d), pd, ldd, _ptr(dx), self.K, _ptr(dw),
+                                        F32 if dw_dtype == f else BF16, _ptr(db), _ptr(ws), nb,
+                                        st), "lmoe_linear_backward")
+        return {"dx": dx, "dw": dw, "dbias": db}
+
+    def device_error(self) -> int:
+        """LMOE_OK, or LMOE_ERR_DEVICE_TIMEOUT if a device-side wait of an earlier call ran out
+        (its output is not valid); call after the stream has synchronised.  Clears the flag."""
+        return last_device_error(self.flag)
 
 
 class Layer:
