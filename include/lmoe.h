@@ -442,6 +442,33 @@ int lmoe_backward(const lmoe_dims *dims, const void *packed, const void *packed_
 int lmoe_quantize_e4m3(const void *x, long long rows, int cols, uint8_t *codes, float *scales,
                        void *stream);
 
+/* The whole layer for a few tokens (decode), in one kernel: the time lmoe_forward spends between
+ * its kernels is what a batch this small is made of.  Arguments as lmoe_forward, with its own
+ * workspace and these differences:
+ *   - at most LMOE_FEW_MAX_TOKENS tokens;
+ *   - routing is against given thresholds (io->tau_in) or none: io NULL, or io->balance 0.
+ *     In-batch thresholds of a few tokens carry no quantile (balance 1 without tau_in is refused);
+ *   - of the other io fields, logits_in, logit_bias, logits_out, idx_out, gate_out and y_f32_out
+ *     are served; tau_out, counts_out, load_stats, tau_ema, save_pre, save_pre_shared, stage_events,
+ *     cand_out and phases are refused; aux_stream, aux_events and shared_sms have no meaning here;
+ *   - the latent is kept in fp32, for the router and the experts (lmoe_forward rounds it to
+ *     bf16), and so are the experts' outputs; hs, h and gamma * u are rounded to bf16 as
+ *     operands, e4m3 experts quantise the latent and h from fp32.  So the two calls agree within
+ *     the layer's tolerance, and route alike up to ties that the latent's rounding decides.
+ *   - workspace: lmoe_few_workspace_bytes, 256-byte aligned, its first 256 bytes zeroed once
+ *     before the first call (a call leaves them as it found them, error flag aside).  Calls on one
+ *     workspace must not overlap.  It serves every smaller batch of the same layer too.
+ * The kernel is a cooperative launch of one CTA per SM that wait on one another; every wait is
+ * bounded, and lmoe_last_device_error reads the workspace's flag.  It may be captured into a graph.
+ * Supported: lmoe_forward's shapes whose operands fit the shared memory of an SM (about 227 KB
+ * less 64 KB for weights in flight: K3 at 8 tokens does).  T == 0 is a no-op.
+ * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE_TOO_SMALL, CUDA. */
+#define LMOE_FEW_MAX_TOKENS 8
+size_t lmoe_few_workspace_bytes(const lmoe_dims *dims);
+int lmoe_forward_few(const lmoe_dims *dims, const void *packed, const void *x,
+                     const void *residual, void *y, void *workspace, size_t ws_bytes, lmoe_io *io,
+                     void *stream);
+
 /* Element types of the calls below. */
 enum lmoe_type {
   LMOE_BF16 = 0,

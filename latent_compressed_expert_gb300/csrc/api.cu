@@ -59,7 +59,7 @@ static bool dims_ok(const lmoe_dims* D) {
   return true;
 }
 
-static int dims_supported(const lmoe_dims* D) {
+int dims_supported(const lmoe_dims* D) {
   if (!dims_ok(D)) return LMOE_ERR_INVALID_ARG;
   if (D->d % 64 || D->L % 64 || D->I % 64) return LMOE_ERR_UNSUPPORTED;
   if (D->S > 0 && (D->Is <= 0 || D->Is % 64)) return LMOE_ERR_UNSUPPORTED;
@@ -152,7 +152,7 @@ WorkspaceLayout workspace_layout(const lmoe_dims& D) {
 
 static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-static uint64_t wait_limit_ns() {
+uint64_t wait_limit_ns() {
   // Upper bound of any single device-side wait.  Legitimate waits last microseconds.
   const char* s = getenv("LMOE_WAIT_LIMIT_MS");
   if (s && *s) {
@@ -165,7 +165,7 @@ static uint64_t wait_limit_ns() {
 // Test hook: LMOE_FAULT_INJECT=stall makes the first GEMM of each call wait on a barrier
 // that nothing arrives on, so the bounded-wait error path can be exercised without any
 // fault.  Read at every call.
-static bool inject_stall() {
+bool inject_stall() {
   const char* s = getenv("LMOE_FAULT_INJECT");
   return s && strcmp(s, "stall") == 0;
 }

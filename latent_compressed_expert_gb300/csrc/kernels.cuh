@@ -26,6 +26,11 @@ struct WorkspaceLayout {
 };
 
 PackedLayout packed_layout(const lmoe_dims& D);
+// The layer's sizes: LMOE_OK, or why they are refused.
+int dims_supported(const lmoe_dims* D);
+// The bound of a device-side wait and the test hook, read from the environment at each call.
+uint64_t wait_limit_ns();
+bool inject_stall();
 WorkspaceLayout workspace_layout(const lmoe_dims& D);
 // lmoe_forward's argument checks for T > 0 (LMOE_OK, or the status it would return).
 int forward_args_check(const lmoe_dims* dims, const void* packed, const void* x,
@@ -139,6 +144,7 @@ int launch_grouped_gemm(const void* W, const void* X, uint64_t x_rows, int x_ld,
 // 64 x box_rows box and the 128-byte swizzle.  Returns false on failure.
 bool make_tmap_bf16(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols, uint64_t ld,
                     uint32_t box_rows);
+bool make_tmap_glu8(CUtensorMap* m, const void* ptr, uint64_t groups, uint64_t cols, uint64_t ld);
 bool make_tmap_bf16_out32(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols,
                           uint64_t ld);
 

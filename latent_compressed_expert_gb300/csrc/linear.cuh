@@ -777,8 +777,7 @@ int launch_linear(const LinearOperand& A, const LinearOperand& B, const LinearAr
 
 // The checks of a linear layer's arguments that its forward and backward share.
 int linear_sizes_ok(const lmoe_linear* p);
-// Sets the fields that every launch needs: the wait limit and the test hook, both read from the
-// environment at each call as the layer's are (LMOE_WAIT_LIMIT_MS, LMOE_FAULT_INJECT).
+// Sets the fields that every launch needs.
 void linear_common(const lmoe_linear* p, LinearArgs* g);
 
 }  // namespace lmoe

@@ -1,7 +1,4 @@
 // linear_fwd.cu -- linear layers: y = act(x w^T + bias) + residual (kernels in linear.cuh).
-#include <stdlib.h>
-#include <string.h>
-
 #include "linear.cuh"
 
 namespace lmoe {
@@ -43,14 +40,8 @@ LinearPlan linear_plan(int R, int C, int D, bool fp8, bool glu, int sms) {
 
 void linear_common(const lmoe_linear* p, LinearArgs* g) {
   g->err = p->dev_flag;
-  g->timeout_ns = 2000ull * 1000000ull;
-  const char* s = getenv("LMOE_WAIT_LIMIT_MS");
-  if (s && *s) {
-    const long v = strtol(s, nullptr, 10);
-    if (v > 0 && v < 60000) g->timeout_ns = static_cast<unsigned long long>(v) * 1000000ull;
-  }
-  s = getenv("LMOE_FAULT_INJECT");
-  g->inject_stall = s && strcmp(s, "stall") == 0;
+  g->timeout_ns = wait_limit_ns();
+  g->inject_stall = inject_stall();
   g->c = p->act == LMOE_ACT_SITU ? p->c : 1.0f;
 }
 

@@ -49,6 +49,7 @@ class IO(ctypes.Structure):
 
 
 OVERLAP_MIN_T = 512  # LMOE_OVERLAP_MIN_T
+FEW_MAX_TOKENS = 8  # LMOE_FEW_MAX_TOKENS
 HOST_PIPE_MAX_DEPTH = 4  # LMOE_HOST_PIPE_MAX_DEPTH
 
 
@@ -112,6 +113,9 @@ SIGNATURES = {
     "lmoe_linear_forward": (_i, [_vp, _vp]),
     "lmoe_linear_backward_workspace_bytes": (_sz, [_vp]),
     "lmoe_linear_backward": (_i, [_vp, _vp, _ll, _vp, _ll, _vp, _i, _vp, _vp, _sz, _vp]),
+    "lmoe_few_workspace_bytes": (_sz, [ctypes.POINTER(Dims)]),
+    "lmoe_forward_few": (_i, [ctypes.POINTER(Dims), _vp, _vp, _vp, _vp, _vp, _sz,
+                              ctypes.POINTER(IO), _vp]),
     "lmoe_load_stats_update": (_i, [_vp, _i, _vp, _vp]),
     "lmoe_route": (_i, [_vp, _vp, _i, _i, _i, _vp, _vp, _vp, _vp]),
     "lmoe_forward": (_i, [ctypes.POINTER(Dims), _vp, _vp, _vp, _vp, _vp, _sz, ctypes.POINTER(IO),
@@ -650,6 +654,7 @@ class Layer:
         self.packed = pack_weights(self.dims, weights, stream)
         self.ws_bytes = workspace_bytes(self.dims)
         self.workspace = torch.empty(self.ws_bytes, dtype=torch.uint8, device=self.device)
+        self.few_ws = None  # forward_few's, allocated by its first call
         self.overlap = overlap
         self.shared_sms = shared_sms
         self.aux_stream = torch.cuda.Stream(device=self.device) if overlap else None
@@ -759,6 +764,70 @@ class Layer:
         if phase == PHASE_ROUTER:
             return (cand, dbg) if debug else cand
         return (y, dbg) if debug else y
+
+    def forward_few(self, x: torch.Tensor, residual: torch.Tensor | None = None, y=None,
+                    tau: torch.Tensor | None = None, logits_in: torch.Tensor | None = None,
+                    logit_bias: torch.Tensor | None = None, debug: bool = False, stream=None):
+        """The layer on at most FEW_MAX_TOKENS tokens in one kernel (lmoe_forward_few), routed
+        against thresholds ``tau`` (e.g. a prefill batch's) or none.  Arguments and debug outputs
+        (logits, idx, gate, y_f32) as ``forward``'s.  The first call allocates a workspace of its
+        own for up to min(max_tokens, FEW_MAX_TOKENS) tokens; make it before capturing a graph."""
+        sh = self.shape
+        T = x.shape[0]
+        bf, f = torch.bfloat16, torch.float32
+        lib = load()
+        if self.few_ws is None:
+            self._few_dims = [dims_of(sh, T=t, expert_fp8=self.expert_fp8)
+                              for t in range(min(self.max_tokens, FEW_MAX_TOKENS) + 1)]
+            sizes = [int(lib.lmoe_few_workspace_bytes(ctypes.byref(D))) for D in self._few_dims]
+            while len(sizes) > 1 and sizes[-1] == 0:  # operands too wide for an SM's shared memory
+                sizes.pop()
+            if sizes[-1] == 0:
+                raise LmoeError(LMOE_ERR_UNSUPPORTED, "lmoe_few_workspace_bytes")
+            self._few_dims = self._few_dims[:len(sizes)]
+            # zeroed before any stream of the caller's uses it
+            self.few_ws = torch.zeros(sizes[-1], dtype=torch.uint8, device=self.device)
+            torch.cuda.current_stream(self.device).synchronize()
+        if T >= len(self._few_dims):
+            raise ValueError(f"lmoe: {T} tokens exceed forward_few's {len(self._few_dims) - 1}")
+        dims = self._few_dims[T]
+        _expect(x, bf, (T, sh.d), "x")
+        if residual is not None:
+            _expect(residual, bf, (T, sh.d), "residual")
+        if y is None:
+            y = torch.empty((T, sh.d), dtype=bf, device=x.device)
+        else:
+            _expect(y, bf, (T, sh.d), "y")
+        io = IO()
+        if tau is not None:
+            _expect(tau, f, (sh.E,), "tau")
+            io.tau_in = _ptr(tau)
+        if logits_in is not None:
+            _expect(logits_in, f, (T, sh.E), "logits_in")
+            io.logits_in = _ptr(logits_in)
+        if logit_bias is not None:
+            _expect(logit_bias, f, (sh.E,), "logit_bias")
+            io.logit_bias = _ptr(logit_bias)
+        dbg = {}
+        if debug:
+            dev = x.device
+            dbg = {"logits": torch.empty((T, sh.E), dtype=f, device=dev),
+                   "idx": torch.empty((T, sh.K), dtype=torch.int32, device=dev),
+                   "gate": torch.empty((T, sh.K), dtype=f, device=dev),
+                   "y_f32": torch.empty((T, sh.d), dtype=f, device=dev)}
+            io.logits_out, io.idx_out = _ptr(dbg["logits"]), _ptr(dbg["idx"])
+            io.gate_out, io.y_f32_out = _ptr(dbg["gate"]), _ptr(dbg["y_f32"])
+        _same_device(self.device, x, residual, y, tau, logits_in, logit_bias)
+        st = _on(self.device) if stream is None else stream.cuda_stream
+        _check(lib.lmoe_forward_few(ctypes.byref(dims), _ptr(self.packed), _ptr(x), _ptr(residual),
+                                    _ptr(y), _ptr(self.few_ws), self.few_ws.numel(),
+                                    ctypes.byref(io), st), "lmoe_forward_few")
+        self.last_kernel_launches = io.kernel_launches
+        return (y, dbg) if debug else y
+
+    def few_device_error(self) -> int:
+        """device_error of forward_few's workspace (call after the stream has synchronised)."""
+        return LMOE_OK if self.few_ws is None else last_device_error(self.few_ws)
 
     def forward_global(self, x: torch.Tensor, residual: torch.Tensor | None = None, y=None,
                        group=None, global_tokens: int | None = None, debug: bool = False,
