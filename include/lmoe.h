@@ -451,12 +451,12 @@ int lmoe_quantize_e4m3(const void *x, long long rows, int cols, uint8_t *codes, 
  *   - of the other io fields, logits_in, logit_bias, logits_out, idx_out, gate_out and y_f32_out
  *     are served; tau_out, counts_out, load_stats, tau_ema, save_pre, save_pre_shared, stage_events,
  *     cand_out and phases are refused; aux_stream, aux_events and shared_sms have no meaning here;
- *   - the latent is kept in fp32, for the router and the experts (lmoe_forward rounds it to
- *     bf16), and so are the experts' outputs; hs, h and gamma * u are rounded to bf16 as
- *     operands, e4m3 experts quantise the latent and h from fp32.  So the two calls agree within
+ *   - the latent is kept to ~2^-17 of itself, as two bf16 terms, for the router and the
+ *     experts (lmoe_forward rounds it to bf16), and the experts' outputs in fp32; hs, h and gamma * u are rounded to bf16 as
+ *     operands, e4m3 experts quantise the latent and h from those values.  So the two calls agree within
  *     the layer's tolerance, and route alike up to ties that the latent's rounding decides.
- *   - workspace: lmoe_few_workspace_bytes, 256-byte aligned, its first 256 bytes zeroed once
- *     before the first call (a call leaves them as it found them, error flag aside).  Calls on one
+ *   - workspace: lmoe_few_workspace_bytes, 256-byte aligned, its first LMOE_FEW_HEADER_BYTES
+ *     zeroed once before the first call (a call leaves them zero, error flag aside).  Calls on one
  *     workspace must not overlap.  It serves every smaller batch of the same layer too.
  * The kernel is a cooperative launch of one CTA per SM that wait on one another; every wait is
  * bounded, and lmoe_last_device_error reads the workspace's flag.  It may be captured into a graph.
@@ -464,6 +464,7 @@ int lmoe_quantize_e4m3(const void *x, long long rows, int cols, uint8_t *codes, 
  * less 64 KB for weights in flight: K3 at 8 tokens does).  T == 0 is a no-op.
  * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE_TOO_SMALL, CUDA. */
 #define LMOE_FEW_MAX_TOKENS 8
+#define LMOE_FEW_HEADER_BYTES 256
 size_t lmoe_few_workspace_bytes(const lmoe_dims *dims);
 int lmoe_forward_few(const lmoe_dims *dims, const void *packed, const void *x,
                      const void *residual, void *y, void *workspace, size_t ws_bytes, lmoe_io *io,

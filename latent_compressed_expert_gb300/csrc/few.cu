@@ -14,16 +14,16 @@
 //
 // A phase is a list of units of 16 weight rows (8 gate and the same features' 8 value rows for
 // the gated ones), dealt round the CTAs; K3's 736, 56, 1024, 448 and 448 units over 152 SMs leave
-// 3 % idle.  A CTA's eight warps split a unit's reduction, and each is its own pipeline: it
-// loads its weights in 2 KB TMA boxes (16 rows x 128 bytes, swizzled) into a private ring, over
-// units and phases as far ahead as the ring reaches -- weights do not depend on what the other
-// CTAs compute, so a grid barrier finds the next phase's loads already in flight -- and multiplies
-// each box by the tokens (MMA columns, m16n8k16) from shared memory.  A warp's lead needs no
-// barrier but the loads' own; tcgen05 would bring nothing here, since the tensor cores are idle
-// most of the time, and its 128-row tiles would need eight times the units' rows.
+// 3 % idle.  One thread loads a unit's weights, up to eight boxes of 16 rows x 128 bytes at a
+// time, into a ring, over units and phases as far ahead as the ring reaches: weights do not
+// depend on what the other CTAs compute, so a grid barrier finds the next phase's loads already
+// in flight.  Eight warps split the reduction, warp w taking box w of every stage, and multiply
+// it by the tokens (the eight columns of an m16n8k16 MMA) from shared memory.  tcgen05 would bring
+// nothing here: the tensor cores are idle most of the time, and its 128-row tiles would make
+// units too large to deal out evenly.
 //
-// Arithmetic: fp32 accumulation; the latent stays fp32 (for the products it is split into two
-// bf16 terms, hi + lo, so that routing sees ~2^-17 of it), hs, h and gamma u are rounded to bf16
+// Arithmetic: fp32 accumulation; the latent is kept as two bf16 terms,
+// hi + lo, ~2^-17 of its fp32 value, for the router and the experts, hs, h and gamma u are rounded to bf16
 // once as the next product's operand (e4m3 experts: the latent and h to e4m3 codes with a scale
 // per row from their fp32 values); rms(u) is applied after the product, which is the same for a
 // factor per token.  e4m3 products run as fp16 MMAs on the codes' exact values.
@@ -39,19 +39,28 @@ namespace lmoe {
 
 constexpr int FEW_T = LMOE_FEW_MAX_TOKENS;
 constexpr int FEW_WARPS = 8;
-constexpr int FEW_THREADS = FEW_WARPS * 32;
-constexpr int FEW_BOX = 16 * 128;       // bytes of a weight box
-constexpr int FEW_MAX_SLOTS = 16;       // of a warp's ring
-constexpr int FEW_MIN_SLOTS = 3;
-constexpr int FEW_MAX_SPLITS = 4;
+constexpr int FEW_THREADS = FEW_WARPS * 32;  // that compute; one more warp loads
+constexpr int FEW_BOX = 16 * 128;            // bytes of a weight box
+constexpr int FEW_BOXES = FEW_WARPS * FEW_BOX;  // of a stage
+constexpr int FEW_SCALES = 1024;             // e4m3: and its weight rows' scales
+constexpr int few_stage_bytes(bool fp8) { return FEW_BOXES + (fp8 ? FEW_SCALES : 0); }
+constexpr int FEW_MAX_STAGES = 14;
+constexpr int FEW_MIN_STAGES = 3;
+constexpr int FEW_MAX_SPLITS = 2;  // parts of u that are added in any order: a + b = b + a
 constexpr int FEW_MAX_PAIRS = FEW_T * 32;  // (token, expert) pairs
+constexpr int FEW_CAND = 64;               // candidates ranked at once in a token's selection
 
 enum FewPhase : int { FEW_IN = 0, FEW_ROUTER, FEW_GATE_UP, FEW_DOWN, FEW_OUT, FEW_NUM_PHASES };
 
 struct FewArgs {
   int T, d, L, E, K, I, sw;   // sw: shared width
   float c, eps;
-  int splits, slots;          // DOWN's parts; boxes in a warp's ring
+  int splits;                 // DOWN's parts
+  int stages, more;           // stages of the ring; and while the experts run (GATE_UP, DOWN):
+  int more_off;               // those beyond `stages` lie at tok + more_off
+  int out_pitch;              // OUT: shared-memory distance of the tokens' rows
+  int nb[5];                  // boxes of a stage, by phase (DOWN: of one expert)
+  int group;                  // DOWN: experts of a stage
   int tok_bytes;              // shared memory of the tokens' operands
   const __nv_bfloat16* x;
   const __nv_bfloat16* resid;
@@ -68,11 +77,16 @@ struct FewArgs {
   const float* s_ed;
   // workspace
   uint32_t* head;             // [0] error bits, [1] barrier arrivals, [2] CTAs done, [3] gave up
-  float* lat;                 // [T, L]
+  __nv_bfloat16* lat;         // [2, T, L]: hi, then lo
   __nv_bfloat16* hs;          // [T, sw]
   float* logits;              // [T, E]
+  uint32_t* keys;             // [T, E] selection keys of the logits
   void* h;                    // [T K, I] bf16, or fp32 (e4m3)
-  float* u;                   // [splits, T, L]
+  float* u;                   // [T, L]
+  uint8_t* lat8;              // e4m3: codes and scales of the latent and of h
+  float* lat_scale;
+  uint8_t* h8;
+  float* h_scale;
   unsigned long long timeout_ns;
   int inject_stall;           // test hook: the first grid barrier waits for one arrival too many
 };
@@ -83,18 +97,24 @@ struct FewMaps {
 
 // Small tables in shared memory.
 struct FewTables {
-  uint64_t bars[FEW_WARPS * FEW_MAX_SLOTS];
+  uint64_t full[FEW_MAX_STAGES], empty[FEW_MAX_STAGES];
+  uint64_t idle;                            // HBM has nothing to do for a while
+  uint64_t routed;                          // the experts are known
+  uint64_t staged;                          // a phase's token operands have landed
   float red[2][FEW_WARPS][16 * 8];          // partial tiles, two units in turn
-  uint32_t bits[4096 / 32];                 // which experts are used
-  int32_t expert[FEW_MAX_PAIRS];            // the used experts, ascending
+  int32_t expert[FEW_MAX_PAIRS];            // the used experts, in order of first use
   int16_t pair[FEW_MAX_PAIRS][FEW_T];       // pair t K + j of token t with that expert, or -1
   float gate[FEW_MAX_PAIRS][FEW_T];         // its gate, or 0
-  int32_t sel[FEW_MAX_PAIRS];
+  alignas(16) int32_t sel[FEW_MAX_PAIRS];   // expert and gate of every pair
   float sel_gate[FEW_MAX_PAIRS];
+  int16_t rank[FEW_MAX_PAIRS];              // place in `expert` of a pair that is its first use
+  int32_t first_uses[FEW_WARPS];
+  uint2 cand[FEW_WARPS][FEW_CAND];          // candidates of a token's selection
+  uint32_t won[FEW_WARPS][32];
   float h_scale[FEW_MAX_PAIRS];             // e4m3: of a pair's h row
   float lat_scale[FEW_T];                   // e4m3: of a token's latent
   float rstd[FEW_T];
-  float warp_sum[FEW_WARPS][FEW_T];
+  float warp_sum[FEW_WARPS];
   uint4 zero;                               // the operand of tokens that a box does not concern
   int used;
   int abort;
@@ -102,24 +122,19 @@ struct FewTables {
 
 constexpr int few_pitch(int bytes) { return bytes + 16; }  // rows 16 bytes apart mod 128
 
+// What both sides know of the sequence of units and stages.
 template <bool FP8>
-struct Few {
-  const FewArgs& a;
-  const FewMaps& m;
-  FewTables* s;
-  uint8_t* ring;       // this warp's slots
-  uint64_t* bars;
-  uint8_t* tok;        // tokens' operands
-  int warp, lane, cta, ctas;
-  // producer and consumer positions in the warp's sequence of boxes
-  uint32_t made = 0, used = 0;
-  int p_phase = FEW_IN, p_unit = 0, p_c = 0, p_end = 0, p_last = FEW_ROUTER;
-  bool p_done = false, ok = true;
-
-  __device__ Few(const FewArgs& a_, const FewMaps& m_) : a(a_), m(m_) {}
-
+struct FewPlan {
+  static constexpr int STAGE = few_stage_bytes(FP8);
   static constexpr int KC = FP8 ? 128 : 64;  // reduction elements of an expert box
+  const FewArgs& a;
+  FewTables* s;
+  int cta, ctas;
 
+  __device__ FewPlan(const FewArgs& a_, FewTables* s_) : a(a_), s(s_) {
+    cta = blockIdx.x;
+    ctas = gridDim.x;
+  }
   __device__ int units(int ph) const {
     switch (ph) {
       case FEW_IN: return a.L / 16 + a.sw / 8;
@@ -129,112 +144,183 @@ struct Few {
       default: return a.d / 16;
     }
   }
+  // The ring in phase ph: its length, and where a stage lies.  Both sides step through the slots in
+  // the same order; each slot's barriers keep their own parity.
+  __device__ int ring_stages(int ph) const {
+    return ph == FEW_GATE_UP || ph == FEW_DOWN ? a.more : a.stages;
+  }
+  __device__ uint8_t* stage_at(uint8_t* ring, int slot) const {
+    return slot < a.stages ? ring + slot * STAGE
+                           : ring + a.stages * STAGE + a.more_off + (slot - a.stages) * STAGE;
+  }
+  // boxes along a unit's reduction (DOWN: one expert's)
+  __device__ int boxes(int ph) const {
+    switch (ph) {
+      case FEW_IN: return a.d / 64;
+      case FEW_ROUTER: return a.L / 64;
+      case FEW_GATE_UP: return a.L / KC;
+      case FEW_DOWN: return a.I / KC;
+      default: return (a.L + a.sw) / 64;
+    }
+  }
   // DOWN: the experts [e0, e1) of a unit's part
   __device__ void experts(int unit, int* e0, int* e1) const {
     const int part = unit % a.splits;
     *e0 = s->used * part / a.splits;
     *e1 = s->used * (part + 1) / a.splits;
   }
-  // this warp's boxes [c0, c1) of a unit
-  __device__ void range(int ph, int unit, int* c0, int* c1) const {
-    int n;
-    if (ph == FEW_IN) n = a.d / 64;
-    else if (ph == FEW_ROUTER) n = a.L / 64;
-    else if (ph == FEW_GATE_UP) n = a.L / KC;
-    else if (ph == FEW_OUT) n = (a.L + a.sw) / 64;
-    else {
-      int e0, e1;
-      experts(unit, &e0, &e1);
-      n = (e1 - e0) * (a.I / KC);
+};
+
+// The loading thread.
+template <bool FP8>
+__device__ void few_load(const FewPlan<FP8>& p, const FewMaps& m, uint8_t* ring) {
+  const FewArgs& a = p.a;
+  FewTables* s = p.s;
+  int slot = 0, in_ring = 0;
+  uint32_t parity = ~0u;  // bit i: of the wait for slot i to be free; the first round passes at once
+  bool ok = true;
+  // every weight is read once: first out of L2 again, but for what was fetched ahead
+  const uint64_t once = ptx::l2_policy_evict_first();
+  // the next stage's buffer, or null when a wait ran out
+  auto stage = [&](int boxes, int scales) -> uint8_t* {
+    ok = ok && ptx::mbar_wait(&s->empty[slot], (parity >> slot) & 1u, &s->abort, a.timeout_ns);
+    if (!ok) return nullptr;
+    ptx::mbar_arrive_expect_tx(&s->full[slot], static_cast<uint32_t>(boxes * FEW_BOX + scales * 4));
+    return p.stage_at(ring, slot);
+  };
+  auto next = [&]() {
+    parity ^= 1u << slot;
+    if (++slot >= in_ring) slot = 0;
+  };
+  for (int ph = FEW_IN; ok && ph < FEW_NUM_PHASES; ++ph) {
+    if (ph == FEW_GATE_UP) {
+      // Its weights depend on the routing.  Until that is known (from the first barrier on), HBM
+      // brings the CTA's first unit of OUT into L2, where the expert weights, which are the first
+      // to be evicted, leave it: K3, one token 92.1 -> 90.3 us, eight 285 -> 280; two units 93.4.
+      ok = ptx::mbar_wait(&s->idle, 0, &s->abort, a.timeout_ns);
+      if (!ok) break;
+      const uint64_t keep = ptx::l2_policy_evict_last();
+      const int no = p.boxes(FEW_OUT);
+      for (int k = 0; p.cta < p.units(FEW_OUT) && k < no; k += a.nb[FEW_OUT])
+        ptx::tma_prefetch_3d(&m.out, 0, p.cta * 16, k, keep);
+      ok = ptx::mbar_wait(&s->routed, 0, &s->abort, a.timeout_ns);
+      if (!ok) break;
     }
-    *c0 = n * warp / FEW_WARPS;
-    *c1 = n * (warp + 1) / FEW_WARPS;
-  }
-  __device__ void load_box(int ph, int unit, int c, uint8_t* dst, uint64_t* bar) const {
-    switch (ph) {
-      case FEW_IN:
-        if (unit < a.L / 16) {
-          ptx::tma_load_2d(dst, &m.down, bar, c * 64, unit * 16);
-        } else {
-          const int f = (unit - a.L / 16) * 8;
-          ptx::tma_load_4d(dst, &m.shared, bar, c * 64, f % GLU_GROUP, 0, f / GLU_GROUP);
-        }
-        break;
-      case FEW_ROUTER: ptx::tma_load_2d(dst, &m.router, bar, c * 64, unit * 16); break;
-      case FEW_GATE_UP: {
-        const int per = a.I / 8, e = s->expert[unit / per], f = unit % per * 8;
-        const int row = f / GLU_GROUP * (2 * GLU_GROUP);  // of the packed expert, its gate group
-        const int tiles = (2 * a.I + BLOCK_M - 1) / BLOCK_M;
-        const int tile = (e * tiles + row / BLOCK_M) * (a.L / KC) + c;
-        ptx::tma_load_4d(dst, &m.gate_up, bar, 0, f % GLU_GROUP, 0,
-                         tile * (BLOCK_M / (2 * GLU_GROUP)) + row % BLOCK_M / (2 * GLU_GROUP));
-        break;
-      }
-      case FEW_DOWN: {
+    const int n = p.boxes(ph), nb = a.nb[ph], units = p.units(ph);
+    in_ring = p.ring_stages(ph);
+    if (slot >= in_ring) slot = 0;
+    for (int unit = p.cta; ok && unit < units; unit += p.ctas) {
+      if (ph == FEW_DOWN) {
+        const int row = unit / a.splits * 16, tiles = (a.L + BLOCK_M - 1) / BLOCK_M;
         int e0, e1;
-        experts(unit, &e0, &e1);
-        const int nk = a.I / KC, e = s->expert[e0 + c / nk], row = unit / a.splits * 16;
-        const int tiles = (a.L + BLOCK_M - 1) / BLOCK_M;
-        const int tile = (e * tiles + row / BLOCK_M) * nk + c % nk;
-        ptx::tma_load_2d(dst, &m.edown, bar, 0, tile * BLOCK_M + row % BLOCK_M);
-        break;
-      }
-      default: ptx::tma_load_2d(dst, &m.out, bar, c * 64, unit * 16);
-    }
-  }
-  // Starts the producer at phase `first`, up to and including `last`, and fills the ring.
-  __device__ void produce_phases(int first, int last) {
-    p_phase = first;
-    p_last = last;
-    p_unit = cta;
-    p_done = false;
-    p_c = p_end = 0;
-    if (p_unit < units(p_phase)) range(p_phase, p_unit, &p_c, &p_end);
-    else p_unit -= ctas;  // none in this phase: produce() steps on
-    for (int i = 0; i < a.slots; ++i) produce();
-  }
-  // Issues the warp's next box into the slot that `made` names (which must be free).
-  __device__ void produce() {
-    while (!p_done && p_c == p_end) {
-      p_unit += ctas;
-      if (p_unit >= units(p_phase)) {
-        if (p_phase == p_last) {
-          p_done = true;
-          break;
+        p.experts(unit, &e0, &e1);
+        for (int e = e0; ok && e < e1; e += a.group) {
+          const int ge = min(a.group, e1 - e);
+          for (int k = 0; ok && k < n; k += nb) {
+            const bool sc = FP8 && k == 0;  // with an expert's first boxes
+            uint8_t* dst = stage(ge * nb, sc ? ge * 16 : 0);
+            if (!dst) break;
+            for (int i = 0; i < ge; ++i) {
+              const int tile = s->expert[e + i] * tiles + row / BLOCK_M;
+              ptx::tma_load_4d_hint(dst + i * nb * FEW_BOX, &m.edown, &s->full[slot], 0,
+                                    row % BLOCK_M, k, tile, once);
+              if (sc)
+                ptx::bulk_load(dst + FEW_BOXES + i * 64,
+                               a.s_ed + static_cast<size_t>(tile) * BLOCK_M + row % BLOCK_M, 64,
+                               &s->full[slot]);
+            }
+            next();
+          }
         }
-        ++p_phase;
-        p_unit = cta - ctas;
         continue;
       }
-      range(p_phase, p_unit, &p_c, &p_end);
+      const bool shared = ph == FEW_IN && unit >= a.L / 16;
+      int f = 0, y = unit * 16, tile = 0;
+      if (shared) f = (unit - a.L / 16) * 8;
+      if (ph == FEW_GATE_UP) f = unit % (a.I / 8) * 8;
+      if (shared || ph == FEW_GATE_UP)  // packed row of the features' gate rows
+        y = f / GLU_GROUP * (2 * GLU_GROUP) + f % GLU_GROUP;
+      if (ph == FEW_GATE_UP) {
+        tile = s->expert[unit / (a.I / 8)] * ((2 * a.I + BLOCK_M - 1) / BLOCK_M) + y / BLOCK_M;
+        y %= BLOCK_M;
+      }
+      const CUtensorMap* map = ph == FEW_IN ? &m.down : ph == FEW_ROUTER ? &m.router : &m.out;
+      for (int k = 0; k < n; k += nb) {
+        const bool sc = FP8 && ph == FEW_GATE_UP && k == 0;
+        uint8_t* dst = stage(nb, sc ? 16 : 0);
+        if (!dst) break;
+        if (sc) {  // eight gate rows' and the same features' value rows'
+          const float* src = a.s_gu + static_cast<size_t>(tile) * BLOCK_M + y;
+          ptx::bulk_load(dst + FEW_BOXES, src, 32, &s->full[slot]);
+          ptx::bulk_load(dst + FEW_BOXES + 32, src + GLU_GROUP, 32, &s->full[slot]);
+        }
+        if (ph == FEW_GATE_UP)
+          ptx::tma_load_5d_hint(dst, &m.gate_up, &s->full[slot], 0, y, 0, k, tile, once);
+        else if (shared)
+          ptx::tma_load_4d_hint(dst, &m.shared, &s->full[slot], 0, y, 0, k, once);
+        else
+          ptx::tma_load_3d_hint(dst, map, &s->full[slot], 0, y, k, once);
+        next();
+      }
     }
-    if (p_done || !ok) return;
-    if (lane == 0) {
-      const uint32_t slot = made % a.slots;
-      ptx::mbar_arrive_expect_tx(&bars[slot], FEW_BOX);
-      load_box(p_phase, p_unit, p_c, ring + slot * FEW_BOX, &bars[slot]);
-    }
-    ++p_c;
-    ++made;
   }
-  // Waits for the warp's next box; its shared-memory address.
+  if (!ok && !*static_cast<volatile int*>(&s->abort)) {
+    *static_cast<volatile int*>(&s->abort) = 1;
+    atomicOr(a.head, DEVERR_TIMEOUT_PRODUCER);
+  }
+  // every copy lands before the CTA may leave (bounded): each slot's last one; a slot never used
+  // has its bit still set, and its barrier passes for it
+  for (int i = 0; i < a.more; ++i) {
+    const uint64_t t0 = ptx::globaltimer_ns();
+    while (!ptx::mbar_try_wait(&s->full[i], ((parity >> i) & 1u)))
+      if (ptx::globaltimer_ns() - t0 > a.timeout_ns) break;
+  }
+}
+
+// The computing warps.
+template <bool FP8>
+struct Few : FewPlan<FP8> {
+  using P = FewPlan<FP8>;
+  using P::a;
+  using P::cta;
+  using P::ctas;
+  using P::experts;
+  using P::KC;
+  using P::s;
+  using P::units;
+  uint8_t* ring;
+  uint8_t* tok;        // tokens' operands
+  int warp, lane;
+  int slot = 0, in_ring = 0;
+  uint32_t parity = 0, staged = 0, arrivals = 0;  // parity: bit i, of slot i's next stage
+  bool ok = true;
+
+  __device__ Few(const FewArgs& a_, FewTables* s_) : P(a_, s_) {}
+
+  __device__ static void sync() { ptx::named_sync(1, FEW_THREADS); }
+
+  // Waits for the next stage; the shared-memory address of this warp's box.
   __device__ uint32_t take() {
-    const uint32_t slot = used % a.slots;
-    if (ok && !__all_sync(0xffffffffu, ptx::mbar_wait(&bars[slot], (used / a.slots) & 1u,
-                                                      &s->abort, a.timeout_ns))) {
+    if (ok && !__all_sync(0xffffffffu,
+                          ptx::mbar_wait(&s->full[slot], (parity >> slot) & 1u, &s->abort,
+                                         a.timeout_ns))) {
       ok = false;
       if (lane == 0) {
         s->abort = 1;
         atomicOr(a.head, DEVERR_TIMEOUT_MMA);
       }
     }
-    return ptx::smem_u32(ring + slot * FEW_BOX);
+    return ptx::smem_u32(P::stage_at(ring, slot) + warp * FEW_BOX);
   }
   __device__ void release() {
-    if (!ok) return;  // used stays at the box that never came
-    ++used;
     __syncwarp();  // every lane has read the box
-    produce();
+    if (lane == 0 && ok) ptx::mbar_arrive(&s->empty[slot]);
+    parity ^= 1u << slot;
+    if (++slot >= in_ring) slot = 0;
+  }
+  __device__ void enter(int ph) {
+    in_ring = P::ring_stages(ph);
+    if (slot >= in_ring) slot = 0;
   }
   // acc += box (16 rows x 128 bytes) . tokens.  b: address of this lane's operand row of the
   // box's columns (row lane & 7, 16-byte piece lane >> 3), bstep 64, or 0 for the zero piece.
@@ -283,7 +369,7 @@ struct Few {
     const int g = lane >> 2, c = (lane & 3) * 2;
     *reinterpret_cast<float2*>(r + g * 8 + c) = make_float2(t[0], t[1]);
     *reinterpret_cast<float2*>(r + (g + 8) * 8 + c) = make_float2(t[2], t[3]);
-    __syncthreads();
+    sync();
     return s->red[n & 1][0];
   }
   __device__ static float total(const float* red, int i) {
@@ -293,14 +379,15 @@ struct Few {
     return v;
   }
 
-  // Waits until every CTA has arrived for the n-th time (from 1); false: gave up.
-  __device__ bool grid_barrier(int n) {
-    __syncthreads();
+  // Waits until every CTA has arrived as often as this one; false: gave up.
+  __device__ bool grid_barrier() {
+    ++arrivals;
+    ptx::fence_proxy_async();  // this thread's results, for the others' bulk copies
+    sync();
     if (threadIdx.x == 0) {
-      __threadfence();
-      atomicAdd(a.head + 1, 1u);
+      ptx::red_release_add_u32(a.head + 1, 1u);
       const uint32_t target =
-          static_cast<uint32_t>(ctas) * n + (n == 1 && a.inject_stall ? 1u : 0u);
+          static_cast<uint32_t>(ctas) * arrivals + (arrivals == 1 && a.inject_stall ? 1u : 0u);
       const uint64_t t0 = ptx::globaltimer_ns();
       for (uint32_t it = 1;; ++it) {
         if (ptx::ld_acquire_u32(a.head + 1) >= target) break;
@@ -317,127 +404,182 @@ struct Few {
           }
         }
       }
-      __threadfence();
     }
-    __syncthreads();
+    sync();
     return *static_cast<volatile int*>(&s->abort) == 0;
   }
 
   // ---------------------------------------------------------------- operands of the phases
-  __device__ void stage_x() {
-    const int pitch = few_pitch(a.d * 2), nv = a.d / 8;
-    for (int i = threadIdx.x; i < a.T * nv; i += FEW_THREADS) {
-      const int t = i / nv, v = i % nv;
-      *reinterpret_cast<uint4*>(tok + t * pitch + v * 16) =
-          __ldg(reinterpret_cast<const uint4*>(a.x + static_cast<size_t>(t) * a.d) + v);
-    }
+  // Rows of `bytes` (row distance src_pitch) into shared memory by bulk copies, which warp 0
+  // issues; landed() waits for all of a phase's.  What other CTAs wrote is read through the async
+  // proxy: they fence before the grid barrier, and so does the reader after it.
+  __device__ void copy_rows(uint8_t* dst, int dst_pitch, const void* src, size_t src_pitch,
+                            int rows, int bytes) {
+    if (warp != 0) return;
+    ptx::fence_proxy_async();
+    if (lane == 0) ptx::mbar_expect_tx(&s->staged, static_cast<uint32_t>(rows) * bytes);
+    __syncwarp();
+    for (int r = lane; r < rows; r += 32)
+      ptx::bulk_load(dst + r * dst_pitch, static_cast<const uint8_t*>(src) + r * src_pitch, bytes,
+                     &s->staged);
   }
-  // latent: rows 0 .. T-1 hi, then lo; e4m3: then the codes
-  __device__ uint32_t lat_lo() const { return static_cast<uint32_t>(a.T * few_pitch(a.L * 2)); }
-  __device__ void stage_lat() {
-    const int pitch = few_pitch(a.L * 2), nv = a.L / 4;
-    for (int i = threadIdx.x; i < a.T * nv; i += FEW_THREADS) {
-      const int t = i / nv, v = i % nv;
-      const float4 f = __ldcg(reinterpret_cast<const float4*>(a.lat + static_cast<size_t>(t) * a.L) + v);
-      const __nv_bfloat162 h0 = __floats2bfloat162_rn(f.x, f.y), h1 = __floats2bfloat162_rn(f.z, f.w);
-      const float2 g0 = __bfloat1622float2(h0), g1 = __bfloat1622float2(h1);
-      const __nv_bfloat162 l0 = __floats2bfloat162_rn(f.x - g0.x, f.y - g0.y);
-      const __nv_bfloat162 l1 = __floats2bfloat162_rn(f.z - g1.x, f.w - g1.y);
-      __nv_bfloat162* p = reinterpret_cast<__nv_bfloat162*>(tok + t * pitch + v * 8);
-      __nv_bfloat162* q = reinterpret_cast<__nv_bfloat162*>(tok + lat_lo() + t * pitch + v * 8);
-      p[0] = h0, p[1] = h1;
-      q[0] = l0, q[1] = l1;
+  __device__ void landed() {
+    __syncwarp();
+    if (threadIdx.x == 0) ptx::mbar_arrive(&s->staged);
+    // whatever else went wrong, copies in flight are waited for (bounded)
+    const uint64_t t0 = ptx::globaltimer_ns();
+    bool there;
+    while (!(there = ptx::mbar_try_wait(&s->staged, staged)))
+      if (ptx::globaltimer_ns() - t0 > a.timeout_ns) break;
+    if (!__all_sync(0xffffffffu, there)) {
+      ok = false;
+      if (lane == 0) {
+        s->abort = 1;
+        atomicOr(a.head, DEVERR_TIMEOUT_MMA);
+      }
     }
-    if constexpr (FP8) {
-      if (warp < a.T)
-        s->lat_scale[warp] = quantize(a.lat + static_cast<size_t>(warp) * a.L, a.L,
-                                      tok + 2 * lat_lo() + warp * few_pitch(a.L));
-    }
+    staged ^= 1u;
   }
-  // One fp32 row of global memory as codes in shared memory, by a warp; its scale.
-  __device__ float quantize(const float* row, int n, uint8_t* dst) {
+  // A row of n fp32 values (four at a time from get) as e4m3 codes with its scale, by all threads.
+  template <typename Get>
+  __device__ void quantize(int n, Get get, uint8_t* codes, float* scale) {
     float amax = 0.0f;
-    for (int v = lane; v < n / 4; v += 32) {
-      const float4 f = __ldcg(reinterpret_cast<const float4*>(row) + v);
+    for (int v = threadIdx.x; v < n / 4; v += FEW_THREADS) {
+      const float4 f = get(v);
       amax = fmaxf(fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y))), fmaxf(fabsf(f.z), fabsf(f.w)));
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    if (lane == 0) s->warp_sum[warp] = amax;
+    sync();
+    for (int w = 0; w < FEW_WARPS; ++w) amax = fmaxf(amax, s->warp_sum[w]);
     float sc = __fdiv_rn(amax, 448.0f);
     sc = sc > 0.0f ? sc : 1.0f;
-    for (int v = lane; v < n / 4; v += 32) {
-      const float4 f = __ldcg(reinterpret_cast<const float4*>(row) + v);
-      const uint32_t lo = ptx::cvt_e4m3x2(__fdiv_rn(f.y, sc), __fdiv_rn(f.x, sc));
-      const uint32_t hi = ptx::cvt_e4m3x2(__fdiv_rn(f.w, sc), __fdiv_rn(f.z, sc));
-      reinterpret_cast<uint32_t*>(dst)[v] = lo | (hi << 16);
+    for (int v = threadIdx.x; v < n / 4; v += FEW_THREADS) {
+      const float4 f = get(v);
+      reinterpret_cast<uint32_t*>(codes)[v] =
+          ptx::cvt_e4m3x2(__fdiv_rn(f.y, sc), __fdiv_rn(f.x, sc)) |
+          (static_cast<uint32_t>(ptx::cvt_e4m3x2(__fdiv_rn(f.w, sc), __fdiv_rn(f.z, sc))) << 16);
     }
-    return sc;
+    if (threadIdx.x == 0) *scale = sc;
+    sync();  // warp_sum is free again
+  }
+  __device__ void stage_x() {
+    copy_rows(tok, few_pitch(a.d * 2), a.x, static_cast<size_t>(a.d) * 2, a.T, a.d * 2);
+    landed();
+  }
+  // latent: rows 0 .. T-1 hi, then lo; e4m3: after the router their codes (stage_codes)
+  __device__ uint32_t lat_lo() const { return static_cast<uint32_t>(a.T * few_pitch(a.L * 2)); }
+  __device__ void stage_lat() {
+    const int pitch = few_pitch(a.L * 2);
+    copy_rows(tok, pitch, a.lat, static_cast<size_t>(a.L) * 2, 2 * a.T, a.L * 2);
+    landed();
+    if constexpr (FP8) {  // a token per CTA, of those that have the least to do for the router
+      for (int t = ctas - 1 - cta; t < a.T; t += ctas) {
+        const uint2* hi = reinterpret_cast<const uint2*>(tok + t * pitch);
+        const uint2* lo = reinterpret_cast<const uint2*>(tok + lat_lo() + t * pitch);
+        auto get = [&](int v) {
+          const uint2 h = hi[v], l = lo[v];
+          auto two = [](uint32_t p, uint32_t q) {
+            return make_float2(__uint_as_float(p << 16) + __uint_as_float(q << 16),
+                               __uint_as_float(p & 0xFFFF0000u) + __uint_as_float(q & 0xFFFF0000u));
+          };
+          const float2 f = two(h.x, l.x), g = two(h.y, l.y);
+          return make_float4(f.x, f.y, g.x, g.y);
+        };
+        quantize(a.L, get, a.lat8 + static_cast<size_t>(t) * a.L, a.lat_scale + t);
+      }
+    }
+  }
+  __device__ void stage_codes() {
+    if constexpr (FP8) {
+      if (threadIdx.x < a.T) s->lat_scale[threadIdx.x] = __ldcg(a.lat_scale + threadIdx.x);
+      copy_rows(tok, few_pitch(a.L), a.lat8, a.L, a.T, a.L);  // the router is done with hi and lo
+      landed();
+      sync();
+    }
+  }
+  // e4m3: h's rows to codes, a row per CTA
+  __device__ void quantize_h() {
+    for (int p = cta; p < a.T * a.K; p += ctas) {
+      const float4* row =
+          reinterpret_cast<const float4*>(static_cast<const float*>(a.h) + static_cast<size_t>(p) * a.I);
+      quantize(a.I, [&](int v) { return __ldcg(row + v); }, a.h8 + static_cast<size_t>(p) * a.I,
+               a.h_scale + p);
+    }
   }
   __device__ void stage_h() {
-    const int pairs = a.T * a.K;
-    if constexpr (FP8) {
-      for (int p = warp; p < pairs; p += FEW_WARPS) {
-        const float sc = quantize(static_cast<const float*>(a.h) + static_cast<size_t>(p) * a.I, a.I,
-                                  tok + p * few_pitch(a.I));
-        if (lane == 0) s->h_scale[p] = sc;
-      }
-    } else {
-      const int pitch = few_pitch(a.I * 2), nv = a.I / 8;
-      for (int i = threadIdx.x; i < pairs * nv; i += FEW_THREADS) {
-        const int p = i / nv, v = i % nv;
-        *reinterpret_cast<uint4*>(tok + p * pitch + v * 16) =
-            __ldcg(reinterpret_cast<const uint4*>(a.h) + static_cast<size_t>(p) * nv + v);
-      }
-    }
+    const int pairs = a.T * a.K, bytes = FP8 ? a.I : a.I * 2;
+    copy_rows(tok, few_pitch(bytes), FP8 ? static_cast<const void*>(a.h8) : a.h, bytes, pairs, bytes);
+    if (FP8 && threadIdx.x < pairs) s->h_scale[threadIdx.x] = __ldcg(a.h_scale + threadIdx.x);
+    landed();
+    if constexpr (FP8) sync();
   }
-  // [gamma u | hs], and rstd of u
+  // [gamma u | hs], and rstd of u.  u arrives in fp32 by bulk copies (loads through the LSU, all
+  // SMs asking for the same lines, took 10 us at eight tokens); warp t turns token t's row into
+  // bf16 where it lies, from the front, so that no value is overwritten before it was read.
   __device__ void stage_z() {
-    const int pitch = few_pitch((a.L + a.sw) * 2), nv = a.L / 4;
-    for (int t = 0; t < a.T; ++t) {
+    const int pitch = a.out_pitch, nv = a.L / 4;
+    copy_rows(tok, pitch, a.u, static_cast<size_t>(a.L) * 4, a.T, a.L * 4);
+    constexpr int NV = 14;
+    float4 g[NV];
+    auto load_gamma = [&](int v0) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+        g[j] = v0 + 32 * j < nv ? __ldg(reinterpret_cast<const float4*>(a.gamma) + v0 + 32 * j)
+                                : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    };
+    if (warp < a.T) load_gamma(lane);
+    landed();
+    if (warp < a.T) {
       float sq = 0.0f;
-      for (int v = threadIdx.x; v < nv; v += FEW_THREADS) {
-        float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (int p = 0; p < a.splits; ++p) {
-          const float4 g = __ldcg(reinterpret_cast<const float4*>(
-              a.u + (static_cast<size_t>(p) * a.T + t) * a.L) + v);
-          f.x += g.x, f.y += g.y, f.z += g.z, f.w += g.w;
+      for (int v0 = lane; v0 - lane < nv; v0 += NV * 32) {
+        float4 f[NV];
+        if (v0 != lane) load_gamma(v0);
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+          const int v = v0 + 32 * j;
+          f[j] = v < nv ? *reinterpret_cast<const float4*>(tok + warp * pitch + v * 16)
+                        : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         }
-        sq = fmaf(f.x, f.x, fmaf(f.y, f.y, fmaf(f.z, f.z, fmaf(f.w, f.w, sq))));
-        const float4 g = __ldg(reinterpret_cast<const float4*>(a.gamma) + v);
-        __nv_bfloat162* o = reinterpret_cast<__nv_bfloat162*>(tok + t * pitch + v * 8);
-        o[0] = __floats2bfloat162_rn(f.x * g.x, f.y * g.y);
-        o[1] = __floats2bfloat162_rn(f.z * g.z, f.w * g.w);
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+          const int v = v0 + 32 * j;
+          sq = fmaf(f[j].x, f[j].x, fmaf(f[j].y, f[j].y, sq));
+          sq = fmaf(f[j].z, f[j].z, fmaf(f[j].w, f[j].w, sq));
+          if (v < nv) {
+            __nv_bfloat162* o = reinterpret_cast<__nv_bfloat162*>(tok + warp * pitch + v * 8);
+            o[0] = __floats2bfloat162_rn(f[j].x * g[j].x, f[j].y * g[j].y);
+            o[1] = __floats2bfloat162_rn(f[j].z * g[j].z, f[j].w * g[j].w);
+          }
+        }
+        __syncwarp();
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
-      if (lane == 0) s->warp_sum[warp][t] = sq;
+      if (lane == 0) s->rstd[warp] = __frsqrt_rn(__fdiv_rn(sq, static_cast<float>(a.L)) + a.eps);
     }
-    const int ns = a.sw / 8;
-    for (int i = threadIdx.x; i < a.T * ns; i += FEW_THREADS) {
-      const int t = i / ns, v = i % ns;
-      *reinterpret_cast<uint4*>(tok + t * pitch + a.L * 2 + v * 16) =
-          __ldcg(reinterpret_cast<const uint4*>(a.hs + static_cast<size_t>(t) * a.sw) + v);
-    }
-    __syncthreads();
-    if (threadIdx.x < a.T) {
-      float sq = 0.0f;
-      for (int w = 0; w < FEW_WARPS; ++w) sq += s->warp_sum[w][threadIdx.x];
-      s->rstd[threadIdx.x] = __frsqrt_rn(__fdiv_rn(sq, static_cast<float>(a.L)) + a.eps);
+    sync();  // every row is bf16 before hs lands behind it
+    if (a.sw > 0) {
+      copy_rows(tok + a.L * 2, pitch, a.hs, static_cast<size_t>(a.sw) * 2, a.T, a.sw * 2);
+      landed();
     }
   }
 
   // ---------------------------------------------------------------- phases
   __device__ void phase_in() {
+    enter(FEW_IN);
     const int pitch = few_pitch(a.d * 2);
     const Row r = token_row((lane & 7) < a.T ? lane & 7 : -1, pitch);
+    const int nc = P::boxes(FEW_IN), nb = a.nb[FEW_IN];
     int n = 0;
     for (int unit = cta; unit < units(FEW_IN); unit += ctas, ++n) {
-      int c, end;
-      range(FEW_IN, unit, &c, &end);
       float acc[2][4] = {};
-      for (; c < end; ++c) {
+      for (int k = 0; k < nc; k += nb) {
         const uint32_t box = take();
-        multiply<false>(box, r.base + r.on * c * 128, r.on * 64, acc);
+        const int c = k + warp;
+        if (warp < nb && c < nc) multiply<false>(box, r.base + r.on * c * 128, r.on * 64, acc);
         release();
       }
       const float t4[4] = {acc[0][0] + acc[1][0], acc[0][1] + acc[1][1], acc[0][2] + acc[1][2],
@@ -446,7 +588,13 @@ struct Few {
       const int i = threadIdx.x, t = i & 7;
       if (t >= a.T) continue;
       if (unit < a.L / 16) {
-        if (i < 128) a.lat[static_cast<size_t>(t) * a.L + unit * 16 + (i >> 3)] = total(red, i);
+        if (i < 128) {
+          const float v = total(red, i);
+          const __nv_bfloat16 hi = __float2bfloat16_rn(v);
+          const size_t o = static_cast<size_t>(t) * a.L + unit * 16 + (i >> 3);
+          a.lat[o] = hi;
+          a.lat[static_cast<size_t>(a.T) * a.L + o] = __float2bfloat16_rn(v - __bfloat162float(hi));
+        }
       } else if (i < 64) {
         const int f = (unit - a.L / 16) * 8 + (i >> 3);
         a.hs[static_cast<size_t>(t) * a.sw + f] =
@@ -455,17 +603,20 @@ struct Few {
     }
   }
   __device__ void phase_router() {
+    enter(FEW_ROUTER);
     const int pitch = few_pitch(a.L * 2), row = (lane & 7) < a.T ? lane & 7 : -1;
     const Row hi = token_row(row, pitch), lo = token_row(row, pitch, lat_lo());
+    const int nc = P::boxes(FEW_ROUTER), nb = a.nb[FEW_ROUTER];
     int n = 0;
     for (int unit = cta; unit < units(FEW_ROUTER); unit += ctas, ++n) {
-      int c, end;
-      range(FEW_ROUTER, unit, &c, &end);
       float acc[2][4] = {}, rest[2][4] = {};
-      for (; c < end; ++c) {
+      for (int k = 0; k < nc; k += nb) {
         const uint32_t box = take();
-        multiply<false>(box, hi.base + hi.on * c * 128, hi.on * 64, acc);
-        multiply<false>(box, lo.base + lo.on * c * 128, lo.on * 64, rest);
+        const int c = k + warp;
+        if (warp < nb && c < nc) {
+          multiply<false>(box, hi.base + hi.on * c * 128, hi.on * 64, acc);
+          multiply<false>(box, lo.base + lo.on * c * 128, lo.on * 64, rest);
+        }
         release();
       }
       float t4[4];
@@ -473,27 +624,102 @@ struct Few {
       for (int k = 0; k < 4; ++k) t4[k] = (acc[0][k] + acc[1][k]) + (rest[0][k] + rest[1][k]);
       const float* red = join(n, t4);
       const int i = threadIdx.x, t = i & 7, e = unit * 16 + (i >> 3);
-      if (i < 128 && t < a.T)
-        a.logits[static_cast<size_t>(t) * a.E + e] =
-            total(red, i) + (a.bias ? __ldg(a.bias + e) : 0.0f);
+      if (i < 128 && t < a.T) {
+        const float z = total(red, i) + (a.bias ? __ldg(a.bias + e) : 0.0f);
+        a.logits[static_cast<size_t>(t) * a.E + e] = z;
+        a.keys[static_cast<size_t>(t) * a.E + e] = key(z, e);
+      }
     }
+    if (a.logits_in)
+      for (int i = cta * FEW_THREADS + threadIdx.x; i < a.T * a.E; i += ctas * FEW_THREADS)
+        a.keys[i] = key(__ldg(a.logits_in + i), i % a.E);
+  }
+  // What the selection goes by: the order of fl32(s - tau).
+  __device__ uint32_t key(float z, int e) const {
+    const float sc = score_sigmoid(z);
+    return order_key(a.tau ? __fsub_rn(sc, __ldg(a.tau + e)) : sc);
+  }
+  // The K largest keys of a token, by a warp: lane j returns the j-th (larger key first, then the
+  // lower expert), as select_rounds does.  The K-th largest of the lanes' maxima is a lower bound
+  // of the K-th largest key; the keys that reach it are few unless many are equal, and are ranked
+  // against each other.
+  __device__ int top_k(uint32_t* keys) {
+    const uint4* k4 = reinterpret_cast<const uint4*>(keys);
+    const int nq = a.E / 4;
+    uint32_t top = 0u;
+#pragma unroll 4
+    for (int q = lane; q < nq; q += 32) {
+      const uint4 k = k4[q];
+      top = max(max(top, max(k.x, k.y)), max(k.z, k.w));
+    }
+    int rank = 0;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      const uint32_t other = __shfl_sync(0xffffffffu, top, j);
+      rank += other > top || (other == top && j < lane);
+    }
+    const uint32_t bound =
+        max(1u, __shfl_sync(0xffffffffu, top,
+                            __ffs(__ballot_sync(0xffffffffu, rank == a.K - 1)) - 1));
+    int n = 0;  // of this lane
+#pragma unroll 4
+    for (int q = lane; q < nq; q += 32) {
+      const uint4 k = k4[q];
+      n += (k.x >= bound) + (k.y >= bound) + (k.z >= bound) + (k.w >= bound);
+    }
+    int at = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, at, o);
+      if (lane >= o) at += v;
+    }
+    const int all = __shfl_sync(0xffffffffu, at, 31);
+    if (all > FEW_CAND || all < a.K) return select_rounds(keys, a.E, a.K, lane);
+    at -= n;
+    uint2* cand = s->cand[warp];  // (key, expert)
+    if (n > 0) {
+      for (int q = lane; q < nq; q += 32) {
+        const uint4 k = k4[q];
+        const uint32_t v[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (v[c] >= bound) cand[at++] = make_uint2(v[c], 4 * q + c);
+      }
+    }
+    __syncwarp();
+    // each candidate's place among the others; a place below K is a winner's slot
+    uint32_t* won = s->won[warp];
+    for (int c = lane; c < all; c += 32) {
+      const uint2 me = cand[c];
+      int r = 0;
+#pragma unroll 8
+      for (int j = 0; j < all; ++j) {
+        const uint2 o = cand[j];
+        r += o.x > me.x || (o.x == me.x && o.y < me.y);
+      }
+      if (r < a.K) won[r] = me.y;
+    }
+    __syncwarp();
+    return lane < a.K ? static_cast<int>(won[lane]) : 0;
   }
   // Every CTA: the top-K experts of every token, then the list of the experts used.  keys: scratch
-  // over the (idle) rings, for as many tokens at a time as fit.
-  __device__ void select(uint32_t* keys, int fit) {
+  // over the (idle) ring: the logits and the keys of as many tokens at a time as fit.
+  __device__ void select() {
     const float* z = a.logits_in ? a.logits_in : a.logits;
+    const int pairs = a.T * a.K;
+    const int fit = min(FEW_WARPS, a.stages * FEW_BOXES / (a.E * 8));
+    float* lg = reinterpret_cast<float*>(ring);
+    uint32_t* keys = reinterpret_cast<uint32_t*>(lg) + fit * a.E;
     for (int t0 = 0; t0 < a.T; t0 += fit) {
+      const int nt = min(fit, a.T - t0);
+      const size_t from = static_cast<size_t>(t0) * a.E, row = static_cast<size_t>(a.E) * 4;
+      copy_rows(reinterpret_cast<uint8_t*>(keys), a.E * 4, a.keys + from, row, nt, a.E * 4);
+      copy_rows(reinterpret_cast<uint8_t*>(lg), a.E * 4, z + from, row, nt, a.E * 4);
+      landed();
       const int t = t0 + warp;
-      if (warp < fit && t < a.T) {
-        uint32_t* k = keys + static_cast<size_t>(warp) * a.E;
-        const float* zr = z + static_cast<size_t>(t) * a.E;
-        for (int e = lane; e < a.E; e += 32) {
-          const float sc = score_sigmoid(__ldcg(zr + e));
-          k[e] = order_key(a.tau ? __fsub_rn(sc, __ldg(a.tau + e)) : sc);
-        }
-        __syncwarp();
-        const int e = min(select_rounds(k, a.E, a.K, lane), a.E - 1);
-        const float sj = lane < a.K ? score_sigmoid(__ldcg(zr + e)) : 0.0f;
+      if (warp < nt) {
+        const int e = min(top_k(keys + static_cast<size_t>(warp) * a.E), a.E - 1);
+        const float sj = lane < a.K ? score_sigmoid(lg[warp * a.E + e]) : 0.0f;
         float sum = 0.0f;
         for (int j = 0; j < a.K; ++j) sum = __fadd_rn(sum, __shfl_sync(0xffffffffu, sj, j));
         if (lane < a.K) {
@@ -506,65 +732,78 @@ struct Few {
           }
         }
       }
-      __syncthreads();
+      sync();
     }
-    const int pairs = a.T * a.K;
-    for (int i = threadIdx.x; i < 128; i += FEW_THREADS) s->bits[i] = 0u;
-    for (int i = threadIdx.x; i < FEW_MAX_PAIRS * FEW_T; i += FEW_THREADS) {
-      s->pair[i / FEW_T][i % FEW_T] = -1;
-      s->gate[i / FEW_T][i % FEW_T] = 0.0f;
-    }
-    __syncthreads();
-    for (int p = threadIdx.x; p < pairs; p += FEW_THREADS)
-      atomicOr(&s->bits[s->sel[p] >> 5], 1u << (s->sel[p] & 31));
-    __syncthreads();
-    // rank of a used expert: bits before it
-    for (int p = threadIdx.x; p < pairs; p += FEW_THREADS) {
+    // pair p (one per thread): the first pair with the same expert, and that one's place
+    const int p = threadIdx.x;
+    int first = p;
+    if (p < pairs) {
       const int e = s->sel[p];
-      int rank = __popc(s->bits[e >> 5] & ((1u << (e & 31)) - 1u));
-      for (int w = 0; w < (e >> 5); ++w) rank += __popc(s->bits[w]);
-      s->expert[rank] = e;
-      s->pair[rank][p / a.K] = static_cast<int16_t>(p);
-      s->gate[rank][p / a.K] = s->sel_gate[p];
+#pragma unroll 4
+      for (int q = 0; q < pairs; q += 4) {  // beyond the last pair: -1
+        const int4 o = *reinterpret_cast<const int4*>(s->sel + q);
+        if (o.w == e) first = min(first, q + 3);
+        if (o.z == e) first = min(first, q + 2);
+        if (o.y == e) first = min(first, q + 1);
+        if (o.x == e) first = min(first, q);
+      }
     }
-    if (threadIdx.x < 32) {
-      int n = 0;
-      for (int w = lane; w < 128; w += 32) n += __popc(s->bits[w]);
-      n = __reduce_add_sync(0xffffffffu, n);
-      if (lane == 0) s->used = n;
+    const uint32_t who = __ballot_sync(0xffffffffu, p < pairs && first == p);
+    if (lane == 0) s->first_uses[warp] = __popc(who);
+    sync();
+    int before = 0, all = 0;
+    for (int w = 0; w < FEW_WARPS; ++w) {
+      if (w < warp) before += s->first_uses[w];
+      all += s->first_uses[w];
+    }
+    if (p < pairs && first == p) {
+      const int r = before + __popc(who & ((1u << lane) - 1u));
+      s->rank[p] = static_cast<int16_t>(r);
+      s->expert[r] = s->sel[p];
+    }
+    if (p == 0) s->used = all;
+    sync();
+    if (p < pairs) {
+      const int r = s->rank[first];
+      s->pair[r][p / a.K] = static_cast<int16_t>(p);
+      s->gate[r][p / a.K] = s->sel_gate[p];
     }
   }
   __device__ void phase_gate_up() {
+    enter(FEW_GATE_UP);
     const int row = (lane & 7) < a.T ? lane & 7 : -1;
     const int pitch = FP8 ? few_pitch(a.L) : few_pitch(a.L * 2);
-    const Row hi = token_row(row, pitch, FP8 ? 2 * lat_lo() : 0), lo = token_row(row, pitch, lat_lo());
+    const Row hi = token_row(row, pitch), lo = token_row(row, pitch, FP8 ? 0 : lat_lo());
     const int per = a.I / 8, tiles = (2 * a.I + BLOCK_M - 1) / BLOCK_M;
+    const int nc = P::boxes(FEW_GATE_UP), nb = a.nb[FEW_GATE_UP];
     int n = 0;
     for (int unit = cta; unit < units(FEW_GATE_UP); unit += ctas, ++n) {
-      int c, end;
-      range(FEW_GATE_UP, unit, &c, &end);
+      // thread i < 64 finishes feature i / 8 of the unit for token i % 8
+      const int i = threadIdx.x, t = i & 7, rank = unit / per;
+      const int p = i < 64 ? s->pair[rank][t] : -1;
+      const int f = unit % per * 8 + (i >> 3);
+      float gs = 1.0f, vs = 1.0f;
       float acc[2][4] = {}, rest[2][4] = {};
-      for (; c < end; ++c) {
+      for (int k = 0; k < nc; k += nb) {
         const uint32_t box = take();
-        multiply<FP8>(box, hi.base + hi.on * c * 128, hi.on * 64, acc);
-        if constexpr (!FP8) multiply<false>(box, lo.base + lo.on * c * 128, lo.on * 64, rest);
+        const int c = k + warp;
+        if (FP8 && k == 0 && i < 64) {
+          const float* sc = reinterpret_cast<const float*>(P::stage_at(ring, slot) + FEW_BOXES);
+          gs = sc[i >> 3], vs = sc[8 + (i >> 3)];
+        }
+        if (warp < nb && c < nc) {
+          multiply<FP8>(box, hi.base + hi.on * c * 128, hi.on * 64, acc);
+          if constexpr (!FP8) multiply<false>(box, lo.base + lo.on * c * 128, lo.on * 64, rest);
+        }
         release();
       }
       float t4[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) t4[k] = (acc[0][k] + acc[1][k]) + (rest[0][k] + rest[1][k]);
       const float* red = join(n, t4);
-      const int i = threadIdx.x, t = i & 7, rank = unit / per;
-      const int p = i < 64 ? s->pair[rank][t] : -1;
       if (p < 0) continue;
-      const int f = unit % per * 8 + (i >> 3);
       float g = total(red, i), v = total(red, i + 64);
-      if constexpr (FP8) {
-        const float* ws = a.s_gu + static_cast<size_t>(s->expert[rank]) * tiles * BLOCK_M +
-                          f / GLU_GROUP * (2 * GLU_GROUP) + f % GLU_GROUP;
-        g *= __ldg(ws) * s->lat_scale[t];
-        v *= __ldg(ws + GLU_GROUP) * s->lat_scale[t];
-      }
+      if constexpr (FP8) g *= gs * s->lat_scale[t], v *= vs * s->lat_scale[t];
       const float h = situ_glu(g, v, a.c, 1.0f / a.c);
       const size_t o = static_cast<size_t>(p) * a.I + f;
       if constexpr (FP8) static_cast<float*>(a.h)[o] = h;
@@ -572,77 +811,74 @@ struct Few {
     }
   }
   __device__ void phase_down() {
+    enter(FEW_DOWN);
     const int pitch = FP8 ? few_pitch(a.I) : few_pitch(a.I * 2);
-    const int nk = a.I / KC, tiles = (a.L + BLOCK_M - 1) / BLOCK_M;
+    const int nk = P::boxes(FEW_DOWN), nb = a.nb[FEW_DOWN];
     const int g = lane >> 2, t2 = (lane & 3) * 2;
+    const int sub = warp / nb, kw = warp % nb;  // which of a stage's experts, and its box
     int n = 0;
     for (int unit = cta; unit < units(FEW_DOWN); unit += ctas, ++n) {
-      int c, end, e0, e1;
-      range(FEW_DOWN, unit, &c, &end);
+      int e0, e1;
       experts(unit, &e0, &e1);
       float sum[4] = {};
-      while (c < end) {  // expert by expert: its part of the reduction, times the tokens' gates
-        const int rank = e0 + c / nk, k0 = c % nk;
-        const int stop = min(end, c - k0 + nk);
-        const Row r = token_row(s->pair[rank][lane & 7], pitch);
+      for (int e = e0; e < e1; e += a.group) {
+        const int rank = e + sub;
+        const bool mine = sub < a.group && rank < e1;
+        const Row r = token_row(mine ? s->pair[rank][lane & 7] : -1, pitch);
         float w0 = 1.0f, w1 = 1.0f;
-        if constexpr (FP8) {
-          const float* ws = a.s_ed + static_cast<size_t>(s->expert[rank]) * tiles * BLOCK_M +
-                            unit / a.splits * 16 + g;
-          w0 = __ldg(ws), w1 = __ldg(ws + 8);
-        }
         float acc[2][4] = {};
-        for (int k = k0; c < stop; ++c, ++k) {
+        for (int k = 0; k < nk; k += nb) {
           const uint32_t box = take();
-          multiply<FP8>(box, r.base + r.on * k * 128, r.on * 64, acc);
+          const int c = k + kw;
+          if (FP8 && k == 0 && mine) {
+            const float* sc =
+                reinterpret_cast<const float*>(P::stage_at(ring, slot) + FEW_BOXES) + sub * 16 + g;
+            w0 = sc[0], w1 = sc[8];
+          }
+          if (mine && c < nk) multiply<FP8>(box, r.base + r.on * c * 128, r.on * 64, acc);
           release();
         }
+        if (mine) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int t = t2 + (k & 1);
-          float f = s->gate[rank][t];
-          if constexpr (FP8) {
-            const int p = s->pair[rank][t];
-            f *= p < 0 ? 0.0f : s->h_scale[p] * (k < 2 ? w0 : w1);
+          for (int k = 0; k < 4; ++k) {  // times the tokens' gates
+            const int t = t2 + (k & 1);
+            float f = s->gate[rank][t];
+            if constexpr (FP8) {
+              const int p = s->pair[rank][t];
+              f *= p < 0 ? 0.0f : s->h_scale[p] * (k < 2 ? w0 : w1);
+            }
+            sum[k] = fmaf(acc[0][k] + acc[1][k], f, sum[k]);
           }
-          sum[k] = fmaf(acc[0][k] + acc[1][k], f, sum[k]);
         }
       }
       const float* red = join(n, sum);
+      // u starts at zero and receives at most two parts, so that their order does not matter
       const int i = threadIdx.x, t = i & 7;
       if (i < 128 && t < a.T)
-        a.u[(static_cast<size_t>(unit % a.splits) * a.T + t) * a.L + unit / a.splits * 16 + (i >> 3)] =
-            total(red, i);
+        atomicAdd(a.u + static_cast<size_t>(t) * a.L + unit / a.splits * 16 + (i >> 3), total(red, i));
     }
   }
   __device__ void phase_out() {
-    const int pitch = few_pitch((a.L + a.sw) * 2);
-    const Row r = token_row((lane & 7) < a.T ? lane & 7 : -1, pitch);
+    enter(FEW_OUT);
+    const Row r = token_row((lane & 7) < a.T ? lane & 7 : -1, a.out_pitch);
     const int nz = a.L / 64, t2 = (lane & 3) * 2;
     const float r0 = t2 < a.T ? s->rstd[t2] : 0.0f, r1 = t2 + 1 < a.T ? s->rstd[t2 + 1] : 0.0f;
+    const int nc = P::boxes(FEW_OUT), nb = a.nb[FEW_OUT];
     int n = 0;
     for (int unit = cta; unit < units(FEW_OUT); unit += ctas, ++n) {
-      int c, end;
-      range(FEW_OUT, unit, &c, &end);
-      float acc[2][4] = {};
-      float sum[4] = {};
-      for (; c < end && c < nz; ++c) {
+      float az[2][4] = {}, as[2][4] = {};
+      for (int k = 0; k < nc; k += nb) {
         const uint32_t box = take();
-        multiply<false>(box, r.base + r.on * c * 128, r.on * 64, acc);
+        const int c = k + warp;
+        const uint32_t b = r.base + r.on * c * 128;
+        if (warp < nb && c < nz) multiply<false>(box, b, r.on * 64, az);
+        else if (warp < nb && c < nc) multiply<false>(box, b, r.on * 64, as);
         release();
       }
+      float sum[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        sum[k] = (acc[0][k] + acc[1][k]) * (k & 1 ? r1 : r0);
-        acc[0][k] = acc[1][k] = 0.0f;
-      }
-      for (; c < end; ++c) {
-        const uint32_t box = take();
-        multiply<false>(box, r.base + r.on * c * 128, r.on * 64, acc);
-        release();
-      }
-#pragma unroll
-      for (int k = 0; k < 4; ++k) sum[k] += acc[0][k] + acc[1][k];
+      for (int k = 0; k < 4; ++k)
+        sum[k] = fmaf(az[0][k] + az[1][k], k & 1 ? r1 : r0, as[0][k] + as[1][k]);
       const float* red = join(n, sum);
       const int i = threadIdx.x, t = i & 7;
       if (i < 128 && t < a.T) {
@@ -655,73 +891,81 @@ struct Few {
     }
   }
 
-  __device__ bool run(uint8_t* rings) {
-    produce_phases(FEW_IN, FEW_ROUTER);
+  __device__ bool run() {
+    for (int i = threadIdx.x; i < FEW_MAX_PAIRS * FEW_T; i += FEW_THREADS) {
+      (&s->pair[0][0])[i] = -1;
+      (&s->gate[0][0])[i] = 0.0f;
+    }
+    for (int i = threadIdx.x; i < FEW_MAX_PAIRS; i += FEW_THREADS) s->sel[i] = -1;
+    // u, for DOWN's additions (three barriers from here)
+    for (int i = cta * FEW_THREADS + threadIdx.x; i < a.T * a.L / 4; i += ctas * FEW_THREADS)
+      reinterpret_cast<float4*>(a.u)[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     stage_x();
-    __syncthreads();
     phase_in();
-    if (!grid_barrier(1)) return false;
+    if (!grid_barrier()) return false;
+    if (threadIdx.x == 0) ptx::mbar_arrive(&s->idle);
     stage_lat();
-    __syncthreads();
     phase_router();
-    if (!grid_barrier(2)) return false;
-    // the rings are empty now: the selection's scratch
-    int fit = FEW_WARPS * a.slots * FEW_BOX / (a.E * 4);
-    select(reinterpret_cast<uint32_t*>(rings), fit < FEW_WARPS ? fit : FEW_WARPS);
-    ptx::fence_proxy_async_smem();  // before the next loads into the rings
-    __syncthreads();
+    if (!grid_barrier()) return false;
+    select();
+    ptx::fence_proxy_async_smem();  // before the next loads into the ring
+    sync();
+    if (threadIdx.x == 0) ptx::mbar_arrive(&s->routed);
     if (a.logits_out)
       for (int i = cta * FEW_THREADS + threadIdx.x; i < a.T * a.E; i += ctas * FEW_THREADS)
         a.logits_out[i] = __ldcg((a.logits_in ? a.logits_in : a.logits) + i);
-    produce_phases(FEW_GATE_UP, FEW_OUT);
+    stage_codes();
     phase_gate_up();
-    if (!grid_barrier(3)) return false;
+    if (!grid_barrier()) return false;
+    if constexpr (FP8) {
+      quantize_h();
+      if (!grid_barrier()) return false;
+    }
     stage_h();
-    __syncthreads();
     phase_down();
-    if (!grid_barrier(4)) return false;
+    if (!grid_barrier()) return false;
     stage_z();
-    __syncthreads();
     phase_out();
     return true;
   }
 };
 
 template <bool FP8>
-__global__ void __launch_bounds__(FEW_THREADS, 1)
+__global__ void __launch_bounds__(FEW_THREADS + 32, 1)
 few_kernel(const __grid_constant__ FewMaps maps, const __grid_constant__ FewArgs a) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = ptx::smem_u32(smem_raw);
-  uint8_t* rings = smem_raw + (((raw + 1023u) & ~1023u) - raw);
-  FewTables* s = reinterpret_cast<FewTables*>(rings + FEW_WARPS * a.slots * FEW_BOX + a.tok_bytes);
-  Few<FP8> f(a, maps);
-  f.s = s;
-  f.warp = threadIdx.x >> 5;
-  f.lane = threadIdx.x & 31;
-  f.cta = blockIdx.x;
-  f.ctas = gridDim.x;
-  f.ring = rings + f.warp * a.slots * FEW_BOX;
-  f.bars = s->bars + f.warp * FEW_MAX_SLOTS;
-  f.tok = rings + FEW_WARPS * a.slots * FEW_BOX;
-  if (threadIdx.x < FEW_WARPS * FEW_MAX_SLOTS) ptx::mbar_init(&s->bars[threadIdx.x], 1);
+  uint8_t* ring = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+  uint8_t* tok = ring + a.stages * few_stage_bytes(FP8);
+  FewTables* s = reinterpret_cast<FewTables*>(tok + a.tok_bytes);
   if (threadIdx.x == 0) {
+    for (int i = 0; i < a.more; ++i) {
+      ptx::mbar_init(&s->full[i], 1);
+      ptx::mbar_init(&s->empty[i], FEW_WARPS);
+    }
+    ptx::mbar_init(&s->idle, 1);
+    ptx::mbar_init(&s->routed, 1);
+    ptx::mbar_init(&s->staged, 1);
     s->zero = make_uint4(0u, 0u, 0u, 0u);
     s->used = 0;
     s->abort = 0;
+    ptx::fence_mbar_init();
   }
-  ptx::fence_mbar_init();
   __syncthreads();
-  f.run(rings);
-  // a warp that gave up still waits (bounded) for its boxes in flight
-  for (; f.used != f.made; ++f.used) {
-    const uint32_t slot = f.used % a.slots;
-    const uint64_t t0 = ptx::globaltimer_ns();
-    while (!ptx::mbar_try_wait(&f.bars[slot], (f.used / a.slots) & 1u))
-      if (ptx::globaltimer_ns() - t0 > a.timeout_ns) break;
+  if (threadIdx.x >= FEW_THREADS) {
+    if (threadIdx.x == FEW_THREADS) few_load(FewPlan<FP8>(a, s), maps, ring);
+  } else {
+    Few<FP8> f(a, s);
+    f.warp = threadIdx.x >> 5;
+    f.lane = threadIdx.x & 31;
+    f.ring = ring;
+    f.tok = tok;
+    f.run();
   }
   __syncthreads();
   // the last CTA to leave resets the words of the barrier for the next call
   if (threadIdx.x == 0) {
+    if (s->abort) atomicExch(a.head + 3, 1u);
     __threadfence();
     if (atomicAdd(a.head + 2, 1u) == gridDim.x - 1) {
       a.head[1] = 0u;
@@ -733,11 +977,11 @@ few_kernel(const __grid_constant__ FewMaps maps, const __grid_constant__ FewArgs
 }
 
 struct FewLayout {
-  size_t lat, hs, logits, h, u, total;
+  size_t lat, hs, logits, keys, h, u, lat8, lat_scale, h8, h_scale, total;
 };
 static FewLayout few_layout(const lmoe_dims& D) {
   FewLayout W{};
-  size_t off = 256;
+  size_t off = LMOE_FEW_HEADER_BYTES;
   auto take = [&](size_t bytes) {
     const size_t o = off;
     off += (bytes + 255) / 256 * 256;
@@ -747,32 +991,54 @@ static FewLayout few_layout(const lmoe_dims& D) {
   W.lat = take(T * D.L * 4);
   W.hs = take(T * sw * 2);
   W.logits = take(T * D.E * 4);
+  W.keys = take(T * D.E * 4);
   W.h = take(T * D.K * D.I * 4);
-  W.u = take(FEW_MAX_SPLITS * T * D.L * 4);
+  W.u = take(T * D.L * 4);
+  if (D.expert_fp8) {
+    W.lat8 = take(T * D.L);
+    W.lat_scale = take(T * 4);
+    W.h8 = take(T * D.K * D.I);
+    W.h_scale = take(T * D.K * 4);
+  }
   W.total = off;
   return W;
 }
 
-// Shared memory of the tokens' operands: the largest of the phases'.
-static size_t few_tok_bytes(const lmoe_dims& D) {
-  const size_t T = D.T, sw = D.S > 0 ? static_cast<size_t>(D.S) * D.Is : 0;
-  const size_t in = T * few_pitch(D.d * 2);
-  const size_t lat = T * (2 * few_pitch(D.L * 2) + (D.expert_fp8 ? few_pitch(D.L) : 0));
-  const size_t h = T * D.K * few_pitch(D.expert_fp8 ? D.I : D.I * 2);
-  const size_t out = T * few_pitch((D.L + static_cast<int>(sw)) * 2);
-  size_t b = in > lat ? in : lat;
-  b = b > h ? b : h;
-  b = b > out ? b : out;
-  return (b + 15) / 16 * 16;
-}
-
+// Shared memory: the tokens' operands take the largest of the phases' needs, the ring the rest;
+// while the experts run, whose operands may be smaller (e4m3 codes), the ring has that too.
+struct FewSmem {
+  size_t tok;
+  int stages, more, more_off, out_pitch;
+};
 constexpr size_t FEW_SMEM_MAX = 232448 - 1024;  // less the alignment's slack
 
-static int few_slots(const lmoe_dims& D) {
-  const size_t fixed = few_tok_bytes(D) + sizeof(FewTables);
-  if (fixed >= FEW_SMEM_MAX) return 0;
-  const size_t n = (FEW_SMEM_MAX - fixed) / (FEW_WARPS * FEW_BOX);
-  return static_cast<int>(n < FEW_MAX_SLOTS ? n : FEW_MAX_SLOTS);
+static FewSmem few_smem(const lmoe_dims& D) {
+  const size_t T = D.T, sw = D.S > 0 ? static_cast<size_t>(D.S) * D.Is : 0;
+  const bool fp8 = D.expert_fp8 != 0;
+  auto larger = [](size_t a, size_t b) { return a > b ? a : b; };
+  FewSmem M{};
+  // OUT: a row holds [gamma u | hs] in bf16, and u in fp32 before that
+  M.out_pitch = few_pitch(static_cast<int>(larger((D.L + sw) * 2, D.L * size_t{4})));
+  const size_t hi_lo = T * 2 * few_pitch(D.L * 2);
+  const size_t experts = larger(fp8 ? T * few_pitch(D.L) : hi_lo,
+                                T * D.K * few_pitch(fp8 ? D.I : D.I * 2));
+  M.tok = larger(larger(T * few_pitch(D.d * 2), hi_lo), larger(experts, T * M.out_pitch));
+  M.tok = (M.tok + 15) / 16 * 16;
+  const size_t fixed = M.tok + sizeof(FewTables), stage = few_stage_bytes(fp8);
+  if (fixed >= FEW_SMEM_MAX) return M;
+  M.stages = static_cast<int>((FEW_SMEM_MAX - fixed) / stage);
+  if (M.stages > FEW_MAX_STAGES) M.stages = FEW_MAX_STAGES;
+  M.more_off = static_cast<int>((experts + 1023) / 1024 * 1024);
+  M.more = M.stages;
+  if (static_cast<size_t>(M.more_off) < M.tok) M.more += static_cast<int>((M.tok - M.more_off) / stage);
+  if (M.more > FEW_MAX_STAGES) M.more = FEW_MAX_STAGES;
+  return M;
+}
+
+// Boxes of a stage for a reduction of n: as few stages as eight boxes allow, equally full.
+static int few_boxes(int n) {
+  const int stages = static_cast<int>(ceil_div(n, FEW_WARPS));
+  return static_cast<int>(ceil_div(n, stages));
 }
 
 static int few_supported(const lmoe_dims* D) {
@@ -785,8 +1051,8 @@ static int few_supported(const lmoe_dims* D) {
   const int64_t ed = static_cast<int64_t>(D->E) * ceil_div(D->L, BLOCK_M) * BLOCK_M *
                      ceil_div(D->I, 64);
   if (gu >= (int64_t{1} << 31) || ed >= (int64_t{1} << 31)) return LMOE_ERR_UNSUPPORTED;
-  const int slots = few_slots(*D);
-  if (slots < FEW_MIN_SLOTS || static_cast<size_t>(slots) * FEW_WARPS * FEW_BOX < D->E * size_t{4})
+  const int stages = few_smem(*D).stages;
+  if (stages < FEW_MIN_STAGES || stages * size_t{FEW_BOXES} < D->E * size_t{8})
     return LMOE_ERR_UNSUPPORTED;
   return LMOE_OK;
 }
@@ -800,7 +1066,7 @@ static int launch_few(const FewMaps& maps, const FewArgs& a, int sms, size_t sme
     return LMOE_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(sms));
-  cfg.blockDim = dim3(FEW_THREADS);
+  cfg.blockDim = dim3(FEW_THREADS + 32);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -875,8 +1141,12 @@ int lmoe_forward_few(const lmoe_dims* dims, const void* packed, const void* x,
       a.splits = n;
     }
   }
-  a.slots = few_slots(D);
-  a.tok_bytes = static_cast<int>(few_tok_bytes(D));
+  const FewSmem M = few_smem(D);
+  a.stages = M.stages;
+  a.more = M.more;
+  a.more_off = M.more_off;
+  a.out_pitch = M.out_pitch;
+  a.tok_bytes = static_cast<int>(M.tok);
   a.x = static_cast<const __nv_bfloat16*>(x);
   a.resid = static_cast<const __nv_bfloat16*>(residual);
   a.y = static_cast<__nv_bfloat16*>(y);
@@ -891,29 +1161,64 @@ int lmoe_forward_few(const lmoe_dims* dims, const void* packed, const void* x,
   a.s_gu = reinterpret_cast<const float*>(pk + P.sgu);
   a.s_ed = reinterpret_cast<const float*>(pk + P.sed);
   a.head = reinterpret_cast<uint32_t*>(ws);
-  a.lat = reinterpret_cast<float*>(ws + W.lat);
+  a.lat = reinterpret_cast<__nv_bfloat16*>(ws + W.lat);
   a.hs = reinterpret_cast<__nv_bfloat16*>(ws + W.hs);
   a.logits = reinterpret_cast<float*>(ws + W.logits);
+  a.keys = reinterpret_cast<uint32_t*>(ws + W.keys);
   a.h = ws + W.h;
   a.u = reinterpret_cast<float*>(ws + W.u);
+  a.lat8 = ws + W.lat8;
+  a.lat_scale = reinterpret_cast<float*>(ws + W.lat_scale);
+  a.h8 = ws + W.h8;
+  a.h_scale = reinterpret_cast<float*>(ws + W.h_scale);
   a.timeout_ns = wait_limit_ns();
   a.inject_stall = inject_stall() ? 1 : 0;
-  const int per = D.expert_fp8 ? 2 : 1;  // e4m3: two codes per 2-byte unit of the tensor maps
-  const int64_t rows_gu = static_cast<int64_t>(D.E) * ceil_div(2 * D.I, BLOCK_M) * BLOCK_M *
-                          (D.L / (64 * per));
-  const int64_t rows_ed = static_cast<int64_t>(D.E) * ceil_div(D.L, BLOCK_M) * BLOCK_M *
-                          (D.I / (64 * per));
+  const int kc = D.expert_fp8 ? 128 : 64;
+  a.nb[FEW_IN] = few_boxes(D.d / 64);
+  a.nb[FEW_ROUTER] = few_boxes(D.L / 64);
+  a.nb[FEW_GATE_UP] = few_boxes(D.L / kc);
+  a.nb[FEW_DOWN] = few_boxes(D.I / kc);
+  a.nb[FEW_OUT] = few_boxes((D.L + sw) / 64);
+  // a short expert reduction shares its stage with other experts'
+  a.group = D.I / kc == a.nb[FEW_DOWN] ? FEW_WARPS / a.nb[FEW_DOWN] : 1;
+  // maps with the reduction in units of 64 x 2 bytes as a dimension, so that one load takes several
+  // boxes, each 16 rows x 128 bytes: [rows][K] as {64, rows, K / 64}; with 8 gate and 8 value rows,
+  // GLU_GROUP rows apart, {64, rows, 2, K / 64}; tiled expert weights as {64, row of a tile, (2,)
+  // column tile, row tile}
+  auto rows_map = [](CUtensorMap* m, const void* p, int64_t rows, int K, int nb) {
+    const uint64_t dims[3] = {64, static_cast<uint64_t>(rows), static_cast<uint64_t>(K / 64)};
+    const uint64_t strides[2] = {static_cast<uint64_t>(K) * 2, 128};
+    const uint32_t box[3] = {64, 16, static_cast<uint32_t>(nb)};
+    return make_tmap_boxes(m, p, 3, dims, strides, box);
+  };
+  const uint64_t tile = BLOCK_M * 128;
+  const uint64_t gu_k = D.L / kc, gu_n = static_cast<uint64_t>(D.E) * ceil_div(2 * D.I, BLOCK_M);
+  const uint64_t ed_k = D.I / kc, ed_n = static_cast<uint64_t>(D.E) * ceil_div(D.L, BLOCK_M);
+  const uint64_t gu_dims[5] = {64, BLOCK_M - GLU_GROUP, 2, gu_k, gu_n};
+  const uint64_t gu_strides[4] = {128, GLU_GROUP * 128, tile, gu_k * tile};
+  const uint32_t gu_box[5] = {64, 8, 2, static_cast<uint32_t>(a.nb[FEW_GATE_UP]), 1};
+  const uint64_t ed_dims[4] = {64, BLOCK_M, ed_k, ed_n};
+  const uint64_t ed_strides[3] = {128, tile, ed_k * tile};
+  const uint32_t ed_box[4] = {64, 16, static_cast<uint32_t>(a.nb[FEW_DOWN]), 1};
   FewMaps m;
   memset(&m, 0, sizeof m);
-  if (!make_tmap_bf16(&m.down, pk + P.w1, D.L, D.d, D.d, 16) ||
-      (sw > 0 && !make_tmap_glu8(&m.shared, pk + P.w1 + static_cast<size_t>(D.L) * D.d * 2,
-                                 sw / GLU_GROUP, D.d, D.d)) ||
-      !make_tmap_bf16(&m.router, pk + P.wr, D.E, D.L, D.L, 16) ||
-      !make_tmap_glu8(&m.gate_up, pk + P.wgu, rows_gu / (2 * GLU_GROUP), 64, 64) ||
-      !make_tmap_bf16(&m.edown, pk + P.wed, rows_ed, 64, 64, 16) ||
-      !make_tmap_bf16(&m.out, pk + P.w2, D.d, D.L + sw, D.L + sw, 16))
+  if (sw > 0) {
+    const uint64_t dims[4] = {64, static_cast<uint64_t>(2 * sw - GLU_GROUP), 2,
+                              static_cast<uint64_t>(D.d / 64)};
+    const uint64_t strides[3] = {static_cast<uint64_t>(D.d) * 2,
+                                 static_cast<uint64_t>(GLU_GROUP) * D.d * 2, 128};
+    const uint32_t box[4] = {64, 8, 2, static_cast<uint32_t>(a.nb[FEW_IN])};
+    if (!make_tmap_boxes(&m.shared, pk + P.w1 + static_cast<size_t>(D.L) * D.d * 2, 4, dims,
+                         strides, box))
+      return LMOE_ERR_CUDA;
+  }
+  if (!rows_map(&m.down, pk + P.w1, D.L, D.d, a.nb[FEW_IN]) ||
+      !rows_map(&m.router, pk + P.wr, D.E, D.L, a.nb[FEW_ROUTER]) ||
+      !rows_map(&m.out, pk + P.w2, D.d, D.L + sw, a.nb[FEW_OUT]) ||
+      !make_tmap_boxes(&m.gate_up, pk + P.wgu, 5, gu_dims, gu_strides, gu_box) ||
+      !make_tmap_boxes(&m.edown, pk + P.wed, 4, ed_dims, ed_strides, ed_box))
     return LMOE_ERR_CUDA;
-  const size_t smem = 1024 + static_cast<size_t>(a.slots) * FEW_WARPS * FEW_BOX + a.tok_bytes +
+  const size_t smem = 1024 + static_cast<size_t>(a.stages) * few_stage_bytes(D.expert_fp8 != 0) + a.tok_bytes +
                       sizeof(FewTables);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int out = D.expert_fp8 ? launch_few<true>(m, a, sms, smem, st)

@@ -850,22 +850,23 @@ bool make_tmap_bf16(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t col
   return r == CUDA_SUCCESS;
 }
 
-// Gate and value rows interleaved in groups of GLU_GROUP, as [group][gate, value][GLU_GROUP rows]
-// of `cols` bf16 (row distance ld): boxes of 64 columns x 8 gate rows and the same features' 8
-// value rows, 128-byte swizzled.
-bool make_tmap_glu8(CUtensorMap* m, const void* ptr, uint64_t groups, uint64_t cols, uint64_t ld) {
+bool make_tmap_boxes(CUtensorMap* m, const void* ptr, int rank, const uint64_t* dims,
+                     const uint64_t* strides, const uint32_t* box) {
   auto enc = tmap_encoder();
-  if (!enc || groups == 0 || cols == 0 || (reinterpret_cast<uintptr_t>(ptr) & 15u) != 0 ||
-      (ld * 2) % 16 != 0)
-    return false;
-  const cuuint64_t gdim[4] = {cols, GLU_GROUP, 2, groups};
-  const cuuint64_t gstride[3] = {ld * 2, GLU_GROUP * ld * 2, 2 * GLU_GROUP * ld * 2};
-  const cuuint32_t box[4] = {static_cast<cuuint32_t>(BLOCK_K), 8, 2, 1};
-  const cuuint32_t estride[4] = {1, 1, 1, 1};
-  const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), gdim,
-                         gstride, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (!enc || rank < 2 || rank > 5 || (reinterpret_cast<uintptr_t>(ptr) & 15u) != 0) return false;
+  cuuint64_t gdim[5], gstride[4];
+  cuuint32_t b[5], estride[5];
+  for (int i = 0; i < rank; ++i) {
+    if (dims[i] == 0) return false;
+    gdim[i] = dims[i];
+    b[i] = box[i];
+    estride[i] = 1;
+    if (i > 0) gstride[i - 1] = strides[i - 1];
+  }
+  const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(rank),
+                         const_cast<void*>(ptr), gdim, gstride, b, estride,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
 

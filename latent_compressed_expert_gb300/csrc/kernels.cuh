@@ -144,7 +144,10 @@ int launch_grouped_gemm(const void* W, const void* X, uint64_t x_rows, int x_ld,
 // 64 x box_rows box and the 128-byte swizzle.  Returns false on failure.
 bool make_tmap_bf16(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols, uint64_t ld,
                     uint32_t box_rows);
-bool make_tmap_glu8(CUtensorMap* m, const void* ptr, uint64_t groups, uint64_t cols, uint64_t ld);
+// Any bf16 tensor of up to five dimensions (strides in bytes, multiples of 16, from the second
+// dimension on; they may overlap), 128-byte swizzled boxes of 64 elements along the first.
+bool make_tmap_boxes(CUtensorMap* m, const void* ptr, int rank, const uint64_t* dims,
+                     const uint64_t* strides, const uint32_t* box);
 bool make_tmap_bf16_out32(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols,
                           uint64_t ld);
 
