@@ -2,22 +2,27 @@
 // the linear layers' forward (linear_fwd.cu) and gradients (linear_bwd.cu).
 //
 //   MODE_FWD  p[M, N]  = x[M, K] . w[N, K]^T         both operands K-major
-//   MODE_DX   dx[M, K] = dp[M, N] . w[N, K]          the second operand MN-major
+//   MODE_DX   dx[M, K] = dp[M, N] . w[N, K]          the weights MN-major
 //   MODE_DW   dw[N, K] = dp[M, N]^T . x[M, K]        both operands MN-major
-// Below, every mode is C[R, C] = A . B^T reduced over D.  A K-major operand is loaded in boxes of
-// 64 reduction elements (128 bytes; 128 elements of e4m3) by its rows, an MN-major one in boxes
-// of 64 of its columns by 64 reduction rows; TMA fills what lies outside with zeros, so no size
-// has to be a multiple of a tile.
+// A K-major operand is loaded in boxes of 64 reduction elements (128 bytes; 128 elements of e4m3)
+// by its rows, an MN-major one in boxes of 64 of its columns by 64 reduction rows; TMA fills what
+// lies outside with zeros, so no size has to be a multiple of a tile.
+//
+// The MMA's operands are P, on its 128-row side (256 over an SM pair), and Q, its bn columns.  In
+// MODE_FWD and MODE_DX P is the weights and Q the rows of x or dp: whatever the number of rows, all
+// that a stage brings of the weights is used, and bn = 16 .. 256 is cut to divide the rows evenly.
+// The accumulator is then the output tile transposed, and is turned round in shared memory.  In
+// MODE_DW P is dp^T, Q is x^T, and the accumulator the output tile itself.
 //
 // Two kernels, chosen by linear_plan:
-//   linear_pair_kernel   256 x BN tiles over SM pairs (cta_group::2), persistent, two
-//                        accumulator sets, so that one tile is written while the next is
-//                        computed.  An SM stages 16 KB of A and BN / 2 rows of B per K-block.
-//   linear_tile_kernel   128 x BN tiles, one per cluster of ks CTAs that split the reduction
+//   linear_pair_kernel   256 x bn tiles over SM pairs (cta_group::2), persistent, two accumulator
+//                        sets, so that one tile is written while the next is computed.  An SM
+//                        stages 16 KB of P and bn / 2 rows of Q per K-block.
+//   linear_tile_kernel   128 x bn tiles, one per cluster of ks CTAs that split the reduction
 //                        between them and add their parts through distributed shared memory in
-//                        rank order (no scratch, no second kernel, a fixed order).  Two CTAs
-//                        fit an SM.  For problems with too few tiles to fill the SM pairs, down
-//                        to one row, where the time is the weights' way from HBM.
+//                        rank order (no scratch, no second kernel, a fixed order).  For problems
+//                        with too few tiles to fill the SM pairs, down to one row, where the time
+//                        is the weights' way from HBM.
 // Every wait is bounded; on time-out a role records an error bit, raises the CTA's abort flag,
 // waits for its copies in flight and the kernel ends with its output unspecified.
 #pragma once
@@ -49,29 +54,34 @@ struct LinearArgs {
   __nv_bfloat16* pre;   // pre-activations [R, rows of B], or null
   int64_t ldp;
   float c;              // SiTU-GLU cap
+  // the plan
+  int bn;               // columns of the MMA
+  int stages;           // of 16 KB of P and bn (SM pair: bn / 2) rows of Q
   int ks;               // linear_tile_kernel: CTAs of a cluster
   int inject_stall;     // test hook: the MMA role first waits on a barrier nobody arrives on
   uint32_t* err;
   unsigned long long timeout_ns;
 };
 
-constexpr int LINEAR_THREADS = 192;
+constexpr int LINEAR_THREADS = 320;  // TMA, MMA and eight epilogue warps (two per TMEM lane quarter)
 constexpr int LINEAR_RASTER = 16;  // row tiles that sweep the column tiles together
 
 template <int MODE>
-struct LinearMajor {
-  static constexpr bool A_MN = MODE == MODE_DW;
-  static constexpr bool B_MN = MODE != MODE_FWD;
+struct LinearMode_ {
+  static constexpr bool SWAP = MODE != MODE_DW;    // the accumulator is the output transposed
+  static constexpr bool P_MN = MODE != MODE_FWD, Q_MN = MODE == MODE_DW;
 };
 
 template <int MODE, bool FP8>
-constexpr uint32_t linear_idesc(int M, int N) {
+__host__ __device__ constexpr uint32_t linear_idesc(int M, int N) {
   return FP8 ? ptx::idesc_e4m3_f32(M, N)
-             : ptx::idesc_bf16_f32(M, N) | (LinearMajor<MODE>::A_MN ? 1u << 15 : 0u) |
-                   (LinearMajor<MODE>::B_MN ? 1u << 16 : 0u);
+             : ptx::idesc_bf16_f32(M, N) | (LinearMode_<MODE>::P_MN ? 1u << 15 : 0u) |
+                   (LinearMode_<MODE>::Q_MN ? 1u << 16 : 0u);
 }
 
+constexpr int LINEAR_P_BYTES = BLOCK_M * 128;       // a CTA's part of P in a stage
 constexpr int LINEAR_BOX_BYTES = 64 * BLOCK_K * 2;  // one MN-major box
+constexpr int LINEAR_MAX_STAGES = 8;
 template <bool FP8>
 constexpr int LINEAR_KSTEP = FP8 ? 128 : 64;        // reduction elements per K-block
 
@@ -99,15 +109,24 @@ __device__ __forceinline__ uint4 linear_pack8(const float (&v)[8]) {
   return w;
 }
 
-__device__ __forceinline__ void linear_scale_bias8(const LinearArgs& g, int brow, float xs,
-                                                   bool fp8, float (&v)[8]) {
-  if (fp8) {
+// Scales and bias of eight consecutive rows of B, which a thread keeps over the rows it stores.
+struct LinearCols {
+  float ws[8], bias[8];
+};
+template <bool FP8>
+__device__ __forceinline__ void linear_cols(const LinearArgs& g, int brow, bool live, LinearCols* c) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] *= xs * __ldg(g.ws + brow + i);
+  for (int i = 0; i < 8; ++i) {
+    if (FP8) c->ws[i] = live ? __ldg(g.ws + brow + i) : 0.0f;
+    c->bias[i] = live && g.bias ? __ldg(g.bias + brow + i) : 0.0f;
   }
-  if (g.bias) {
+}
+template <bool FP8>
+__device__ __forceinline__ void linear_scale_bias8(const LinearCols& c, float xs, float (&v)[8]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] += __ldg(g.bias + brow + i);
+  for (int i = 0; i < 8; ++i) {
+    if (FP8) v[i] *= xs * c.ws[i];
+    v[i] += c.bias[i];
   }
 }
 
@@ -119,11 +138,12 @@ __device__ __forceinline__ uint4 linear_resid8(const LinearArgs& g, int row, int
 // Eight columns of one output row: scales, bias, the bf16 copy of the pre-activation, the
 // activation, the residual (r: already loaded), one rounding to bf16.
 template <int MODE, bool FP8>
-__device__ __forceinline__ void linear_store8(const LinearArgs& g, int row, int col, float xs,
-                                              float (&v)[8], const uint4& r) {
+__device__ __forceinline__ void linear_store8(const LinearArgs& g, int row, int col,
+                                              const LinearCols& c, float xs, float (&v)[8],
+                                              const uint4& r) {
   const size_t rr = static_cast<size_t>(row);
   if constexpr (MODE == MODE_FWD) {
-    linear_scale_bias8(g, col, xs, FP8, v);
+    linear_scale_bias8<FP8>(c, xs, v);
     if (g.pre) *reinterpret_cast<uint4*>(g.pre + rr * g.ldp + col) = linear_pack8(v);
     if (g.act != LMOE_ACT_NONE) {
 #pragma unroll
@@ -151,12 +171,13 @@ __device__ __forceinline__ void linear_store8(const LinearArgs& g, int row, int 
 
 // The same for eight features of a gated layer: gate and value pre-activations.
 template <bool FP8>
-__device__ __forceinline__ void linear_store_glu8(const LinearArgs& g, int row, int col, float xs,
-                                                  float inv_c, float (&a)[8], float (&b)[8],
-                                                  const uint4& r) {
+__device__ __forceinline__ void linear_store_glu8(const LinearArgs& g, int row, int col,
+                                                  const LinearCols& ca, const LinearCols& cb,
+                                                  float xs, float inv_c, float (&a)[8],
+                                                  float (&b)[8], const uint4& r) {
   const size_t rr = static_cast<size_t>(row);
-  linear_scale_bias8(g, col, xs, FP8, a);
-  linear_scale_bias8(g, g.glu_off + col, xs, FP8, b);
+  linear_scale_bias8<FP8>(ca, xs, a);
+  linear_scale_bias8<FP8>(cb, xs, b);
   if (g.pre) {
     *reinterpret_cast<uint4*>(g.pre + rr * g.ldp + col) = linear_pack8(a);
     *reinterpret_cast<uint4*>(g.pre + rr * g.ldp + g.glu_off + col) = linear_pack8(b);
@@ -187,69 +208,105 @@ __device__ __forceinline__ LinearTile linear_tile(int tile, int mt, int nt, int 
   return {(first + local % gm) * TM, local / gm * TN};
 }
 
-// ------------------------------------------------------------------------- one-SM tiles
-template <int BN>
-struct LinearTileCfg {
-  static constexpr int A_BYTES = BLOCK_M * 128;
-  static constexpr int STAGE_BYTES = A_BYTES + BN * 128;
-  static constexpr int STAGES = BN == 64 ? 4 : 3;
-  static constexpr int BAR_OFF = STAGES * STAGE_BYTES;
-  static constexpr int NUM_BARS = 2 * STAGES + 1;
-  static constexpr int MISC_OFF = BAR_OFF + NUM_BARS * 8;
-  static constexpr int SMEM_BYTES = MISC_OFF + 16 + 1024;  // + slack for 1024 alignment
-  // fp32 partial tile over the stages once they are done with; rows padded by one float4,
-  // so that the eight rows that a quarter warp writes fall into different banks
-  static constexpr int LDS = BN + 4;
-  static_assert(BLOCK_M * LDS * 4 <= BAR_OFF, "the partial tile fits the stages");
-  static_assert(2 * (SMEM_BYTES + 1024) <= 228 * 1024, "two CTAs per SM");
+// What the kernels share: shared memory as stages (1024-byte aligned), barriers behind them.
+struct LinearSmem {
+  uint8_t* base;
+  uint64_t *full, *empty, *extra;
+  uint32_t* tmem_slot;
+  volatile int* abort_flag;
 };
+constexpr int LINEAR_BARS = 2 * LINEAR_MAX_STAGES + 5;
+constexpr int LINEAR_MISC = LINEAR_BARS * 8 + 16;  // bytes behind the stages
+__device__ __forceinline__ LinearSmem linear_smem(uint8_t* raw, int stage_area) {
+  const uint32_t addr = ptx::smem_u32(raw);
+  LinearSmem m;
+  m.base = raw + (((addr + 1023u) & ~1023u) - addr);
+  m.full = reinterpret_cast<uint64_t*>(m.base + stage_area);
+  m.empty = m.full + LINEAR_MAX_STAGES;
+  m.extra = m.empty + LINEAR_MAX_STAGES;
+  m.tmem_slot = reinterpret_cast<uint32_t*>(m.extra + 5);
+  m.abort_flag = reinterpret_cast<volatile int*>(m.tmem_slot + 1);
+  return m;
+}
 
-template <int BN, int MODE, bool FP8, bool GLU>
+// One K-block's MMAs: 32 bytes of K-major rows, 16 rows of MN-major boxes, at a time.
+template <int MODE, bool FP8, bool PAIR>
+__device__ __forceinline__ void linear_mma(uint32_t d, uint32_t sp, uint32_t sq, uint32_t idesc,
+                                           bool first) {
+  using T = LinearMode_<MODE>;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint64_t da = T::P_MN ? ptx::smem_desc_sw128_mn(sp + k * 2048, LINEAR_BOX_BYTES)
+                                : ptx::smem_desc_sw128(sp + k * 32);
+    const uint64_t db = T::Q_MN ? ptx::smem_desc_sw128_mn(sq + k * 2048, LINEAR_BOX_BYTES)
+                                : ptx::smem_desc_sw128(sq + k * 32);
+    const uint32_t acc = first && k == 0 ? 0u : 1u;
+    if constexpr (FP8 && PAIR) ptx::umma_e4m3_pair(d, da, db, idesc, acc);
+    else if constexpr (FP8) ptx::umma_e4m3(d, da, db, idesc, acc);
+    else if constexpr (PAIR) ptx::umma_bf16_pair(d, da, db, idesc, acc);
+    else ptx::umma_bf16(d, da, db, idesc, acc);
+  }
+}
+
+__device__ __forceinline__ void linear_read8(const float* p, float (&v)[8]) {
+  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+  v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+
+// ------------------------------------------------------------------------- one-SM tiles
+// fp32 partial output tile over the stages once they are done with, rows (SWAP: bn of them, of
+// 128; MODE_DW: 128, of bn) padded by one float4, so that neighbouring rows start in other banks.
+constexpr int linear_part_ld(bool swap, int bn) { return (swap ? BLOCK_M : bn) + 4; }
+constexpr int linear_stage_area(int mode, int bn, int stages) {
+  const int a = stages * (LINEAR_P_BYTES + bn * 128);
+  const int b = (mode != MODE_DW ? bn : BLOCK_M) * linear_part_ld(mode != MODE_DW, bn) * 4;
+  return ((a > b ? a : b) + 15) / 16 * 16;
+}
+
+template <int MODE, bool FP8, bool GLU>
 __global__ void __launch_bounds__(LINEAR_THREADS, 2)
-linear_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+linear_tile_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
                    const LinearArgs g) {
-  using C = LinearTileCfg<BN>;
-  using MJ = LinearMajor<MODE>;
-  constexpr int TN = GLU ? BN / 2 : BN;  // output columns of a tile
-  constexpr uint32_t IDESC = linear_idesc<MODE, FP8>(BLOCK_M, BN);
+  using T = LinearMode_<MODE>;
+  const int bn = g.bn, stages = g.stages, ks = g.ks;
+  const int stage_bytes = LINEAR_P_BYTES + bn * 128;
+  const int TM = T::SWAP ? bn : BLOCK_M;                        // output rows of a tile
+  const int TN = T::SWAP ? (GLU ? BLOCK_M / 2 : BLOCK_M) : bn;  // and columns
+  const int lds = linear_part_ld(T::SWAP, bn);
+  const int tmem_cols = bn <= 32 ? 32 : bn <= 64 ? 64 : bn <= 128 ? 128 : 256;
   extern __shared__ uint8_t smem_raw[];
-  const uint32_t raw_addr = ptx::smem_u32(smem_raw);
-  uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF);
-  uint64_t* empty = full + C::STAGES;
-  uint64_t* tfull = empty + C::STAGES;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::MISC_OFF);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::MISC_OFF + 4);
-
+  const LinearSmem m = linear_smem(smem_raw, linear_stage_area(MODE, bn, stages));
+  uint64_t* tfull = m.extra;
+  volatile int* abort_flag = m.abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int ks = g.ks;
   const int rank = ks > 1 ? static_cast<int>(ptx::cluster_ctarank()) : 0;
   const uint64_t limit = g.timeout_ns;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < C::STAGES; ++s) {
-      ptx::mbar_init(&full[s], 1);
-      ptx::mbar_init(&empty[s], 1);
+    for (int s = 0; s < stages; ++s) {
+      ptx::mbar_init(&m.full[s], 1);
+      ptx::mbar_init(&m.empty[s], 1);
     }
     ptx::mbar_init(tfull, 1);
     *abort_flag = 0;
     ptx::fence_mbar_init();
-    ptx::prefetch_tmap(&tmA);
-    ptx::prefetch_tmap(&tmB);
+    ptx::prefetch_tmap(&tmP);
+    ptx::prefetch_tmap(&tmQ);
   }
   if (warp == 1) {
-    ptx::tmem_alloc(tmem_slot, BN);
+    ptx::tmem_alloc(m.tmem_slot, tmem_cols);
     ptx::tmem_relinquish();
   }
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
-  const uint32_t tmem_base = *tmem_slot;
+  const uint32_t tmem_base = *m.tmem_slot;
   pdl_wait();  // from here on: the previous kernel's outputs are visible
   pdl_launch_dependents();
 
-  const int mt = (g.R + BLOCK_M - 1) / BLOCK_M, nt = (g.C + TN - 1) / TN;
-  const LinearTile t = linear_tile(static_cast<int>(blockIdx.x) / ks, mt, nt, BLOCK_M, TN);
+  const int mt = (g.R + TM - 1) / TM, nt = (g.C + TN - 1) / TN;
+  const LinearTile t = linear_tile(static_cast<int>(blockIdx.x) / ks, mt, nt, TM, TN);
   const int nkb = (g.D + LINEAR_KSTEP<FP8> - 1) / LINEAR_KSTEP<FP8>;
   const int kb0 = static_cast<int>(static_cast<int64_t>(nkb) * rank / ks);
   const int nk = static_cast<int>(static_cast<int64_t>(nkb) * (rank + 1) / ks) - kb0;
@@ -257,38 +314,39 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
   if (warp == 0) {
     if (lane == 0) {
       // ------------------------------------------------------------ TMA producer
-      int it = 0;
+      const int prow = T::SWAP ? t.col0 : t.row0, qrow = T::SWAP ? t.row0 : t.col0;
+      int it = 0, s = 0;
+      uint32_t parity = 1;
       for (; it < nk; ++it) {
-        const int s = it % C::STAGES;
-        if (!ptx::mbar_wait(&empty[s], ((it / C::STAGES) & 1) ^ 1, abort_flag, limit)) {
+        if (!ptx::mbar_wait(&m.empty[s], parity, abort_flag, limit)) {
           linear_fail(g, abort_flag, DEVERR_TIMEOUT_PRODUCER);
           break;
         }
-        uint8_t* sa = smem + s * C::STAGE_BYTES;
-        uint8_t* sb = sa + C::A_BYTES;
+        uint8_t* sp = m.base + s * stage_bytes;
+        uint8_t* sq = sp + LINEAR_P_BYTES;
         const int k = (kb0 + it) * BLOCK_K;  // in 2-byte units of the maps
-        ptx::mbar_arrive_expect_tx(&full[s], C::STAGE_BYTES);
-        if constexpr (MJ::A_MN) {
+        ptx::mbar_arrive_expect_tx(&m.full[s], stage_bytes);
+        if constexpr (T::P_MN) {
 #pragma unroll
           for (int i = 0; i < BLOCK_M / 64; ++i)
-            ptx::tma_load_2d(sa + i * LINEAR_BOX_BYTES, &tmA, &full[s], t.row0 + 64 * i, k);
+            ptx::tma_load_2d(sp + i * LINEAR_BOX_BYTES, &tmP, &m.full[s], prow + 64 * i, k);
+        } else if constexpr (GLU) {  // 64 gate rows, then the same features' value rows
+          ptx::tma_load_2d(sp, &tmP, &m.full[s], k, prow);
+          ptx::tma_load_2d(sp + BLOCK_M / 2 * 128, &tmP, &m.full[s], k, g.glu_off + prow);
         } else {
-          ptx::tma_load_2d(sa, &tmA, &full[s], k, t.row0);
+          ptx::tma_load_2d(sp, &tmP, &m.full[s], k, prow);
         }
-        if constexpr (MJ::B_MN) {
-#pragma unroll
-          for (int i = 0; i < BN / 64; ++i)
-            ptx::tma_load_2d(sb + i * LINEAR_BOX_BYTES, &tmB, &full[s], t.col0 + 64 * i, k);
-        } else if constexpr (GLU) {  // BN / 2 gate rows, then the same features' value rows
-          ptx::tma_load_2d(sb, &tmB, &full[s], k, t.col0);
-          ptx::tma_load_2d(sb + TN * 128, &tmB, &full[s], k, g.glu_off + t.col0);
+        if constexpr (T::Q_MN) {
+          for (int i = 0; i < bn / 64; ++i)
+            ptx::tma_load_2d(sq + i * LINEAR_BOX_BYTES, &tmQ, &m.full[s], qrow + 64 * i, k);
         } else {
-          ptx::tma_load_2d(sb, &tmB, &full[s], k, t.col0);
+          ptx::tma_load_2d(sq, &tmQ, &m.full[s], k, qrow);
         }
+        if (++s == stages) s = 0, parity ^= 1u;
       }
       // every issued copy lands before the stages are written over or the CTA leaves
-      for (int j = it > C::STAGES ? it - C::STAGES : 0; j < it; ++j)
-        if (!linear_drain(&full[j % C::STAGES], (j / C::STAGES) & 1, limit)) {
+      for (int j = it > stages ? it - stages : 0; j < it; ++j)
+        if (!linear_drain(&m.full[j % stages], (j / stages) & 1, limit)) {
           linear_fail(g, abort_flag, DEVERR_TIMEOUT_DRAIN);
           break;
         }
@@ -296,29 +354,21 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
   } else if (warp == 1) {
     if (lane == 0) {
       // ------------------------------------------------------------ MMA issuer
+      const uint32_t idesc = linear_idesc<MODE, FP8>(BLOCK_M, bn);
       const bool stalled = g.inject_stall && !ptx::mbar_wait(tfull, 0, abort_flag, limit);
       if (stalled) linear_fail(g, abort_flag, DEVERR_TIMEOUT_MMA);
+      int s = 0;
+      uint32_t parity = 0;
       for (int it = 0; !stalled && it < nk; ++it) {
-        const int s = it % C::STAGES;
-        if (!ptx::mbar_wait(&full[s], (it / C::STAGES) & 1, abort_flag, limit)) {
+        if (!ptx::mbar_wait(&m.full[s], parity, abort_flag, limit)) {
           linear_fail(g, abort_flag, DEVERR_TIMEOUT_MMA);
           break;
         }
         ptx::tc_fence_after();
-        const uint32_t sa = ptx::smem_u32(smem + s * C::STAGE_BYTES);
-        const uint32_t sb = sa + C::A_BYTES;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {  // 32 bytes of a K-major row, 16 rows of an MN-major box
-          const uint64_t da = MJ::A_MN ? ptx::smem_desc_sw128_mn(sa + k * 2048, LINEAR_BOX_BYTES)
-                                       : ptx::smem_desc_sw128(sa + k * 32);
-          const uint64_t db = MJ::B_MN ? ptx::smem_desc_sw128_mn(sb + k * 2048, LINEAR_BOX_BYTES)
-                                       : ptx::smem_desc_sw128(sb + k * 32);
-          if constexpr (FP8)
-            ptx::umma_e4m3(tmem_base, da, db, IDESC, (it | k) != 0 ? 1u : 0u);
-          else
-            ptx::umma_bf16(tmem_base, da, db, IDESC, (it | k) != 0 ? 1u : 0u);
-        }
-        ptx::umma_commit(&empty[s]);
+        const uint32_t sp = ptx::smem_u32(m.base + s * stage_bytes);
+        linear_mma<MODE, FP8, false>(tmem_base, sp, sp + LINEAR_P_BYTES, idesc, it == 0);
+        ptx::umma_commit(&m.empty[s]);
+        if (++s == stages) s = 0, parity ^= 1u;
       }
       ptx::umma_commit(tfull);  // the accumulator, and every MMA issued
       if (!linear_drain(tfull, 0, limit)) linear_fail(g, abort_flag, DEVERR_TIMEOUT_DRAIN);
@@ -326,20 +376,34 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
   }
   __syncwarp();
   // ---------------------------------------------------------------- epilogue
-  float* part = reinterpret_cast<float*>(smem);
-  const int rows = min(BLOCK_M, g.R - t.row0);
+  float* part = reinterpret_cast<float*>(m.base);
+  const int rows = min(TM, g.R - t.row0);
   if (warp >= 2) {
-    const int q = warp & 3;  // TMEM lane quarter this warp may access
+    // TMEM lane quarter this warp may access, and which of the two warps there it is: they take
+    // the column chunks in turn
+    const int q = warp & 3, half = (warp - 2) >> 2;
     const bool ok = ptx::mbar_wait(tfull, 0, abort_flag, limit);
     if (__all_sync(0xffffffffu, ok)) {
       ptx::tc_fence_after();
-      if (q * 32 < rows) {
+      const uint32_t tq = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+      const int lane_row = q * 32 + lane;
+      if constexpr (T::SWAP) {
+        // lane: a column of the output tile; accumulator columns: its rows, of which `rows` exist
 #pragma unroll 1
-        for (int ch = 0; ch < BN / 32; ++ch) {
+        for (int ch = half; ch * 16 < rows; ch += 2) {
+          float v[16];
+          ptx::tmem_ld_32x32b_x16(tq + ch * 16, v);
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (ch * 16 + j < rows) part[(ch * 16 + j) * lds + lane_row] = v[j];
+        }
+      } else if (q * 32 < rows) {
+#pragma unroll 1
+        for (int ch = half; ch < bn / 32; ch += 2) {
           float v[32];
-          ptx::tmem_ld_32x32b_x32(tmem_base + (static_cast<uint32_t>(q * 32) << 16) + ch * 32, v);
-          if (q * 32 + lane < rows) {
-            float4* p = reinterpret_cast<float4*>(part + (q * 32 + lane) * C::LDS + ch * 32);
+          ptx::tmem_ld_32x32b_x32(tq + ch * 32, v);
+          if (lane_row < rows) {
+            float4* p = reinterpret_cast<float4*>(part + lane_row * lds + ch * 32);
 #pragma unroll
             for (int j = 0; j < 8; ++j)
               p[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
@@ -357,23 +421,31 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
     __syncthreads();
   if (warp == 1) {
     ptx::tc_fence_after();
-    ptx::tmem_dealloc(tmem_base, BN);
+    ptx::tmem_dealloc(tmem_base, tmem_cols);
   }
   if (*abort_flag == 0) {
-    constexpr int G = TN / 8;  // groups of eight output columns
+    const int G = TN / 8;  // groups of eight output columns
     const uint32_t part0 = ptx::smem_u32(part);
     const float inv_c = 1.0f / g.c;
     const int mine = (rows - rank + ks - 1) / ks;  // rows rank, rank + ks, ...
+    // (SWAP: G divides the number of threads, so that a thread's columns are the same throughout)
+    const int c0 = static_cast<int>(threadIdx.x) % G * 8;
+    LinearCols ca, cb;
+    if constexpr (MODE == MODE_FWD) {
+      linear_cols<FP8>(g, t.col0 + c0, t.col0 + c0 < g.C, &ca);
+      if constexpr (GLU) linear_cols<FP8>(g, g.glu_off + t.col0 + c0, t.col0 + c0 < g.C, &cb);
+    }
+#pragma unroll 2
     for (int i = threadIdx.x; i < mine * G; i += LINEAR_THREADS) {
-      const int r = rank + i / G * ks, c8 = i % G * 8;
+      const int r = rank + i / G * ks, c8 = T::SWAP ? c0 : i % G * 8;
       const int row = t.row0 + r, col = t.col0 + c8;
-      if (col >= g.C) continue;
       uint4 res = make_uint4(0u, 0u, 0u, 0u);
-      if (MODE == MODE_FWD && g.resid) res = linear_resid8(g, row, col);
+      if (MODE == MODE_FWD && g.resid && col < g.C) res = linear_resid8(g, row, col);
       float a[8], b[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) a[k] = b[k] = 0.0f;
-      const uint32_t off = part0 + (r * C::LDS + c8) * 4;
+      const uint32_t off = part0 + (r * lds + c8) * 4;
+#pragma unroll 4
       for (int p = 0; p < ks; ++p) {  // in rank order
         const uint32_t src = ks > 1 ? ptx::mapa_shared(off, p) : off;
         float f[8];
@@ -382,60 +454,86 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
 #pragma unroll
         for (int k = 0; k < 8; ++k) a[k] += f[k];
         if constexpr (GLU) {
-          ptx::ld_cluster_f32x4(src + TN * 4, f);
-          ptx::ld_cluster_f32x4(src + TN * 4 + 16, f + 4);
+          ptx::ld_cluster_f32x4(src + BLOCK_M / 2 * 4, f);
+          ptx::ld_cluster_f32x4(src + BLOCK_M / 2 * 4 + 16, f + 4);
 #pragma unroll
           for (int k = 0; k < 8; ++k) b[k] += f[k];
         }
       }
-      const float xs = FP8 ? __ldg(g.xs + row) : 1.0f;
-      if constexpr (GLU)
-        linear_store_glu8<FP8>(g, row, col, xs, inv_c, a, b, res);
-      else
-        linear_store8<MODE, FP8>(g, row, col, xs, a, res);
+      if (col < g.C) {
+        const float xs = FP8 ? __ldg(g.xs + row) : 1.0f;
+        if constexpr (GLU)
+          linear_store_glu8<FP8>(g, row, col, ca, cb, xs, inv_c, a, b, res);
+        else
+          linear_store8<MODE, FP8>(g, row, col, ca, xs, a, res);
+      }
     }
   }
   if (ks > 1) ptx::cluster_sync();  // no CTA leaves while another reads its part
 }
 
 // ------------------------------------------------------------------------- SM pairs
-template <int BN>
-struct LinearPairCfg {
-  static constexpr int A_BYTES = BLOCK_M * 128;
-  static constexpr int B_BYTES = BN / 2 * 128;
-  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-  static constexpr int STAGES = BN == 256 ? 7 : 9;
-  static constexpr int TMEM_COLS = 2 * BN;  // two accumulator sets
-  static constexpr int BAR_OFF = STAGES * STAGE_BYTES;
-  static constexpr int NUM_BARS = 2 * STAGES + 5;
-  static constexpr int MISC_OFF = BAR_OFF + NUM_BARS * 8;
-  static constexpr int SMEM_BYTES = MISC_OFF + 16 + 1024;  // + slack for 1024 alignment
-  static_assert(SMEM_BYTES <= 232448, "shared memory budget");
-};
+// The epilogue's shared memory.  SWAP: two buffers, one for each half of its warps, through which
+// they turn 32 accumulator columns round (32 output rows of 128 columns, padded, as above).
+// MODE_DW: 32 rows x 32 fp32 (or bf16) for each of its warps, on their way into a tensor store.
+constexpr int LINEAR_TURN_LD = BLOCK_M + 4;
+constexpr int LINEAR_TURN_BYTES = 32 * LINEAR_TURN_LD * 4;
+static_assert(2 * LINEAR_TURN_BYTES >= 8 * 32 * 128, "both forms fit");
 
-// Rank r of a pair holds rows 128 r .. of the tile's A and half of its B: columns BN / 2 * r ..
-// (GLU: rank 0 the gate rows, rank 1 the value rows of the same BN / 2 features); the MMAs, issued
-// by rank 0, read both CTAs' shared memory, and each CTA's TMEM receives its 128 output rows.
-// full[s] and tempty[a] of rank 0 collect both CTAs' copies and epilogue warps; empty[s] and
-// tfull[a] of both get rank 0's commits; cluster barriers bracket set-up and teardown.
-template <int BN, int MODE, bool FP8, bool GLU>
+// MODE_DW's epilogue: a warp's 32 rows by 32 accumulator columns at a time through its own buffer
+// into a tensor store, whose map cuts rows and columns outside the output.  (Through registers and
+// store instructions, eight rows of 64 or 128 bytes each, the wgrad of a few rows took 1.6 times
+// as long.)
+template <typename Release>
+__device__ __forceinline__ void linear_dw_chunk(const CUtensorMap* tmO, const LinearArgs& g,
+                                                uint8_t* buf, int lane, uint32_t taddr, int row,
+                                                int col, bool last, Release release) {
+  float v[32];
+  ptx::tmem_ld_32x32b_x32(taddr, v);
+  if (last) release();
+  if (lane == 0) ptx::bulk_wait_group_read<0>();  // the buffer's last store has read it
+  __syncwarp();
+  if (g.out_f32) {  // 128-byte rows, 16-byte pieces XOR row % 8 (the 128-byte swizzle)
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      reinterpret_cast<float4*>(buf + lane * 128)[j ^ (lane & 7)] =
+          make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+  } else {  // 64-byte rows, pieces XOR row / 2 % 4 (the 64-byte swizzle)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float w[8] = {v[8 * j],     v[8 * j + 1], v[8 * j + 2], v[8 * j + 3],
+                          v[8 * j + 4], v[8 * j + 5], v[8 * j + 6], v[8 * j + 7]};
+      reinterpret_cast<uint4*>(buf + lane * 64)[j ^ ((lane >> 1) & 3)] = linear_pack8(w);
+    }
+  }
+  ptx::fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    ptx::tma_store_2d(tmO, buf, col, row);
+    ptx::bulk_commit_group();
+  }
+}
+
+// Rank r of a pair holds 128 rows of P (128 r ..; GLU: 64 gate rows of features 64 r .. and the
+// same features' value rows) and half of Q's columns; the MMAs, issued by rank 0, read both CTAs'
+// shared memory, and each CTA's TMEM receives its P rows by all bn columns.  full[s] and tempty[a]
+// of rank 0 collect both CTAs' copies and epilogue warps; empty[s] and tfull[a] of both get rank
+// 0's commits; cluster barriers bracket set-up and teardown.
+template <int MODE, bool FP8, bool GLU>
 __global__ void __launch_bounds__(LINEAR_THREADS, 1)
-linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                   const LinearArgs g) {
-  using C = LinearPairCfg<BN>;
-  using MJ = LinearMajor<MODE>;
-  constexpr int TM = 2 * BLOCK_M, TN = GLU ? BN / 2 : BN;
-  constexpr uint32_t IDESC = linear_idesc<MODE, FP8>(TM, BN);
+linear_pair_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
+                   const __grid_constant__ CUtensorMap tmO, const LinearArgs g) {
+  using T = LinearMode_<MODE>;
+  const int bn = g.bn, stages = g.stages;
+  const int stage_bytes = LINEAR_P_BYTES + bn / 2 * 128;
+  constexpr int PROWS = GLU ? BLOCK_M / 2 : BLOCK_M;  // output columns (MODE_DW: rows) of a CTA
+  const int TM = T::SWAP ? bn : 2 * PROWS, TN = T::SWAP ? 2 * PROWS : bn;
+  constexpr int TMEM_COLS = 512;  // two accumulator sets, 256 columns apart
   extern __shared__ uint8_t smem_raw[];
-  const uint32_t raw_addr = ptx::smem_u32(smem_raw);
-  uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF);
-  uint64_t* empty = full + C::STAGES;
-  uint64_t* tfull = empty + C::STAGES;
-  uint64_t* tempty = tfull + 2;
-  uint64_t* drain = tempty + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::MISC_OFF);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::MISC_OFF + 4);
+  const LinearSmem m = linear_smem(smem_raw, stages * stage_bytes + 2 * LINEAR_TURN_BYTES);
+  float* turn = reinterpret_cast<float*>(m.base + stages * stage_bytes);
+  uint64_t *tfull = m.extra, *tempty = m.extra + 2, *drain = m.extra + 4;
+  volatile int* abort_flag = m.abort_flag;
 
   const int rank = static_cast<int>(ptx::cluster_ctarank());
   const bool lead = rank == 0;
@@ -445,29 +543,29 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
   const uint64_t limit = g.timeout_ns;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < C::STAGES; ++s) {
-      ptx::mbar_init(&full[s], 1);  // rank 0's producer; the bytes come from both CTAs
-      ptx::mbar_init(&empty[s], 1);
+    for (int s = 0; s < stages; ++s) {
+      ptx::mbar_init(&m.full[s], 1);  // rank 0's producer; the bytes come from both CTAs
+      ptx::mbar_init(&m.empty[s], 1);
     }
     for (int a = 0; a < 2; ++a) {
       ptx::mbar_init(&tfull[a], 1);
-      ptx::mbar_init(&tempty[a], 2 * 4);  // the four epilogue warps of each CTA
+      ptx::mbar_init(&tempty[a], 2 * 8);  // the eight epilogue warps of each CTA
     }
     ptx::mbar_init(drain, 1);
     *abort_flag = 0;
     ptx::fence_mbar_init();
-    ptx::prefetch_tmap(&tmA);
-    ptx::prefetch_tmap(&tmB);
+    ptx::prefetch_tmap(&tmP);
+    ptx::prefetch_tmap(&tmQ);
   }
   ptx::cluster_sync();  // both CTAs' barriers exist before either signals the other's
   if (warp == 1) {
-    ptx::tmem_alloc_pair(tmem_slot, C::TMEM_COLS);
+    ptx::tmem_alloc_pair(m.tmem_slot, TMEM_COLS);
     ptx::tmem_relinquish_pair();
   }
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
-  const uint32_t tmem_base = *tmem_slot;
+  const uint32_t tmem_base = *m.tmem_slot;
   pdl_wait();  // from here on: the previous kernel's outputs are visible
   pdl_launch_dependents();
   const int cid = static_cast<int>(ptx::cluster_id_x());
@@ -477,44 +575,48 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
     if (lane == 0) {
       // ------------------------------------------------------------ TMA producer (both ranks)
       uint32_t it = 0;
+      int s = 0;
+      uint32_t parity = 1;
       bool ok = true;
       for (int tile = cid; ok && tile < total; tile += ncl) {
         const LinearTile t = linear_tile(tile, mt, nt, TM, TN);
-        const int arow = t.row0 + rank * BLOCK_M;
-        const int brow = GLU ? t.col0 + rank * g.glu_off : t.col0 + rank * (BN / 2);
+        const int prow = (T::SWAP ? t.col0 : t.row0) + rank * PROWS;
+        const int qrow = (T::SWAP ? t.row0 : t.col0) + rank * (bn / 2);
         for (int kb = 0; kb < nk; ++kb, ++it) {
-          const int s = static_cast<int>(it % C::STAGES);
-          if (!ptx::mbar_wait(&empty[s], ((it / C::STAGES) & 1u) ^ 1u, abort_flag, limit)) {
+          if (!ptx::mbar_wait(&m.empty[s], parity, abort_flag, limit)) {
             linear_fail(g, abort_flag, DEVERR_TIMEOUT_PRODUCER);
             ok = false;
             break;
           }
-          uint8_t* sa = smem + s * C::STAGE_BYTES;
-          uint8_t* sb = sa + C::A_BYTES;
-          const uint32_t fb = ptx::mapa_shared(ptx::smem_u32(&full[s]), 0);
-          if (lead) ptx::mbar_arrive_expect_tx(&full[s], 2u * C::STAGE_BYTES);
+          uint8_t* sp = m.base + s * stage_bytes;
+          uint8_t* sq = sp + LINEAR_P_BYTES;
+          const uint32_t fb = ptx::mapa_shared(ptx::smem_u32(&m.full[s]), 0);
+          if (lead) ptx::mbar_arrive_expect_tx(&m.full[s], 2u * stage_bytes);
           const int k = kb * BLOCK_K;
-          if constexpr (MJ::A_MN) {
+          if constexpr (T::P_MN) {
 #pragma unroll
             for (int i = 0; i < BLOCK_M / 64; ++i)
-              ptx::tma_load_2d_pair(sa + i * LINEAR_BOX_BYTES, &tmA, fb, arow + 64 * i, k);
+              ptx::tma_load_2d_pair(sp + i * LINEAR_BOX_BYTES, &tmP, fb, prow + 64 * i, k);
+          } else if constexpr (GLU) {
+            ptx::tma_load_2d_pair(sp, &tmP, fb, k, prow);
+            ptx::tma_load_2d_pair(sp + PROWS * 128, &tmP, fb, k, g.glu_off + prow);
           } else {
-            ptx::tma_load_2d_pair(sa, &tmA, fb, k, arow);
+            ptx::tma_load_2d_pair(sp, &tmP, fb, k, prow);
           }
-          if constexpr (MJ::B_MN) {
-#pragma unroll
-            for (int i = 0; i < BN / 128; ++i)
-              ptx::tma_load_2d_pair(sb + i * LINEAR_BOX_BYTES, &tmB, fb, brow + 64 * i, k);
+          if constexpr (T::Q_MN) {
+            for (int i = 0; i < bn / 128; ++i)
+              ptx::tma_load_2d_pair(sq + i * LINEAR_BOX_BYTES, &tmQ, fb, qrow + 64 * i, k);
           } else {
-            ptx::tma_load_2d_pair(sb, &tmB, fb, k, brow);
+            ptx::tma_load_2d_pair(sq, &tmQ, fb, k, qrow);
           }
+          if (++s == stages) s = 0, parity ^= 1u;
         }
       }
       // rank 0's last full phases cover both CTAs' last copies: they land before the pair exits
       if (lead) {
-        const uint32_t first = it > static_cast<uint32_t>(C::STAGES) ? it - C::STAGES : 0u;
-        for (uint32_t j = first; j < it; ++j)
-          if (!linear_drain(&full[j % C::STAGES], (j / C::STAGES) & 1u, limit)) {
+        const uint32_t n = static_cast<uint32_t>(stages);
+        for (uint32_t j = it > n ? it - n : 0u; j < it; ++j)
+          if (!linear_drain(&m.full[j % n], (j / n) & 1u, limit)) {
             linear_fail(g, abort_flag, DEVERR_TIMEOUT_DRAIN);
             break;
           }
@@ -523,8 +625,9 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
   } else if (warp == 1) {
     if (lane == 0 && lead) {
       // ------------------------------------------------------------ MMA issuer (rank 0)
-      uint32_t it = 0;
-      int lt = 0;
+      const uint32_t idesc = linear_idesc<MODE, FP8>(2 * BLOCK_M, bn);
+      int lt = 0, s = 0;
+      uint32_t parity = 0;
       bool ok = !g.inject_stall || ptx::mbar_wait(drain, 0, abort_flag, limit);
       if (!ok) linear_fail(g, abort_flag, DEVERR_TIMEOUT_MMA);
       for (int tile = cid; ok && tile < total; tile += ncl, ++lt) {
@@ -534,29 +637,18 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
           break;
         }
         ptx::tc_fence_after();
-        const uint32_t d = tmem_base + static_cast<uint32_t>(acc * BN);
-        for (int kb = 0; kb < nk; ++kb, ++it) {
-          const int s = static_cast<int>(it % C::STAGES);
-          if (!ptx::mbar_wait(&full[s], (it / C::STAGES) & 1u, abort_flag, limit)) {
+        const uint32_t d = tmem_base + static_cast<uint32_t>(acc * 256);
+        for (int kb = 0; kb < nk; ++kb) {
+          if (!ptx::mbar_wait(&m.full[s], parity, abort_flag, limit)) {
             linear_fail(g, abort_flag, DEVERR_TIMEOUT_MMA);
             ok = false;
             break;
           }
           ptx::tc_fence_after();
-          const uint32_t sa = ptx::smem_u32(smem + s * C::STAGE_BYTES);
-          const uint32_t sb = sa + C::A_BYTES;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint64_t da = MJ::A_MN ? ptx::smem_desc_sw128_mn(sa + k * 2048, LINEAR_BOX_BYTES)
-                                         : ptx::smem_desc_sw128(sa + k * 32);
-            const uint64_t db = MJ::B_MN ? ptx::smem_desc_sw128_mn(sb + k * 2048, LINEAR_BOX_BYTES)
-                                         : ptx::smem_desc_sw128(sb + k * 32);
-            if constexpr (FP8)
-              ptx::umma_e4m3_pair(d, da, db, IDESC, (kb | k) != 0 ? 1u : 0u);
-            else
-              ptx::umma_bf16_pair(d, da, db, IDESC, (kb | k) != 0 ? 1u : 0u);
-          }
-          ptx::umma_commit_pair(&empty[s], 0x3);
+          const uint32_t sp = ptx::smem_u32(m.base + s * stage_bytes);
+          linear_mma<MODE, FP8, true>(d, sp, sp + LINEAR_P_BYTES, idesc, kb == 0);
+          ptx::umma_commit_pair(&m.empty[s], 0x3);
+          if (++s == stages) s = 0, parity ^= 1u;
         }
         if (ok) ptx::umma_commit_pair(&tfull[acc], 0x3);
       }
@@ -565,76 +657,102 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
       if (!linear_drain(drain, 0u, limit)) linear_fail(g, abort_flag, DEVERR_TIMEOUT_DRAIN);
     }
   } else {
-    // ------------------------------------------------------------ epilogue (warps 2..5, both
-    // ranks): a thread owns one of this CTA's 128 output rows and walks the tile's columns, 32
-    // at a time; the next 32 columns' residual is loaded before these are read from TMEM
-    const int q = warp & 3;
+    // ------------------------------------------------------------ epilogue (warps 2..9, both
+    // ranks): two halves of four warps take chunks of 32 accumulator columns in turn, each through
+    // a buffer that its warps fill and then read as eight consecutive output columns per thread.
+    // One half waits on TMEM and shared memory while the other computes: with one half alone a
+    // 256 x 256 tile took 5.5 us, the time of a reduction of 1100
+    const int q = warp & 3, half = (warp - 2) >> 2, tid = (threadIdx.x - 64) & 127;
+    const int bar = 1 + half;
     const float inv_c = 1.0f / g.c;
+    float* buf = turn + half * (LINEAR_TURN_BYTES / 4);
     const uint32_t te[2] = {ptx::mapa_shared(ptx::smem_u32(&tempty[0]), 0),
                             ptx::mapa_shared(ptx::smem_u32(&tempty[1]), 0)};
+    constexpr int G = PROWS / 8;            // column groups of a buffer's rows
+    constexpr int ITEMS = 32 * G / 128;     // per thread
+    const int gr = tid / G, gc = tid % G;   // item j: buffer row gr + j 128 / G, group gc
     int lt = 0;
     for (int tile = cid; tile < total; tile += ncl, ++lt) {
       const int acc = lt & 1;
       const LinearTile t = linear_tile(tile, mt, nt, TM, TN);
-      const int row = t.row0 + rank * BLOCK_M + q * 32 + lane;
-      const bool row_ok = row < g.R;
-      const bool use_res = MODE == MODE_FWD && g.resid && row_ok;
-      uint4 rnext[4];
+      // SWAP: output row of item j in chunk ch, and this thread's columns
+      auto row_of = [&](int ch, int j) { return t.row0 + ch * 32 + gr + j * (128 / G); };
+      const int col = t.col0 + rank * PROWS + gc * 8;
+      const int chunks = (min(bn, T::SWAP ? g.R - t.row0 : g.C - t.col0) + 31) / 32;
+      LinearCols ca, cb;
+      if constexpr (MODE == MODE_FWD) {
+        linear_cols<FP8>(g, col, col < g.C, &ca);
+        if constexpr (GLU) linear_cols<FP8>(g, g.glu_off + col, col < g.C, &cb);
+      }
+      uint4 rnext[ITEMS];
       auto load_res = [&](int ch) {
+        if (MODE != MODE_FWD || !g.resid || col >= g.C) return;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int col = t.col0 + ch * 32 + 8 * j;
-          rnext[j] = make_uint4(0u, 0u, 0u, 0u);
-          if (use_res && col < g.C) rnext[j] = linear_resid8(g, row, col);
-        }
+        for (int j = 0; j < ITEMS; ++j)
+          if (row_of(ch, j) < g.R) rnext[j] = linear_resid8(g, row_of(ch, j), col);
       };
-      load_res(0);
-      const float xs = FP8 && row_ok ? __ldg(g.xs + row) : 1.0f;
+      load_res(half);
       const bool got = ptx::mbar_wait(&tfull[acc], (lt >> 1) & 1, abort_flag, limit);
-      if (!__all_sync(0xffffffffu, got)) {
+      // a half's warps leave together: they share its barrier
+      if (!ptx::named_and(bar, 128, got)) {
         if (lane == 0) linear_fail(g, abort_flag, DEVERR_TIMEOUT_EPILOGUE);
         break;
       }
       ptx::tc_fence_after();
       const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
-                          static_cast<uint32_t>(acc * BN);
+                          static_cast<uint32_t>(acc * 256);
+      auto release = [&]() {  // this warp has read its part of the accumulator
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (lead)
+            ptx::mbar_arrive(&tempty[acc]);
+          else
+            ptx::mbar_arrive_cluster(te[acc]);
+        }
+      };
+      if (half >= chunks) release();
 #pragma unroll 1
-      for (int ch = 0; ch < TN / 32; ++ch) {
-        const int col0 = t.col0 + ch * 32;
-        if (col0 >= g.C) break;  // uniform across the warp
-        uint4 rcur[4];
+      for (int ch = half; ch < chunks; ch += 2) {
+        const uint32_t taddr = tb + static_cast<uint32_t>(ch * 32);
+        if constexpr (!T::SWAP) {
+          linear_dw_chunk(&tmO, g, reinterpret_cast<uint8_t*>(turn) + (warp - 2) * 4096, lane, taddr,
+                          t.row0 + rank * BLOCK_M + q * 32, t.col0 + ch * 32, ch + 2 >= chunks,
+                          release);
+        } else {
+          uint4 rcur[ITEMS];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) rcur[j] = rnext[j];
-        if (ch + 1 < TN / 32) load_res(ch + 1);
-        float v[32], u[32];
-        ptx::tmem_ld_32x32b_x32(tb + static_cast<uint32_t>(ch * 32), v);
-        if constexpr (GLU) ptx::tmem_ld_32x32b_x32(tb + static_cast<uint32_t>(TN + ch * 32), u);
-        if (row_ok) {
+          for (int j = 0; j < ITEMS; ++j) rcur[j] = rnext[j];
+          float v[32];
+          ptx::tmem_ld_32x32b_x32(taddr, v);
+          if (ch + 2 >= chunks) release();
+          if (ch + 2 < chunks) load_res(ch + 2);
+          ptx::named_sync(bar, 128);  // the buffer's last chunk has been read
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if (col0 + 8 * j >= g.C) break;
-            float a[8], b[8];
+          for (int j = 0; j < 32; ++j) buf[j * LINEAR_TURN_LD + q * 32 + lane] = v[j];
+          ptx::named_sync(bar, 128);
+          if (col >= g.C) continue;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              a[i] = v[8 * j + i];
-              if constexpr (GLU) b[i] = u[8 * j + i];
+          for (int j = 0; j < ITEMS; ++j) {
+            const int row = row_of(ch, j);
+            if (row >= g.R) continue;
+            const float* p = buf + (gr + j * (128 / G)) * LINEAR_TURN_LD + gc * 8;
+            const float xs = FP8 ? __ldg(g.xs + row) : 1.0f;
+            float a[8];
+            linear_read8(p, a);
+            if constexpr (GLU) {
+              float b[8];
+              linear_read8(p + PROWS, b);
+              linear_store_glu8<FP8>(g, row, col, ca, cb, xs, inv_c, a, b, rcur[j]);
+            } else {
+              linear_store8<MODE, FP8>(g, row, col, ca, xs, a, rcur[j]);
             }
-            if constexpr (GLU)
-              linear_store_glu8<FP8>(g, row, col0 + 8 * j, xs, inv_c, a, b, rcur[j]);
-            else
-              linear_store8<MODE, FP8>(g, row, col0 + 8 * j, xs, a, rcur[j]);
           }
         }
       }
-      ptx::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if (lead)
-          ptx::mbar_arrive(&tempty[acc]);
-        else
-          ptx::mbar_arrive_cluster(te[acc]);
-      }
     }
+    // the tensor stores complete before the CTA leaves (they read its shared memory)
+    if (!T::SWAP && lane == 0) ptx::bulk_wait_group_all();
   }
 
   ptx::tc_fence_before();
@@ -642,7 +760,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
   ptx::cluster_sync();  // the peer is done with this CTA's barriers, shared memory and TMEM
   if (warp == 1) {
     ptx::tc_fence_after();
-    ptx::tmem_dealloc_pair(tmem_base, C::TMEM_COLS);
+    ptx::tmem_dealloc_pair(tmem_base, TMEM_COLS);
   }
 }
 
@@ -650,16 +768,25 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
 // Which kernel, from sizes alone (linear_fwd.cu).
 struct LinearPlan {
   bool pair;
-  int bn, ks;
+  int bn, stages, ks;
 };
-LinearPlan linear_plan(int R, int C, int D, bool fp8, bool glu, int sms);
+constexpr int LINEAR_SMEM_MAX = 232448;           // of a CTA alone on its SM
+constexpr int LINEAR_SMEM_HALF = 113 * 1024;   // of two: an SM has 228 KB, 1 KB of it per CTA taken
+constexpr int linear_smem_bytes(bool pair, int mode, int bn, int stages) {
+  return (pair ? stages * (LINEAR_P_BYTES + bn / 2 * 128) + 2 * LINEAR_TURN_BYTES
+               : linear_stage_area(mode, bn, stages)) +
+         LINEAR_MISC + 1024;  // + slack for 1024 alignment
+}
+LinearPlan linear_plan(int mode, int R, int C, int D, bool fp8, bool glu, int sms);
 
 constexpr int LINEAR_MAX_DEVICES = 64;
 
-// A kernel's one-time set-up on a device: its shared memory, and (cluster > 1) how many of its
-// clusters can be resident at once, 0 when that is not known.  Returns < 0 on a CUDA error.
+// A kernel's one-time set-up on a device: the most shared memory it may ask for, and (cluster > 1)
+// how many of its clusters can be resident at once with that, 0 when that is not known.  Returns
+// < 0 on a CUDA error.
 template <typename K>
-int linear_kernel_setup(K kernel, int smem, int cluster, int dev, std::atomic<int>* cache) {
+int linear_kernel_setup(K kernel, int cluster, int dev, std::atomic<int>* cache) {
+  constexpr int smem = LINEAR_SMEM_MAX;
   const bool cached = dev >= 0 && dev < LINEAR_MAX_DEVICES;
   if (cached) {
     const int v = cache[dev].load(std::memory_order_acquire);
@@ -690,19 +817,32 @@ int linear_kernel_setup(K kernel, int smem, int cluster, int dev, std::atomic<in
   return active;
 }
 
-template <int BN, int MODE, bool FP8, bool GLU>
-int launch_linear_tile(const CUtensorMap& ta, const CUtensorMap& tb, const LinearArgs& g, int dev,
+struct LinearOperand {
+  const void* p;
+  int64_t rows, cols, ld;  // as stored, in 2-byte units
+};
+// Boxes of 64 reduction elements by `rows` rows, or (MN-major) 64 columns by 64 reduction rows.
+inline bool linear_map(CUtensorMap* m, const LinearOperand& o, bool mn, int rows) {
+  return make_tmap_bf16(m, o.p, o.rows, o.cols, o.ld, mn ? 64 : rows);
+}
+
+template <int MODE, bool FP8, bool GLU>
+int launch_linear_tile(const LinearOperand& P, const LinearOperand& Q, const LinearArgs& g, int dev,
                        cudaStream_t stream) {
-  using C = LinearTileCfg<BN>;
+  using T = LinearMode_<MODE>;
   static std::atomic<int> cache[LINEAR_MAX_DEVICES];
-  auto kernel = linear_tile_kernel<BN, MODE, FP8, GLU>;
-  if (linear_kernel_setup(kernel, C::SMEM_BYTES, 1, dev, cache) < 0) return LMOE_ERR_CUDA;
-  const int64_t ctas = ceil_div(g.R, BLOCK_M) * ceil_div(g.C, GLU ? BN / 2 : BN) * g.ks;
+  auto kernel = linear_tile_kernel<MODE, FP8, GLU>;
+  if (linear_kernel_setup(kernel, 1, dev, cache) < 0) return LMOE_ERR_CUDA;
+  CUtensorMap tp, tq;
+  if (!linear_map(&tp, P, T::P_MN, GLU ? BLOCK_M / 2 : BLOCK_M) || !linear_map(&tq, Q, T::Q_MN, g.bn))
+    return LMOE_ERR_CUDA;
+  const int tm = T::SWAP ? g.bn : BLOCK_M, tn = T::SWAP ? (GLU ? BLOCK_M / 2 : BLOCK_M) : g.bn;
+  const int64_t ctas = ceil_div(g.R, tm) * ceil_div(g.C, tn) * g.ks;
   if (ctas > INT32_MAX) return LMOE_ERR_UNSUPPORTED;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas));
   cfg.blockDim = dim3(LINEAR_THREADS);
-  cfg.dynamicSmemBytes = C::SMEM_BYTES;
+  cfg.dynamicSmemBytes = static_cast<size_t>(linear_smem_bytes(false, MODE, g.bn, g.stages));
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -713,26 +853,36 @@ int launch_linear_tile(const CUtensorMap& ta, const CUtensorMap& tb, const Linea
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = g.ks > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, ta, tb, g) == cudaSuccess ? LMOE_OK : LMOE_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, kernel, tp, tq, g) == cudaSuccess ? LMOE_OK : LMOE_ERR_CUDA;
 }
 
-template <int BN, int MODE, bool FP8, bool GLU>
-int launch_linear_pair(const CUtensorMap& ta, const CUtensorMap& tb, const LinearArgs& g, int dev,
+template <int MODE, bool FP8, bool GLU>
+int launch_linear_pair(const LinearOperand& P, const LinearOperand& Q, const LinearArgs& g, int dev,
                        int sms, cudaStream_t stream) {
-  using C = LinearPairCfg<BN>;
+  using T = LinearMode_<MODE>;
   static std::atomic<int> cache[LINEAR_MAX_DEVICES];
-  auto kernel = linear_pair_kernel<BN, MODE, FP8, GLU>;
+  auto kernel = linear_pair_kernel<MODE, FP8, GLU>;
   // a persistent grid: no more pairs than can be resident at once (an SM pair shares a GPC)
-  const int active = linear_kernel_setup(kernel, C::SMEM_BYTES, 2, dev, cache);
+  const int active = linear_kernel_setup(kernel, 2, dev, cache);
   if (active < 0) return LMOE_ERR_CUDA;
-  int64_t pairs = ceil_div(g.R, 2 * BLOCK_M) * ceil_div(g.C, GLU ? BN / 2 : BN);
+  CUtensorMap tp, tq;
+  const int prows = GLU ? BLOCK_M / 2 : BLOCK_M;
+  if (!linear_map(&tp, P, T::P_MN, prows) || !linear_map(&tq, Q, T::Q_MN, g.bn / 2))
+    return LMOE_ERR_CUDA;
+  CUtensorMap to{};
+  if (!T::SWAP &&
+      !(g.out_f32 ? make_tmap_f32_out32(&to, g.out, g.R, g.C, g.ldo)
+                  : make_tmap_bf16_out32(&to, g.out, g.R, g.C, g.ldo)))
+    return LMOE_ERR_CUDA;
+  const int tm = T::SWAP ? g.bn : 2 * prows, tn = T::SWAP ? 2 * prows : g.bn;
+  int64_t pairs = ceil_div(g.R, tm) * ceil_div(g.C, tn);
   if (pairs > INT32_MAX / 2) return LMOE_ERR_UNSUPPORTED;
   if (pairs > sms / 2) pairs = sms / 2;
   if (active > 0 && pairs > active) pairs = active;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
   cfg.blockDim = dim3(LINEAR_THREADS);
-  cfg.dynamicSmemBytes = C::SMEM_BYTES;
+  cfg.dynamicSmemBytes = static_cast<size_t>(linear_smem_bytes(true, MODE, g.bn, g.stages));
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -743,36 +893,26 @@ int launch_linear_pair(const CUtensorMap& ta, const CUtensorMap& tb, const Linea
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kernel, ta, tb, g) == cudaSuccess ? LMOE_OK : LMOE_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, kernel, tp, tq, to, g) == cudaSuccess ? LMOE_OK : LMOE_ERR_CUDA;
 }
 
-struct LinearOperand {
-  const void* p;
-  int64_t rows, cols, ld;  // as stored, in 2-byte units
-};
-
-// One product: tensor maps for the planned kernel's boxes, then the launch.
+// One product C[R, C] = A . B^T over D, A's rows (MODE_DW: columns) being the output's rows.
 template <int MODE, bool FP8, bool GLU>
 int launch_linear(const LinearOperand& A, const LinearOperand& B, const LinearArgs& g_in,
                   cudaStream_t stream) {
-  using MJ = LinearMajor<MODE>;
   LinearArgs g = g_in;
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return LMOE_ERR_CUDA;
-  const LinearPlan p = linear_plan(g.R, g.C, g.D, FP8, GLU, sms);
-  const int brows = p.pair || GLU ? p.bn / 2 : p.bn;  // rows of B per K-major box
-  CUtensorMap ta, tb;
-  if (!make_tmap_bf16(&ta, A.p, A.rows, A.cols, A.ld, MJ::A_MN ? 64 : BLOCK_M) ||
-      !make_tmap_bf16(&tb, B.p, B.rows, B.cols, B.ld, MJ::B_MN ? 64 : brows))
-    return LMOE_ERR_CUDA;
+  const LinearPlan p = linear_plan(MODE, g.R, g.C, g.D, FP8, GLU, sms);
+  g.bn = p.bn;
+  g.stages = p.stages;
   g.ks = p.ks;
-  if (p.pair)
-    return p.bn == 256 ? launch_linear_pair<256, MODE, FP8, GLU>(ta, tb, g, dev, sms, stream)
-                       : launch_linear_pair<128, MODE, FP8, GLU>(ta, tb, g, dev, sms, stream);
-  return p.bn == 128 ? launch_linear_tile<128, MODE, FP8, GLU>(ta, tb, g, dev, stream)
-                     : launch_linear_tile<64, MODE, FP8, GLU>(ta, tb, g, dev, stream);
+  constexpr bool SWAP = LinearMode_<MODE>::SWAP;
+  const LinearOperand &P = SWAP ? B : A, &Q = SWAP ? A : B;
+  return p.pair ? launch_linear_pair<MODE, FP8, GLU>(P, Q, g, dev, sms, stream)
+                : launch_linear_tile<MODE, FP8, GLU>(P, Q, g, dev, stream);
 }
 
 // The checks of a linear layer's arguments that its forward and backward share.

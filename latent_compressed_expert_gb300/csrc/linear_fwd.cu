@@ -3,36 +3,69 @@
 
 namespace lmoe {
 
-// The least of an estimate in ns.  A K-block costs an SM the larger of its MMAs' time (RATE: the
-// measured bf16 rate per SM) and its bytes' way through L2 into shared memory (FEED); the weights
-// come from HBM once in any case.  A cluster that splits the reduction pays for the exchange.
-LinearPlan linear_plan(int R, int C, int D, bool fp8, bool glu, int sms) {
-  constexpr double RATE = 12500.0, FEED = 100.0;  // FLOP/ns and bytes/ns per SM
+// The least of an estimate in ns over the tilings.  Its constants, fitted to measured times (within
+// ~15 %) of 1 to 8192 rows against 512 to 7168 features and reductions:
+//   RATE     FLOP/ns of an SM's MMAs (the measured bf16 rate)
+//   FEED     bytes/ns that two CTAs of an SM draw through L2 into their stages
+//   ROUND    ns from a stage's load to its being free again, per SM alone and over an SM pair: a
+//            CTA draws no more than its stages hold per round
+//   EPILOGUE ns per accumulator column of a tile's epilogue; that of an SM pair's last tile, or of
+//            a tile alone, is not hidden
+//   HBM      bytes/ns; what is read and written crosses it once in any case
+LinearPlan linear_plan(int mode, int R, int C, int D, bool fp8, bool glu, int sms) {
+  constexpr double RATE = 12500.0, FEED = 150.0, ROUND = 1550.0, ROUND_PAIR = 2050.0;
+  constexpr double EPILOGUE = 15.0, EPILOGUE_PAIR = 11.0, HBM = 6600.0;
+  const bool dw = mode == MODE_DW;
   const int nk = static_cast<int>(ceil_div(D, fp8 ? 128 : 64));
-  const double flop = 2.0 * BLOCK_K * 1.0;  // per output element and K-block, in bf16 units
-  LinearPlan best{false, 64, 1};
+  const int P = dw ? R : C, Q = dw ? C : R;  // extents along the MMA's rows and columns
+  const double flop = 2.0 * BLOCK_K;         // per output element and K-block, in bf16 time
+  const double floor = (128.0 * nk * (static_cast<double>(C) * (glu ? 2 : 1) + R) +
+                        2.0 * R * C) / HBM;
+  auto larger = [](double a, double b) { return a > b ? a : b; };
+  LinearPlan best{false, 64, 3, 1};
   double least = 1e300;
-  auto offer = [&](bool pair, int bn, int ks, double ns) {
+  auto offer = [&](bool pair, int bn, int stages, int ks, double ns) {
     if (ns < least) {
       least = ns;
-      best = {pair, bn, ks};
+      best = {pair, bn, stages, ks};
     }
   };
-  for (int bn = 256; bn >= 128; bn /= 2) {
-    const int64_t tiles = ceil_div(R, 2 * BLOCK_M) * ceil_div(C, glu ? bn / 2 : bn);
-    const double mma = flop * BLOCK_M * bn / RATE, feed = (BLOCK_M + bn / 2) * 128.0 / FEED;
-    offer(true, bn, 1,
-          static_cast<double>(ceil_div(tiles, sms / 2)) * nk * (mma > feed ? mma : feed) + 4000.0);
-  }
-  const int arows = R < BLOCK_M ? R : BLOCK_M;
-  for (int bn = 128; bn >= 64; bn /= 2) {
-    const int64_t tiles = ceil_div(R, BLOCK_M) * ceil_div(C, glu ? bn / 2 : bn);
-    const double mma = flop * BLOCK_M * bn / RATE, feed = (arows + bn) * 128.0 / FEED;
-    for (int ks = 1; ks <= 8; ks *= 2) {
-      if (ks > 1 && (nk < 4 * ks || tiles * ks > 2 * sms)) break;
-      offer(false, bn, ks,
-            static_cast<double>(ceil_div(tiles * ks, sms) * ceil_div(nk, ks)) *
-                    (mma > feed ? mma : feed) + (ks > 1 ? 4000.0 : 3000.0));
+  // pieces of Q: as few as fit, or a few more for an even deal
+  const int unit_pair = dw ? 128 : 32, unit_tile = dw ? 64 : 16;
+  for (int n = static_cast<int>(ceil_div(Q, 256)), i = 0; i < 4; ++i, ++n) {
+    const int64_t per = ceil_div(Q, n);
+    {
+      const int bn = static_cast<int>(ceil_div(per, unit_pair)) * unit_pair;
+      const int64_t tiles = ceil_div(Q, bn) * ceil_div(P, glu ? BLOCK_M : 2 * BLOCK_M);
+      int st = LINEAR_MAX_STAGES;
+      while (linear_smem_bytes(true, mode, bn, st) > LINEAR_SMEM_MAX) --st;
+      const double tile = larger(nk * larger(flop * BLOCK_M * bn / RATE, ROUND_PAIR / st),
+                                 EPILOGUE_PAIR * bn);
+      offer(true, bn, st, 1, larger(static_cast<double>(ceil_div(tiles, sms / 2)) * tile, floor) +
+                                 EPILOGUE_PAIR * bn + 3000.0);
+    }
+    {
+      const int bn = static_cast<int>(ceil_div(per, unit_tile)) * unit_tile;
+      const int64_t tiles = ceil_div(Q, bn) * ceil_div(P, glu ? BLOCK_M / 2 : BLOCK_M);
+      int st = LINEAR_MAX_STAGES, per_sm = 2;
+      while (st > 3 && linear_smem_bytes(false, mode, bn, st) > LINEAR_SMEM_HALF) --st;
+      if (linear_smem_bytes(false, mode, bn, st) > LINEAR_SMEM_HALF) {  // then alone on its SM
+        per_sm = 1;
+        st = LINEAR_MAX_STAGES;
+        while (linear_smem_bytes(false, mode, bn, st) > LINEAR_SMEM_MAX) --st;
+      }
+      const double bytes = (BLOCK_M + (bn < Q ? bn : Q)) * 128.0;
+      for (int ks = 1; ks <= 8; ++ks) {
+        const int64_t ctas = tiles * ks;
+        if (ks > 1 && (nk < 2 * ks || ctas > per_sm * sms || (per_sm == 1 && ks > 4))) break;
+        const int64_t kb = ceil_div(nk, ks), waves = ceil_div(ctas, per_sm * sms);
+        const double shared = static_cast<double>(ceil_div(ctas, sms) * kb) *
+                              larger(flop * BLOCK_M * bn / RATE, bytes / FEED);
+        const double alone = static_cast<double>(waves * kb) * ROUND / st;
+        offer(false, bn, st, ks,
+              larger(larger(shared, alone), floor) + EPILOGUE * bn * (ctas > sms ? 2.0 : 1.0) +
+                  3500.0 * static_cast<double>(waves) + (ks > 1 ? 700.0 + 300.0 * ks : 0.0));
+      }
     }
   }
   return best;
