@@ -139,6 +139,8 @@ _lib = None
 def load():
     """Load liblmoe.so (built by ``python -m latent_compressed_expert_gb300.build``)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -432,52 +434,82 @@ def last_device_error(workspace: torch.Tensor) -> int:
     return int(load().lmoe_last_device_error(_ptr(workspace)))
 
 
-def _rows(t, dtype, shape, name):
-    """(address, distance between rows) of a 2-D device tensor whose rows are contiguous."""
-    if t.dtype != dtype or tuple(t.shape) != shape:
-        _expect(t, dtype, shape, name)
-    if not t.is_cuda:
-        raise ValueError("lmoe: tensors must be CUDA device tensors")
+# The calls below run for microseconds on the device, so what the host does per call is kept
+# small: each argument is looked at once, and the current stream is asked for as the raw handle.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _rows(t, dtype, rows, cols, dev, name):
+    """(address, distance between rows) of a [rows, cols] tensor on device number dev whose rows
+    are contiguous."""
+    if t.dtype is not dtype or t.shape != (rows, cols):
+        _expect(t, dtype, (rows, cols), name)
+    if t.get_device() != dev:
+        raise ValueError(f"lmoe: {name} must be on CUDA device {dev}, not {t.device}")
     rs, cs = t.stride()
-    if cs != 1 and shape[1] > 1:
+    if cs != 1 and cols > 1:
         raise ValueError(f"lmoe: the rows of {name} must be contiguous")
-    return t.data_ptr(), rs if shape[0] > 1 else shape[1]
+    return t.data_ptr(), rs if rows > 1 else cols
 
 
-def _same_device(dev, *tensors):
-    for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError(f"lmoe: tensors on {dev} and on {t.device}")
+def _vector(t, n, dev, name):
+    """Address of a contiguous fp32 [n] tensor on device number dev."""
+    if t.dtype is not torch.float32 or t.shape != (n,):
+        _expect(t, torch.float32, (n,), name)
+    if t.get_device() != dev:
+        raise ValueError(f"lmoe: {name} must be on CUDA device {dev}, not {t.device}")
+    if n > 1 and t.stride(0) != 1:
+        raise ValueError(f"lmoe: {name} must be contiguous")
+    return t.data_ptr()
 
 
 def _on(dev):
-    """The device's current stream; its device must be the current one."""
-    if dev.index != torch.cuda.current_device():
-        raise ValueError(f"lmoe: tensors on {dev}, but the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
-    return torch.cuda.current_stream().cuda_stream
+    """Device dev's current stream, dev being the current device.  (A call on another stream makes
+    that the current one first, so that what it allocates belongs to that stream too.)"""
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"lmoe: tensors on CUDA device {dev}, but the current device is "
+                         f"{torch.cuda.current_device()}")
+    return _raw_stream(dev)
 
 
-def _add_rmsnorm(x, gamma, residual, eps, fp8, train, y, total, stream):
+def _device_of(t, name):
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"lmoe: {name} must be a CUDA device tensor")
+    return dev
+
+
+def _add_rmsnorm(x, gamma, residual, eps, fp8, train, y, total):
     rows, cols = x.shape
-    bf, dev = torch.bfloat16, x.device
-    px, ldx = _rows(x, bf, (rows, cols), "x")
-    pr, ldr = (None, 0) if residual is None else _rows(residual, bf, (rows, cols), "residual")
-    _expect(gamma, torch.float32, (cols,), "gamma")
-    if total is None and residual is not None:
-        total = torch.empty((rows, cols), dtype=bf, device=dev)
-    pt, ldt = (None, 0) if total is None else _rows(total, bf, (rows, cols), "total")
-    yt = torch.uint8 if fp8 else bf
+    bf, f, device = torch.bfloat16, torch.float32, x.device
+    dev = _device_of(x, "x")
+    px, ldx = _rows(x, bf, rows, cols, dev, "x")
+    pg = _vector(gamma, cols, dev, "gamma")
+    pr = pt = ps = pi = None
+    ldr = ldt = 0
+    if residual is not None:
+        pr, ldr = _rows(residual, bf, rows, cols, dev, "residual")
+        if total is None:
+            total = torch.empty((rows, cols), dtype=bf, device=device)
+            pt, ldt = total.data_ptr(), cols
+    if total is not None and pt is None:
+        pt, ldt = _rows(total, bf, rows, cols, dev, "total")
     if y is None:
-        y = torch.empty((rows, cols), dtype=yt, device=dev)
-    py, ldy = _rows(y, yt, (rows, cols), "y")
-    scales = torch.empty(rows, dtype=torch.float32, device=dev) if fp8 else None
-    rstd = torch.empty(rows, dtype=torch.float32, device=dev) if train else None
-    _same_device(dev, gamma, residual, total, y)
-    st = _on(dev) if stream is None else stream.cuda_stream
-    _check(load().lmoe_add_rmsnorm(px, ldx, pr, ldr, _ptr(gamma), rows, cols, eps, py, ldy,
-                                   E4M3 if fp8 else BF16, _ptr(scales), pt, ldt, _ptr(rstd), st),
-           "lmoe_add_rmsnorm")
+        y = torch.empty((rows, cols), dtype=torch.uint8 if fp8 else bf, device=device)
+        py, ldy = y.data_ptr(), cols
+    else:
+        py, ldy = _rows(y, bf, rows, cols, dev, "y")
+    scales = rstd = None
+    if fp8:
+        scales = torch.empty(rows, dtype=f, device=device)
+        ps = scales.data_ptr()
+    if train:
+        rstd = torch.empty(rows, dtype=f, device=device)
+        pi = rstd.data_ptr()
+    rc = load().lmoe_add_rmsnorm(px, ldx, pr, ldr, pg, rows, cols, eps, py, ldy,
+                                 E4M3 if fp8 else BF16, ps, pt, ldt, pi, _on(dev))
+    if rc:
+        _check(rc, "lmoe_add_rmsnorm")
     return y, scales, x if total is None else total, rstd
 
 
@@ -487,7 +519,10 @@ def add_rmsnorm(x: torch.Tensor, gamma: torch.Tensor, residual: torch.Tensor | N
     (rows contiguous, at any stride), gamma [cols] fp32 -> (y, total), or with train
     (y, total, rstd) for add_rmsnorm_backward.  total is x + residual in bf16 (x itself
     without a residual); ``y`` and ``total`` may be given, and may be x or residual."""
-    y, _, total, rstd = _add_rmsnorm(x, gamma, residual, eps, False, train, y, total, stream)
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return add_rmsnorm(x, gamma, residual, eps, train, y, total)
+    y, _, total, rstd = _add_rmsnorm(x, gamma, residual, eps, False, train, y, total)
     return (y, total, rstd) if train else (y, total)
 
 
@@ -495,7 +530,10 @@ def add_rmsnorm_e4m3(x: torch.Tensor, gamma: torch.Tensor, residual: torch.Tenso
                      eps: float = 1e-6, total=None, stream=None):
     """add_rmsnorm with y as e4m3 codes (uint8) and one fp32 scale per row:
     (codes, scales, total)."""
-    return _add_rmsnorm(x, gamma, residual, eps, True, False, None, total, stream)[:3]
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return add_rmsnorm_e4m3(x, gamma, residual, eps, total)
+    return _add_rmsnorm(x, gamma, residual, eps, True, False, None, total)[:3]
 
 
 def add_rmsnorm_backward(dy: torch.Tensor, total: torch.Tensor, gamma: torch.Tensor,
@@ -504,28 +542,32 @@ def add_rmsnorm_backward(dy: torch.Tensor, total: torch.Tensor, gamma: torch.Ten
     """Gradients of add_rmsnorm (lmoe_add_rmsnorm_backward): dy, and dtotal (the gradient that
     reaches total itself, or None), [rows, cols] bf16 -> (dx bf16, dgamma fp32 or None); dx is
     the gradient of x and of residual."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return add_rmsnorm_backward(dy, total, gamma, rstd, dtotal, want_dgamma, dx)
     rows, cols = dy.shape
-    bf, f, dev = torch.bfloat16, torch.float32, dy.device
-    pd, ldy = _rows(dy, bf, (rows, cols), "dy")
-    pt, ldt = _rows(total, bf, (rows, cols), "total")
-    pe, lde = (None, 0) if dtotal is None else _rows(dtotal, bf, (rows, cols), "dtotal")
-    _expect(gamma, f, (cols,), "gamma")
-    _expect(rstd, f, (rows,), "rstd")
+    bf, f, device = torch.bfloat16, torch.float32, dy.device
+    dev = _device_of(dy, "dy")
+    pd, ldy = _rows(dy, bf, rows, cols, dev, "dy")
+    pt, ldt = _rows(total, bf, rows, cols, dev, "total")
+    pe, lde = (None, 0) if dtotal is None else _rows(dtotal, bf, rows, cols, dev, "dtotal")
+    pg = _vector(gamma, cols, dev, "gamma")
+    pi = _vector(rstd, rows, dev, "rstd")
     if dx is None:
-        dx = torch.empty((rows, cols), dtype=bf, device=dev)
-    po, ldo = _rows(dx, bf, (rows, cols), "dx")
+        dx = torch.empty((rows, cols), dtype=bf, device=device)
+    po, ldo = _rows(dx, bf, rows, cols, dev, "dx")
     lib = load()
-    dgamma = ws = None
+    dgamma = pm = pw = None
     nb = 0
     if want_dgamma:
-        dgamma = torch.empty(cols, dtype=f, device=dev)
+        dgamma = torch.empty(cols, dtype=f, device=device)
         nb = lib.lmoe_add_rmsnorm_backward_workspace_bytes(rows, cols)
-        ws = torch.empty(nb, dtype=torch.uint8, device=dev)
-    _same_device(dev, total, gamma, rstd, dtotal, dx)
-    st = _on(dev) if stream is None else stream.cuda_stream
-    _check(lib.lmoe_add_rmsnorm_backward(pd, ldy, pt, ldt, _ptr(gamma), _ptr(rstd), pe, lde, rows,
-                                         cols, po, ldo, _ptr(dgamma), _ptr(ws), nb, st),
-           "lmoe_add_rmsnorm_backward")
+        ws = torch.empty(nb, dtype=torch.uint8, device=device)
+        pm, pw = dgamma.data_ptr(), ws.data_ptr()
+    rc = lib.lmoe_add_rmsnorm_backward(pd, ldy, pt, ldt, pg, pi, pe, lde, rows, cols, po, ldo, pm,
+                                       pw, nb, _on(dev))
+    if rc:
+        _check(rc, "lmoe_add_rmsnorm_backward")
     return dx, dgamma
 
 
@@ -545,56 +587,59 @@ class Linear:
         rows, K = w.shape
         if act == "situ" and rows % 2:
             raise ValueError("lmoe: a gated layer needs as many value rows as gate rows")
-        self.fp8 = w.dtype == torch.uint8
+        self.fp8 = w.dtype is torch.uint8
         if self.fp8 != (w_scales is not None):
             raise ValueError("lmoe: e4m3 codes (uint8) and w_scales go together")
         self.w, self.bias, self.w_scales, self.act, self.c = w, bias, w_scales, act, c
         self.rows, self.K, self.N = rows, K, rows // 2 if act == "situ" else rows
-        self.device = w.device
+        self.device, self._dev = w.device, _device_of(w, "w")
         self._dtype = torch.uint8 if self.fp8 else torch.bfloat16
-        self._pw, self._ldw = _rows(w, self._dtype, (rows, K), "w")
-        f = torch.float32
-        for t, name in ((bias, "bias"), (w_scales, "w_scales")):
-            if t is not None:
-                _expect(t, f, (rows,), name)
-        self._pb, self._pws = _ptr(bias), _ptr(w_scales)
-        _same_device(w.device, bias, w_scales)
+        pw, ldw = _rows(w, self._dtype, rows, K, self._dev, "w")
+        pb = None if bias is None else _vector(bias, rows, self._dev, "bias")
+        pws = None if w_scales is None else _vector(w_scales, rows, self._dev, "w_scales")
         self.flag = torch.zeros(1, dtype=torch.int32, device=w.device)
-        self._pflag = self.flag.data_ptr()
+        torch.cuda.current_stream(w.device).synchronize()  # before any stream of the caller's
+        self._sizes = (self.N, K, ACTS[act], E4M3 if self.fp8 else BF16, c)
+        self._weights = (pw, ldw, pws, pb)
+        self._flag = self.flag.data_ptr()
 
-    def _desc(self, M, px, ldx):
-        return LinearDesc(M, self.N, self.K, ACTS[self.act], E4M3 if self.fp8 else BF16, self.c,
-                          px, ldx, None, self._pw, self._ldw, self._pws, self._pb, None, 0, None,
-                          0, None, 0, self._pflag)
+    def _desc(self, M, px, ldx, pxs, pr, ldr, py, ldy, pp, ldp):
+        return ctypes.byref(LinearDesc(M, *self._sizes, px, ldx, pxs, *self._weights, pr, ldr, py,
+                                       ldy, pp, ldp, self._flag))
 
     def forward(self, x: torch.Tensor, residual: torch.Tensor | None = None,
                 x_scales: torch.Tensor | None = None, train: bool = False, y=None, stream=None):
         """x [M, K] bf16 (or e4m3 codes with x_scales [M]), residual [M, N] bf16 -> y [M, N] bf16;
         with train, (y, pre), the bf16 pre-activations that ``backward`` needs (None without an
         activation).  Rows at any stride of whole 16 bytes.  ``y`` may be given (or be residual)."""
-        M = x.shape[0]
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.forward(x, residual, x_scales, train, y)
+        M, N, dev = x.shape[0], self.N, self._dev
         bf = torch.bfloat16
-        px, ldx = _rows(x, self._dtype, (M, self.K), "x")
-        d = self._desc(M, px, ldx)
+        px, ldx = _rows(x, self._dtype, M, self.K, dev, "x")
+        pxs = pr = pp = pre = None
+        ldr = 0
         if self.fp8:
             if x_scales is None:
                 raise ValueError("lmoe: e4m3 rows need x_scales")
-            _expect(x_scales, torch.float32, (M,), "x_scales")
-            d.x_scales = _ptr(x_scales)
+            pxs = _vector(x_scales, M, dev, "x_scales")
         elif x_scales is not None:
             raise ValueError("lmoe: x_scales belong to e4m3 rows")
         if residual is not None:
-            d.residual, d.ldr = _rows(residual, bf, (M, self.N), "residual")
+            pr, ldr = _rows(residual, bf, M, N, dev, "residual")
         if y is None:
-            y = torch.empty((M, self.N), dtype=bf, device=self.device)
-        d.y, d.ldy = _rows(y, bf, (M, self.N), "y")
-        pre = None
+            y = torch.empty((M, N), dtype=bf, device=self.device)
+            py, ldy = y.data_ptr(), N
+        else:
+            py, ldy = _rows(y, bf, M, N, dev, "y")
         if train and self.act != "none":
             pre = torch.empty((M, self.rows), dtype=bf, device=self.device)
-            d.pre, d.ldp = pre.data_ptr(), self.rows
-        _same_device(self.device, x, residual, x_scales, y)
-        st = _on(self.device) if stream is None else stream.cuda_stream
-        _check(load().lmoe_linear_forward(ctypes.byref(d), st), "lmoe_linear_forward")
+            pp = pre.data_ptr()
+        rc = load().lmoe_linear_forward(self._desc(M, px, ldx, pxs, pr, ldr, py, ldy, pp, self.rows),
+                                        _on(dev))
+        if rc:
+            _check(rc, "lmoe_linear_forward")
         return (y, pre) if train else y
 
     def backward(self, x: torch.Tensor, dy: torch.Tensor, pre: torch.Tensor | None = None,
@@ -603,30 +648,40 @@ class Linear:
         """Gradients for the x and pre of a ``forward(train=True)``: dy [M, N] bf16 -> dx [M, K]
         bf16, dw (fp32, or bf16 with dw_dtype) and, when the layer has a bias, dbias fp32.  The
         residual's gradient is dy itself."""
-        M = dy.shape[0]
-        bf, f, dev = torch.bfloat16, torch.float32, self.device
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.backward(x, dy, pre, dw_dtype, want_dx, want_dw)
+        M, dev = dy.shape[0], self._dev
+        bf, f = torch.bfloat16, torch.float32
         if self.fp8:
             raise LmoeError(LMOE_ERR_UNSUPPORTED, "lmoe_linear_backward")
         if dw_dtype not in (bf, f):
             raise ValueError("lmoe: dw_dtype must be torch.float32 or torch.bfloat16")
-        px, ldx = _rows(x, bf, (M, self.K), "x")
-        pd, ldd = _rows(dy, bf, (M, self.N), "dy")
-        d = self._desc(M, px, ldx)
+        px, ldx = _rows(x, bf, M, self.K, dev, "x")
+        pd, ldd = _rows(dy, bf, M, self.N, dev, "dy")
+        pp, ldp = None, 0
         if self.act != "none":
             if pre is None:
                 raise ValueError("lmoe: this layer's backward needs the forward's pre")
-            d.pre, d.ldp = _rows(pre, bf, (M, self.rows), "pre")
-        dx = torch.empty((M, self.K), dtype=bf, device=dev) if want_dx else None
-        dw = torch.empty((self.rows, self.K), dtype=dw_dtype, device=dev) if want_dw else None
-        db = None if self.bias is None else torch.empty(self.rows, dtype=f, device=dev)
+            pp, ldp = _rows(pre, bf, M, self.rows, dev, "pre")
+        dx = dw = db = pdx = pdw = pdb = None
+        if want_dx:
+            dx = torch.empty((M, self.K), dtype=bf, device=self.device)
+            pdx = dx.data_ptr()
+        if want_dw:
+            dw = torch.empty((self.rows, self.K), dtype=dw_dtype, device=self.device)
+            pdw = dw.data_ptr()
+        if self.bias is not None:
+            db = torch.empty(self.rows, dtype=f, device=self.device)
+            pdb = db.data_ptr()
         lib = load()
-        nb = lib.lmoe_linear_backward_workspace_bytes(ctypes.byref(d))
-        ws = torch.empty(nb, dtype=torch.uint8, device=dev)
-        _same_device(dev, x, dy, pre)
-        st = _on(dev) if stream is None else stream.cuda_stream
-        _check(lib.lmoe_linear_backward(ctypes.byref(d), pd, ldd, _ptr(dx), self.K, _ptr(dw),
-                                        F32 if dw_dtype == f else BF16, _ptr(db), _ptr(ws), nb,
-                                        st), "lmoe_linear_backward")
+        d = self._desc(M, px, ldx, None, None, 0, None, 0, pp, ldp)
+        nb = lib.lmoe_linear_backward_workspace_bytes(d)
+        ws = torch.empty(nb, dtype=torch.uint8, device=self.device)
+        rc = lib.lmoe_linear_backward(d, pd, ldd, pdx, self.K, pdw, F32 if dw_dtype is f else BF16,
+                                      pdb, ws.data_ptr(), nb, _on(dev))
+        if rc:
+            _check(rc, "lmoe_linear_backward")
         return {"dx": dx, "dw": dw, "dbias": db}
 
     def device_error(self) -> int:
@@ -772,6 +827,9 @@ class Layer:
         against thresholds ``tau`` (e.g. a prefill batch's) or none.  Arguments and debug outputs
         (logits, idx, gate, y_f32) as ``forward``'s.  The first call allocates a workspace of its
         own for up to min(max_tokens, FEW_MAX_TOKENS) tokens; make it before capturing a graph."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.forward_few(x, residual, y, tau, logits_in, logit_bias, debug)
         sh = self.shape
         T = x.shape[0]
         bf, f = torch.bfloat16, torch.float32
@@ -817,8 +875,7 @@ class Layer:
                    "y_f32": torch.empty((T, sh.d), dtype=f, device=dev)}
             io.logits_out, io.idx_out = _ptr(dbg["logits"]), _ptr(dbg["idx"])
             io.gate_out, io.y_f32_out = _ptr(dbg["gate"]), _ptr(dbg["y_f32"])
-        _same_device(self.device, x, residual, y, tau, logits_in, logit_bias)
-        st = _on(self.device) if stream is None else stream.cuda_stream
+        st = _on(self.device.index)
         _check(lib.lmoe_forward_few(ctypes.byref(dims), _ptr(self.packed), _ptr(x), _ptr(residual),
                                     _ptr(y), _ptr(self.few_ws), self.few_ws.numel(),
                                     ctypes.byref(io), st), "lmoe_forward_few")
