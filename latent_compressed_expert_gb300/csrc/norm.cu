@@ -79,6 +79,32 @@ __device__ __forceinline__ float row_reduce(float v, float* red, int tpr) {
   return v;
 }
 
+// The same with a barrier always (a block that holds one row).
+template <typename OP>
+__device__ __forceinline__ float row_reduce_sync(float v, float* red, int tpr) {
+  if (tpr > 32) return row_reduce<OP>(v, red, tpr);
+  v = row_reduce<OP>(v, red, tpr);
+  __syncthreads();
+  return v;
+}
+
+// Correctly rounded quotients by one divisor: with r = 1 / s and q = x r, both rounded, and the
+// exact remainder of q, q + (x - q s) r rounds to x / s (Markstein, IBM J. Res. Dev. 34, 1990).  Three
+// operations instead of a division's ten, which made the e4m3 kernels issue-bound.  Where 1 / s or
+// a remainder could leave the normal range, the division itself.
+struct Divisor {
+  float s, r;
+  bool plain;
+  __device__ explicit Divisor(float s_) : s(s_), r(1.0f / s_) {
+    plain = !(s_ >= 0x1p-96f && s_ <= 0x1p96f);
+  }
+  __device__ __forceinline__ float of(float x) const {
+    if (plain) return __fdiv_rn(x, s);
+    const float q = __fmul_rn(x, r);
+    return __fmaf_rn(__fmaf_rn(-q, s, x), r, q);
+  }
+};
+
 __device__ __forceinline__ float e4m3_scale(float amax) {
   const float s = __fdiv_rn(amax, NORM_E4M3_MAX);
   return s > 0.0f ? s : 1.0f;
@@ -98,6 +124,24 @@ struct NormArgs {
   float eps;
   int tpr;                   // threads per row, a multiple of 32
 };
+
+// Eight values of a row: bf16, or codes of their quotients by s.
+template <bool FP8>
+__device__ __forceinline__ void norm_store8(const NormArgs& a, int64_t row, int v,
+                                            const Divisor& s, const float (&f)[8]) {
+  if constexpr (FP8) {
+    uint32_t w[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const float* q = f + 4 * k;
+      w[k] = ptx::cvt_e4m3x2(s.of(q[1]), s.of(q[0])) |
+             (static_cast<uint32_t>(ptx::cvt_e4m3x2(s.of(q[3]), s.of(q[2]))) << 16);
+    }
+    reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.y) + row * a.ldy)[v] = make_uint2(w[0], w[1]);
+  } else {
+    reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.y) + row * a.ldy)[v] = pack8(f);
+  }
+}
 
 // Whole rows in registers: a row belongs to tpr threads, thread i of it to the 8-element
 // vectors i, i + tpr, ...; a block holds blockDim / tpr rows.  NV vectors per thread: 4 for
@@ -169,24 +213,11 @@ add_rmsnorm_kernel(const NormArgs a) {
     if (a.rstd) a.rstd[row] = rstd;
     if constexpr (FP8) a.scales[row] = s;
   }
+  const Divisor by(s);
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int v = t + i * tpr;
-    if (v >= nvec) continue;
-    if constexpr (FP8) {
-      uint32_t w[2];
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const float* q = f[i] + 4 * k;
-        w[k] = ptx::cvt_e4m3x2(__fdiv_rn(q[1], s), __fdiv_rn(q[0], s)) |
-               (static_cast<uint32_t>(ptx::cvt_e4m3x2(__fdiv_rn(q[3], s), __fdiv_rn(q[2], s)))
-                << 16);
-      }
-      reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.y) + row * a.ldy)[v] =
-          make_uint2(w[0], w[1]);
-    } else {
-      reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.y) + row * a.ldy)[v] = pack8(f[i]);
-    }
+    if (v < nvec) norm_store8<FP8>(a, row, v, by, f[i]);
   }
 }
 
@@ -284,17 +315,47 @@ struct NormBwdArgs {
   int cols;
 };
 
-// Rows in registers, as the forward; block b takes rows b, b + grid, ... and keeps its share
-// of dgamma in registers over them (a thread's columns never change), so that dy and total are
-// read once for both gradients.
+// dx of a row's vector, and what it adds to dgamma and to the row's dot product.
+__device__ __forceinline__ float norm_bwd_dot8(const uint4& dv, const uint4& tv, const float (&g)[8],
+                                               float rstd, float dot, float (&acc)[8]) {
+  float d[8], x[8];
+  unpack8(dv, d);
+  unpack8(tv, x);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const float dxh = d[k] * (x[k] * rstd);
+    acc[k] += dxh;
+    dot = fmaf(dxh, g[k], dot);
+  }
+  return dot;
+}
+__device__ __forceinline__ uint4 norm_bwd_dx8(const uint4& dv, const uint4& tv, const uint4& ev,
+                                              bool has_e, const float (&g)[8], float rstd,
+                                              float dot) {
+  float d[8], x[8], e[8];
+  unpack8(dv, d);
+  unpack8(tv, x);
+  unpack8(ev, e);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    d[k] = (d[k] * g[k] - x[k] * rstd * dot) * rstd;
+    if (has_e) d[k] += e[k];
+  }
+  return pack8(d);
+}
+
+// Rows in registers, as the forward: a block holds blockDim / tpr rows at a time, and walks over
+// them with its share of dgamma in registers (a thread's columns never change), so that dy and
+// total are read once for both gradients.  A block joins its rows' shares in order at the end.
 template <int NV>
 __global__ void __launch_bounds__(NV == 1 ? NORM_MAX_THREADS : NORM_MAX_THREADS4)
-add_rmsnorm_bwd_kernel(const NormBwdArgs a) {
+add_rmsnorm_bwd_kernel(const NormBwdArgs a, int tpr) {
   __shared__ float red[2][32];
+  extern __shared__ __align__(16) float share[];  // [cols], with more than one row per block
   pdl_wait();
   pdl_launch_dependents();
-  const int nvec = a.cols >> 3, tpr = blockDim.x;
-  const int t = threadIdx.x;
+  const int nvec = a.cols >> 3, rpb = blockDim.x / tpr;
+  const int t = threadIdx.x % tpr, sub = threadIdx.x / tpr;
   const float inv_n = __fdiv_rn(1.0f, static_cast<float>(a.cols));
   float acc[NV][8];
 #pragma unroll
@@ -302,58 +363,149 @@ add_rmsnorm_bwd_kernel(const NormBwdArgs a) {
 #pragma unroll
     for (int k = 0; k < 8; ++k) acc[i][k] = 0.0f;
   int ping = 0;
-  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, ping ^= 1) {
-    uint4 dv[NV], tv[NV], rv[NV];
-    const uint4* dr = reinterpret_cast<const uint4*>(a.dy + row * a.ldy);
-    const uint4* tr = reinterpret_cast<const uint4*>(a.total + row * a.ldt);
-    const uint4* rr = reinterpret_cast<const uint4*>(a.dtotal + row * a.ldd);
+  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * rpb; r0 < a.rows;
+       r0 += static_cast<int64_t>(gridDim.x) * rpb, ping ^= 1) {
+    const int64_t row = r0 + sub;
+    const bool live = row < a.rows;  // other rows of the block still meet the barriers
+    uint4 dv[NV], tv[NV], ev[NV];
+    const int64_t at = live ? row : 0;
+    const uint4* dr = reinterpret_cast<const uint4*>(a.dy + at * a.ldy);
+    const uint4* tr = reinterpret_cast<const uint4*>(a.total + at * a.ldt);
+    const uint4* er = reinterpret_cast<const uint4*>(a.dtotal + at * a.ldd);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = t + i * tpr;
-      dv[i] = tv[i] = rv[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (v < nvec) {
+      dv[i] = tv[i] = ev[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (live && v < nvec) {
         dv[i] = ldg_stream(dr + v);
         tv[i] = ldg_stream(tr + v);
-        if (a.dtotal) rv[i] = ldg_stream(rr + v);
+        if (a.dtotal) ev[i] = ldg_stream(er + v);
       }
     }
+    const float rstd = __ldg(a.rstd + at);
+    float dot = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if (t + i * tpr < nvec) {
+        float g[8];
+        load_gamma8(a.gamma, t + i * tpr, g);
+        dot = norm_bwd_dot8(dv[i], tv[i], g, rstd, dot, acc[i]);
+      }
+    }
+    dot = row_reduce<RowSum>(dot, red[ping], tpr) * inv_n;
+    uint4* o = reinterpret_cast<uint4*>(a.dx + at * a.ldx);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = t + i * tpr;
+      if (live && v < nvec) {
+        float g[8];
+        load_gamma8(a.gamma, v, g);
+        o[v] = norm_bwd_dx8(dv[i], tv[i], ev[i], a.dtotal != nullptr, g, rstd, dot);
+      }
+    }
+  }
+  if (!a.part) return;
+  float* p = a.part + static_cast<int64_t>(blockIdx.x) * a.cols;
+  for (int j = 0; j < rpb; ++j) {
+    if (sub == j) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int v = t + i * tpr;
+        if (v >= nvec) continue;
+        float4* to = reinterpret_cast<float4*>(j + 1 == rpb ? p : share) + 2 * v;
+        if (j > 0) {
+          const float4* from = reinterpret_cast<const float4*>(share) + 2 * v;
+          const float4 b0 = from[0], b1 = from[1];
+          const float b[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
+#pragma unroll
+          for (int k = 0; k < 8; ++k) acc[i][k] += b[k];
+        }
+        to[0] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+        to[1] = make_float4(acc[i][4], acc[i][5], acc[i][6], acc[i][7]);
+      }
+    }
+    if (rpb > 1) __syncthreads();
+  }
+}
+
+// Many long rows: a block has the next rows' operands on their way into shared memory by bulk
+// copies while it computes, since the registers of its dgamma leave no room for loads ahead.  (The
+// forward, whose blocks are many and hold no such sums, is faster without.)  7168 columns: 2 blocks
+// of 2 stages per SM.
+constexpr int NORM_STAGES = 4;
+constexpr int NORM_STREAM_ROW = 4096;  // bytes of a row from which this form is used
+constexpr int NORM_STREAM_SMEM = 110 * 1024;  // of a block, two of which share an SM
+constexpr int NORM_STREAM_THREADS = 448;
+constexpr unsigned long long NORM_WAIT_NS = 2000000000ull;
+
+__global__ void __launch_bounds__(NORM_STREAM_THREADS, 2)
+add_rmsnorm_bwd_stream_kernel(const NormBwdArgs a, int stages) {
+  constexpr int NV = 2;
+  extern __shared__ __align__(16) uint8_t ring[];
+  __shared__ uint64_t full[NORM_STAGES];
+  __shared__ float red[2][32];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int tpr = blockDim.x, t = threadIdx.x, nvec = a.cols >> 3, bytes = a.cols * 2;
+  const int ops = a.dtotal ? 3 : 2;
+  const float inv_n = __fdiv_rn(1.0f, static_cast<float>(a.cols));
+  if (t == 0) {
+    for (int i = 0; i < stages; ++i) ptx::mbar_init(&full[i], 1);
+    ptx::fence_mbar_init();
+  }
+  __syncthreads();
+  const int64_t step = gridDim.x;
+  auto fetch = [&](int64_t row, int stage) {  // by thread 0
+    if (row >= a.rows) return;
+    uint8_t* to = ring + stage * ops * bytes;
+    ptx::mbar_arrive_expect_tx(&full[stage], static_cast<uint32_t>(ops * bytes));
+    ptx::bulk_load(to, a.dy + row * a.ldy, bytes, &full[stage]);
+    ptx::bulk_load(to + bytes, a.total + row * a.ldt, bytes, &full[stage]);
+    if (ops == 3) ptx::bulk_load(to + 2 * bytes, a.dtotal + row * a.ldd, bytes, &full[stage]);
+  };
+  if (t == 0)
+    for (int i = 0; i < stages; ++i) fetch(blockIdx.x + i * step, i);
+  float acc[NV][8];
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) acc[i][k] = 0.0f;
+  int stage = 0, flip = 0;
+  uint32_t parity = 0;
+  for (int64_t row = blockIdx.x; row < a.rows; row += step, flip ^= 1) {
     const float rstd = __ldg(a.rstd + row);
+    const uint64_t t0 = ptx::globaltimer_ns();
+    while (!ptx::mbar_try_wait(&full[stage], parity))  // a copy's own time; bounded all the same
+      if (ptx::globaltimer_ns() - t0 > NORM_WAIT_NS) break;
+    const uint8_t* base = ring + stage * ops * bytes;
+    uint4 dv[NV], tv[NV], ev[NV];
     float dot = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = t + i * tpr;
+      dv[i] = tv[i] = ev[i] = make_uint4(0u, 0u, 0u, 0u);
       if (v < nvec) {
-        float d[8], x[8], g[8];
-        unpack8(dv[i], d);
-        unpack8(tv[i], x);
+        dv[i] = reinterpret_cast<const uint4*>(base)[v];
+        tv[i] = reinterpret_cast<const uint4*>(base + bytes)[v];
+        if (ops == 3) ev[i] = reinterpret_cast<const uint4*>(base + 2 * bytes)[v];
+        float g[8];
         load_gamma8(a.gamma, v, g);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float dxh = d[k] * (x[k] * rstd);
-          acc[i][k] += dxh;
-          dot = fmaf(dxh, g[k], dot);
-        }
+        dot = norm_bwd_dot8(dv[i], tv[i], g, rstd, dot, acc[i]);
       }
     }
-    dot = row_reduce<RowSum>(dot, red[ping], tpr) * inv_n;
+    dot = row_reduce_sync<RowSum>(dot, red[flip], tpr) * inv_n;
+    if (t == 0) fetch(row + stages * step, stage);  // past that barrier the stage has been read
     uint4* o = reinterpret_cast<uint4*>(a.dx + row * a.ldx);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = t + i * tpr;
       if (v < nvec) {
-        float d[8], x[8], g[8], r[8];
-        unpack8(dv[i], d);
-        unpack8(tv[i], x);
-        unpack8(rv[i], r);
+        float g[8];
         load_gamma8(a.gamma, v, g);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          d[k] = (d[k] * g[k] - x[k] * rstd * dot) * rstd;
-          if (a.dtotal) d[k] += r[k];
-        }
-        o[v] = pack8(d);
+        o[v] = norm_bwd_dx8(dv[i], tv[i], ev[i], ops == 3, g, rstd, dot);
       }
     }
+    if (++stage == stages) stage = 0, parity ^= 1u;
   }
   if (!a.part) return;
   float4* p = reinterpret_cast<float4*>(a.part + static_cast<int64_t>(blockIdx.x) * a.cols);
@@ -401,12 +553,12 @@ __global__ void __launch_bounds__(NORM_BLOCK) dgamma_any_kernel(const NormBwdArg
   a.part[static_cast<int64_t>(blockIdx.y) * a.cols + c] = s;
 }
 
-// out[c] = sum over parts of part[p, c], in a fixed order: a block takes 32 columns, its
-// eight warps every eighth part.
-__global__ void __launch_bounds__(256) column_sum_kernel(const float* __restrict__ part,
-                                                         int parts, int cols,
-                                                         float* __restrict__ out) {
-  __shared__ float red[8][32];
+// out[c] = sum over parts of part[p, c], in a fixed order: a block takes 32 columns, its 32 warps
+// every 32nd part (few loads in a row per thread: the time is their latency).
+constexpr int COLSUM_WARPS = 32;
+__global__ void __launch_bounds__(COLSUM_WARPS * 32)
+column_sum_kernel(const float* __restrict__ part, int parts, int cols, float* __restrict__ out) {
+  __shared__ float red[COLSUM_WARPS][33];
   pdl_wait();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
@@ -414,25 +566,25 @@ __global__ void __launch_bounds__(256) column_sum_kernel(const float* __restrict
   float s = 0.0f;
   if (c < cols) {
 #pragma unroll 8
-    for (int p = w; p < parts; p += 8) s += __ldg(part + static_cast<int64_t>(p) * cols + c);
+    for (int p = w; p < parts; p += COLSUM_WARPS)
+      s += __ldg(part + static_cast<int64_t>(p) * cols + c);
   }
   red[w][lane] = s;
   __syncthreads();
-  if (w == 0 && c < cols) {
+  s = red[lane][w];  // warp w: column w of the block, its warps' sums by a tree
 #pragma unroll
-    for (int i = 1; i < 8; ++i) s += red[i][lane];
-    out[c] = s;
-  }
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if (lane == 0 && blockIdx.x * 32 + w < cols) out[blockIdx.x * 32 + w] = s;
 }
 
 int launch_column_sum(const float* part, int parts, int cols, float* out, cudaStream_t stream) {
-  return launch_pdl(column_sum_kernel, static_cast<unsigned>(ceil_div(cols, 32)), 256, 0, stream,
-                    part, parts, cols, out) == cudaSuccess
+  return launch_pdl(column_sum_kernel, static_cast<unsigned>(ceil_div(cols, 32)),
+                    COLSUM_WARPS * 32, 0, stream, part, parts, cols, out) == cudaSuccess
              ? LMOE_OK
              : LMOE_ERR_CUDA;
 }
 
-constexpr int NORM_BWD_MAX_PARTS = 512;
+constexpr int NORM_BWD_MAX_PARTS = 640;
 
 static int launch_add_rmsnorm_bwd(const NormBwdArgs& a, float* dgamma, cudaStream_t stream) {
   int sms = 0;
@@ -444,11 +596,34 @@ static int launch_add_rmsnorm_bwd(const NormBwdArgs& a, float* dgamma, cudaStrea
   int parts = 2 * sms < NORM_BWD_MAX_PARTS ? 2 * sms : NORM_BWD_MAX_PARTS;
   if (a.rows < parts) parts = static_cast<int>(a.rows);
   cudaError_t rc = cudaSuccess;
-  if (vec) {
+  const int row_bytes = (a.dtotal ? 3 : 2) * a.cols * 2;
+  if (vec && a.rows > 2 * sms && a.cols * 2 >= NORM_STREAM_ROW && nvec <= 2 * NORM_STREAM_THREADS &&
+      2 * row_bytes <= NORM_STREAM_SMEM) {
+    int stages = NORM_STREAM_SMEM / row_bytes;
+    if (stages > NORM_STAGES) stages = NORM_STAGES;
+    rc = cudaFuncSetAttribute(add_rmsnorm_bwd_stream_kernel,
+                              cudaFuncAttributeMaxDynamicSharedMemorySize, NORM_STREAM_SMEM);
+    const int threads = static_cast<int>(ceil_div(ceil_div(nvec, 2), 32) * 32);
+    // shorter rows: up to four blocks per SM, as threads and two stages each allow
+    int blocks = 2;
+    while (blocks < 4 && (blocks + 1) * threads <= 2 * NORM_STREAM_THREADS &&
+           (blocks + 1) * (2 * row_bytes + 1536) <= 2 * NORM_STREAM_SMEM)
+      ++blocks;
+    while (stages > 2 && blocks * (stages * row_bytes + 1536) > 2 * NORM_STREAM_SMEM) --stages;
+    parts = blocks * sms < NORM_BWD_MAX_PARTS ? blocks * sms : NORM_BWD_MAX_PARTS;
+    if (a.rows < parts) parts = static_cast<int>(a.rows);
+    if (rc == cudaSuccess)
+      rc = launch_pdl(add_rmsnorm_bwd_stream_kernel, static_cast<unsigned>(parts),
+                      static_cast<unsigned>(threads), static_cast<size_t>(stages) * row_bytes,
+                      stream, a, stages);
+  } else if (vec) {
     const bool few = a.rows <= parts && nvec <= NORM_MAX_THREADS;
     const int tpr = static_cast<int>(ceil_div(ceil_div(nvec, few ? 1 : 4), 32) * 32);
-    rc = few ? launch_pdl(add_rmsnorm_bwd_kernel<1>, parts, tpr, 0, stream, a)
-             : launch_pdl(add_rmsnorm_bwd_kernel<4>, parts, tpr, 0, stream, a);
+    const int rpb = tpr < NORM_BLOCK && !few ? NORM_BLOCK / tpr : 1;
+    if (ceil_div(a.rows, rpb) < parts) parts = static_cast<int>(ceil_div(a.rows, rpb));
+    const size_t share = rpb > 1 ? static_cast<size_t>(a.cols) * sizeof(float) : 0;
+    rc = few ? launch_pdl(add_rmsnorm_bwd_kernel<1>, parts, tpr, 0, stream, a, tpr)
+             : launch_pdl(add_rmsnorm_bwd_kernel<4>, parts, tpr * rpb, share, stream, a, tpr);
   } else {
     if (a.part)
       rc = launch_pdl(dgamma_any_kernel,
