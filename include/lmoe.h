@@ -492,7 +492,8 @@ enum lmoe_type {
  * Any cols and any alignment to the element size are accepted; 16-byte-aligned rows (8 bytes for
  * codes) of a multiple of 8 columns, at most 16384, take the fast path.  A row that is not finite
  * gives what the formulas give.  rows == 0 is a no-op.
- * Errors: INVALID_ARG (null pointers, sizes, strides, type, misaligned), UNSUPPORTED (rows >= 2^31). */
+ * Errors: INVALID_ARG (null pointers, sizes, strides, type, misaligned), UNSUPPORTED (rows >= 2^31,
+ * cols > 2^30). */
 int lmoe_add_rmsnorm(const void *x, long long ldx, const void *residual, long long ldr,
                      const float *gamma, long long rows, int cols, float eps, void *y,
                      long long ldy, int y_type, float *y_scales, void *total, long long ldt,
@@ -507,7 +508,7 @@ int lmoe_add_rmsnorm(const void *x, long long ldx, const void *residual, long lo
  *   dx [rows, cols] bf16 out (it may be dy or dtotal itself), dgamma [cols] fp32 out, or NULL
  *   (not wanted; ws is then unused); ws: lmoe_add_rmsnorm_backward_workspace_bytes of device
  *   scratch, 16-byte aligned.  Strides, widths and alignment as above.  rows == 0 sets dgamma to 0.
- * Errors: INVALID_ARG, UNSUPPORTED (rows >= 2^31), WORKSPACE_TOO_SMALL. */
+ * Errors: INVALID_ARG, UNSUPPORTED (rows >= 2^31, cols > 2^30), WORKSPACE_TOO_SMALL, CUDA. */
 size_t lmoe_add_rmsnorm_backward_workspace_bytes(long long rows, int cols);
 int lmoe_add_rmsnorm_backward(const void *dy, long long ldy, const void *total, long long ldt,
                               const float *gamma, const float *rstd, const void *dtotal,
@@ -551,7 +552,8 @@ typedef struct lmoe_linear {
 /* The layer's output y (and pre).  N a multiple of 8, K of 8 (16 for e4m3); x, w, residual, y and
  * pre 16-byte aligned with row distances in whole 16 bytes.  y and pre overlap no input (y may be
  * residual itself).  M == 0 is a no-op.
- * Errors: INVALID_ARG, UNSUPPORTED (N, K; 2^27 or more 64 x 64 tiles), CUDA. */
+ * Errors: INVALID_ARG, UNSUPPORTED (N, K; M, K or rows above 2^30; above 2^27 tiles of 64 x 64),
+ * CUDA. */
 int lmoe_linear_forward(const lmoe_linear *p, void *stream);
 
 /* Its gradients, given dy = dLoss/dy [M, N] bf16 (rows lddy elements apart) and the forward's

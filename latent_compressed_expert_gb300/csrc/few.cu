@@ -1109,6 +1109,9 @@ int lmoe_forward_few(const lmoe_dims* dims, const void* packed, const void* x,
   if (!al16(packed) || !al16(x) || !al16(y) || !al16(residual) || !al16(workspace) ||
       !al16(opt.tau_in) || !al16(opt.logits_in) || !al16(opt.logit_bias))
     return LMOE_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(opt.logits_out) | reinterpret_cast<uintptr_t>(opt.idx_out) |
+       reinterpret_cast<uintptr_t>(opt.gate_out) | reinterpret_cast<uintptr_t>(opt.y_f32_out)) & 3u)
+    return LMOE_ERR_INVALID_ARG;
   if (y == x || (residual && y == residual)) return LMOE_ERR_INVALID_ARG;
   const FewLayout W = few_layout(D);
   if (ws_bytes < W.total) return LMOE_ERR_WORKSPACE_TOO_SMALL;

@@ -67,7 +67,7 @@ constexpr int LINEAR_THREADS = 320;  // TMA, MMA and eight epilogue warps (two p
 constexpr int LINEAR_RASTER = 16;  // row tiles that sweep the column tiles together
 
 template <int MODE>
-struct LinearMode_ {
+struct LinearTraits {
   static constexpr bool SWAP = MODE != MODE_DW;    // the accumulator is the output transposed
   static constexpr bool P_MN = MODE != MODE_FWD, Q_MN = MODE == MODE_DW;
 };
@@ -75,8 +75,8 @@ struct LinearMode_ {
 template <int MODE, bool FP8>
 __host__ __device__ constexpr uint32_t linear_idesc(int M, int N) {
   return FP8 ? ptx::idesc_e4m3_f32(M, N)
-             : ptx::idesc_bf16_f32(M, N) | (LinearMode_<MODE>::P_MN ? 1u << 15 : 0u) |
-                   (LinearMode_<MODE>::Q_MN ? 1u << 16 : 0u);
+             : ptx::idesc_bf16_f32(M, N) | (LinearTraits<MODE>::P_MN ? 1u << 15 : 0u) |
+                   (LinearTraits<MODE>::Q_MN ? 1u << 16 : 0u);
 }
 
 constexpr int LINEAR_P_BYTES = BLOCK_M * 128;       // a CTA's part of P in a stage
@@ -233,7 +233,7 @@ __device__ __forceinline__ LinearSmem linear_smem(uint8_t* raw, int stage_area) 
 template <int MODE, bool FP8, bool PAIR>
 __device__ __forceinline__ void linear_mma(uint32_t d, uint32_t sp, uint32_t sq, uint32_t idesc,
                                            bool first) {
-  using T = LinearMode_<MODE>;
+  using T = LinearTraits<MODE>;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const uint64_t da = T::P_MN ? ptx::smem_desc_sw128_mn(sp + k * 2048, LINEAR_BOX_BYTES)
@@ -268,7 +268,7 @@ template <int MODE, bool FP8, bool GLU>
 __global__ void __launch_bounds__(LINEAR_THREADS, 2)
 linear_tile_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
                    const LinearArgs g) {
-  using T = LinearMode_<MODE>;
+  using T = LinearTraits<MODE>;
   const int bn = g.bn, stages = g.stages, ks = g.ks;
   const int stage_bytes = LINEAR_P_BYTES + bn * 128;
   const int TM = T::SWAP ? bn : BLOCK_M;                        // output rows of a tile
@@ -523,7 +523,7 @@ template <int MODE, bool FP8, bool GLU>
 __global__ void __launch_bounds__(LINEAR_THREADS, 1)
 linear_pair_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
                    const __grid_constant__ CUtensorMap tmO, const LinearArgs g) {
-  using T = LinearMode_<MODE>;
+  using T = LinearTraits<MODE>;
   const int bn = g.bn, stages = g.stages;
   const int stage_bytes = LINEAR_P_BYTES + bn / 2 * 128;
   constexpr int PROWS = GLU ? BLOCK_M / 2 : BLOCK_M;  // output columns (MODE_DW: rows) of a CTA
@@ -829,7 +829,7 @@ inline bool linear_map(CUtensorMap* m, const LinearOperand& o, bool mn, int rows
 template <int MODE, bool FP8, bool GLU>
 int launch_linear_tile(const LinearOperand& P, const LinearOperand& Q, const LinearArgs& g, int dev,
                        cudaStream_t stream) {
-  using T = LinearMode_<MODE>;
+  using T = LinearTraits<MODE>;
   static std::atomic<int> cache[LINEAR_MAX_DEVICES];
   auto kernel = linear_tile_kernel<MODE, FP8, GLU>;
   if (linear_kernel_setup(kernel, 1, dev, cache) < 0) return LMOE_ERR_CUDA;
@@ -859,7 +859,7 @@ int launch_linear_tile(const LinearOperand& P, const LinearOperand& Q, const Lin
 template <int MODE, bool FP8, bool GLU>
 int launch_linear_pair(const LinearOperand& P, const LinearOperand& Q, const LinearArgs& g, int dev,
                        int sms, cudaStream_t stream) {
-  using T = LinearMode_<MODE>;
+  using T = LinearTraits<MODE>;
   static std::atomic<int> cache[LINEAR_MAX_DEVICES];
   auto kernel = linear_pair_kernel<MODE, FP8, GLU>;
   // a persistent grid: no more pairs than can be resident at once (an SM pair shares a GPC)
@@ -909,7 +909,7 @@ int launch_linear(const LinearOperand& A, const LinearOperand& B, const LinearAr
   g.bn = p.bn;
   g.stages = p.stages;
   g.ks = p.ks;
-  constexpr bool SWAP = LinearMode_<MODE>::SWAP;
+  constexpr bool SWAP = LinearTraits<MODE>::SWAP;
   const LinearOperand &P = SWAP ? B : A, &Q = SWAP ? A : B;
   return p.pair ? launch_linear_pair<MODE, FP8, GLU>(P, Q, g, dev, sms, stream)
                 : launch_linear_tile<MODE, FP8, GLU>(P, Q, g, dev, stream);

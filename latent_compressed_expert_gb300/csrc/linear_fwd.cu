@@ -87,8 +87,10 @@ int linear_sizes_ok(const lmoe_linear* p) {
   if (p->act == LMOE_ACT_SITU && !(p->c > 0.0f)) return LMOE_ERR_INVALID_ARG;
   // whole 16-byte rows (TMA), and 32-bit tile counts
   const int unit = p->type == LMOE_E4M3 ? 16 : 8;
-  if (p->N % 8 || p->K % unit || p->N > (1 << 30)) return LMOE_ERR_UNSUPPORTED;
   const int64_t rows = p->act == LMOE_ACT_SITU ? 2 * static_cast<int64_t>(p->N) : p->N;
+  constexpr int MOST = 1 << 30;  // row and column numbers and a tile more fit an int
+  if (p->N % 8 || p->K % unit || rows > MOST || p->M > MOST || p->K > MOST)
+    return LMOE_ERR_UNSUPPORTED;
   if (ceil_div(p->M, 64) * ceil_div(rows, 64) > (1 << 27) ||
       ceil_div(rows, 64) * ceil_div(p->K, 64) > (1 << 27) ||
       ceil_div(p->M, 64) * ceil_div(p->K, 64) > (1 << 27))
@@ -141,7 +143,9 @@ extern "C" int lmoe_linear_forward(const lmoe_linear* p, void* stream) {
   if (p->ldy < p->N || p->ldy % 8 || (p->residual && (p->ldr < p->N || p->ldr % 8)) ||
       (p->pre && (p->ldp < rows || p->ldp % 8)))
     return LMOE_ERR_INVALID_ARG;
-  if (p->y == p->x || (p->pre && (p->pre == p->y || p->pre == p->x))) return LMOE_ERR_INVALID_ARG;
+  if (p->y == p->x || p->y == p->w) return LMOE_ERR_INVALID_ARG;
+  if (p->pre && (p->pre == p->y || p->pre == p->x || p->pre == p->w || p->pre == p->residual))
+    return LMOE_ERR_INVALID_ARG;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   return fp8 ? forward<true>(*p, st) : forward<false>(*p, st);
 }

@@ -641,6 +641,8 @@ static int launch_add_rmsnorm_bwd(const NormBwdArgs& a, float* dgamma, cudaStrea
 
 using namespace lmoe;
 
+constexpr int NORM_MAX_COLS = 1 << 30;
+
 extern "C" {
 
 int lmoe_add_rmsnorm(const void* x, long long ldx, const void* residual, long long ldr,
@@ -649,7 +651,7 @@ int lmoe_add_rmsnorm(const void* x, long long ldx, const void* residual, long lo
                      float* rstd, void* stream) {
   if (rows < 0 || cols < 1 || !(eps >= 0.0f)) return LMOE_ERR_INVALID_ARG;
   if (y_type != LMOE_BF16 && y_type != LMOE_E4M3) return LMOE_ERR_INVALID_ARG;
-  if (rows > INT32_MAX) return LMOE_ERR_UNSUPPORTED;  // the grid
+  if (rows > INT32_MAX || cols > NORM_MAX_COLS) return LMOE_ERR_UNSUPPORTED;  // grid, int indices
   if (rows == 0) return LMOE_OK;
   if (!x || !gamma || !y || (y_type == LMOE_E4M3 && !y_scales)) return LMOE_ERR_INVALID_ARG;
   if (ldx < cols || ldy < cols || (residual && ldr < cols) || (total && ldt < cols))
@@ -682,7 +684,7 @@ int lmoe_add_rmsnorm(const void* x, long long ldx, const void* residual, long lo
 }
 
 size_t lmoe_add_rmsnorm_backward_workspace_bytes(long long rows, int cols) {
-  if (rows < 0 || cols < 1) return 0;
+  if (rows < 0 || rows > INT32_MAX || cols < 1 || cols > NORM_MAX_COLS) return 0;
   const long long parts = rows < NORM_BWD_MAX_PARTS ? rows : NORM_BWD_MAX_PARTS;
   return static_cast<size_t>(parts > 0 ? parts : 1) * cols * sizeof(float);
 }
@@ -692,7 +694,7 @@ int lmoe_add_rmsnorm_backward(const void* dy, long long ldy, const void* total, 
                               long long ldd, long long rows, int cols, void* dx, long long ldx,
                               float* dgamma, void* ws, size_t ws_bytes, void* stream) {
   if (rows < 0 || cols < 1) return LMOE_ERR_INVALID_ARG;
-  if (rows > INT32_MAX) return LMOE_ERR_UNSUPPORTED;
+  if (rows > INT32_MAX || cols > NORM_MAX_COLS) return LMOE_ERR_UNSUPPORTED;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (rows == 0)
     return !dgamma || cudaMemsetAsync(dgamma, 0, sizeof(float) * cols, st) == cudaSuccess

@@ -497,6 +497,8 @@ def _add_rmsnorm(x, gamma, residual, eps, fp8, train, y, total):
     if y is None:
         y = torch.empty((rows, cols), dtype=torch.uint8 if fp8 else bf, device=device)
         py, ldy = y.data_ptr(), cols
+    elif train and pt is None and y.data_ptr() == px:
+        raise ValueError("lmoe: y over x would destroy the total that the backward needs")
     else:
         py, ldy = _rows(y, bf, rows, cols, dev, "y")
     scales = rstd = None
