@@ -17,7 +17,8 @@
 // Two kernels, chosen by linear_plan:
 //   linear_pair_kernel   256 x bn tiles over SM pairs (cta_group::2), persistent, two accumulator
 //                        sets, so that one tile is written while the next is computed.  An SM
-//                        stages 16 KB of P and bn / 2 rows of Q per K-block.
+//                        stages 16 KB of P and bn / 2 rows of Q per K-block.  Its MODE_GRADS
+//                        computes dx, dw or both.
 //   linear_tile_kernel   128 x bn tiles, one per cluster of ks CTAs that split the reduction
 //                        between them and add their parts through distributed shared memory in
 //                        rank order (no scratch, no second kernel, a fixed order).  For problems
@@ -36,7 +37,13 @@
 
 namespace lmoe {
 
-enum LinearMode : int { MODE_FWD = 0, MODE_DX = 1, MODE_DW = 2 };
+enum LinearMode : int { MODE_FWD = 0, MODE_DX = 1, MODE_DW = 2, MODE_GRADS = 3 };
+
+// A product's extents over SM pairs.
+struct LinearPart {
+  int R, C, D;          // output rows and columns, reduction length
+  int bn;               // columns of the MMA
+};
 
 struct LinearArgs {
   int R, C, D;          // output rows and columns (GLU: features), reduction length
@@ -58,6 +65,10 @@ struct LinearArgs {
   int bn;               // columns of the MMA
   int stages;           // of 16 KB of P and bn (SM pair: bn / 2) rows of Q
   int ks;               // linear_tile_kernel: CTAs of a cluster
+  LinearPart dw;        // MODE_GRADS: the weight gradient (the fields above: dx)
+  int dx_tiles;         // its tiles of dx, which come first; 0: dw alone
+  int dw_tiles;         // 0: dx alone
+  int dw_lead;          // tiles of dw that a pair with fewer tiles of dx takes before the others
   int inject_stall;     // test hook: the MMA role first waits on a barrier nobody arrives on
   uint32_t* err;
   unsigned long long timeout_ns;
@@ -159,7 +170,7 @@ __device__ __forceinline__ void linear_store8(const LinearArgs& g, int row, int 
       }
     }
   }
-  if (MODE != MODE_FWD && g.out_f32) {
+  if (MODE == MODE_DW && g.out_f32) {
     float4* o = reinterpret_cast<float4*>(static_cast<float*>(g.out) + rr * g.ldo + col);
     o[0] = make_float4(v[0], v[1], v[2], v[3]);
     o[1] = make_float4(v[4], v[5], v[6], v[7]);
@@ -473,14 +484,18 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constan
 }
 
 // ------------------------------------------------------------------------- SM pairs
-// The epilogue's shared memory.  SWAP: two buffers, one for each half of its warps, through which
-// they turn 32 accumulator columns round (32 output rows of 128 columns, padded, as above).
-// MODE_DW: 32 rows x 32 fp32 (or bf16) for each of its warps, on their way into a tensor store.
+// The epilogue's shared memory: a buffer for each half of its warps, through which they turn 32
+// accumulator columns round (32 output rows of 128 columns, padded, as above).  dw: 32 rows x 32
+// fp32 (or bf16) for each of the half's warps, on their way into a tensor store.
 constexpr int LINEAR_TURN_LD = BLOCK_M + 4;
 constexpr int LINEAR_TURN_BYTES = 32 * LINEAR_TURN_LD * 4;
-static_assert(2 * LINEAR_TURN_BYTES >= 8 * 32 * 128, "both forms fit");
+constexpr int linear_dw_buffer(int half, int q) {  // 1024-byte aligned, within the half's buffer
+  return (half * LINEAR_TURN_BYTES + 1023) / 1024 * 1024 + q * 32 * 128;
+}
+static_assert(linear_dw_buffer(0, 4) <= LINEAR_TURN_BYTES, "both forms fit");
+static_assert(linear_dw_buffer(1, 4) <= 2 * LINEAR_TURN_BYTES, "both forms fit");
 
-// MODE_DW's epilogue: a warp's 32 rows by 32 accumulator columns at a time through its own buffer
+// dw's epilogue: a warp's 32 rows by 32 accumulator columns at a time through its own buffer
 // into a tensor store, whose map cuts rows and columns outside the output.  (Through registers and
 // store instructions, eight rows of 64 or 128 bytes each, the wgrad of a few rows took 1.6 times
 // as long.)
@@ -514,20 +529,88 @@ __device__ __forceinline__ void linear_dw_chunk(const CUtensorMap* tmO, const Li
   }
 }
 
+struct LinearPairTile {
+  bool dw;
+  LinearPart part;
+  int row0, col0;
+};
+
+// The tiles of an SM pair, in order.  MODE_GRADS: the pairs are dealt dx's tiles, which are the
+// longer ones, then dw's, of which those pairs that got one tile of dx less take the first
+// dw_lead rounds.  What does not depend on the tile is worked out once: a tile of few K-blocks has
+// no time for divisions.
+template <int MODE, bool GLU>
+struct LinearPairDeal {
+  static constexpr int COLS = GLU ? BLOCK_M : 2 * BLOCK_M;  // output columns (dw: rows) of P's rows
+  int cid, ncl;
+  int mt, nt, tiles;      // row and column tiles, tiles (MODE_GRADS: of this pair) of the main part
+  int dw_mt, dw_nt;
+  int first, lead, ahead;  // dw: this pair's first tile of the leading rounds, how many, their total
+  int stride;              // of the leading rounds
+
+  __device__ __forceinline__ LinearPairDeal(const LinearArgs& g, int cid_, int ncl_)
+      : cid(cid_), ncl(ncl_) {
+    mt = MODE == MODE_GRADS && g.dx_tiles == 0 ? 0 : (g.R + g.bn - 1) / g.bn;
+    nt = (g.C + COLS - 1) / COLS;
+    tiles = mt * nt;
+    if constexpr (MODE == MODE_GRADS) {
+      const int extra = g.dx_tiles % ncl;
+      tiles = g.dx_tiles / ncl + (cid < extra ? 1 : 0);
+      dw_mt = (g.dw.R + COLS - 1) / COLS;
+      dw_nt = g.dw_tiles == 0 ? 0 : (g.dw.C + g.dw.bn - 1) / g.dw.bn;
+      stride = ncl - extra;
+      ahead = g.dw_lead * stride;
+      first = cid - extra;
+      lead = cid < extra ? 0 : g.dw_lead;
+    }
+  }
+  // the pair's i-th tile, if it has that many
+  __device__ __forceinline__ bool at(const LinearArgs& g, int i, LinearPairTile* t) const {
+    int tile = cid + i * ncl;
+    t->dw = MODE == MODE_GRADS && i >= tiles;
+    if (t->dw) {
+      const int j = i - tiles;
+      tile = j < lead ? j * stride + first : ahead + (j - lead) * ncl + cid;
+      if (tile >= g.dw_tiles) return false;
+      t->part = g.dw;
+      const LinearTile p = linear_tile(tile, dw_mt, dw_nt, COLS, g.dw.bn);
+      t->row0 = p.row0;
+      t->col0 = p.col0;
+      return true;
+    }
+    if (MODE == MODE_FWD && tile >= tiles) return false;
+    t->part = LinearPart{g.R, g.C, g.D, g.bn};
+    const LinearTile p = linear_tile(tile, mt, nt, g.bn, COLS);
+    t->row0 = p.row0;
+    t->col0 = p.col0;
+    return true;
+  }
+};
+
+struct LinearPairMaps {
+  CUtensorMap p, q;        // MODE_FWD; MODE_GRADS: dx
+  CUtensorMap dw_p, dw_q;  // MODE_GRADS: dw
+  CUtensorMap dw_out;
+};
+
 // Rank r of a pair holds 128 rows of P (128 r ..; GLU: 64 gate rows of features 64 r .. and the
 // same features' value rows) and half of Q's columns; the MMAs, issued by rank 0, read both CTAs'
 // shared memory, and each CTA's TMEM receives its P rows by all bn columns.  full[s] and tempty[a]
 // of rank 0 collect both CTAs' copies and epilogue warps; empty[s] and tfull[a] of both get rank
 // 0's commits; cluster barriers bracket set-up and teardown.
+// MODE_GRADS computes both gradients in one launch: neither product of a few hundred rows has
+// tiles enough to keep all SM pairs busy, and while dx reads the weights, dw writes its output
+// (333 rows, 3584 x 7168, fp32 dw: 38.4 us against 47.2 one after the other; 2048 rows, 7168 x 4096,
+// bf16 dw: 139 against 152, 0.96 of the bf16 peak; at 4096 rows and more it makes no difference).
 template <int MODE, bool FP8, bool GLU>
 __global__ void __launch_bounds__(LINEAR_THREADS, 1)
-linear_pair_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
-                   const __grid_constant__ CUtensorMap tmO, const LinearArgs g) {
-  using T = LinearTraits<MODE>;
-  const int bn = g.bn, stages = g.stages;
-  const int stage_bytes = LINEAR_P_BYTES + bn / 2 * 128;
-  constexpr int PROWS = GLU ? BLOCK_M / 2 : BLOCK_M;  // output columns (MODE_DW: rows) of a CTA
-  const int TM = T::SWAP ? bn : 2 * PROWS, TN = T::SWAP ? 2 * PROWS : bn;
+linear_pair_kernel(const __grid_constant__ LinearPairMaps maps, const LinearArgs g) {
+  static_assert(MODE == MODE_FWD || MODE == MODE_GRADS, "");
+  constexpr int MAIN = MODE == MODE_FWD ? MODE_FWD : MODE_DX;
+  const int stages = g.stages;
+  const int wide = MODE == MODE_GRADS && g.dw.bn > g.bn ? g.dw.bn : g.bn;
+  const int stage_bytes = LINEAR_P_BYTES + wide / 2 * 128;
+  constexpr int PROWS = GLU ? BLOCK_M / 2 : BLOCK_M;  // output columns (dw: rows) of a CTA
   constexpr int TMEM_COLS = 512;  // two accumulator sets, 256 columns apart
   extern __shared__ uint8_t smem_raw[];
   const LinearSmem m = linear_smem(smem_raw, stages * stage_bytes + 2 * LINEAR_TURN_BYTES);
@@ -538,8 +621,6 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constan
   const int rank = static_cast<int>(ptx::cluster_ctarank());
   const bool lead = rank == 0;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int mt = (g.R + TM - 1) / TM, nt = (g.C + TN - 1) / TN, total = mt * nt;
-  const int nk = (g.D + LINEAR_KSTEP<FP8> - 1) / LINEAR_KSTEP<FP8>;
   const uint64_t limit = g.timeout_ns;
 
   if (threadIdx.x == 0) {
@@ -554,8 +635,12 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constan
     ptx::mbar_init(drain, 1);
     *abort_flag = 0;
     ptx::fence_mbar_init();
-    ptx::prefetch_tmap(&tmP);
-    ptx::prefetch_tmap(&tmQ);
+    ptx::prefetch_tmap(&maps.p);
+    ptx::prefetch_tmap(&maps.q);
+    if constexpr (MODE == MODE_GRADS) {
+      ptx::prefetch_tmap(&maps.dw_p);
+      ptx::prefetch_tmap(&maps.dw_q);
+    }
   }
   ptx::cluster_sync();  // both CTAs' barriers exist before either signals the other's
   if (warp == 1) {
@@ -570,6 +655,10 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constan
   pdl_launch_dependents();
   const int cid = static_cast<int>(ptx::cluster_id_x());
   const int ncl = static_cast<int>(ptx::ncluster_x());
+  const LinearPairDeal<MODE, GLU> deal(g, cid, ncl);
+  auto tile_at = [&](int i, LinearPairTile* t) { return deal.at(g, i, t); };
+  auto blocks = [](const LinearPart& p) { return (p.D + LINEAR_KSTEP<FP8> - 1) / LINEAR_KSTEP<FP8>; };
+  LinearPairTile t;
 
   if (warp == 0) {
     if (lane == 0) {
@@ -578,10 +667,10 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constan
       int s = 0;
       uint32_t parity = 1;
       bool ok = true;
-      for (int tile = cid; ok && tile < total; tile += ncl) {
-        const LinearTile t = linear_tile(tile, mt, nt, TM, TN);
-        const int prow = (T::SWAP ? t.col0 : t.row0) + rank * PROWS;
-        const int qrow = (T::SWAP ? t.row0 : t.col0) + rank * (bn / 2);
+      for (int i = 0; ok && tile_at(i, &t); ++i) {
+        const int bn = t.part.bn, nk = blocks(t.part);
+        const int prow = (t.dw ? t.row0 : t.col0) + rank * PROWS;
+        const int qrow = (t.dw ? t.col0 : t.row0) + rank * (bn / 2);
         for (int kb = 0; kb < nk; ++kb, ++it) {
           if (!ptx::mbar_wait(&m.empty[s], parity, abort_flag, limit)) {
             linear_fail(g, abort_flag, DEVERR_TIMEOUT_PRODUCER);
@@ -591,23 +680,26 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constan
           uint8_t* sp = m.base + s * stage_bytes;
           uint8_t* sq = sp + LINEAR_P_BYTES;
           const uint32_t fb = ptx::mapa_shared(ptx::smem_u32(&m.full[s]), 0);
-          if (lead) ptx::mbar_arrive_expect_tx(&m.full[s], 2u * stage_bytes);
+          if (lead)
+            ptx::mbar_arrive_expect_tx(&m.full[s],
+                                       2u * static_cast<uint32_t>(LINEAR_P_BYTES + bn / 2 * 128));
           const int k = kb * BLOCK_K;
-          if constexpr (T::P_MN) {
+          if constexpr (MODE == MODE_GRADS) {
+            const CUtensorMap* p = t.dw ? &maps.dw_p : &maps.p;
 #pragma unroll
-            for (int i = 0; i < BLOCK_M / 64; ++i)
-              ptx::tma_load_2d_pair(sp + i * LINEAR_BOX_BYTES, &tmP, fb, prow + 64 * i, k);
+            for (int b = 0; b < BLOCK_M / 64; ++b)
+              ptx::tma_load_2d_pair(sp + b * LINEAR_BOX_BYTES, p, fb, prow + 64 * b, k);
           } else if constexpr (GLU) {
-            ptx::tma_load_2d_pair(sp, &tmP, fb, k, prow);
-            ptx::tma_load_2d_pair(sp + PROWS * 128, &tmP, fb, k, g.glu_off + prow);
+            ptx::tma_load_2d_pair(sp, &maps.p, fb, k, prow);
+            ptx::tma_load_2d_pair(sp + PROWS * 128, &maps.p, fb, k, g.glu_off + prow);
           } else {
-            ptx::tma_load_2d_pair(sp, &tmP, fb, k, prow);
+            ptx::tma_load_2d_pair(sp, &maps.p, fb, k, prow);
           }
-          if constexpr (T::Q_MN) {
-            for (int i = 0; i < bn / 128; ++i)
-              ptx::tma_load_2d_pair(sq + i * LINEAR_BOX_BYTES, &tmQ, fb, qrow + 64 * i, k);
+          if (MODE == MODE_GRADS && t.dw) {
+            for (int b = 0; b < bn / 128; ++b)
+              ptx::tma_load_2d_pair(sq + b * LINEAR_BOX_BYTES, &maps.dw_q, fb, qrow + 64 * b, k);
           } else {
-            ptx::tma_load_2d_pair(sq, &tmQ, fb, k, qrow);
+            ptx::tma_load_2d_pair(sq, &maps.q, fb, k, qrow);
           }
           if (++s == stages) s = 0, parity ^= 1u;
         }
@@ -625,19 +717,21 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constan
   } else if (warp == 1) {
     if (lane == 0 && lead) {
       // ------------------------------------------------------------ MMA issuer (rank 0)
-      const uint32_t idesc = linear_idesc<MODE, FP8>(2 * BLOCK_M, bn);
-      int lt = 0, s = 0;
+      int s = 0;
       uint32_t parity = 0;
       bool ok = !g.inject_stall || ptx::mbar_wait(drain, 0, abort_flag, limit);
       if (!ok) linear_fail(g, abort_flag, DEVERR_TIMEOUT_MMA);
-      for (int tile = cid; ok && tile < total; tile += ncl, ++lt) {
-        const int acc = lt & 1;
-        if (!ptx::mbar_wait(&tempty[acc], ((lt >> 1) & 1) ^ 1, abort_flag, limit)) {
+      for (int i = 0; ok && tile_at(i, &t); ++i) {
+        const int acc = i & 1, nk = blocks(t.part);
+        if (!ptx::mbar_wait(&tempty[acc], ((i >> 1) & 1) ^ 1, abort_flag, limit)) {
           linear_fail(g, abort_flag, DEVERR_TIMEOUT_MMA);
           break;
         }
         ptx::tc_fence_after();
         const uint32_t d = tmem_base + static_cast<uint32_t>(acc * 256);
+        const uint32_t idesc = MODE == MODE_GRADS && t.dw
+                                   ? linear_idesc<MODE_DW, FP8>(2 * BLOCK_M, t.part.bn)
+                                   : linear_idesc<MAIN, FP8>(2 * BLOCK_M, t.part.bn);
         for (int kb = 0; kb < nk; ++kb) {
           if (!ptx::mbar_wait(&m.full[s], parity, abort_flag, limit)) {
             linear_fail(g, abort_flag, DEVERR_TIMEOUT_MMA);
@@ -646,7 +740,10 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constan
           }
           ptx::tc_fence_after();
           const uint32_t sp = ptx::smem_u32(m.base + s * stage_bytes);
-          linear_mma<MODE, FP8, true>(d, sp, sp + LINEAR_P_BYTES, idesc, kb == 0);
+          if (MODE == MODE_GRADS && t.dw)
+            linear_mma<MODE_DW, FP8, true>(d, sp, sp + LINEAR_P_BYTES, idesc, kb == 0);
+          else
+            linear_mma<MAIN, FP8, true>(d, sp, sp + LINEAR_P_BYTES, idesc, kb == 0);
           ptx::umma_commit_pair(&m.empty[s], 0x3);
           if (++s == stages) s = 0, parity ^= 1u;
         }
@@ -671,14 +768,13 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constan
     constexpr int G = PROWS / 8;            // column groups of a buffer's rows
     constexpr int ITEMS = 32 * G / 128;     // per thread
     const int gr = tid / G, gc = tid % G;   // item j: buffer row gr + j 128 / G, group gc
-    int lt = 0;
-    for (int tile = cid; tile < total; tile += ncl, ++lt) {
-      const int acc = lt & 1;
-      const LinearTile t = linear_tile(tile, mt, nt, TM, TN);
-      // SWAP: output row of item j in chunk ch, and this thread's columns
+    for (int i = 0; tile_at(i, &t); ++i) {
+      const int acc = i & 1;
+      // output row of item j in chunk ch, and this thread's columns (not dw)
       auto row_of = [&](int ch, int j) { return t.row0 + ch * 32 + gr + j * (128 / G); };
       const int col = t.col0 + rank * PROWS + gc * 8;
-      const int chunks = (min(bn, T::SWAP ? g.R - t.row0 : g.C - t.col0) + 31) / 32;
+      const int chunks =
+          (min(t.part.bn, t.dw ? t.part.C - t.col0 : t.part.R - t.row0) + 31) / 32;
       LinearCols ca, cb;
       if constexpr (MODE == MODE_FWD) {
         linear_cols<FP8>(g, col, col < g.C, &ca);
@@ -692,7 +788,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constan
           if (row_of(ch, j) < g.R) rnext[j] = linear_resid8(g, row_of(ch, j), col);
       };
       load_res(half);
-      const bool got = ptx::mbar_wait(&tfull[acc], (lt >> 1) & 1, abort_flag, limit);
+      const bool got = ptx::mbar_wait(&tfull[acc], (i >> 1) & 1, abort_flag, limit);
       // a half's warps leave together: they share its barrier
       if (!ptx::named_and(bar, 128, got)) {
         if (lane == 0) linear_fail(g, abort_flag, DEVERR_TIMEOUT_EPILOGUE);
@@ -712,47 +808,48 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constan
         }
       };
       if (half >= chunks) release();
+      if (MODE == MODE_GRADS && t.dw) {
+#pragma unroll 1
+        for (int ch = half; ch < chunks; ch += 2)
+          linear_dw_chunk(&maps.dw_out, g, reinterpret_cast<uint8_t*>(turn) + linear_dw_buffer(half, q), lane,
+                          tb + static_cast<uint32_t>(ch * 32), t.row0 + rank * BLOCK_M + q * 32,
+                          t.col0 + ch * 32, ch + 2 >= chunks, release);
+        continue;
+      }
 #pragma unroll 1
       for (int ch = half; ch < chunks; ch += 2) {
-        const uint32_t taddr = tb + static_cast<uint32_t>(ch * 32);
-        if constexpr (!T::SWAP) {
-          linear_dw_chunk(&tmO, g, reinterpret_cast<uint8_t*>(turn) + (warp - 2) * 4096, lane, taddr,
-                          t.row0 + rank * BLOCK_M + q * 32, t.col0 + ch * 32, ch + 2 >= chunks,
-                          release);
-        } else {
-          uint4 rcur[ITEMS];
+        uint4 rcur[ITEMS];
 #pragma unroll
-          for (int j = 0; j < ITEMS; ++j) rcur[j] = rnext[j];
-          float v[32];
-          ptx::tmem_ld_32x32b_x32(taddr, v);
-          if (ch + 2 >= chunks) release();
-          if (ch + 2 < chunks) load_res(ch + 2);
-          ptx::named_sync(bar, 128);  // the buffer's last chunk has been read
+        for (int j = 0; j < ITEMS; ++j) rcur[j] = rnext[j];
+        float v[32];
+        ptx::tmem_ld_32x32b_x32(tb + static_cast<uint32_t>(ch * 32), v);
+        if (ch + 2 >= chunks) release();
+        if (ch + 2 < chunks) load_res(ch + 2);
+        ptx::named_sync(bar, 128);  // the buffer's last chunk has been read
 #pragma unroll
-          for (int j = 0; j < 32; ++j) buf[j * LINEAR_TURN_LD + q * 32 + lane] = v[j];
-          ptx::named_sync(bar, 128);
-          if (col >= g.C) continue;
+        for (int j = 0; j < 32; ++j) buf[j * LINEAR_TURN_LD + q * 32 + lane] = v[j];
+        ptx::named_sync(bar, 128);
+        if (col >= g.C) continue;
 #pragma unroll
-          for (int j = 0; j < ITEMS; ++j) {
-            const int row = row_of(ch, j);
-            if (row >= g.R) continue;
-            const float* p = buf + (gr + j * (128 / G)) * LINEAR_TURN_LD + gc * 8;
-            const float xs = FP8 ? __ldg(g.xs + row) : 1.0f;
-            float a[8];
-            linear_read8(p, a);
-            if constexpr (GLU) {
-              float b[8];
-              linear_read8(p + PROWS, b);
-              linear_store_glu8<FP8>(g, row, col, ca, cb, xs, inv_c, a, b, rcur[j]);
-            } else {
-              linear_store8<MODE, FP8>(g, row, col, ca, xs, a, rcur[j]);
-            }
+        for (int j = 0; j < ITEMS; ++j) {
+          const int row = row_of(ch, j);
+          if (row >= g.R) continue;
+          const float* p = buf + (gr + j * (128 / G)) * LINEAR_TURN_LD + gc * 8;
+          const float xs = FP8 ? __ldg(g.xs + row) : 1.0f;
+          float a[8];
+          linear_read8(p, a);
+          if constexpr (GLU) {
+            float b[8];
+            linear_read8(p + PROWS, b);
+            linear_store_glu8<FP8>(g, row, col, ca, cb, xs, inv_c, a, b, rcur[j]);
+          } else {
+            linear_store8<MAIN, FP8>(g, row, col, ca, xs, a, rcur[j]);
           }
         }
       }
     }
     // the tensor stores complete before the CTA leaves (they read its shared memory)
-    if (!T::SWAP && lane == 0) ptx::bulk_wait_group_all();
+    if (MODE == MODE_GRADS && lane == 0) ptx::bulk_wait_group_all();
   }
 
   ptx::tc_fence_before();
@@ -769,6 +866,11 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constan
 struct LinearPlan {
   bool pair;
   int bn, stages, ks;
+  double ns;            // estimate
+};
+struct LinearGradsPlan {
+  int bn, dw_bn, stages, dw_lead;
+  double ns;
 };
 constexpr int LINEAR_SMEM_MAX = 232448;           // of a CTA alone on its SM
 constexpr int LINEAR_SMEM_HALF = 113 * 1024;   // of two: an SM has 228 KB, 1 KB of it per CTA taken
@@ -777,7 +879,10 @@ constexpr int linear_smem_bytes(bool pair, int mode, int bn, int stages) {
                : linear_stage_area(mode, bn, stages)) +
          LINEAR_MISC + 1024;  // + slack for 1024 alignment
 }
-LinearPlan linear_plan(int mode, int R, int C, int D, bool fp8, bool glu, int sms);
+// out_size: bytes of an output element.
+LinearPlan linear_plan(int mode, int R, int C, int D, int out_size, bool fp8, bool glu, int sms);
+// Both gradients in one launch: dx [R, C] over D and dw [D, C] over R.
+LinearGradsPlan linear_grads_plan(int R, int C, int D, int dw_size, int sms);
 
 constexpr int LINEAR_MAX_DEVICES = 64;
 
@@ -856,33 +961,26 @@ int launch_linear_tile(const LinearOperand& P, const LinearOperand& Q, const Lin
   return cudaLaunchKernelEx(&cfg, kernel, tp, tq, g) == cudaSuccess ? LMOE_OK : LMOE_ERR_CUDA;
 }
 
+inline int64_t linear_pair_tiles(int P, int Q, int bn, bool glu) {
+  return ceil_div(P, glu ? BLOCK_M : 2 * BLOCK_M) * ceil_div(Q, bn);
+}
+
+// pairs: no more than have work.
 template <int MODE, bool FP8, bool GLU>
-int launch_linear_pair(const LinearOperand& P, const LinearOperand& Q, const LinearArgs& g, int dev,
+int launch_linear_pair(const LinearPairMaps& maps, const LinearArgs& g, int64_t pairs, int dev,
                        int sms, cudaStream_t stream) {
-  using T = LinearTraits<MODE>;
   static std::atomic<int> cache[LINEAR_MAX_DEVICES];
   auto kernel = linear_pair_kernel<MODE, FP8, GLU>;
   // a persistent grid: no more pairs than can be resident at once (an SM pair shares a GPC)
   const int active = linear_kernel_setup(kernel, 2, dev, cache);
   if (active < 0) return LMOE_ERR_CUDA;
-  CUtensorMap tp, tq;
-  const int prows = GLU ? BLOCK_M / 2 : BLOCK_M;
-  if (!linear_map(&tp, P, T::P_MN, prows) || !linear_map(&tq, Q, T::Q_MN, g.bn / 2))
-    return LMOE_ERR_CUDA;
-  CUtensorMap to{};
-  if (!T::SWAP &&
-      !(g.out_f32 ? make_tmap_f32_out32(&to, g.out, g.R, g.C, g.ldo)
-                  : make_tmap_bf16_out32(&to, g.out, g.R, g.C, g.ldo)))
-    return LMOE_ERR_CUDA;
-  const int tm = T::SWAP ? g.bn : 2 * prows, tn = T::SWAP ? 2 * prows : g.bn;
-  int64_t pairs = ceil_div(g.R, tm) * ceil_div(g.C, tn);
-  if (pairs > INT32_MAX / 2) return LMOE_ERR_UNSUPPORTED;
   if (pairs > sms / 2) pairs = sms / 2;
   if (active > 0 && pairs > active) pairs = active;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
   cfg.blockDim = dim3(LINEAR_THREADS);
-  cfg.dynamicSmemBytes = static_cast<size_t>(linear_smem_bytes(true, MODE, g.bn, g.stages));
+  cfg.dynamicSmemBytes = static_cast<size_t>(linear_smem_bytes(
+      true, MODE, MODE == MODE_GRADS && g.dw.bn > g.bn ? g.dw.bn : g.bn, g.stages));
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -893,26 +991,14 @@ int launch_linear_pair(const LinearOperand& P, const LinearOperand& Q, const Lin
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kernel, tp, tq, to, g) == cudaSuccess ? LMOE_OK : LMOE_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, kernel, maps, g) == cudaSuccess ? LMOE_OK : LMOE_ERR_CUDA;
 }
 
-// One product C[R, C] = A . B^T over D, A's rows (MODE_DW: columns) being the output's rows.
-template <int MODE, bool FP8, bool GLU>
-int launch_linear(const LinearOperand& A, const LinearOperand& B, const LinearArgs& g_in,
-                  cudaStream_t stream) {
-  LinearArgs g = g_in;
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return LMOE_ERR_CUDA;
-  const LinearPlan p = linear_plan(MODE, g.R, g.C, g.D, FP8, GLU, sms);
-  g.bn = p.bn;
-  g.stages = p.stages;
-  g.ks = p.ks;
-  constexpr bool SWAP = LinearTraits<MODE>::SWAP;
-  const LinearOperand &P = SWAP ? B : A, &Q = SWAP ? A : B;
-  return p.pair ? launch_linear_pair<MODE, FP8, GLU>(P, Q, g, dev, sms, stream)
-                : launch_linear_tile<MODE, FP8, GLU>(P, Q, g, dev, stream);
+inline int linear_device(int* dev, int* sms) {
+  return cudaGetDevice(dev) == cudaSuccess &&
+                 cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, *dev) == cudaSuccess
+             ? LMOE_OK
+             : LMOE_ERR_CUDA;
 }
 
 // The checks of a linear layer's arguments that its forward and backward share.

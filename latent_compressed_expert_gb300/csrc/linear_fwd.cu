@@ -12,23 +12,33 @@ namespace lmoe {
 //   EPILOGUE ns per accumulator column of a tile's epilogue; that of an SM pair's last tile, or of
 //            a tile alone, is not hidden
 //   HBM      bytes/ns; what is read and written crosses it once in any case
-LinearPlan linear_plan(int mode, int R, int C, int D, bool fp8, bool glu, int sms) {
-  constexpr double RATE = 12500.0, FEED = 150.0, ROUND = 1550.0, ROUND_PAIR = 2050.0;
-  constexpr double EPILOGUE = 15.0, EPILOGUE_PAIR = 11.0, HBM = 6600.0;
+constexpr double RATE = 12500.0, FEED = 150.0, ROUND = 1550.0, ROUND_PAIR = 2050.0;
+constexpr double EPILOGUE = 15.0, EPILOGUE_PAIR = 11.0, HBM = 6600.0;
+constexpr double EPILOGUE_DW = 8.5, EPILOGUE_DW_F32 = 11.5;  // of dw's tensor stores
+constexpr double TILE_DW = 250.0;                            // and for each of its tiles
+constexpr double FLOP = 2.0 * BLOCK_K;  // per output element and K-block, in bf16 time
+
+static int pair_stages(int bn) {
+  int st = LINEAR_MAX_STAGES;
+  while (linear_smem_bytes(true, MODE_FWD, bn, st) > LINEAR_SMEM_MAX) --st;
+  return st;
+}
+static double pair_tile_ns(int nk, int bn, int stages, double epilogue) {
+  const double mma = FLOP * BLOCK_M * bn / RATE, round = ROUND_PAIR / stages;
+  const double ns = nk * (mma > round ? mma : round);
+  return ns > epilogue * bn ? ns : epilogue * bn;
+}
+
+LinearPlan linear_plan(int mode, int R, int C, int D, int out_size, bool fp8, bool glu, int sms) {
   const bool dw = mode == MODE_DW;
   const int nk = static_cast<int>(ceil_div(D, fp8 ? 128 : 64));
   const int P = dw ? R : C, Q = dw ? C : R;  // extents along the MMA's rows and columns
-  const double flop = 2.0 * BLOCK_K;         // per output element and K-block, in bf16 time
   const double floor = (128.0 * nk * (static_cast<double>(C) * (glu ? 2 : 1) + R) +
-                        2.0 * R * C) / HBM;
+                        static_cast<double>(out_size) * R * C) / HBM;
   auto larger = [](double a, double b) { return a > b ? a : b; };
-  LinearPlan best{false, 64, 3, 1};
-  double least = 1e300;
+  LinearPlan best{false, 64, 3, 1, 1e300};
   auto offer = [&](bool pair, int bn, int stages, int ks, double ns) {
-    if (ns < least) {
-      least = ns;
-      best = {pair, bn, stages, ks};
-    }
+    if (ns < best.ns) best = {pair, bn, stages, ks, ns};
   };
   // pieces of Q: as few as fit, or a few more for an even deal
   const int unit_pair = dw ? 128 : 32, unit_tile = dw ? 64 : 16;
@@ -37,12 +47,10 @@ LinearPlan linear_plan(int mode, int R, int C, int D, bool fp8, bool glu, int sm
     {
       const int bn = static_cast<int>(ceil_div(per, unit_pair)) * unit_pair;
       const int64_t tiles = ceil_div(Q, bn) * ceil_div(P, glu ? BLOCK_M : 2 * BLOCK_M);
-      int st = LINEAR_MAX_STAGES;
-      while (linear_smem_bytes(true, mode, bn, st) > LINEAR_SMEM_MAX) --st;
-      const double tile = larger(nk * larger(flop * BLOCK_M * bn / RATE, ROUND_PAIR / st),
-                                 EPILOGUE_PAIR * bn);
-      offer(true, bn, st, 1, larger(static_cast<double>(ceil_div(tiles, sms / 2)) * tile, floor) +
-                                 EPILOGUE_PAIR * bn + 3000.0);
+      const int st = pair_stages(bn);
+      const double all = static_cast<double>(ceil_div(tiles, sms / 2)) * 
+                         pair_tile_ns(nk, bn, st, EPILOGUE_PAIR);
+      offer(true, bn, st, 1, larger(all, floor) + EPILOGUE_PAIR * bn + 3000.0);
     }
     {
       const int bn = static_cast<int>(ceil_div(per, unit_tile)) * unit_tile;
@@ -60,12 +68,44 @@ LinearPlan linear_plan(int mode, int R, int C, int D, bool fp8, bool glu, int sm
         if (ks > 1 && (nk < 2 * ks || ctas > per_sm * sms || (per_sm == 1 && ks > 4))) break;
         const int64_t kb = ceil_div(nk, ks), waves = ceil_div(ctas, per_sm * sms);
         const double shared = static_cast<double>(ceil_div(ctas, sms) * kb) *
-                              larger(flop * BLOCK_M * bn / RATE, bytes / FEED);
+                              larger(FLOP * BLOCK_M * bn / RATE, bytes / FEED);
         const double alone = static_cast<double>(waves * kb) * ROUND / st;
         offer(false, bn, st, ks,
               larger(larger(shared, alone), floor) + EPILOGUE * bn * (ctas > sms ? 2.0 : 1.0) +
                   3500.0 * static_cast<double>(waves) + (ks > 1 ? 700.0 + 300.0 * ks : 0.0));
       }
+    }
+  }
+  return best;
+}
+
+LinearGradsPlan linear_grads_plan(int R, int C, int D, int dw_size, int sms) {
+  const int nk = static_cast<int>(ceil_div(D, 64)), dw_nk = static_cast<int>(ceil_div(R, 64));
+  const int64_t pairs = sms / 2;
+  const double floor = (2.0 * (2.0 * R * C + static_cast<double>(R) * D + static_cast<double>(C) * D) +
+                        static_cast<double>(dw_size) * C * D) / HBM;
+  LinearGradsPlan best{64, 128, 4, 0, 1e300};
+  for (int n = static_cast<int>(ceil_div(R, 256)), i = 0; i < 4; ++i, ++n) {
+    const int bn = static_cast<int>(ceil_div(ceil_div(R, n), 32)) * 32;
+    for (int dw_bn = 128; dw_bn <= 256; dw_bn += 128) {
+      const int st = pair_stages(bn > dw_bn ? bn : dw_bn);
+      const int64_t tiles = linear_pair_tiles(C, R, bn, false);
+      const int64_t dw_tiles = linear_pair_tiles(D, C, dw_bn, false);
+      const double t = pair_tile_ns(nk, bn, st, EPILOGUE_PAIR);
+      const double dt = TILE_DW + pair_tile_ns(dw_nk, dw_bn, st, dw_size == 4 ? EPILOGUE_DW_F32
+                                                                              : EPILOGUE_DW);
+      // the pairs that get one tile of dx less start with as many of dw as that takes
+      const int64_t extra = tiles % pairs, fewer = pairs - extra;
+      int64_t lead = extra ? static_cast<int64_t>(t / dt + 0.5) : 0;
+      if (lead > ceil_div(dw_tiles, fewer)) lead = ceil_div(dw_tiles, fewer);
+      const int64_t rest = dw_tiles > lead * fewer ? ceil_div(dw_tiles - lead * fewer, pairs) : 0;
+      const double a = static_cast<double>(tiles / pairs) * t + static_cast<double>(lead + rest) * dt;
+      const double b = static_cast<double>(ceil_div(tiles, pairs)) * t +
+                       static_cast<double>(rest) * dt;
+      double ns = a > b ? a : b;
+      if (ns < floor) ns = floor;
+      ns += EPILOGUE_PAIR * dw_bn + 3000.0;
+      if (ns < best.ns) best = {bn, dw_bn, st, static_cast<int>(lead), ns};
     }
   }
   return best;
@@ -100,6 +140,24 @@ int linear_sizes_ok(const lmoe_linear* p) {
   return LMOE_OK;
 }
 
+template <bool FP8, bool GLU>
+static int forward(const LinearOperand& X, const LinearOperand& W, LinearArgs& g,
+                   cudaStream_t stream) {
+  int dev = 0, sms = 0;
+  if (linear_device(&dev, &sms) != LMOE_OK) return LMOE_ERR_CUDA;
+  const LinearPlan p = linear_plan(MODE_FWD, g.R, g.C, g.D, 2, FP8, GLU, sms);
+  g.bn = p.bn;
+  g.stages = p.stages;
+  g.ks = p.ks;
+  if (!p.pair) return launch_linear_tile<MODE_FWD, FP8, GLU>(W, X, g, dev, stream);
+  LinearPairMaps m{};
+  if (!linear_map(&m.p, W, false, GLU ? BLOCK_M / 2 : BLOCK_M) ||
+      !linear_map(&m.q, X, false, g.bn / 2))
+    return LMOE_ERR_CUDA;
+  return launch_linear_pair<MODE_FWD, FP8, GLU>(m, g, linear_pair_tiles(g.C, g.R, g.bn, GLU), dev,
+                                                sms, stream);
+}
+
 template <bool FP8>
 static int forward(const lmoe_linear& p, cudaStream_t stream) {
   LinearArgs g{};
@@ -122,8 +180,7 @@ static int forward(const lmoe_linear& p, cudaStream_t stream) {
   const int per = FP8 ? 2 : 1;  // elements per 2-byte unit of the tensor maps
   const LinearOperand A{p.x, p.M, p.K / per, p.ldx / per};
   const LinearOperand B{p.w, glu ? 2 * static_cast<int64_t>(p.N) : p.N, p.K / per, p.ldw / per};
-  return glu ? launch_linear<MODE_FWD, FP8, true>(A, B, g, stream)
-             : launch_linear<MODE_FWD, FP8, false>(A, B, g, stream);
+  return glu ? forward<FP8, true>(A, B, g, stream) : forward<FP8, false>(A, B, g, stream);
 }
 
 }  // namespace lmoe
