@@ -27,6 +27,7 @@
 // once as the next product's operand (e4m3 experts: the latent and h to e4m3 codes with a scale
 // per row from their fp32 values); rms(u) is applied after the product, which is the same for a
 // factor per token.  e4m3 products run as fp16 MMAs on the codes' exact values.
+#include <stddef.h>
 #include <string.h>
 
 #include "act.cuh"
@@ -39,7 +40,10 @@ namespace lmoe {
 
 constexpr int FEW_T = LMOE_FEW_MAX_TOKENS;
 constexpr int FEW_WARPS = 8;
-constexpr int FEW_THREADS = FEW_WARPS * 32;  // that compute; one more warp loads
+constexpr int FEW_THREADS = FEW_WARPS * 32;  // that compute; one more warp loads, and
+constexpr int FEW_FINISH = 2;                // these add the partial tiles up and store results
+constexpr int FEW_RED = 2;                   // units whose partial tiles are under way
+constexpr int FEW_BLOCK = FEW_THREADS + 32 + FEW_FINISH * 32;
 constexpr int FEW_BOX = 16 * 128;            // bytes of a weight box
 constexpr int FEW_BOXES = FEW_WARPS * FEW_BOX;  // of a stage
 constexpr int FEW_SCALES = 1024;             // e4m3: and its weight rows' scales
@@ -56,8 +60,7 @@ struct FewArgs {
   int T, d, L, E, K, I, sw;   // sw: shared width
   float c, eps;
   int splits;                 // DOWN's parts
-  int stages, more;           // stages of the ring; and while the experts run (GATE_UP, DOWN):
-  int more_off;               // those beyond `stages` lie at tok + more_off
+  int stages, more;           // stages of the ring; and while the experts run (GATE_UP, DOWN)
   int out_pitch;              // OUT: shared-memory distance of the tokens' rows
   int nb[5];                  // boxes of a stage, by phase (DOWN: of one expert)
   int group;                  // DOWN: experts of a stage
@@ -101,18 +104,18 @@ struct FewTables {
   uint64_t idle;                            // HBM has nothing to do for a while
   uint64_t routed;                          // the experts are known
   uint64_t staged;                          // a phase's token operands have landed
-  float red[2][FEW_WARPS][16 * 8];          // partial tiles, two units in turn
+  uint64_t red_full[FEW_RED], red_empty[FEW_RED];
+  uint64_t finished[FEW_OUT];               // a phase's results are stored
+  float red[FEW_RED][FEW_WARPS][16 * 8];    // partial tiles, units in turn
   int32_t expert[FEW_MAX_PAIRS];            // the used experts, in order of first use
   int16_t pair[FEW_MAX_PAIRS][FEW_T];       // pair t K + j of token t with that expert, or -1
-  float gate[FEW_MAX_PAIRS][FEW_T];         // its gate, or 0
+  alignas(8) float gate[FEW_MAX_PAIRS][FEW_T];  // its gate, or 0 (e4m3, DOWN: times h's scale)
   alignas(16) int32_t sel[FEW_MAX_PAIRS];   // expert and gate of every pair
   float sel_gate[FEW_MAX_PAIRS];
   int16_t rank[FEW_MAX_PAIRS];              // place in `expert` of a pair that is its first use
   int32_t first_uses[FEW_WARPS];
   uint2 cand[FEW_WARPS][FEW_CAND];          // candidates of a token's selection
   uint32_t won[FEW_WARPS][32];
-  float h_scale[FEW_MAX_PAIRS];             // e4m3: of a pair's h row
-  float lat_scale[FEW_T];                   // e4m3: of a token's latent
   float rstd[FEW_T];
   float warp_sum[FEW_WARPS];
   uint4 zero;                               // the operand of tokens that a box does not concern
@@ -144,14 +147,11 @@ struct FewPlan {
       default: return a.d / 16;
     }
   }
-  // The ring in phase ph: its length, and where a stage lies.  Both sides step through the slots in
+  // The ring's length in phase ph.  Its stages lie one below the other, the first at the top, so that
+  // the longer form reaches down into the tokens' operands.  Both sides step through the slots in
   // the same order; each slot's barriers keep their own parity.
   __device__ int ring_stages(int ph) const {
     return ph == FEW_GATE_UP || ph == FEW_DOWN ? a.more : a.stages;
-  }
-  __device__ uint8_t* stage_at(uint8_t* ring, int slot) const {
-    return slot < a.stages ? ring + slot * STAGE
-                           : ring + a.stages * STAGE + a.more_off + (slot - a.stages) * STAGE;
   }
   // boxes along a unit's reduction (DOWN: one expert's)
   __device__ int boxes(int ph) const {
@@ -163,6 +163,11 @@ struct FewPlan {
       default: return (a.L + a.sw) / 64;
     }
   }
+  // What the selection goes by: the order of fl32(s - tau).
+  __device__ uint32_t key(float z, int e) const {
+    const float sc = score_sigmoid(z);
+    return order_key(a.tau ? __fsub_rn(sc, __ldg(a.tau + e)) : sc);
+  }
   // DOWN: the experts [e0, e1) of a unit's part
   __device__ void experts(int unit, int* e0, int* e1) const {
     const int part = unit % a.splits;
@@ -173,7 +178,7 @@ struct FewPlan {
 
 // The loading thread.
 template <bool FP8>
-__device__ void few_load(const FewPlan<FP8>& p, const FewMaps& m, uint8_t* ring) {
+__device__ void few_load(const FewPlan<FP8>& p, const FewMaps& m, uint8_t* top) {
   const FewArgs& a = p.a;
   FewTables* s = p.s;
   int slot = 0, in_ring = 0;
@@ -186,7 +191,7 @@ __device__ void few_load(const FewPlan<FP8>& p, const FewMaps& m, uint8_t* ring)
     ok = ok && ptx::mbar_wait(&s->empty[slot], (parity >> slot) & 1u, &s->abort, a.timeout_ns);
     if (!ok) return nullptr;
     ptx::mbar_arrive_expect_tx(&s->full[slot], static_cast<uint32_t>(boxes * FEW_BOX + scales * 4));
-    return p.stage_at(ring, slot);
+    return top - (slot + 1) * FewPlan<FP8>::STAGE;
   };
   auto next = [&]() {
     parity ^= 1u << slot;
@@ -288,69 +293,88 @@ struct Few : FewPlan<FP8> {
   using P::KC;
   using P::s;
   using P::units;
-  uint8_t* ring;
+  using P::STAGE;
+  uint8_t* ring;       // of a.stages stages
   uint8_t* tok;        // tokens' operands
+  uint32_t top, bars;  // shared-memory addresses: of this warp's box above slot 0, of `full`
   int warp, lane;
   int slot = 0, in_ring = 0;
   uint32_t parity = 0, staged = 0, arrivals = 0;  // parity: bit i, of slot i's next stage
+  uint32_t unit_no = 0;                           // units handed on
   bool ok = true;
 
   __device__ Few(const FewArgs& a_, FewTables* s_) : P(a_, s_) {}
 
   __device__ static void sync() { ptx::named_sync(1, FEW_THREADS); }
 
-  // Waits for the next stage; the shared-memory address of this warp's box.
-  __device__ uint32_t take() {
-    if (ok && !__all_sync(0xffffffffu,
-                          ptx::mbar_wait(&s->full[slot], (parity >> slot) & 1u, &s->abort,
-                                         a.timeout_ns))) {
-      ok = false;
-      if (lane == 0) {
+  // Bounded.  The clock is not read while the answer comes soon, which it mostly does.
+  __device__ __forceinline__ void wait(uint32_t bar, uint32_t phase) {
+    uint64_t t0 = 0;
+    for (uint32_t it = 1; ok && !__all_sync(0xffffffffu, ptx::mbar_try_wait_at(bar, phase)); ++it) {
+      if ((it & 15u) != 0u) continue;
+      const uint64_t now = ptx::globaltimer_ns();
+      if (it == 16u) t0 = now;
+      const bool late = now - t0 > a.timeout_ns;
+      if (__any_sync(0xffffffffu, late || *static_cast<volatile int*>(&s->abort))) {
+        ok = false;
         s->abort = 1;
-        atomicOr(a.head, DEVERR_TIMEOUT_MMA);
+        if (lane == 0) atomicOr(a.head, DEVERR_TIMEOUT_MMA);
       }
     }
-    return ptx::smem_u32(P::stage_at(ring, slot) + warp * FEW_BOX);
   }
-  __device__ void release() {
+  // Waits for the next stage; the shared-memory address of this warp's box.
+  __device__ __forceinline__ uint32_t take() {
+    wait(bars + slot * 8, (parity >> slot) & 1u);
+    return top - slot * STAGE;
+  }
+  // e4m3: the scales that came with it, from the address of this warp's box
+  __device__ uint32_t scales(uint32_t box) const { return box - warp * FEW_BOX + FEW_BOXES; }
+  __device__ __forceinline__ void release() {
     __syncwarp();  // every lane has read the box
-    if (lane == 0 && ok) ptx::mbar_arrive(&s->empty[slot]);
+    if (lane == 0 && ok)
+      ptx::mbar_arrive_at(bars + static_cast<uint32_t>(offsetof(FewTables, empty) -
+                                                       offsetof(FewTables, full)) + slot * 8);
     parity ^= 1u << slot;
     if (++slot >= in_ring) slot = 0;
+  }
+  __device__ void pass() {  // a stage without a box for this warp
+    take();
+    release();
   }
   __device__ void enter(int ph) {
     in_ring = P::ring_stages(ph);
     if (slot >= in_ring) slot = 0;
   }
-  // acc += box (16 rows x 128 bytes) . tokens.  b: address of this lane's operand row of the
-  // box's columns (row lane & 7, 16-byte piece lane >> 3), bstep 64, or 0 for the zero piece.
+  // A box (16 rows x 128 bytes) and the tokens' operands for it, as MMA fragments.  The tokens' are
+  // loaded before the wait for the box, and the box's slot is given back as soon as it is in
+  // registers: eight warps hide little of each other's latency.
+  struct Box {
+    uint32_t r[4][4];
+  };
+  struct Toks {
+    uint32_t r[2][4];
+  };
+  __device__ __forceinline__ Box load_box(uint32_t box) const {
+    const uint32_t row = (lane & 7) + ((lane >> 3) & 1) * 8;
+    Box f;
+#pragma unroll
+    for (int p = 0; p < 4; ++p)
+      ptx::ldmatrix_x4(box + row * 128 + (((2 * p + (lane >> 4)) ^ (row & 7)) << 4), f.r[p]);
+    return f;
+  }
+  // Partial sums, in two chains.
+  struct Acc {
+    float v[2][4] = {};
+    __device__ __forceinline__ float sum(int k) const { return v[0][k] + v[1][k]; }
+  };
+  // acc += box . tokens
   template <bool CODES>
-  __device__ __forceinline__ void multiply(uint32_t box, uint32_t b, uint32_t bstep,
-                                           float (&acc)[2][4]) {
-    const uint32_t arow = (lane & 7) + ((lane >> 3) & 1) * 8;
+  __device__ __forceinline__ static void multiply(const Box& box, const Toks& tok, Acc& acc) {
 #pragma unroll
-    for (int kp = 0; kp < 2; ++kp) {
-      uint32_t bf[4];
-      ptx::ldmatrix_x4(b + kp * bstep, bf);
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        uint32_t af[4];
-        const uint32_t piece = 4 * kp + 2 * j + (lane >> 4);
-        ptx::ldmatrix_x4(box + arow * 128 + ((piece ^ (arow & 7)) << 4), af);
-        if constexpr (CODES) {
-          // a word holds four codes k .. k + 3: its halves serve as the two k groups of an MMA,
-          // the same on both operands
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t r0 = af[2 * h], r1 = af[2 * h + 1], bw = bf[2 * j + h];
-            ptx::mma_f16_16816(acc[h], ptx::cvt_f16x2_e4m3(r0), ptx::cvt_f16x2_e4m3(r1),
-                               ptx::cvt_f16x2_e4m3(r0 >> 16), ptx::cvt_f16x2_e4m3(r1 >> 16),
-                               ptx::cvt_f16x2_e4m3(bw), ptx::cvt_f16x2_e4m3(bw >> 16));
-          }
-        } else {
-          ptx::mma_bf16_16816(acc[j], af, bf[2 * j], bf[2 * j + 1]);
-        }
-      }
+    for (int p = 0; p < 4; ++p) {
+      const uint32_t* bf = &tok.r[p / 2][p % 2 * 2];
+      if constexpr (CODES) ptx::mma_e4m3_16832(acc.v[p % 2], box.r[p], bf[0], bf[1]);
+      else ptx::mma_bf16_16816(acc.v[p % 2], box.r[p], bf[0], bf[1]);
     }
   }
 
@@ -362,29 +386,38 @@ struct Few : FewPlan<FP8> {
     if (row < 0) return {ptx::smem_u32(&s->zero), 0};
     return {ptx::smem_u32(tok) + offset + static_cast<uint32_t>(row) * pitch + (lane >> 3) * 16, 1};
   }
+  // its part for box c of the reduction
+  __device__ __forceinline__ static Toks load_tok(const Row& r, int c) {
+    Toks t;
+    ptx::ldmatrix_x4(r.base + r.on * c * 128, t.r[0]);
+    ptx::ldmatrix_x4(r.base + r.on * (c * 128 + 64), t.r[1]);
+    return t;
+  }
 
-  // Writes the warp's 16 x 8 partial tile of unit number n; after the barrier all eight are there.
-  __device__ float* join(int n, const float (&t)[4]) {
-    float* r = s->red[n & 1][warp];
+  // Hands the warp's 16 x 8 partial tile of the next unit to the finishing warps.
+  __device__ void join(const float (&t)[4]) {
+    const int b = unit_no % FEW_RED;
+    wait(ptx::smem_u32(&s->red_empty[b]), (unit_no / FEW_RED & 1) ^ 1);
+    float* r = s->red[b][warp];
     const int g = lane >> 2, c = (lane & 3) * 2;
     *reinterpret_cast<float2*>(r + g * 8 + c) = make_float2(t[0], t[1]);
     *reinterpret_cast<float2*>(r + (g + 8) * 8 + c) = make_float2(t[2], t[3]);
-    sync();
-    return s->red[n & 1][0];
-  }
-  __device__ static float total(const float* red, int i) {
-    float v = red[i];
-#pragma unroll
-    for (int w = 1; w < FEW_WARPS; ++w) v += red[w * 128 + i];
-    return v;
+    __syncwarp();
+    if (lane == 0 && ok) ptx::mbar_arrive(&s->red_full[b]);
+    ++unit_no;
   }
 
   // Waits until every CTA has arrived as often as this one; false: gave up.
-  __device__ bool grid_barrier() {
+  // phase: that ends here, its results stored by the finishing warps; or -1.
+  __device__ bool grid_barrier(int phase) {
     ++arrivals;
     ptx::fence_proxy_async();  // this thread's results, for the others' bulk copies
     sync();
     if (threadIdx.x == 0) {
+      if (phase >= 0 && !ptx::mbar_wait(&s->finished[phase], 0, &s->abort, a.timeout_ns)) {
+        s->abort = 1;
+        atomicOr(a.head, DEVERR_TIMEOUT_EPILOGUE);
+      }
       ptx::red_release_add_u32(a.head + 1, 1u);
       const uint32_t target =
           static_cast<uint32_t>(ctas) * arrivals + (arrivals == 1 && a.inject_stall ? 1u : 0u);
@@ -493,7 +526,6 @@ struct Few : FewPlan<FP8> {
   }
   __device__ void stage_codes() {
     if constexpr (FP8) {
-      if (threadIdx.x < a.T) s->lat_scale[threadIdx.x] = __ldcg(a.lat_scale + threadIdx.x);
       copy_rows(tok, few_pitch(a.L), a.lat8, a.L, a.T, a.L);  // the router is done with hi and lo
       landed();
       sync();
@@ -511,7 +543,12 @@ struct Few : FewPlan<FP8> {
   __device__ void stage_h() {
     const int pairs = a.T * a.K, bytes = FP8 ? a.I : a.I * 2;
     copy_rows(tok, few_pitch(bytes), FP8 ? static_cast<const void*>(a.h8) : a.h, bytes, pairs, bytes);
-    if (FP8 && threadIdx.x < pairs) s->h_scale[threadIdx.x] = __ldcg(a.h_scale + threadIdx.x);
+    if constexpr (FP8) {  // h's scales into the gates
+      for (int i = threadIdx.x; i < s->used * FEW_T; i += FEW_THREADS) {
+        const int p = s->pair[i / FEW_T][i % FEW_T];
+        if (p >= 0) s->gate[i / FEW_T][i % FEW_T] *= __ldcg(a.h_scale + p);
+      }
+    }
     landed();
     if constexpr (FP8) sync();
   }
@@ -573,33 +610,21 @@ struct Few : FewPlan<FP8> {
     const int pitch = few_pitch(a.d * 2);
     const Row r = token_row((lane & 7) < a.T ? lane & 7 : -1, pitch);
     const int nc = P::boxes(FEW_IN), nb = a.nb[FEW_IN];
-    int n = 0;
-    for (int unit = cta; unit < units(FEW_IN); unit += ctas, ++n) {
-      float acc[2][4] = {};
+    for (int unit = cta; unit < units(FEW_IN); unit += ctas) {
+      Acc acc;
       for (int k = 0; k < nc; k += nb) {
-        const uint32_t box = take();
         const int c = k + warp;
-        if (warp < nb && c < nc) multiply<false>(box, r.base + r.on * c * 128, r.on * 64, acc);
-        release();
-      }
-      const float t4[4] = {acc[0][0] + acc[1][0], acc[0][1] + acc[1][1], acc[0][2] + acc[1][2],
-                           acc[0][3] + acc[1][3]};
-      const float* red = join(n, t4);
-      const int i = threadIdx.x, t = i & 7;
-      if (t >= a.T) continue;
-      if (unit < a.L / 16) {
-        if (i < 128) {
-          const float v = total(red, i);
-          const __nv_bfloat16 hi = __float2bfloat16_rn(v);
-          const size_t o = static_cast<size_t>(t) * a.L + unit * 16 + (i >> 3);
-          a.lat[o] = hi;
-          a.lat[static_cast<size_t>(a.T) * a.L + o] = __float2bfloat16_rn(v - __bfloat162float(hi));
+        if (warp >= nb || c >= nc) {
+          pass();
+          continue;
         }
-      } else if (i < 64) {
-        const int f = (unit - a.L / 16) * 8 + (i >> 3);
-        a.hs[static_cast<size_t>(t) * a.sw + f] =
-            __float2bfloat16_rn(situ_glu(total(red, i), total(red, i + 64), a.c, 1.0f / a.c));
+        const Toks tk = load_tok(r, c);
+        const Box bx = load_box(take());
+        release();
+        multiply<false>(bx, tk, acc);
       }
+      const float t4[4] = {acc.sum(0), acc.sum(1), acc.sum(2), acc.sum(3)};
+      join(t4);
     }
   }
   __device__ void phase_router() {
@@ -607,37 +632,28 @@ struct Few : FewPlan<FP8> {
     const int pitch = few_pitch(a.L * 2), row = (lane & 7) < a.T ? lane & 7 : -1;
     const Row hi = token_row(row, pitch), lo = token_row(row, pitch, lat_lo());
     const int nc = P::boxes(FEW_ROUTER), nb = a.nb[FEW_ROUTER];
-    int n = 0;
-    for (int unit = cta; unit < units(FEW_ROUTER); unit += ctas, ++n) {
-      float acc[2][4] = {}, rest[2][4] = {};
+    for (int unit = cta; unit < units(FEW_ROUTER); unit += ctas) {
+      Acc acc, rest;
       for (int k = 0; k < nc; k += nb) {
-        const uint32_t box = take();
         const int c = k + warp;
-        if (warp < nb && c < nc) {
-          multiply<false>(box, hi.base + hi.on * c * 128, hi.on * 64, acc);
-          multiply<false>(box, lo.base + lo.on * c * 128, lo.on * 64, rest);
+        if (warp >= nb || c >= nc) {
+          pass();
+          continue;
         }
+        const Toks th = load_tok(hi, c), tl = load_tok(lo, c);
+        const Box bx = load_box(take());
         release();
+        multiply<false>(bx, th, acc);
+        multiply<false>(bx, tl, rest);
       }
       float t4[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) t4[k] = (acc[0][k] + acc[1][k]) + (rest[0][k] + rest[1][k]);
-      const float* red = join(n, t4);
-      const int i = threadIdx.x, t = i & 7, e = unit * 16 + (i >> 3);
-      if (i < 128 && t < a.T) {
-        const float z = total(red, i) + (a.bias ? __ldg(a.bias + e) : 0.0f);
-        a.logits[static_cast<size_t>(t) * a.E + e] = z;
-        a.keys[static_cast<size_t>(t) * a.E + e] = key(z, e);
-      }
+      for (int k = 0; k < 4; ++k) t4[k] = acc.sum(k) + rest.sum(k);
+      join(t4);
     }
     if (a.logits_in)
       for (int i = cta * FEW_THREADS + threadIdx.x; i < a.T * a.E; i += ctas * FEW_THREADS)
-        a.keys[i] = key(__ldg(a.logits_in + i), i % a.E);
-  }
-  // What the selection goes by: the order of fl32(s - tau).
-  __device__ uint32_t key(float z, int e) const {
-    const float sc = score_sigmoid(z);
-    return order_key(a.tau ? __fsub_rn(sc, __ldg(a.tau + e)) : sc);
+        a.keys[i] = P::key(__ldg(a.logits_in + i), i % a.E);
   }
   // The K largest keys of a token, by a warp: lane j returns the j-th (larger key first, then the
   // lower expert), as select_rounds does.  The K-th largest of the lanes' maxima is a lower bound
@@ -774,40 +790,34 @@ struct Few : FewPlan<FP8> {
     const int row = (lane & 7) < a.T ? lane & 7 : -1;
     const int pitch = FP8 ? few_pitch(a.L) : few_pitch(a.L * 2);
     const Row hi = token_row(row, pitch), lo = token_row(row, pitch, FP8 ? 0 : lat_lo());
-    const int per = a.I / 8, tiles = (2 * a.I + BLOCK_M - 1) / BLOCK_M;
-    const int nc = P::boxes(FEW_GATE_UP), nb = a.nb[FEW_GATE_UP];
-    int n = 0;
-    for (int unit = cta; unit < units(FEW_GATE_UP); unit += ctas, ++n) {
-      // thread i < 64 finishes feature i / 8 of the unit for token i % 8
-      const int i = threadIdx.x, t = i & 7, rank = unit / per;
-      const int p = i < 64 ? s->pair[rank][t] : -1;
-      const int f = unit % per * 8 + (i >> 3);
-      float gs = 1.0f, vs = 1.0f;
-      float acc[2][4] = {}, rest[2][4] = {};
+    const int nc = P::boxes(FEW_GATE_UP), nb = a.nb[FEW_GATE_UP], g = lane >> 2;
+    for (int unit = cta; unit < units(FEW_GATE_UP); unit += ctas) {
+      float gs = 1.0f, vs = 1.0f;  // e4m3: scales of this lane's gate and value row
+      Acc acc, rest;
       for (int k = 0; k < nc; k += nb) {
-        const uint32_t box = take();
         const int c = k + warp;
-        if (FP8 && k == 0 && i < 64) {
-          const float* sc = reinterpret_cast<const float*>(P::stage_at(ring, slot) + FEW_BOXES);
-          gs = sc[i >> 3], vs = sc[8 + (i >> 3)];
+        if (warp >= nb || c >= nc) {
+          pass();
+          continue;
         }
-        if (warp < nb && c < nc) {
-          multiply<FP8>(box, hi.base + hi.on * c * 128, hi.on * 64, acc);
-          if constexpr (!FP8) multiply<false>(box, lo.base + lo.on * c * 128, lo.on * 64, rest);
+        const Toks th = load_tok(hi, c);
+        Toks tl;
+        if constexpr (!FP8) tl = load_tok(lo, c);
+        const uint32_t box = take();
+        if (FP8 && k == 0) {
+          gs = ptx::ld_shared_f32(scales(box) + g * 4);
+          vs = ptx::ld_shared_f32(scales(box) + (8 + g) * 4);
         }
+        const Box bx = load_box(box);
         release();
+        multiply<FP8>(bx, th, acc);
+        if constexpr (!FP8) multiply<false>(bx, tl, rest);
       }
       float t4[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) t4[k] = (acc[0][k] + acc[1][k]) + (rest[0][k] + rest[1][k]);
-      const float* red = join(n, t4);
-      if (p < 0) continue;
-      float g = total(red, i), v = total(red, i + 64);
-      if constexpr (FP8) g *= gs * s->lat_scale[t], v *= vs * s->lat_scale[t];
-      const float h = situ_glu(g, v, a.c, 1.0f / a.c);
-      const size_t o = static_cast<size_t>(p) * a.I + f;
-      if constexpr (FP8) static_cast<float*>(a.h)[o] = h;
-      else static_cast<__nv_bfloat16*>(a.h)[o] = __float2bfloat16_rn(h);
+      for (int k = 0; k < 4; ++k)
+        t4[k] = FP8 ? acc.sum(k) * (k < 2 ? gs : vs) : acc.sum(k) + rest.sum(k);
+      join(t4);
     }
   }
   __device__ void phase_down() {
@@ -816,46 +826,43 @@ struct Few : FewPlan<FP8> {
     const int nk = P::boxes(FEW_DOWN), nb = a.nb[FEW_DOWN];
     const int g = lane >> 2, t2 = (lane & 3) * 2;
     const int sub = warp / nb, kw = warp % nb;  // which of a stage's experts, and its box
-    int n = 0;
-    for (int unit = cta; unit < units(FEW_DOWN); unit += ctas, ++n) {
+    for (int unit = cta; unit < units(FEW_DOWN); unit += ctas) {
       int e0, e1;
       experts(unit, &e0, &e1);
       float sum[4] = {};
       for (int e = e0; e < e1; e += a.group) {
         const int rank = e + sub;
-        const bool mine = sub < a.group && rank < e1;
-        const Row r = token_row(mine ? s->pair[rank][lane & 7] : -1, pitch);
+        if (sub >= a.group || rank >= e1) {
+          for (int k = 0; k < nk; k += nb) pass();
+          continue;
+        }
+        const Row r = token_row(s->pair[rank][lane & 7], pitch);
+        const float2 f = *reinterpret_cast<const float2*>(&s->gate[rank][t2]);
         float w0 = 1.0f, w1 = 1.0f;
-        float acc[2][4] = {};
+        Acc acc;
         for (int k = 0; k < nk; k += nb) {
-          const uint32_t box = take();
           const int c = k + kw;
-          if (FP8 && k == 0 && mine) {
-            const float* sc =
-                reinterpret_cast<const float*>(P::stage_at(ring, slot) + FEW_BOXES) + sub * 16 + g;
-            w0 = sc[0], w1 = sc[8];
+          if (c >= nk) {
+            pass();
+            continue;
           }
-          if (mine && c < nk) multiply<FP8>(box, r.base + r.on * c * 128, r.on * 64, acc);
+          const Toks tk = load_tok(r, c);
+          const uint32_t box = take();
+          if (FP8 && k == 0) {
+            w0 = ptx::ld_shared_f32(scales(box) + (sub * 16 + g) * 4);
+            w1 = ptx::ld_shared_f32(scales(box) + (sub * 16 + 8 + g) * 4);
+          }
+          const Box bx = load_box(box);
           release();
+          multiply<FP8>(bx, tk, acc);
         }
-        if (mine) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {  // times the tokens' gates
-            const int t = t2 + (k & 1);
-            float f = s->gate[rank][t];
-            if constexpr (FP8) {
-              const int p = s->pair[rank][t];
-              f *= p < 0 ? 0.0f : s->h_scale[p] * (k < 2 ? w0 : w1);
-            }
-            sum[k] = fmaf(acc[0][k] + acc[1][k], f, sum[k]);
-          }
-        }
+        // times the tokens' gates (e4m3: and both scales)
+        sum[0] = fmaf(acc.sum(0), f.x * w0, sum[0]);
+        sum[1] = fmaf(acc.sum(1), f.y * w0, sum[1]);
+        sum[2] = fmaf(acc.sum(2), f.x * w1, sum[2]);
+        sum[3] = fmaf(acc.sum(3), f.y * w1, sum[3]);
       }
-      const float* red = join(n, sum);
-      // u starts at zero and receives at most two parts, so that their order does not matter
-      const int i = threadIdx.x, t = i & 7;
-      if (i < 128 && t < a.T)
-        atomicAdd(a.u + static_cast<size_t>(t) * a.L + unit / a.splits * 16 + (i >> 3), total(red, i));
+      join(sum);
     }
   }
   __device__ void phase_out() {
@@ -864,30 +871,24 @@ struct Few : FewPlan<FP8> {
     const int nz = a.L / 64, t2 = (lane & 3) * 2;
     const float r0 = t2 < a.T ? s->rstd[t2] : 0.0f, r1 = t2 + 1 < a.T ? s->rstd[t2 + 1] : 0.0f;
     const int nc = P::boxes(FEW_OUT), nb = a.nb[FEW_OUT];
-    int n = 0;
-    for (int unit = cta; unit < units(FEW_OUT); unit += ctas, ++n) {
-      float az[2][4] = {}, as[2][4] = {};
+    for (int unit = cta; unit < units(FEW_OUT); unit += ctas) {
+      Acc az, as;
       for (int k = 0; k < nc; k += nb) {
-        const uint32_t box = take();
         const int c = k + warp;
-        const uint32_t b = r.base + r.on * c * 128;
-        if (warp < nb && c < nz) multiply<false>(box, b, r.on * 64, az);
-        else if (warp < nb && c < nc) multiply<false>(box, b, r.on * 64, as);
+        if (warp >= nb || c >= nc) {
+          pass();
+          continue;
+        }
+        const Toks tk = load_tok(r, c);
+        const Box bx = load_box(take());
         release();
+        if (c < nz) multiply<false>(bx, tk, az);
+        else multiply<false>(bx, tk, as);
       }
       float sum[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        sum[k] = fmaf(az[0][k] + az[1][k], k & 1 ? r1 : r0, as[0][k] + as[1][k]);
-      const float* red = join(n, sum);
-      const int i = threadIdx.x, t = i & 7;
-      if (i < 128 && t < a.T) {
-        const size_t o = static_cast<size_t>(t) * a.d + unit * 16 + (i >> 3);
-        float v = total(red, i);
-        if (a.resid) v += __bfloat162float(a.resid[o]);
-        if (a.y32_out) a.y32_out[o] = v;
-        a.y[o] = __float2bfloat16_rn(v);
-      }
+      for (int k = 0; k < 4; ++k) sum[k] = fmaf(az.sum(k), k & 1 ? r1 : r0, as.sum(k));
+      join(sum);
     }
   }
 
@@ -902,11 +903,11 @@ struct Few : FewPlan<FP8> {
       reinterpret_cast<float4*>(a.u)[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     stage_x();
     phase_in();
-    if (!grid_barrier()) return false;
+    if (!grid_barrier(FEW_IN)) return false;
     if (threadIdx.x == 0) ptx::mbar_arrive(&s->idle);
     stage_lat();
     phase_router();
-    if (!grid_barrier()) return false;
+    if (!grid_barrier(FEW_ROUTER)) return false;
     select();
     ptx::fence_proxy_async_smem();  // before the next loads into the ring
     sync();
@@ -916,33 +917,165 @@ struct Few : FewPlan<FP8> {
         a.logits_out[i] = __ldcg((a.logits_in ? a.logits_in : a.logits) + i);
     stage_codes();
     phase_gate_up();
-    if (!grid_barrier()) return false;
+    if (!grid_barrier(FEW_GATE_UP)) return false;
     if constexpr (FP8) {
       quantize_h();
-      if (!grid_barrier()) return false;
+      if (!grid_barrier(-1)) return false;
     }
     stage_h();
     phase_down();
-    if (!grid_barrier()) return false;
+    if (!grid_barrier(FEW_DOWN)) return false;
     stage_z();
     phase_out();
     return true;
   }
 };
 
+// The finishing warps: thread i of 64 takes elements i and i + 64 of a unit's 16 x 8 tile (rows
+// i / 8 and i / 8 + 8, gated units: a feature's gate and value, for token i % 8), adds up the
+// eight partial tiles and stores the results.  Computing warps that did this between their boxes
+// held each other up at every unit (e4m3, four tokens: @FIN@).
 template <bool FP8>
-__global__ void __launch_bounds__(FEW_THREADS + 32, 1)
+struct FewFinish : FewPlan<FP8> {
+  using P = FewPlan<FP8>;
+  using P::a;
+  using P::cta;
+  using P::ctas;
+  using P::s;
+  using P::units;
+  int i, t, row, lane;
+  uint32_t unit_no = 0;
+  bool ok = true;
+
+  __device__ FewFinish(const FewArgs& a_, FewTables* s_, int thread)
+      : P(a_, s_), i(thread), t(thread & 7), row(thread >> 3), lane(thread & 31) {}
+
+  __device__ bool wait(uint64_t* bar, uint32_t phase) {
+    if (ok && !__all_sync(0xffffffffu, ptx::mbar_wait(bar, phase, &s->abort, a.timeout_ns))) {
+      ok = false;
+      if (lane == 0) {
+        s->abort = 1;
+        atomicOr(a.head, DEVERR_TIMEOUT_EPILOGUE);
+      }
+    }
+    return ok;
+  }
+  // Both elements of the next unit.
+  __device__ bool total(float (&v)[2]) {
+    const int b = unit_no % FEW_RED;
+    if (!wait(&s->red_full[b], unit_no / FEW_RED & 1)) return false;
+    float p[2][FEW_WARPS];
+#pragma unroll
+    for (int k = 0; k < FEW_WARPS; ++k)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) p[h][k] = s->red[b][k][64 * h + i];
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(&s->red_empty[b]);
+    ++unit_no;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      v[h] = ((p[h][0] + p[h][1]) + (p[h][2] + p[h][3])) + ((p[h][4] + p[h][5]) + (p[h][6] + p[h][7]));
+    return true;
+  }
+  // All results of a phase are on their way; the next grid barrier publishes them.
+  __device__ void finished(int phase) {
+    ptx::fence_proxy_async();  // for the others' bulk copies
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(&s->finished[phase]);
+  }
+
+  __device__ void run() {
+    const float inv_c = 1.0f / a.c;
+    const bool token = t < a.T;
+    float v[2];
+    for (int unit = cta; unit < units(FEW_IN); unit += ctas) {
+      if (!total(v)) return;
+      if (!token) continue;
+      if (unit >= a.L / 16) {
+        const int f = (unit - a.L / 16) * 8 + row;
+        a.hs[static_cast<size_t>(t) * a.sw + f] =
+            __float2bfloat16_rn(situ_glu(v[0], v[1], a.c, inv_c));
+        continue;
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const __nv_bfloat16 hi = __float2bfloat16_rn(v[h]);
+        const size_t o = static_cast<size_t>(t) * a.L + unit * 16 + row + 8 * h;
+        a.lat[o] = hi;
+        a.lat[static_cast<size_t>(a.T) * a.L + o] = __float2bfloat16_rn(v[h] - __bfloat162float(hi));
+      }
+    }
+    finished(FEW_IN);
+    for (int unit = cta; unit < units(FEW_ROUTER); unit += ctas) {
+      if (!total(v)) return;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int e = unit * 16 + row + 8 * h;
+        const float z = v[h] + (a.bias ? __ldg(a.bias + e) : 0.0f);
+        if (!token) continue;
+        a.logits[static_cast<size_t>(t) * a.E + e] = z;
+        a.keys[static_cast<size_t>(t) * a.E + e] = P::key(z, e);
+      }
+    }
+    finished(FEW_ROUTER);
+    if (!wait(&s->routed, 0)) return;
+    const int per = a.I / 8;
+    const float ls = FP8 && token ? __ldcg(a.lat_scale + t) : 1.0f;
+    for (int unit = cta; unit < units(FEW_GATE_UP); unit += ctas) {
+      const int p = s->pair[unit / per][t];
+      if (!total(v)) return;
+      if (p < 0) continue;
+      const size_t o = static_cast<size_t>(p) * a.I + unit % per * 8 + row;
+      if constexpr (FP8)
+        static_cast<float*>(a.h)[o] = situ_glu(v[0] * ls, v[1] * ls, a.c, inv_c);
+      else
+        static_cast<__nv_bfloat16*>(a.h)[o] = __float2bfloat16_rn(situ_glu(v[0], v[1], a.c, inv_c));
+    }
+    finished(FEW_GATE_UP);
+    // u starts at zero and receives at most two parts, so that their order does not matter
+    for (int unit = cta; unit < units(FEW_DOWN); unit += ctas) {
+      if (!total(v)) return;
+      float* u = a.u + static_cast<size_t>(t) * a.L + unit / a.splits * 16 + row;
+      if (token) atomicAdd(u, v[0]);
+      if (token) atomicAdd(u + 8, v[1]);
+    }
+    finished(FEW_DOWN);
+    for (int unit = cta; unit < units(FEW_OUT); unit += ctas) {
+      const size_t o = static_cast<size_t>(t) * a.d + unit * 16 + row;
+      float r[2] = {0.0f, 0.0f};
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (token && a.resid) r[h] = __bfloat162float(a.resid[o + 8 * h]);
+      if (!total(v)) return;
+      if (!token) continue;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (a.y32_out) a.y32_out[o + 8 * h] = v[h] + r[h];
+        a.y[o + 8 * h] = __float2bfloat16_rn(v[h] + r[h]);
+      }
+    }
+  }
+};
+
+template <bool FP8>
+__global__ void __launch_bounds__(FEW_BLOCK, 1)
 few_kernel(const __grid_constant__ FewMaps maps, const __grid_constant__ FewArgs a) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = ptx::smem_u32(smem_raw);
-  uint8_t* ring = smem_raw + (((raw + 1023u) & ~1023u) - raw);
-  uint8_t* tok = ring + a.stages * few_stage_bytes(FP8);
-  FewTables* s = reinterpret_cast<FewTables*>(tok + a.tok_bytes);
+  uint8_t* tok = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+  uint8_t* ring = tok + a.tok_bytes;
+  uint8_t* top = ring + a.stages * few_stage_bytes(FP8);
+  FewTables* s = reinterpret_cast<FewTables*>(top);
   if (threadIdx.x == 0) {
     for (int i = 0; i < a.more; ++i) {
       ptx::mbar_init(&s->full[i], 1);
       ptx::mbar_init(&s->empty[i], FEW_WARPS);
     }
+    for (int i = 0; i < FEW_RED; ++i) {
+      ptx::mbar_init(&s->red_full[i], FEW_WARPS);
+      ptx::mbar_init(&s->red_empty[i], FEW_FINISH);
+    }
+    for (int i = 0; i < FEW_OUT; ++i) ptx::mbar_init(&s->finished[i], FEW_FINISH);
     ptx::mbar_init(&s->idle, 1);
     ptx::mbar_init(&s->routed, 1);
     ptx::mbar_init(&s->staged, 1);
@@ -952,14 +1085,18 @@ few_kernel(const __grid_constant__ FewMaps maps, const __grid_constant__ FewArgs
     ptx::fence_mbar_init();
   }
   __syncthreads();
-  if (threadIdx.x >= FEW_THREADS) {
-    if (threadIdx.x == FEW_THREADS) few_load(FewPlan<FP8>(a, s), maps, ring);
+  if (threadIdx.x >= FEW_THREADS + 32) {
+    FewFinish<FP8>(a, s, threadIdx.x - (FEW_THREADS + 32)).run();
+  } else if (threadIdx.x >= FEW_THREADS) {
+    if (threadIdx.x == FEW_THREADS) few_load(FewPlan<FP8>(a, s), maps, top);
   } else {
     Few<FP8> f(a, s);
     f.warp = threadIdx.x >> 5;
     f.lane = threadIdx.x & 31;
     f.ring = ring;
     f.tok = tok;
+    f.top = ptx::smem_u32(top) - Few<FP8>::STAGE + f.warp * FEW_BOX;
+    f.bars = ptx::smem_u32(s->full);
     f.run();
   }
   __syncthreads();
@@ -1008,7 +1145,7 @@ static FewLayout few_layout(const lmoe_dims& D) {
 // while the experts run, whose operands may be smaller (e4m3 codes), the ring has that too.
 struct FewSmem {
   size_t tok;
-  int stages, more, more_off, out_pitch;
+  int stages, more, out_pitch;
 };
 constexpr size_t FEW_SMEM_MAX = 232448 - 1024;  // less the alignment's slack
 
@@ -1023,14 +1160,12 @@ static FewSmem few_smem(const lmoe_dims& D) {
   const size_t experts = larger(fp8 ? T * few_pitch(D.L) : hi_lo,
                                 T * D.K * few_pitch(fp8 ? D.I : D.I * 2));
   M.tok = larger(larger(T * few_pitch(D.d * 2), hi_lo), larger(experts, T * M.out_pitch));
-  M.tok = (M.tok + 15) / 16 * 16;
+  M.tok = (M.tok + 1023) / 1024 * 1024;  // the ring behind it
   const size_t fixed = M.tok + sizeof(FewTables), stage = few_stage_bytes(fp8);
   if (fixed >= FEW_SMEM_MAX) return M;
   M.stages = static_cast<int>((FEW_SMEM_MAX - fixed) / stage);
   if (M.stages > FEW_MAX_STAGES) M.stages = FEW_MAX_STAGES;
-  M.more_off = static_cast<int>((experts + 1023) / 1024 * 1024);
-  M.more = M.stages;
-  if (static_cast<size_t>(M.more_off) < M.tok) M.more += static_cast<int>((M.tok - M.more_off) / stage);
+  M.more = M.stages + static_cast<int>((M.tok - experts) / stage);
   if (M.more > FEW_MAX_STAGES) M.more = FEW_MAX_STAGES;
   return M;
 }
@@ -1066,7 +1201,7 @@ static int launch_few(const FewMaps& maps, const FewArgs& a, int sms, size_t sme
     return LMOE_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(sms));
-  cfg.blockDim = dim3(FEW_THREADS + 32);
+  cfg.blockDim = dim3(FEW_BLOCK);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -1147,7 +1282,6 @@ int lmoe_forward_few(const lmoe_dims* dims, const void* packed, const void* x,
   const FewSmem M = few_smem(D);
   a.stages = M.stages;
   a.more = M.more;
-  a.more_off = M.more_off;
   a.out_pitch = M.out_pitch;
   a.tok_bytes = static_cast<int>(M.tok);
   a.x = static_cast<const __nv_bfloat16*>(x);

@@ -601,7 +601,7 @@ struct LinearPairMaps {
 // MODE_GRADS computes both gradients in one launch: neither product of a few hundred rows has
 // tiles enough to keep all SM pairs busy, and while dx reads the weights, dw writes its output
 // (333 rows, 3584 x 7168, fp32 dw: 38.4 us against 47.2 one after the other; 2048 rows, 7168 x 4096,
-// bf16 dw: 139 against 152, 0.96 of the bf16 peak; at 4096 rows and more it makes no difference).
+// bf16 dw: 139 against 152, 0.91 of the bf16 peak; at 4096 rows and more it makes no difference).
 template <int MODE, bool FP8, bool GLU>
 __global__ void __launch_bounds__(LINEAR_THREADS, 1)
 linear_pair_kernel(const __grid_constant__ LinearPairMaps maps, const LinearArgs g) {
