@@ -39,15 +39,13 @@
 namespace lmoe {
 
 constexpr int FEW_T = LMOE_FEW_MAX_TOKENS;
-constexpr int FEW_WARPS = 8;
-constexpr int FEW_THREADS = FEW_WARPS * 32;  // that compute; one more warp loads, and
-constexpr int FEW_FINISH = 2;                // these add the partial tiles up and store results
+constexpr int FEW_WARPS = 8;                 // that compute, one for each box of a stage
+constexpr int FEW_FINISH = 2;                // that add the partial tiles up and store results
 constexpr int FEW_RED = 2;                   // units whose partial tiles are under way
-constexpr int FEW_BLOCK = FEW_THREADS + 32 + FEW_FINISH * 32;
+constexpr int FEW_THREADS = FEW_WARPS * 32;
+constexpr int FEW_BLOCK = FEW_THREADS + 32 + FEW_FINISH * 32;  // one more warp loads
 constexpr int FEW_BOX = 16 * 128;            // bytes of a weight box
-constexpr int FEW_BOXES = FEW_WARPS * FEW_BOX;  // of a stage
-constexpr int FEW_SCALES = 1024;             // e4m3: and its weight rows' scales
-constexpr int few_stage_bytes(bool fp8) { return FEW_BOXES + (fp8 ? FEW_SCALES : 0); }
+constexpr int FEW_STAGE = FEW_WARPS * FEW_BOX;
 constexpr int FEW_MAX_STAGES = 14;
 constexpr int FEW_MIN_STAGES = 3;
 constexpr int FEW_MAX_SPLITS = 2;  // parts of u that are added in any order: a + b = b + a
@@ -64,7 +62,7 @@ struct FewArgs {
   int out_pitch;              // OUT: shared-memory distance of the tokens' rows
   int nb[5];                  // boxes of a stage, by phase (DOWN: of one expert)
   int group;                  // DOWN: experts of a stage
-  int tok_bytes;              // shared memory of the tokens' operands
+  int top;                    // end of the ring, from the start of the tokens' operands
   const __nv_bfloat16* x;
   const __nv_bfloat16* resid;
   __nv_bfloat16* y;
@@ -106,7 +104,7 @@ struct FewTables {
   uint64_t staged;                          // a phase's token operands have landed
   uint64_t red_full[FEW_RED], red_empty[FEW_RED];
   uint64_t finished[FEW_OUT];               // a phase's results are stored
-  float red[FEW_RED][FEW_WARPS][16 * 8];    // partial tiles, units in turn
+  float red[FEW_RED][FEW_WARPS][16 * 8];        // partial tiles, units in turn
   int32_t expert[FEW_MAX_PAIRS];            // the used experts, in order of first use
   int16_t pair[FEW_MAX_PAIRS][FEW_T];       // pair t K + j of token t with that expert, or -1
   alignas(8) float gate[FEW_MAX_PAIRS][FEW_T];  // its gate, or 0 (e4m3, DOWN: times h's scale)
@@ -114,8 +112,6 @@ struct FewTables {
   float sel_gate[FEW_MAX_PAIRS];
   int16_t rank[FEW_MAX_PAIRS];              // place in `expert` of a pair that is its first use
   int32_t first_uses[FEW_WARPS];
-  uint2 cand[FEW_WARPS][FEW_CAND];          // candidates of a token's selection
-  uint32_t won[FEW_WARPS][32];
   float rstd[FEW_T];
   float warp_sum[FEW_WARPS];
   uint4 zero;                               // the operand of tokens that a box does not concern
@@ -123,12 +119,13 @@ struct FewTables {
   int abort;
 };
 
+// A token's scratch while its experts are selected: logits, keys, candidates, winners.
+__host__ __device__ constexpr int few_select_bytes(int E) { return 8 * E + 8 * FEW_CAND + 4 * 32; }
 constexpr int few_pitch(int bytes) { return bytes + 16; }  // rows 16 bytes apart mod 128
 
 // What both sides know of the sequence of units and stages.
 template <bool FP8>
 struct FewPlan {
-  static constexpr int STAGE = few_stage_bytes(FP8);
   static constexpr int KC = FP8 ? 128 : 64;  // reduction elements of an expert box
   const FewArgs& a;
   FewTables* s;
@@ -163,35 +160,62 @@ struct FewPlan {
       default: return (a.L + a.sw) / 64;
     }
   }
+  // GATE_UP's units of a CTA in order, their expert's rank and first feature kept without divisions.
+  struct Gate {
+    int rank, f, step_rank, step_f, I;
+    __device__ Gate(const FewPlan& p) : I(p.a.I) {
+      const int per = I / 8;
+      rank = p.cta / per;
+      f = p.cta % per * 8;
+      step_rank = p.ctas / per;
+      step_f = p.ctas % per * 8;
+    }
+    __device__ void next() {
+      rank += step_rank;
+      f += step_f;
+      if (f >= I) f -= I, ++rank;
+    }
+  };
+  // Packed row of feature f's gate row; its value row lies GLU_GROUP behind.
+  __device__ static int gate_row(int f) {
+    return f / GLU_GROUP * (2 * GLU_GROUP) + f % GLU_GROUP;
+  }
   // What the selection goes by: the order of fl32(s - tau).
   __device__ uint32_t key(float z, int e) const {
     const float sc = score_sigmoid(z);
     return order_key(a.tau ? __fsub_rn(sc, __ldg(a.tau + e)) : sc);
   }
-  // DOWN: the experts [e0, e1) of a unit's part
+  // DOWN: a unit's first weight row, and the experts [e0, e1) of its part (of one or two)
+  __device__ int down_row(int unit) const { return (a.splits == 2 ? unit >> 1 : unit) * 16; }
   __device__ void experts(int unit, int* e0, int* e1) const {
-    const int part = unit % a.splits;
-    *e0 = s->used * part / a.splits;
-    *e1 = s->used * (part + 1) / a.splits;
+    const int used = s->used, half = used >> 1;
+    *e0 = a.splits == 2 && (unit & 1) ? half : 0;
+    *e1 = a.splits == 2 && !(unit & 1) ? half : used;
   }
 };
 
-// The loading thread.
+// The loading warp.  Its lane 0 issues the copies; DOWN's, one of each expert of a stage, go out from
+// as many lanes at once.
 template <bool FP8>
 __device__ void few_load(const FewPlan<FP8>& p, const FewMaps& m, uint8_t* top) {
   const FewArgs& a = p.a;
   FewTables* s = p.s;
+  const int lane = threadIdx.x & 31;
   int slot = 0, in_ring = 0;
   uint32_t parity = ~0u;  // bit i: of the wait for slot i to be free; the first round passes at once
   bool ok = true;
+  auto wait = [&](uint64_t* bar, uint32_t phase) {
+    return __all_sync(0xffffffffu, ptx::mbar_wait(bar, phase, &s->abort, a.timeout_ns));
+  };
   // every weight is read once: first out of L2 again, but for what was fetched ahead
   const uint64_t once = ptx::l2_policy_evict_first();
   // the next stage's buffer, or null when a wait ran out
-  auto stage = [&](int boxes, int scales) -> uint8_t* {
-    ok = ok && ptx::mbar_wait(&s->empty[slot], (parity >> slot) & 1u, &s->abort, a.timeout_ns);
+  auto stage = [&](int boxes) -> uint8_t* {
+    ok = ok && wait(&s->empty[slot], (parity >> slot) & 1u);
     if (!ok) return nullptr;
-    ptx::mbar_arrive_expect_tx(&s->full[slot], static_cast<uint32_t>(boxes * FEW_BOX + scales * 4));
-    return top - (slot + 1) * FewPlan<FP8>::STAGE;
+    if (lane == 0)
+      ptx::mbar_arrive_expect_tx(&s->full[slot], static_cast<uint32_t>(boxes * FEW_BOX));
+    return top - (slot + 1) * FEW_STAGE;
   };
   auto next = [&]() {
     parity ^= 1u << slot;
@@ -202,73 +226,69 @@ __device__ void few_load(const FewPlan<FP8>& p, const FewMaps& m, uint8_t* top) 
       // Its weights depend on the routing.  Until that is known (from the first barrier on), HBM
       // brings the CTA's first unit of OUT into L2, where the expert weights, which are the first
       // to be evicted, leave it: K3, one token 92.1 -> 90.3 us, eight 285 -> 280; two units 93.4.
-      ok = ptx::mbar_wait(&s->idle, 0, &s->abort, a.timeout_ns);
+      ok = wait(&s->idle, 0);
       if (!ok) break;
       const uint64_t keep = ptx::l2_policy_evict_last();
       const int no = p.boxes(FEW_OUT);
-      for (int k = 0; p.cta < p.units(FEW_OUT) && k < no; k += a.nb[FEW_OUT])
-        ptx::tma_prefetch_3d(&m.out, 0, p.cta * 16, k, keep);
-      ok = ptx::mbar_wait(&s->routed, 0, &s->abort, a.timeout_ns);
+      if (lane == 0)
+        for (int k = 0; p.cta < p.units(FEW_OUT) && k < no; k += a.nb[FEW_OUT])
+          ptx::tma_prefetch_3d(&m.out, 0, p.cta * 16, k, keep);
+      ok = wait(&s->routed, 0);
       if (!ok) break;
     }
     const int n = p.boxes(ph), nb = a.nb[ph], units = p.units(ph);
     in_ring = p.ring_stages(ph);
     if (slot >= in_ring) slot = 0;
-    for (int unit = p.cta; ok && unit < units; unit += p.ctas) {
-      if (ph == FEW_DOWN) {
-        const int row = unit / a.splits * 16, tiles = (a.L + BLOCK_M - 1) / BLOCK_M;
+    if (ph == FEW_DOWN) {
+      const int tiles = (a.L + BLOCK_M - 1) / BLOCK_M;
+      for (int unit = p.cta; ok && unit < units; unit += p.ctas) {
+        const int row = p.down_row(unit), tile0 = row / BLOCK_M, y = row % BLOCK_M;
         int e0, e1;
         p.experts(unit, &e0, &e1);
         for (int e = e0; ok && e < e1; e += a.group) {
           const int ge = min(a.group, e1 - e);
+          const int tile = lane < ge ? s->expert[e + lane] * tiles + tile0 : 0;
           for (int k = 0; ok && k < n; k += nb) {
-            const bool sc = FP8 && k == 0;  // with an expert's first boxes
-            uint8_t* dst = stage(ge * nb, sc ? ge * 16 : 0);
+            uint8_t* dst = stage(ge * nb);
             if (!dst) break;
-            for (int i = 0; i < ge; ++i) {
-              const int tile = s->expert[e + i] * tiles + row / BLOCK_M;
-              ptx::tma_load_4d_hint(dst + i * nb * FEW_BOX, &m.edown, &s->full[slot], 0,
-                                    row % BLOCK_M, k, tile, once);
-              if (sc)
-                ptx::bulk_load(dst + FEW_BOXES + i * 64,
-                               a.s_ed + static_cast<size_t>(tile) * BLOCK_M + row % BLOCK_M, 64,
-                               &s->full[slot]);
-            }
+            if (lane < ge)
+              ptx::tma_load_4d_hint(dst + lane * nb * FEW_BOX, &m.edown, &s->full[slot], 0, y, k,
+                                    tile, once);
             next();
           }
         }
-        continue;
       }
+      continue;
+    }
+    typename FewPlan<FP8>::Gate gate(p);
+    const int tiles = (2 * a.I + BLOCK_M - 1) / BLOCK_M;
+    for (int unit = p.cta; ok && unit < units; unit += p.ctas) {
       const bool shared = ph == FEW_IN && unit >= a.L / 16;
-      int f = 0, y = unit * 16, tile = 0;
-      if (shared) f = (unit - a.L / 16) * 8;
-      if (ph == FEW_GATE_UP) f = unit % (a.I / 8) * 8;
-      if (shared || ph == FEW_GATE_UP)  // packed row of the features' gate rows
-        y = f / GLU_GROUP * (2 * GLU_GROUP) + f % GLU_GROUP;
+      int y = unit * 16, tile = 0;
+      if (shared) y = p.gate_row((unit - a.L / 16) * 8);
       if (ph == FEW_GATE_UP) {
-        tile = s->expert[unit / (a.I / 8)] * ((2 * a.I + BLOCK_M - 1) / BLOCK_M) + y / BLOCK_M;
+        y = p.gate_row(gate.f);
+        tile = s->expert[gate.rank] * tiles + y / BLOCK_M;
         y %= BLOCK_M;
+        gate.next();
       }
       const CUtensorMap* map = ph == FEW_IN ? &m.down : ph == FEW_ROUTER ? &m.router : &m.out;
       for (int k = 0; k < n; k += nb) {
-        const bool sc = FP8 && ph == FEW_GATE_UP && k == 0;
-        uint8_t* dst = stage(nb, sc ? 16 : 0);
+        uint8_t* dst = stage(nb);
         if (!dst) break;
-        if (sc) {  // eight gate rows' and the same features' value rows'
-          const float* src = a.s_gu + static_cast<size_t>(tile) * BLOCK_M + y;
-          ptx::bulk_load(dst + FEW_BOXES, src, 32, &s->full[slot]);
-          ptx::bulk_load(dst + FEW_BOXES + 32, src + GLU_GROUP, 32, &s->full[slot]);
+        if (lane == 0) {
+          if (ph == FEW_GATE_UP)
+            ptx::tma_load_5d_hint(dst, &m.gate_up, &s->full[slot], 0, y, 0, k, tile, once);
+          else if (shared)
+            ptx::tma_load_4d_hint(dst, &m.shared, &s->full[slot], 0, y, 0, k, once);
+          else
+            ptx::tma_load_3d_hint(dst, map, &s->full[slot], 0, y, k, once);
         }
-        if (ph == FEW_GATE_UP)
-          ptx::tma_load_5d_hint(dst, &m.gate_up, &s->full[slot], 0, y, 0, k, tile, once);
-        else if (shared)
-          ptx::tma_load_4d_hint(dst, &m.shared, &s->full[slot], 0, y, 0, k, once);
-        else
-          ptx::tma_load_3d_hint(dst, map, &s->full[slot], 0, y, k, once);
         next();
       }
     }
   }
+  if (lane != 0) return;
   if (!ok && !*static_cast<volatile int*>(&s->abort)) {
     *static_cast<volatile int*>(&s->abort) = 1;
     atomicOr(a.head, DEVERR_TIMEOUT_PRODUCER);
@@ -293,7 +313,6 @@ struct Few : FewPlan<FP8> {
   using P::KC;
   using P::s;
   using P::units;
-  using P::STAGE;
   uint8_t* ring;       // of a.stages stages
   uint8_t* tok;        // tokens' operands
   uint32_t top, bars;  // shared-memory addresses: of this warp's box above slot 0, of `full`
@@ -325,10 +344,8 @@ struct Few : FewPlan<FP8> {
   // Waits for the next stage; the shared-memory address of this warp's box.
   __device__ __forceinline__ uint32_t take() {
     wait(bars + slot * 8, (parity >> slot) & 1u);
-    return top - slot * STAGE;
+    return top - slot * FEW_STAGE;
   }
-  // e4m3: the scales that came with it, from the address of this warp's box
-  __device__ uint32_t scales(uint32_t box) const { return box - warp * FEW_BOX + FEW_BOXES; }
   __device__ __forceinline__ void release() {
     __syncwarp();  // every lane has read the box
     if (lane == 0 && ok)
@@ -337,9 +354,13 @@ struct Few : FewPlan<FP8> {
     parity ^= 1u << slot;
     if (++slot >= in_ring) slot = 0;
   }
-  __device__ void pass() {  // a stage without a box for this warp
-    take();
-    release();
+  // Whether this warp has a box in the next stage; if not, the stage is behind.
+  __device__ __forceinline__ bool live(bool box) {
+    if (!box) {
+      take();
+      release();
+    }
+    return box;
   }
   __device__ void enter(int ph) {
     in_ring = P::ring_stages(ph);
@@ -448,7 +469,7 @@ struct Few : FewPlan<FP8> {
   // proxy: they fence before the grid barrier, and so does the reader after it.
   __device__ void copy_rows(uint8_t* dst, int dst_pitch, const void* src, size_t src_pitch,
                             int rows, int bytes) {
-    if (warp != 0) return;
+    if (threadIdx.x >= 32) return;
     ptx::fence_proxy_async();
     if (lane == 0) ptx::mbar_expect_tx(&s->staged, static_cast<uint32_t>(rows) * bytes);
     __syncwarp();
@@ -553,55 +574,64 @@ struct Few : FewPlan<FP8> {
     if constexpr (FP8) sync();
   }
   // [gamma u | hs], and rstd of u.  u arrives in fp32 by bulk copies (loads through the LSU, all
-  // SMs asking for the same lines, took 10 us at eight tokens); warp t turns token t's row into
-  // bf16 where it lies, from the front, so that no value is overwritten before it was read.
+  // SMs asking for the same lines, took 10 us at eight tokens); the warps, shared out to the tokens,
+  // turn it into bf16 where it lies, from the front, a piece being in registers before any of it
+  // is written over.
   __device__ void stage_z() {
     const int pitch = a.out_pitch, nv = a.L / 4;
     copy_rows(tok, pitch, a.u, static_cast<size_t>(a.L) * 4, a.T, a.L * 4);
-    constexpr int NV = 14;
-    float4 g[NV];
-    auto load_gamma = [&](int v0) {
+    constexpr int NV = 4;
+    const int per = FEW_WARPS / a.T, t = warp / per, step = per * 32;
+    const int v0 = (warp % per) * 32 + lane;
+    const bool live = t < a.T;
+    uint8_t* row = tok + t * pitch;
+    float4 f[NV], g[NV];
+    auto load_gamma = [&](int from) {
 #pragma unroll
       for (int j = 0; j < NV; ++j)
-        g[j] = v0 + 32 * j < nv ? __ldg(reinterpret_cast<const float4*>(a.gamma) + v0 + 32 * j)
-                                : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (live && from + step * j < nv)
+          g[j] = __ldg(reinterpret_cast<const float4*>(a.gamma) + from + step * j);
     };
-    if (warp < a.T) load_gamma(lane);
+    load_gamma(v0);
     landed();
-    if (warp < a.T) {
-      float sq = 0.0f;
-      for (int v0 = lane; v0 - lane < nv; v0 += NV * 32) {
-        float4 f[NV];
-        if (v0 != lane) load_gamma(v0);
+    float sq = 0.0f;
+    for (int from = 0; from < nv; from += step * NV) {
+      const int v1 = v0 + from;
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-          const int v = v0 + 32 * j;
-          f[j] = v < nv ? *reinterpret_cast<const float4*>(tok + warp * pitch + v * 16)
-                        : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        }
-        __syncwarp();
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-          const int v = v0 + 32 * j;
-          sq = fmaf(f[j].x, f[j].x, fmaf(f[j].y, f[j].y, sq));
-          sq = fmaf(f[j].z, f[j].z, fmaf(f[j].w, f[j].w, sq));
-          if (v < nv) {
-            __nv_bfloat162* o = reinterpret_cast<__nv_bfloat162*>(tok + warp * pitch + v * 8);
-            o[0] = __floats2bfloat162_rn(f[j].x * g[j].x, f[j].y * g[j].y);
-            o[1] = __floats2bfloat162_rn(f[j].z * g[j].z, f[j].w * g[j].w);
-          }
-        }
-        __syncwarp();
+      for (int j = 0; j < NV; ++j) {
+        const int v = v1 + step * j;
+        f[j] = live && v < nv ? *reinterpret_cast<const float4*>(row + v * 16)
+                              : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       }
+      if (per > 1) sync();
+      else __syncwarp();
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
-      if (lane == 0) s->rstd[warp] = __frsqrt_rn(__fdiv_rn(sq, static_cast<float>(a.L)) + a.eps);
+      for (int j = 0; j < NV; ++j) {
+        const int v = v1 + step * j;
+        sq = fmaf(f[j].x, f[j].x, fmaf(f[j].y, f[j].y, sq));
+        sq = fmaf(f[j].z, f[j].z, fmaf(f[j].w, f[j].w, sq));
+        if (live && v < nv) {
+          __nv_bfloat162* o = reinterpret_cast<__nv_bfloat162*>(row + v * 8);
+          o[0] = __floats2bfloat162_rn(f[j].x * g[j].x, f[j].y * g[j].y);
+          o[1] = __floats2bfloat162_rn(f[j].z * g[j].z, f[j].w * g[j].w);
+        }
+      }
+      load_gamma(v1 + step * NV);  // (the next piece's values lie behind what was just written)
     }
-    sync();  // every row is bf16 before hs lands behind it
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
+    if (lane == 0) s->warp_sum[warp] = sq;
+    sync();  // and every row is bf16 before hs lands behind it
+    if (threadIdx.x < a.T) {
+      float all = 0.0f;
+      for (int w = 0; w < per; ++w) all += s->warp_sum[threadIdx.x * per + w];
+      s->rstd[threadIdx.x] = __frsqrt_rn(__fdiv_rn(all, static_cast<float>(a.L)) + a.eps);
+    }
     if (a.sw > 0) {
       copy_rows(tok + a.L * 2, pitch, a.hs, static_cast<size_t>(a.sw) * 2, a.T, a.sw * 2);
       landed();
     }
+    sync();  // rstd
   }
 
   // ---------------------------------------------------------------- phases
@@ -614,10 +644,7 @@ struct Few : FewPlan<FP8> {
       Acc acc;
       for (int k = 0; k < nc; k += nb) {
         const int c = k + warp;
-        if (warp >= nb || c >= nc) {
-          pass();
-          continue;
-        }
+        if (!live(warp < nb && c < nc)) continue;
         const Toks tk = load_tok(r, c);
         const Box bx = load_box(take());
         release();
@@ -636,10 +663,7 @@ struct Few : FewPlan<FP8> {
       Acc acc, rest;
       for (int k = 0; k < nc; k += nb) {
         const int c = k + warp;
-        if (warp >= nb || c >= nc) {
-          pass();
-          continue;
-        }
+        if (!live(warp < nb && c < nc)) continue;
         const Toks th = load_tok(hi, c), tl = load_tok(lo, c);
         const Box bx = load_box(take());
         release();
@@ -656,10 +680,10 @@ struct Few : FewPlan<FP8> {
         a.keys[i] = P::key(__ldg(a.logits_in + i), i % a.E);
   }
   // The K largest keys of a token, by a warp: lane j returns the j-th (larger key first, then the
-  // lower expert), as select_rounds does.  The K-th largest of the lanes' maxima is a lower bound
+  // lower expert), as select_rounds does.  cand (FEW_CAND of (key, expert)) and won (32): scratch.  The K-th largest of the lanes' maxima is a lower bound
   // of the K-th largest key; the keys that reach it are few unless many are equal, and are ranked
   // against each other.
-  __device__ int top_k(uint32_t* keys) {
+  __device__ int top_k(uint32_t* keys, uint2* cand, uint32_t* won) {
     const uint4* k4 = reinterpret_cast<const uint4*>(keys);
     const int nq = a.E / 4;
     uint32_t top = 0u;
@@ -692,7 +716,6 @@ struct Few : FewPlan<FP8> {
     const int all = __shfl_sync(0xffffffffu, at, 31);
     if (all > FEW_CAND || all < a.K) return select_rounds(keys, a.E, a.K, lane);
     at -= n;
-    uint2* cand = s->cand[warp];  // (key, expert)
     if (n > 0) {
       for (int q = lane; q < nq; q += 32) {
         const uint4 k = k4[q];
@@ -704,7 +727,6 @@ struct Few : FewPlan<FP8> {
     }
     __syncwarp();
     // each candidate's place among the others; a place below K is a winner's slot
-    uint32_t* won = s->won[warp];
     for (int c = lane; c < all; c += 32) {
       const uint2 me = cand[c];
       int r = 0;
@@ -723,9 +745,11 @@ struct Few : FewPlan<FP8> {
   __device__ void select() {
     const float* z = a.logits_in ? a.logits_in : a.logits;
     const int pairs = a.T * a.K;
-    const int fit = min(FEW_WARPS, a.stages * FEW_BOXES / (a.E * 8));
+    const int fit = min(FEW_WARPS, a.stages * FEW_STAGE / few_select_bytes(a.E));
     float* lg = reinterpret_cast<float*>(ring);
     uint32_t* keys = reinterpret_cast<uint32_t*>(lg) + fit * a.E;
+    uint2* cand = reinterpret_cast<uint2*>(keys + fit * a.E);
+    uint32_t* won = reinterpret_cast<uint32_t*>(cand + fit * FEW_CAND);
     for (int t0 = 0; t0 < a.T; t0 += fit) {
       const int nt = min(fit, a.T - t0);
       const size_t from = static_cast<size_t>(t0) * a.E, row = static_cast<size_t>(a.E) * 4;
@@ -734,7 +758,9 @@ struct Few : FewPlan<FP8> {
       landed();
       const int t = t0 + warp;
       if (warp < nt) {
-        const int e = min(top_k(keys + static_cast<size_t>(warp) * a.E), a.E - 1);
+        const int e = min(top_k(keys + static_cast<size_t>(warp) * a.E, cand + warp * FEW_CAND,
+                                won + warp * 32),
+                          a.E - 1);
         const float sj = lane < a.K ? score_sigmoid(lg[warp * a.E + e]) : 0.0f;
         float sum = 0.0f;
         for (int j = 0; j < a.K; ++j) sum = __fadd_rn(sum, __shfl_sync(0xffffffffu, sj, j));
@@ -790,25 +816,16 @@ struct Few : FewPlan<FP8> {
     const int row = (lane & 7) < a.T ? lane & 7 : -1;
     const int pitch = FP8 ? few_pitch(a.L) : few_pitch(a.L * 2);
     const Row hi = token_row(row, pitch), lo = token_row(row, pitch, FP8 ? 0 : lat_lo());
-    const int nc = P::boxes(FEW_GATE_UP), nb = a.nb[FEW_GATE_UP], g = lane >> 2;
+    const int nc = P::boxes(FEW_GATE_UP), nb = a.nb[FEW_GATE_UP];
     for (int unit = cta; unit < units(FEW_GATE_UP); unit += ctas) {
-      float gs = 1.0f, vs = 1.0f;  // e4m3: scales of this lane's gate and value row
       Acc acc, rest;
       for (int k = 0; k < nc; k += nb) {
         const int c = k + warp;
-        if (warp >= nb || c >= nc) {
-          pass();
-          continue;
-        }
+        if (!live(warp < nb && c < nc)) continue;
         const Toks th = load_tok(hi, c);
         Toks tl;
         if constexpr (!FP8) tl = load_tok(lo, c);
-        const uint32_t box = take();
-        if (FP8 && k == 0) {
-          gs = ptx::ld_shared_f32(scales(box) + g * 4);
-          vs = ptx::ld_shared_f32(scales(box) + (8 + g) * 4);
-        }
-        const Box bx = load_box(box);
+        const Box bx = load_box(take());
         release();
         multiply<FP8>(bx, th, acc);
         if constexpr (!FP8) multiply<false>(bx, tl, rest);
@@ -816,7 +833,7 @@ struct Few : FewPlan<FP8> {
       float t4[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        t4[k] = FP8 ? acc.sum(k) * (k < 2 ? gs : vs) : acc.sum(k) + rest.sum(k);
+        t4[k] = FP8 ? acc.sum(k) : acc.sum(k) + rest.sum(k);
       join(t4);
     }
   }
@@ -824,43 +841,53 @@ struct Few : FewPlan<FP8> {
     enter(FEW_DOWN);
     const int pitch = FP8 ? few_pitch(a.I) : few_pitch(a.I * 2);
     const int nk = P::boxes(FEW_DOWN), nb = a.nb[FEW_DOWN];
-    const int g = lane >> 2, t2 = (lane & 3) * 2;
+    const int g = lane >> 2, t2 = (lane & 3) * 2, tiles = (a.L + BLOCK_M - 1) / BLOCK_M;
     const int sub = warp / nb, kw = warp % nb;  // which of a stage's experts, and its box
     for (int unit = cta; unit < units(FEW_DOWN); unit += ctas) {
       int e0, e1;
       experts(unit, &e0, &e1);
       float sum[4] = {};
+      // e4m3: scales of this warp's next two experts' rows, lanes 0 .. 15 the first's, and of the two
+      // behind them.  (As bulk copies beside the boxes they cost the copy engine as much time as half a
+      // stage.)
+      const int row = P::down_row(unit);
+      auto scales = [&](int at) {
+        at += sub + (lane >> 4) * a.group;
+        if (sub >= a.group || at >= e1) return 1.0f;
+        return __ldg(a.s_ed + static_cast<size_t>(s->expert[at]) * tiles * BLOCK_M + row + (lane & 15));
+      };
+      float two = 1.0f, behind = 1.0f;
+      if constexpr (FP8) behind = scales(e0);
+      int second = 16;
       for (int e = e0; e < e1; e += a.group) {
         const int rank = e + sub;
-        if (sub >= a.group || rank >= e1) {
-          for (int k = 0; k < nk; k += nb) pass();
-          continue;
+        const bool mine = sub < a.group && rank < e1;
+        float2 w = make_float2(1.0f, 1.0f);
+        if constexpr (FP8) {
+          if ((second ^= 16) == 0) {
+            two = behind;
+            behind = scales(e + 2 * a.group);
+          }
+          w.x = __shfl_sync(0xffffffffu, two, second + g);
+          w.y = __shfl_sync(0xffffffffu, two, second + g + 8);
         }
-        const Row r = token_row(s->pair[rank][lane & 7], pitch);
-        const float2 f = *reinterpret_cast<const float2*>(&s->gate[rank][t2]);
-        float w0 = 1.0f, w1 = 1.0f;
+        const Row r = token_row(mine ? s->pair[rank][lane & 7] : -1, pitch);
+        const float2 f = mine ? *reinterpret_cast<const float2*>(&s->gate[rank][t2])
+                              : make_float2(0.0f, 0.0f);
         Acc acc;
         for (int k = 0; k < nk; k += nb) {
           const int c = k + kw;
-          if (c >= nk) {
-            pass();
-            continue;
-          }
+          if (!live(mine && c < nk)) continue;
           const Toks tk = load_tok(r, c);
-          const uint32_t box = take();
-          if (FP8 && k == 0) {
-            w0 = ptx::ld_shared_f32(scales(box) + (sub * 16 + g) * 4);
-            w1 = ptx::ld_shared_f32(scales(box) + (sub * 16 + 8 + g) * 4);
-          }
-          const Box bx = load_box(box);
+          const Box bx = load_box(take());
           release();
           multiply<FP8>(bx, tk, acc);
         }
         // times the tokens' gates (e4m3: and both scales)
-        sum[0] = fmaf(acc.sum(0), f.x * w0, sum[0]);
-        sum[1] = fmaf(acc.sum(1), f.y * w0, sum[1]);
-        sum[2] = fmaf(acc.sum(2), f.x * w1, sum[2]);
-        sum[3] = fmaf(acc.sum(3), f.y * w1, sum[3]);
+        sum[0] = fmaf(acc.sum(0), f.x * w.x, sum[0]);
+        sum[1] = fmaf(acc.sum(1), f.y * w.x, sum[1]);
+        sum[2] = fmaf(acc.sum(2), f.x * w.y, sum[2]);
+        sum[3] = fmaf(acc.sum(3), f.y * w.y, sum[3]);
       }
       join(sum);
     }
@@ -875,10 +902,7 @@ struct Few : FewPlan<FP8> {
       Acc az, as;
       for (int k = 0; k < nc; k += nb) {
         const int c = k + warp;
-        if (warp >= nb || c >= nc) {
-          pass();
-          continue;
-        }
+        if (!live(warp < nb && c < nc)) continue;
         const Toks tk = load_tok(r, c);
         const Box bx = load_box(take());
         release();
@@ -973,8 +997,13 @@ struct FewFinish : FewPlan<FP8> {
     if (lane == 0) ptx::mbar_arrive(&s->red_empty[b]);
     ++unit_no;
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-      v[h] = ((p[h][0] + p[h][1]) + (p[h][2] + p[h][3])) + ((p[h][4] + p[h][5]) + (p[h][6] + p[h][7]));
+    for (int n = FEW_WARPS / 2; n > 0; n /= 2)
+#pragma unroll
+      for (int k = 0; k < n; ++k)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) p[h][k] += p[h][k + n];
+    v[0] = p[0][0];
+    v[1] = p[1][0];
     return true;
   }
   // All results of a phase are on their way; the next grid barrier publishes them.
@@ -1019,15 +1048,23 @@ struct FewFinish : FewPlan<FP8> {
     }
     finished(FEW_ROUTER);
     if (!wait(&s->routed, 0)) return;
-    const int per = a.I / 8;
+    typename P::Gate gate(*this);
+    const int tiles = (2 * a.I + BLOCK_M - 1) / BLOCK_M;
     const float ls = FP8 && token ? __ldcg(a.lat_scale + t) : 1.0f;
     for (int unit = cta; unit < units(FEW_GATE_UP); unit += ctas) {
-      const int p = s->pair[unit / per][t];
+      const int rank = gate.rank, f = gate.f, p = s->pair[rank][t];
+      gate.next();
+      float gs = 1.0f, vs = 1.0f;
+      if constexpr (FP8) {
+        const float* sc = a.s_gu + static_cast<size_t>(s->expert[rank]) * tiles * BLOCK_M +
+                          P::gate_row(f) + row;
+        gs = __ldg(sc) * ls, vs = __ldg(sc + GLU_GROUP) * ls;
+      }
       if (!total(v)) return;
       if (p < 0) continue;
-      const size_t o = static_cast<size_t>(p) * a.I + unit % per * 8 + row;
+      const size_t o = static_cast<size_t>(p) * a.I + f + row;
       if constexpr (FP8)
-        static_cast<float*>(a.h)[o] = situ_glu(v[0] * ls, v[1] * ls, a.c, inv_c);
+        static_cast<float*>(a.h)[o] = situ_glu(v[0] * gs, v[1] * vs, a.c, inv_c);
       else
         static_cast<__nv_bfloat16*>(a.h)[o] = __float2bfloat16_rn(situ_glu(v[0], v[1], a.c, inv_c));
     }
@@ -1035,7 +1072,7 @@ struct FewFinish : FewPlan<FP8> {
     // u starts at zero and receives at most two parts, so that their order does not matter
     for (int unit = cta; unit < units(FEW_DOWN); unit += ctas) {
       if (!total(v)) return;
-      float* u = a.u + static_cast<size_t>(t) * a.L + unit / a.splits * 16 + row;
+      float* u = a.u + static_cast<size_t>(t) * a.L + P::down_row(unit) + row;
       if (token) atomicAdd(u, v[0]);
       if (token) atomicAdd(u + 8, v[1]);
     }
@@ -1063,8 +1100,8 @@ few_kernel(const __grid_constant__ FewMaps maps, const __grid_constant__ FewArgs
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = ptx::smem_u32(smem_raw);
   uint8_t* tok = smem_raw + (((raw + 1023u) & ~1023u) - raw);
-  uint8_t* ring = tok + a.tok_bytes;
-  uint8_t* top = ring + a.stages * few_stage_bytes(FP8);
+  uint8_t* top = tok + a.top;
+  uint8_t* ring = top - a.stages * FEW_STAGE;
   FewTables* s = reinterpret_cast<FewTables*>(top);
   if (threadIdx.x == 0) {
     for (int i = 0; i < a.more; ++i) {
@@ -1088,14 +1125,14 @@ few_kernel(const __grid_constant__ FewMaps maps, const __grid_constant__ FewArgs
   if (threadIdx.x >= FEW_THREADS + 32) {
     FewFinish<FP8>(a, s, threadIdx.x - (FEW_THREADS + 32)).run();
   } else if (threadIdx.x >= FEW_THREADS) {
-    if (threadIdx.x == FEW_THREADS) few_load(FewPlan<FP8>(a, s), maps, top);
+    few_load(FewPlan<FP8>(a, s), maps, top);
   } else {
     Few<FP8> f(a, s);
     f.warp = threadIdx.x >> 5;
     f.lane = threadIdx.x & 31;
     f.ring = ring;
     f.tok = tok;
-    f.top = ptx::smem_u32(top) - Few<FP8>::STAGE + f.warp * FEW_BOX;
+    f.top = ptx::smem_u32(top) - FEW_STAGE + f.warp * FEW_BOX;
     f.bars = ptx::smem_u32(s->full);
     f.run();
   }
@@ -1144,8 +1181,7 @@ static FewLayout few_layout(const lmoe_dims& D) {
 // Shared memory: the tokens' operands take the largest of the phases' needs, the ring the rest;
 // while the experts run, whose operands may be smaller (e4m3 codes), the ring has that too.
 struct FewSmem {
-  size_t tok;
-  int stages, more, out_pitch;
+  int stages, more, top, out_pitch;
 };
 constexpr size_t FEW_SMEM_MAX = 232448 - 1024;  // less the alignment's slack
 
@@ -1159,14 +1195,17 @@ static FewSmem few_smem(const lmoe_dims& D) {
   const size_t hi_lo = T * 2 * few_pitch(D.L * 2);
   const size_t experts = larger(fp8 ? T * few_pitch(D.L) : hi_lo,
                                 T * D.K * few_pitch(fp8 ? D.I : D.I * 2));
-  M.tok = larger(larger(T * few_pitch(D.d * 2), hi_lo), larger(experts, T * M.out_pitch));
-  M.tok = (M.tok + 1023) / 1024 * 1024;  // the ring behind it
-  const size_t fixed = M.tok + sizeof(FewTables), stage = few_stage_bytes(fp8);
-  if (fixed >= FEW_SMEM_MAX) return M;
-  M.stages = static_cast<int>((FEW_SMEM_MAX - fixed) / stage);
-  if (M.stages > FEW_MAX_STAGES) M.stages = FEW_MAX_STAGES;
-  M.more = M.stages + static_cast<int>((M.tok - experts) / stage);
-  if (M.more > FEW_MAX_STAGES) M.more = FEW_MAX_STAGES;
+  const size_t all = larger(larger(T * few_pitch(D.d * 2), hi_lo), larger(experts, T * M.out_pitch));
+  const size_t stage = FEW_STAGE, room = FEW_SMEM_MAX - sizeof(FewTables);
+  auto fit = [&](size_t used) {  // stages that lie above `used` bytes
+    used = (used + 1023) / 1024 * 1024;
+    const int n = used < room ? static_cast<int>((room - used) / stage) : 0;
+    return n < FEW_MAX_STAGES ? n : FEW_MAX_STAGES;
+  };
+  M.stages = fit(all);
+  M.more = fit(experts);
+  M.top = static_cast<int>(larger((all + 1023) / 1024 * 1024 + M.stages * stage,
+                                  (experts + 1023) / 1024 * 1024 + M.more * stage));
   return M;
 }
 
@@ -1187,7 +1226,7 @@ static int few_supported(const lmoe_dims* D) {
                      ceil_div(D->I, 64);
   if (gu >= (int64_t{1} << 31) || ed >= (int64_t{1} << 31)) return LMOE_ERR_UNSUPPORTED;
   const int stages = few_smem(*D).stages;
-  if (stages < FEW_MIN_STAGES || stages * size_t{FEW_BOXES} < D->E * size_t{8})
+  if (stages < FEW_MIN_STAGES || stages * FEW_STAGE < few_select_bytes(D->E))
     return LMOE_ERR_UNSUPPORTED;
   return LMOE_OK;
 }
@@ -1283,7 +1322,7 @@ int lmoe_forward_few(const lmoe_dims* dims, const void* packed, const void* x,
   a.stages = M.stages;
   a.more = M.more;
   a.out_pitch = M.out_pitch;
-  a.tok_bytes = static_cast<int>(M.tok);
+  a.top = M.top;
   a.x = static_cast<const __nv_bfloat16*>(x);
   a.resid = static_cast<const __nv_bfloat16*>(residual);
   a.y = static_cast<__nv_bfloat16*>(y);
@@ -1355,8 +1394,7 @@ int lmoe_forward_few(const lmoe_dims* dims, const void* packed, const void* x,
       !make_tmap_boxes(&m.gate_up, pk + P.wgu, 5, gu_dims, gu_strides, gu_box) ||
       !make_tmap_boxes(&m.edown, pk + P.wed, 4, ed_dims, ed_strides, ed_box))
     return LMOE_ERR_CUDA;
-  const size_t smem = 1024 + static_cast<size_t>(a.stages) * few_stage_bytes(D.expert_fp8 != 0) + a.tok_bytes +
-                      sizeof(FewTables);
+  const size_t smem = 1024 + static_cast<size_t>(a.top) + sizeof(FewTables);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int out = D.expert_fp8 ? launch_few<true>(m, a, sms, smem, st)
                                : launch_few<false>(m, a, sms, smem, st);
