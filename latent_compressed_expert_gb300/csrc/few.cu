@@ -84,7 +84,8 @@ struct FewArgs {
   uint32_t* keys;             // [T, E] selection keys of the logits
   void* h;                    // [T K, I] bf16, or fp32 (e4m3)
   float* u;                   // [T, L]
-  uint8_t* lat8;              // e4m3: codes and scales of the latent and of h
+  float* lat32;               // e4m3: the latent in fp32 [T, L];
+  uint8_t* lat8;              // codes and scales of the latent and of h
   float* lat_scale;
   uint8_t* h8;
   float* h_scale;
@@ -528,20 +529,13 @@ struct Few : FewPlan<FP8> {
     const int pitch = few_pitch(a.L * 2);
     copy_rows(tok, pitch, a.lat, static_cast<size_t>(a.L) * 2, 2 * a.T, a.L * 2);
     landed();
-    if constexpr (FP8) {  // a token per CTA, of those that have the least to do for the router
+    // a token per CTA, of those that have the least to do for the router.  From the fp32 latent: one code
+    // that hi + lo turned would, through h's own rounding, cost a token a hundredth of its branch
+    if constexpr (FP8) {
       for (int t = ctas - 1 - cta; t < a.T; t += ctas) {
-        const uint2* hi = reinterpret_cast<const uint2*>(tok + t * pitch);
-        const uint2* lo = reinterpret_cast<const uint2*>(tok + lat_lo() + t * pitch);
-        auto get = [&](int v) {
-          const uint2 h = hi[v], l = lo[v];
-          auto two = [](uint32_t p, uint32_t q) {
-            return make_float2(__uint_as_float(p << 16) + __uint_as_float(q << 16),
-                               __uint_as_float(p & 0xFFFF0000u) + __uint_as_float(q & 0xFFFF0000u));
-          };
-          const float2 f = two(h.x, l.x), g = two(h.y, l.y);
-          return make_float4(f.x, f.y, g.x, g.y);
-        };
-        quantize(a.L, get, a.lat8 + static_cast<size_t>(t) * a.L, a.lat_scale + t);
+        const float4* row = reinterpret_cast<const float4*>(a.lat32 + static_cast<size_t>(t) * a.L);
+        quantize(a.L, [&](int v) { return __ldcg(row + v); }, a.lat8 + static_cast<size_t>(t) * a.L,
+                 a.lat_scale + t);
       }
     }
   }
@@ -1030,6 +1024,7 @@ struct FewFinish : FewPlan<FP8> {
       for (int h = 0; h < 2; ++h) {
         const __nv_bfloat16 hi = __float2bfloat16_rn(v[h]);
         const size_t o = static_cast<size_t>(t) * a.L + unit * 16 + row + 8 * h;
+        if constexpr (FP8) a.lat32[o] = v[h];
         a.lat[o] = hi;
         a.lat[static_cast<size_t>(a.T) * a.L + o] = __float2bfloat16_rn(v[h] - __bfloat162float(hi));
       }
@@ -1151,7 +1146,7 @@ few_kernel(const __grid_constant__ FewMaps maps, const __grid_constant__ FewArgs
 }
 
 struct FewLayout {
-  size_t lat, hs, logits, keys, h, u, lat8, lat_scale, h8, h_scale, total;
+  size_t lat, hs, logits, keys, h, u, lat32, lat8, lat_scale, h8, h_scale, total;
 };
 static FewLayout few_layout(const lmoe_dims& D) {
   FewLayout W{};
@@ -1169,6 +1164,7 @@ static FewLayout few_layout(const lmoe_dims& D) {
   W.h = take(T * D.K * D.I * 4);
   W.u = take(T * D.L * 4);
   if (D.expert_fp8) {
+    W.lat32 = take(T * D.L * 4);
     W.lat8 = take(T * D.L);
     W.lat_scale = take(T * 4);
     W.h8 = take(T * D.K * D.I);
@@ -1343,6 +1339,7 @@ int lmoe_forward_few(const lmoe_dims* dims, const void* packed, const void* x,
   a.keys = reinterpret_cast<uint32_t*>(ws + W.keys);
   a.h = ws + W.h;
   a.u = reinterpret_cast<float*>(ws + W.u);
+  a.lat32 = reinterpret_cast<float*>(ws + W.lat32);
   a.lat8 = ws + W.lat8;
   a.lat_scale = reinterpret_cast<float*>(ws + W.lat_scale);
   a.h8 = ws + W.h8;
