@@ -14,19 +14,25 @@
 //
 // A phase is a list of units of 16 weight rows (8 gate and the same features' 8 value rows for
 // the gated ones), dealt round the CTAs; K3's 736, 56, 1024, 448 and 448 units over 152 SMs leave
-// 3 % idle.  One thread loads a unit's weights, up to eight boxes of 16 rows x 128 bytes at a
+// 3 % idle.  A loading warp brings a unit's weights, up to eight boxes of 16 rows x 128 bytes at a
 // time, into a ring, over units and phases as far ahead as the ring reaches: weights do not
 // depend on what the other CTAs compute, so a grid barrier finds the next phase's loads already
 // in flight.  Eight warps split the reduction, warp w taking box w of every stage, and multiply
-// it by the tokens (the eight columns of an m16n8k16 MMA) from shared memory.  tcgen05 would bring
-// nothing here: the tensor cores are idle most of the time, and its 128-row tiles would make
-// units too large to deal out evenly.
+// it by the tokens (the eight columns of an m16n8k16 MMA) from shared memory; two more warps add
+// their partial tiles up and store the results.  tcgen05 would bring nothing here: the tensor cores
+// are idle most of the time, and its 128-row tiles would make units too large to deal out evenly.
 //
-// Arithmetic: fp32 accumulation; the latent is kept as two bf16 terms,
-// hi + lo, ~2^-17 of its fp32 value, for the router and the experts, hs, h and gamma u are rounded to bf16
-// once as the next product's operand (e4m3 experts: the latent and h to e4m3 codes with a scale
-// per row from their fp32 values); rms(u) is applied after the product, which is the same for a
-// factor per token.  e4m3 products run as fp16 MMAs on the codes' exact values.
+// Measured (K3, in a CUDA graph): one token 84 to 86 us (0.81 of the weights' time at the rate of a
+// copy; lmoe_forward 175), eight 259 to 264 us (0.92; 331); e4m3 experts, four tokens 126 us (0.75;
+// 207).  The expert phases of bf16 layers run at HBM's rate; what is left are the barriers (~2 us
+// each), the selection (4 us) and the operands' way into shared memory (1 to 5 us a phase).  With
+// e4m3 experts the computing warps' ~500 cycles a box, of instructions and of shared memory's
+// latency, are as long as HBM takes for a stage.
+//
+// Arithmetic: fp32 accumulation; the latent is kept as two bf16 terms, hi + lo, ~2^-17 of its fp32
+// value, for the router and bf16 experts; hs, h and gamma u are rounded to bf16 once as the next
+// product's operand (e4m3 experts: the latent and h to e4m3 codes with a scale per row, from their
+// fp32 values); rms(u) is applied after the product, which is the same for a factor per token.
 #include <stddef.h>
 #include <string.h>
 
@@ -226,7 +232,7 @@ __device__ void few_load(const FewPlan<FP8>& p, const FewMaps& m, uint8_t* top) 
     if (ph == FEW_GATE_UP) {
       // Its weights depend on the routing.  Until that is known (from the first barrier on), HBM
       // brings the CTA's first unit of OUT into L2, where the expert weights, which are the first
-      // to be evicted, leave it: K3, one token 92.1 -> 90.3 us, eight 285 -> 280; two units 93.4.
+      // to be evicted, leave it: K3, one token 92.1 -> 90.3 us, eight 285 -> 280 (two units: 93.4).
       ok = wait(&s->idle, 0);
       if (!ok) break;
       const uint64_t keep = ptx::l2_policy_evict_last();
@@ -529,8 +535,8 @@ struct Few : FewPlan<FP8> {
     const int pitch = few_pitch(a.L * 2);
     copy_rows(tok, pitch, a.lat, static_cast<size_t>(a.L) * 2, 2 * a.T, a.L * 2);
     landed();
-    // a token per CTA, of those that have the least to do for the router.  From the fp32 latent: one code
-    // that hi + lo turned would, through h's own rounding, cost a token a hundredth of its branch
+    // a token per CTA, of those that have the least to do for the router.  From the fp32 latent: one
+    // code that hi + lo turned would, through h's own rounding, cost a token a hundredth of its branch
     if constexpr (FP8) {
       for (int t = ctas - 1 - cta; t < a.T; t += ctas) {
         const float4* row = reinterpret_cast<const float4*>(a.lat32 + static_cast<size_t>(t) * a.L);
@@ -674,9 +680,9 @@ struct Few : FewPlan<FP8> {
         a.keys[i] = P::key(__ldg(a.logits_in + i), i % a.E);
   }
   // The K largest keys of a token, by a warp: lane j returns the j-th (larger key first, then the
-  // lower expert), as select_rounds does.  cand (FEW_CAND of (key, expert)) and won (32): scratch.  The K-th largest of the lanes' maxima is a lower bound
+  // lower expert), as select_rounds does.  The K-th largest of the lanes' maxima is a lower bound
   // of the K-th largest key; the keys that reach it are few unless many are equal, and are ranked
-  // against each other.
+  // against each other.  Scratch: cand (FEW_CAND of (key, expert)), won (32).
   __device__ int top_k(uint32_t* keys, uint2* cand, uint32_t* won) {
     const uint4* k4 = reinterpret_cast<const uint4*>(keys);
     const int nq = a.E / 4;
@@ -952,7 +958,7 @@ struct Few : FewPlan<FP8> {
 // The finishing warps: thread i of 64 takes elements i and i + 64 of a unit's 16 x 8 tile (rows
 // i / 8 and i / 8 + 8, gated units: a feature's gate and value, for token i % 8), adds up the
 // eight partial tiles and stores the results.  Computing warps that did this between their boxes
-// held each other up at every unit (e4m3, four tokens: @FIN@).
+// held each other up at every unit.
 template <bool FP8>
 struct FewFinish : FewPlan<FP8> {
   using P = FewPlan<FP8>;
