@@ -29,8 +29,7 @@
 //                        is the weights' way from HBM: 2 rows of 7168 x 4096 13.6 us (4.3 TB/s), 77
 //                        rows of 3584 x 7168 15.5 us.  About 4 us of that are the launch, the first
 //                        load and the last tile's way through the cluster.
-// Sums are fp32 in TMEM.  The MMA cuts off what it adds below the accumulator's last bit, so that
-// long sums come out low: an fp32 dw by 3e-7 of its size over 333 rows, 1e-6 over 1000, 9e-6 over 8192.
+// Sums are fp32 in TMEM (an fp32 dw over SM pairs: in registers from 512 rows on, LINEAR_DW_PART).
 // Every wait is bounded; on time-out a role records an error bit, raises the CTA's abort flag,
 // waits for its copies in flight and the kernel ends with its output unspecified.
 #pragma once
@@ -502,17 +501,17 @@ constexpr int linear_dw_buffer(int half, int q) {  // 1024-byte aligned, within 
 static_assert(linear_dw_buffer(0, 4) <= LINEAR_TURN_BYTES, "both forms fit");
 static_assert(linear_dw_buffer(1, 4) <= 2 * LINEAR_TURN_BYTES, "both forms fit");
 
-// dw's epilogue: a warp's 32 rows by 32 accumulator columns at a time through its own buffer
-// into a tensor store, whose map cuts rows and columns outside the output.  (Through registers and
-// store instructions, eight rows of 64 or 128 bytes each, the wgrad of a few rows took 1.6 times
-// as long.)
-template <typename Release>
-__device__ __forceinline__ void linear_dw_chunk(const CUtensorMap* tmO, const LinearArgs& g,
-                                                uint8_t* buf, int lane, uint32_t taddr, int row,
-                                                int col, bool last, Release release) {
-  float v[32];
-  ptx::tmem_ld_32x32b_x32(taddr, v);
-  if (last) release();
+// An fp32 dw's sums are taken out of TMEM after this many K-blocks (512 rows) and go on in
+// registers, which round: the MMA cuts off what it adds below the accumulator's last bit, and a sum
+// over 8192 rows came out 9e-6 of itself too low.  The epilogue has the time.
+constexpr int LINEAR_DW_PART = 8;
+
+// dw's epilogue: a warp's 32 rows by 32 columns at a time through its own buffer into a tensor store,
+// whose map cuts rows and columns outside the output.  (Through registers and store instructions,
+// eight rows of 64 or 128 bytes each, the wgrad of a few rows took 1.6 times as long.)
+__device__ __forceinline__ void linear_dw_store(const CUtensorMap* tmO, const LinearArgs& g,
+                                                uint8_t* buf, int lane, const float (&v)[32],
+                                                int row, int col) {
   if (lane == 0) ptx::bulk_wait_group_read<0>();  // the buffer's last store has read it
   __syncwarp();
   if (g.out_f32) {  // 128-byte rows, 16-byte pieces XOR row % 8 (the 128-byte swizzle)
@@ -665,6 +664,10 @@ linear_pair_kernel(const __grid_constant__ LinearPairMaps maps, const LinearArgs
   const LinearPairDeal<MODE, GLU> deal(g, cid, ncl);
   auto tile_at = [&](int i, LinearPairTile* t) { return deal.at(g, i, t); };
   auto blocks = [](const LinearPart& p) { return (p.D + LINEAR_KSTEP<FP8> - 1) / LINEAR_KSTEP<FP8>; };
+  // K-blocks that an accumulator takes up before the epilogue takes it over
+  auto part_of = [&](const LinearPairTile& t, int nk) {
+    return MODE == MODE_GRADS && t.dw && g.out_f32 ? min(nk, LINEAR_DW_PART) : nk;
+  };
   LinearPairTile t;
 
   if (warp == 0) {
@@ -728,33 +731,37 @@ linear_pair_kernel(const __grid_constant__ LinearPairMaps maps, const LinearArgs
       uint32_t parity = 0;
       bool ok = !g.inject_stall || ptx::mbar_wait(drain, 0, abort_flag, limit);
       if (!ok) linear_fail(g, abort_flag, DEVERR_TIMEOUT_MMA);
-      for (int i = 0; ok && tile_at(i, &t); ++i) {
-        const int acc = i & 1, nk = blocks(t.part);
-        if (!ptx::mbar_wait(&tempty[acc], ((i >> 1) & 1) ^ 1, abort_flag, limit)) {
-          linear_fail(g, abort_flag, DEVERR_TIMEOUT_MMA);
-          break;
-        }
-        ptx::tc_fence_after();
-        const uint32_t d = tmem_base + static_cast<uint32_t>(acc * 256);
+      for (int i = 0, lt = 0; ok && tile_at(i, &t); ++i) {
+        const int nk = blocks(t.part), part = part_of(t, nk);
         const uint32_t idesc = MODE == MODE_GRADS && t.dw
                                    ? linear_idesc<MODE_DW, FP8>(2 * BLOCK_M, t.part.bn)
                                    : linear_idesc<MAIN, FP8>(2 * BLOCK_M, t.part.bn);
-        for (int kb = 0; kb < nk; ++kb) {
-          if (!ptx::mbar_wait(&m.full[s], parity, abort_flag, limit)) {
+        for (int k0 = 0; ok && k0 < nk; k0 += part, ++lt) {
+          const int acc = lt & 1, k1 = min(k0 + part, nk);
+          if (!ptx::mbar_wait(&tempty[acc], ((lt >> 1) & 1) ^ 1, abort_flag, limit)) {
             linear_fail(g, abort_flag, DEVERR_TIMEOUT_MMA);
             ok = false;
             break;
           }
           ptx::tc_fence_after();
-          const uint32_t sp = ptx::smem_u32(m.base + s * stage_bytes);
-          if (MODE == MODE_GRADS && t.dw)
-            linear_mma<MODE_DW, FP8, true>(d, sp, sp + LINEAR_P_BYTES, idesc, kb == 0);
-          else
-            linear_mma<MAIN, FP8, true>(d, sp, sp + LINEAR_P_BYTES, idesc, kb == 0);
-          ptx::umma_commit_pair(&m.empty[s], 0x3);
-          if (++s == stages) s = 0, parity ^= 1u;
+          const uint32_t d = tmem_base + static_cast<uint32_t>(acc * 256);
+          for (int kb = k0; kb < k1; ++kb) {
+            if (!ptx::mbar_wait(&m.full[s], parity, abort_flag, limit)) {
+              linear_fail(g, abort_flag, DEVERR_TIMEOUT_MMA);
+              ok = false;
+              break;
+            }
+            ptx::tc_fence_after();
+            const uint32_t sp = ptx::smem_u32(m.base + s * stage_bytes);
+            if (MODE == MODE_GRADS && t.dw)
+              linear_mma<MODE_DW, FP8, true>(d, sp, sp + LINEAR_P_BYTES, idesc, kb == k0);
+            else
+              linear_mma<MAIN, FP8, true>(d, sp, sp + LINEAR_P_BYTES, idesc, kb == k0);
+            ptx::umma_commit_pair(&m.empty[s], 0x3);
+            if (++s == stages) s = 0, parity ^= 1u;
+          }
+          if (ok) ptx::umma_commit_pair(&tfull[acc], 0x3);
         }
-        if (ok) ptx::umma_commit_pair(&tfull[acc], 0x3);
       }
       // all MMAs issued by this thread complete before TMEM is released
       ptx::umma_commit_pair(drain, 0x1);
@@ -775,8 +782,8 @@ linear_pair_kernel(const __grid_constant__ LinearPairMaps maps, const LinearArgs
     constexpr int G = PROWS / 8;            // column groups of a buffer's rows
     constexpr int ITEMS = 32 * G / 128;     // per thread
     const int gr = tid / G, gc = tid % G;   // item j: buffer row gr + j 128 / G, group gc
-    for (int i = 0; tile_at(i, &t); ++i) {
-      const int acc = i & 1;
+    for (int i = 0, lt = 0; tile_at(i, &t); ++i, ++lt) {
+      int acc = lt & 1;
       // output row of item j in chunk ch, and this thread's columns (not dw)
       auto row_of = [&](int ch, int j) { return t.row0 + ch * 32 + gr + j * (128 / G); };
       const int col = t.col0 + rank * PROWS + gc * 8;
@@ -795,15 +802,17 @@ linear_pair_kernel(const __grid_constant__ LinearPairMaps maps, const LinearArgs
           if (row_of(ch, j) < g.R) rnext[j] = linear_resid8(g, row_of(ch, j), col);
       };
       load_res(half);
-      const bool got = ptx::mbar_wait(&tfull[acc], (i >> 1) & 1, abort_flag, limit);
-      // a half's warps leave together: they share its barrier
-      if (!ptx::named_and(bar, 128, got)) {
-        if (lane == 0) linear_fail(g, abort_flag, DEVERR_TIMEOUT_EPILOGUE);
-        break;
-      }
-      ptx::tc_fence_after();
-      const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
-                          static_cast<uint32_t>(acc * 256);
+      auto arrived = [&]() {
+        const bool got = ptx::mbar_wait(&tfull[acc], (lt >> 1) & 1, abort_flag, limit);
+        // a half's warps leave together: they share its barrier
+        const bool all = ptx::named_and(bar, 128, got);
+        if (!all && lane == 0) linear_fail(g, abort_flag, DEVERR_TIMEOUT_EPILOGUE);
+        ptx::tc_fence_after();
+        return all;
+      };
+      if (!arrived()) break;
+      uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
+                    static_cast<uint32_t>(acc * 256);
       auto release = [&]() {  // this warp has read its part of the accumulator
         ptx::tc_fence_before();
         __syncwarp();
@@ -814,16 +823,54 @@ linear_pair_kernel(const __grid_constant__ LinearPairMaps maps, const LinearArgs
             ptx::mbar_arrive_cluster(te[acc]);
         }
       };
-      if (half >= chunks) release();
       if (MODE == MODE_GRADS && t.dw) {
+        const int nk = blocks(t.part), parts = (nk + part_of(t, nk) - 1) / part_of(t, nk);
+        uint8_t* own = reinterpret_cast<uint8_t*>(turn) + linear_dw_buffer(half, q);
+        const int row = t.row0 + rank * BLOCK_M + q * 32;
+        if (parts == 1) {
+          if (half >= chunks) release();
 #pragma unroll 1
-        for (int ch = half; ch < chunks; ch += 2)
-          linear_dw_chunk(&maps.dw_out, g,
-                          reinterpret_cast<uint8_t*>(turn) + linear_dw_buffer(half, q), lane,
-                          tb + static_cast<uint32_t>(ch * 32), t.row0 + rank * BLOCK_M + q * 32,
-                          t.col0 + ch * 32, ch + 2 >= chunks, release);
+          for (int ch = half; ch < chunks; ch += 2) {
+            float v[32];
+            ptx::tmem_ld_32x32b_x32(tb + static_cast<uint32_t>(ch * 32), v);
+            if (ch + 2 >= chunks) release();
+            linear_dw_store(&maps.dw_out, g, own, lane, v, row, t.col0 + ch * 32);
+          }
+          continue;
+        }
+        float sum[4][32];  // of this warp's chunks
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int j = 0; j < 32; ++j) sum[c][j] = 0.0f;
+        bool ok = true;
+        for (int p = 0;;) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            if (half + 2 * c >= chunks) continue;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              float v[16];
+              ptx::tmem_ld_32x32b_x16(tb + static_cast<uint32_t>((half + 2 * c) * 32 + 16 * h), v);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) sum[c][16 * h + j] += v[j];
+            }
+          }
+          release();
+          if (++p == parts) break;
+          ++lt;
+          acc = lt & 1;
+          if (!(ok = arrived())) break;
+          tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * 256);
+        }
+        if (!ok) break;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (half + 2 * c < chunks)
+            linear_dw_store(&maps.dw_out, g, own, lane, sum[c], row, t.col0 + (half + 2 * c) * 32);
         continue;
       }
+      if (half >= chunks) release();
 #pragma unroll 1
       for (int ch = half; ch < chunks; ch += 2) {
         uint4 rcur[ITEMS];

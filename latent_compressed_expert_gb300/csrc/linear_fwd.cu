@@ -66,6 +66,8 @@ LinearPlan linear_plan(int mode, int R, int C, int D, int out_size, bool fp8, bo
       for (int ks = 1; ks <= 8; ++ks) {
         const int64_t ctas = tiles * ks;
         if (ks > 1 && (nk < 2 * ks || ctas > per_sm * sms || (per_sm == 1 && ks > 4))) break;
+        // a tile's fp32 sums stay in TMEM (LINEAR_DW_PART): not for more than 1024 rows
+        if (dw && out_size == 4 && ceil_div(nk, ks) > 2 * LINEAR_DW_PART) continue;
         const int64_t kb = ceil_div(nk, ks), waves = ceil_div(ctas, per_sm * sms);
         const double shared = static_cast<double>(ceil_div(ctas, sms) * kb) *
                               larger(FLOP * BLOCK_M * bn / RATE, bytes / FEED);

@@ -352,3 +352,17 @@ def test_refusals(dev):
                                     _codes(w)[1]).backward(x, x)):
         with pytest.raises(lmoe.LmoeError):
             bad()
+
+
+def test_weight_gradient_of_many_rows(dev):
+    """An fp32 dw does not lose precision with the number of rows.  The MMA adds 16 rows at a time and
+    cuts off less than 2^-23 of what has been summed, 2^-24 on average; over the 512 rows that stay in
+    one accumulator, whose partial sums grow like the root of their number, that is
+    32 * 2/3 * 2^-24 = 1.3e-6 of the sum, to which the fp32 additions of the parts bring at most
+    8 * 2^-24.  2e-6 bounds both; 4096 rows in one accumulator would be 4e-6 off."""
+    M, N, K = 4096, 2048, 1024
+    x, dy = _draw(dev, M, K, 1), _draw(dev, M, N, 2)
+    lin = lmoe.Linear(_draw(dev, N, K, 3, K ** -0.5))
+    want = dy.double().T @ x.double()
+    for g in (lin.backward(x, dy), lin.backward(x, dy, want_dx=False)):
+        assert (g["dw"].double() - want).norm() <= 2e-6 * want.norm()
