@@ -565,7 +565,7 @@ int lmoe_linear_forward(const lmoe_linear *p, void *stream);
  * The residual's gradient is dy.  Any of dx, dw, dbias may be NULL (not wanted).  bf16 layers
  * only.  ws: lmoe_linear_backward_workspace_bytes(p) of device scratch, 16-byte aligned; not
  * needed when act is LMOE_ACT_NONE and dbias is NULL.  M == 0 zeroes dw and dbias.  Alignment as
- * above; dw rows are K apart.
+ * above; dw rows are K apart.  Outputs overlap no input, nor each other.
  * Errors: INVALID_ARG, UNSUPPORTED (also LMOE_E4M3), WORKSPACE_TOO_SMALL, CUDA. */
 size_t lmoe_linear_backward_workspace_bytes(const lmoe_linear *p);
 int lmoe_linear_backward(const lmoe_linear *p, const void *dy, long long lddy, void *dx,

@@ -234,7 +234,10 @@ int lmoe_linear_backward(const lmoe_linear* p, const void* dy, long long lddy, v
   if (lddy < p->N || lddy % 8 || (dx && (lddx < p->K || lddx % 8)) ||
       (act && (p->ldp < rows || p->ldp % 8)))
     return LMOE_ERR_INVALID_ARG;
-  if (dx && (dx == dy || dx == p->x || dx == p->w)) return LMOE_ERR_INVALID_ARG;
+  for (const void* out : {static_cast<const void*>(dx), static_cast<const void*>(dw)})
+    if (out && (out == dy || out == p->x || out == p->w || (act && out == p->pre)))
+      return LMOE_ERR_INVALID_ARG;
+  if (dx && dx == dw) return LMOE_ERR_INVALID_ARG;
   const LinearBwdLayout L = linear_bwd_layout(*p);
   const bool need_ws = act || dbias;
   if (need_ws && (!ws || !al16(ws))) return LMOE_ERR_INVALID_ARG;

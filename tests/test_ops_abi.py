@@ -152,6 +152,8 @@ def test_linear_backward_sizes(lib, change, code):
     ({}, dict(dx=BUF["dx"] + 8), ARG), ({}, dict(dw=BUF["dw"] + 4), ARG),
     ({}, dict(dbias=BUF["dbias"] + 4), ARG), ({}, dict(type=lmoe.E4M3), ARG),
     ({}, dict(dx=BUF["dy"]), ARG), ({}, dict(dx=BUF["x"]), ARG), ({}, dict(dx=BUF["w"]), ARG),
+    ({}, dict(dw=BUF["dy"]), ARG), ({}, dict(dw=BUF["x"]), ARG), ({}, dict(dw=BUF["w"]), ARG),
+    ({}, dict(dw=BUF["dx"]), ARG), (SITU, dict(dw=BUF["pre"]), ARG), (SITU, dict(dx=BUF["pre"]), ARG),
     (dict(x=None), {}, ARG), (dict(w=None), {}, ARG), (dict(dev_flag=None), {}, ARG),
     (dict(**SITU, pre=None), {}, ARG), (dict(**SITU, ldp=64), {}, ARG),
     (dict(**SITU, pre=BUF["pre"] + 8), {}, ARG),
