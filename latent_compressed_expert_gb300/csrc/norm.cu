@@ -18,6 +18,7 @@ namespace lmoe {
 
 constexpr int NORM_MAX_THREADS = 1024;     // of a block whose threads hold one vector each
 constexpr int NORM_MAX_THREADS4 = 512;     // ... four vectors each
+constexpr int NORM_BOUND4 = 576;           // 65536 / (2 * 576) registers: 56
 constexpr int NORM_BLOCK = 256;            // threads of a block that holds several short rows
 constexpr float NORM_E4M3_MAX = 448.0f;
 
@@ -147,10 +148,12 @@ __device__ __forceinline__ void norm_store8(const NormArgs& a, int64_t row, int 
 // vectors i, i + tpr, ...; a block holds blockDim / tpr rows.  NV vectors per thread: 4 for
 // throughput (128 bytes of loads in flight per thread), 1 when there are few rows, where the
 // time is one load's latency and a reduction over as many warps as a row can use.
-// Measured: 8192 rows of 7168, bf16 71.5 us (6.6 TB/s, the rate of a copy), e4m3 71.5 us (5.8 TB/s:
+// Measured: 8192 rows of 7168, bf16 71.5 us (6.6 TB/s, the rate of a copy), e4m3 67.4 us (6.1 TB/s:
 // the second reduction, of amax, leaves HBM idle); 65536 rows of 512 42.9 us; one row 2.7 us.
+// NORM_BOUND4 keeps the registers to 56, which lets five blocks of a 7168-wide row share an SM
+// (e4m3 takes 60 left to itself: four blocks, 71.5 us; 48 spill: 99 us).
 template <int NV, bool FP8>
-__global__ void __launch_bounds__(NV == 1 ? NORM_MAX_THREADS : NORM_MAX_THREADS4)
+__global__ void __launch_bounds__(NV == 1 ? NORM_MAX_THREADS : NORM_BOUND4, NV == 1 ? 1 : 2)
 add_rmsnorm_kernel(const NormArgs a) {
   __shared__ float red[2][32];
   pdl_wait();
