@@ -1,4 +1,6 @@
-// act.cuh -- the activations of the linear layers and their slopes, in fp32.
+// act.cuh -- the activations of the linear layers and their slopes, in fp32.  A NaN stays one (no
+// fmin or fmax, which return the other operand), and infinities give what the formulas give: an
+// exponential that overflows makes __fdividef's quotient 0, which is the limit.
 #pragma once
 
 #include "common.cuh"
@@ -16,11 +18,11 @@ __device__ __forceinline__ float soft_cap(float x, float c, float inv_c) {
     p = fmaf(q, p, -1.0f / 3.0f);
     return fmaf(x * q, p, x);
   }
-  return c * (1.0f - __fdividef(2.0f, 1.0f + __expf(fminf(2.0f * r, 80.0f))));
+  return c * (1.0f - __fdividef(2.0f, 1.0f + __expf(2.0f * r)));
 }
 
 __device__ __forceinline__ float sigmoid_of(float x) {
-  return __fdividef(1.0f, 1.0f + __expf(fminf(-x, 80.0f)));
+  return __fdividef(1.0f, 1.0f + __expf(-x));
 }
 
 // SiTU-GLU of a gate and a value pre-activation.

@@ -297,3 +297,37 @@ def test_refusals(dev):
     with pytest.raises(ValueError):
         wl.forward_few(synth.make_x(wide, seed=1, device=dev, T=8))
     wl.forward_few(synth.make_x(wide, seed=1, device=dev, T=2))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_nan(dev, fp8):
+    """NaN in a token, in an expert's weights and in a shared expert's: the outputs that depend on
+    them are NaN, as Layer.forward's are, and no others."""
+    sh = H.mid_shape(8)
+    clean = synth.make_weights(sh, seed=1, device=dev)
+    x = synth.make_x(sh, seed=3, device=dev, T=3)
+    # routing given: tokens 0 and 2 share expert 5
+    logits = torch.full((3, sh.E), -8.0, device=dev)
+    logits[0, 0:8] = logits[1, 8:16] = logits[2, 5:13] = 1.0
+    nan = float("nan")
+    layer = lmoe.Layer(sh, clean, max_tokens=8, expert_fp8=fp8)
+    base = layer.forward_few(x, logits_in=logits)
+    assert torch.isfinite(base.float()).all()
+    bad = x.clone()
+    bad[1, 7] = nan
+    cases = [(clean, bad, [1])]
+    for name, at, tokens in (("w_gate", (5, 3, 9), [0, 2]), ("w_value", (9, 3, 9), [1, 2]),
+                             ("w_sgate", (1, 3, 9), [0, 1, 2]),
+                             ("w_svalue", (0, 3, 9), [0, 1, 2])):
+        w = dict(clean)
+        w[name] = clean[name].clone()
+        w[name][at] = nan
+        cases.append((w, x, tokens))
+    for i, (w, xi, tokens) in enumerate(cases):
+        layer = lmoe.Layer(sh, w, max_tokens=8, expert_fp8=fp8)
+        y = layer.forward_few(xi, logits_in=logits)
+        full = layer.forward(xi, logits_in=logits, balance=False)
+        assert torch.isnan(full[tokens].float()).all(), i
+        assert torch.isnan(y[tokens].float()).all(), i
+        others = [t for t in range(3) if t not in tokens]
+        assert torch.equal(y[others], base[others]), i

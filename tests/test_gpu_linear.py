@@ -366,3 +366,102 @@ def test_weight_gradient_of_many_rows(dev):
     want = dy.double().T @ x.double()
     for g in (lin.backward(x, dy), lin.backward(x, dy, want_dx=False)):
         assert (g["dw"].double() - want).norm() <= 2e-6 * want.norm()
+
+
+def _within_or_nan(got, want, bound, tag):
+    """_within, and NaN exactly where the formula gives it."""
+    nan = want.isnan()
+    assert torch.equal(got.isnan(), nan), (tag, int(got.isnan().sum()), int(nan.sum()))
+    ok = want.isinf() & (got.double() == want) | nan
+    _within(got.double().masked_fill(ok, 0), want.masked_fill(ok, 0), bound.masked_fill(ok, 0), tag)
+
+
+@pytest.mark.parametrize("M", [5, 2050])
+@pytest.mark.parametrize("act", ["none", "silu", "gelu", "situ"])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_forward_of_nan_and_infinities(dev, M, act, fp8):
+    """Rows with a NaN or an infinity give what the formulas give, others are not touched."""
+    N, K = 264, 272
+    rows = 2 * N if act == "situ" else N
+    w, x, xs, ws = _draw(dev, rows, K, 1, K ** -0.5).contiguous(), _draw(dev, M, K, 2).clone(), None, None
+    clean = x.clone()
+    if fp8:  # codes have a NaN and no infinity
+        (w, ws), (x, xs) = _codes(w), _codes(x)
+        clean = x.clone()
+        x[1, 3] = 0x7f
+    else:
+        x[1, 3], x[2, 0], x[3, K - 1] = float("nan"), float("inf"), -float("inf")
+    lin = lmoe.Linear(w, torch.randn(rows, device=dev), act, w_scales=ws)
+    w64 = w.view(E4M3).double() * ws.double()[:, None] if fp8 else w.double()
+    x64 = x.view(E4M3).double() * xs.double()[:, None] if fp8 else x.double()
+    p = (x64[1:4, None] * w64).sum(2) + lin.bias.double()
+    y64, _ = _act64(p, act, 100.0)
+    y, pre = lin.forward(x, x_scales=xs, train=True)
+    want = lin.forward(clean, x_scales=xs)
+    keep = [i for i in range(M) if i not in (1, 2, 3)]
+    assert torch.equal(y[keep], want[keep])
+    # finite results here: capped gates and values, 2^-8 of themselves; and, of e4m3 rows, sums as at
+    # the head of this file
+    e = K * 2.0 ** -23 * (x64[1:4].nan_to_num(0, 0, 0).abs() @ w64.abs().T)
+    if act == "situ":
+        e = (e[:, :N] + e[:, N:]) * 113.0
+    _within_or_nan(y[1:4], y64, (HALF + 2 * FN) * y64.abs() + 1.2 * e, ("y", act))
+    if pre is not None:
+        e = K * 2.0 ** -23 * (x64[1:4].nan_to_num(0, 0, 0).abs() @ w64.abs().T)
+        _within_or_nan(pre[1:4], p, HALF * p.abs() + 1.01 * e, ("pre", act))
+
+
+@pytest.mark.parametrize("M", [40, 300])
+@pytest.mark.parametrize("act", ["silu", "gelu", "situ"])
+def test_backward_of_nan_and_infinities(dev, M, act):
+    """NaN, infinite and huge pre-activations: gradients as the formulas give them, in the rows and
+    features that they belong to."""
+    N, K = 64, 72
+    rows = 2 * N if act == "situ" else N
+    lin = lmoe.Linear(_draw(dev, rows, K, 1, K ** -0.5), torch.zeros(rows, device=dev), act)
+    x, dy, pre = _draw(dev, M, K, 2), _draw(dev, M, N, 3), _draw(dev, M, rows, 4).clone()
+    pre[7, 5], pre[9, 11], pre[12, 13] = float("nan"), float("inf"), -float("inf")
+    pre[20, 3], pre[21, 4] = 1e38, -1e38
+    if act == "situ":
+        pre[15, N + 20], pre[16, N + 21] = float("nan"), -float("inf")
+    dp, mag = _slope64(pre.double(), dy.double(), act, 100.0)
+    assert dp.isnan().any() and not dp.isinf().any()
+    ed = FN * mag
+    edp = ed + HALF * dp.abs()
+    x64, w64 = x.double(), lin.w.double()
+    g = lin.backward(x, dy, pre)
+    dx64, dw64 = dp @ w64, dp.T @ x64
+    _within_or_nan(g["dx"], dx64, HALF * dx64.abs() + 1.02 * (
+        edp @ w64.abs() + rows * 2.0 ** -23 * (dp.abs() @ w64.abs())), ("dx", act))
+    _within_or_nan(g["dw"], dw64, 2.0 ** -24 * dw64.abs() + 1.02 * (
+        edp.T @ x64.abs() + M * 2.0 ** -23 * (dp.abs().T @ x64.abs())), ("dw", act))
+    _within_or_nan(g["dbias"], dp.sum(0), ed.sum(0) + 512 * 2.0 ** -24 * dp.abs().sum(0),
+                   ("dbias", act))
+
+
+@pytest.mark.parametrize("act", ["silu", "situ"])
+def test_far_below_zero(dev, act):
+    """Finite pre-activations far below zero, where the logistic function is nothing: identity
+    weights bring them through the product exactly."""
+    N = 64
+    rows = 2 * N if act == "situ" else N
+    values = torch.tensor([-1e38, -3e36, -1e30, -1e5, -200.0, -120.0, -90.0, -60.0, 90.0, 1e38])
+    x = torch.ones(10, 64, dtype=BF, device=dev)
+    x[:, 1] = values.to(dev)
+    w = torch.zeros(rows, 64, dtype=BF, device=dev)
+    w[0, 1] = 1.0
+    if act == "situ":
+        w[N, 0] = 1.0
+    lin = lmoe.Linear(w, act=act)
+    y, pre = _check_forward(lin, x, tag=act)
+    dy = torch.ones(10, N, dtype=BF, device=dev)
+    dp, mag = _slope64(pre.double(), dy.double(), act, 100.0)
+    edp = FN * mag + HALF * dp.abs()
+    x64, w64 = x.double(), w.double()
+    g = lin.backward(x, dy, pre)
+    _within_or_nan(g["dx"], dp @ w64, HALF * (dp @ w64).abs() + 1.02 * (
+        edp @ w64.abs() + rows * 2.0 ** -23 * (dp.abs() @ w64.abs())), ("dx", act))
+    # some products of gradients and 1e38 pass fp32's range: infinities of their sign
+    dw64 = (dp.T @ x64).float().double()
+    _within_or_nan(g["dw"], dw64, 2.0 ** -24 * dw64.abs() + 1.02 * (
+        edp.T @ x64.abs() + 10 * 2.0 ** -23 * (dp.abs().T @ x64.abs())), ("dw", act))
