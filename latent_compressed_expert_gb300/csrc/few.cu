@@ -114,7 +114,7 @@ struct FewTables {
   float red[FEW_RED][FEW_WARPS][16 * 8];        // partial tiles, units in turn
   int32_t expert[FEW_MAX_PAIRS];            // the used experts, in order of first use
   int16_t pair[FEW_MAX_PAIRS][FEW_T];       // pair t K + j of token t with that expert, or -1
-  alignas(8) float gate[FEW_MAX_PAIRS][FEW_T];  // its gate, or 0 (e4m3, DOWN: times h's scale)
+  alignas(8) float gate[FEW_MAX_PAIRS][FEW_T];  // its gate, or -1 (e4m3, DOWN: times h's scale)
   alignas(16) int32_t sel[FEW_MAX_PAIRS];   // expert and gate of every pair
   float sel_gate[FEW_MAX_PAIRS];
   int16_t rank[FEW_MAX_PAIRS];              // place in `expert` of a pair that is its first use
@@ -873,7 +873,7 @@ struct Few : FewPlan<FP8> {
         }
         const Row r = token_row(mine ? s->pair[rank][lane & 7] : -1, pitch);
         const float2 f = mine ? *reinterpret_cast<const float2*>(&s->gate[rank][t2])
-                              : make_float2(0.0f, 0.0f);
+                              : make_float2(-1.0f, -1.0f);
         Acc acc;
         for (int k = 0; k < nk; k += nb) {
           const int c = k + kw;
@@ -883,11 +883,16 @@ struct Few : FewPlan<FP8> {
           release();
           multiply<FP8>(bx, tk, acc);
         }
-        // times the tokens' gates (e4m3: and both scales)
-        sum[0] = fmaf(acc.sum(0), f.x * w.x, sum[0]);
-        sum[1] = fmaf(acc.sum(1), f.y * w.x, sum[1]);
-        sum[2] = fmaf(acc.sum(2), f.x * w.y, sum[2]);
-        sum[3] = fmaf(acc.sum(3), f.y * w.y, sum[3]);
+        // times the tokens' gates (e4m3: and both scales).  A token without this expert is left out:
+        // its column is 0 times the weights, which is not 0 where they are not finite
+        if (!(f.x < 0.0f)) {
+          sum[0] = fmaf(acc.sum(0), f.x * w.x, sum[0]);
+          sum[2] = fmaf(acc.sum(2), f.x * w.y, sum[2]);
+        }
+        if (!(f.y < 0.0f)) {
+          sum[1] = fmaf(acc.sum(1), f.y * w.x, sum[1]);
+          sum[3] = fmaf(acc.sum(3), f.y * w.y, sum[3]);
+        }
       }
       join(sum);
     }
@@ -919,7 +924,7 @@ struct Few : FewPlan<FP8> {
   __device__ bool run() {
     for (int i = threadIdx.x; i < FEW_MAX_PAIRS * FEW_T; i += FEW_THREADS) {
       (&s->pair[0][0])[i] = -1;
-      (&s->gate[0][0])[i] = 0.0f;
+      (&s->gate[0][0])[i] = -1.0f;
     }
     for (int i = threadIdx.x; i < FEW_MAX_PAIRS; i += FEW_THREADS) s->sel[i] = -1;
     // u, for DOWN's additions (three barriers from here)

@@ -331,3 +331,27 @@ def test_nan(dev, fp8):
         assert torch.isnan(y[tokens].float()).all(), i
         others = [t for t in range(3) if t not in tokens]
         assert torch.equal(y[others], base[others]), i
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_an_expert_that_is_not_finite_spoils_its_own_tokens(dev, fp8, value):
+    """A NaN or an infinity in an expert's down projection reaches the tokens that use the expert and
+    no others of the batch, whether they share experts with those or not."""
+    sh = H.mid_shape(8)
+    w = synth.make_weights(sh, seed=1, device=dev)
+    x = synth.make_x(sh, seed=3, device=dev, T=3)
+    logits = torch.full((3, sh.E), -8.0, device=dev)
+    logits[0, 0:8] = logits[1, 8:16] = logits[2, 5:13] = 1.0
+    base = lmoe.Layer(sh, w, max_tokens=8, expert_fp8=fp8).forward_few(x, logits_in=logits)
+    for expert, tokens in ((0, [0]), (9, [1, 2])):
+        bad = dict(w)
+        bad["w_edown"] = w["w_edown"].clone()
+        bad["w_edown"][expert, 3, 9] = value
+        layer = lmoe.Layer(sh, bad, max_tokens=8, expert_fp8=fp8)
+        y = layer.forward_few(x, logits_in=logits)
+        full = layer.forward(x, logits_in=logits, balance=False)
+        others = [t for t in range(3) if t not in tokens]
+        assert torch.equal(y[others], base[others])
+        assert torch.equal(y[tokens].isnan(), full[tokens].isnan())
+        assert not torch.equal(y[tokens], base[tokens])
