@@ -579,8 +579,11 @@ class Linear:
 
     w [N, K] bf16, or e4m3 codes (uint8) with fp32 ``w_scales`` [N] (forward only); bias [N] fp32
     or None; act "none", "silu", "gelu" or "situ" (then w, bias and w_scales hold the N gate rows,
-    then the N value rows, and c is the cap).  The layer keeps references, not copies: an
-    optimizer may update w and bias in place.  N must be a multiple of 8, K of 8 (e4m3: 16)."""
+    then the N value rows, and c is the cap).  N must be a multiple of 8, K of 8 (e4m3: 16).
+
+    The layer keeps references, not copies, and looks at them at each call: w, bias and w_scales may be
+    updated in place, given other storage or replaced by tensors of the same sizes and type, on the
+    same device; c may be changed, and bias taken away or added."""
 
     def __init__(self, w: torch.Tensor, bias: torch.Tensor | None = None, act: str = "none",
                  w_scales: torch.Tensor | None = None, c: float = 100.0):
@@ -592,22 +595,37 @@ class Linear:
         self.fp8 = w.dtype is torch.uint8
         if self.fp8 != (w_scales is not None):
             raise ValueError("lmoe: e4m3 codes (uint8) and w_scales go together")
-        self.w, self.bias, self.w_scales, self.act, self.c = w, bias, w_scales, act, c
+        self.w, self.bias, self.w_scales, self._act, self.c = w, bias, w_scales, act, c
         self.rows, self.K, self.N = rows, K, rows // 2 if act == "situ" else rows
         self.device, self._dev = w.device, _device_of(w, "w")
         self._dtype = torch.uint8 if self.fp8 else torch.bfloat16
-        pw, ldw = _rows(w, self._dtype, rows, K, self._dev, "w")
-        pb = None if bias is None else _vector(bias, rows, self._dev, "bias")
-        pws = None if w_scales is None else _vector(w_scales, rows, self._dev, "w_scales")
+        self._sizes = (self.N, K, ACTS[act], E4M3 if self.fp8 else BF16)
+        self._weights()
         self.flag = torch.zeros(1, dtype=torch.int32, device=w.device)
         torch.cuda.current_stream(w.device).synchronize()  # before any stream of the caller's
-        self._sizes = (self.N, K, ACTS[act], E4M3 if self.fp8 else BF16, c)
-        self._weights = (pw, ldw, pws, pb)
         self._flag = self.flag.data_ptr()
 
+    @property
+    def act(self) -> str:
+        return self._act
+
+    def _weights(self):
+        """(w, its row distance, scales, bias) as they are now."""
+        pw, ldw = _rows(self.w, self._dtype, self.rows, self.K, self._dev, "w")
+        pws = pb = None
+        if self.fp8:
+            if self.w_scales is None:
+                raise ValueError("lmoe: e4m3 codes (uint8) and w_scales go together")
+            pws = _vector(self.w_scales, self.rows, self._dev, "w_scales")
+        elif self.w_scales is not None:
+            raise ValueError("lmoe: e4m3 codes (uint8) and w_scales go together")
+        if self.bias is not None:
+            pb = _vector(self.bias, self.rows, self._dev, "bias")
+        return pw, ldw, pws, pb
+
     def _desc(self, M, px, ldx, pxs, pr, ldr, py, ldy, pp, ldp):
-        return ctypes.byref(LinearDesc(M, *self._sizes, px, ldx, pxs, *self._weights, pr, ldr, py,
-                                       ldy, pp, ldp, self._flag))
+        return ctypes.byref(LinearDesc(M, *self._sizes, self.c, px, ldx, pxs, *self._weights(), pr,
+                                       ldr, py, ldy, pp, ldp, self._flag))
 
     def forward(self, x: torch.Tensor, residual: torch.Tensor | None = None,
                 x_scales: torch.Tensor | None = None, train: bool = False, y=None, stream=None):

@@ -465,3 +465,71 @@ def test_far_below_zero(dev, act):
     dw64 = (dp.T @ x64).float().double()
     _within_or_nan(g["dw"], dw64, 2.0 ** -24 * dw64.abs() + 1.02 * (
         edp.T @ x64.abs() + 10 * 2.0 ** -23 * (dp.abs().T @ x64.abs())), ("dw", act))
+
+
+def _pair(dev, rows, K, seed, fp8=False, ld=None):
+    """Weights (e4m3: with scales) and a bias."""
+    w = _draw(dev, rows, K, seed, K ** -0.5, ld=ld)
+    w, ws = _codes(w) if fp8 else (w, None)
+    return w, torch.randn(rows, device=dev), ws
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_weights_and_bias_replaced(dev, fp8):
+    """Tensors assigned to a layer, and storage that a tensor of it was given, are what the next call
+    computes with; what does not fit the layer is refused."""
+    N, K, M = 64, 80, 9
+    x, xs = (_codes(_draw(dev, M, K, 2)) if fp8 else (_draw(dev, M, K, 2), None))
+    w, b, ws = _pair(dev, N, K, 1, fp8)
+    lin = lmoe.Linear(w, b, "silu", w_scales=ws)
+    kept = [w, b, ws]
+
+    def fresh():
+        return lmoe.Linear(lin.w.clone(), None if lin.bias is None else lin.bias.clone(), "silu",
+                           w_scales=None if ws is None else lin.w_scales.clone())
+
+    def check():
+        y, pre = lin.forward(x, x_scales=xs, train=True)
+        want, _ = fresh().forward(x, x_scales=xs, train=True)
+        assert torch.equal(y, want)
+        if not fp8:
+            dy = _draw(dev, M, N, 5)
+            got, want = lin.backward(x, dy, pre), fresh().backward(x, dy, pre)
+            assert all((got[n] is None) == (want[n] is None) and
+                       (got[n] is None or torch.equal(got[n], want[n])) for n in want)
+
+    check()
+    lin.w, lin.bias, lin.w_scales = _pair(dev, N, K, 3, fp8, ld=None if fp8 else K + 16)
+    check()
+    kept += [lin.w, lin.bias, lin.w_scales]
+    new = _pair(dev, N, K, 4, fp8)
+    kept += [lin.w.data, lin.bias.data]
+    lin.w.data, lin.bias.data = new[0], new[1]
+    if fp8:
+        kept.append(lin.w_scales.data)
+        lin.w_scales.data = new[2]
+    check()
+    lin.bias = None
+    check()
+    lin.bias = new[1]
+    check()
+    for bad in (dict(w=new[0][:32]), dict(w=new[0].float()), dict(w=new[0].cpu()),
+                dict(bias=new[1][:32]), dict(bias=new[1].to(BF)),
+                dict(w_scales=None if fp8 else new[1]), dict(w_scales=new[1][:32])):
+        was = {n: getattr(lin, n) for n in bad}
+        for n, t in bad.items():
+            setattr(lin, n, t)
+        with pytest.raises(ValueError):
+            lin.forward(x, x_scales=xs)
+        for n, t in was.items():
+            setattr(lin, n, t)
+    check()
+
+
+def test_cap_changed_and_activation_fixed(dev):
+    lin = lmoe.Linear(_draw(dev, 128, 64, 1, 1 / 8), act="situ", c=100.0)
+    x = _draw(dev, 9, 64, 2, 30.0)
+    lin.c = 2.0
+    assert torch.equal(lin.forward(x), lmoe.Linear(lin.w, act="situ", c=2.0).forward(x))
+    with pytest.raises(AttributeError):
+        lin.act = "none"
