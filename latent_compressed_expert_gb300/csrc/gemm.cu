@@ -28,7 +28,6 @@
 // its in-flight copies and MMAs, and the CTA frees its TMEM and exits.
 #include <cudaTypedefs.h>
 
-#include <mutex>
 
 #include "common.cuh"
 #include "kernels.cuh"
@@ -778,18 +777,31 @@ __global__ void __launch_bounds__(256) splitk_reduce_kernel(const GemmArgs g) {
 // ------------------------------------------------------------------------------------
 // host side
 // ------------------------------------------------------------------------------------
+template <typename F>
+static F driver_entry(const char* name, int version) {
+  void* p = nullptr;
+  cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+  const bool ok = cudaGetDriverEntryPointByVersion(name, &p, version, cudaEnableDefault, &q) ==
+                      cudaSuccess && q == cudaDriverEntryPointSuccess;
+  return ok ? reinterpret_cast<F>(p) : nullptr;
+}
+
+// Encoding needs a current context, which a host thread that has made no launch or allocation yet
+// lacks (asking for the device and its attributes makes none current): its device's primary one then.
+static bool context_current() {
+  static const auto current = driver_entry<CUresult (*)(CUcontext*)>("cuCtxGetCurrent", 4000);
+  CUcontext ctx = nullptr;
+  if (!current) return false;
+  if (current(&ctx) == CUDA_SUCCESS && ctx) return true;
+  int dev = 0;
+  return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess;
+}
+
+// null: not to be had
 static PFN_cuTensorMapEncodeTiled_v12000 tmap_encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  });
-  return fn;
+  static const auto fn =
+      driver_entry<PFN_cuTensorMapEncodeTiled_v12000>("cuTensorMapEncodeTiled", 12000);
+  return fn && context_current() ? fn : nullptr;
 }
 
 // fp32 output of `groups` row-major [rows, cols] matrices (row stride ld, group stride gstride

@@ -96,3 +96,38 @@ def test_decode_agrees_with_the_prompt(ex):
     got = torch.cat([block.decode(x[i:i + 8]) for i in range(0, shape.T, 8)])
     err = (got.double() - out.double()).abs().sum() / out.double().abs().sum()
     assert err <= 2 * 5e-3
+
+
+def test_first_call_of_a_host_thread(ex):
+    """Calls from host threads that have used no GPU yet, with their outputs already allocated."""
+    import ctypes
+    import threading
+
+    dev = torch.device("cuda:0")
+    lib, stream = lmoe.load(), torch.cuda.current_stream().cuda_stream
+    layer = lmoe.Layer(synth.TINY, synth.make_weights(synth.TINY, seed=0, device=dev), max_tokens=8)
+    x = synth.make_x(synth.TINY, seed=1, device=dev, T=2)
+    y = torch.empty_like(x)
+    want = layer.forward_few(x)
+    calls = [(lambda: lib.lmoe_forward_few(
+        ctypes.byref(layer._few_dims[2]), layer.packed.data_ptr(), x.data_ptr(), None, y.data_ptr(),
+        layer.few_ws.data_ptr(), layer.few_ws.numel(), None, stream), y, want)]
+    for M in (3, 9000):  # a cluster's tile, SM pairs
+        xl = torch.randn(M, 256, device=dev).bfloat16()
+        lin = lmoe.Linear(torch.randn(2048, 256, device=dev).bfloat16())
+        out, ref = torch.empty(M, 2048, dtype=torch.bfloat16, device=dev), lin.forward(xl)
+        d = lin._desc(M, xl.data_ptr(), 256, None, None, 0, out.data_ptr(), 2048, None, 0)
+        calls.append((lambda d=d, keep=(lin, xl): lib.lmoe_linear_forward(d, stream), out, ref))
+        dx, back = torch.empty_like(xl), lin.backward(xl, ref, want_dw=False)["dx"]
+        b = lin._desc(M, xl.data_ptr(), 256, None, None, 0, None, 0, None, 0)
+        calls.append((lambda b=b, r=ref, o=dx: lib.lmoe_linear_backward(
+            b, r.data_ptr(), 2048, o.data_ptr(), 256, None, 0, None, None, 0, stream), dx, back))
+    torch.cuda.synchronize()
+    for call, out, ref in calls:
+        codes = []
+        t = threading.Thread(target=lambda: codes.append(call()))
+        t.start()
+        t.join()
+        torch.cuda.synchronize()
+        assert codes == [lmoe.LMOE_OK]
+        assert torch.equal(out, ref)
