@@ -509,12 +509,19 @@ int lmoe_add_rmsnorm(const void *x, long long ldx, const void *residual, long lo
  *   dx [rows, cols] bf16 out (it may be dy or dtotal itself), dgamma [cols] fp32 out, or NULL
  *   (not wanted; ws is then unused); ws: lmoe_add_rmsnorm_backward_workspace_bytes of device
  *   scratch, 16-byte aligned.  Strides, widths and alignment as above.  rows == 0 sets dgamma to 0.
+ * Should a device-side wait run out, lmoe_norm_last_device_error says so, and the rows of dx that
+ * were left, and dgamma, are NaN.
  * Errors: INVALID_ARG, UNSUPPORTED (rows >= 2^31, cols > 2^30), WORKSPACE_TOO_SMALL, CUDA. */
 size_t lmoe_add_rmsnorm_backward_workspace_bytes(long long rows, int cols);
 int lmoe_add_rmsnorm_backward(const void *dy, long long ldy, const void *total, long long ldt,
                               const float *gamma, const float *rstd, const void *dtotal,
                               long long ldd, long long rows, int cols, void *dx, long long ldx,
                               float *dgamma, void *ws, size_t ws_bytes, void *stream);
+
+/* lmoe_last_device_error for lmoe_add_rmsnorm_backward, which has no word of the caller's: reads and
+ * clears one that the library keeps on each device (the current one's).  Call after the streams of
+ * its calls have synchronised. */
+int lmoe_norm_last_device_error(void);
 
 /* Linear layers with a fused epilogue, for the dense projections around the layer ([IK3]
  * baseline decoder passage: the dense FFN that the experts replace, and the block's other

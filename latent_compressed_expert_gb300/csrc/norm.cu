@@ -80,15 +80,6 @@ __device__ __forceinline__ float row_reduce(float v, float* red, int tpr) {
   return v;
 }
 
-// The same with a barrier always (a block that holds one row).
-template <typename OP>
-__device__ __forceinline__ float row_reduce_sync(float v, float* red, int tpr) {
-  if (tpr > 32) return row_reduce<OP>(v, red, tpr);
-  v = row_reduce<OP>(v, red, tpr);
-  __syncthreads();
-  return v;
-}
-
 // Correctly rounded quotients by one divisor: with r = 1 / s and q = x r, both rounded, and the
 // exact remainder of q, q + (x - q s) r rounds to x / s (Markstein, IBM J. Res. Dev. 34, 1990).  Three
 // operations instead of a division's ten, which made the e4m3 kernels issue-bound.  Where 1 / s or
@@ -319,6 +310,8 @@ struct NormBwdArgs {
   int64_t ldy, ldt, ldd, ldx;
   int64_t rows;
   int cols;
+  unsigned long long timeout_ns;  // of the streaming form's waits
+  int inject_stall;               // test hook: its first wait is for a barrier nobody arrives on
 };
 
 // dx of a row's vector, and what it adds to dgamma and to the row's dot product.
@@ -439,19 +432,22 @@ add_rmsnorm_bwd_kernel(const NormBwdArgs a, int tpr) {
 // copies while it computes, since the registers of its dgamma leave no room for loads ahead.  (The
 // forward, whose blocks are many and hold no such sums, is faster without.)  7168 columns: 2 blocks
 // of 2 stages per SM.  Measured: 8192 rows of 7168 80 us with the column sum (5.9 TB/s; the kernel
-// above 93 us).
+// above 93 us; cp.async by each thread for itself, which needs no barrier, 91 us).
+// A wait that runs out sets norm_error; its block then waits for its copies in flight and makes the
+// rows that it has left and its share of dgamma NaN, so that nobody takes them for gradients.
 constexpr int NORM_STAGES = 4;
 constexpr int NORM_STREAM_ROW = 4096;  // bytes of a row from which this form is used
 constexpr int NORM_STREAM_SMEM = 110 * 1024;  // of a block, two of which share an SM
 constexpr int NORM_STREAM_THREADS = 448;
-constexpr unsigned long long NORM_WAIT_NS = 2000000000ull;
+__device__ uint32_t norm_error;  // of the calls on this device, which have no word of their own
 
 __global__ void __launch_bounds__(NORM_STREAM_THREADS, 2)
 add_rmsnorm_bwd_stream_kernel(const NormBwdArgs a, int stages) {
   constexpr int NV = 2;
   extern __shared__ __align__(16) uint8_t ring[];
-  __shared__ uint64_t full[NORM_STAGES];
+  __shared__ uint64_t full[NORM_STAGES], nobody;
   __shared__ float red[2][32];
+  __shared__ volatile int late[2];  // by rows in turn: a thread's wait for the row has run out
   pdl_wait();
   pdl_launch_dependents();
   const int tpr = blockDim.x, t = threadIdx.x, nvec = a.cols >> 3, bytes = a.cols * 2;
@@ -459,6 +455,8 @@ add_rmsnorm_bwd_stream_kernel(const NormBwdArgs a, int stages) {
   const float inv_n = __fdiv_rn(1.0f, static_cast<float>(a.cols));
   if (t == 0) {
     for (int i = 0; i < stages; ++i) ptx::mbar_init(&full[i], 1);
+    ptx::mbar_init(&nobody, 1);
+    late[0] = late[1] = 0;
     ptx::fence_mbar_init();
   }
   __syncthreads();
@@ -480,11 +478,18 @@ add_rmsnorm_bwd_stream_kernel(const NormBwdArgs a, int stages) {
     for (int k = 0; k < 8; ++k) acc[i][k] = 0.0f;
   int stage = 0, flip = 0;
   uint32_t parity = 0;
-  for (int64_t row = blockIdx.x; row < a.rows; row += step, flip ^= 1) {
-    const float rstd = __ldg(a.rstd + row);
+  auto landed = [&](uint64_t* bar, uint32_t phase) {
+    if (ptx::mbar_try_wait(bar, phase)) return true;
     const uint64_t t0 = ptx::globaltimer_ns();
-    while (!ptx::mbar_try_wait(&full[stage], parity))  // a copy's own time; bounded all the same
-      if (ptx::globaltimer_ns() - t0 > NORM_WAIT_NS) break;
+    while (!ptx::mbar_try_wait(bar, phase))
+      if (ptx::globaltimer_ns() - t0 > a.timeout_ns) return false;
+    return true;
+  };
+  int64_t row = blockIdx.x;
+  for (; row < a.rows; row += step, flip ^= 1) {
+    const float rstd = __ldg(a.rstd + row);
+    const bool stall = a.inject_stall && row == blockIdx.x;
+    if (!landed(stall ? &nobody : &full[stage], parity)) late[flip] = 1;
     const uint8_t* base = ring + stage * ops * bytes;
     uint4 dv[NV], tv[NV], ev[NV];
     float dot = 0.0f;
@@ -501,7 +506,8 @@ add_rmsnorm_bwd_stream_kernel(const NormBwdArgs a, int stages) {
         dot = norm_bwd_dot8(dv[i], tv[i], g, rstd, dot, acc[i]);
       }
     }
-    dot = row_reduce_sync<RowSum>(dot, red[flip], tpr) * inv_n;
+    dot = row_reduce<RowSum>(dot, red[flip], tpr) * inv_n;  // (at least 128 threads: one barrier)
+    if (late[flip]) break;  // what it says here, it says to every thread
     if (t == 0) fetch(row + stages * step, stage);  // past that barrier the stage has been read
     uint4* o = reinterpret_cast<uint4*>(a.dx + row * a.ldx);
 #pragma unroll
@@ -514,6 +520,22 @@ add_rmsnorm_bwd_stream_kernel(const NormBwdArgs a, int stages) {
       }
     }
     if (++stage == stages) stage = 0, parity ^= 1u;
+  }
+  if (row < a.rows) {
+    if (t == 0) {
+      atomicOr(&norm_error, DEVERR_TIMEOUT_PRODUCER);
+      for (int i = 0; i < stages && row + i * step < a.rows; ++i) {
+        if (!landed(&full[stage], parity)) atomicOr(&norm_error, DEVERR_TIMEOUT_DRAIN);
+        if (++stage == stages) stage = 0, parity ^= 1u;
+      }
+    }
+    const uint4 nan = make_uint4(~0u, ~0u, ~0u, ~0u);
+    for (; row < a.rows; row += step)
+      for (int v = t; v < nvec; v += tpr) reinterpret_cast<uint4*>(a.dx + row * a.ldx)[v] = nan;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) acc[i][k] = __uint_as_float(~0u);
   }
   if (!a.part) return;
   float4* p = reinterpret_cast<float4*>(a.part + static_cast<int64_t>(blockIdx.x) * a.cols);
@@ -735,7 +757,15 @@ int lmoe_add_rmsnorm_backward(const void* dy, long long ldy, const void* total, 
   a.ldx = ldx;
   a.rows = rows;
   a.cols = cols;
+  a.timeout_ns = wait_limit_ns();
+  a.inject_stall = inject_stall();
   return launch_add_rmsnorm_bwd(a, dgamma, st);
+}
+
+int lmoe_norm_last_device_error(void) {
+  void* word = nullptr;
+  return cudaGetSymbolAddress(&word, norm_error) == cudaSuccess ? lmoe_last_device_error(word)
+                                                                 : LMOE_ERR_CUDA;
 }
 
 }  // extern "C"

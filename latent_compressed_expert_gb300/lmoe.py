@@ -110,6 +110,7 @@ SIGNATURES = {
     "lmoe_add_rmsnorm_backward_workspace_bytes": (_sz, [_ll, _i]),
     "lmoe_add_rmsnorm_backward": (_i, [_vp, _ll, _vp, _ll, _vp, _vp, _vp, _ll, _ll, _i, _vp, _ll,
                                        _vp, _vp, _sz, _vp]),
+    "lmoe_norm_last_device_error": (_i, []),
     "lmoe_linear_forward": (_i, [_vp, _vp]),
     "lmoe_linear_backward_workspace_bytes": (_sz, [_vp]),
     "lmoe_linear_backward": (_i, [_vp, _vp, _ll, _vp, _ll, _vp, _i, _vp, _vp, _sz, _vp]),
@@ -543,7 +544,8 @@ def add_rmsnorm_backward(dy: torch.Tensor, total: torch.Tensor, gamma: torch.Ten
                          want_dgamma: bool = True, dx=None, stream=None):
     """Gradients of add_rmsnorm (lmoe_add_rmsnorm_backward): dy, and dtotal (the gradient that
     reaches total itself, or None), [rows, cols] bf16 -> (dx bf16, dgamma fp32 or None); dx is
-    the gradient of x and of residual."""
+    the gradient of x and of residual.  ``norm_device_error`` reports a device-side wait that ran
+    out (the gradients are then NaN)."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return add_rmsnorm_backward(dy, total, gamma, rstd, dtotal, want_dgamma, dx)
@@ -571,6 +573,12 @@ def add_rmsnorm_backward(dy: torch.Tensor, total: torch.Tensor, gamma: torch.Ten
     if rc:
         _check(rc, "lmoe_add_rmsnorm_backward")
     return dx, dgamma
+
+
+def norm_device_error() -> int:
+    """LMOE_OK, or LMOE_ERR_DEVICE_TIMEOUT if a device-side wait of an earlier add_rmsnorm_backward on
+    the current device ran out; call after its stream has synchronised.  Clears the word."""
+    return int(load().lmoe_norm_last_device_error())
 
 
 class Linear:

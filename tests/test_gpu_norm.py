@@ -269,3 +269,28 @@ def test_refusals(dev):
             bad()
     with pytest.raises(lmoe.LmoeError):
         lmoe.add_rmsnorm(x, gamma, eps=-1.0)
+
+
+@pytest.mark.parametrize("cols,with_dt", [(7168, True), (2048, False)])
+def test_stalled_wait_reports_timeout_and_recovers(dev, monkeypatch, cols, with_dt):
+    """A device-side wait that runs out (a barrier nothing arrives on): the call ends, it is reported,
+    no row passes for a gradient, and the next call is correct."""
+    rows = 2000
+    dy, total = _draw(dev, rows, cols, 1), _draw(dev, rows, cols, 2)
+    dt = _draw(dev, rows, cols, 3) if with_dt else None
+    gamma = torch.rand(cols, device=dev) + 0.5
+    rstd = (total.double().square().mean(1) + 1e-6).rsqrt().float()
+    want = lmoe.add_rmsnorm_backward(dy, total, gamma, rstd, dt)
+    torch.cuda.synchronize()
+    assert lmoe.norm_device_error() == lmoe.LMOE_OK
+    monkeypatch.setenv("LMOE_WAIT_LIMIT_MS", "100")
+    monkeypatch.setenv("LMOE_FAULT_INJECT", "stall")
+    dx, dg = lmoe.add_rmsnorm_backward(dy, total, gamma, rstd, dt)
+    torch.cuda.synchronize()
+    assert lmoe.norm_device_error() == lmoe.LMOE_ERR_DEVICE_TIMEOUT
+    assert lmoe.norm_device_error() == lmoe.LMOE_OK
+    assert torch.isnan(dx.float()).all() and torch.isnan(dg).all()
+    monkeypatch.delenv("LMOE_FAULT_INJECT")
+    monkeypatch.delenv("LMOE_WAIT_LIMIT_MS")
+    dx, dg = lmoe.add_rmsnorm_backward(dy, total, gamma, rstd, dt)
+    assert torch.equal(dx, want[0]) and torch.equal(dg, want[1])
