@@ -1190,7 +1190,8 @@ static FewLayout few_layout(const lmoe_dims& D) {
 struct FewSmem {
   int stages, more, top, out_pitch;
 };
-constexpr size_t FEW_SMEM_MAX = 232448 - 1024;  // less the alignment's slack
+constexpr int FEW_SMEM_LIMIT = 232448;                    // of an SM's only CTA
+constexpr size_t FEW_SMEM_MAX = FEW_SMEM_LIMIT - 1024;  // less the alignment's slack
 
 static FewSmem few_smem(const lmoe_dims& D) {
   const size_t T = D.T, sw = D.S > 0 ? static_cast<size_t>(D.S) * D.Is : 0;
@@ -1242,8 +1243,10 @@ template <bool FP8>
 static int launch_few(const FewMaps& maps, const FewArgs& a, int sms, size_t smem,
                       cudaStream_t stream) {
   auto kernel = few_kernel<FP8>;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(smem)) != cudaSuccess)
+  // the attribute is the kernel's, not the launch's: with this call's size, another host thread's
+  // smaller one could come between it and the launch
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, FEW_SMEM_LIMIT) !=
+      cudaSuccess)
     return LMOE_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(sms));

@@ -355,3 +355,40 @@ def test_an_expert_that_is_not_finite_spoils_its_own_tokens(dev, fp8, value):
         assert torch.equal(y[others], base[others])
         assert torch.equal(y[tokens].isnan(), full[tokens].isnan())
         assert not torch.equal(y[tokens], base[tokens])
+
+
+def test_two_threads_with_layers_of_different_sizes(dev):
+    """Calls of different batch sizes from two host threads, each on a workspace of its own and both
+    on one stream: every launch is accepted and every output right."""
+    import ctypes
+    import threading
+
+    sh = H.mid_shape(8)
+    w = synth.make_weights(sh, seed=1, device=dev)
+    work = []
+    for T in (1, 8):
+        layer = lmoe.Layer(sh, w, max_tokens=8)
+        x = synth.make_x(sh, seed=T, device=dev, T=T)
+        work.append((layer, x, layer.forward_few(x), torch.empty_like(x)))
+    torch.cuda.synchronize()
+    stream = torch.cuda.current_stream().cuda_stream
+    codes = [[], []]
+
+    def run(i):
+        layer, x, _, y = work[i]
+        lib, D = lmoe.load(), ctypes.byref(layer._few_dims[x.shape[0]])
+        args = [ctypes.c_void_p(t.data_ptr()) for t in (layer.packed, x)] + [None] + \
+            [ctypes.c_void_p(t.data_ptr()) for t in (y, layer.few_ws)]
+        for _ in range(4000):
+            codes[i].append(lib.lmoe_forward_few(D, *args, layer.few_ws.numel(), None, stream))
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert all(c == lmoe.LMOE_OK for part in codes for c in part), [
+        sum(c != 0 for c in part) for part in codes]
+    for layer, _, want, y in work:
+        assert torch.equal(y, want) and layer.few_device_error() == lmoe.LMOE_OK
