@@ -558,8 +558,8 @@ typedef struct lmoe_linear {
 } lmoe_linear;
 
 /* The layer's output y (and pre).  N a multiple of 8, K of 8 (16 for e4m3); x, w, residual, y and
- * pre 16-byte aligned with row distances in whole 16 bytes.  y and pre overlap no input (y may be
- * residual itself).  M == 0 is a no-op.
+ * pre 16-byte aligned with row distances in whole 16 bytes, the others 4-byte aligned.  y and pre
+ * overlap no input (y may be residual itself).  M == 0 is a no-op.
  * Errors: INVALID_ARG, UNSUPPORTED (N, K; M, K or rows above 2^30; above 2^27 tiles of 64 x 64),
  * CUDA. */
 int lmoe_linear_forward(const lmoe_linear *p, void *stream);

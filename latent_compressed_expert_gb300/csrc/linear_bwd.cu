@@ -230,7 +230,9 @@ int lmoe_linear_backward(const lmoe_linear* p, const void* dy, long long lddy, v
   const bool act = p->act != LMOE_ACT_NONE;
   if (!dy || (dx && !p->w) || (dw && !p->x) || (act && !p->pre) || !p->dev_flag)
     return LMOE_ERR_INVALID_ARG;
-  if (!al16(dy) || !al16(p->x) || !al16(p->w) || !al16(p->pre)) return LMOE_ERR_INVALID_ARG;
+  if (!al16(dy) || !al16(p->x) || !al16(p->w) || !al16(p->pre) ||
+      (reinterpret_cast<uintptr_t>(p->dev_flag) & 3u))
+    return LMOE_ERR_INVALID_ARG;
   if (lddy < p->N || lddy % 8 || (dx && (lddx < p->K || lddx % 8)) ||
       (act && (p->ldp < rows || p->ldp % 8)))
     return LMOE_ERR_INVALID_ARG;

@@ -199,6 +199,10 @@ extern "C" int lmoe_linear_forward(const lmoe_linear* p, void* stream) {
   const int64_t rows = p->act == LMOE_ACT_SITU ? 2 * static_cast<int64_t>(p->N) : p->N;
   if (!al16(p->x) || !al16(p->w) || !al16(p->y) || !al16(p->residual) || !al16(p->pre))
     return LMOE_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(p->bias) | reinterpret_cast<uintptr_t>(p->dev_flag) |
+       (fp8 ? reinterpret_cast<uintptr_t>(p->x_scales) | reinterpret_cast<uintptr_t>(p->w_scales)
+            : 0)) & 3u)
+    return LMOE_ERR_INVALID_ARG;
   if (p->ldy < p->N || p->ldy % 8 || (p->residual && (p->ldr < p->N || p->ldr % 8)) ||
       (p->pre && (p->ldp < rows || p->ldp % 8)))
     return LMOE_ERR_INVALID_ARG;

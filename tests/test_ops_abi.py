@@ -234,3 +234,16 @@ def test_bindings_refuse_cpu_tensors(lib):
         lmoe.Linear(w, act="relu")
     with pytest.raises(ValueError):
         lmoe.Linear(w, w_scales=torch.ones(64))
+
+
+@no_gpu
+@pytest.mark.parametrize("change", [
+    dict(bias=BUF["bias"] + 2), dict(dev_flag=BUF["flag"] + 1),
+    {**E4M3, "x_scales": BUF["x_scales"] + 2}, {**E4M3, "w_scales": BUF["w_scales"] + 1}])
+def test_linear_forward_refuses_misaligned_words(lib, change):
+    assert lib.lmoe_linear_forward(ctypes.byref(_desc(**change)), None) == ARG
+
+
+@no_gpu
+def test_linear_backward_refuses_a_misaligned_flag(lib):
+    assert _linear_bwd(lib, _desc(dev_flag=BUF["flag"] + 2)) == ARG
