@@ -489,7 +489,8 @@ enum lmoe_type {
  *     recipe of lmoe_quantize_e4m3 from the fp32 y;
  *   total [rows, cols] bf16 (rounded to nearest) and rstd [rows] fp32: outputs, or NULL.
  *   ld*: distance between rows in elements (>= cols), any value.  total may be x or residual
- *   itself, and so may a bf16 y; outputs must not overlap inputs in any other way, nor each other.
+ *   itself, at its row distance, and so may a bf16 y; outputs must not overlap inputs in any other
+ *   way, nor each other.
  * Any cols and any alignment to the element size are accepted; 16-byte-aligned rows (8 bytes for
  * codes) of a multiple of 8 columns, at most 16384, take the fast path.  A row that is not finite
  * gives what the formulas give.  rows == 0 is a no-op.
@@ -506,7 +507,7 @@ int lmoe_add_rmsnorm(const void *x, long long ldx, const void *residual, long lo
  *   dgamma = sum over the rows of dy * xh
  * in fp32, dgamma added in a fixed order.
  *   dy, total, dtotal (NULL: none) [rows, cols] bf16, gamma [cols] and rstd [rows] fp32 in;
- *   dx [rows, cols] bf16 out (it may be dy or dtotal itself), dgamma [cols] fp32 out, or NULL
+ *   dx [rows, cols] bf16 out (it may be dy or dtotal itself, at its row distance), dgamma [cols] fp32 out, or NULL
  *   (not wanted; ws is then unused); ws: lmoe_add_rmsnorm_backward_workspace_bytes of device
  *   scratch, 16-byte aligned.  Strides, widths and alignment as above.  rows == 0 sets dgamma to 0.
  * Should a device-side wait run out, lmoe_norm_last_device_error says so, and the rows of dx that
@@ -548,7 +549,8 @@ typedef struct lmoe_linear {
   const float *bias;      /* [rows] fp32, or NULL */
   const void *residual;   /* [M, N] bf16, rows ldr elements apart, or NULL */
   long long ldr;
-  void *y;                /* [M, N] bf16 out, rows ldy elements apart; may be residual itself */
+  void *y;                /* [M, N] bf16 out, rows ldy elements apart; may be residual itself,
+                             at its row distance */
   long long ldy;
   void *pre;              /* [M, rows] bf16: the pre-activations p, rounded, rows ldp elements
                              apart: written by the forward (NULL: not kept), read by the backward */
@@ -559,7 +561,7 @@ typedef struct lmoe_linear {
 
 /* The layer's output y (and pre).  N a multiple of 8, K of 8 (16 for e4m3); x, w, residual, y and
  * pre 16-byte aligned with row distances in whole 16 bytes, the others 4-byte aligned.  y and pre
- * overlap no input (y may be residual itself).  M == 0 is a no-op.
+ * overlap no input (y may be residual itself, at its row distance).  M == 0 is a no-op.
  * Errors: INVALID_ARG, UNSUPPORTED (N, K; M, K or rows above 2^30; above 2^27 tiles of 64 x 64),
  * CUDA. */
 int lmoe_linear_forward(const lmoe_linear *p, void *stream);

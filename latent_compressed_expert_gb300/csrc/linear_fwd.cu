@@ -207,6 +207,8 @@ extern "C" int lmoe_linear_forward(const lmoe_linear* p, void* stream) {
       (p->pre && (p->ldp < rows || p->ldp % 8)))
     return LMOE_ERR_INVALID_ARG;
   if (p->y == p->x || p->y == p->w) return LMOE_ERR_INVALID_ARG;
+  // y over the residual: the same rows, or a row would be written before another tile reads it
+  if (p->M > 1 && p->y == p->residual && p->ldy != p->ldr) return LMOE_ERR_INVALID_ARG;
   if (p->pre && (p->pre == p->y || p->pre == p->x || p->pre == p->w || p->pre == p->residual))
     return LMOE_ERR_INVALID_ARG;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -10,6 +10,8 @@
 //   dgamma = sum over rows of dy * xh
 // Every sum is fp32.  All of it is bound by HBM: each operand is read once and each result
 // written once; a row stays in registers between the reductions and the stores.
+#include <utility>
+
 #include "common.cuh"
 #include "kernels.cuh"
 #include "ptx.cuh"
@@ -694,6 +696,10 @@ int lmoe_add_rmsnorm(const void* x, long long ldx, const void* residual, long lo
   if ((reinterpret_cast<uintptr_t>(gamma) | reinterpret_cast<uintptr_t>(y_scales) |
        reinterpret_cast<uintptr_t>(rstd)) & 3u)
     return LMOE_ERR_INVALID_ARG;
+  // an output over an input: the same rows, or a row would be written before another block reads it
+  for (const auto& [out, ldo] : {std::pair<const void*, long long>{total, ldt}, {y, ldy}})
+    if (rows > 1 && out && ((out == x && ldo != ldx) || (out == residual && ldo != ldr)))
+      return LMOE_ERR_INVALID_ARG;
   NormArgs a{};
   a.x = static_cast<const __nv_bfloat16*>(x);
   a.res = static_cast<const __nv_bfloat16*>(residual);
@@ -743,6 +749,8 @@ int lmoe_add_rmsnorm_backward(const void* dy, long long ldy, const void* total, 
   if (dgamma && (!ws || (reinterpret_cast<uintptr_t>(ws) & 15u))) return LMOE_ERR_INVALID_ARG;
   if (dgamma && ws_bytes < lmoe_add_rmsnorm_backward_workspace_bytes(rows, cols))
     return LMOE_ERR_WORKSPACE_TOO_SMALL;
+  if (rows > 1 && ((dx == dy && ldx != ldy) || (dx == dtotal && ldx != ldd)))
+    return LMOE_ERR_INVALID_ARG;
   NormBwdArgs a{};
   a.dy = static_cast<const __nv_bfloat16*>(dy);
   a.total = static_cast<const __nv_bfloat16*>(total);

@@ -247,3 +247,24 @@ def test_linear_forward_refuses_misaligned_words(lib, change):
 @no_gpu
 def test_linear_backward_refuses_a_misaligned_flag(lib):
     assert _linear_bwd(lib, _desc(dev_flag=BUF["flag"] + 2)) == ARG
+
+
+# An output over an input at another row distance: rows would be written over before they are read.
+@no_gpu
+@pytest.mark.parametrize("change", [
+    dict(total=BUF["x"], ldt=72), dict(total=BUF["residual"], ldr=72),
+    dict(y=BUF["x"], ldx=72), dict(y=BUF["residual"], ldy=128)])
+def test_add_rmsnorm_refuses_shifted_rows(lib, change):
+    assert _norm(lib, **change) == ARG
+
+
+@no_gpu
+@pytest.mark.parametrize("change", [dict(dx=BUF["dy"], ldx=72), dict(dx=BUF["dtotal"], ldd=72)])
+def test_add_rmsnorm_backward_refuses_shifted_rows(lib, change):
+    assert _norm_bwd(lib, **change) == ARG
+
+
+@no_gpu
+@pytest.mark.parametrize("change", [dict(ldy=72), dict(ldr=72)])
+def test_linear_refuses_shifted_rows(lib, change):
+    assert lib.lmoe_linear_forward(ctypes.byref(_desc(y=BUF["residual"], **change)), None) == ARG
