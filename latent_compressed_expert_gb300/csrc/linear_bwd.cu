@@ -236,12 +236,16 @@ int lmoe_linear_backward(const lmoe_linear* p, const void* dy, long long lddy, v
   if (lddy < p->N || lddy % 8 || (dx && (lddx < p->K || lddx % 8)) ||
       (act && (p->ldp < rows || p->ldp % 8)))
     return LMOE_ERR_INVALID_ARG;
-  for (const void* out : {static_cast<const void*>(dx), static_cast<const void*>(dw)})
+  const bool need_ws = act || dbias;
+  const void* outs[] = {dx, dw, dbias, need_ws ? ws : nullptr};
+  for (int i = 0; i < 4; ++i) {
+    const void* out = outs[i];
     if (out && (out == dy || out == p->x || out == p->w || (act && out == p->pre)))
       return LMOE_ERR_INVALID_ARG;
-  if (dx && dx == dw) return LMOE_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (out && out == outs[j]) return LMOE_ERR_INVALID_ARG;
+  }
   const LinearBwdLayout L = linear_bwd_layout(*p);
-  const bool need_ws = act || dbias;
   if (need_ws && (!ws || !al16(ws))) return LMOE_ERR_INVALID_ARG;
   if (need_ws && ws_bytes < L.total) return LMOE_ERR_WORKSPACE_TOO_SMALL;
   uint8_t* base = static_cast<uint8_t*>(ws);

@@ -696,6 +696,13 @@ int lmoe_add_rmsnorm(const void* x, long long ldx, const void* residual, long lo
   if ((reinterpret_cast<uintptr_t>(gamma) | reinterpret_cast<uintptr_t>(y_scales) |
        reinterpret_cast<uintptr_t>(rstd)) & 3u)
     return LMOE_ERR_INVALID_ARG;
+  // no output over another, nor codes over the rows they come from
+  const void* outs[] = {y, total, y_type == LMOE_E4M3 ? y_scales : nullptr, rstd};
+  for (int i = 0; i < 4; ++i)
+    for (int j = 0; j < i; ++j)
+      if (outs[i] && outs[i] == outs[j]) return LMOE_ERR_INVALID_ARG;
+  for (const void* out : {y_type == LMOE_E4M3 ? outs[0] : nullptr, outs[2], outs[3]})
+    if (out && (out == x || out == residual || out == gamma)) return LMOE_ERR_INVALID_ARG;
   // an output over an input: the same rows, or a row would be written before another block reads it
   for (const auto& [out, ldo] : {std::pair<const void*, long long>{total, ldt}, {y, ldy}})
     if (rows > 1 && out && ((out == x && ldo != ldx) || (out == residual && ldo != ldr)))
@@ -749,6 +756,9 @@ int lmoe_add_rmsnorm_backward(const void* dy, long long ldy, const void* total, 
   if (dgamma && (!ws || (reinterpret_cast<uintptr_t>(ws) & 15u))) return LMOE_ERR_INVALID_ARG;
   if (dgamma && ws_bytes < lmoe_add_rmsnorm_backward_workspace_bytes(rows, cols))
     return LMOE_ERR_WORKSPACE_TOO_SMALL;
+  for (const void* in : {dy, total, dtotal, static_cast<const void*>(gamma),
+                         static_cast<const void*>(rstd), static_cast<const void*>(dx)})
+    if (dgamma && (dgamma == in || ws == in || ws == dgamma)) return LMOE_ERR_INVALID_ARG;
   if (rows > 1 && ((dx == dy && ldx != ldy) || (dx == dtotal && ldx != ldd)))
     return LMOE_ERR_INVALID_ARG;
   NormBwdArgs a{};

@@ -268,3 +268,33 @@ def test_add_rmsnorm_backward_refuses_shifted_rows(lib, change):
 @pytest.mark.parametrize("change", [dict(ldy=72), dict(ldr=72)])
 def test_linear_refuses_shifted_rows(lib, change):
     assert lib.lmoe_linear_forward(ctypes.byref(_desc(y=BUF["residual"], **change)), None) == ARG
+
+
+# Two outputs at one address, codes or sums over an input, scratch over an operand.
+@no_gpu
+@pytest.mark.parametrize("change", [
+    dict(total=BUF["y"]), dict(rstd=BUF["total"]), dict(rstd=BUF["y"]), dict(rstd=BUF["x"]),
+    dict(rstd=BUF["gamma"]), dict(type=lmoe.E4M3, scales=BUF["total"]),
+    dict(type=lmoe.E4M3, scales=BUF["rstd"]), dict(type=lmoe.E4M3, scales=BUF["gamma"]),
+    dict(type=lmoe.E4M3, scales=BUF["scales"], y=BUF["x"]),
+    dict(type=lmoe.E4M3, scales=BUF["scales"], y=BUF["residual"]),
+    dict(type=lmoe.E4M3, scales=BUF["y"])])
+def test_add_rmsnorm_refuses_outputs_over_each_other(lib, change):
+    assert _norm(lib, **change) == ARG
+
+
+@no_gpu
+@pytest.mark.parametrize("change", [
+    *[dict(dgamma=BUF[n]) for n in ("dy", "total", "dtotal", "gamma", "rstd", "dx", "ws")],
+    *[dict(ws=BUF[n]) for n in ("dy", "total", "dtotal", "gamma", "rstd", "dx")]])
+def test_add_rmsnorm_backward_refuses_sums_over_operands(lib, change):
+    assert _norm_bwd(lib, **change) == ARG
+
+
+@no_gpu
+@pytest.mark.parametrize("fields,change", [
+    *[({}, dict(dbias=BUF[n])) for n in ("dx", "dw", "dy", "x", "w", "ws")],
+    *[({}, dict(ws=BUF[n])) for n in ("dx", "dw", "dy", "x", "w")],
+    (SITU, dict(dbias=BUF["pre"])), (SITU, dict(ws=BUF["pre"]))])
+def test_linear_backward_refuses_sums_over_operands(lib, fields, change):
+    assert _linear_bwd(lib, _desc(**fields), **change) == ARG
