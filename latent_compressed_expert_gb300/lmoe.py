@@ -440,6 +440,13 @@ def last_device_error(workspace: torch.Tensor) -> int:
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
+def _expect_on(t, dtype, shape, dev, name):
+    """_expect, and on device number dev."""
+    _expect(t, dtype, shape, name)
+    if t.get_device() != dev:
+        raise ValueError(f"lmoe: {name} must be on CUDA device {dev}, not {t.device}")
+
+
 def _rows(t, dtype, rows, cols, dev, name):
     """(address, distance between rows) of a [rows, cols] tensor on device number dev whose rows
     are contiguous."""
@@ -877,33 +884,33 @@ class Layer:
         if T >= len(self._few_dims):
             raise ValueError(f"lmoe: {T} tokens exceed forward_few's {len(self._few_dims) - 1}")
         dims = self._few_dims[T]
-        _expect(x, bf, (T, sh.d), "x")
+        dev = self.device.index
+        _expect_on(x, bf, (T, sh.d), dev, "x")
         if residual is not None:
-            _expect(residual, bf, (T, sh.d), "residual")
+            _expect_on(residual, bf, (T, sh.d), dev, "residual")
         if y is None:
-            y = torch.empty((T, sh.d), dtype=bf, device=x.device)
+            y = torch.empty((T, sh.d), dtype=bf, device=self.device)
         else:
-            _expect(y, bf, (T, sh.d), "y")
+            _expect_on(y, bf, (T, sh.d), dev, "y")
         io = IO()
         if tau is not None:
-            _expect(tau, f, (sh.E,), "tau")
+            _expect_on(tau, f, (sh.E,), dev, "tau")
             io.tau_in = _ptr(tau)
         if logits_in is not None:
-            _expect(logits_in, f, (T, sh.E), "logits_in")
+            _expect_on(logits_in, f, (T, sh.E), dev, "logits_in")
             io.logits_in = _ptr(logits_in)
         if logit_bias is not None:
-            _expect(logit_bias, f, (sh.E,), "logit_bias")
+            _expect_on(logit_bias, f, (sh.E,), dev, "logit_bias")
             io.logit_bias = _ptr(logit_bias)
         dbg = {}
         if debug:
-            dev = x.device
-            dbg = {"logits": torch.empty((T, sh.E), dtype=f, device=dev),
-                   "idx": torch.empty((T, sh.K), dtype=torch.int32, device=dev),
-                   "gate": torch.empty((T, sh.K), dtype=f, device=dev),
-                   "y_f32": torch.empty((T, sh.d), dtype=f, device=dev)}
+            dbg = {"logits": torch.empty((T, sh.E), dtype=f, device=self.device),
+                   "idx": torch.empty((T, sh.K), dtype=torch.int32, device=self.device),
+                   "gate": torch.empty((T, sh.K), dtype=f, device=self.device),
+                   "y_f32": torch.empty((T, sh.d), dtype=f, device=self.device)}
             io.logits_out, io.idx_out = _ptr(dbg["logits"]), _ptr(dbg["idx"])
             io.gate_out, io.y_f32_out = _ptr(dbg["gate"]), _ptr(dbg["y_f32"])
-        st = _on(self.device.index)
+        st = _on(dev)
         _check(lib.lmoe_forward_few(ctypes.byref(dims), _ptr(self.packed), _ptr(x), _ptr(residual),
                                     _ptr(y), _ptr(self.few_ws), self.few_ws.numel(),
                                     ctypes.byref(io), st), "lmoe_forward_few")

@@ -298,3 +298,43 @@ def test_add_rmsnorm_backward_refuses_sums_over_operands(lib, change):
     (SITU, dict(dbias=BUF["pre"])), (SITU, dict(ws=BUF["pre"]))])
 def test_linear_backward_refuses_sums_over_operands(lib, fields, change):
     assert _linear_bwd(lib, _desc(**fields), **change) == ARG
+
+
+class _Placed:
+    """What the binding asks of a tensor, with the device number given."""
+
+    def __init__(self, t, number):
+        self.dtype, self.shape, self.device, self._t, self._n = t.dtype, t.shape, t.device, t, number
+        self.is_cuda = True
+
+    def get_device(self):
+        return self._n
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return 0x100000
+
+    def numel(self):
+        return 1 << 30
+
+
+@no_gpu
+@pytest.mark.parametrize("name", ["x", "residual", "y", "tau", "logits_in", "logit_bias"])
+def test_forward_few_refuses_tensors_of_another_device(lib, monkeypatch, name):
+    sh = synth.TINY
+    layer = object.__new__(lmoe.Layer)
+    layer.shape, layer.max_tokens, layer.expert_fp8 = sh, 8, False
+    layer.device = torch.device("cuda:0")
+    layer._few_dims = [lmoe.dims_of(sh, T=t) for t in range(3)]
+    layer.few_ws = layer.packed = _Placed(torch.empty(1), 0)
+    monkeypatch.setattr(lmoe, "_on", lambda dev: None)
+    bf = torch.bfloat16
+    shapes = {"x": ((2, sh.d), bf), "residual": ((2, sh.d), bf), "y": ((2, sh.d), bf),
+              "tau": ((sh.E,), torch.float32), "logits_in": ((2, sh.E), torch.float32),
+              "logit_bias": ((sh.E,), torch.float32)}
+    args = {n: _Placed(torch.empty(s, dtype=t), 1 if n == name else 0)
+            for n, (s, t) in shapes.items()}
+    with pytest.raises(ValueError, match=name):
+        layer.forward_few(**args)
