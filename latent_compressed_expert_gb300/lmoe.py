@@ -870,17 +870,7 @@ class Layer:
         bf, f = torch.bfloat16, torch.float32
         lib = load()
         if self.few_ws is None:
-            self._few_dims = [dims_of(sh, T=t, expert_fp8=self.expert_fp8)
-                              for t in range(min(self.max_tokens, FEW_MAX_TOKENS) + 1)]
-            sizes = [int(lib.lmoe_few_workspace_bytes(ctypes.byref(D))) for D in self._few_dims]
-            while len(sizes) > 1 and sizes[-1] == 0:  # operands too wide for an SM's shared memory
-                sizes.pop()
-            if sizes[-1] == 0:
-                raise LmoeError(LMOE_ERR_UNSUPPORTED, "lmoe_few_workspace_bytes")
-            self._few_dims = self._few_dims[:len(sizes)]
-            # zeroed before any stream of the caller's uses it
-            self.few_ws = torch.zeros(sizes[-1], dtype=torch.uint8, device=self.device)
-            torch.cuda.current_stream(self.device).synchronize()
+            self._prepare_few(lib)
         if T >= len(self._few_dims):
             raise ValueError(f"lmoe: {T} tokens exceed forward_few's {len(self._few_dims) - 1}")
         dims = self._few_dims[T]
@@ -916,6 +906,22 @@ class Layer:
                                     ctypes.byref(io), st), "lmoe_forward_few")
         self.last_kernel_launches = io.kernel_launches
         return (y, dbg) if debug else y
+
+    def _prepare_few(self, lib):
+        """forward_few's sizes and workspace, once, whichever host thread comes first."""
+        with _lock:
+            if self.few_ws is not None:
+                return
+            dims = [dims_of(self.shape, T=t, expert_fp8=self.expert_fp8)
+                    for t in range(min(self.max_tokens, FEW_MAX_TOKENS) + 1)]
+            sizes = [int(lib.lmoe_few_workspace_bytes(ctypes.byref(D))) for D in dims]
+            while len(sizes) > 1 and sizes[-1] == 0:  # operands too wide for an SM's shared memory
+                sizes.pop()
+            if sizes[-1] == 0:
+                raise LmoeError(LMOE_ERR_UNSUPPORTED, "lmoe_few_workspace_bytes")
+            ws = torch.zeros(sizes[-1], dtype=torch.uint8, device=self.device)
+            torch.cuda.current_stream(self.device).synchronize()  # before any stream uses it
+            self._few_dims, self.few_ws = dims[:len(sizes)], ws  # few_ws last: it says that all is there
 
     def few_device_error(self) -> int:
         """device_error of forward_few's workspace (call after the stream has synchronised)."""

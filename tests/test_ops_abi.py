@@ -338,3 +338,50 @@ def test_forward_few_refuses_tensors_of_another_device(lib, monkeypatch, name):
             for n, (s, t) in shapes.items()}
     with pytest.raises(ValueError, match=name):
         layer.forward_few(**args)
+
+
+def _layer_without_gpu(monkeypatch, zeros):
+    """A layer whose forward_few has not been called, on a machine without a GPU; `zeros` allocates
+    its workspace."""
+    layer = object.__new__(lmoe.Layer)
+    layer.shape, layer.max_tokens, layer.expert_fp8 = synth.TINY, 8, False
+    layer.device, layer.few_ws = torch.device("cuda:0"), None
+    layer.packed = _Placed(torch.empty(1), 0)
+    monkeypatch.setattr(lmoe, "_on", lambda dev: None)
+    monkeypatch.setattr(torch, "zeros", zeros)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+
+    class Stream:
+        def synchronize(self):
+            pass
+
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: Stream())
+    return layer
+
+
+@no_gpu
+def test_first_forward_few_of_two_threads(lib, monkeypatch):
+    """Both threads end up with one workspace."""
+    import threading
+    import time
+
+    made, used, none = [], [], torch.empty(0, synth.TINY.d, dtype=torch.bfloat16)
+
+    def zeros(*a, **k):
+        time.sleep(0.2)
+        made.append(_Placed(none, 0))
+        return made[-1]
+
+    layer = _layer_without_gpu(monkeypatch, zeros)
+
+    def first():
+        layer.forward_few(_Placed(none, 0), y=_Placed(none, 0))  # no tokens: no launch
+        used.append((layer.few_ws, layer._few_dims))
+
+    threads = [threading.Thread(target=first) for _ in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert len(made) == 1 and len(used) == 2
+    assert used[0][0] is used[1][0] is made[0] and used[0][1] is used[1][1]
