@@ -919,6 +919,9 @@ class Layer:
                 sizes.pop()
             if sizes[-1] == 0:
                 raise LmoeError(LMOE_ERR_UNSUPPORTED, "lmoe_few_workspace_bytes")
+            if torch.cuda.is_current_stream_capturing():  # the graph's memory, zeroed at its replay
+                raise ValueError("lmoe: forward_few's first call allocates its workspace: make it "
+                                 "before capturing a graph")
             ws = torch.zeros(sizes[-1], dtype=torch.uint8, device=self.device)
             torch.cuda.current_stream(self.device).synchronize()  # before any stream uses it
             self._few_dims, self.few_ws = dims[:len(sizes)], ws  # few_ws last: it says that all is there

@@ -392,3 +392,22 @@ def test_two_threads_with_layers_of_different_sizes(dev):
         sum(c != 0 for c in part) for part in codes]
     for layer, _, want, y in work:
         assert torch.equal(y, want) and layer.few_device_error() == lmoe.LMOE_OK
+
+
+def test_first_call_under_capture(dev):
+    """It is refused, the capture goes on, and the layer works afterwards."""
+    sh = H.mid_shape(8)
+    layer = lmoe.Layer(sh, synth.make_weights(sh, seed=1, device=dev), max_tokens=8)
+    x = synth.make_x(sh, seed=7, device=dev, T=3)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        with pytest.raises(ValueError):
+            layer.forward_few(x)
+        twice = x + x
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(twice, 2 * x) and layer.few_ws is None
+    y = layer.forward_few(x)
+    torch.cuda.synchronize()
+    assert layer.few_device_error() == lmoe.LMOE_OK
+    assert torch.equal(layer.forward_few(x), y)

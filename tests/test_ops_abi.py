@@ -385,3 +385,23 @@ def test_first_forward_few_of_two_threads(lib, monkeypatch):
         t.join()
     assert len(made) == 1 and len(used) == 2
     assert used[0][0] is used[1][0] is made[0] and used[0][1] is used[1][1]
+
+
+@no_gpu
+def test_first_forward_few_under_capture_is_refused(lib, monkeypatch):
+    """Nothing is allocated from the graph's memory, and the call is made later as if it were the
+    first."""
+    made, none = [], torch.empty(0, synth.TINY.d, dtype=torch.bfloat16)
+
+    def zeros(*a, **k):
+        made.append(_Placed(none, 0))
+        return made[-1]
+
+    layer = _layer_without_gpu(monkeypatch, zeros)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    with pytest.raises(ValueError, match="before capturing"):
+        layer.forward_few(_Placed(none, 0), y=_Placed(none, 0))
+    assert not made and layer.few_ws is None
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    layer.forward_few(_Placed(none, 0), y=_Placed(none, 0))
+    assert layer.few_ws is made[0] and len(made) == 1
