@@ -1037,7 +1037,9 @@ struct FewFinish : FewPlan<FP8> {
         const size_t o = static_cast<size_t>(t) * a.L + unit * 16 + row + 8 * h;
         if constexpr (FP8) a.lat32[o] = v[h];
         a.lat[o] = hi;
-        a.lat[static_cast<size_t>(a.T) * a.L + o] = __float2bfloat16_rn(v[h] - __bfloat162float(hi));
+        // an infinite latent is all in hi: what is left of it would be NaN
+        const float rest = isinf(__bfloat162float(hi)) ? 0.0f : v[h] - __bfloat162float(hi);
+        a.lat[static_cast<size_t>(a.T) * a.L + o] = __float2bfloat16_rn(rest);
       }
     }
     finished(FEW_IN);

@@ -411,3 +411,22 @@ def test_first_call_under_capture(dev):
     torch.cuda.synchronize()
     assert layer.few_device_error() == lmoe.LMOE_OK
     assert torch.equal(layer.forward_few(x), y)
+
+
+def test_a_latent_past_the_range(dev, oracle_mod):
+    """One latent feature overflows to an infinity: logits of its sign, gates and values at their
+    caps, finite outputs, as in Layer.forward."""
+    sh = H.mid_shape(8)
+    w = synth.make_weights(sh, seed=1, device=dev)
+    x = synth.make_x(sh, seed=3, device=dev, T=1)
+    w["w_down"] = w["w_down"].clone()
+    w["w_down"][3] = 1e38 * torch.sign(x[0])
+    layer = lmoe.Layer(sh, w, max_tokens=8)
+    y, dbg = layer.forward_few(x, debug=True)
+    assert torch.equal(dbg["logits"][0], torch.sign(w["w_router"][:, 3].float()) * float("inf"))
+    idx, gate, _ = oracle_mod.route(dbg["logits"].cpu().numpy(), None, sh.K)
+    assert np.array_equal(dbg["idx"].cpu().numpy(), idx)
+    ref = _reference(sh, w, x, dbg["idx"], dbg["gate"], None, False).cpu().numpy()
+    H.assert_layer_close(y, dbg["y_f32"], ref)
+    full = layer.forward(x, logits_in=dbg["logits"], balance=False)
+    H.assert_close(y.float().cpu().numpy(), full.float().cpu().numpy(), "few vs forward")
