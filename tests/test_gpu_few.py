@@ -430,3 +430,37 @@ def test_a_latent_past_the_range(dev, oracle_mod):
     H.assert_layer_close(y, dbg["y_f32"], ref)
     full = layer.forward(x, logits_in=dbg["logits"], balance=False)
     H.assert_close(y.float().cpu().numpy(), full.float().cpu().numpy(), "few vs forward")
+
+
+@pytest.mark.parametrize("T", [1, 8])
+@pytest.mark.parametrize("sh,fp8", [
+    # DOWN's experts in one part (L / 16 units fill the SMs as evenly as twice as many halves)
+    (synth.LayerShape("one part", T=8, d=256, L=2048, E=32, K=4, I=64, S=1, Is=64), False),
+    (synth.LayerShape("one part", T=8, d=256, L=2048, E=32, K=4, I=128, S=1, Is=64), True),
+    # an expert's reduction over more than one stage: a ragged second one, two whole ones
+    (synth.LayerShape("I 576", T=8, d=256, L=256, E=32, K=4, I=576, S=1, Is=64), False),
+    (synth.LayerShape("I 1024", T=8, d=256, L=128, E=16, K=4, I=1024, S=0, Is=0), False),
+    (synth.LayerShape("I 1152", T=8, d=256, L=256, E=32, K=4, I=1152, S=1, Is=64), True)],
+    ids=lambda v: v.name if isinstance(v, synth.LayerShape) else "e4m3" if v else "bf16")
+def test_parts_and_long_expert_reductions(dev, oracle_mod, sh, fp8, T):
+    w = synth.make_weights(sh, seed=T, device=dev)
+    layer = lmoe.Layer(sh, w, max_tokens=8, expert_fp8=fp8)
+    x = synth.make_x(sh, seed=T, device=dev, T=T)
+    _check(oracle_mod, sh, w, layer, x, tau=_tau(sh, T, dev), residual=x, tag=(sh.name, T))
+
+
+def test_stalled_wait_with_e4m3_experts(dev, monkeypatch):
+    sh = H.mid_shape(8)
+    layer = lmoe.Layer(sh, synth.make_weights(sh, seed=1, device=dev), max_tokens=8, expert_fp8=True)
+    x = synth.make_x(sh, seed=7, device=dev, T=3)
+    want = layer.forward_few(x)
+    monkeypatch.setenv("LMOE_WAIT_LIMIT_MS", "100")
+    monkeypatch.setenv("LMOE_FAULT_INJECT", "stall")
+    layer.forward_few(x)
+    torch.cuda.synchronize()
+    assert layer.few_device_error() == lmoe.LMOE_ERR_DEVICE_TIMEOUT
+    monkeypatch.delenv("LMOE_FAULT_INJECT")
+    monkeypatch.delenv("LMOE_WAIT_LIMIT_MS")
+    assert torch.equal(layer.forward_few(x), want)
+    torch.cuda.synchronize()
+    assert layer.few_device_error() == lmoe.LMOE_OK

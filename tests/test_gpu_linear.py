@@ -533,3 +533,92 @@ def test_cap_changed_and_activation_fixed(dev):
     assert torch.equal(lin.forward(x), lmoe.Linear(lin.w, act="situ", c=2.0).forward(x))
     with pytest.raises(AttributeError):
         lin.act = "none"
+
+
+# Root-mean-square checks, which the worst-case bounds above leave room under.  A bf16 output that is
+# an fp32 sum rounded once is as far from the 64-bit value, in the norm, as that value's own rounding:
+# the sum's error (2^-24 of what has been added at each of K / 16 steps: 2e-5 of it at 7168) is two
+# orders below the rounding (2^-9), and turns it only near a midpoint, where both neighbours are as
+# far.  Partial sums rounded to bf16 would come out at 1.4 times.  ONCE allows 2 %.  dp, rounded to
+# bf16, takes the neighbouring value in about 2^-17 / 2^-9 of its elements, one step off: another
+# 2.4 % of the square; 5 % in all where the reference rounds dp in its place.
+ONCE, ONCE_DP = 1.02, 1.05
+LONG = [(1, 512, 7168), (2, 7168, 4096), (8, 512, 7168), (77, 3584, 7168), (300, 1024, 7168),
+        (2050, 2056, 7168)]
+
+
+def _once(got, want, slack, tag):
+    err = float((got.double() - want).norm())
+    once = float((want.to(BF).double() - want).norm())
+    assert err <= slack * once, (tag, err / once)
+
+
+@pytest.mark.parametrize("M,N,K", LONG)
+@pytest.mark.parametrize("act", ["none", "gelu", "situ"])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_forward_rounds_once(dev, M, N, K, act, fp8):
+    rows = 2 * N if act == "situ" else N
+    w, b, ws = _pair(dev, rows, K, N + K, fp8)
+    x, xs = _codes(_draw(dev, M, K, M)) if fp8 else (_draw(dev, M, K, M), None)
+    lin = lmoe.Linear(w, b, act, w_scales=ws)
+    res = _draw(dev, M, N, 7)
+    w64 = w.view(E4M3).double() * ws.double()[:, None] if fp8 else w.double()
+    x64 = x.view(E4M3).double() * xs.double()[:, None] if fp8 else x.double()
+    p = x64 @ w64.T + b.double()
+    y, pre = lin.forward(x, res, x_scales=xs, train=True)
+    _once(y, _act64(p, act, 100.0)[0] + res.double(), ONCE, "y")
+    if pre is not None:
+        _once(pre, p, ONCE, "pre")
+
+
+@pytest.mark.parametrize("M,N,K", [(8, 7168, 512), (77, 7168, 3584), (300, 7168, 1024),
+                                   (2050, 7168, 1024)])
+@pytest.mark.parametrize("act", ["none", "silu", "situ"])
+def test_gradients_round_once(dev, M, N, K, act):
+    rows = 2 * N if act == "situ" else N
+    lin = lmoe.Linear(_draw(dev, rows, K, N + K, K ** -0.5), torch.zeros(rows, device=dev), act)
+    x, dy = _draw(dev, M, K, 1), _draw(dev, M, N, 3)
+    pre = _draw(dev, M, rows, 4) if act != "none" else None
+    dp = dy.double()
+    if pre is not None:
+        dp = _slope64(pre.double(), dp, act, 100.0)[0].to(BF).double()
+    slack = ONCE if act == "none" else ONCE_DP
+    g = lin.backward(x, dy, pre, dw_dtype=BF)
+    _once(g["dx"], dp @ lin.w.double(), slack, "dx")
+    _once(g["dw"], dp.T @ x.double(), slack, "dw")
+
+
+@pytest.mark.parametrize("M", [40, 3000])
+@pytest.mark.parametrize("wants", [(True, True), (True, False), (False, True)])
+def test_stalled_backward_reports_timeout_and_recovers(dev, monkeypatch, M, wants):
+    """As for the forward, in the kernels of both gradients, together and one by one."""
+    lin = lmoe.Linear(_draw(dev, 2048, 2048, 1, 1 / 45))
+    x, dy = _draw(dev, M, 2048, 2), _draw(dev, M, 2048, 3)
+    run = lambda: lin.backward(x, dy, want_dx=wants[0], want_dw=wants[1])
+    want = run()
+    monkeypatch.setenv("LMOE_WAIT_LIMIT_MS", "100")
+    monkeypatch.setenv("LMOE_FAULT_INJECT", "stall")
+    run()
+    torch.cuda.synchronize()
+    assert lin.device_error() == lmoe.LMOE_ERR_DEVICE_TIMEOUT
+    assert lin.device_error() == lmoe.LMOE_OK
+    monkeypatch.delenv("LMOE_FAULT_INJECT")
+    monkeypatch.delenv("LMOE_WAIT_LIMIT_MS")
+    got = run()
+    assert all(want[n] is None or torch.equal(got[n], want[n]) for n in want)
+
+
+@pytest.mark.parametrize("M", [40, 9000])
+def test_stalled_wait_of_e4m3_products(dev, monkeypatch, M):
+    w, ws = _codes(_draw(dev, 2048, 2048, 1, 1 / 45))
+    x, xs = _codes(_draw(dev, M, 2048, 2))
+    lin = lmoe.Linear(w, w_scales=ws)
+    want = lin.forward(x, x_scales=xs)
+    monkeypatch.setenv("LMOE_WAIT_LIMIT_MS", "100")
+    monkeypatch.setenv("LMOE_FAULT_INJECT", "stall")
+    lin.forward(x, x_scales=xs)
+    torch.cuda.synchronize()
+    assert lin.device_error() == lmoe.LMOE_ERR_DEVICE_TIMEOUT
+    monkeypatch.delenv("LMOE_FAULT_INJECT")
+    monkeypatch.delenv("LMOE_WAIT_LIMIT_MS")
+    assert torch.equal(lin.forward(x, x_scales=xs), want)
