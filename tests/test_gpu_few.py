@@ -464,3 +464,23 @@ def test_stalled_wait_with_e4m3_experts(dev, monkeypatch):
     assert torch.equal(layer.forward_few(x), want)
     torch.cuda.synchronize()
     assert layer.few_device_error() == lmoe.LMOE_OK
+
+
+def test_latent_before_its_codes(dev):
+    """e4m3 experts: the fp32 latent that the codes are taken from (kept in the workspace behind the
+    header, the two bf16 terms, the logits, their keys, h and u).  A box of 64 products is added
+    in two chains, each of two MMAs that cut off less than 2^-23 of their sum, 2^-24 on average: up to
+    2^-23 of a latent where they all point its way.  The 14 boxes of a warp and the eight warps are
+    added with rounding, 2^-25 on average of sums that grow like the root of their number: below
+    2^-24 sqrt(3 + 14 / 2).  In the norm both together stay below 2e-7."""
+    sh = synth.LayerShape("wide", T=8, d=7168, L=3584, E=16, K=1, I=128, S=0, Is=0)
+    w = synth.make_weights(sh, seed=1, device=dev)
+    layer = lmoe.Layer(sh, w, max_tokens=8, expert_fp8=True)
+    x = synth.make_x(sh, seed=2, device=dev, T=8)
+    layer.forward_few(x)
+    torch.cuda.synchronize()
+    pieces = [8 * sh.L * 4, 0, 8 * sh.E * 4, 8 * sh.E * 4, 8 * sh.K * sh.I * 4, 8 * sh.L * 4]
+    at = 256 + sum((n + 255) // 256 * 256 for n in pieces)
+    lat = layer.few_ws[at:at + 8 * sh.L * 4].view(torch.float32).view(8, sh.L)
+    want = x.double() @ w["w_down"].double().T
+    assert (lat.double() - want).norm() <= 2e-7 * want.norm()
