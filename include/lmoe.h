@@ -24,8 +24,9 @@
  *
  * Conventions for every entry point:
  *   - Every pointer argument is DEVICE memory owned by the caller, unless stated.  The
- *     library allocates nothing, keeps no global state between calls and may be called
- *     concurrently on different streams with disjoint buffers.
+ *     library allocates nothing, keeps no global state between calls (lmoe_forward_noalloc's
+ *     array and lmoe_norm_last_device_error's word aside) and may be called concurrently on
+ *     different streams with disjoint buffers.
  *   - bf16 tensors are raw IEEE bfloat16 bit patterns; all matrices are row-major and
  *     weights are stored [out, in].
  *   - `stream` is a cudaStream_t (NULL = legacy default stream).  Every call is
@@ -456,7 +457,7 @@ int lmoe_quantize_e4m3(const void *x, long long rows, int cols, uint8_t *codes, 
  *     rounded to bf16 as operands; e4m3 experts quantise the latent and h from their fp32 values.  So
  *     the two calls agree within the layer's tolerance, and route alike up to ties that the latent's
  *     rounding decides.
- *   - workspace: lmoe_few_workspace_bytes, 256-byte aligned, its first LMOE_FEW_HEADER_BYTES
+ *   - workspace: lmoe_few_workspace_bytes, 16-byte aligned, its first LMOE_FEW_HEADER_BYTES
  *     zeroed once before the first call (a call leaves them zero, error flag aside).  Calls on one
  *     workspace must not overlap.  It serves every smaller batch of the same layer too.
  * The kernel is a cooperative launch of one CTA per SM that wait on one another; every wait is

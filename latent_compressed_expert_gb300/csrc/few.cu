@@ -22,9 +22,9 @@
 // their partial tiles up and store the results.  tcgen05 would bring nothing here: the tensor cores
 // are idle most of the time, and its 128-row tiles would make units too large to deal out evenly.
 //
-// Measured (K3, in a CUDA graph): one token 84 to 86 us (0.81 of the weights' time at the rate of a
-// copy; lmoe_forward 175), eight 259 to 264 us (0.92; 331); e4m3 experts, four tokens 126 us (0.75;
-// 207).  The expert phases of bf16 layers run at HBM's rate; what is left are the barriers (~2 us
+// Measured (K3, in a CUDA graph over inputs in turn, so that few of the weights are in L2): one token
+// 86 us (0.80 of the weights' time at the rate of a copy; lmoe_forward 181), eight 262 us (0.92; 334);
+// e4m3 experts, four tokens 126 us (0.74; 203).  The expert phases of bf16 layers run at HBM's rate; what is left are the barriers (~2 us
 // each), the selection (4 us) and the operands' way into shared memory (1 to 5 us a phase).  With
 // e4m3 experts the computing warps' ~500 cycles a box, of instructions and of shared memory's
 // latency, are as long as HBM takes for a stage.

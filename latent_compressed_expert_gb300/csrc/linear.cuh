@@ -19,16 +19,19 @@
 //                        sets, so that one tile is written while the next is computed.  An SM
 //                        stages 16 KB of P and bn / 2 rows of Q per K-block.  Its MODE_GRADS
 //                        computes dx, dw or both.  Bound by the tensor cores from about 1000 rows
-//                        on: 8192 rows of 2 x 4096 gated features x 7168 512 to 600 us as the power
-//                        cap allows (0.85 to 0.99 of the bf16 rate), e4m3 2048 x 7168 x 4096 41 us
-//                        (0.77 of twice that rate: 2.95 rounds of tiles take 3).
+//                        on: 8192 rows of 4096 features x 7168 255 us (0.99 of the bf16 rate), of 2 x
+//                        4096 gated ones 580 us (0.87; 516 to 600 as the power cap allows).  e4m3
+//                        2048 x 7168 x 4096 43 us (0.74 of twice that rate): a K-block's MMAs are
+//                        as short as the ring's round, and the last tile's epilogue is not hidden.
 //   linear_tile_kernel   128 x bn tiles, one per cluster of ks CTAs that split the reduction
 //                        between them and add their parts through distributed shared memory in
 //                        rank order (no scratch, no second kernel, a fixed order).  For problems
 //                        with too few tiles to fill the SM pairs, down to one row, where the time
-//                        is the weights' way from HBM: 2 rows of 7168 x 4096 13.6 us (4.3 TB/s), 77
-//                        rows of 3584 x 7168 15.5 us.  About 4 us of that are the launch, the first
-//                        load and the last tile's way through the cluster.
+//                        is the weights' way: 2 rows of 7168 x 4096 16.4 us from HBM (3.6 TB/s; 13.6
+//                        with the weights in L2), 77 rows of 3584 x 7168 18.2 us (2.9 TB/s; 15.5).
+//                        DRAM is at a third of its rate: launch, first load and the last tile's way
+//                        through the cluster, one after the other, are the larger part.
+// Times are of calls whose operands rotate past L2, unless another source is named.
 // Sums are fp32 in TMEM (an fp32 dw over SM pairs: in registers from 512 rows on, LINEAR_DW_PART).
 // Every wait is bounded; on time-out a role records an error bit, raises the CTA's abort flag,
 // waits for its copies in flight and the kernel ends with its output unspecified.
@@ -503,7 +506,9 @@ static_assert(linear_dw_buffer(1, 4) <= 2 * LINEAR_TURN_BYTES, "both forms fit")
 
 // An fp32 dw's sums are taken out of TMEM after this many K-blocks (512 rows) and go on in
 // registers, which round: the MMA cuts off what it adds below the accumulator's last bit, and a sum
-// over 8192 rows came out 9e-6 of itself too low.  The epilogue has the time.
+// over 8192 rows came out 9e-6 of itself too low.  The epilogue has the time.  (A bf16 dw, dx and the
+// forward keep their sums in TMEM at any length: what that cuts off is a hundredth of their rounding
+// to bf16 at 8192 terms, a sixth at 2^18.)
 constexpr int LINEAR_DW_PART = 8;
 
 // dw's epilogue: a warp's 32 rows by 32 columns at a time through its own buffer into a tensor store,
@@ -606,8 +611,8 @@ struct LinearPairMaps {
 // 0's commits; cluster barriers bracket set-up and teardown.
 // MODE_GRADS computes both gradients in one launch: neither product of a few hundred rows has
 // tiles enough to keep all SM pairs busy, and while dx reads the weights, dw writes its output
-// (333 rows, 3584 x 7168, fp32 dw: 38.4 us against 47.2 one after the other; 2048 rows, 7168 x 4096,
-// bf16 dw: 139 against 152, 0.91 of the bf16 peak; at 4096 rows and more it makes no difference).
+// (333 rows, 3584 x 7168, fp32 dw, operands in L2: 38.4 us against 47.2 one after the other; 2048 rows,
+// 7168 x 4096, bf16 dw: 139 against 152; at 4096 rows and more it makes no difference).
 template <int MODE, bool FP8, bool GLU>
 __global__ void __launch_bounds__(LINEAR_THREADS, 1)
 linear_pair_kernel(const __grid_constant__ LinearPairMaps maps, const LinearArgs g) {

@@ -141,8 +141,8 @@ __device__ __forceinline__ void norm_store8(const NormArgs& a, int64_t row, int 
 // vectors i, i + tpr, ...; a block holds blockDim / tpr rows.  NV vectors per thread: 4 for
 // throughput (128 bytes of loads in flight per thread), 1 when there are few rows, where the
 // time is one load's latency and a reduction over as many warps as a row can use.
-// Measured: 8192 rows of 7168, bf16 71.5 us (6.6 TB/s, the rate of a copy), e4m3 67.4 us (6.1 TB/s:
-// the second reduction, of amax, leaves HBM idle); 65536 rows of 512 42.9 us; one row 2.7 us.
+// Measured: 8192 rows of 7168, bf16 71.5 us (6.6 TB/s, the rate of a copy), e4m3 68.1 us (6.0 TB/s:
+// the second reduction, of amax, leaves HBM idle); 65536 rows of 512 43.1 us; one row 2.7 us.
 // NORM_BOUND4 keeps the registers to 56, which lets five blocks of a 7168-wide row share an SM
 // (e4m3 takes 60 left to itself: four blocks, 71.5 us; 48 spill: 99 us).
 template <int NV, bool FP8>
@@ -222,7 +222,7 @@ add_rmsnorm_kernel(const NormArgs a) {
 // Any width, stride and alignment: a block per row, element by element, the row read again
 // for each pass (from L2).  An element is last read by the thread that then overwrites it, so
 // that total or y may be x or residual, as in the kernel above.  Bound by its two-byte accesses:
-// 8191 rows of 1001 24.6 us (2.7 TB/s), e4m3 36 us.
+// 8191 rows of 1001 25.3 us (2.6 TB/s), e4m3 36.6 us.
 template <bool FP8>
 __global__ void __launch_bounds__(NORM_BLOCK) add_rmsnorm_any_kernel(const NormArgs a) {
   __shared__ float red[2][32];
@@ -348,7 +348,8 @@ __device__ __forceinline__ uint4 norm_bwd_dx8(const uint4& dv, const uint4& tv, 
 // Rows in registers, as the forward: a block holds blockDim / tpr rows at a time, and walks over
 // them with its share of dgamma in registers (a thread's columns never change), so that dy and
 // total are read once for both gradients.  A block joins its rows' shares in order at the end.
-// Measured: 65536 rows of 512 54.4 us (4.9 TB/s); 300 rows of 7168 10.9 us, two launches' latency.
+// Measured: 65536 rows of 512 54.7 us (4.9 TB/s); 8192 rows of 8192 95.4 us (5.6 TB/s); 300 rows of 7168
+// 10.9 us, two launches' latency.
 template <int NV>
 __global__ void __launch_bounds__(NV == 1 ? NORM_MAX_THREADS : NORM_MAX_THREADS4)
 add_rmsnorm_bwd_kernel(const NormBwdArgs a, int tpr) {
@@ -433,8 +434,9 @@ add_rmsnorm_bwd_kernel(const NormBwdArgs a, int tpr) {
 // Many long rows: a block has the next rows' operands on their way into shared memory by bulk
 // copies while it computes, since the registers of its dgamma leave no room for loads ahead.  (The
 // forward, whose blocks are many and hold no such sums, is faster without.)  7168 columns: 2 blocks
-// of 2 stages per SM.  Measured: 8192 rows of 7168 80 us with the column sum (5.9 TB/s; the kernel
-// above 93 us; cp.async by each thread for itself, which needs no barrier, 91 us).
+// of 2 stages per SM.  Measured: 8192 rows of 7168 81 us with the column sum (5.8 TB/s; the kernel
+// above 93 us; cp.async by each thread for itself, which needs no barrier, 91 us).  Rows of more than
+// two vectors a thread take the kernel above, which comes as near to HBM there.
 // A wait that runs out sets norm_error; its block then waits for its copies in flight and makes the
 // rows that it has left and its share of dgamma NaN, so that nobody takes them for gradients.
 constexpr int NORM_STAGES = 4;
