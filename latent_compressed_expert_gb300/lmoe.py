@@ -497,16 +497,15 @@ def _add_rmsnorm(x, gamma, residual, eps, fp8, train, y, total):
     ldr = ldt = 0
     if residual is not None:
         pr, ldr = _rows(residual, bf, rows, cols, dev, "residual")
-        if total is None:
-            total = torch.empty((rows, cols), dtype=bf, device=device)
-            pt, ldt = total.data_ptr(), cols
+    # (without a residual total is x, unless y is written over it)
+    if total is None and (residual is not None or (y is not None and y.data_ptr() == px)):
+        total = torch.empty((rows, cols), dtype=bf, device=device)
+        pt, ldt = total.data_ptr(), cols
     if total is not None and pt is None:
         pt, ldt = _rows(total, bf, rows, cols, dev, "total")
     if y is None:
         y = torch.empty((rows, cols), dtype=torch.uint8 if fp8 else bf, device=device)
         py, ldy = y.data_ptr(), cols
-    elif train and pt is None and y.data_ptr() == px:
-        raise ValueError("lmoe: y over x would destroy the total that the backward needs")
     else:
         py, ldy = _rows(y, bf, rows, cols, dev, "y")
     scales = rstd = None
@@ -527,8 +526,9 @@ def add_rmsnorm(x: torch.Tensor, gamma: torch.Tensor, residual: torch.Tensor | N
                 eps: float = 1e-6, train: bool = False, y=None, total=None, stream=None):
     """Residual addition with RMSNorm (lmoe_add_rmsnorm): x and residual [rows, cols] bf16
     (rows contiguous, at any stride), gamma [cols] fp32 -> (y, total), or with train
-    (y, total, rstd) for add_rmsnorm_backward.  total is x + residual in bf16 (x itself
-    without a residual); ``y`` and ``total`` may be given, and may be x or residual."""
+    (y, total, rstd) for add_rmsnorm_backward.  total is x + residual in bf16 (without a residual
+    x itself, or a copy where y is written over x); ``y`` and ``total`` may be given, and may be
+    x or residual."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return add_rmsnorm(x, gamma, residual, eps, train, y, total)

@@ -294,3 +294,15 @@ def test_stalled_wait_reports_timeout_and_recovers(dev, monkeypatch, cols, with_
     monkeypatch.delenv("LMOE_WAIT_LIMIT_MS")
     dx, dg = lmoe.add_rmsnorm_backward(dy, total, gamma, rstd, dt)
     assert torch.equal(dx, want[0]) and torch.equal(dg, want[1])
+
+
+@pytest.mark.parametrize("rows", [0, 5, 700])
+@pytest.mark.parametrize("train", [False, True])
+def test_y_over_x_without_a_residual(dev, rows, train):
+    """The total that is returned is x as it was, not the y that lies there now."""
+    x, gamma = _draw(dev, rows, 512, 1), torch.rand(512, device=dev) + 0.5
+    want = lmoe.add_rmsnorm(x, gamma, train=train)
+    over = x.clone()
+    got = lmoe.add_rmsnorm(over, gamma, train=train, y=over)
+    assert got[0] is over and len(got) == len(want)
+    assert all(torch.equal(g, w) for g, w in zip(got, want)) and torch.equal(got[1], x)
