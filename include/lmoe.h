@@ -451,7 +451,8 @@ int lmoe_quantize_e4m3(const void *x, long long rows, int cols, uint8_t *codes, 
  *     In-batch thresholds of a few tokens carry no quantile (balance 1 without tau_in is refused);
  *   - of the other io fields, logits_in, logit_bias, logits_out, idx_out, gate_out and y_f32_out
  *     are served; tau_out, counts_out, load_stats, tau_ema, save_pre, save_pre_shared, stage_events,
- *     cand_out and phases are refused; aux_stream, aux_events and shared_sms have no meaning here;
+ *     cand_out and phases are refused; aux_stream, aux_events and shared_sms have no meaning here,
+ *     and checked mode (LMOE_CHECK_FINITE) is lmoe_forward's alone;
  *   - the latent is kept to ~2^-17 of itself, as two bf16 terms, for the router and bf16 experts
  *     (lmoe_forward rounds it to bf16), and the experts' outputs in fp32; hs, h and gamma * u are
  *     rounded to bf16 as operands; e4m3 experts quantise the latent and h from their fp32 values.  So
