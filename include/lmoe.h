@@ -477,7 +477,9 @@ int lmoe_forward_few(const lmoe_dims *dims, const void *packed, const void *x,
 enum lmoe_type {
   LMOE_BF16 = 0,
   LMOE_E4M3 = 1, /* one-byte codes with fp32 scales, the recipe stated at lmoe_dims */
-  LMOE_F32 = 2
+  LMOE_F32 = 2,
+  LMOE_I32 = 3,
+  LMOE_I64 = 4
 };
 
 /* Residual addition with RMSNorm: the pre-norm of the decoder block that the layer sits in
@@ -582,6 +584,50 @@ size_t lmoe_linear_backward_workspace_bytes(const lmoe_linear *p);
 int lmoe_linear_backward(const lmoe_linear *p, const void *dy, long long lddy, void *dx,
                          long long lddx, void *dw, int dw_type, float *dbias, void *ws,
                          size_t ws_bytes, void *stream);
+
+/* Softmax cross entropy of a linear head over a large vocabulary: the loss at the end of the model
+ * whose blocks hold the layer (the pages name no loss; this is the usual one of a language model).
+ * Per row of x, with the V logits l = x . w^T in fp32:
+ *   lse = log sum exp l;   loss = lse - l[target]
+ * The logits are not kept: no buffer of M x V elements is written or needed.  A row whose target is
+ * outside 0 .. V - 1 (an ignored token) has loss 0 and takes no part in the gradients; its lse is
+ * computed all the same.  The loss is the target's negative log-probability: with one row the call
+ * scores a sampled token. */
+typedef struct lmoe_linear_xent {
+  int M, V, K;            /* rows of x, tokens of the vocabulary, features */
+  const void *x;          /* [M, K] bf16, rows ldx elements apart */
+  long long ldx;
+  const void *w;          /* [V, K] bf16, rows ldw elements apart */
+  long long ldw;
+  const void *target;     /* [M], of target_type */
+  int target_type;        /* LMOE_I32 or LMOE_I64 */
+  float *loss;            /* [M] out, or NULL */
+  float *lse;             /* [M]: written by the forward (or NULL), read by the backward */
+  uint32_t *dev_flag;     /* as in lmoe_linear */
+} lmoe_linear_xent;
+
+/* loss and lse (one of them may be NULL).  K a multiple of 8, any V and M; x and w 16-byte aligned
+ * with row distances in whole 16 bytes.  ws: lmoe_linear_xent_workspace_bytes(p) of device scratch,
+ * 16-byte aligned.  Sums are added in a fixed order.  Outputs overlap no input, nor each other.
+ * An infinite or NaN logit gives what the formulas give, in its own row.  M == 0 is a no-op.
+ * Errors: INVALID_ARG, UNSUPPORTED (K; M, V or K above 2^30; above 2^27 tiles of 64 x 64),
+ * WORKSPACE_TOO_SMALL, CUDA. */
+size_t lmoe_linear_xent_workspace_bytes(const lmoe_linear_xent *p);
+int lmoe_linear_xent_forward(const lmoe_linear_xent *p, void *ws, size_t ws_bytes, void *stream);
+
+/* Its gradients, from dloss [M] fp32, the gradient of each row's loss (1 / rows for their mean), and
+ * the forward's lse; loss is not read:
+ *   d = dloss (exp(l - lse) - onehot(target)), rounded to bf16 as the products' operand;
+ *   dx [M, K] bf16 = d . w, rows lddx elements apart;  dw [V, K] = d^T . x, dw_type LMOE_BF16 or
+ *   LMOE_F32 (the sum over the rows without a second rounding).
+ * Either may be NULL (not wanted).  The logits are computed again, a piece of the vocabulary at a
+ * time: ws, lmoe_linear_xent_backward_workspace_bytes(p) of device scratch, 16-byte aligned, holds d
+ * of one piece (256 MB, or 4096 tokens) and dx in fp32.  M == 0 zeroes dw.  Alignment and overlaps as
+ * above.  Errors: as above. */
+size_t lmoe_linear_xent_backward_workspace_bytes(const lmoe_linear_xent *p);
+int lmoe_linear_xent_backward(const lmoe_linear_xent *p, const float *dloss, void *dx,
+                              long long lddx, void *dw, int dw_type, void *ws, size_t ws_bytes,
+                              void *stream);
 
 /* Size in bytes of the fixed device array that lmoe_forward_noalloc uses as its workspace. */
 #define LMOE_NOALLOC_SCRATCH_BYTES (24u << 20)

@@ -864,6 +864,25 @@ bool make_tmap_bf16_out32(CUtensorMap* m, const void* ptr, uint64_t rows, uint64
   return r == CUDA_SUCCESS;
 }
 
+bool make_tmap_out32(CUtensorMap* m, const void* ptr, int size, uint64_t rows, uint64_t cols,
+                     uint64_t ld, uint64_t batch, uint64_t stride) {
+  auto enc = tmap_encoder();
+  if (!enc || rows == 0 || cols == 0 || batch == 0 || (size != 2 && size != 4) ||
+      (reinterpret_cast<uintptr_t>(ptr) & 15u) != 0 || ld * size % 16 != 0 || ld < cols ||
+      (batch > 1 && stride * size % 16 != 0))
+    return false;
+  const cuuint64_t gdim[3] = {cols, rows, batch};
+  const cuuint64_t gstride[2] = {ld * size, (batch > 1 ? stride : rows * ld) * size};
+  const cuuint32_t box[3] = {32, 32, 1};
+  const cuuint32_t estride[3] = {1, 1, 1};
+  const CUresult r = enc(
+      m, size == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+      const_cast<void*>(ptr), gdim, gstride, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
+      size == 4 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+      CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 bool make_tmap_bf16(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols, uint64_t ld,
                     uint32_t box_rows) {
   auto enc = tmap_encoder();

@@ -152,6 +152,9 @@ bool make_tmap_f32_out32(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_
                          uint64_t ld);
 bool make_tmap_bf16_out32(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols,
                           uint64_t ld);
+// The two above for `batch` matrices of 2- or 4-byte elements, `stride` elements apart.
+bool make_tmap_out32(CUtensorMap* m, const void* ptr, int size, uint64_t rows, uint64_t cols,
+                     uint64_t ld, uint64_t batch, uint64_t stride);
 
 int launch_gemm(const void* A, uint64_t a_rows, int a_ld, const void* B, uint64_t b_rows,
                 int b_ld, const GemmArgs& args, cudaStream_t stream);

@@ -1,0 +1,497 @@
+// tile.cuh -- batched matrix products on the 5th-generation tensor cores whose epilogue sees
+// whole rows: the vocabulary's loss (xent.cu) and the orthogonalisation of updates (ortho.cu).
+//
+//   out[z] = P[z] . Q[z]^T     P [R, D], Q [C, D], 16-bit; either K-major (a row's D elements
+//                              contiguous) or MN-major (stored [D, R] or [D, C])
+// A thread of the epilogue holds one row of the output tile and 32 of its columns at a time, so
+// that sums along a row stay in registers; what it does with them is the kernel's Epi.
+//
+//   PAIR   256 x bn tiles over SM pairs (cta_group::2), else 128 x bn tiles on one SM each; both
+//          persistent with two accumulator sets, one written out while the next is computed.
+//   z      a matrix of the batch, or (ks > 1) a slice of the reduction of one product.
+//   sym    P and Q are the same matrix: only tiles on or above the diagonal are computed, and the
+//          epilogue writes each to both places.
+// TMA fills what lies outside an operand with zeros, so no size is a multiple of a tile.  Every wait
+// is bounded, as in linear.cuh.
+#pragma once
+
+#include "linear.cuh"
+
+namespace lmoe {
+
+struct TileArgs {
+  int R, C, D;          // output rows and columns, reduction length
+  int batch;            // matrices
+  int ks;               // slices of the reduction (batch is 1)
+  int sym;
+  int bn, stages;
+  int p_rows;           // rows of P's K-major boxes (one SM: no more than R, rounded up to 8)
+  int mt, nt, per;      // tiles along rows and columns, tiles of one z
+  int64_t tiles;        // in all
+  int inject_stall;     // test hook: the MMA role first waits on a barrier nobody arrives on
+  uint32_t* err;
+  unsigned long long timeout_ns;
+};
+
+struct TileMaps {
+  CUtensorMap p, q;
+  CUtensorMap out0, out1;  // for the epilogue's tensor stores
+};
+
+struct Tile {
+  int z, row0, col0;
+  int kb0, nk;   // K-blocks
+  bool diag;     // sym: on the diagonal
+};
+
+__device__ __forceinline__ Tile tile_at(const TileArgs& g, int64_t index, int TM) {
+  Tile t;
+  t.z = static_cast<int>(index / g.per);
+  const int local = static_cast<int>(index % g.per);
+  t.diag = false;
+  if (g.sym) {
+    // row i has mt - i tiles: i is the last one whose first tile, i mt - i (i - 1) / 2, is at most
+    // `local`
+    const float n = static_cast<float>(2 * g.mt + 1);
+    int i = static_cast<int>((n - sqrtf(n * n - 8.0f * static_cast<float>(local))) * 0.5f);
+    auto first = [&](int r) { return r * g.mt - r * (r - 1) / 2; };
+    while (i > 0 && first(i) > local) --i;
+    while (i + 1 < g.mt && first(i + 1) <= local) ++i;
+    const int j = i + local - first(i);
+    t.row0 = i * TM;
+    t.col0 = j * g.bn;
+    t.diag = i == j;
+  } else {
+    const LinearTile p = linear_tile(local, g.mt, g.nt, TM, g.bn);
+    t.row0 = p.row0;
+    t.col0 = p.col0;
+  }
+  const int nkb = (g.D + BLOCK_K - 1) / BLOCK_K;
+  t.kb0 = 0;
+  t.nk = nkb;
+  if (g.ks > 1) {
+    t.kb0 = static_cast<int>(static_cast<int64_t>(nkb) * t.z / g.ks);
+    t.nk = static_cast<int>(static_cast<int64_t>(nkb) * (t.z + 1) / g.ks) - t.kb0;
+  }
+  return t;
+}
+
+__device__ __forceinline__ void tile_fail(const TileArgs& g, volatile int* abort_flag,
+                                          uint32_t code) {
+  *abort_flag = 1;
+  atomicOr(g.err, code);
+}
+
+// What an epilogue is given of a tile: this thread's row of it is row0 + row.
+struct TileCtx {
+  const TileMaps* maps;
+  Tile t;
+  int row;        // of the output
+  int half;       // which of the two warps of this TMEM lane quarter: they take chunks in turn
+  int warp_row;   // the warp's first row
+  int lane;
+  uint8_t* buf;   // this warp's TILE_BUF bytes, 1024-byte aligned
+};
+constexpr int TILE_BUF = 4096;
+constexpr int TILE_CHUNK = 32;  // columns of a chunk
+
+constexpr int tile_stage_bytes(bool pair, int bn) { return LINEAR_P_BYTES + (pair ? bn / 2 : bn) * 128; }
+constexpr int tile_smem_bytes(bool pair, int bn, int stages) {
+  return stages * tile_stage_bytes(pair, bn) + 8 * TILE_BUF + LINEAR_MISC + 1024;
+}
+
+// A warp's 32 rows of 32 16-bit values (16 words a thread) into a tensor store of the 64-byte
+// swizzle, whose map cuts off what lies outside.  `buf`: 2 KB that no earlier store still reads.
+__device__ __forceinline__ void tile_store16(const CUtensorMap* m, uint8_t* buf, int lane,
+                                             const uint32_t (&w)[16], int row, int col, int z) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    reinterpret_cast<uint4*>(buf + lane * 64)[j ^ ((lane >> 1) & 3)] =
+        make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+  ptx::fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    ptx::tma_store_3d(m, buf, col, row, z);
+    ptx::bulk_commit_group();
+  }
+}
+// The same turned round: the map's rows are the values' columns.
+__device__ __forceinline__ void tile_store16_turned(const CUtensorMap* m, uint8_t* buf, int lane,
+                                                    const uint32_t (&w)[16], int row, int col,
+                                                    int z) {
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int r = 2 * j + h;  // this thread's column r is element `lane` of row r
+      reinterpret_cast<uint16_t*>(buf + r * 64)[(((lane >> 3) ^ ((r >> 1) & 3)) << 3) + (lane & 7)] =
+          static_cast<uint16_t>(w[j] >> (16 * h));
+    }
+  }
+  ptx::fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    ptx::tma_store_3d(m, buf, row, col, z);
+    ptx::bulk_commit_group();
+  }
+}
+// 32 fp32 values a thread, the 128-byte swizzle, 4 KB.
+__device__ __forceinline__ void tile_store32(const CUtensorMap* m, uint8_t* buf, int lane,
+                                             const float (&v)[32], int row, int col, int z) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    reinterpret_cast<float4*>(buf + lane * 128)[j ^ (lane & 7)] =
+        make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+  ptx::fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    ptx::tma_store_3d(m, buf, col, row, z);
+    ptx::bulk_commit_group();
+  }
+}
+// The warp's earlier tensor stores have read its buffer.
+__device__ __forceinline__ void tile_buf_free(int lane) {
+  if (lane == 0) ptx::bulk_wait_group_read<0>();
+  __syncwarp();
+}
+
+// Epi: a struct of arguments with
+//   struct State; void begin(TileCtx, State&); void load(TileCtx, int col, State&), which fetches
+//   what the chunk at column `col` needs; void chunk(TileCtx, int col, State&, float (&v)[32]);
+//   void end(TileCtx, State&).
+// load is called one chunk ahead of chunk.
+template <bool PAIR, bool P_MN, bool Q_MN, bool F16, class Epi>
+__global__ void __launch_bounds__(LINEAR_THREADS, 1)
+tile_kernel(const __grid_constant__ TileMaps maps, const TileArgs g, const Epi epi) {
+  const int bn = g.bn, stages = g.stages;
+  constexpr int TM = PAIR ? 2 * BLOCK_M : BLOCK_M;
+  constexpr int TMEM_COLS = 512;  // two accumulator sets, 256 columns apart
+  const int qn = PAIR ? bn / 2 : bn;  // columns of Q that this CTA stages
+  const int stage_bytes = LINEAR_P_BYTES + qn * 128;
+  extern __shared__ uint8_t smem_raw[];
+  const LinearSmem m = linear_smem(smem_raw, stages * stage_bytes + 8 * TILE_BUF);
+  uint64_t *tfull = m.extra, *tempty = m.extra + 2, *drain = m.extra + 4;
+  volatile int* abort_flag = m.abort_flag;
+  const int rank = PAIR ? static_cast<int>(ptx::cluster_ctarank()) : 0;
+  const bool lead = rank == 0;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint64_t limit = g.timeout_ns;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < stages; ++s) {
+      ptx::mbar_init(&m.full[s], 1);
+      ptx::mbar_init(&m.empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      ptx::mbar_init(&tfull[a], 1);
+      ptx::mbar_init(&tempty[a], PAIR ? 2 * 8 : 8);  // the epilogue warps
+    }
+    ptx::mbar_init(drain, 1);
+    *abort_flag = 0;
+    ptx::fence_mbar_init();
+    ptx::prefetch_tmap(&maps.p);
+    ptx::prefetch_tmap(&maps.q);
+  }
+  if constexpr (PAIR) ptx::cluster_sync();  // both CTAs' barriers exist before either signals
+  if (warp == 1) {
+    if constexpr (PAIR) {
+      ptx::tmem_alloc_pair(m.tmem_slot, TMEM_COLS);
+      ptx::tmem_relinquish_pair();
+    } else {
+      ptx::tmem_alloc(m.tmem_slot, TMEM_COLS);
+      ptx::tmem_relinquish();
+    }
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem_base = *m.tmem_slot;
+  pdl_wait();  // from here on: the previous kernel's outputs are visible
+  pdl_launch_dependents();
+  const int64_t first = PAIR ? ptx::cluster_id_x() : blockIdx.x;
+  const int64_t step = PAIR ? ptx::ncluster_x() : gridDim.x;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ------------------------------------------------------------ TMA producer (both ranks)
+      uint32_t it = 0, parity = 1;
+      int s = 0;
+      bool ok = true;
+      const uint32_t bytes =
+          (P_MN ? LINEAR_P_BYTES : static_cast<uint32_t>(g.p_rows) * 128u) + qn * 128u;
+      for (int64_t index = first; ok && index < g.tiles; index += step) {
+        const Tile t = tile_at(g, index, TM);
+        const int prow = t.row0 + rank * BLOCK_M, qrow = t.col0 + rank * qn;
+        const int z = g.ks > 1 ? 0 : t.z;
+        for (int kb = 0; kb < t.nk; ++kb, ++it) {
+          if (!ptx::mbar_wait(&m.empty[s], parity, abort_flag, limit)) {
+            tile_fail(g, abort_flag, DEVERR_TIMEOUT_PRODUCER);
+            ok = false;
+            break;
+          }
+          uint8_t* sp = m.base + s * stage_bytes;
+          uint8_t* sq = sp + LINEAR_P_BYTES;
+          const uint32_t fb = PAIR ? ptx::mapa_shared(ptx::smem_u32(&m.full[s]), 0) : 0u;
+          if (lead) ptx::mbar_arrive_expect_tx(&m.full[s], (PAIR ? 2u : 1u) * bytes);
+          const int k = (t.kb0 + kb) * BLOCK_K;
+          auto load = [&](uint8_t* dst, const CUtensorMap* map, int c0, int c1) {
+            if constexpr (PAIR)
+              ptx::tma_load_3d_pair(dst, map, fb, c0, c1, z);
+            else
+              ptx::tma_load_3d(dst, map, &m.full[s], c0, c1, z);
+          };
+          if constexpr (P_MN) {
+#pragma unroll
+            for (int b = 0; b < BLOCK_M / 64; ++b)
+              load(sp + b * LINEAR_BOX_BYTES, &maps.p, prow + 64 * b, k);
+          } else {
+            load(sp, &maps.p, k, prow);
+          }
+          if constexpr (Q_MN) {
+            for (int b = 0; b < qn / 64; ++b)
+              load(sq + b * LINEAR_BOX_BYTES, &maps.q, qrow + 64 * b, k);
+          } else {
+            load(sq, &maps.q, k, qrow);
+          }
+          if (++s == stages) s = 0, parity ^= 1u;
+        }
+      }
+      // every issued copy lands before the CTA (rank 0's barriers: the pair) leaves
+      if (lead) {
+        const uint32_t n = static_cast<uint32_t>(stages);
+        for (uint32_t j = it > n ? it - n : 0u; j < it; ++j)
+          if (!linear_drain(&m.full[j % n], (j / n) & 1u, limit)) {
+            tile_fail(g, abort_flag, DEVERR_TIMEOUT_DRAIN);
+            break;
+          }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && lead) {
+      // ------------------------------------------------------------ MMA issuer (rank 0)
+      const uint32_t idesc = (F16 ? ptx::idesc_f16_f32(TM, bn) : ptx::idesc_bf16_f32(TM, bn)) |
+                             (P_MN ? 1u << 15 : 0u) | (Q_MN ? 1u << 16 : 0u);
+      uint32_t parity = 0;
+      int s = 0, lt = 0;
+      bool ok = !g.inject_stall || ptx::mbar_wait(drain, 0, abort_flag, limit);
+      if (!ok) tile_fail(g, abort_flag, DEVERR_TIMEOUT_MMA);
+      for (int64_t index = first; ok && index < g.tiles; index += step, ++lt) {
+        const Tile t = tile_at(g, index, TM);
+        const int acc = lt & 1;
+        if (!ptx::mbar_wait(&tempty[acc], ((lt >> 1) & 1) ^ 1, abort_flag, limit)) {
+          tile_fail(g, abort_flag, DEVERR_TIMEOUT_MMA);
+          break;
+        }
+        ptx::tc_fence_after();
+        const uint32_t d = tmem_base + static_cast<uint32_t>(acc * 256);
+        for (int kb = 0; kb < t.nk; ++kb) {
+          if (!ptx::mbar_wait(&m.full[s], parity, abort_flag, limit)) {
+            tile_fail(g, abort_flag, DEVERR_TIMEOUT_MMA);
+            ok = false;
+            break;
+          }
+          ptx::tc_fence_after();
+          const uint32_t sp = ptx::smem_u32(m.base + s * stage_bytes);
+          const uint32_t sq = sp + LINEAR_P_BYTES;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint64_t da = P_MN ? ptx::smem_desc_sw128_mn(sp + k * 2048, LINEAR_BOX_BYTES)
+                                     : ptx::smem_desc_sw128(sp + k * 32);
+            const uint64_t db = Q_MN ? ptx::smem_desc_sw128_mn(sq + k * 2048, LINEAR_BOX_BYTES)
+                                     : ptx::smem_desc_sw128(sq + k * 32);
+            const uint32_t add = kb == 0 && k == 0 ? 0u : 1u;
+            if constexpr (PAIR)
+              ptx::umma_bf16_pair(d, da, db, idesc, add);
+            else
+              ptx::umma_bf16(d, da, db, idesc, add);
+          }
+          if constexpr (PAIR)
+            ptx::umma_commit_pair(&m.empty[s], 0x3);
+          else
+            ptx::umma_commit(&m.empty[s]);
+          if (++s == stages) s = 0, parity ^= 1u;
+        }
+        if (ok) {
+          if constexpr (PAIR)
+            ptx::umma_commit_pair(&tfull[acc], 0x3);
+          else
+            ptx::umma_commit(&tfull[acc]);
+        }
+      }
+      // all MMAs issued by this thread complete before TMEM is released
+      if constexpr (PAIR)
+        ptx::umma_commit_pair(drain, 0x1);
+      else
+        ptx::umma_commit(drain);
+      if (!linear_drain(drain, 0u, limit)) tile_fail(g, abort_flag, DEVERR_TIMEOUT_DRAIN);
+    }
+  } else {
+    // -------------------------------------------------------------- epilogue (warps 2..9)
+    const int q = warp & 3, half = (warp - 2) >> 2;
+    TileCtx c;
+    c.maps = &maps;
+    c.half = half;
+    c.lane = lane;
+    c.buf = m.base + stages * stage_bytes + (warp - 2) * TILE_BUF;
+    const uint32_t te[2] = {PAIR ? ptx::mapa_shared(ptx::smem_u32(&tempty[0]), 0) : 0u,
+                            PAIR ? ptx::mapa_shared(ptx::smem_u32(&tempty[1]), 0) : 0u};
+    typename Epi::State st;
+    int lt = 0;
+    for (int64_t index = first; index < g.tiles; index += step, ++lt) {
+      c.t = tile_at(g, index, TM);
+      c.warp_row = c.t.row0 + rank * BLOCK_M + q * 32;
+      c.row = c.warp_row + lane;
+      const int acc = lt & 1;
+      // a warp whose rows lie outside has nothing to do
+      const int cols = c.warp_row < g.R ? min(bn, g.C - c.t.col0) : 0;
+      const int chunks = (cols + TILE_CHUNK - 1) / TILE_CHUNK;
+      if (half < chunks) {
+        epi.begin(g, c, st);
+        epi.load(g, c, c.t.col0 + half * TILE_CHUNK, st);
+      }
+      const bool got = ptx::mbar_wait(&tfull[acc], (lt >> 1) & 1, abort_flag, limit);
+      if (!__all_sync(0xffffffffu, got)) {
+        if (lane == 0) tile_fail(g, abort_flag, DEVERR_TIMEOUT_EPILOGUE);
+        break;
+      }
+      ptx::tc_fence_after();
+      const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
+                          static_cast<uint32_t>(acc * 256);
+      auto release = [&]() {  // this warp has read its part of the accumulator
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (PAIR && !lead)
+            ptx::mbar_arrive_cluster(te[acc]);
+          else
+            ptx::mbar_arrive(&tempty[acc]);
+        }
+      };
+      if (half >= chunks) release();
+#pragma unroll 1
+      for (int ch = half; ch < chunks; ch += 2) {
+        float v[32];
+        ptx::tmem_ld_32x32b_x32(tb + static_cast<uint32_t>(ch * TILE_CHUNK), v);
+        if (ch + 2 >= chunks) release();
+        const int col = c.t.col0 + ch * TILE_CHUNK;
+        epi.chunk(g, c, col, st, v, ch + 2 < chunks ? col + 2 * TILE_CHUNK : -1);
+      }
+      if (half < chunks) epi.end(g, c, st);
+    }
+    // the tensor stores complete before the CTA leaves (they read its shared memory)
+    if (lane == 0) ptx::bulk_wait_group_all();
+  }
+
+  ptx::tc_fence_before();
+  __syncthreads();
+  if constexpr (PAIR) ptx::cluster_sync();  // the peer is done with this CTA's barriers and TMEM
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    if constexpr (PAIR)
+      ptx::tmem_dealloc_pair(tmem_base, TMEM_COLS);
+    else
+      ptx::tmem_dealloc(tmem_base, TMEM_COLS);
+  }
+}
+
+// ------------------------------------------------------------------------- host side
+// An operand as stored: `rows` of `cols` elements ld apart, matrices `stride` apart.
+struct TileOperand {
+  const void* p;
+  int64_t rows, cols, ld, stride;
+};
+inline bool tile_map(CUtensorMap* m, const TileOperand& o, int batch, bool mn, int box_rows) {
+  const uint64_t dims[3] = {static_cast<uint64_t>(o.cols), static_cast<uint64_t>(o.rows),
+                            static_cast<uint64_t>(batch)};
+  const uint64_t strides[2] = {static_cast<uint64_t>(o.ld) * 2,
+                               static_cast<uint64_t>(batch > 1 ? o.stride : o.rows * o.ld) * 2};
+  const uint32_t box[3] = {64, static_cast<uint32_t>(mn ? 64 : box_rows), 1};
+  return make_tmap_boxes(m, o.p, 3, dims, strides, box);
+}
+
+// Tiles of a product, by time: `bn` is 0 for the least of an estimate over SM pairs of 256 columns
+// and single SMs of 64 to 256, else given for one SM alone.  The estimate's constants are those of
+// the linear layers: FLOP/ns of an SM's MMAs, bytes/ns into an SM's stages, ns per accumulator
+// column of a tile's epilogue.
+struct TilePlan {
+  bool pair;
+  int bn;
+  double ns;
+};
+inline TilePlan tile_plan(int64_t R, int64_t C, int64_t D, int64_t batch, bool sym, int sms) {
+  constexpr double RATE = 12500.0, FEED = 150.0, EPILOGUE = 11.0;
+  const double nk = static_cast<double>(ceil_div(D, BLOCK_K));
+  TilePlan best{false, 128, 1e300};
+  auto offer = [&](bool pair, int bn) {
+    const int64_t tm = pair ? 256 : 128, mt = ceil_div(R, tm), nt = ceil_div(C, bn);
+    const int64_t tiles = batch * (sym ? mt * (mt + 1) / 2 : mt * nt);
+    const int64_t units = pair ? sms / 2 : sms;
+    const double mma = 2.0 * BLOCK_K * BLOCK_M * bn / RATE;
+    const double feed = tile_stage_bytes(pair, bn) / FEED;
+    double tile = nk * (mma > feed ? mma : feed);
+    if (tile < EPILOGUE * bn) tile = EPILOGUE * bn;
+    const double ns = static_cast<double>(ceil_div(tiles, units)) * tile + EPILOGUE * bn + 200.0;
+    if (ns < best.ns) best = {pair, bn, ns};
+  };
+  offer(true, 256);
+  offer(false, 128);
+  if (!sym) {
+    offer(false, 64);
+    offer(false, 256);
+  }
+  return best;
+}
+
+// Fills the plan's part of g, encodes P and Q and launches.  maps: the epilogue's are already there.
+template <bool PAIR, bool P_MN, bool Q_MN, bool F16, class Epi>
+int launch_tile(const TileOperand& P, const TileOperand& Q, TileMaps& maps, TileArgs g,
+                const Epi& epi, int bn, int dev, int sms, cudaStream_t stream) {
+  static std::atomic<int> cache[LINEAR_MAX_DEVICES];
+  auto kernel = tile_kernel<PAIR, P_MN, Q_MN, F16, Epi>;
+  const int active = linear_kernel_setup(kernel, PAIR ? 2 : 1, dev, cache);
+  if (active < 0) return LMOE_ERR_CUDA;
+  constexpr int TM = PAIR ? 2 * BLOCK_M : BLOCK_M;
+  g.bn = bn;
+  g.stages = LINEAR_MAX_STAGES;
+  while (tile_smem_bytes(PAIR, bn, g.stages) > LINEAR_SMEM_MAX) --g.stages;
+  g.p_rows = PAIR || g.R >= BLOCK_M ? BLOCK_M : (g.R + 7) / 8 * 8;
+  g.mt = static_cast<int>(ceil_div(g.R, TM));
+  g.nt = static_cast<int>(ceil_div(g.C, bn));
+  const int64_t per = g.sym ? static_cast<int64_t>(g.mt) * (g.mt + 1) / 2
+                            : static_cast<int64_t>(g.mt) * g.nt;
+  if (per > (1 << 27)) return LMOE_ERR_UNSUPPORTED;
+  g.per = static_cast<int>(per);
+  g.tiles = per * (g.ks > 1 ? g.ks : g.batch);
+  g.timeout_ns = wait_limit_ns();
+  if (!tile_map(&maps.p, P, g.batch, P_MN, g.p_rows) ||
+      !tile_map(&maps.q, Q, g.batch, Q_MN, PAIR ? bn / 2 : bn))
+    return LMOE_ERR_CUDA;
+  int64_t units = PAIR ? sms / 2 : sms;
+  if (PAIR && active > 0 && units > active) units = active;
+  if (units > g.tiles) units = g.tiles;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((PAIR ? 2 : 1) * units));
+  cfg.blockDim = dim3(LINEAR_THREADS);
+  cfg.dynamicSmemBytes = static_cast<size_t>(tile_smem_bytes(PAIR, bn, g.stages));
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = PAIR ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, maps, g, epi) == cudaSuccess ? LMOE_OK : LMOE_ERR_CUDA;
+}
+// The plan's choice between the two forms.
+template <bool P_MN, bool Q_MN, bool F16, class Epi>
+int launch_tile(const TileOperand& P, const TileOperand& Q, TileMaps& maps, const TileArgs& g,
+                const Epi& epi, const TilePlan& plan, int dev, int sms, cudaStream_t stream) {
+  return plan.pair
+             ? launch_tile<true, P_MN, Q_MN, F16>(P, Q, maps, g, epi, plan.bn, dev, sms, stream)
+             : launch_tile<false, P_MN, Q_MN, F16>(P, Q, maps, g, epi, plan.bn, dev, sms, stream);
+}
+
+}  // namespace lmoe

@@ -1,0 +1,478 @@
+// xent.cu -- softmax cross entropy of a linear head over a large vocabulary, and its gradients,
+// without the logits in memory (matrix products in tile.cuh):
+//   l = x w^T,  lse = log sum exp l,  loss = lse - l[target]
+//   d = g (exp(l - lse) - onehot(target)),  dx = d w,  dw = d^T x
+// Forward: the products' epilogue, which holds rows of logits in registers, keeps a running maximum
+// and sum of its columns; a second kernel joins the tiles' (maximum, sum) in a fixed order.
+// Backward: for one piece of the vocabulary after the other the logits are computed again, d goes
+// to scratch as bf16, and both products read it there.
+#include "tile.cuh"
+
+namespace lmoe {
+
+constexpr float LOG2E = 1.4426950408889634f;
+
+// What sums with maximum m are taken relative to: m, or 0 where that is infinite, so that an
+// infinite logit gives an infinite sum and rows of -inf a sum of 0.
+__device__ __forceinline__ float lse_base(float m) { return fabsf(m) < INFINITY ? m : 0.0f; }
+__device__ __forceinline__ float lse_factor(float m, float to) {
+  return m == to ? 1.0f : exp2f((m - to) * LOG2E);
+}
+__device__ __forceinline__ void lse_join(float& m, float& s, float m2, float s2) {
+  const float top = fmaxf(m, m2);
+  s = s * lse_factor(m, top) + s2 * lse_factor(m2, top);
+  m = top;
+}
+
+struct XentTarget {
+  const void* p;
+  int wide;  // int64, else int32
+  int V;
+  // the row's target, -1 where it has none
+  __device__ __forceinline__ int of(int row) const {
+    const long long t = wide ? __ldg(static_cast<const long long*>(p) + row)
+                             : __ldg(static_cast<const int*>(p) + row);
+    return t >= 0 && t < V ? static_cast<int>(t) : -1;
+  }
+};
+
+// ------------------------------------------------------------------------- forward
+struct LseEpi {
+  XentTarget target;
+  float2* part;    // [2 tile columns][M] (maximum, sum)
+  float* picked;   // [M] the targets' logits
+  struct State {
+    float m, s;
+    int target;
+  };
+  __device__ __forceinline__ void begin(const TileArgs& g, const TileCtx& c, State& st) const {
+    st.m = -INFINITY;
+    st.s = 0.0f;
+    st.target = c.row < g.R ? target.of(c.row) : -1;
+  }
+  __device__ __forceinline__ void load(const TileArgs&, const TileCtx&, int, State&) const {}
+  __device__ __forceinline__ void chunk(const TileArgs& g, const TileCtx& c, int col, State& st,
+                                        float (&v)[32], int) const {
+    if (col + 32 > g.C) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (col + j >= g.C) v[j] = -INFINITY;
+    }
+    const int at = st.target - col;
+    if (at >= 0 && at < 32) {
+      float l = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 32; ++j) l = j == at ? v[j] : l;
+      picked[c.row] = l;
+    }
+    float top[4] = {st.m, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+    for (int j = 0; j < 32; ++j) top[j & 3] = fmaxf(top[j & 3], v[j]);
+    const float m = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), base = lse_base(m);
+    float sum[4] = {st.s * lse_factor(st.m, m), 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int j = 0; j < 32; ++j) sum[j & 3] += exp2f((v[j] - base) * LOG2E);
+    st.s = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+    st.m = m;
+  }
+  __device__ __forceinline__ void end(const TileArgs& g, const TileCtx& c, State& st) const {
+    if (c.row < g.R)
+      part[static_cast<int64_t>(c.t.col0 / g.bn * 2 + c.half) * g.R + c.row] =
+          make_float2(st.m, st.s);
+  }
+};
+
+// lse and loss of 32 rows a block from the tiles' parts: a warp takes every 32nd part, the warps'
+// are joined in order.
+constexpr int JOIN_WARPS = 32;
+__global__ void __launch_bounds__(JOIN_WARPS * 32)
+lse_join_kernel(const float2* __restrict__ part, int parts, int M, XentTarget target,
+                const float* __restrict__ picked, float* __restrict__ loss,
+                float* __restrict__ lse) {
+  __shared__ float2 red[JOIN_WARPS][32];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int row = blockIdx.x * 32 + lane;
+  float m = -INFINITY, s = 0.0f;
+  if (row < M) {
+#pragma unroll 8
+    for (int p = w; p < parts; p += JOIN_WARPS) {
+      const float2 v = __ldg(part + static_cast<int64_t>(p) * M + row);
+      lse_join(m, s, v.x, v.y);
+    }
+  }
+  red[w][lane] = make_float2(m, s);
+  __syncthreads();
+  if (w != 0 || row >= M) return;
+  for (int i = 1; i < JOIN_WARPS; ++i) lse_join(m, s, red[i][lane].x, red[i][lane].y);
+  const float l = lse_base(m) + logf(s);
+  if (lse) lse[row] = l;
+  if (loss) loss[row] = target.of(row) >= 0 ? l - picked[row] : 0.0f;
+}
+
+// ------------------------------------------------------------------------- backward
+// d of a piece of the vocabulary, from column `col0` on.
+struct XentGradEpi {
+  XentTarget target;
+  const float* lse;
+  const float* dloss;
+  int col0;
+  struct State {
+    float lse, g;
+    int target;
+  };
+  __device__ __forceinline__ void begin(const TileArgs& g, const TileCtx& c, State& st) const {
+    st.target = c.row < g.R ? target.of(c.row) : -1;
+    st.lse = st.g = 0.0f;
+    if (st.target >= 0) {
+      st.lse = __ldg(lse + c.row);
+      st.g = __ldg(dloss + c.row);
+      st.target -= col0;
+    } else {
+      st.target = INT32_MIN;
+    }
+  }
+  __device__ __forceinline__ void load(const TileArgs&, const TileCtx&, int, State&) const {}
+  __device__ __forceinline__ void chunk(const TileArgs&, const TileCtx& c, int col, State& st,
+                                        float (&v)[32], int) const {
+    uint32_t w[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      float d[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float p = exp2f((v[2 * j + h] - st.lse) * LOG2E);
+        d[h] = st.g * (p - (st.target == col + 2 * j + h ? 1.0f : 0.0f));
+        if (st.target == INT32_MIN) d[h] = 0.0f;  // whatever its logits are
+      }
+      const __nv_bfloat162 b = __floats2bfloat162_rn(d[0], d[1]);
+      w[j] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    tile_buf_free(c.lane);
+    tile_store16(&c.maps->out0, c.buf, c.lane, w, c.warp_row, col, 0);
+  }
+  __device__ __forceinline__ void end(const TileArgs&, const TileCtx&, State&) const {}
+};
+
+// dx's fp32 sums [ks][M, K] over the pieces.
+struct XentDxEpi {
+  float* sum;
+  int add;  // not the first piece
+  struct State {
+    float4 next[8];
+  };
+  __device__ __forceinline__ float4* at(const TileArgs& g, const TileCtx& c, int col) const {
+    return reinterpret_cast<float4*>(
+        sum + (static_cast<int64_t>(g.ks > 1 ? c.t.z : 0) * g.R + c.row) * g.C + col);
+  }
+  __device__ __forceinline__ void begin(const TileArgs&, const TileCtx&, State&) const {}
+  __device__ __forceinline__ void load(const TileArgs& g, const TileCtx& c, int col,
+                                       State& st) const {
+    if (!add || c.row >= g.R) return;
+    const float4* p = at(g, c, col);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (col + 4 * j < g.C) st.next[j] = p[j];
+  }
+  __device__ __forceinline__ void chunk(const TileArgs& g, const TileCtx& c, int col, State& st,
+                                        float (&v)[32], int next) const {
+    if (add) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        v[4 * j] += st.next[j].x;
+        v[4 * j + 1] += st.next[j].y;
+        v[4 * j + 2] += st.next[j].z;
+        v[4 * j + 3] += st.next[j].w;
+      }
+      if (next >= 0) load(g, c, next, st);
+    }
+    if (c.row >= g.R) return;
+    float4* p = at(g, c, col);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (col + 4 * j < g.C)
+        p[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+  }
+  __device__ __forceinline__ void end(const TileArgs&, const TileCtx&, State&) const {}
+};
+
+// A plain output, bf16 or fp32.
+struct StoreEpi {
+  int f32;
+  struct State {};
+  __device__ __forceinline__ void begin(const TileArgs&, const TileCtx&, State&) const {}
+  __device__ __forceinline__ void load(const TileArgs&, const TileCtx&, int, State&) const {}
+  __device__ __forceinline__ void chunk(const TileArgs&, const TileCtx& c, int col, State&,
+                                        float (&v)[32], int) const {
+    tile_buf_free(c.lane);
+    if (f32) {
+      tile_store32(&c.maps->out0, c.buf, c.lane, v, c.warp_row, col, c.t.z);
+      return;
+    }
+    uint32_t w[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+      w[j] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    tile_store16(&c.maps->out0, c.buf, c.lane, w, c.warp_row, col, c.t.z);
+  }
+  __device__ __forceinline__ void end(const TileArgs&, const TileCtx&, State&) const {}
+};
+
+// dx = the slices' sums added in order, rounded to bf16; a thread takes eight columns.
+__global__ void __launch_bounds__(256)
+xent_dx_kernel(const float* __restrict__ sum, int ks, int64_t M, int K, __nv_bfloat16* dx,
+               int64_t lddx) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int per = K / 8;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= M * per) return;
+  const int64_t row = i / per;
+  const int col = static_cast<int>(i % per) * 8;
+  float a[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) a[j] = 0.0f;
+  for (int s = 0; s < ks; ++s) {
+    float f[8];
+    linear_read8(sum + (s * M + row) * K + col, f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) a[j] += f[j];
+  }
+  *reinterpret_cast<uint4*>(dx + row * lddx + col) = linear_pack8(a);
+}
+
+// ------------------------------------------------------------------------- host side
+// Up to 128 rows the head's way from HBM is the time: tiles of 128 rows, of as many columns as
+// deals the vocabulary evenly to the SMs.
+static TilePlan lse_plan(int64_t M, int64_t V, int64_t K, int sms) {
+  if (M > BLOCK_M) return tile_plan(M, V, K, 1, false, sms);
+  TilePlan best{false, 256, 1e300};
+  for (int bn = 64; bn <= 256; bn += 32) {
+    const double ns = static_cast<double>(ceil_div(ceil_div(V, bn), sms)) * (bn + 16);
+    if (ns < best.ns) best = {false, bn, ns};
+  }
+  return best;
+}
+
+struct XentLayout {
+  size_t part, picked, total;
+};
+// The parts are those of the narrowest tiles, so that the size is the same on every device.
+static XentLayout xent_layout(const lmoe_linear_xent& p) {
+  XentLayout L{};
+  L.picked = (static_cast<size_t>(ceil_div(p.V, 64)) * 2 * p.M * sizeof(float2) + 255) / 256 * 256;
+  L.total = L.picked + static_cast<size_t>(p.M) * sizeof(float);
+  return L;
+}
+
+// Backward: a piece's d is about 256 MB (it is written once and read twice), and at least 4096
+// columns, which the products that read it need to be worth their sums' way through memory.
+constexpr int64_t XENT_PIECE_BYTES = int64_t{256} << 20;
+constexpr int XENT_PIECE_MIN = 4096;
+constexpr int XENT_MAX_SLICES = 32;
+struct XentBwdLayout {
+  int64_t piece, ldd;  // columns of a piece; distance between rows of d
+  int slices;          // at most
+  size_t d, sum, total;
+};
+static XentBwdLayout xent_bwd_layout(const lmoe_linear_xent& p) {
+  XentBwdLayout L{};
+  L.piece = XENT_PIECE_BYTES / 2 / p.M / 256 * 256;
+  if (L.piece < XENT_PIECE_MIN) L.piece = XENT_PIECE_MIN;
+  if (L.piece > p.V) L.piece = p.V;
+  L.ldd = ceil_div(L.piece, 8) * 8;
+  // slices of dx's reduction while its tiles would leave SMs idle
+  const int64_t tiles = ceil_div(p.M, BLOCK_M) * ceil_div(p.K, 256);
+  int64_t s = 152 / tiles;
+  if (s > ceil_div(L.piece, BLOCK_K) / 8) s = ceil_div(L.piece, BLOCK_K) / 8;
+  if (s > XENT_MAX_SLICES) s = XENT_MAX_SLICES;
+  L.slices = s < 1 ? 1 : static_cast<int>(s);
+  L.d = 0;
+  L.sum = (static_cast<size_t>(p.M) * L.ldd * 2 + 255) / 256 * 256;
+  L.total = L.sum + static_cast<size_t>(L.slices) * p.M * p.K * sizeof(float);
+  return L;
+}
+
+static int xent_sizes_ok(const lmoe_linear_xent* p) {
+  if (!p || p->M < 0 || p->V < 1 || p->K < 1) return LMOE_ERR_INVALID_ARG;
+  if (p->target_type != LMOE_I32 && p->target_type != LMOE_I64) return LMOE_ERR_INVALID_ARG;
+  constexpr int MOST = 1 << 30;
+  if (p->K % 8 || p->M > MOST || p->V > MOST || p->K > MOST) return LMOE_ERR_UNSUPPORTED;
+  if (ceil_div(p->M, 64) * ceil_div(p->V, 64) > (1 << 27) ||
+      ceil_div(p->M, 64) * ceil_div(p->K, 64) > (1 << 27) ||
+      ceil_div(p->V, 64) * ceil_div(p->K, 64) > (1 << 27))
+    return LMOE_ERR_UNSUPPORTED;
+  if (p->ldx < p->K || p->ldw < p->K || p->ldx % 8 || p->ldw % 8) return LMOE_ERR_INVALID_ARG;
+  return LMOE_OK;
+}
+
+static bool aligned(const void* p, uintptr_t to) {
+  return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0;
+}
+static int xent_inputs_ok(const lmoe_linear_xent* p) {
+  if (!p->x || !p->w || !p->target || !p->dev_flag) return LMOE_ERR_INVALID_ARG;
+  if (!aligned(p->x, 16) || !aligned(p->w, 16) || !aligned(p->dev_flag, 4) ||
+      !aligned(p->target, p->target_type == LMOE_I64 ? 8 : 4) || !aligned(p->loss, 4) ||
+      !aligned(p->lse, 4))
+    return LMOE_ERR_INVALID_ARG;
+  return LMOE_OK;
+}
+
+static TileArgs xent_args(const lmoe_linear_xent& p, int R, int C, int D) {
+  TileArgs g{};
+  g.R = R;
+  g.C = C;
+  g.D = D;
+  g.batch = g.ks = 1;
+  g.err = p.dev_flag;
+  return g;
+}
+
+static int xent_forward(const lmoe_linear_xent& p, uint8_t* ws, cudaStream_t stream) {
+  int dev = 0, sms = 0;
+  if (linear_device(&dev, &sms) != LMOE_OK) return LMOE_ERR_CUDA;
+  const XentLayout L = xent_layout(p);
+  const XentTarget target{p.target, p.target_type == LMOE_I64, p.V};
+  float2* part = reinterpret_cast<float2*>(ws);
+  float* picked = reinterpret_cast<float*>(ws + L.picked);
+  const TilePlan plan = lse_plan(p.M, p.V, p.K, sms);
+  TileArgs g = xent_args(p, p.M, p.V, p.K);
+  g.inject_stall = inject_stall();
+  TileMaps maps{};
+  const int rc = launch_tile<false, false, false>(
+      TileOperand{p.x, p.M, p.K, p.ldx, 0}, TileOperand{p.w, p.V, p.K, p.ldw, 0}, maps, g,
+      LseEpi{target, part, picked}, plan, dev, sms, stream);
+  if (rc != LMOE_OK) return rc;
+  // a last tile of one chunk has one part
+  const int nt = static_cast<int>(ceil_div(p.V, plan.bn));
+  const int parts = 2 * nt - (p.V - (nt - 1) * plan.bn <= TILE_CHUNK ? 1 : 0);
+  return launch_pdl(lse_join_kernel, static_cast<unsigned>(ceil_div(p.M, 32)), JOIN_WARPS * 32, 0,
+                    stream, part, parts, p.M, target, picked, p.loss, p.lse) == cudaSuccess
+             ? LMOE_OK
+             : LMOE_ERR_CUDA;
+}
+
+static int xent_backward(const lmoe_linear_xent& p, const float* dloss, __nv_bfloat16* dx,
+                         int64_t lddx, void* dw, bool dw_f32, uint8_t* ws, cudaStream_t stream) {
+  int dev = 0, sms = 0, rc = LMOE_OK;
+  if (linear_device(&dev, &sms) != LMOE_OK) return LMOE_ERR_CUDA;
+  const XentBwdLayout L = xent_bwd_layout(p);
+  float* sum = reinterpret_cast<float*>(ws + L.sum);
+  const XentTarget target{p.target, p.target_type == LMOE_I64, p.V};
+  const TileOperand X{p.x, p.M, p.K, p.ldx, 0};
+  bool stall = inject_stall();
+  int slices = 1;
+  for (int64_t c0 = 0; c0 < p.V; c0 += L.piece) {
+    const int cols = static_cast<int>(p.V - c0 < L.piece ? p.V - c0 : L.piece);
+    const TileOperand W{static_cast<const __nv_bfloat16*>(p.w) + c0 * p.ldw, cols, p.K, p.ldw, 0};
+    const TileOperand Dl{ws + L.d, p.M, cols, L.ldd, 0};
+    {
+      TileMaps maps{};
+      if (!make_tmap_out32(&maps.out0, ws + L.d, 2, p.M, cols, L.ldd, 1, 0)) return LMOE_ERR_CUDA;
+      TileArgs g = xent_args(p, p.M, cols, p.K);
+      g.inject_stall = stall;
+      stall = false;
+      rc = launch_tile<false, false, false>(
+          X, W, maps, g, XentGradEpi{target, p.lse, dloss, static_cast<int>(c0)},
+          lse_plan(p.M, cols, p.K, sms), dev, sms, stream);
+      if (rc != LMOE_OK) return rc;
+    }
+    if (dx) {
+      TileMaps maps{};
+      TileArgs g = xent_args(p, p.M, p.K, cols);
+      const int nkb = static_cast<int>(ceil_div(cols, BLOCK_K));
+      if (c0 == 0) slices = L.slices;
+      g.ks = slices < nkb ? slices : nkb;
+      const TilePlan plan =
+          slices > 1 ? TilePlan{false, 256, 0.0} : tile_plan(p.M, p.K, cols, 1, false, sms);
+      rc = launch_tile<false, true, false>(Dl, W, maps, g, XentDxEpi{sum, c0 > 0}, plan, dev, sms,
+                                           stream);
+      if (rc != LMOE_OK) return rc;
+    }
+    if (dw) {
+      TileMaps maps{};
+      uint8_t* out = static_cast<uint8_t*>(dw) + c0 * p.K * (dw_f32 ? 4 : 2);
+      if (!make_tmap_out32(&maps.out0, out, dw_f32 ? 4 : 2, cols, p.K, p.K, 1, 0))
+        return LMOE_ERR_CUDA;
+      rc = launch_tile<true, true, false>(Dl, X, maps, xent_args(p, cols, p.K, p.M),
+                                          StoreEpi{dw_f32}, tile_plan(cols, p.K, p.M, 1, false, sms),
+                                          dev, sms, stream);
+      if (rc != LMOE_OK) return rc;
+    }
+  }
+  if (!dx) return LMOE_OK;
+  const int64_t threads = static_cast<int64_t>(p.M) * (p.K / 8);
+  return launch_pdl(xent_dx_kernel, static_cast<unsigned>(ceil_div(threads, 256)), 256, 0, stream,
+                    sum, slices, p.M, p.K, dx, lddx) == cudaSuccess
+             ? LMOE_OK
+             : LMOE_ERR_CUDA;
+}
+
+}  // namespace lmoe
+
+using namespace lmoe;
+
+extern "C" {
+
+size_t lmoe_linear_xent_workspace_bytes(const lmoe_linear_xent* p) {
+  if (xent_sizes_ok(p) != LMOE_OK || p->M == 0) return 0;
+  return xent_layout(*p).total;
+}
+
+int lmoe_linear_xent_forward(const lmoe_linear_xent* p, void* ws, size_t ws_bytes, void* stream) {
+  int rc = xent_sizes_ok(p);
+  if (rc != LMOE_OK) return rc;
+  if (p->M == 0) return LMOE_OK;
+  if ((rc = xent_inputs_ok(p)) != LMOE_OK) return rc;
+  if (!p->loss && !p->lse) return LMOE_ERR_INVALID_ARG;
+  const void* outs[] = {p->loss, p->lse, ws};
+  for (int i = 0; i < 3; ++i) {
+    if (outs[i] && (outs[i] == p->x || outs[i] == p->w || outs[i] == p->target))
+      return LMOE_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (outs[i] && outs[i] == outs[j]) return LMOE_ERR_INVALID_ARG;
+  }
+  if (!ws || !aligned(ws, 16)) return LMOE_ERR_INVALID_ARG;
+  if (ws_bytes < xent_layout(*p).total) return LMOE_ERR_WORKSPACE_TOO_SMALL;
+  return xent_forward(*p, static_cast<uint8_t*>(ws), static_cast<cudaStream_t>(stream));
+}
+
+size_t lmoe_linear_xent_backward_workspace_bytes(const lmoe_linear_xent* p) {
+  if (xent_sizes_ok(p) != LMOE_OK || p->M == 0) return 0;
+  return xent_bwd_layout(*p).total;
+}
+
+int lmoe_linear_xent_backward(const lmoe_linear_xent* p, const float* dloss, void* dx,
+                              long long lddx, void* dw, int dw_type, void* ws, size_t ws_bytes,
+                              void* stream_) {
+  int rc = xent_sizes_ok(p);
+  if (rc != LMOE_OK) return rc;
+  if (dw && dw_type != LMOE_BF16 && dw_type != LMOE_F32) return LMOE_ERR_INVALID_ARG;
+  if (!aligned(dx, 16) || !aligned(dw, 16)) return LMOE_ERR_INVALID_ARG;
+  const cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+  if (p->M == 0) {
+    const size_t bytes = static_cast<size_t>(dw_type == LMOE_F32 ? 4 : 2) * p->V * p->K;
+    return !dw || cudaMemsetAsync(dw, 0, bytes, stream) == cudaSuccess ? LMOE_OK : LMOE_ERR_CUDA;
+  }
+  if ((rc = xent_inputs_ok(p)) != LMOE_OK) return rc;
+  if (!p->lse || !dloss || !aligned(dloss, 4)) return LMOE_ERR_INVALID_ARG;
+  if (dx && (lddx < p->K || lddx % 8)) return LMOE_ERR_INVALID_ARG;
+  if (!dx && !dw) return LMOE_OK;
+  const void* outs[] = {dx, dw, ws};
+  for (int i = 0; i < 3; ++i) {
+    const void* o = outs[i];
+    if (o && (o == p->x || o == p->w || o == p->target || o == p->lse || o == dloss))
+      return LMOE_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (o && o == outs[j]) return LMOE_ERR_INVALID_ARG;
+  }
+  if (!ws || !aligned(ws, 16)) return LMOE_ERR_INVALID_ARG;
+  if (ws_bytes < xent_bwd_layout(*p).total) return LMOE_ERR_WORKSPACE_TOO_SMALL;
+  return xent_backward(*p, dloss, static_cast<__nv_bfloat16*>(dx), lddx, dw, dw_type == LMOE_F32,
+                       static_cast<uint8_t*>(ws), stream);
+}
+
+}  // extern "C"

@@ -67,11 +67,17 @@ class LinearDesc(ctypes.Structure):
                 ("ldy", _ll), ("pre", _vp), ("ldp", _ll), ("dev_flag", _vp)]
 
 
+class LinearXentDesc(ctypes.Structure):
+    _fields_ = [("M", _i), ("V", _i), ("K", _i), ("x", _vp), ("ldx", _ll), ("w", _vp),
+                ("ldw", _ll), ("target", _vp), ("target_type", _i), ("loss", _vp), ("lse", _vp),
+                ("dev_flag", _vp)]
+
+
 # enum lmoe_act
 ACTS = {"none": 0, "silu": 1, "gelu": 2, "situ": 3}
 
 # enum lmoe_type
-BF16, E4M3, F32 = 0, 1, 2
+BF16, E4M3, F32, I32, I64 = 0, 1, 2, 3, 4
 
 # enum lmoe_phase
 PHASE_ALL, PHASE_ROUTER, PHASE_EXPERTS = 0, 1, 2
@@ -114,6 +120,10 @@ SIGNATURES = {
     "lmoe_linear_forward": (_i, [_vp, _vp]),
     "lmoe_linear_backward_workspace_bytes": (_sz, [_vp]),
     "lmoe_linear_backward": (_i, [_vp, _vp, _ll, _vp, _ll, _vp, _i, _vp, _vp, _sz, _vp]),
+    "lmoe_linear_xent_workspace_bytes": (_sz, [_vp]),
+    "lmoe_linear_xent_forward": (_i, [_vp, _vp, _sz, _vp]),
+    "lmoe_linear_xent_backward_workspace_bytes": (_sz, [_vp]),
+    "lmoe_linear_xent_backward": (_i, [_vp, _vp, _vp, _ll, _vp, _i, _vp, _sz, _vp]),
     "lmoe_few_workspace_bytes": (_sz, [ctypes.POINTER(Dims)]),
     "lmoe_forward_few": (_i, [ctypes.POINTER(Dims), _vp, _vp, _vp, _vp, _vp, _sz,
                               ctypes.POINTER(IO), _vp]),
@@ -718,6 +728,92 @@ class Linear:
         if rc:
             _check(rc, "lmoe_linear_backward")
         return {"dx": dx, "dw": dw, "dbias": db}
+
+    def device_error(self) -> int:
+        """LMOE_OK, or LMOE_ERR_DEVICE_TIMEOUT if a device-side wait of an earlier call ran out
+        (its output is not valid); call after the stream has synchronised.  Clears the flag."""
+        return last_device_error(self.flag)
+
+
+class LinearCrossEntropy:
+    """The softmax cross entropy of a linear head w [V, K] bf16 over V tokens, and its gradients,
+    without logits in memory (lmoe_linear_xent_forward / _backward).  K must be a multiple of 8.
+
+    Like ``Linear`` it keeps a reference to w and looks at it at each call: w may be updated in place
+    or replaced by a tensor of the same size and type on the same device."""
+
+    def __init__(self, w: torch.Tensor):
+        self.w = w
+        self.V, self.K = w.shape
+        self.device, self._dev = w.device, _device_of(w, "w")
+        _rows(w, torch.bfloat16, self.V, self.K, self._dev, "w")
+        self.flag = torch.zeros(1, dtype=torch.int32, device=w.device)
+        torch.cuda.current_stream(w.device).synchronize()  # before any stream of the caller's
+        self._flag = self.flag.data_ptr()
+
+    def _desc(self, x, target, loss, lse):
+        dev, M = self._dev, x.shape[0]
+        px, ldx = _rows(x, torch.bfloat16, M, self.K, dev, "x")
+        pw, ldw = _rows(self.w, torch.bfloat16, self.V, self.K, dev, "w")
+        if target.dtype not in (torch.int32, torch.int64):
+            raise ValueError(f"lmoe: target must be torch.int32 or torch.int64, not {target.dtype}")
+        _expect_on(target, target.dtype, (M,), dev, "target")
+        if M > 1 and target.stride(0) != 1:
+            raise ValueError("lmoe: target must be contiguous")
+        return ctypes.byref(LinearXentDesc(
+            M, self.V, self.K, px, ldx, pw, ldw, target.data_ptr(),
+            I64 if target.dtype is torch.int64 else I32, loss, lse, self._flag))
+
+    def forward(self, x: torch.Tensor, target: torch.Tensor, stream=None):
+        """x [M, K] bf16 (rows at any stride of whole 16 bytes), target [M] int64 or int32 -> (loss,
+        lse), both [M] fp32: of each row, the target's negative log-probability and the logarithm of
+        the sum that it is divided by, which ``backward`` needs.  A row whose target is outside
+        0 .. V-1 has loss 0."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.forward(x, target)
+        M = x.shape[0]
+        loss = torch.empty(M, dtype=torch.float32, device=self.device)
+        lse = torch.empty(M, dtype=torch.float32, device=self.device)
+        d = self._desc(x, target, loss.data_ptr(), lse.data_ptr())
+        lib = load()
+        nb = lib.lmoe_linear_xent_workspace_bytes(d)
+        ws = torch.empty(nb, dtype=torch.uint8, device=self.device)
+        rc = lib.lmoe_linear_xent_forward(d, ws.data_ptr(), nb, _on(self._dev))
+        if rc:
+            _check(rc, "lmoe_linear_xent_forward")
+        return loss, lse
+
+    def backward(self, x: torch.Tensor, target: torch.Tensor, lse: torch.Tensor,
+                 dloss: torch.Tensor, dw_dtype=torch.float32, want_dx: bool = True,
+                 want_dw: bool = True, stream=None) -> dict:
+        """Gradients for the x, target and lse of a ``forward``: dloss [M] fp32, the gradient of each
+        row's loss -> dx [M, K] bf16, dw [V, K] (fp32, or bf16 with dw_dtype).  Rows without a target
+        have none."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.backward(x, target, lse, dloss, dw_dtype, want_dx, want_dw)
+        M, dev = x.shape[0], self._dev
+        bf, f = torch.bfloat16, torch.float32
+        if dw_dtype not in (bf, f):
+            raise ValueError("lmoe: dw_dtype must be torch.float32 or torch.bfloat16")
+        pg = _vector(dloss, M, dev, "dloss")
+        d = self._desc(x, target, None, _vector(lse, M, dev, "lse"))
+        dx = dw = pdx = pdw = None
+        if want_dx:
+            dx = torch.empty((M, self.K), dtype=bf, device=self.device)
+            pdx = dx.data_ptr()
+        if want_dw:
+            dw = torch.empty((self.V, self.K), dtype=dw_dtype, device=self.device)
+            pdw = dw.data_ptr()
+        lib = load()
+        nb = lib.lmoe_linear_xent_backward_workspace_bytes(d)
+        ws = torch.empty(nb, dtype=torch.uint8, device=self.device)
+        rc = lib.lmoe_linear_xent_backward(d, pg, pdx, self.K, pdw, F32 if dw_dtype is f else BF16,
+                                           ws.data_ptr(), nb, _on(dev))
+        if rc:
+            _check(rc, "lmoe_linear_xent_backward")
+        return {"dx": dx, "dw": dw}
 
     def device_error(self) -> int:
         """LMOE_OK, or LMOE_ERR_DEVICE_TIMEOUT if a device-side wait of an earlier call ran out

@@ -1,0 +1,371 @@
+"""Softmax cross entropy of a linear head and its gradients against plain 64-bit arithmetic.
+
+Tolerances, derived.  A logit is K products, exact in fp32, added in fp32: off by at most
+e = K 2^-23 sum|x||w| (the tensor cores may truncate).  exp2 of (l - base) log2(e): two roundings of an
+argument of at most 128 (what is further below the maximum is zero next to it), and exp2's own 2 ulp:
+relative 128 * 2^-22 + 2^-21.  A row's sum: at most 128 + V / 1024 additions one after the other,
+2^-24 each (columns of a tile in four chains, tiles over 32 warps, warps).  log: 2^-22 of its value.
+In the backward pass d is rounded to bf16, half a step being 2^-8 of it; the products' sums are as
+above, over V and M terms, and dx and a bf16 dw are rounded once more."""
+import pytest
+import torch
+
+from latent_compressed_expert_gb300 import lmoe
+
+pytestmark = pytest.mark.gpu
+BF = torch.bfloat16
+HALF, ULP = 2.0 ** -8, 2.0 ** -23
+EXP = 128 * 2.0 ** -22 + 2.0 ** -21
+
+
+@pytest.fixture(scope="module")
+def dev():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA GPU")
+    from latent_compressed_expert_gb300 import build
+    build.build()
+    lmoe.load()
+    return torch.device("cuda:0")
+
+
+def _draw(dev, rows, cols, seed, std=1.0, ld=None):
+    g = torch.Generator(device=dev).manual_seed(seed)
+    ld = cols if ld is None else ld
+    return (torch.randn(rows, ld, generator=g, device=dev) * std).to(BF)[:, :cols]
+
+
+def _targets(dev, M, V, seed, ignored=0.2, dtype=torch.int64):
+    g = torch.Generator(device=dev).manual_seed(seed)
+    t = torch.randint(0, V, (M,), generator=g, device=dev)
+    off = torch.rand(M, generator=g, device=dev) < ignored
+    return torch.where(off, torch.tensor(-100, device=dev), t).to(dtype)
+
+
+def _logits(x, w):
+    x, w = x.double(), w.double()
+    return x @ w.T, x.shape[1] * ULP * (x.abs() @ w.abs().T)
+
+
+def _within(got, want, bound, tag):
+    err = (got.double() - want).abs()
+    assert torch.isfinite(got.double()).all(), tag
+    assert (err <= bound + 1e-35).all(), (tag, float((err / (bound + 1e-35)).max()))
+
+
+def _check_forward(head, x, t, tag=""):
+    V = head.V
+    loss, lse = head.forward(x, t)
+    l, e = _logits(x, head.w)
+    want = torch.logsumexp(l, 1)
+    bound = e.amax(1) + EXP + (128 + V / 1024) * 2.0 ** -24 + 2.0 ** -21 * want.abs() + 2.0 ** -22
+    _within(lse, want, bound, (tag, "lse"))
+    on = (t >= 0) & (t < V)
+    at = torch.where(on, t, torch.zeros_like(t)).long().unsqueeze(1)
+    picked = l.gather(1, at).squeeze(1)
+    assert (loss[~on] == 0).all(), tag
+    both = bound + e.gather(1, at).squeeze(1) + ULP * (want.abs() + picked.abs())
+    _within(loss[on], (want - picked)[on], both[on], (tag, "loss"))
+    torch.cuda.synchronize()
+    assert head.device_error() == lmoe.LMOE_OK
+    return loss, lse
+
+
+def _check_backward(head, x, t, lse, g, tag="", **kw):
+    V, w = head.V, head.w
+    l, e = _logits(x, w)
+    on = ((t >= 0) & (t < V)).unsqueeze(1)
+    p = (l - lse.double().unsqueeze(1)).exp()
+    hot = torch.arange(V, device=x.device) == t.unsqueeze(1)
+    gd = g.double().unsqueeze(1)
+    zero = torch.zeros((), dtype=torch.float64, device=x.device)
+    d = torch.where(on, gd * (p - hot.double()), zero)
+    ed = torch.where(on, gd.abs() * p * (1.01 * e + EXP) + (HALF + 2 * ULP) * d.abs(), zero)
+    x64, w64 = x.double(), w.double()
+    dx, dw = d @ w64, d.T @ x64
+    ex = ed @ w64.abs() + 1.01 * V * ULP * (d.abs() @ w64.abs()) + HALF * dx.abs()
+    ew = ed.T @ x64.abs() + 1.01 * x.shape[0] * ULP * (d.abs().T @ x64.abs())
+    out = head.backward(x, t, lse, g, **kw)
+    if out["dx"] is not None:
+        _within(out["dx"], dx, 1.01 * ex, (tag, "dx"))
+    if out["dw"] is not None:
+        half = HALF if out["dw"].dtype is BF else ULP
+        _within(out["dw"], dw, 1.01 * (ew + half * dw.abs()), (tag, "dw"))
+    torch.cuda.synchronize()
+    assert head.device_error() == lmoe.LMOE_OK
+    return out
+
+
+def _weights_of_rows(dev, M, seed):
+    g = torch.Generator(device=dev).manual_seed(seed)
+    return torch.rand(M, generator=g, device=dev) - 0.25
+
+
+# one row and one token; a chunk and its edge; tiles of one SM of several widths and their edges;
+# SM pairs; many tiles of the vocabulary
+SIZES = [(1, 1, 8), (1, 31, 8), (1, 33, 64), (3, 65, 72), (1, 1000, 512), (2, 70001, 136),
+         (77, 1003, 1000), (128, 4099, 264), (129, 257, 136), (255, 96, 64), (300, 5000, 1024),
+         (1000, 8200, 512), (257, 513, 7168), (2049, 300, 128)]
+
+
+@pytest.mark.parametrize("M,V,K", SIZES)
+def test_forward(dev, M, V, K):
+    head = lmoe.LinearCrossEntropy(_draw(dev, V, K, V + K, 3 * K ** -0.5))
+    _check_forward(head, _draw(dev, M, K, M), _targets(dev, M, V, 5), (M, V, K))
+
+
+@pytest.mark.parametrize("M,V,K", SIZES)
+@pytest.mark.parametrize("dw", [torch.float32, BF])
+def test_backward(dev, M, V, K, dw):
+    head = lmoe.LinearCrossEntropy(_draw(dev, V, K, V + K, 3 * K ** -0.5))
+    x, t = _draw(dev, M, K, M), _targets(dev, M, V, 5)
+    _, lse = head.forward(x, t)
+    _check_backward(head, x, t, lse, _weights_of_rows(dev, M, 9), (M, V, K), dw_dtype=dw)
+
+
+def test_several_pieces(dev):
+    """A vocabulary of two whole pieces and a part of one, with a target in each."""
+    M, V, K = 33000, 9001, 64
+    head = lmoe.LinearCrossEntropy(_draw(dev, V, K, 1, 0.5))
+    x, t = _draw(dev, M, K, 2), _targets(dev, M, V, 3)
+    t[:3] = torch.tensor([4095, 4096, 9000], device=dev)
+    _, lse = _check_forward(head, x, t)
+    a = head.backward(x, t, lse, _weights_of_rows(dev, M, 4))
+    for part in (slice(0, 500), slice(32500, M)):  # rows of dx by themselves
+        sub = _check_backward(head, x[part], t[part], lse[part],
+                              _weights_of_rows(dev, M, 4)[part], want_dw=False)
+        # the pieces' order of adding differs from the smaller call's: both within their bounds
+        big = a["dx"][part].double()
+        assert (big - sub["dx"].double()).abs().max() <= 2 * HALF * big.abs().max()
+    # dw over all rows, in 64 bits
+    l = x.double() @ head.w.double().T
+    p = (l - lse.double().unsqueeze(1)).exp_()
+    p[torch.arange(M, device=dev)[t >= 0], t[t >= 0]] -= 1
+    p *= (_weights_of_rows(dev, M, 4).double() * (t >= 0)).unsqueeze(1)
+    want = p.T @ x.double()
+    bound = (HALF + 2 * EXP + M * ULP) * (p.abs().T @ x.double().abs())
+    _within(a["dw"], want, 1.01 * bound, "dw")
+
+
+@pytest.mark.parametrize("dtype", [torch.int32, torch.int64])
+def test_target_types_and_strides(dev, dtype):
+    M, V, K = 50, 777, 128
+    w = _draw(dev, V, K, 1, 0.3, ld=K + 40)
+    x = _draw(dev, M, K, 2, ld=K + 8)
+    head = lmoe.LinearCrossEntropy(w)
+    t = _targets(dev, M, V, 3, dtype=dtype)
+    t[0], t[1], t[2] = V, V - 1, torch.iinfo(dtype).min
+    _, lse = _check_forward(head, x, t, dtype)
+    _check_backward(head, x, t, lse, _weights_of_rows(dev, M, 4), dtype)
+
+
+def test_no_targets_at_all(dev):
+    M, V, K = 40, 600, 64
+    head = lmoe.LinearCrossEntropy(_draw(dev, V, K, 1))
+    x, t = _draw(dev, M, K, 2), torch.full((M,), -1, device=dev)
+    x[3] = float("nan")
+    loss, lse = head.forward(x, t)
+    assert (loss == 0).all() and torch.isnan(lse[3]) and torch.isfinite(lse[4:]).all()
+    x[3] = 1.0
+    out = head.backward(x, t, lse, torch.ones(M, device=dev))
+    assert not out["dx"].any() and not out["dw"].any()  # also where lse is NaN
+
+
+def test_rows_that_are_not_finite(dev):
+    """Each row's infinities and NaN stay in its own loss, lse and dx."""
+    M, V, K = 140, 700, 64
+    w = _draw(dev, V, K, 1, 0.2)
+    w[:, 0] = 1.0
+    x, t = _draw(dev, M, K, 2), _targets(dev, M, V, 3, ignored=0.0)
+    head = lmoe.LinearCrossEntropy(w)
+    clean = head.forward(x, t)
+    xx = x.clone()
+    xx[5, 3] = float("nan")
+    xx[6, 0] = float("inf")       # all logits +inf
+    xx[7, 0] = float("-inf")      # all logits -inf
+    loss, lse = head.forward(xx, t)
+    assert torch.isnan(lse[5]) and lse[6] == float("inf") and lse[7] == float("-inf")
+    assert torch.isnan(loss[5:8]).all()  # inf - inf
+    others = [i for i in range(M) if i not in (5, 6, 7)]
+    assert torch.equal(loss[others], clean[0][others]) and torch.equal(lse[others], clean[1][others])
+    # one token of weight zero probability: w row -> logit -inf for every row with x[0] > 0
+    w2 = w.clone()
+    w2[9, 0] = float("-inf")
+    x2 = x.clone()
+    x2[:, 0] = 1.0
+    t2 = torch.where(t == 9, 10, t)
+    h2 = lmoe.LinearCrossEntropy(w2)
+    loss2, lse2 = h2.forward(x2, t2)
+    keep = [i for i in range(V) if i != 9]
+    want = torch.logsumexp(x2.double() @ w2[keep].double().T, 1)
+    _within(lse2, want, 1e-4 + 0 * want, "lse without a token")
+    assert torch.isfinite(loss2).all()
+
+
+def test_large_logits(dev):
+    """A row's maximum far from zero on either side; probabilities of one and zero."""
+    M, V, K = 130, 1200, 64
+    w = _draw(dev, V, K, 1, 1.0)
+    x = _draw(dev, M, K, 2)
+    w[:, 0], x[:, 0] = 8.0, 0.0
+    x[:40, 0], x[40:80, 0] = 400.0, -400.0
+    x[80:, 1:] *= 30
+    head = lmoe.LinearCrossEntropy(w)
+    t = _targets(dev, M, V, 3)
+    _, lse = _check_forward(head, x, t)
+    _check_backward(head, x, t, lse, _weights_of_rows(dev, M, 4))
+
+
+def test_against_differences(dev):
+    """dx and dw against central differences of the loss along directions that bf16 holds exactly:
+    values in steps of 2^-5 up to 1, moved by 2^-5.  With logits z(h) = z + h u and |u| <= U, the
+    third derivative of the loss is at most 2 U^3: h^2 U^3 / 3 in the difference quotient."""
+    M, V, K, h = 8, 40, 16, 2.0 ** -5
+    gen = torch.Generator(device=dev).manual_seed(7)
+    grid = lambda *s: torch.randint(-30, 31, s, generator=gen, device=dev).to(BF) * h
+    x, w = grid(M, K).to(BF), grid(V, K).to(BF)
+    t = _targets(dev, M, V, 3, ignored=0.1)
+    g = torch.rand(M, generator=gen, device=dev)
+    head = lmoe.LinearCrossEntropy(w)
+    _, lse = head.forward(x, t)
+    out = head.backward(x, t, lse, g)
+    sign = lambda *s: (torch.randint(0, 2, s, generator=gen, device=dev) * 2 - 1).to(BF)
+    total = lambda xx, ww: float((lmoe.LinearCrossEntropy(ww).forward(xx, t)[0].double() * g).sum())
+    for _ in range(4):
+        ux, uw = sign(M, K), sign(V, K)
+        for grad, u, f in ((out["dx"], ux, lambda s: total(x + s * h * ux, w)),
+                           (out["dw"], uw, lambda s: total(x, w + s * h * uw))):
+            diff = (f(1) - f(-1)) / (2 * h)
+            got = float((grad.double() * u.double()).sum())
+            U = float((x if u is uw else w).double().abs().sum(1).max())
+            tol = h * h * U ** 3 / 3 * float(g.sum()) + 2 * HALF * float(grad.double().abs().sum()) \
+                + 1e-5 / h
+            assert abs(diff - got) <= tol, (diff, got, tol)
+
+
+def test_same_bits_every_time_and_in_any_batch(dev):
+    """Sums are added in a fixed order, and rows do not see their neighbours."""
+    M, V, K = 100, 3000, 256
+    head = lmoe.LinearCrossEntropy(_draw(dev, V, K, 1, 0.2))
+    x, t = _draw(dev, M, K, 2), _targets(dev, M, V, 3)
+    loss, lse = head.forward(x, t)
+    g = _weights_of_rows(dev, M, 4)
+    out = head.backward(x, t, lse, g)
+    for _ in range(3):
+        again = head.forward(x, t)
+        assert torch.equal(again[0], loss) and torch.equal(again[1], lse)
+        o = head.backward(x, t, lse, g)
+        assert torch.equal(o["dx"], out["dx"]) and torch.equal(o["dw"], out["dw"])
+    one = head.forward(x[17:18], t[17:18])
+    assert torch.equal(one[1], lse[17:18])
+
+
+def test_parts_of_the_gradients(dev):
+    M, V, K = 60, 500, 128
+    head = lmoe.LinearCrossEntropy(_draw(dev, V, K, 1, 0.2))
+    x, t = _draw(dev, M, K, 2), _targets(dev, M, V, 3)
+    _, lse = head.forward(x, t)
+    g = _weights_of_rows(dev, M, 4)
+    both = head.backward(x, t, lse, g)
+    a, b = head.backward(x, t, lse, g, want_dw=False), head.backward(x, t, lse, g, want_dx=False)
+    assert a["dw"] is None and b["dx"] is None
+    assert torch.equal(a["dx"], both["dx"]) and torch.equal(b["dw"], both["dw"])
+
+
+def test_no_rows(dev):
+    head = lmoe.LinearCrossEntropy(_draw(dev, 300, 64, 1))
+    x, t = torch.empty(0, 64, dtype=BF, device=dev), torch.empty(0, dtype=torch.int64, device=dev)
+    loss, lse = head.forward(x, t)
+    assert loss.numel() == lse.numel() == 0
+    out = head.backward(x, t, lse, torch.empty(0, device=dev))
+    assert out["dx"].shape == (0, 64) and not out["dw"].any()
+
+
+def test_streams_and_graphs(dev):
+    """On a stream of its own, from two streams at once, and captured: the same bits; a graph's replay
+    takes the inputs as they are then."""
+    M, V, K = 200, 5000, 512
+    head = lmoe.LinearCrossEntropy(_draw(dev, V, K, 1, 0.1))
+    xs = [_draw(dev, M, K, s) for s in (2, 3)]
+    t, g = _targets(dev, M, V, 4), _weights_of_rows(dev, M, 5)
+
+    def step(x, stream=None):
+        loss, lse = head.forward(x, t, stream=stream)
+        out = head.backward(x, t, lse, g, stream=stream)
+        return loss, lse, out["dx"], out["dw"]
+
+    want = [step(x) for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in xs]
+    for _ in range(5):
+        got = [step(x, s) for x, s in zip(xs, streams)]
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert all(torch.equal(p, q) for p, q in zip(a, b))
+    x = xs[0].clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kept = step(x)
+    for i in (1, 0, 1):
+        x.copy_(xs[i])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(kept, want[i]))
+
+
+def test_weights_are_looked_at_each_call(dev):
+    head = lmoe.LinearCrossEntropy(_draw(dev, 300, 64, 1))
+    x, t = _draw(dev, 9, 64, 2), _targets(dev, 9, 300, 3)
+    head.w = _draw(dev, 300, 64, 8)
+    _check_forward(head, x, t)
+    head.w.mul_(0.5)
+    _check_forward(head, x, t)
+
+
+def test_refusals(dev):
+    head = lmoe.LinearCrossEntropy(_draw(dev, 300, 64, 1))
+    x, t = _draw(dev, 9, 64, 2), _targets(dev, 9, 300, 3)
+    with pytest.raises(ValueError):
+        head.forward(x.float(), t)
+    with pytest.raises(ValueError):
+        head.forward(x, t.float())
+    with pytest.raises(ValueError):
+        head.forward(x, t[:8])
+    with pytest.raises(ValueError):
+        head.forward(x, t.cpu())
+    with pytest.raises(ValueError):
+        head.forward(x, torch.stack([t, t], 1)[:, 0])
+    with pytest.raises(ValueError):
+        head.forward(x.cpu(), t)
+    lse = torch.zeros(9, device=dev)
+    with pytest.raises(ValueError):
+        head.backward(x, t, lse, lse, dw_dtype=torch.float16)
+    with pytest.raises(ValueError):
+        head.backward(x, t, lse[:8], lse)
+    with pytest.raises(ValueError):
+        head.backward(x, t, lse, lse.double())
+    with pytest.raises(lmoe.LmoeError):
+        lmoe.LinearCrossEntropy(_draw(dev, 300, 60, 1)).forward(_draw(dev, 9, 60, 2), t)
+    with pytest.raises(lmoe.LmoeError):   # rows at 8-byte steps
+        head.forward(_draw(dev, 9, 64, 2, ld=68), t)
+
+
+@pytest.mark.parametrize("M", [16, 300])
+def test_stalled_wait_is_reported(dev, monkeypatch, M):
+    """A wait that runs out ends the call with an error status; the next call is right again."""
+    V, K = 2000, 128
+    head = lmoe.LinearCrossEntropy(_draw(dev, V, K, 1, 0.2))
+    x, t = _draw(dev, M, K, 2), _targets(dev, M, V, 3)
+    want = head.forward(x, t)
+    g = _weights_of_rows(dev, M, 4)
+    monkeypatch.setenv("LMOE_WAIT_LIMIT_MS", "50")
+    monkeypatch.setenv("LMOE_FAULT_INJECT", "stall")
+    for call in (lambda: head.forward(x, t), lambda: head.backward(x, t, want[1], g)):
+        call()
+        torch.cuda.synchronize()
+        assert head.device_error() == lmoe.LMOE_ERR_DEVICE_TIMEOUT
+    monkeypatch.delenv("LMOE_FAULT_INJECT")
+    monkeypatch.delenv("LMOE_WAIT_LIMIT_MS")
+    again = head.forward(x, t)
+    torch.cuda.synchronize()
+    assert head.device_error() == lmoe.LMOE_OK
+    assert torch.equal(again[0], want[0]) and torch.equal(again[1], want[1])
