@@ -629,6 +629,59 @@ int lmoe_linear_xent_backward(const lmoe_linear_xent *p, const float *dloss, voi
                               long long lddx, void *dw, int dw_type, void *ws, size_t ws_bytes,
                               void *stream);
 
+/* Orthogonalising matrices by Newton-Schulz products, and the weight update that uses it.  [SU] names
+ * Per-Head Muon as the model's optimizer and gives no formulas; these are the usual ones, for a batch
+ * of matrices of one shape (experts, heads, or one), each by itself:
+ *   X = U / (|U|_F + eps);  for each of `steps` triples (a, b, c):  A = X X^T,
+ *   X = a X + (b A + c A^2) X
+ * which brings the singular values of U near 1 and leaves its singular vectors.
+ * lmoe_orthogonalize: U = grad, out = X.
+ * lmoe_muon_update:   momentum = beta momentum + grad;
+ *                     U = grad + beta momentum (nesterov), or momentum;
+ *                     w = w (1 - rate weight_decay) - rate scale X
+ *   from the fp32 master where there is one (then w, if given, is its rounding to bf16), else from w.
+ * Matrices [batch, rows, cols] with contiguous columns, rows ld* apart and matrices *_stride apart, in
+ * elements, at any value that keeps them apart (views into larger buffers, interleaved batches). */
+#define LMOE_MUON_MAX_STEPS 64
+typedef struct lmoe_muon {
+  int batch, rows, cols;
+  int steps;               /* 1 .. LMOE_MUON_MAX_STEPS */
+  const float *coeffs;     /* HOST memory, [steps][3], read during the call.  Muon's: 5 times
+                              3.4445, -4.7750, 2.0315 */
+  float eps;               /* > 0 (1e-7) */
+  const void *grad;        /* of grad_type */
+  int grad_type;           /* LMOE_BF16 or LMOE_F32 */
+  long long ldg, grad_stride;
+  void *out;               /* bf16 (lmoe_orthogonalize); may be grad itself */
+  long long ldo, out_stride;
+  float *momentum;         /* fp32, in and out (lmoe_muon_update, as all that follows) */
+  long long ldm, momentum_stride;
+  float beta;
+  int nesterov;
+  void *w;                 /* bf16, in and out, or NULL */
+  long long ldw, w_stride;
+  float *master;           /* fp32, in and out, or NULL */
+  long long ldmaster, master_stride;
+  float rate, weight_decay, scale;
+  uint32_t *dev_flag;      /* as in lmoe_linear */
+} lmoe_muon;
+
+/* ws: lmoe_muon_workspace_bytes(p) of device scratch, 16-byte aligned (6 bytes for each element of the
+ * batch and 4 for each of its matrices' smaller side squared).  Any rows and cols and any alignment to
+ * the element size; multiples of 8 columns in whole 16 bytes are read faster.  A size of 0 is a no-op.
+ * Arithmetic: products of fp16 operands with fp32 sums, X as two fp16 terms and the diagonals of A and
+ * of b A + c A^2 in fp32 beside them, the norm in 64 bits; X comes out within 1e-3 of itself or so (in
+ * the norm, against the formulas in 64 bits; up to 1e-2 for matrices of a few elements), before its
+ * rounding to bf16.  The iterates must keep to
+ * fp16's range: singular values of X up to 8 (from 1 at the start) and entries of b A + c A^2 up to
+ * 255 are safe.  A matrix that is not finite gives NaN, in its own place in the batch only.
+ * Outputs overlap no input, nor each other (out may be grad, which is read before it is written).
+ * Errors: INVALID_ARG (also coeffs, eps or rates that are not finite), UNSUPPORTED (rows or cols above
+ * 2^20, rows cols above 2^32, batch above 65535), WORKSPACE_TOO_SMALL, CUDA. */
+size_t lmoe_muon_workspace_bytes(const lmoe_muon *p);
+int lmoe_orthogonalize(const lmoe_muon *p, void *ws, size_t ws_bytes, void *stream);
+int lmoe_muon_update(const lmoe_muon *p, void *ws, size_t ws_bytes, void *stream);
+
 /* Size in bytes of the fixed device array that lmoe_forward_noalloc uses as its workspace. */
 #define LMOE_NOALLOC_SCRATCH_BYTES (24u << 20)
 

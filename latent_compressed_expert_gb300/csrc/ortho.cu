@@ -1,0 +1,634 @@
+// ortho.cu -- orthogonalising matrices by Newton-Schulz products, and the weight update that uses
+// it (matrix products in tile.cuh):
+//   X = G / (|G|_F + eps);   steps times  A = X X^T,  B = b A + c A^2,  X = a X + B X
+// on the smaller side: a matrix taller than wide takes A = X^T X and X = a X + X B.  Nothing is
+// transposed in memory: the tensor cores read X along either dimension.  A and B are symmetric, and
+// only their tiles on and above the diagonal are computed.
+//
+// Precision.  The products' operands are fp16 (11 bits at the bf16 rate; the iterates' range is
+// known), their sums fp32.  Three things are kept apart from that rounding:
+//   - X is two fp16 terms, hi + lo, in the term a X, which every step grows by a: directions of
+//     small singular values gain a factor of a^steps (485 for five of Muon's), and so would the
+//     rounding of X in them (a gradient of low rank came out 2e-2 to 4e-2 off without lo).
+//   - The diagonals of A and B are fp32 vectors and zero in the matrices: a wide matrix's A is near
+//     a multiple of the identity, and the rounding of its diagonal was most of the error (3e-3).
+//     With A = D + O:  A^2 = D^2 + D O + O D + O^2, of which only O^2 is a product.
+//   - In B X the diagonal's part takes hi, as the product does, while later steps can still amplify
+//     what the two would differ by, and X itself in the last two steps.
+// The result is then 4e-4 to 1e-3 off in the norm, half of what its rounding to bf16 adds.
+#include <cuda_fp16.h>
+
+#include "tile.cuh"
+
+namespace lmoe {
+
+// Scales of the fp16 operands, powers of two: X up to 2^8 and A up to 2^6 in magnitude fit, and what
+// is 2^-15 of 1 or more keeps all its bits.
+constexpr float X_SCALE = 256.0f, A_SCALE = 1024.0f, B_SCALE = 256.0f, LO_SCALE = 2048.0f;
+constexpr int EXACT_STEPS = 2;  // the last ones, in which B's diagonal takes X itself
+
+__device__ __forceinline__ uint32_t pack_half2(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float2 unpack_half2(uint32_t w) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+// X as hi + lo / LO_SCALE, both of X X_SCALE: two values
+__device__ __forceinline__ void split_half2(float a, float b, uint32_t* hi, uint32_t* lo) {
+  a *= X_SCALE;
+  b *= X_SCALE;
+  *hi = pack_half2(a, b);
+  const float2 h = unpack_half2(*hi);
+  *lo = pack_half2((a - h.x) * LO_SCALE, (b - h.y) * LO_SCALE);
+}
+
+// 32 fp16 values of a row as 16 words, of which those of columns below `cols` (rounded up to 8) are
+// there.
+__device__ __forceinline__ void load_row32(const __half* p, int col, int cols, uint32_t (&w)[16]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    uint4 u = make_uint4(0u, 0u, 0u, 0u);
+    if (col + 8 * j < cols) u = *reinterpret_cast<const uint4*>(p + col + 8 * j);
+    w[4 * j] = u.x;
+    w[4 * j + 1] = u.y;
+    w[4 * j + 2] = u.z;
+    w[4 * j + 3] = u.w;
+  }
+}
+// 32 floats that all threads want, at a multiple of 32 of an array padded to a multiple of 4.
+__device__ __forceinline__ float4 diag4(const float* p, int col, int cols) {
+  return col < cols ? __ldg(reinterpret_cast<const float4*>(p + col))
+                    : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+}
+
+// A: its diagonal, and the rest as fp16.
+struct GramEpi {
+  float* diag;   // [batch][ld]
+  int64_t ld;
+  struct State {};
+  __device__ __forceinline__ void begin(const TileArgs&, const TileCtx&, State&) const {}
+  __device__ __forceinline__ void load(const TileArgs&, const TileCtx&, int, State&) const {}
+  __device__ __forceinline__ void chunk(const TileArgs& g, const TileCtx& c, int col, State&,
+                                        float (&v)[32], int) const {
+    constexpr float TO_A = 1.0f / (X_SCALE * X_SCALE);
+    const int at = c.t.diag ? c.row - col : -1;
+    if (at >= 0 && at < 32) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (j == at) {
+          if (c.row < g.R) diag[c.t.z * ld + c.row] = v[j] * TO_A;
+          v[j] = 0.0f;
+        }
+    }
+    uint32_t w[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      w[j] = pack_half2(v[2 * j] * (TO_A * A_SCALE), v[2 * j + 1] * (TO_A * A_SCALE));
+    tile_buf_free(c.lane);
+    tile_store16(&c.maps->out0, c.buf, c.lane, w, c.warp_row, col, c.t.z);
+    if (!c.t.diag)
+      tile_store16_turned(&c.maps->out0, c.buf + 2048, c.lane, w, c.warp_row, col, c.t.z);
+  }
+  __device__ __forceinline__ void end(const TileArgs&, const TileCtx&, State&) const {}
+};
+
+// B = b A + c A^2: its diagonal, and the rest as fp16.
+struct PolyEpi {
+  const __half* a;     // A without its diagonal, [batch][rows][lda]
+  const float* adiag;  // [batch][ld]
+  float* bdiag;
+  int64_t ld, lda, stride;
+  float b, c;
+  struct State {
+    float d;
+    uint32_t next[16];
+  };
+  __device__ __forceinline__ void begin(const TileArgs& g, const TileCtx& c_, State& st) const {
+    st.d = c_.row < g.R ? __ldg(adiag + c_.t.z * ld + c_.row) : 0.0f;
+  }
+  __device__ __forceinline__ void load(const TileArgs& g, const TileCtx& t, int col,
+                                       State& st) const {
+    load_row32(a + t.t.z * stride + static_cast<int64_t>(t.row) * lda, col, t.row < g.R ? g.C : 0,
+               st.next);
+  }
+  __device__ __forceinline__ void chunk(const TileArgs& g, const TileCtx& t, int col, State& st,
+                                        float (&v)[32], int next) const {
+    const float* dj = adiag + t.t.z * ld;
+    constexpr float TO_A2 = 1.0f / (A_SCALE * A_SCALE);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float4 d = diag4(dj, col + 4 * j, g.C);
+      const float2 o0 = unpack_half2(st.next[2 * j]), o1 = unpack_half2(st.next[2 * j + 1]);
+      const float o[4] = {o0.x, o0.y, o1.x, o1.y}, dd[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float f = o[k] * (1.0f / A_SCALE);
+        v[4 * j + k] = c * fmaf(st.d + dd[k], f, v[4 * j + k] * TO_A2) + b * f;
+      }
+    }
+    const int at = t.t.diag ? t.row - col : -1;
+    if (at >= 0 && at < 32) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (j == at) {  // here O is zero: v is c times O^2
+          if (t.row < g.R) bdiag[t.t.z * ld + t.row] = v[j] + st.d * fmaf(c, st.d, b);
+          v[j] = 0.0f;
+        }
+    }
+    if (next >= 0) load(g, t, next, st);
+    uint32_t w[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) w[j] = pack_half2(v[2 * j] * B_SCALE, v[2 * j + 1] * B_SCALE);
+    tile_buf_free(t.lane);
+    tile_store16(&t.maps->out0, t.buf, t.lane, w, t.warp_row, col, t.t.z);
+    if (!t.t.diag)
+      tile_store16_turned(&t.maps->out0, t.buf + 2048, t.lane, w, t.warp_row, col, t.t.z);
+  }
+  __device__ __forceinline__ void end(const TileArgs&, const TileCtx&, State&) const {}
+};
+
+// A matrix of the caller's, of any row and batch distance.
+template <typename T>
+struct Matrices {
+  T* p;
+  int64_t ld, stride;
+  __device__ __forceinline__ T* at(int64_t z, int64_t row, int64_t col) const {
+    return p + z * stride + row * ld + col;
+  }
+};
+
+// What becomes of the last step's X.
+struct MuonOut {
+  Matrices<__nv_bfloat16> o;       // X itself, or p null and
+  Matrices<__nv_bfloat16> w;       // w = keep w - step X, from the fp32 master where there is one
+  Matrices<float> master;
+  float keep, step;
+  __device__ __forceinline__ void put(int64_t z, int64_t row, int64_t col, float x) const {
+    if (o.p) {
+      *o.at(z, row, col) = __float2bfloat16_rn(x);
+      return;
+    }
+    const float old = master.p ? *master.at(z, row, col) : __bfloat162float(*w.at(z, row, col));
+    const float now = fmaf(-step, x, keep * old);
+    if (master.p) *master.at(z, row, col) = now;
+    if (w.p) *w.at(z, row, col) = __float2bfloat16_rn(now);
+  }
+};
+
+// X = a X + B X (TALL: X B).  LAST: into MuonOut.
+template <bool TALL, bool LAST>
+struct ApplyEpi {
+  const __half *hi, *lo;  // [batch][rows][ldx]
+  const float* bdiag;     // [batch][ld]
+  int64_t ldx, stride, ld;
+  float a;
+  int exact;              // B's diagonal takes X, not hi
+  MuonOut out;
+  struct State {
+    float d;
+    uint32_t h[16], l[16];
+  };
+  __device__ __forceinline__ void begin(const TileArgs& g, const TileCtx& t, State& st) const {
+    st.d = !TALL && t.row < g.R ? __ldg(bdiag + t.t.z * ld + t.row) : 0.0f;
+  }
+  __device__ __forceinline__ void load(const TileArgs& g, const TileCtx& t, int col,
+                                       State& st) const {
+    const int64_t off = t.t.z * stride + static_cast<int64_t>(t.row) * ldx;
+    const int cols = t.row < g.R ? g.C : 0;
+    load_row32(hi + off, col, cols, st.h);
+    load_row32(lo + off, col, cols, st.l);
+  }
+  __device__ __forceinline__ void chunk(const TileArgs& g, const TileCtx& t, int col, State& st,
+                                        float (&v)[32], int next) const {
+    const float* dj = bdiag + t.t.z * ld;
+    constexpr float TO_BX = 1.0f / (B_SCALE * X_SCALE);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      float d[4] = {st.d, st.d, st.d, st.d};
+      if constexpr (TALL) {
+        const float4 f = diag4(dj, col + 4 * j, g.C);
+        d[0] = f.x, d[1] = f.y, d[2] = f.z, d[3] = f.w;
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 h2 = unpack_half2(st.h[2 * j + k / 2]), l2 = unpack_half2(st.l[2 * j + k / 2]);
+        const float h = k & 1 ? h2.y : h2.x, l = k & 1 ? l2.y : l2.x;
+        const float x = fmaf(l, 1.0f / LO_SCALE, h) * (1.0f / X_SCALE);
+        const float xd = exact ? x : h * (1.0f / X_SCALE);
+        v[4 * j + k] = fmaf(v[4 * j + k], TO_BX, fmaf(a, x, d[k] * xd));
+      }
+    }
+    if (next >= 0) load(g, t, next, st);
+    tile_buf_free(t.lane);
+    if constexpr (!LAST) {
+      uint32_t h[16], l[16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) split_half2(v[2 * j], v[2 * j + 1], &h[j], &l[j]);
+      tile_store16(&t.maps->out0, t.buf, t.lane, h, t.warp_row, col, t.t.z);
+      tile_store16(&t.maps->out1, t.buf + 2048, t.lane, l, t.warp_row, col, t.t.z);
+    } else {
+      // turned round in shared memory, so that a warp writes along rows; the word's place within
+      // its row is XORed with the row, which leaves no bank conflicts either way
+      float* buf = reinterpret_cast<float*>(t.buf);
+#pragma unroll
+      for (int j = 0; j < 32; ++j) buf[t.lane * 32 + (j ^ t.lane)] = v[j];
+      __syncwarp();
+      const int rows = min(32, g.R - t.warp_row);
+      if (col + t.lane < g.C) {
+#pragma unroll 4
+        for (int r = 0; r < rows; ++r)
+          out.put(t.t.z, t.warp_row + r, col + t.lane, buf[r * 32 + (t.lane ^ r)]);
+      }
+      __syncwarp();
+    }
+  }
+  __device__ __forceinline__ void end(const TileArgs&, const TileCtx&, State&) const {}
+};
+
+// ------------------------------------------------------------------------- the first X
+struct MuonIn {
+  const void* grad;
+  int f32;
+  int64_t ldg, stride;
+  Matrices<float> m;   // momentum, or p null
+  float beta;
+  int nesterov;
+  int rows, cols;
+  int vec;             // whole 16-byte groups of eight columns everywhere
+  double* part;        // [batch][parts] sums of squares
+  int parts;
+  float eps;
+  __half *hi, *lo;
+  int64_t ldx, xstride;
+};
+
+// Eight columns of the gradient, those from cols on as 0.
+__device__ __forceinline__ void muon_grad8(const MuonIn& p, int64_t z, uint32_t row, int col,
+                                           float (&g)[8]) {
+  const int64_t off = z * p.stride + static_cast<int64_t>(row) * p.ldg + col;
+  if (p.vec) {
+    if (p.f32) {
+      linear_read8(static_cast<const float*>(p.grad) + off, g);
+    } else {
+      const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.grad) + off);
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        g[2 * i] = __uint_as_float(w[i] << 16);
+        g[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+      }
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    g[i] = 0.0f;
+    if (col + i < p.cols)
+      g[i] = p.f32 ? static_cast<const float*>(p.grad)[off + i]
+                   : __bfloat162float(static_cast<const __nv_bfloat16*>(p.grad)[off + i]);
+  }
+}
+// The matrix to be orthogonalised there; STEP: after the momentum's step.
+template <bool STEP>
+__device__ __forceinline__ void muon_input8(const MuonIn& p, int64_t z, uint32_t row, int col,
+                                            float (&u)[8]) {
+  muon_grad8(p, z, row, col, u);
+  if (!p.m.p) return;
+  float* m = p.m.at(z, row, col);
+  float f[8];
+  if (p.vec) {
+    linear_read8(m, f);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = col + i < p.cols ? m[i] : 0.0f;
+  }
+  if (STEP) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = fmaf(p.beta, f[i], u[i]);
+    if (p.vec) {
+      float4* o = reinterpret_cast<float4*>(m);
+      o[0] = make_float4(f[0], f[1], f[2], f[3]);
+      o[1] = make_float4(f[4], f[5], f[6], f[7]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (col + i < p.cols) m[i] = f[i];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) u[i] = p.nesterov ? fmaf(p.beta, f[i], u[i]) : f[i];
+}
+
+// Sums of squares of a matrix, blocks x of its groups of eight columns; the momentum's step.  Eight
+// squares are added in fp32, of values brought near 1 by a power of two where they are far from it
+// (their squares would leave fp32's range), the groups in 64 bits, everything in a fixed order.
+__global__ void __launch_bounds__(256) muon_square_kernel(const MuonIn p) {
+  __shared__ double red[8];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int64_t z = blockIdx.y;
+  const uint32_t per = (p.cols + 7) / 8, groups = per * static_cast<uint32_t>(p.rows);
+  double sum = 0.0;
+  for (uint32_t i = blockIdx.x * 256 + threadIdx.x; i < groups; i += p.parts * 256) {
+    const uint32_t row = i / per;
+    float u[8];
+    muon_input8<true>(p, z, row, static_cast<int>(i - row * per) * 8, u);
+    float top = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(u[k]));
+    float up = 1.0f;
+    double down = 1.0;
+    if (top > 0x1p40f) up = 0x1p-90f, down = 0x1p180;
+    if (top < 0x1p-40f) up = 0x1p90f, down = 0x1p-180;
+    float s = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s = fmaf(u[k] * up, u[k] * up, s);
+    sum += static_cast<double>(s) * down;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = sum;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < 8; ++w) sum += red[w];
+    p.part[z * p.parts + blockIdx.x] = sum;
+  }
+}
+
+// X = U / (|U| + eps) as hi + lo.
+__global__ void __launch_bounds__(256) muon_scale_kernel(const MuonIn p) {
+  __shared__ double red[8];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int64_t z = blockIdx.y;
+  double sum = 0.0;
+  for (int i = threadIdx.x; i < p.parts; i += 256) sum += p.part[z * p.parts + i];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = sum;
+  __syncthreads();
+  sum = 0.0;
+  for (int w = 0; w < 8; ++w) sum += red[w];
+  // 1 / (|U| + eps) as s1 s2, s1 a power of two: neither leaves fp32's range, nor does u s1 where
+  // u is at most |U|
+  const double norm = sqrt(sum) + static_cast<double>(p.eps);
+  int e = 0;
+  const double frac = frexp(norm, &e);  // norm = frac 2^e, 1/2 <= frac < 1
+  const int e1 = e > 120 ? 120 : e < -120 ? -120 : e;
+  const float s1 = static_cast<float>(ldexp(1.0, -e1));
+  const float s2 = static_cast<float>(ldexp(1.0 / frac, e1 - e));
+  const uint32_t per = (p.cols + 7) / 8, groups = per * static_cast<uint32_t>(p.rows);
+  for (uint32_t i = blockIdx.x * 256 + threadIdx.x; i < groups; i += gridDim.x * 256) {
+    const uint32_t row = i / per;
+    const int col = static_cast<int>(i - row * per) * 8;
+    float u[8];
+    muon_input8<false>(p, z, row, col, u);
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      split_half2(u[2 * k] * s1 * s2, u[2 * k + 1] * s1 * s2, &h[k], &l[k]);
+    const int64_t off = z * p.xstride + static_cast<int64_t>(row) * p.ldx + col;
+    *reinterpret_cast<uint4*>(p.hi + off) = make_uint4(h[0], h[1], h[2], h[3]);
+    *reinterpret_cast<uint4*>(p.lo + off) = make_uint4(l[0], l[1], l[2], l[3]);
+  }
+}
+
+// ------------------------------------------------------------------------- host side
+constexpr int MUON_MAX_PARTS = 1024;
+
+struct MuonLayout {
+  bool tall;
+  int side;              // the smaller one
+  int64_t ldx, lda, ldd;
+  int parts;
+  size_t hi[2], lo, a, b, adiag, bdiag, part, total;
+};
+static MuonLayout muon_layout(const lmoe_muon& p) {
+  MuonLayout L{};
+  L.tall = p.rows > p.cols;
+  L.side = L.tall ? p.cols : p.rows;
+  L.ldx = ceil_div(p.cols, 8) * 8;
+  L.lda = L.ldd = ceil_div(L.side, 8) * 8;
+  const int64_t blocks = ceil_div(static_cast<int64_t>(p.rows) * ceil_div(p.cols, 8), 4 * 256);
+  L.parts = static_cast<int>(blocks < MUON_MAX_PARTS ? blocks : MUON_MAX_PARTS);
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = off;
+    off += (bytes + 255) / 256 * 256;
+    return o;
+  };
+  const size_t n = static_cast<size_t>(p.batch), x = n * p.rows * L.ldx * 2;
+  L.hi[0] = take(x);
+  L.hi[1] = take(x);
+  L.lo = take(x);
+  L.a = take(n * L.side * L.lda * 2);
+  L.b = take(n * L.side * L.lda * 2);
+  L.adiag = take(n * L.ldd * 4);
+  L.bdiag = take(n * L.ldd * 4);
+  L.part = take(n * L.parts * 8);
+  L.total = off;
+  return L;
+}
+
+template <bool TALL, bool LAST>
+static int muon_apply(const TileOperand& X, const TileOperand& B, TileMaps& maps, const TileArgs& g,
+                      const ApplyEpi<TALL, LAST>& epi, int dev, int sms, cudaStream_t stream) {
+  const TilePlan plan = tile_plan(g.R, g.C, g.D, g.batch, false, sms);
+  if constexpr (TALL)
+    return launch_tile<false, false, true>(X, B, maps, g, epi, plan, dev, sms, stream);
+  else
+    return launch_tile<false, true, true>(B, X, maps, g, epi, plan, dev, sms, stream);
+}
+
+static bool vec16(const void* p, int64_t ld, int64_t stride, int size) {
+  return ((reinterpret_cast<uintptr_t>(p) | static_cast<uintptr_t>(ld * size) |
+           static_cast<uintptr_t>(stride * size)) & 15u) == 0;
+}
+
+// momentum: the update, else the orthogonalisation alone.
+static int muon_run(const lmoe_muon& p, bool update, uint8_t* ws, cudaStream_t stream) {
+  int dev = 0, sms = 0, rc = LMOE_OK;
+  if (linear_device(&dev, &sms) != LMOE_OK) return LMOE_ERR_CUDA;
+  const MuonLayout L = muon_layout(p);
+  __half* hi[2] = {reinterpret_cast<__half*>(ws + L.hi[0]), reinterpret_cast<__half*>(ws + L.hi[1])};
+  __half* lo = reinterpret_cast<__half*>(ws + L.lo);
+  __half* am = reinterpret_cast<__half*>(ws + L.a);
+  __half* bm = reinterpret_cast<__half*>(ws + L.b);
+  float* adiag = reinterpret_cast<float*>(ws + L.adiag);
+  float* bdiag = reinterpret_cast<float*>(ws + L.bdiag);
+  const int64_t xstride = p.rows * L.ldx, astride = L.side * L.lda;
+  const bool one = p.batch == 1;
+
+  MuonIn in{};
+  in.grad = p.grad;
+  in.f32 = p.grad_type == LMOE_F32;
+  in.ldg = p.ldg;
+  in.stride = one ? 0 : p.grad_stride;
+  in.rows = p.rows;
+  in.cols = p.cols;
+  in.vec = p.cols % 8 == 0 && vec16(p.grad, p.rows > 1 ? p.ldg : 0, in.stride, in.f32 ? 4 : 2);
+  if (update) {
+    in.m = {p.momentum, p.ldm, one ? 0 : p.momentum_stride};
+    in.beta = p.beta;
+    in.nesterov = p.nesterov;
+    in.vec = in.vec && vec16(p.momentum, p.rows > 1 ? p.ldm : 0, in.m.stride, 4);
+  }
+  in.part = reinterpret_cast<double*>(ws + L.part);
+  in.parts = L.parts;
+  in.eps = p.eps;
+  in.hi = hi[0];
+  in.lo = lo;
+  in.ldx = L.ldx;
+  in.xstride = xstride;
+  const dim3 grid(static_cast<unsigned>(L.parts), static_cast<unsigned>(p.batch));
+  if (launch_pdl(muon_square_kernel, grid, 256, 0, stream, in) != cudaSuccess ||
+      launch_pdl(muon_scale_kernel, grid, 256, 0, stream, in) != cudaSuccess)
+    return LMOE_ERR_CUDA;
+
+  MuonOut out{};
+  if (update) {
+    out.w = {static_cast<__nv_bfloat16*>(p.w), p.ldw, one ? 0 : p.w_stride};
+    out.master = {p.master, p.ldmaster, one ? 0 : p.master_stride};
+    out.keep = static_cast<float>(1.0 - static_cast<double>(p.rate) * p.weight_decay);
+    out.step = static_cast<float>(static_cast<double>(p.rate) * p.scale);
+  } else {
+    out.o = {static_cast<__nv_bfloat16*>(p.out), p.ldo, one ? 0 : p.out_stride};
+  }
+
+  TileArgs g{};
+  g.batch = p.batch;
+  g.ks = 1;
+  g.err = p.dev_flag;
+  g.inject_stall = inject_stall();
+  const TileOperand A{am, L.side, L.side, L.lda, astride}, B{bm, L.side, L.side, L.lda, astride};
+  TileMaps am_out{}, bm_out{};
+  if (!make_tmap_out32(&am_out.out0, am, 2, L.side, L.side, L.lda, p.batch, astride) ||
+      !make_tmap_out32(&bm_out.out0, bm, 2, L.side, L.side, L.lda, p.batch, astride))
+    return LMOE_ERR_CUDA;
+  for (int k = 0; k < p.steps; ++k) {
+    const float ca = p.coeffs[3 * k], cb = p.coeffs[3 * k + 1], cc = p.coeffs[3 * k + 2];
+    const TileOperand X{hi[k & 1], p.rows, p.cols, L.ldx, xstride};
+    TileArgs s = g;
+    s.sym = 1;
+    s.R = s.C = L.side;
+    s.D = L.tall ? p.rows : p.cols;
+    const GramEpi gram{adiag, L.ldd};
+    const TilePlan gp = tile_plan(s.R, s.C, s.D, p.batch, true, sms);
+    rc = L.tall ? launch_tile<true, true, true>(X, X, am_out, s, gram, gp, dev, sms, stream)
+                : launch_tile<false, false, true>(X, X, am_out, s, gram, gp, dev, sms, stream);
+    if (rc != LMOE_OK) return rc;
+    g.inject_stall = s.inject_stall = 0;
+    s.D = L.side;
+    rc = launch_tile<false, false, true>(
+        A, A, bm_out, s, PolyEpi{am, adiag, bdiag, L.ldd, L.lda, astride, cb, cc},
+        tile_plan(s.R, s.C, s.D, p.batch, true, sms), dev, sms, stream);
+    if (rc != LMOE_OK) return rc;
+    TileArgs f = g;
+    f.R = p.rows;
+    f.C = p.cols;
+    f.D = L.side;
+    const int exact = k + EXACT_STEPS >= p.steps;
+    TileMaps maps{};
+    if (k + 1 == p.steps) {
+      rc = L.tall ? muon_apply<true, true>(X, B, maps, f,
+                                           {hi[k & 1], lo, bdiag, L.ldx, xstride, L.ldd, ca, exact, out},
+                                           dev, sms, stream)
+                  : muon_apply<false, true>(X, B, maps, f,
+                                            {hi[k & 1], lo, bdiag, L.ldx, xstride, L.ldd, ca, exact, out},
+                                            dev, sms, stream);
+    } else {
+      if (!make_tmap_out32(&maps.out0, hi[~k & 1], 2, p.rows, p.cols, L.ldx, p.batch, xstride) ||
+          !make_tmap_out32(&maps.out1, lo, 2, p.rows, p.cols, L.ldx, p.batch, xstride))
+        return LMOE_ERR_CUDA;
+      rc = L.tall ? muon_apply<true, false>(X, B, maps, f,
+                                            {hi[k & 1], lo, bdiag, L.ldx, xstride, L.ldd, ca, exact, out},
+                                            dev, sms, stream)
+                  : muon_apply<false, false>(X, B, maps, f,
+                                             {hi[k & 1], lo, bdiag, L.ldx, xstride, L.ldd, ca, exact, out},
+                                             dev, sms, stream);
+    }
+    if (rc != LMOE_OK) return rc;
+  }
+  return LMOE_OK;
+}
+
+static int muon_sizes_ok(const lmoe_muon* p) {
+  if (!p || p->batch < 0 || p->rows < 0 || p->cols < 0) return LMOE_ERR_INVALID_ARG;
+  constexpr int SIDE = 1 << 20;
+  if (p->rows > SIDE || p->cols > SIDE || p->batch > 65535 ||
+      static_cast<int64_t>(p->rows) * p->cols > (int64_t{1} << 32))
+    return LMOE_ERR_UNSUPPORTED;
+  return LMOE_OK;
+}
+
+static bool misaligned(const void* p, uintptr_t to) {
+  return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0;
+}
+// The row and batch distances of a matrix that is there.
+static bool distances_ok(const lmoe_muon* p, const void* m, long long ld, long long stride,
+                         bool written) {
+  if (!m) return true;
+  if (p->rows > 1 && ld < p->cols) return false;
+  return p->batch <= 1 || stride >= (written ? p->cols : 0);
+}
+
+static int muon_common_ok(const lmoe_muon* p, const void* ws, size_t ws_bytes) {
+  if (p->grad_type != LMOE_BF16 && p->grad_type != LMOE_F32) return LMOE_ERR_INVALID_ARG;
+  if (!p->grad || !p->coeffs || !p->dev_flag || !ws) return LMOE_ERR_INVALID_ARG;
+  if (p->steps < 1 || p->steps > LMOE_MUON_MAX_STEPS || !(p->eps > 0.0f) || !isfinite(p->eps))
+    return LMOE_ERR_INVALID_ARG;
+  for (int i = 0; i < 3 * p->steps; ++i)
+    if (!isfinite(p->coeffs[i])) return LMOE_ERR_INVALID_ARG;
+  if (misaligned(p->grad, p->grad_type == LMOE_F32 ? 4 : 2) || misaligned(p->dev_flag, 4) ||
+      misaligned(ws, 16) || !distances_ok(p, p->grad, p->ldg, p->grad_stride, false))
+    return LMOE_ERR_INVALID_ARG;
+  return ws_bytes < muon_layout(*p).total ? LMOE_ERR_WORKSPACE_TOO_SMALL : LMOE_OK;
+}
+
+}  // namespace lmoe
+
+using namespace lmoe;
+
+extern "C" {
+
+size_t lmoe_muon_workspace_bytes(const lmoe_muon* p) {
+  if (muon_sizes_ok(p) != LMOE_OK || p->batch == 0 || p->rows == 0 || p->cols == 0) return 0;
+  return muon_layout(*p).total;
+}
+
+int lmoe_orthogonalize(const lmoe_muon* p, void* ws, size_t ws_bytes, void* stream) {
+  int rc = muon_sizes_ok(p);
+  if (rc != LMOE_OK) return rc;
+  if (p->batch == 0 || p->rows == 0 || p->cols == 0) return LMOE_OK;
+  if (!p->out || misaligned(p->out, 2) || !distances_ok(p, p->out, p->ldo, p->out_stride, true) ||
+      p->out == ws || p->grad == ws)
+    return LMOE_ERR_INVALID_ARG;
+  if ((rc = muon_common_ok(p, ws, ws_bytes)) != LMOE_OK) return rc;
+  return muon_run(*p, false, static_cast<uint8_t*>(ws), static_cast<cudaStream_t>(stream));
+}
+
+int lmoe_muon_update(const lmoe_muon* p, void* ws, size_t ws_bytes, void* stream) {
+  int rc = muon_sizes_ok(p);
+  if (rc != LMOE_OK) return rc;
+  if (p->batch == 0 || p->rows == 0 || p->cols == 0) return LMOE_OK;
+  if (!p->momentum || (!p->w && !p->master)) return LMOE_ERR_INVALID_ARG;
+  if (!isfinite(p->beta) || !isfinite(p->rate) || !isfinite(p->weight_decay) ||
+      !isfinite(p->scale))
+    return LMOE_ERR_INVALID_ARG;
+  if (misaligned(p->momentum, 4) || misaligned(p->w, 2) || misaligned(p->master, 4) ||
+      !distances_ok(p, p->momentum, p->ldm, p->momentum_stride, true) ||
+      !distances_ok(p, p->w, p->ldw, p->w_stride, true) ||
+      !distances_ok(p, p->master, p->ldmaster, p->master_stride, true))
+    return LMOE_ERR_INVALID_ARG;
+  const void* outs[] = {p->momentum, p->w, p->master, ws};
+  for (int i = 0; i < 4; ++i) {
+    if (outs[i] && outs[i] == p->grad) return LMOE_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (outs[i] && outs[i] == outs[j]) return LMOE_ERR_INVALID_ARG;
+  }
+  if ((rc = muon_common_ok(p, ws, ws_bytes)) != LMOE_OK) return rc;
+  return muon_run(*p, true, static_cast<uint8_t*>(ws), static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

@@ -73,6 +73,17 @@ class LinearXentDesc(ctypes.Structure):
                 ("dev_flag", _vp)]
 
 
+class MuonDesc(ctypes.Structure):
+    _fields_ = [("batch", _i), ("rows", _i), ("cols", _i), ("steps", _i), ("coeffs", _vp),
+                ("eps", _f), ("grad", _vp), ("grad_type", _i), ("ldg", _ll), ("grad_stride", _ll),
+                ("out", _vp), ("ldo", _ll), ("out_stride", _ll), ("momentum", _vp), ("ldm", _ll),
+                ("momentum_stride", _ll), ("beta", _f), ("nesterov", _i), ("w", _vp), ("ldw", _ll),
+                ("w_stride", _ll), ("master", _vp), ("ldmaster", _ll), ("master_stride", _ll),
+                ("rate", _f), ("weight_decay", _f), ("scale", _f), ("dev_flag", _vp)]
+
+
+MUON_MAX_STEPS = 64  # LMOE_MUON_MAX_STEPS
+
 # enum lmoe_act
 ACTS = {"none": 0, "silu": 1, "gelu": 2, "situ": 3}
 
@@ -124,6 +135,9 @@ SIGNATURES = {
     "lmoe_linear_xent_forward": (_i, [_vp, _vp, _sz, _vp]),
     "lmoe_linear_xent_backward_workspace_bytes": (_sz, [_vp]),
     "lmoe_linear_xent_backward": (_i, [_vp, _vp, _vp, _ll, _vp, _i, _vp, _sz, _vp]),
+    "lmoe_muon_workspace_bytes": (_sz, [_vp]),
+    "lmoe_orthogonalize": (_i, [_vp, _vp, _sz, _vp]),
+    "lmoe_muon_update": (_i, [_vp, _vp, _sz, _vp]),
     "lmoe_few_workspace_bytes": (_sz, [ctypes.POINTER(Dims)]),
     "lmoe_forward_few": (_i, [ctypes.POINTER(Dims), _vp, _vp, _vp, _vp, _vp, _sz,
                               ctypes.POINTER(IO), _vp]),
@@ -481,6 +495,20 @@ def _vector(t, n, dev, name):
     return t.data_ptr()
 
 
+def _matrices(t, dtype, shape, dev, name):
+    """(address, distance between rows, between matrices) of a tensor of the given shape, (rows, cols)
+    or (batch, rows, cols), on device number dev, whose rows are contiguous."""
+    if t.dtype is not dtype or t.shape != shape:
+        _expect(t, dtype, shape, name)
+    if t.get_device() != dev:
+        raise ValueError(f"lmoe: {name} must be on CUDA device {dev}, not {t.device}")
+    s = t.stride()
+    if s[-1] != 1 and shape[-1] > 1:
+        raise ValueError(f"lmoe: the rows of {name} must be contiguous")
+    return (t.data_ptr(), s[-2] if shape[-2] > 1 else shape[-1],
+            s[0] if len(shape) == 3 and shape[0] > 1 else shape[-2] * shape[-1])
+
+
 def _on(dev):
     """Device dev's current stream, dev being the current device.  (A call on another stream makes
     that the current one first, so that what it allocates belongs to that stream too.)"""
@@ -814,6 +842,92 @@ class LinearCrossEntropy:
         if rc:
             _check(rc, "lmoe_linear_xent_backward")
         return {"dx": dx, "dw": dw}
+
+    def device_error(self) -> int:
+        """LMOE_OK, or LMOE_ERR_DEVICE_TIMEOUT if a device-side wait of an earlier call ran out
+        (its output is not valid); call after the stream has synchronised.  Clears the flag."""
+        return last_device_error(self.flag)
+
+
+class Muon:
+    """Orthogonalised updates of weights (lmoe_orthogonalize, lmoe_muon_update): Newton-Schulz
+    iterations of ``steps`` steps with coefficients ``coeffs``, one triple for all of them or one for
+    each.  Matrices are [rows, cols], or [batch, rows, cols] of which each is taken by itself (experts,
+    heads), with contiguous rows at any distance: the gradients of ``Layer.backward_layer`` and
+    ``Linear.backward`` go in as they are.  The object keeps no state of the weights: momentum is the
+    caller's."""
+
+    def __init__(self, beta: float = 0.95, nesterov: bool = True, weight_decay: float = 0.0,
+                 steps: int = 5, coeffs=(3.4445, -4.7750, 2.0315), eps: float = 1e-7, device=None):
+        c = torch.as_tensor(coeffs, dtype=torch.float32)
+        if c.shape not in ((3,), (steps, 3)) or not 1 <= steps <= MUON_MAX_STEPS:
+            raise ValueError(f"lmoe: 1 to {MUON_MAX_STEPS} steps, and a triple of coefficients for all "
+                             "of them or for each")
+        self.beta, self.nesterov, self.weight_decay = beta, nesterov, weight_decay
+        self.steps, self.eps = steps, eps
+        self._coeffs = (_f * (3 * steps))(*c.expand(steps, 3).flatten().tolist())
+        self._coeffs_ptr = ctypes.cast(self._coeffs, _vp)
+        self.device = torch.device("cuda", torch.cuda.current_device()) if device is None \
+            else torch.device(device)
+        self.flag = torch.zeros(1, dtype=torch.int32, device=self.device)
+        self.device = self.flag.device
+        torch.cuda.current_stream(self.device).synchronize()  # before any stream of the caller's
+        self._dev, self._flag = self.flag.get_device(), self.flag.data_ptr()
+
+    def _desc(self, grad):
+        if grad.dtype not in (torch.bfloat16, torch.float32):
+            raise ValueError(f"lmoe: grad must be torch.bfloat16 or torch.float32, not {grad.dtype}")
+        shape = tuple(grad.shape)
+        if len(shape) not in (2, 3):
+            raise ValueError(f"lmoe: grad must be [rows, cols] or [batch, rows, cols], not {shape}")
+        d = MuonDesc()
+        d.batch, d.rows, d.cols = (1, *shape) if len(shape) == 2 else shape
+        d.steps, d.coeffs, d.eps, d.dev_flag = self.steps, self._coeffs_ptr, self.eps, self._flag
+        d.grad, d.ldg, d.grad_stride = _matrices(grad, grad.dtype, shape, self._dev, "grad")
+        d.grad_type = F32 if grad.dtype is torch.float32 else BF16
+        return d, shape
+
+    def _call(self, name, d):
+        lib, ref = load(), ctypes.byref(d)
+        nb = lib.lmoe_muon_workspace_bytes(ref)
+        ws = torch.empty(nb, dtype=torch.uint8, device=self.device)
+        rc = getattr(lib, name)(ref, ws.data_ptr(), nb, _on(self._dev))
+        if rc:
+            _check(rc, name)
+
+    def orthogonalize(self, grad: torch.Tensor, out=None, stream=None) -> torch.Tensor:
+        """grad, bf16 or fp32 -> its orthogonalisation in bf16 (``out``, which may be grad itself)."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.orthogonalize(grad, out)
+        d, shape = self._desc(grad)
+        if out is None:
+            out = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
+        d.out, d.ldo, d.out_stride = _matrices(out, torch.bfloat16, shape, self._dev, "out")
+        self._call("lmoe_orthogonalize", d)
+        return out
+
+    def update(self, w: torch.Tensor | None, grad: torch.Tensor, momentum: torch.Tensor,
+               rate: float, scale: float = 1.0, master: torch.Tensor | None = None, stream=None):
+        """One step, in place: momentum (fp32) = beta momentum + grad, then
+        w = w (1 - rate weight_decay) - rate scale X, X the orthogonalisation of grad + beta momentum
+        (or of momentum, without nesterov).  w is bf16; with an fp32 ``master`` that is what is updated,
+        and w, or None, receives its rounding."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.update(w, grad, momentum, rate, scale, master)
+        d, shape = self._desc(grad)
+        f = torch.float32
+        d.momentum, d.ldm, d.momentum_stride = _matrices(momentum, f, shape, self._dev, "momentum")
+        if w is None and master is None:
+            raise ValueError("lmoe: an update needs w or master")
+        if w is not None:
+            d.w, d.ldw, d.w_stride = _matrices(w, torch.bfloat16, shape, self._dev, "w")
+        if master is not None:
+            d.master, d.ldmaster, d.master_stride = _matrices(master, f, shape, self._dev, "master")
+        d.beta, d.nesterov, d.weight_decay = self.beta, int(self.nesterov), self.weight_decay
+        d.rate, d.scale = rate, scale
+        self._call("lmoe_muon_update", d)
 
     def device_error(self) -> int:
         """LMOE_OK, or LMOE_ERR_DEVICE_TIMEOUT if a device-side wait of an earlier call ran out
