@@ -9,7 +9,8 @@
 // known), their sums fp32.  Three things are kept apart from that rounding:
 //   - X is two fp16 terms, hi + lo, in the term a X, which every step grows by a: directions of
 //     small singular values gain a factor of a^steps (485 for five of Muon's), and so would the
-//     rounding of X in them (a gradient of low rank came out 2e-2 to 4e-2 off without lo).
+//     rounding of X in them (a gradient of low rank came out 2e-2 to 4e-2 off without lo).  The last
+//     step's X is hi alone: nothing grows after it (6e-4 instead of 5e-4 there).
 //   - The diagonals of A and B are fp32 vectors and zero in the matrices: a wide matrix's A is near
 //     a multiple of the identity, and the rounding of its diagonal was most of the error (3e-3).
 //     With A = D + O:  A^2 = D^2 + D O + O D + O^2, of which only O^2 is a product.
@@ -64,6 +65,7 @@ __device__ __forceinline__ float4 diag4(const float* p, int col, int cols) {
 
 // A: its diagonal, and the rest as fp16.
 struct GramEpi {
+  static constexpr int PART = 0;
   float* diag;   // [batch][ld]
   int64_t ld;
   struct State {};
@@ -95,6 +97,7 @@ struct GramEpi {
 
 // B = b A + c A^2: its diagonal, and the rest as fp16.
 struct PolyEpi {
+  static constexpr int PART = 0;
   const __half* a;     // A without its diagonal, [batch][rows][lda]
   const float* adiag;  // [batch][ld]
   float* bdiag;
@@ -164,6 +167,7 @@ struct MuonOut {
   Matrices<__nv_bfloat16> w;       // w = keep w - step X, from the fp32 master where there is one
   Matrices<float> master;
   float keep, step;
+  int vec;                         // whole 16-byte groups of eight columns everywhere
   __device__ __forceinline__ void put(int64_t z, int64_t row, int64_t col, float x) const {
     if (o.p) {
       *o.at(z, row, col) = __float2bfloat16_rn(x);
@@ -177,17 +181,22 @@ struct MuonOut {
 };
 
 // X = a X + B X (TALL: X B).  LAST: into MuonOut.
+// (Row by row, with a load and a store of one column a thread, the update of 4096 x 7168 weights took
+// 438 us, of which the product is 150: its loads waited for one another.)
 template <bool TALL, bool LAST>
 struct ApplyEpi {
+  static constexpr int PART = 0;
   const __half *hi, *lo;  // [batch][rows][ldx]
   const float* bdiag;     // [batch][ld]
   int64_t ldx, stride, ld;
   float a;
   int exact;              // B's diagonal takes X, not hi
+  int keep_lo;            // the next step is not the last
   MuonOut out;
   struct State {
     float d;
-    uint32_t h[16], l[16];
+    uint32_t h[16], l[LAST ? 1 : 16];
+    uint4 old[LAST ? 8 : 1];  // the weights: bf16 in every other one, or the fp32 master
   };
   __device__ __forceinline__ void begin(const TileArgs& g, const TileCtx& t, State& st) const {
     st.d = !TALL && t.row < g.R ? __ldg(bdiag + t.t.z * ld + t.row) : 0.0f;
@@ -197,7 +206,58 @@ struct ApplyEpi {
     const int64_t off = t.t.z * stride + static_cast<int64_t>(t.row) * ldx;
     const int cols = t.row < g.R ? g.C : 0;
     load_row32(hi + off, col, cols, st.h);
-    load_row32(lo + off, col, cols, st.l);
+    if constexpr (!LAST) {
+      load_row32(lo + off, col, cols, st.l);
+    } else if (out.vec && !out.o.p) {
+      const int c8 = col + t.lane % 4 * 8;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = t.warp_row + 8 * i + t.lane / 4;
+        if (row >= g.R || c8 >= g.C) continue;
+        if (out.master.p) {
+          const uint4* p = reinterpret_cast<const uint4*>(out.master.at(t.t.z, row, c8));
+          st.old[2 * i] = p[0];
+          st.old[2 * i + 1] = p[1];
+        } else {
+          st.old[2 * i] = *reinterpret_cast<const uint4*>(out.w.at(t.t.z, row, c8));
+        }
+      }
+    }
+  }
+  // The chunk's 32 x 32 of the last X, from shared memory, a thread eight columns of every eighth row.
+  __device__ __forceinline__ void put8(const TileArgs& g, const TileCtx& t, int col,
+                                       const State& st, const float* buf) const {
+    const int c8 = t.lane % 4 * 8;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = 8 * i + t.lane / 4, row = t.warp_row + r;
+      if (row >= g.R || col + c8 >= g.C) continue;
+      float x[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x[k] = buf[r * 32 + ((c8 + k) ^ r)];
+      if (out.o.p) {
+        *reinterpret_cast<uint4*>(out.o.at(t.t.z, row, col + c8)) = linear_pack8(x);
+        continue;
+      }
+      const uint4 a = st.old[2 * i], b = st.old[2 * i + 1];
+      if (out.master.p) {
+        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          x[k] = fmaf(-out.step, x[k], out.keep * __uint_as_float(w[k]));
+        float4* p = reinterpret_cast<float4*>(out.master.at(t.t.z, row, col + c8));
+        p[0] = make_float4(x[0], x[1], x[2], x[3]);
+        p[1] = make_float4(x[4], x[5], x[6], x[7]);
+      } else {
+        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          x[k] = fmaf(-out.step, x[k],
+                      out.keep * __uint_as_float(k & 1 ? w[k / 2] & 0xFFFF0000u : w[k / 2] << 16));
+      }
+      if (out.w.p)
+        *reinterpret_cast<uint4*>(out.w.at(t.t.z, row, col + c8)) = linear_pack8(x);
+    }
   }
   __device__ __forceinline__ void chunk(const TileArgs& g, const TileCtx& t, int col, State& st,
                                         float (&v)[32], int next) const {
@@ -212,21 +272,27 @@ struct ApplyEpi {
       }
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const float2 h2 = unpack_half2(st.h[2 * j + k / 2]), l2 = unpack_half2(st.l[2 * j + k / 2]);
-        const float h = k & 1 ? h2.y : h2.x, l = k & 1 ? l2.y : l2.x;
-        const float x = fmaf(l, 1.0f / LO_SCALE, h) * (1.0f / X_SCALE);
-        const float xd = exact ? x : h * (1.0f / X_SCALE);
-        v[4 * j + k] = fmaf(v[4 * j + k], TO_BX, fmaf(a, x, d[k] * xd));
+        const float2 h2 = unpack_half2(st.h[2 * j + k / 2]);
+        const float h = k & 1 ? h2.y : h2.x;
+        if constexpr (LAST) {
+          v[4 * j + k] = fmaf(v[4 * j + k], TO_BX, (a + d[k]) * (h * (1.0f / X_SCALE)));
+        } else {
+          const float2 l2 = unpack_half2(st.l[2 * j + k / 2]);
+          const float x = fmaf(k & 1 ? l2.y : l2.x, 1.0f / LO_SCALE, h) * (1.0f / X_SCALE);
+          const float xd = exact ? x : h * (1.0f / X_SCALE);
+          v[4 * j + k] = fmaf(v[4 * j + k], TO_BX, fmaf(a, x, d[k] * xd));
+        }
       }
     }
-    if (next >= 0) load(g, t, next, st);
-    tile_buf_free(t.lane);
     if constexpr (!LAST) {
+      if (next >= 0) load(g, t, next, st);
+      tile_buf_free(t.lane);
       uint32_t h[16], l[16];
 #pragma unroll
       for (int j = 0; j < 16; ++j) split_half2(v[2 * j], v[2 * j + 1], &h[j], &l[j]);
       tile_store16(&t.maps->out0, t.buf, t.lane, h, t.warp_row, col, t.t.z);
-      tile_store16(&t.maps->out1, t.buf + 2048, t.lane, l, t.warp_row, col, t.t.z);
+      if (keep_lo)
+        tile_store16(&t.maps->out1, t.buf + 2048, t.lane, l, t.warp_row, col, t.t.z);
     } else {
       // turned round in shared memory, so that a warp writes along rows; the word's place within
       // its row is XORed with the row, which leaves no bank conflicts either way
@@ -234,13 +300,16 @@ struct ApplyEpi {
 #pragma unroll
       for (int j = 0; j < 32; ++j) buf[t.lane * 32 + (j ^ t.lane)] = v[j];
       __syncwarp();
-      const int rows = min(32, g.R - t.warp_row);
-      if (col + t.lane < g.C) {
+      if (out.vec) {
+        put8(g, t, col, st, buf);
+      } else if (col + t.lane < g.C) {
+        const int rows = min(32, g.R - t.warp_row);
 #pragma unroll 4
         for (int r = 0; r < rows; ++r)
           out.put(t.t.z, t.warp_row + r, col + t.lane, buf[r * 32 + (t.lane ^ r)]);
       }
       __syncwarp();
+      if (next >= 0) load(g, t, next, st);
     }
   }
   __device__ __forceinline__ void end(const TileArgs&, const TileCtx&, State&) const {}
@@ -395,7 +464,9 @@ __global__ void __launch_bounds__(256) muon_scale_kernel(const MuonIn p) {
 }
 
 // ------------------------------------------------------------------------- host side
-constexpr int MUON_MAX_PARTS = 1024;
+// Blocks of the two passes before the products, in all: eight on each of 152 SMs, whose 2048 threads
+// have 32 bytes or more each under way.
+constexpr int MUON_BLOCKS = 8 * 152;
 
 struct MuonLayout {
   bool tall;
@@ -410,8 +481,9 @@ static MuonLayout muon_layout(const lmoe_muon& p) {
   L.side = L.tall ? p.cols : p.rows;
   L.ldx = ceil_div(p.cols, 8) * 8;
   L.lda = L.ldd = ceil_div(L.side, 8) * 8;
-  const int64_t blocks = ceil_div(static_cast<int64_t>(p.rows) * ceil_div(p.cols, 8), 4 * 256);
-  L.parts = static_cast<int>(blocks < MUON_MAX_PARTS ? blocks : MUON_MAX_PARTS);
+  const int64_t blocks = ceil_div(static_cast<int64_t>(p.rows) * ceil_div(p.cols, 8), 256);
+  const int64_t most = ceil_div(MUON_BLOCKS, p.batch);
+  L.parts = static_cast<int>(blocks < most ? blocks : most);
   size_t off = 0;
   auto take = [&](size_t bytes) {
     const size_t o = off;
@@ -495,6 +567,11 @@ static int muon_run(const lmoe_muon& p, bool update, uint8_t* ws, cudaStream_t s
   } else {
     out.o = {static_cast<__nv_bfloat16*>(p.out), p.ldo, one ? 0 : p.out_stride};
   }
+  const bool rows = p.rows > 1;
+  out.vec = p.cols % 8 == 0 &&
+            vec16(out.o.p, out.o.p && rows ? out.o.ld : 0, out.o.stride, 2) &&
+            vec16(out.w.p, out.w.p && rows ? out.w.ld : 0, out.w.stride, 2) &&
+            vec16(out.master.p, out.master.p && rows ? out.master.ld : 0, out.master.stride, 4);
 
   TileArgs g{};
   g.batch = p.batch;
@@ -528,24 +605,24 @@ static int muon_run(const lmoe_muon& p, bool update, uint8_t* ws, cudaStream_t s
     f.R = p.rows;
     f.C = p.cols;
     f.D = L.side;
-    const int exact = k + EXACT_STEPS >= p.steps;
+    const int exact = k + EXACT_STEPS >= p.steps, keep_lo = k + 2 < p.steps;
     TileMaps maps{};
     if (k + 1 == p.steps) {
       rc = L.tall ? muon_apply<true, true>(X, B, maps, f,
-                                           {hi[k & 1], lo, bdiag, L.ldx, xstride, L.ldd, ca, exact, out},
+                                           {hi[k & 1], lo, bdiag, L.ldx, xstride, L.ldd, ca, exact, keep_lo, out},
                                            dev, sms, stream)
                   : muon_apply<false, true>(X, B, maps, f,
-                                            {hi[k & 1], lo, bdiag, L.ldx, xstride, L.ldd, ca, exact, out},
+                                            {hi[k & 1], lo, bdiag, L.ldx, xstride, L.ldd, ca, exact, keep_lo, out},
                                             dev, sms, stream);
     } else {
       if (!make_tmap_out32(&maps.out0, hi[~k & 1], 2, p.rows, p.cols, L.ldx, p.batch, xstride) ||
           !make_tmap_out32(&maps.out1, lo, 2, p.rows, p.cols, L.ldx, p.batch, xstride))
         return LMOE_ERR_CUDA;
       rc = L.tall ? muon_apply<true, false>(X, B, maps, f,
-                                            {hi[k & 1], lo, bdiag, L.ldx, xstride, L.ldd, ca, exact, out},
+                                            {hi[k & 1], lo, bdiag, L.ldx, xstride, L.ldd, ca, exact, keep_lo, out},
                                             dev, sms, stream)
                   : muon_apply<false, false>(X, B, maps, f,
-                                             {hi[k & 1], lo, bdiag, L.ldx, xstride, L.ldd, ca, exact, out},
+                                             {hi[k & 1], lo, bdiag, L.ldx, xstride, L.ldd, ca, exact, keep_lo, out},
                                              dev, sms, stream);
     }
     if (rc != LMOE_OK) return rc;

@@ -100,6 +100,12 @@ constexpr int tile_smem_bytes(bool pair, int bn, int stages) {
   return stages * tile_stage_bytes(pair, bn) + 8 * TILE_BUF + LINEAR_MISC + 1024;
 }
 
+constexpr int tile_stages(bool pair, int bn) {
+  int st = LINEAR_MAX_STAGES;
+  while (tile_smem_bytes(pair, bn, st) > LINEAR_SMEM_MAX) --st;
+  return st;
+}
+
 // A warp's 32 rows of 32 16-bit values (16 words a thread) into a tensor store of the 64-byte
 // swizzle, whose map cuts off what lies outside.  `buf`: 2 KB that no earlier store still reads.
 __device__ __forceinline__ void tile_store16(const CUtensorMap* m, uint8_t* buf, int lane,
@@ -159,7 +165,9 @@ __device__ __forceinline__ void tile_buf_free(int lane) {
 //   struct State; void begin(TileCtx, State&); void load(TileCtx, int col, State&), which fetches
 //   what the chunk at column `col` needs; void chunk(TileCtx, int col, State&, float (&v)[32]);
 //   void end(TileCtx, State&).
-// load is called one chunk ahead of chunk.
+// load is called one chunk ahead of chunk.  PART: K-blocks after which an accumulator is taken out of
+// TMEM and the sum goes on in registers, which round (the MMA cuts off what it adds below the last
+// bit, which makes long sums too small); 0: never.
 template <bool PAIR, bool P_MN, bool Q_MN, bool F16, class Epi>
 __global__ void __launch_bounds__(LINEAR_THREADS, 1)
 tile_kernel(const __grid_constant__ TileMaps maps, const TileArgs g, const Epi epi) {
@@ -275,16 +283,19 @@ tile_kernel(const __grid_constant__ TileMaps maps, const TileArgs g, const Epi e
       int s = 0, lt = 0;
       bool ok = !g.inject_stall || ptx::mbar_wait(drain, 0, abort_flag, limit);
       if (!ok) tile_fail(g, abort_flag, DEVERR_TIMEOUT_MMA);
-      for (int64_t index = first; ok && index < g.tiles; index += step, ++lt) {
-        const Tile t = tile_at(g, index, TM);
+      for (int64_t index = first; ok && index < g.tiles; index += step) {
+       const Tile t = tile_at(g, index, TM);
+       for (int k0 = 0; ok && k0 < t.nk; k0 += Epi::PART ? Epi::PART : t.nk, ++lt) {
         const int acc = lt & 1;
         if (!ptx::mbar_wait(&tempty[acc], ((lt >> 1) & 1) ^ 1, abort_flag, limit)) {
           tile_fail(g, abort_flag, DEVERR_TIMEOUT_MMA);
+          ok = false;
           break;
         }
         ptx::tc_fence_after();
         const uint32_t d = tmem_base + static_cast<uint32_t>(acc * 256);
-        for (int kb = 0; kb < t.nk; ++kb) {
+        const int k1 = Epi::PART ? min(t.nk, k0 + Epi::PART) : t.nk;
+        for (int kb = k0; kb < k1; ++kb) {
           if (!ptx::mbar_wait(&m.full[s], parity, abort_flag, limit)) {
             tile_fail(g, abort_flag, DEVERR_TIMEOUT_MMA);
             ok = false;
@@ -299,7 +310,7 @@ tile_kernel(const __grid_constant__ TileMaps maps, const TileArgs g, const Epi e
                                      : ptx::smem_desc_sw128(sp + k * 32);
             const uint64_t db = Q_MN ? ptx::smem_desc_sw128_mn(sq + k * 2048, LINEAR_BOX_BYTES)
                                      : ptx::smem_desc_sw128(sq + k * 32);
-            const uint32_t add = kb == 0 && k == 0 ? 0u : 1u;
+            const uint32_t add = kb == k0 && k == 0 ? 0u : 1u;
             if constexpr (PAIR)
               ptx::umma_bf16_pair(d, da, db, idesc, add);
             else
@@ -317,6 +328,7 @@ tile_kernel(const __grid_constant__ TileMaps maps, const TileArgs g, const Epi e
           else
             ptx::umma_commit(&tfull[acc]);
         }
+       }
       }
       // all MMAs issued by this thread complete before TMEM is released
       if constexpr (PAIR)
@@ -341,7 +353,6 @@ tile_kernel(const __grid_constant__ TileMaps maps, const TileArgs g, const Epi e
       c.t = tile_at(g, index, TM);
       c.warp_row = c.t.row0 + rank * BLOCK_M + q * 32;
       c.row = c.warp_row + lane;
-      const int acc = lt & 1;
       // a warp whose rows lie outside has nothing to do
       const int cols = c.warp_row < g.R ? min(bn, g.C - c.t.col0) : 0;
       const int chunks = (cols + TILE_CHUNK - 1) / TILE_CHUNK;
@@ -349,14 +360,17 @@ tile_kernel(const __grid_constant__ TileMaps maps, const TileArgs g, const Epi e
         epi.begin(g, c, st);
         epi.load(g, c, c.t.col0 + half * TILE_CHUNK, st);
       }
-      const bool got = ptx::mbar_wait(&tfull[acc], (lt >> 1) & 1, abort_flag, limit);
-      if (!__all_sync(0xffffffffu, got)) {
-        if (lane == 0) tile_fail(g, abort_flag, DEVERR_TIMEOUT_EPILOGUE);
-        break;
-      }
-      ptx::tc_fence_after();
-      const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
-                          static_cast<uint32_t>(acc * 256);
+      int acc = lt & 1;
+      uint32_t tb = 0;
+      auto arrived = [&]() {
+        acc = lt & 1;
+        tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * 256);
+        const bool got = ptx::mbar_wait(&tfull[acc], (lt >> 1) & 1, abort_flag, limit);
+        const bool all = __all_sync(0xffffffffu, got);
+        if (!all && lane == 0) tile_fail(g, abort_flag, DEVERR_TIMEOUT_EPILOGUE);
+        ptx::tc_fence_after();
+        return all;
+      };
       auto release = [&]() {  // this warp has read its part of the accumulator
         ptx::tc_fence_before();
         __syncwarp();
@@ -367,6 +381,44 @@ tile_kernel(const __grid_constant__ TileMaps maps, const TileArgs g, const Epi e
             ptx::mbar_arrive(&tempty[acc]);
         }
       };
+      if (!arrived()) break;
+      if constexpr (Epi::PART > 0) {
+        if (c.t.nk > Epi::PART) {
+          float sum[4][32];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 32; ++j) sum[i][j] = 0.0f;
+          bool ok = true;
+          for (int k0 = 0;;) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if (half + 2 * i >= chunks) continue;
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                float v[16];
+                ptx::tmem_ld_32x32b_x16(
+                    tb + static_cast<uint32_t>((half + 2 * i) * TILE_CHUNK + 16 * h), v);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) sum[i][16 * h + j] += v[j];
+              }
+            }
+            release();
+            if ((k0 += Epi::PART) >= c.t.nk) break;
+            ++lt;
+            if (!(ok = arrived())) break;
+          }
+          if (!ok) break;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int ch = half + 2 * i, col = c.t.col0 + ch * TILE_CHUNK;
+            if (ch < chunks)
+              epi.chunk(g, c, col, st, sum[i], ch + 2 < chunks ? col + 2 * TILE_CHUNK : -1);
+          }
+          if (half < chunks) epi.end(g, c, st);
+          continue;
+        }
+      }
       if (half >= chunks) release();
 #pragma unroll 1
       for (int ch = half; ch < chunks; ch += 2) {
@@ -411,15 +463,16 @@ inline bool tile_map(CUtensorMap* m, const TileOperand& o, int batch, bool mn, i
 
 // Tiles of a product, by time: `bn` is 0 for the least of an estimate over SM pairs of 256 columns
 // and single SMs of 64 to 256, else given for one SM alone.  The estimate's constants are those of
-// the linear layers: FLOP/ns of an SM's MMAs, bytes/ns into an SM's stages, ns per accumulator
-// column of a tile's epilogue.
+// the linear layers: FLOP/ns of an SM's MMAs, bytes/ns into an SM's stages, ns from a stage's load to
+// its being free again (an SM draws no more than its stages hold per round), ns per accumulator column
+// of a tile's epilogue.
 struct TilePlan {
   bool pair;
   int bn;
   double ns;
 };
 inline TilePlan tile_plan(int64_t R, int64_t C, int64_t D, int64_t batch, bool sym, int sms) {
-  constexpr double RATE = 12500.0, FEED = 150.0, EPILOGUE = 11.0;
+  constexpr double RATE = 12500.0, FEED = 150.0, ROUND = 2050.0, EPILOGUE = 11.0;
   const double nk = static_cast<double>(ceil_div(D, BLOCK_K));
   TilePlan best{false, 128, 1e300};
   auto offer = [&](bool pair, int bn) {
@@ -428,7 +481,9 @@ inline TilePlan tile_plan(int64_t R, int64_t C, int64_t D, int64_t batch, bool s
     const int64_t units = pair ? sms / 2 : sms;
     const double mma = 2.0 * BLOCK_K * BLOCK_M * bn / RATE;
     const double feed = tile_stage_bytes(pair, bn) / FEED;
-    double tile = nk * (mma > feed ? mma : feed);
+    const double round = ROUND / tile_stages(pair, bn);
+    const double block = mma > feed ? mma : feed;
+    double tile = nk * (block > round ? block : round);
     if (tile < EPILOGUE * bn) tile = EPILOGUE * bn;
     const double ns = static_cast<double>(ceil_div(tiles, units)) * tile + EPILOGUE * bn + 200.0;
     if (ns < best.ns) best = {pair, bn, ns};
@@ -452,8 +507,7 @@ int launch_tile(const TileOperand& P, const TileOperand& Q, TileMaps& maps, Tile
   if (active < 0) return LMOE_ERR_CUDA;
   constexpr int TM = PAIR ? 2 * BLOCK_M : BLOCK_M;
   g.bn = bn;
-  g.stages = LINEAR_MAX_STAGES;
-  while (tile_smem_bytes(PAIR, bn, g.stages) > LINEAR_SMEM_MAX) --g.stages;
+  g.stages = tile_stages(PAIR, bn);
   g.p_rows = PAIR || g.R >= BLOCK_M ? BLOCK_M : (g.R + 7) / 8 * 8;
   g.mt = static_cast<int>(ceil_div(g.R, TM));
   g.nt = static_cast<int>(ceil_div(g.C, bn));
