@@ -17,32 +17,10 @@
 //   - In B X the diagonal's part takes hi, as the product does, while later steps can still amplify
 //     what the two would differ by, and X itself in the last two steps.
 // The result is then 4e-4 to 1e-3 off in the norm, half of what its rounding to bf16 adds.
-#include <cuda_fp16.h>
-
+#include "muon.cuh"
 #include "tile.cuh"
 
 namespace lmoe {
-
-// Scales of the fp16 operands, powers of two: X up to 2^8 and A up to 2^6 in magnitude fit, and what
-// is 2^-15 of 1 or more keeps all its bits.
-constexpr float X_SCALE = 256.0f, A_SCALE = 1024.0f, B_SCALE = 256.0f, LO_SCALE = 2048.0f;
-constexpr int EXACT_STEPS = 2;  // the last ones, in which B's diagonal takes X itself
-
-__device__ __forceinline__ uint32_t pack_half2(float a, float b) {
-  const __half2 h = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-__device__ __forceinline__ float2 unpack_half2(uint32_t w) {
-  return __half22float2(*reinterpret_cast<const __half2*>(&w));
-}
-// X as hi + lo / LO_SCALE, both of X X_SCALE: two values
-__device__ __forceinline__ void split_half2(float a, float b, uint32_t* hi, uint32_t* lo) {
-  a *= X_SCALE;
-  b *= X_SCALE;
-  *hi = pack_half2(a, b);
-  const float2 h = unpack_half2(*hi);
-  *lo = pack_half2((a - h.x) * LO_SCALE, (b - h.y) * LO_SCALE);
-}
 
 // 32 fp16 values of a row as 16 words, of which those of columns below `cols` (rounded up to 8) are
 // there.
@@ -151,35 +129,6 @@ struct PolyEpi {
   __device__ __forceinline__ void end(const TileArgs&, const TileCtx&, State&) const {}
 };
 
-// A matrix of the caller's, of any row and batch distance.
-template <typename T>
-struct Matrices {
-  T* p;
-  int64_t ld, stride;
-  __device__ __forceinline__ T* at(int64_t z, int64_t row, int64_t col) const {
-    return p + z * stride + row * ld + col;
-  }
-};
-
-// What becomes of the last step's X.
-struct MuonOut {
-  Matrices<__nv_bfloat16> o;       // X itself, or p null and
-  Matrices<__nv_bfloat16> w;       // w = keep w - step X, from the fp32 master where there is one
-  Matrices<float> master;
-  float keep, step;
-  int vec;                         // whole 16-byte groups of eight columns everywhere
-  __device__ __forceinline__ void put(int64_t z, int64_t row, int64_t col, float x) const {
-    if (o.p) {
-      *o.at(z, row, col) = __float2bfloat16_rn(x);
-      return;
-    }
-    const float old = master.p ? *master.at(z, row, col) : __bfloat162float(*w.at(z, row, col));
-    const float now = fmaf(-step, x, keep * old);
-    if (master.p) *master.at(z, row, col) = now;
-    if (w.p) *w.at(z, row, col) = __float2bfloat16_rn(now);
-  }
-};
-
 // X = a X + B X (TALL: X B).  LAST: into MuonOut.
 // (Row by row, with a load and a store of one column a thread, the update of 4096 x 7168 weights took
 // 438 us, of which the product is 150: its loads waited for one another.)
@@ -196,7 +145,7 @@ struct ApplyEpi {
   struct State {
     float d;
     uint32_t h[16], l[LAST ? 1 : 16];
-    uint4 old[LAST ? 8 : 1];  // the weights: bf16 in every other one, or the fp32 master
+    MuonOut::Old old[LAST ? 4 : 1];
   };
   __device__ __forceinline__ void begin(const TileArgs& g, const TileCtx& t, State& st) const {
     st.d = !TALL && t.row < g.R ? __ldg(bdiag + t.t.z * ld + t.row) : 0.0f;
@@ -208,25 +157,18 @@ struct ApplyEpi {
     load_row32(hi + off, col, cols, st.h);
     if constexpr (!LAST) {
       load_row32(lo + off, col, cols, st.l);
-    } else if (out.vec && !out.o.p) {
+    } else if (out.vec) {
       const int c8 = col + t.lane % 4 * 8;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int row = t.warp_row + 8 * i + t.lane / 4;
-        if (row >= g.R || c8 >= g.C) continue;
-        if (out.master.p) {
-          const uint4* p = reinterpret_cast<const uint4*>(out.master.at(t.t.z, row, c8));
-          st.old[2 * i] = p[0];
-          st.old[2 * i + 1] = p[1];
-        } else {
-          st.old[2 * i] = *reinterpret_cast<const uint4*>(out.w.at(t.t.z, row, c8));
-        }
+        if (row < g.R && c8 < g.C) out.load8(t.t.z, row, c8, &st.old[i]);
       }
     }
   }
   // The chunk's 32 x 32 of the last X, from shared memory, a thread eight columns of every eighth row.
-  __device__ __forceinline__ void put8(const TileArgs& g, const TileCtx& t, int col,
-                                       const State& st, const float* buf) const {
+  __device__ __forceinline__ void put_chunk(const TileArgs& g, const TileCtx& t, int col,
+                                            const State& st, const float* buf) const {
     const int c8 = t.lane % 4 * 8;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -235,28 +177,7 @@ struct ApplyEpi {
       float x[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) x[k] = buf[r * 32 + ((c8 + k) ^ r)];
-      if (out.o.p) {
-        *reinterpret_cast<uint4*>(out.o.at(t.t.z, row, col + c8)) = linear_pack8(x);
-        continue;
-      }
-      const uint4 a = st.old[2 * i], b = st.old[2 * i + 1];
-      if (out.master.p) {
-        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          x[k] = fmaf(-out.step, x[k], out.keep * __uint_as_float(w[k]));
-        float4* p = reinterpret_cast<float4*>(out.master.at(t.t.z, row, col + c8));
-        p[0] = make_float4(x[0], x[1], x[2], x[3]);
-        p[1] = make_float4(x[4], x[5], x[6], x[7]);
-      } else {
-        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          x[k] = fmaf(-out.step, x[k],
-                      out.keep * __uint_as_float(k & 1 ? w[k / 2] & 0xFFFF0000u : w[k / 2] << 16));
-      }
-      if (out.w.p)
-        *reinterpret_cast<uint4*>(out.w.at(t.t.z, row, col + c8)) = linear_pack8(x);
+      out.put8(t.t.z, row, col + c8, x, st.old[i]);
     }
   }
   __device__ __forceinline__ void chunk(const TileArgs& g, const TileCtx& t, int col, State& st,
@@ -301,7 +222,7 @@ struct ApplyEpi {
       for (int j = 0; j < 32; ++j) buf[t.lane * 32 + (j ^ t.lane)] = v[j];
       __syncwarp();
       if (out.vec) {
-        put8(g, t, col, st, buf);
+        put_chunk(g, t, col, st, buf);
       } else if (col + t.lane < g.C) {
         const int rows = min(32, g.R - t.warp_row);
 #pragma unroll 4
@@ -316,82 +237,7 @@ struct ApplyEpi {
 };
 
 // ------------------------------------------------------------------------- the first X
-struct MuonIn {
-  const void* grad;
-  int f32;
-  int64_t ldg, stride;
-  Matrices<float> m;   // momentum, or p null
-  float beta;
-  int nesterov;
-  int rows, cols;
-  int vec;             // whole 16-byte groups of eight columns everywhere
-  double* part;        // [batch][parts] sums of squares
-  int parts;
-  float eps;
-  __half *hi, *lo;
-  int64_t ldx, xstride;
-};
-
-// Eight columns of the gradient, those from cols on as 0.
-__device__ __forceinline__ void muon_grad8(const MuonIn& p, int64_t z, uint32_t row, int col,
-                                           float (&g)[8]) {
-  const int64_t off = z * p.stride + static_cast<int64_t>(row) * p.ldg + col;
-  if (p.vec) {
-    if (p.f32) {
-      linear_read8(static_cast<const float*>(p.grad) + off, g);
-    } else {
-      const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.grad) + off);
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        g[2 * i] = __uint_as_float(w[i] << 16);
-        g[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-      }
-    }
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    g[i] = 0.0f;
-    if (col + i < p.cols)
-      g[i] = p.f32 ? static_cast<const float*>(p.grad)[off + i]
-                   : __bfloat162float(static_cast<const __nv_bfloat16*>(p.grad)[off + i]);
-  }
-}
-// The matrix to be orthogonalised there; STEP: after the momentum's step.
-template <bool STEP>
-__device__ __forceinline__ void muon_input8(const MuonIn& p, int64_t z, uint32_t row, int col,
-                                            float (&u)[8]) {
-  muon_grad8(p, z, row, col, u);
-  if (!p.m.p) return;
-  float* m = p.m.at(z, row, col);
-  float f[8];
-  if (p.vec) {
-    linear_read8(m, f);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = col + i < p.cols ? m[i] : 0.0f;
-  }
-  if (STEP) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = fmaf(p.beta, f[i], u[i]);
-    if (p.vec) {
-      float4* o = reinterpret_cast<float4*>(m);
-      o[0] = make_float4(f[0], f[1], f[2], f[3]);
-      o[1] = make_float4(f[4], f[5], f[6], f[7]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (col + i < p.cols) m[i] = f[i];
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) u[i] = p.nesterov ? fmaf(p.beta, f[i], u[i]) : f[i];
-}
-
-// Sums of squares of a matrix, blocks x of its groups of eight columns; the momentum's step.  Eight
-// squares are added in fp32, of values brought near 1 by a power of two where they are far from it
-// (their squares would leave fp32's range), the groups in 64 bits, everything in a fixed order.
+// Sums of squares of a matrix, blocks x of its groups of eight columns; the momentum's step.
 __global__ void __launch_bounds__(256) muon_square_kernel(const MuonIn p) {
   __shared__ double red[8];
   pdl_wait();
@@ -403,17 +249,7 @@ __global__ void __launch_bounds__(256) muon_square_kernel(const MuonIn p) {
     const uint32_t row = i / per;
     float u[8];
     muon_input8<true>(p, z, row, static_cast<int>(i - row * per) * 8, u);
-    float top = 0.0f;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(u[k]));
-    float up = 1.0f;
-    double down = 1.0;
-    if (top > 0x1p40f) up = 0x1p-90f, down = 0x1p180;
-    if (top < 0x1p-40f) up = 0x1p90f, down = 0x1p-180;
-    float s = 0.0f;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) s = fmaf(u[k] * up, u[k] * up, s);
-    sum += static_cast<double>(s) * down;
+    sum += muon_square8(u);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -439,14 +275,8 @@ __global__ void __launch_bounds__(256) muon_scale_kernel(const MuonIn p) {
   __syncthreads();
   sum = 0.0;
   for (int w = 0; w < 8; ++w) sum += red[w];
-  // 1 / (|U| + eps) as s1 s2, s1 a power of two: neither leaves fp32's range, nor does u s1 where
-  // u is at most |U|
-  const double norm = sqrt(sum) + static_cast<double>(p.eps);
-  int e = 0;
-  const double frac = frexp(norm, &e);  // norm = frac 2^e, 1/2 <= frac < 1
-  const int e1 = e > 120 ? 120 : e < -120 ? -120 : e;
-  const float s1 = static_cast<float>(ldexp(1.0, -e1));
-  const float s2 = static_cast<float>(ldexp(1.0 / frac, e1 - e));
+  float s1, s2;
+  muon_factors(sum, p.eps, &s1, &s2);
   const uint32_t per = (p.cols + 7) / 8, groups = per * static_cast<uint32_t>(p.rows);
   for (uint32_t i = blockIdx.x * 256 + threadIdx.x; i < groups; i += gridDim.x * 256) {
     const uint32_t row = i / per;
@@ -553,11 +383,6 @@ static int muon_run(const lmoe_muon& p, bool update, uint8_t* ws, cudaStream_t s
   in.lo = lo;
   in.ldx = L.ldx;
   in.xstride = xstride;
-  const dim3 grid(static_cast<unsigned>(L.parts), static_cast<unsigned>(p.batch));
-  if (launch_pdl(muon_square_kernel, grid, 256, 0, stream, in) != cudaSuccess ||
-      launch_pdl(muon_scale_kernel, grid, 256, 0, stream, in) != cudaSuccess)
-    return LMOE_ERR_CUDA;
-
   MuonOut out{};
   if (update) {
     out.w = {static_cast<__nv_bfloat16*>(p.w), p.ldw, one ? 0 : p.w_stride};
@@ -573,6 +398,11 @@ static int muon_run(const lmoe_muon& p, bool update, uint8_t* ws, cudaStream_t s
             vec16(out.w.p, out.w.p && rows ? out.w.ld : 0, out.w.stride, 2) &&
             vec16(out.master.p, out.master.p && rows ? out.master.ld : 0, out.master.stride, 4);
 
+  if (launch_muon_small({in, out, p.batch, p.steps, p.coeffs, p.dev_flag}, stream, &rc)) return rc;
+  const dim3 grid(static_cast<unsigned>(L.parts), static_cast<unsigned>(p.batch));
+  if (launch_pdl(muon_square_kernel, grid, 256, 0, stream, in) != cudaSuccess ||
+      launch_pdl(muon_scale_kernel, grid, 256, 0, stream, in) != cudaSuccess)
+    return LMOE_ERR_CUDA;
   TileArgs g{};
   g.batch = p.batch;
   g.ks = 1;

@@ -420,6 +420,18 @@ __device__ __forceinline__ void ld_cluster_f32x4(uint32_t cluster_addr, float* f
                : "r"(cluster_addr)
                : "memory");
 }
+__device__ __forceinline__ double ld_cluster_f64(uint32_t cluster_addr) {
+  double v;
+  asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(cluster_addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_cluster_f32(uint32_t cluster_addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr), "f"(v) : "memory");
+}
+__device__ __forceinline__ void st_cluster_u32x2(uint32_t cluster_addr, uint32_t a, uint32_t b) {
+  asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(cluster_addr), "r"(a), "r"(b)
+               : "memory");
+}
 // One arrival on an mbarrier given by its shared::cluster address (either CTA of the pair),
 // with the default semantics (release at CTA scope).  A release at cluster scope here made
 // every arrival wait ~1 us, which serialised the pipeline it signals.
