@@ -30,6 +30,19 @@ __device__ __forceinline__ void split_half2(float a, float b, uint32_t* hi, uint
   *lo = pack_half2((a - h.x) * LO_SCALE, (b - h.y) * LO_SCALE);
 }
 
+// Takes element `at` (if it is one of them) out of a row's 32: its value, and 0 in its place.  (Few
+// instructions: a kernel of one tile runs through its epilogue once, and fetching that code was most
+// of the time, 5 to 8 us of a symmetric product of 128 x 128.)
+__device__ __forceinline__ float take_out(float (&v)[32], int at) {
+  float x = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {
+    x = j == at ? v[j] : x;
+    v[j] = j == at ? 0.0f : v[j];
+  }
+  return x;
+}
+
 // A matrix of the caller's, of any row and batch distance.
 template <typename T>
 struct Matrices {

@@ -35,12 +35,6 @@ __device__ __forceinline__ void load_row32(const __half* p, int col, int cols, u
     w[4 * j + 3] = u.w;
   }
 }
-// 32 floats that all threads want, at a multiple of 32 of an array padded to a multiple of 4.
-__device__ __forceinline__ float4 diag4(const float* p, int col, int cols) {
-  return col < cols ? __ldg(reinterpret_cast<const float4*>(p + col))
-                    : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-}
-
 // A: its diagonal, and the rest as fp16.
 struct GramEpi {
   static constexpr int PART = 0;
@@ -52,14 +46,9 @@ struct GramEpi {
   __device__ __forceinline__ void chunk(const TileArgs& g, const TileCtx& c, int col, State&,
                                         float (&v)[32], int) const {
     constexpr float TO_A = 1.0f / (X_SCALE * X_SCALE);
-    const int at = c.t.diag ? c.row - col : -1;
-    if (at >= 0 && at < 32) {
-#pragma unroll
-      for (int j = 0; j < 32; ++j)
-        if (j == at) {
-          if (c.row < g.R) diag[c.t.z * ld + c.row] = v[j] * TO_A;
-          v[j] = 0.0f;
-        }
+    if (c.t.diag && c.warp_row == col) {
+      const float x = take_out(v, c.lane);
+      if (c.row < g.R) diag[c.t.z * ld + c.row] = x * TO_A;
     }
     uint32_t w[16];
 #pragma unroll
@@ -82,7 +71,7 @@ struct PolyEpi {
   int64_t ld, lda, stride;
   float b, c;
   struct State {
-    float d;
+    float d, dj;  // A's diagonal at this thread's row, and at column `lane` of the chunk
     uint32_t next[16];
   };
   __device__ __forceinline__ void begin(const TileArgs& g, const TileCtx& c_, State& st) const {
@@ -92,30 +81,21 @@ struct PolyEpi {
                                        State& st) const {
     load_row32(a + t.t.z * stride + static_cast<int64_t>(t.row) * lda, col, t.row < g.R ? g.C : 0,
                st.next);
+    st.dj = col + t.lane < g.C ? __ldg(adiag + t.t.z * ld + col + t.lane) : 0.0f;
   }
   __device__ __forceinline__ void chunk(const TileArgs& g, const TileCtx& t, int col, State& st,
                                         float (&v)[32], int next) const {
-    const float* dj = adiag + t.t.z * ld;
     constexpr float TO_A2 = 1.0f / (A_SCALE * A_SCALE);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float4 d = diag4(dj, col + 4 * j, g.C);
-      const float2 o0 = unpack_half2(st.next[2 * j]), o1 = unpack_half2(st.next[2 * j + 1]);
-      const float o[4] = {o0.x, o0.y, o1.x, o1.y}, dd[4] = {d.x, d.y, d.z, d.w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float f = o[k] * (1.0f / A_SCALE);
-        v[4 * j + k] = c * fmaf(st.d + dd[k], f, v[4 * j + k] * TO_A2) + b * f;
-      }
+    for (int j = 0; j < 32; ++j) {
+      const float2 o = unpack_half2(st.next[j / 2]);
+      const float f = (j & 1 ? o.y : o.x) * (1.0f / A_SCALE);
+      const float d = st.d + __shfl_sync(0xffffffffu, st.dj, j);
+      v[j] = c * fmaf(d, f, v[j] * TO_A2) + b * f;
     }
-    const int at = t.t.diag ? t.row - col : -1;
-    if (at >= 0 && at < 32) {
-#pragma unroll
-      for (int j = 0; j < 32; ++j)
-        if (j == at) {  // here O is zero: v is c times O^2
-          if (t.row < g.R) bdiag[t.t.z * ld + t.row] = v[j] + st.d * fmaf(c, st.d, b);
-          v[j] = 0.0f;
-        }
+    if (t.t.diag && t.warp_row == col) {  // here O is zero: v is c times O^2
+      const float x = take_out(v, t.lane);
+      if (t.row < g.R) bdiag[t.t.z * ld + t.row] = x + st.d * fmaf(c, st.d, b);
     }
     if (next >= 0) load(g, t, next, st);
     uint32_t w[16];
@@ -143,7 +123,7 @@ struct ApplyEpi {
   int keep_lo;            // the next step is not the last
   MuonOut out;
   struct State {
-    float d;
+    float d;  // B's diagonal at this thread's row, or (TALL) at column `lane` of the chunk
     uint32_t h[16], l[LAST ? 1 : 16];
     MuonOut::Old old[LAST ? 4 : 1];
   };
@@ -155,6 +135,8 @@ struct ApplyEpi {
     const int64_t off = t.t.z * stride + static_cast<int64_t>(t.row) * ldx;
     const int cols = t.row < g.R ? g.C : 0;
     load_row32(hi + off, col, cols, st.h);
+    if constexpr (TALL)
+      st.d = col + t.lane < g.C ? __ldg(bdiag + t.t.z * ld + col + t.lane) : 0.0f;
     if constexpr (!LAST) {
       load_row32(lo + off, col, cols, st.l);
     } else if (out.vec) {
@@ -182,27 +164,18 @@ struct ApplyEpi {
   }
   __device__ __forceinline__ void chunk(const TileArgs& g, const TileCtx& t, int col, State& st,
                                         float (&v)[32], int next) const {
-    const float* dj = bdiag + t.t.z * ld;
     constexpr float TO_BX = 1.0f / (B_SCALE * X_SCALE);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      float d[4] = {st.d, st.d, st.d, st.d};
-      if constexpr (TALL) {
-        const float4 f = diag4(dj, col + 4 * j, g.C);
-        d[0] = f.x, d[1] = f.y, d[2] = f.z, d[3] = f.w;
-      }
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float2 h2 = unpack_half2(st.h[2 * j + k / 2]);
-        const float h = k & 1 ? h2.y : h2.x;
-        if constexpr (LAST) {
-          v[4 * j + k] = fmaf(v[4 * j + k], TO_BX, (a + d[k]) * (h * (1.0f / X_SCALE)));
-        } else {
-          const float2 l2 = unpack_half2(st.l[2 * j + k / 2]);
-          const float x = fmaf(k & 1 ? l2.y : l2.x, 1.0f / LO_SCALE, h) * (1.0f / X_SCALE);
-          const float xd = exact ? x : h * (1.0f / X_SCALE);
-          v[4 * j + k] = fmaf(v[4 * j + k], TO_BX, fmaf(a, x, d[k] * xd));
-        }
+    for (int j = 0; j < 32; ++j) {
+      const float d = TALL ? __shfl_sync(0xffffffffu, st.d, j) : st.d;
+      const float2 h2 = unpack_half2(st.h[j / 2]);
+      const float h = j & 1 ? h2.y : h2.x;
+      if constexpr (LAST) {
+        v[j] = fmaf(v[j], TO_BX, (a + d) * (h * (1.0f / X_SCALE)));
+      } else {
+        const float2 l2 = unpack_half2(st.l[j / 2]);
+        const float x = fmaf(j & 1 ? l2.y : l2.x, 1.0f / LO_SCALE, h);
+        v[j] = fmaf(v[j], TO_BX, fmaf(a, x, d * (exact ? x : h)) * (1.0f / X_SCALE));
       }
     }
     if constexpr (!LAST) {

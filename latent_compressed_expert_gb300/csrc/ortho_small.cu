@@ -227,12 +227,7 @@ muon_small_kernel(const __grid_constant__ SmallArgs a) {
           *reinterpret_cast<float4*>(ex + row * 512 + (((ch * 8 + j) ^ (row & 31)) << 4)) =
               make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
       } else {
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-          if (col + j == row) {
-            d[row] = v[j] * TO_A;
-            v[j] = 0.0f;
-          }
+        if (col == q * 32) d[row] = take_out(v, lane) * TO_A;
         uint32_t w[16];
 #pragma unroll
         for (int j = 0; j < 16; ++j)
@@ -302,11 +297,8 @@ muon_small_kernel(const __grid_constant__ SmallArgs a) {
         const float2 o2 = unpack_half2(w[j / 2]);
         const float o = (j & 1 ? o2.y : o2.x) * (1.0f / A_SCALE);
         v[j] = cc * fmaf(di + d[col + j], o, v[j] * TO_A2) + cb * o;
-        if (col + j == row) {
-          be[row] = v[j] + di * fmaf(cc, di, cb);
-          v[j] = 0.0f;
-        }
       }
+      if (col == q * 32) be[row] = take_out(v, lane) + di * fmaf(cc, di, cb);
 #pragma unroll
       for (int j = 0; j < 16; ++j) w[j] = pack_half2(v[2 * j] * B_SCALE, v[2 * j + 1] * B_SCALE);
       small_put32(ob, row, col, w);
