@@ -22,19 +22,6 @@
 
 namespace lmoe {
 
-// 32 fp16 values of a row as 16 words, of which those of columns below `cols` (rounded up to 8) are
-// there.
-__device__ __forceinline__ void load_row32(const __half* p, int col, int cols, uint32_t (&w)[16]) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    uint4 u = make_uint4(0u, 0u, 0u, 0u);
-    if (col + 8 * j < cols) u = *reinterpret_cast<const uint4*>(p + col + 8 * j);
-    w[4 * j] = u.x;
-    w[4 * j + 1] = u.y;
-    w[4 * j + 2] = u.z;
-    w[4 * j + 3] = u.w;
-  }
-}
 // A: its diagonal, and the rest as fp16.
 struct GramEpi {
   static constexpr int PART = 0;
@@ -72,36 +59,39 @@ struct PolyEpi {
   float b, c;
   struct State {
     float d, dj;  // A's diagonal at this thread's row, and at column `lane` of the chunk
-    uint32_t next[16];
+    uint4 next[4];
   };
   __device__ __forceinline__ void begin(const TileArgs& g, const TileCtx& c_, State& st) const {
     st.d = c_.row < g.R ? __ldg(adiag + c_.t.z * ld + c_.row) : 0.0f;
   }
   __device__ __forceinline__ void load(const TileArgs& g, const TileCtx& t, int col,
                                        State& st) const {
-    load_row32(a + t.t.z * stride + static_cast<int64_t>(t.row) * lda, col, t.row < g.R ? g.C : 0,
-               st.next);
+    tile_fetch16(a + t.t.z * stride, lda, t.warp_row, col, g.R, g.C, t.lane, st.next);
     st.dj = col + t.lane < g.C ? __ldg(adiag + t.t.z * ld + col + t.lane) : 0.0f;
   }
   __device__ __forceinline__ void chunk(const TileArgs& g, const TileCtx& t, int col, State& st,
                                         float (&v)[32], int next) const {
     constexpr float TO_A2 = 1.0f / (A_SCALE * A_SCALE);
+    uint32_t w[16];
+    tile_buf_free(t.lane);
+    tile_spread16(t.buf, t.lane, st.next);
+    const float dj = st.dj;
+    if (next >= 0) load(g, t, next, st);
+    __syncwarp();
+    tile_row16(t.buf, t.lane, w);
 #pragma unroll
     for (int j = 0; j < 32; ++j) {
-      const float2 o = unpack_half2(st.next[j / 2]);
+      const float2 o = unpack_half2(w[j / 2]);
       const float f = (j & 1 ? o.y : o.x) * (1.0f / A_SCALE);
-      const float d = st.d + __shfl_sync(0xffffffffu, st.dj, j);
+      const float d = st.d + __shfl_sync(0xffffffffu, dj, j);
       v[j] = c * fmaf(d, f, v[j] * TO_A2) + b * f;
     }
     if (t.t.diag && t.warp_row == col) {  // here O is zero: v is c times O^2
       const float x = take_out(v, t.lane);
       if (t.row < g.R) bdiag[t.t.z * ld + t.row] = x + st.d * fmaf(c, st.d, b);
     }
-    if (next >= 0) load(g, t, next, st);
-    uint32_t w[16];
 #pragma unroll
     for (int j = 0; j < 16; ++j) w[j] = pack_half2(v[2 * j] * B_SCALE, v[2 * j + 1] * B_SCALE);
-    tile_buf_free(t.lane);
     tile_store16(&t.maps->out0, t.buf, t.lane, w, t.warp_row, col, t.t.z);
     if (!t.t.diag)
       tile_store16_turned(&t.maps->out0, t.buf + 2048, t.lane, w, t.warp_row, col, t.t.z);
@@ -124,7 +114,7 @@ struct ApplyEpi {
   MuonOut out;
   struct State {
     float d;  // B's diagonal at this thread's row, or (TALL) at column `lane` of the chunk
-    uint32_t h[16], l[LAST ? 1 : 16];
+    uint4 h[4], l[LAST ? 1 : 4];
     MuonOut::Old old[LAST ? 4 : 1];
   };
   __device__ __forceinline__ void begin(const TileArgs& g, const TileCtx& t, State& st) const {
@@ -132,13 +122,11 @@ struct ApplyEpi {
   }
   __device__ __forceinline__ void load(const TileArgs& g, const TileCtx& t, int col,
                                        State& st) const {
-    const int64_t off = t.t.z * stride + static_cast<int64_t>(t.row) * ldx;
-    const int cols = t.row < g.R ? g.C : 0;
-    load_row32(hi + off, col, cols, st.h);
+    tile_fetch16(hi + t.t.z * stride, ldx, t.warp_row, col, g.R, g.C, t.lane, st.h);
     if constexpr (TALL)
       st.d = col + t.lane < g.C ? __ldg(bdiag + t.t.z * ld + col + t.lane) : 0.0f;
     if constexpr (!LAST) {
-      load_row32(lo + off, col, cols, st.l);
+      tile_fetch16(lo + t.t.z * stride, ldx, t.warp_row, col, g.R, g.C, t.lane, st.l);
     } else if (out.vec) {
       const int c8 = col + t.lane % 4 * 8;
 #pragma unroll
@@ -165,23 +153,29 @@ struct ApplyEpi {
   __device__ __forceinline__ void chunk(const TileArgs& g, const TileCtx& t, int col, State& st,
                                         float (&v)[32], int next) const {
     constexpr float TO_BX = 1.0f / (B_SCALE * X_SCALE);
+    uint32_t h[16], l[16];
+    tile_buf_free(t.lane);
+    tile_spread16(t.buf, t.lane, st.h);
+    if constexpr (!LAST) tile_spread16(t.buf + 2048, t.lane, st.l);
+    const float di = st.d;
+    __syncwarp();
+    tile_row16(t.buf, t.lane, h);
+    if constexpr (!LAST) tile_row16(t.buf + 2048, t.lane, l);
+    if (!LAST && next >= 0) load(g, t, next, st);
 #pragma unroll
     for (int j = 0; j < 32; ++j) {
-      const float d = TALL ? __shfl_sync(0xffffffffu, st.d, j) : st.d;
-      const float2 h2 = unpack_half2(st.h[j / 2]);
-      const float h = j & 1 ? h2.y : h2.x;
+      const float d = TALL ? __shfl_sync(0xffffffffu, di, j) : di;
+      const float2 h2 = unpack_half2(h[j / 2]);
+      const float f = j & 1 ? h2.y : h2.x;
       if constexpr (LAST) {
-        v[j] = fmaf(v[j], TO_BX, (a + d) * (h * (1.0f / X_SCALE)));
+        v[j] = fmaf(v[j], TO_BX, (a + d) * (f * (1.0f / X_SCALE)));
       } else {
-        const float2 l2 = unpack_half2(st.l[j / 2]);
-        const float x = fmaf(j & 1 ? l2.y : l2.x, 1.0f / LO_SCALE, h);
-        v[j] = fmaf(v[j], TO_BX, fmaf(a, x, d * (exact ? x : h)) * (1.0f / X_SCALE));
+        const float2 l2 = unpack_half2(l[j / 2]);
+        const float x = fmaf(j & 1 ? l2.y : l2.x, 1.0f / LO_SCALE, f);
+        v[j] = fmaf(v[j], TO_BX, fmaf(a, x, d * (exact ? x : f)) * (1.0f / X_SCALE));
       }
     }
     if constexpr (!LAST) {
-      if (next >= 0) load(g, t, next, st);
-      tile_buf_free(t.lane);
-      uint32_t h[16], l[16];
 #pragma unroll
       for (int j = 0; j < 16; ++j) split_half2(v[2 * j], v[2 * j + 1], &h[j], &l[j]);
       tile_store16(&t.maps->out0, t.buf, t.lane, h, t.warp_row, col, t.t.z);
@@ -191,6 +185,7 @@ struct ApplyEpi {
       // turned round in shared memory, so that a warp writes along rows; the word's place within
       // its row is XORed with the row, which leaves no bank conflicts either way
       float* buf = reinterpret_cast<float*>(t.buf);
+      __syncwarp();
 #pragma unroll
       for (int j = 0; j < 32; ++j) buf[t.lane * 32 + (j ^ t.lane)] = v[j];
       __syncwarp();

@@ -155,6 +155,38 @@ __device__ __forceinline__ void tile_store32(const CUtensorMap* m, uint8_t* buf,
     ptx::bulk_commit_group();
   }
 }
+// A warp's 32 rows of 32 16-bit values from memory: four threads take 16 bytes each of a row, so that a
+// load touches eight lines (a row for each thread touches 32 in each of four loads, which the L1's tags
+// take a cycle each for: 4 us of a 256 x 256 tile's epilogue).  Rows from R and columns from C on (C
+// rounded up to 8) are left alone.
+__device__ __forceinline__ void tile_fetch16(const void* base, int64_t ld, int row, int col, int R,
+                                             int C, int lane, uint4 (&v)[4]) {
+  const int c = col + lane % 4 * 8;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = row + 8 * i + lane / 4;
+    if (r < R && c < C)
+      v[i] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + r * ld + c);
+  }
+}
+// Through 2 KB of shared memory to a row for each thread, where tile_store16 puts its own.
+__device__ __forceinline__ void tile_spread16(uint8_t* buf, int lane, const uint4 (&v)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = 8 * i + lane / 4;
+    reinterpret_cast<uint4*>(buf + r * 64)[(lane % 4) ^ ((r >> 1) & 3)] = v[i];
+  }
+}
+__device__ __forceinline__ void tile_row16(const uint8_t* buf, int lane, uint32_t (&w)[16]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint4 u = reinterpret_cast<const uint4*>(buf + lane * 64)[j ^ ((lane >> 1) & 3)];
+    w[4 * j] = u.x;
+    w[4 * j + 1] = u.y;
+    w[4 * j + 2] = u.z;
+    w[4 * j + 3] = u.w;
+  }
+}
 // The warp's earlier tensor stores have read its buffer.
 __device__ __forceinline__ void tile_buf_free(int lane) {
   if (lane == 0) ptx::bulk_wait_group_read<0>();
