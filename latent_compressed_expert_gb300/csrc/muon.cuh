@@ -21,13 +21,14 @@ __device__ __forceinline__ uint32_t pack_half2(float a, float b) {
 __device__ __forceinline__ float2 unpack_half2(uint32_t w) {
   return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
-// X as hi + lo / LO_SCALE, both of X X_SCALE: two values
-__device__ __forceinline__ void split_half2(float a, float b, uint32_t* hi, uint32_t* lo) {
-  a *= X_SCALE;
-  b *= X_SCALE;
+// Two values of X in units of X_SCALE as hi + lo / LO_SCALE.
+__device__ __forceinline__ void split_scaled(float a, float b, uint32_t* hi, uint32_t* lo) {
   *hi = pack_half2(a, b);
   const float2 h = unpack_half2(*hi);
   *lo = pack_half2((a - h.x) * LO_SCALE, (b - h.y) * LO_SCALE);
+}
+__device__ __forceinline__ void split_half2(float a, float b, uint32_t* hi, uint32_t* lo) {
+  split_scaled(a * X_SCALE, b * X_SCALE, hi, lo);
 }
 
 // Takes element `at` (if it is one of them) out of a row's 32: its value, and 0 in its place.  (Few
@@ -181,21 +182,34 @@ __device__ __forceinline__ void muon_input8(const MuonIn& p, int64_t z, uint32_t
   for (int i = 0; i < 8; ++i) u[i] = p.nesterov ? fmaf(p.beta, f[i], u[i]) : f[i];
 }
 
-// The squares of eight values, added in fp32 after bringing them near 1 by a power of two where they
-// are far from it (their squares would leave fp32's range).
-__device__ __forceinline__ double muon_square8(const float (&u)[8]) {
-  float top = 0.0f;
+// A sum of squares.  Eight of them are added in fp32, and those sums to an fp32 pair (sum and what its
+// roundings lost); where the values are so far from 1 that their squares would leave fp32's range, they
+// are brought near it by a power of two and added in 64 bits.  (All in 64 bits, of which the GPU has few
+// units, took longer than the gradients' way from HBM.)
+struct MuonSquares {
+  float s = 0.0f, lost = 0.0f;
+  double far = 0.0;
+  __device__ __forceinline__ void add8(const float (&u)[8]) {
+    float top = 0.0f;
 #pragma unroll
-  for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(u[k]));
-  float up = 1.0f;
-  double down = 1.0;
-  if (top > 0x1p40f) up = 0x1p-90f, down = 0x1p180;
-  if (top < 0x1p-40f) up = 0x1p90f, down = 0x1p-180;
-  float s = 0.0f;
+    for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(u[k]));
+    const bool high = top > 0x1p40f, low = top < 0x1p-40f;
+    const float up = high ? 0x1p-90f : low ? 0x1p90f : 1.0f;
+    float q = 0.0f;
 #pragma unroll
-  for (int k = 0; k < 8; ++k) s = fmaf(u[k] * up, u[k] * up, s);
-  return static_cast<double>(s) * down;
-}
+    for (int k = 0; k < 8; ++k) q = fmaf(u[k] * up, u[k] * up, q);
+    if (high || low) {
+      if (top > 0.0f) far += static_cast<double>(q) * (high ? 0x1p180 : 0x1p-180);
+      return;
+    }
+    const float t = s + q, b = t - s;
+    lost += (s - (t - b)) + (q - b);
+    s = t;
+  }
+  __device__ __forceinline__ double sum() const {
+    return static_cast<double>(s) + static_cast<double>(lost) + far;
+  }
+};
 
 // 1 / (|U| + eps) as s1 s2, s1 a power of two: neither leaves fp32's range, nor does u s1 where u is
 // at most |U|.

@@ -71,27 +71,27 @@ struct PolyEpi {
   }
   __device__ __forceinline__ void chunk(const TileArgs& g, const TileCtx& t, int col, State& st,
                                         float (&v)[32], int next) const {
-    constexpr float TO_A2 = 1.0f / (A_SCALE * A_SCALE);
+    // in units of B_SCALE, o of A_SCALE:  c O^2 + (c (d_i + d_j) + b) o
+    const float k2 = c * (B_SCALE / (A_SCALE * A_SCALE));
     uint32_t w[16];
     tile_buf_free(t.lane);
     tile_spread16(t.buf, t.lane, st.next);
-    const float dj = st.dj;
+    const float di = fmaf(c, st.d, b) * (B_SCALE / A_SCALE), dj = c * st.dj * (B_SCALE / A_SCALE);
     if (next >= 0) load(g, t, next, st);
     __syncwarp();
     tile_row16(t.buf, t.lane, w);
 #pragma unroll
     for (int j = 0; j < 32; ++j) {
       const float2 o = unpack_half2(w[j / 2]);
-      const float f = (j & 1 ? o.y : o.x) * (1.0f / A_SCALE);
-      const float d = st.d + __shfl_sync(0xffffffffu, dj, j);
-      v[j] = c * fmaf(d, f, v[j] * TO_A2) + b * f;
+      const float d = di + __shfl_sync(0xffffffffu, dj, j);
+      v[j] = fmaf(d, j & 1 ? o.y : o.x, k2 * v[j]);
     }
     if (t.t.diag && t.warp_row == col) {  // here O is zero: v is c times O^2
-      const float x = take_out(v, t.lane);
+      const float x = take_out(v, t.lane) * (1.0f / B_SCALE);
       if (t.row < g.R) bdiag[t.t.z * ld + t.row] = x + st.d * fmaf(c, st.d, b);
     }
 #pragma unroll
-    for (int j = 0; j < 16; ++j) w[j] = pack_half2(v[2 * j] * B_SCALE, v[2 * j + 1] * B_SCALE);
+    for (int j = 0; j < 16; ++j) w[j] = pack_half2(v[2 * j], v[2 * j + 1]);
     tile_store16(&t.maps->out0, t.buf, t.lane, w, t.warp_row, col, t.t.z);
     if (!t.t.diag)
       tile_store16_turned(&t.maps->out0, t.buf + 2048, t.lane, w, t.warp_row, col, t.t.z);
@@ -152,32 +152,35 @@ struct ApplyEpi {
   }
   __device__ __forceinline__ void chunk(const TileArgs& g, const TileCtx& t, int col, State& st,
                                         float (&v)[32], int next) const {
-    constexpr float TO_BX = 1.0f / (B_SCALE * X_SCALE);
+    // In units of X_SCALE, with d of B's diagonal and X = hi + lo / LO_SCALE:
+    //   a X + d (X or hi) = (a + d) hi + (a + (d or 0)) / LO_SCALE lo
+    constexpr float TO_BX = LAST ? 1.0f / (B_SCALE * X_SCALE) : 1.0f / B_SCALE;
     uint32_t h[16], l[16];
     tile_buf_free(t.lane);
     tile_spread16(t.buf, t.lane, st.h);
     if constexpr (!LAST) tile_spread16(t.buf + 2048, t.lane, st.l);
-    const float di = st.d;
+    float ph = a + st.d, pl = (exact ? ph : a) * (1.0f / LO_SCALE);
+    if (LAST) ph *= 1.0f / X_SCALE;
     __syncwarp();
     tile_row16(t.buf, t.lane, h);
     if constexpr (!LAST) tile_row16(t.buf + 2048, t.lane, l);
     if (!LAST && next >= 0) load(g, t, next, st);
 #pragma unroll
     for (int j = 0; j < 32; ++j) {
-      const float d = TALL ? __shfl_sync(0xffffffffu, di, j) : di;
+      const float qh = TALL ? __shfl_sync(0xffffffffu, ph, j) : ph;
       const float2 h2 = unpack_half2(h[j / 2]);
       const float f = j & 1 ? h2.y : h2.x;
       if constexpr (LAST) {
-        v[j] = fmaf(v[j], TO_BX, (a + d) * (f * (1.0f / X_SCALE)));
+        v[j] = fmaf(v[j], TO_BX, qh * f);
       } else {
+        const float ql = TALL ? __shfl_sync(0xffffffffu, pl, j) : pl;
         const float2 l2 = unpack_half2(l[j / 2]);
-        const float x = fmaf(j & 1 ? l2.y : l2.x, 1.0f / LO_SCALE, f);
-        v[j] = fmaf(v[j], TO_BX, fmaf(a, x, d * (exact ? x : f)) * (1.0f / X_SCALE));
+        v[j] = fmaf(v[j], TO_BX, fmaf(qh, f, ql * (j & 1 ? l2.y : l2.x)));
       }
     }
     if constexpr (!LAST) {
 #pragma unroll
-      for (int j = 0; j < 16; ++j) split_half2(v[2 * j], v[2 * j + 1], &h[j], &l[j]);
+      for (int j = 0; j < 16; ++j) split_scaled(v[2 * j], v[2 * j + 1], &h[j], &l[j]);
       tile_store16(&t.maps->out0, t.buf, t.lane, h, t.warp_row, col, t.t.z);
       if (keep_lo)
         tile_store16(&t.maps->out1, t.buf + 2048, t.lane, l, t.warp_row, col, t.t.z);
@@ -212,13 +215,14 @@ __global__ void __launch_bounds__(256) muon_square_kernel(const MuonIn p) {
   pdl_launch_dependents();
   const int64_t z = blockIdx.y;
   const uint32_t per = (p.cols + 7) / 8, groups = per * static_cast<uint32_t>(p.rows);
-  double sum = 0.0;
+  MuonSquares squares;
   for (uint32_t i = blockIdx.x * 256 + threadIdx.x; i < groups; i += p.parts * 256) {
     const uint32_t row = i / per;
     float u[8];
     muon_input8<true>(p, z, row, static_cast<int>(i - row * per) * 8, u);
-    sum += muon_square8(u);
+    squares.add8(u);
   }
+  double sum = squares.sum();
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = sum;
@@ -231,20 +235,20 @@ __global__ void __launch_bounds__(256) muon_square_kernel(const MuonIn p) {
 
 // X = U / (|U| + eps) as hi + lo.
 __global__ void __launch_bounds__(256) muon_scale_kernel(const MuonIn p) {
-  __shared__ double red[8];
+  __shared__ float factors[2];
   pdl_wait();
   pdl_launch_dependents();
   const int64_t z = blockIdx.y;
-  double sum = 0.0;
-  for (int i = threadIdx.x; i < p.parts; i += 256) sum += p.part[z * p.parts + i];
+  if (threadIdx.x < 32) {  // alone: the SM has few 64-bit units
+    double sum = 0.0;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < p.parts; i += 32) sum += p.part[z * p.parts + i];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = sum;
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (threadIdx.x == 0) muon_factors(sum, p.eps, &factors[0], &factors[1]);
+  }
   __syncthreads();
-  sum = 0.0;
-  for (int w = 0; w < 8; ++w) sum += red[w];
-  float s1, s2;
-  muon_factors(sum, p.eps, &s1, &s2);
+  const float s1 = factors[0], s2 = factors[1];
   const uint32_t per = (p.cols + 7) / 8, groups = per * static_cast<uint32_t>(p.rows);
   for (uint32_t i = blockIdx.x * 256 + threadIdx.x; i < groups; i += gridDim.x * 256) {
     const uint32_t row = i / per;

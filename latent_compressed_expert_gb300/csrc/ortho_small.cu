@@ -137,7 +137,7 @@ muon_small_kernel(const __grid_constant__ SmallArgs a) {
     *r = static_cast<uint32_t>(TALL ? j0 + k : k);
     *c = (i - k * per) * 8 + (TALL ? 0 : j0);
   };
-  double sum = 0.0;
+  MuonSquares squares;
 #pragma unroll 2
   for (int i = tid; i < groups; i += SMALL_THREADS) {
     uint32_t r;
@@ -145,8 +145,9 @@ muon_small_kernel(const __grid_constant__ SmallArgs a) {
     place(i, &r, &c);
     float u[8];
     muon_input8<true>(a.in, z, r, c, u);
-    sum += muon_square8(u);
+    squares.add8(u);
   }
+  double sum = squares.sum();
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   if (lane == 0) sums[warp] = sum;
@@ -159,14 +160,17 @@ muon_small_kernel(const __grid_constant__ SmallArgs a) {
     ptx::cluster_sync();
   else
     __syncthreads();
-  sum = sums[8];
-  if (cn > 1) {
-    sum = 0.0;
-    const uint32_t at = ptx::smem_u32(sums + 8);
-    for (int p = 0; p < cn; ++p) sum += ptx::ld_cluster_f64(ptx::mapa_shared(at, p));
+  if (tid == 0) {  // alone: the SM has few 64-bit units
+    sum = sums[8];
+    if (cn > 1) {
+      sum = 0.0;
+      const uint32_t at = ptx::smem_u32(sums + 8);
+      for (int p = 0; p < cn; ++p) sum += ptx::ld_cluster_f64(ptx::mapa_shared(at, p));
+    }
+    muon_factors(sum, a.in.eps, &d[0], &d[1]);
   }
-  float s1, s2;
-  muon_factors(sum, a.in.eps, &s1, &s2);
+  __syncthreads();
+  const float s1 = d[0], s2 = d[1];
 #pragma unroll 2
   for (int i = tid; i < groups; i += SMALL_THREADS) {
     uint32_t r;
@@ -198,7 +202,6 @@ muon_small_kernel(const __grid_constant__ SmallArgs a) {
   const uint32_t idesc_s = ptx::idesc_f16_f32(BLOCK_M, s16);
   const uint32_t tq = tmem + (static_cast<uint32_t>(q * 32) << 16);
   constexpr float TO_A = 1.0f / (X_SCALE * X_SCALE), TO_A2 = 1.0f / (A_SCALE * A_SCALE);
-  constexpr float TO_BX = 1.0f / (B_SCALE * X_SCALE);
 
 #pragma unroll 1
   for (int k = 0; k < a.steps; ++k) {
@@ -291,16 +294,17 @@ muon_small_kernel(const __grid_constant__ SmallArgs a) {
       ptx::tmem_ld_32x32b_x32(tq + 128 + col, v);
       uint32_t w[16];
       small_row32(ob, row, col, w);
-      const float di = d[row];
+      const float di = d[row], pi = fmaf(cc, di, cb) * (B_SCALE / A_SCALE);
+      const float pj = cc * d[col + lane] * (B_SCALE / A_SCALE);
 #pragma unroll
       for (int j = 0; j < 32; ++j) {
-        const float2 o2 = unpack_half2(w[j / 2]);
-        const float o = (j & 1 ? o2.y : o2.x) * (1.0f / A_SCALE);
-        v[j] = cc * fmaf(di + d[col + j], o, v[j] * TO_A2) + cb * o;
+        const float2 o = unpack_half2(w[j / 2]);
+        const float p = pi + __shfl_sync(0xffffffffu, pj, j);
+        v[j] = fmaf(p, j & 1 ? o.y : o.x, cc * (B_SCALE * TO_A2) * v[j]);
       }
-      if (col == q * 32) be[row] = take_out(v, lane) + di * fmaf(cc, di, cb);
+      if (col == q * 32) be[row] = take_out(v, lane) * (1.0f / B_SCALE) + di * fmaf(cc, di, cb);
 #pragma unroll
-      for (int j = 0; j < 16; ++j) w[j] = pack_half2(v[2 * j] * B_SCALE, v[2 * j + 1] * B_SCALE);
+      for (int j = 0; j < 16; ++j) w[j] = pack_half2(v[2 * j], v[2 * j + 1]);
       small_put32(ob, row, col, w);
     }
     all_sync();
@@ -313,7 +317,8 @@ muon_small_kernel(const __grid_constant__ SmallArgs a) {
       ptx::umma_commit(bar);
     }
     done();
-    const float bi = be[row];
+    // as in ortho.cu: in units of X_SCALE, (a + d) hi + (a + (d or 0)) / LO_SCALE lo
+    const float ph = ca + be[row], pl = (exact ? ph : ca) * (1.0f / LO_SCALE);
     float* buf = reinterpret_cast<float*>(ex + warp * 4096);
 #pragma unroll 1
     for (int ch = half; ch < W / 32; ch += 2) {
@@ -326,17 +331,16 @@ muon_small_kernel(const __grid_constant__ SmallArgs a) {
 #pragma unroll
       for (int j = 0; j < 32; ++j) {
         const float2 h2 = unpack_half2(h[j / 2]);
-        const float f = j & 1 ? h2.y : h2.x;
-        float x = f;
+        float x = ph * (j & 1 ? h2.y : h2.x);
         if (!last) {
           const float2 l2 = unpack_half2(l[j / 2]);
-          x = fmaf(j & 1 ? l2.y : l2.x, 1.0f / LO_SCALE, f);
+          x = fmaf(pl, j & 1 ? l2.y : l2.x, x);
         }
-        v[j] = fmaf(v[j], TO_BX, fmaf(ca, x, bi * (exact ? x : f)) * (1.0f / X_SCALE));
+        v[j] = fmaf(v[j], 1.0f / B_SCALE, x);
       }
       if (!last) {
 #pragma unroll
-        for (int j = 0; j < 16; ++j) split_half2(v[2 * j], v[2 * j + 1], &h[j], &l[j]);
+        for (int j = 0; j < 16; ++j) split_scaled(v[2 * j], v[2 * j + 1], &h[j], &l[j]);
         small_put32(hi, row, col, h);
         small_put32(lo, row, col, l);
         continue;
@@ -345,7 +349,8 @@ muon_small_kernel(const __grid_constant__ SmallArgs a) {
       const int r0 = TALL ? j0 + col : q * 32, c0 = TALL ? q * 32 : j0 + col;
       const int rows = TALL ? a.len : a.side, cols = TALL ? a.side : a.len;
 #pragma unroll
-      for (int j = 0; j < 32; ++j) buf[TALL ? j * 32 + (lane ^ j) : lane * 32 + (j ^ lane)] = v[j];
+      for (int j = 0; j < 32; ++j)
+        buf[TALL ? j * 32 + (lane ^ j) : lane * 32 + (j ^ lane)] = v[j] * (1.0f / X_SCALE);
       __syncwarp();
       if (a.out.vec) {
         const int c8 = lane % 4 * 8;
