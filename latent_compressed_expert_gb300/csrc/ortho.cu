@@ -22,15 +22,26 @@
 
 namespace lmoe {
 
+// A chunk of a symmetric matrix, to its place and (off the diagonal's tiles) to the one it has on the
+// other side.
+__device__ __forceinline__ void put_symmetric(const TileCtx& c, int col, const uint32_t (&w)[16]) {
+  tile_put16(c.buf, c.lane, w);
+  if (!c.t.diag) tile_put16_turned(c.buf + 2048, c.lane, w);
+  tile_send(c.lane, [&] {
+    ptx::tma_store_3d(&c.maps->out0, c.buf, col, c.warp_row, c.t.z);
+    if (!c.t.diag) ptx::tma_store_3d(&c.maps->out0, c.buf + 2048, c.warp_row, col, c.t.z);
+  });
+}
+
 // A: its diagonal, and the rest as fp16.
 struct GramEpi {
   static constexpr int PART = 0;
   float* diag;   // [batch][ld]
   int64_t ld;
   struct State {};
-  __device__ __forceinline__ void begin(const TileArgs&, const TileCtx&, State&) const {}
-  __device__ __forceinline__ void load(const TileArgs&, const TileCtx&, int, State&) const {}
-  __device__ __forceinline__ void chunk(const TileArgs& g, const TileCtx& c, int col, State&,
+  __device__ __forceinline__ void begin(const TileArgs&, TileCtx&, State&) const {}
+  __device__ __forceinline__ void load(const TileArgs&, TileCtx&, int, State&) const {}
+  __device__ __forceinline__ void chunk(const TileArgs& g, TileCtx& c, int col, State&,
                                         float (&v)[32], int) const {
     constexpr float TO_A = 1.0f / (X_SCALE * X_SCALE);
     if (c.t.diag && c.warp_row == col) {
@@ -41,12 +52,10 @@ struct GramEpi {
 #pragma unroll
     for (int j = 0; j < 16; ++j)
       w[j] = pack_half2(v[2 * j] * (TO_A * A_SCALE), v[2 * j + 1] * (TO_A * A_SCALE));
-    tile_buf_free(c.lane);
-    tile_store16(&c.maps->out0, c.buf, c.lane, w, c.warp_row, col, c.t.z);
-    if (!c.t.diag)
-      tile_store16_turned(&c.maps->out0, c.buf + 2048, c.lane, w, c.warp_row, col, c.t.z);
+    tile_next_buf(c);
+    put_symmetric(c, col, w);
   }
-  __device__ __forceinline__ void end(const TileArgs&, const TileCtx&, State&) const {}
+  __device__ __forceinline__ void end(const TileArgs&, TileCtx&, State&) const {}
 };
 
 // B = b A + c A^2: its diagonal, and the rest as fp16.
@@ -61,20 +70,20 @@ struct PolyEpi {
     float d, dj;  // A's diagonal at this thread's row, and at column `lane` of the chunk
     uint4 next[4];
   };
-  __device__ __forceinline__ void begin(const TileArgs& g, const TileCtx& c_, State& st) const {
+  __device__ __forceinline__ void begin(const TileArgs& g, TileCtx& c_, State& st) const {
     st.d = c_.row < g.R ? __ldg(adiag + c_.t.z * ld + c_.row) : 0.0f;
   }
-  __device__ __forceinline__ void load(const TileArgs& g, const TileCtx& t, int col,
+  __device__ __forceinline__ void load(const TileArgs& g, TileCtx& t, int col,
                                        State& st) const {
     tile_fetch16(a + t.t.z * stride, lda, t.warp_row, col, g.R, g.C, t.lane, st.next);
     st.dj = col + t.lane < g.C ? __ldg(adiag + t.t.z * ld + col + t.lane) : 0.0f;
   }
-  __device__ __forceinline__ void chunk(const TileArgs& g, const TileCtx& t, int col, State& st,
+  __device__ __forceinline__ void chunk(const TileArgs& g, TileCtx& t, int col, State& st,
                                         float (&v)[32], int next) const {
     // in units of B_SCALE, o of A_SCALE:  c O^2 + (c (d_i + d_j) + b) o
     const float k2 = c * (B_SCALE / (A_SCALE * A_SCALE));
     uint32_t w[16];
-    tile_buf_free(t.lane);
+    tile_next_buf(t);
     tile_spread16(t.buf, t.lane, st.next);
     const float di = fmaf(c, st.d, b) * (B_SCALE / A_SCALE), dj = c * st.dj * (B_SCALE / A_SCALE);
     if (next >= 0) load(g, t, next, st);
@@ -92,11 +101,9 @@ struct PolyEpi {
     }
 #pragma unroll
     for (int j = 0; j < 16; ++j) w[j] = pack_half2(v[2 * j], v[2 * j + 1]);
-    tile_store16(&t.maps->out0, t.buf, t.lane, w, t.warp_row, col, t.t.z);
-    if (!t.t.diag)
-      tile_store16_turned(&t.maps->out0, t.buf + 2048, t.lane, w, t.warp_row, col, t.t.z);
+    put_symmetric(t, col, w);
   }
-  __device__ __forceinline__ void end(const TileArgs&, const TileCtx&, State&) const {}
+  __device__ __forceinline__ void end(const TileArgs&, TileCtx&, State&) const {}
 };
 
 // X = a X + B X (TALL: X B).  LAST: into MuonOut.
@@ -117,10 +124,10 @@ struct ApplyEpi {
     uint4 h[4], l[LAST ? 1 : 4];
     MuonOut::Old old[LAST ? 4 : 1];
   };
-  __device__ __forceinline__ void begin(const TileArgs& g, const TileCtx& t, State& st) const {
+  __device__ __forceinline__ void begin(const TileArgs& g, TileCtx& t, State& st) const {
     st.d = !TALL && t.row < g.R ? __ldg(bdiag + t.t.z * ld + t.row) : 0.0f;
   }
-  __device__ __forceinline__ void load(const TileArgs& g, const TileCtx& t, int col,
+  __device__ __forceinline__ void load(const TileArgs& g, TileCtx& t, int col,
                                        State& st) const {
     tile_fetch16(hi + t.t.z * stride, ldx, t.warp_row, col, g.R, g.C, t.lane, st.h);
     if constexpr (TALL)
@@ -137,7 +144,7 @@ struct ApplyEpi {
     }
   }
   // The chunk's 32 x 32 of the last X, from shared memory, a thread eight columns of every eighth row.
-  __device__ __forceinline__ void put_chunk(const TileArgs& g, const TileCtx& t, int col,
+  __device__ __forceinline__ void put_chunk(const TileArgs& g, TileCtx& t, int col,
                                             const State& st, const float* buf) const {
     const int c8 = t.lane % 4 * 8;
 #pragma unroll
@@ -150,13 +157,13 @@ struct ApplyEpi {
       out.put8(t.t.z, row, col + c8, x, st.old[i]);
     }
   }
-  __device__ __forceinline__ void chunk(const TileArgs& g, const TileCtx& t, int col, State& st,
+  __device__ __forceinline__ void chunk(const TileArgs& g, TileCtx& t, int col, State& st,
                                         float (&v)[32], int next) const {
     // In units of X_SCALE, with d of B's diagonal and X = hi + lo / LO_SCALE:
     //   a X + d (X or hi) = (a + d) hi + (a + (d or 0)) / LO_SCALE lo
     constexpr float TO_BX = LAST ? 1.0f / (B_SCALE * X_SCALE) : 1.0f / B_SCALE;
     uint32_t h[16], l[16];
-    tile_buf_free(t.lane);
+    tile_next_buf(t);
     tile_spread16(t.buf, t.lane, st.h);
     if constexpr (!LAST) tile_spread16(t.buf + 2048, t.lane, st.l);
     float ph = a + st.d, pl = (exact ? ph : a) * (1.0f / LO_SCALE);
@@ -181,9 +188,12 @@ struct ApplyEpi {
     if constexpr (!LAST) {
 #pragma unroll
       for (int j = 0; j < 16; ++j) split_scaled(v[2 * j], v[2 * j + 1], &h[j], &l[j]);
-      tile_store16(&t.maps->out0, t.buf, t.lane, h, t.warp_row, col, t.t.z);
-      if (keep_lo)
-        tile_store16(&t.maps->out1, t.buf + 2048, t.lane, l, t.warp_row, col, t.t.z);
+      tile_put16(t.buf, t.lane, h);
+      if (keep_lo) tile_put16(t.buf + 2048, t.lane, l);
+      tile_send(t.lane, [&] {
+        ptx::tma_store_3d(&t.maps->out0, t.buf, col, t.warp_row, t.t.z);
+        if (keep_lo) ptx::tma_store_3d(&t.maps->out1, t.buf + 2048, col, t.warp_row, t.t.z);
+      });
     } else {
       // turned round in shared memory, so that a warp writes along rows; the word's place within
       // its row is XORed with the row, which leaves no bank conflicts either way
@@ -204,7 +214,7 @@ struct ApplyEpi {
       if (next >= 0) load(g, t, next, st);
     }
   }
-  __device__ __forceinline__ void end(const TileArgs&, const TileCtx&, State&) const {}
+  __device__ __forceinline__ void end(const TileArgs&, TileCtx&, State&) const {}
 };
 
 // ------------------------------------------------------------------------- the first X

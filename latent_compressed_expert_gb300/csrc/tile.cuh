@@ -25,6 +25,7 @@ struct TileArgs {
   int ks;               // slices of the reduction (batch is 1)
   int sym;
   int bn, stages;
+  int bufs;             // buffers of an epilogue warp
   int p_rows;           // rows of P's K-major boxes (one SM: no more than R, rounded up to 8)
   int mt, nt, per;      // tiles along rows and columns, tiles of one z
   int64_t tiles;        // in all
@@ -90,41 +91,38 @@ struct TileCtx {
   int half;       // which of the two warps of this TMEM lane quarter: they take chunks in turn
   int warp_row;   // the warp's first row
   int lane;
-  uint8_t* buf;   // this warp's TILE_BUF bytes, 1024-byte aligned
+  uint8_t* buf;        // this warp's TILE_BUF bytes for the chunk, 1024-byte aligned (tile_next_buf)
+  int bufs;            // one, or two that the chunks take in turn, the second TILE_BUFS behind the
+  uint8_t* first_buf;  // first
+  int second;
 };
-constexpr int TILE_BUF = 4096;
+constexpr int TILE_BUF = 4096, TILE_BUFS = 8 * TILE_BUF;
 constexpr int TILE_CHUNK = 32;  // columns of a chunk
 
 constexpr int tile_stage_bytes(bool pair, int bn) { return LINEAR_P_BYTES + (pair ? bn / 2 : bn) * 128; }
-constexpr int tile_smem_bytes(bool pair, int bn, int stages) {
-  return stages * tile_stage_bytes(pair, bn) + 8 * TILE_BUF + LINEAR_MISC + 1024;
+constexpr int tile_smem_bytes(bool pair, int bn, int stages, int bufs) {
+  return stages * tile_stage_bytes(pair, bn) + bufs * TILE_BUFS + LINEAR_MISC + 1024;
 }
-
-constexpr int tile_stages(bool pair, int bn) {
+constexpr int tile_stages(bool pair, int bn, int bufs) {
   int st = LINEAR_MAX_STAGES;
-  while (tile_smem_bytes(pair, bn, st) > LINEAR_SMEM_MAX) --st;
+  while (tile_smem_bytes(pair, bn, st, bufs) > LINEAR_SMEM_MAX) --st;
   return st;
 }
+// A chunk waits for the tensor store of the one before it to have read the buffer.  A second buffer
+// takes that wait away, and a stage: for reductions of at most this many K-blocks, where the epilogue
+// is the longer part.
+constexpr int TILE_SHORT = 16;
 
-// A warp's 32 rows of 32 16-bit values (16 words a thread) into a tensor store of the 64-byte
-// swizzle, whose map cuts off what lies outside.  `buf`: 2 KB that no earlier store still reads.
-__device__ __forceinline__ void tile_store16(const CUtensorMap* m, uint8_t* buf, int lane,
-                                             const uint32_t (&w)[16], int row, int col, int z) {
+// A warp's 32 rows of 32 16-bit values (16 words a thread) into 2 KB of its buffer, as a tensor store
+// of the 64-byte swizzle reads them.
+__device__ __forceinline__ void tile_put16(uint8_t* buf, int lane, const uint32_t (&w)[16]) {
 #pragma unroll
   for (int j = 0; j < 4; ++j)
     reinterpret_cast<uint4*>(buf + lane * 64)[j ^ ((lane >> 1) & 3)] =
         make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-  ptx::fence_proxy_async_smem();
-  __syncwarp();
-  if (lane == 0) {
-    ptx::tma_store_3d(m, buf, col, row, z);
-    ptx::bulk_commit_group();
-  }
 }
-// The same turned round: the map's rows are the values' columns.
-__device__ __forceinline__ void tile_store16_turned(const CUtensorMap* m, uint8_t* buf, int lane,
-                                                    const uint32_t (&w)[16], int row, int col,
-                                                    int z) {
+// The same turned round: the stored rows are the values' columns.
+__device__ __forceinline__ void tile_put16_turned(uint8_t* buf, int lane, const uint32_t (&w)[16]) {
 #pragma unroll
   for (int j = 0; j < 16; ++j) {
 #pragma unroll
@@ -134,27 +132,36 @@ __device__ __forceinline__ void tile_store16_turned(const CUtensorMap* m, uint8_
           static_cast<uint16_t>(w[j] >> (16 * h));
     }
   }
-  ptx::fence_proxy_async_smem();
-  __syncwarp();
-  if (lane == 0) {
-    ptx::tma_store_3d(m, buf, row, col, z);
-    ptx::bulk_commit_group();
-  }
 }
-// 32 fp32 values a thread, the 128-byte swizzle, 4 KB.
-__device__ __forceinline__ void tile_store32(const CUtensorMap* m, uint8_t* buf, int lane,
-                                             const float (&v)[32], int row, int col, int z) {
+// 32 fp32 values a thread, 4 KB, the 128-byte swizzle.
+__device__ __forceinline__ void tile_put32(uint8_t* buf, int lane, const float (&v)[32]) {
 #pragma unroll
   for (int j = 0; j < 8; ++j)
     reinterpret_cast<float4*>(buf + lane * 128)[j ^ (lane & 7)] =
         make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+}
+// Sends a chunk's buffer off: `stores` issues its tensor stores, whose maps cut off what lies outside.
+template <class F>
+__device__ __forceinline__ void tile_send(int lane, F stores) {
   ptx::fence_proxy_async_smem();
   __syncwarp();
   if (lane == 0) {
-    ptx::tma_store_3d(m, buf, col, row, z);
+    stores();
     ptx::bulk_commit_group();
   }
 }
+// The chunk's buffer, which the stores of the last chunk that used it have read.
+__device__ __forceinline__ void tile_next_buf(TileCtx& c) {
+  if (c.bufs == 2) {
+    c.second ^= 1;
+    c.buf = c.first_buf + c.second * TILE_BUFS;
+    if (c.lane == 0) ptx::bulk_wait_group_read<1>();
+  } else if (c.lane == 0) {
+    ptx::bulk_wait_group_read<0>();
+  }
+  __syncwarp();
+}
+
 // A warp's 32 rows of 32 16-bit values from memory: four threads take 16 bytes each of a row, so that a
 // load touches eight lines (a row for each thread touches 32 in each of four loads, which the L1's tags
 // take a cycle each for: 4 us of a 256 x 256 tile's epilogue).  Rows from R and columns from C on (C
@@ -169,7 +176,7 @@ __device__ __forceinline__ void tile_fetch16(const void* base, int64_t ld, int r
       v[i] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + r * ld + c);
   }
 }
-// Through 2 KB of shared memory to a row for each thread, where tile_store16 puts its own.
+// Through 2 KB of shared memory to a row for each thread, where tile_put16 puts its own.
 __device__ __forceinline__ void tile_spread16(uint8_t* buf, int lane, const uint4 (&v)[4]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -187,17 +194,10 @@ __device__ __forceinline__ void tile_row16(const uint8_t* buf, int lane, uint32_
     w[4 * j + 3] = u.w;
   }
 }
-// The warp's earlier tensor stores have read its buffer.
-__device__ __forceinline__ void tile_buf_free(int lane) {
-  if (lane == 0) ptx::bulk_wait_group_read<0>();
-  __syncwarp();
-}
-
 // Epi: a struct of arguments with
-//   struct State; void begin(TileCtx, State&); void load(TileCtx, int col, State&), which fetches
-//   what the chunk at column `col` needs; void chunk(TileCtx, int col, State&, float (&v)[32]);
-//   void end(TileCtx, State&).
-// load is called one chunk ahead of chunk.  PART: K-blocks after which an accumulator is taken out of
+//   struct State; begin, before a tile's chunks; load, which fetches what the first chunk, at column
+//   `col`, needs; chunk, given 32 of its row's values and the column of the chunk after it (or -1), for
+//   which it fetches what that needs; end, after the chunks.  PART: K-blocks after which an accumulator is taken out of
 // TMEM and the sum goes on in registers, which round (the MMA cuts off what it adds below the last
 // bit, which makes long sums too small); 0: never.
 template <bool PAIR, bool P_MN, bool Q_MN, bool F16, class Epi>
@@ -209,7 +209,7 @@ tile_kernel(const __grid_constant__ TileMaps maps, const TileArgs g, const Epi e
   const int qn = PAIR ? bn / 2 : bn;  // columns of Q that this CTA stages
   const int stage_bytes = LINEAR_P_BYTES + qn * 128;
   extern __shared__ uint8_t smem_raw[];
-  const LinearSmem m = linear_smem(smem_raw, stages * stage_bytes + 8 * TILE_BUF);
+  const LinearSmem m = linear_smem(smem_raw, stages * stage_bytes + g.bufs * TILE_BUFS);
   uint64_t *tfull = m.extra, *tempty = m.extra + 2, *drain = m.extra + 4;
   volatile int* abort_flag = m.abort_flag;
   const int rank = PAIR ? static_cast<int>(ptx::cluster_ctarank()) : 0;
@@ -376,7 +376,9 @@ tile_kernel(const __grid_constant__ TileMaps maps, const TileArgs g, const Epi e
     c.maps = &maps;
     c.half = half;
     c.lane = lane;
-    c.buf = m.base + stages * stage_bytes + (warp - 2) * TILE_BUF;
+    c.bufs = g.bufs;
+    c.second = 0;
+    c.buf = c.first_buf = m.base + stages * stage_bytes + (warp - 2) * TILE_BUF;
     const uint32_t te[2] = {PAIR ? ptx::mapa_shared(ptx::smem_u32(&tempty[0]), 0) : 0u,
                             PAIR ? ptx::mapa_shared(ptx::smem_u32(&tempty[1]), 0) : 0u};
     typename Epi::State st;
@@ -507,13 +509,14 @@ inline TilePlan tile_plan(int64_t R, int64_t C, int64_t D, int64_t batch, bool s
   constexpr double RATE = 12500.0, FEED = 150.0, ROUND = 2050.0, EPILOGUE = 11.0;
   const double nk = static_cast<double>(ceil_div(D, BLOCK_K));
   TilePlan best{false, 128, 1e300};
+  const int bufs = nk <= TILE_SHORT ? 2 : 1;
   auto offer = [&](bool pair, int bn) {
     const int64_t tm = pair ? 256 : 128, mt = ceil_div(R, tm), nt = ceil_div(C, bn);
     const int64_t tiles = batch * (sym ? mt * (mt + 1) / 2 : mt * nt);
     const int64_t units = pair ? sms / 2 : sms;
     const double mma = 2.0 * BLOCK_K * BLOCK_M * bn / RATE;
     const double feed = tile_stage_bytes(pair, bn) / FEED;
-    const double round = ROUND / tile_stages(pair, bn);
+    const double round = ROUND / tile_stages(pair, bn, bufs);
     const double block = mma > feed ? mma : feed;
     double tile = nk * (block > round ? block : round);
     if (tile < EPILOGUE * bn) tile = EPILOGUE * bn;
@@ -539,7 +542,8 @@ int launch_tile(const TileOperand& P, const TileOperand& Q, TileMaps& maps, Tile
   if (active < 0) return LMOE_ERR_CUDA;
   constexpr int TM = PAIR ? 2 * BLOCK_M : BLOCK_M;
   g.bn = bn;
-  g.stages = tile_stages(PAIR, bn);
+  g.bufs = g.D <= TILE_SHORT * BLOCK_K ? 2 : 1;
+  g.stages = tile_stages(PAIR, bn, g.bufs);
   g.p_rows = PAIR || g.R >= BLOCK_M ? BLOCK_M : (g.R + 7) / 8 * 8;
   g.mt = static_cast<int>(ceil_div(g.R, TM));
   g.nt = static_cast<int>(ceil_div(g.C, bn));
@@ -558,7 +562,7 @@ int launch_tile(const TileOperand& P, const TileOperand& Q, TileMaps& maps, Tile
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>((PAIR ? 2 : 1) * units));
   cfg.blockDim = dim3(LINEAR_THREADS);
-  cfg.dynamicSmemBytes = static_cast<size_t>(tile_smem_bytes(PAIR, bn, g.stages));
+  cfg.dynamicSmemBytes = static_cast<size_t>(tile_smem_bytes(PAIR, bn, g.stages, g.bufs));
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

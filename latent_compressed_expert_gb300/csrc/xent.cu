@@ -48,13 +48,13 @@ struct LseEpi {
     float m, s;
     int target;
   };
-  __device__ __forceinline__ void begin(const TileArgs& g, const TileCtx& c, State& st) const {
+  __device__ __forceinline__ void begin(const TileArgs& g, TileCtx& c, State& st) const {
     st.m = -INFINITY;
     st.s = 0.0f;
     st.target = c.row < g.R ? target.of(c.row) : -1;
   }
-  __device__ __forceinline__ void load(const TileArgs&, const TileCtx&, int, State&) const {}
-  __device__ __forceinline__ void chunk(const TileArgs& g, const TileCtx& c, int col, State& st,
+  __device__ __forceinline__ void load(const TileArgs&, TileCtx&, int, State&) const {}
+  __device__ __forceinline__ void chunk(const TileArgs& g, TileCtx& c, int col, State& st,
                                         float (&v)[32], int) const {
     if (col + 32 > g.C) {
 #pragma unroll
@@ -78,7 +78,7 @@ struct LseEpi {
     st.s = (sum[0] + sum[1]) + (sum[2] + sum[3]);
     st.m = m;
   }
-  __device__ __forceinline__ void end(const TileArgs& g, const TileCtx& c, State& st) const {
+  __device__ __forceinline__ void end(const TileArgs& g, TileCtx& c, State& st) const {
     if (c.row < g.R)
       part[static_cast<int64_t>(c.t.col0 / g.bn * 2 + c.half) * g.R + c.row] =
           make_float2(st.m, st.s);
@@ -126,7 +126,7 @@ struct XentGradEpi {
     float lse, g;
     int target;
   };
-  __device__ __forceinline__ void begin(const TileArgs& g, const TileCtx& c, State& st) const {
+  __device__ __forceinline__ void begin(const TileArgs& g, TileCtx& c, State& st) const {
     st.target = c.row < g.R ? target.of(c.row) : -1;
     st.lse = st.g = 0.0f;
     if (st.target >= 0) {
@@ -137,8 +137,8 @@ struct XentGradEpi {
       st.target = INT32_MIN;
     }
   }
-  __device__ __forceinline__ void load(const TileArgs&, const TileCtx&, int, State&) const {}
-  __device__ __forceinline__ void chunk(const TileArgs&, const TileCtx& c, int col, State& st,
+  __device__ __forceinline__ void load(const TileArgs&, TileCtx&, int, State&) const {}
+  __device__ __forceinline__ void chunk(const TileArgs&, TileCtx& c, int col, State& st,
                                         float (&v)[32], int) const {
     uint32_t w[16];
 #pragma unroll
@@ -153,10 +153,11 @@ struct XentGradEpi {
       const __nv_bfloat162 b = __floats2bfloat162_rn(d[0], d[1]);
       w[j] = *reinterpret_cast<const uint32_t*>(&b);
     }
-    tile_buf_free(c.lane);
-    tile_store16(&c.maps->out0, c.buf, c.lane, w, c.warp_row, col, 0);
+    tile_next_buf(c);
+    tile_put16(c.buf, c.lane, w);
+    tile_send(c.lane, [&] { ptx::tma_store_3d(&c.maps->out0, c.buf, col, c.warp_row, 0); });
   }
-  __device__ __forceinline__ void end(const TileArgs&, const TileCtx&, State&) const {}
+  __device__ __forceinline__ void end(const TileArgs&, TileCtx&, State&) const {}
 };
 
 // dx's fp32 sums [ks][M, K] over the pieces.
@@ -167,12 +168,12 @@ struct XentDxEpi {
   struct State {
     float4 next[8];
   };
-  __device__ __forceinline__ float4* at(const TileArgs& g, const TileCtx& c, int col) const {
+  __device__ __forceinline__ float4* at(const TileArgs& g, TileCtx& c, int col) const {
     return reinterpret_cast<float4*>(
         sum + (static_cast<int64_t>(g.ks > 1 ? c.t.z : 0) * g.R + c.row) * g.C + col);
   }
-  __device__ __forceinline__ void begin(const TileArgs&, const TileCtx&, State&) const {}
-  __device__ __forceinline__ void load(const TileArgs& g, const TileCtx& c, int col,
+  __device__ __forceinline__ void begin(const TileArgs&, TileCtx&, State&) const {}
+  __device__ __forceinline__ void load(const TileArgs& g, TileCtx& c, int col,
                                        State& st) const {
     if (!add || c.row >= g.R) return;
     const float4* p = at(g, c, col);
@@ -180,7 +181,7 @@ struct XentDxEpi {
     for (int j = 0; j < 8; ++j)
       if (col + 4 * j < g.C) st.next[j] = p[j];
   }
-  __device__ __forceinline__ void chunk(const TileArgs& g, const TileCtx& c, int col, State& st,
+  __device__ __forceinline__ void chunk(const TileArgs& g, TileCtx& c, int col, State& st,
                                         float (&v)[32], int next) const {
     if (add) {
 #pragma unroll
@@ -192,14 +193,13 @@ struct XentDxEpi {
       }
       if (next >= 0) load(g, c, next, st);
     }
-    if (c.row >= g.R) return;
-    float4* p = at(g, c, col);
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (col + 4 * j < g.C)
-        p[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+    tile_next_buf(c);
+    tile_put32(c.buf, c.lane, v);
+    tile_send(c.lane, [&] {
+      ptx::tma_store_3d(&c.maps->out0, c.buf, col, c.warp_row, g.ks > 1 ? c.t.z : 0);
+    });
   }
-  __device__ __forceinline__ void end(const TileArgs&, const TileCtx&, State&) const {}
+  __device__ __forceinline__ void end(const TileArgs&, TileCtx&, State&) const {}
 };
 
 // A plain output, bf16 or fp32.
@@ -207,24 +207,25 @@ struct StoreEpi {
   static constexpr int PART = 0;
   int f32;
   struct State {};
-  __device__ __forceinline__ void begin(const TileArgs&, const TileCtx&, State&) const {}
-  __device__ __forceinline__ void load(const TileArgs&, const TileCtx&, int, State&) const {}
-  __device__ __forceinline__ void chunk(const TileArgs&, const TileCtx& c, int col, State&,
+  __device__ __forceinline__ void begin(const TileArgs&, TileCtx&, State&) const {}
+  __device__ __forceinline__ void load(const TileArgs&, TileCtx&, int, State&) const {}
+  __device__ __forceinline__ void chunk(const TileArgs&, TileCtx& c, int col, State&,
                                         float (&v)[32], int) const {
-    tile_buf_free(c.lane);
+    tile_next_buf(c);
     if (f32) {
-      tile_store32(&c.maps->out0, c.buf, c.lane, v, c.warp_row, col, c.t.z);
-      return;
-    }
-    uint32_t w[16];
+      tile_put32(c.buf, c.lane, v);
+    } else {
+      uint32_t w[16];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
-      w[j] = *reinterpret_cast<const uint32_t*>(&b);
+      for (int j = 0; j < 16; ++j) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+        w[j] = *reinterpret_cast<const uint32_t*>(&b);
+      }
+      tile_put16(c.buf, c.lane, w);
     }
-    tile_store16(&c.maps->out0, c.buf, c.lane, w, c.warp_row, col, c.t.z);
+    tile_send(c.lane, [&] { ptx::tma_store_3d(&c.maps->out0, c.buf, col, c.warp_row, c.t.z); });
   }
-  __device__ __forceinline__ void end(const TileArgs&, const TileCtx&, State&) const {}
+  __device__ __forceinline__ void end(const TileArgs&, TileCtx&, State&) const {}
 };
 
 // dx = the slices' sums added in order, rounded to bf16; a thread takes eight columns.
@@ -388,6 +389,9 @@ static int xent_backward(const lmoe_linear_xent& p, const float* dloss, __nv_bfl
     }
     if (dx) {
       TileMaps maps{};
+      if (!make_tmap_out32(&maps.out0, sum, 4, p.M, p.K, p.K, L.slices,
+                           static_cast<uint64_t>(p.M) * p.K))
+        return LMOE_ERR_CUDA;
       TileArgs g = xent_args(p, p.M, p.K, cols);
       const int nkb = static_cast<int>(ceil_div(cols, BLOCK_K));
       if (c0 == 0) slices = L.slices;
