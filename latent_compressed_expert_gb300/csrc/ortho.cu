@@ -315,14 +315,16 @@ static MuonLayout muon_layout(const lmoe_muon& p) {
   return L;
 }
 
+constexpr TileEpilogue ORTHO_EPILOGUE{800.0, 19.0};
+
 template <bool TALL, bool LAST>
 static int muon_apply(const TileOperand& X, const TileOperand& B, TileMaps& maps, const TileArgs& g,
                       const ApplyEpi<TALL, LAST>& epi, int dev, int sms, cudaStream_t stream) {
-  const TilePlan plan = tile_plan(g.R, g.C, g.D, g.batch, false, sms);
+  const TilePlan plan = tile_plan(g.R, g.C, g.D, g.batch, false, sms, ORTHO_EPILOGUE, true);
   if constexpr (TALL)
-    return launch_tile<false, false, true>(X, B, maps, g, epi, plan, dev, sms, stream);
+    return launch_tile<false, false, true, true>(X, B, maps, g, epi, plan, dev, sms, stream);
   else
-    return launch_tile<false, true, true>(B, X, maps, g, epi, plan, dev, sms, stream);
+    return launch_tile<false, true, true, true>(B, X, maps, g, epi, plan, dev, sms, stream);
 }
 
 static bool vec16(const void* p, int64_t ld, int64_t stride, int size) {
@@ -403,15 +405,17 @@ static int muon_run(const lmoe_muon& p, bool update, uint8_t* ws, cudaStream_t s
     s.R = s.C = L.side;
     s.D = L.tall ? p.rows : p.cols;
     const GramEpi gram{adiag, L.ldd};
-    const TilePlan gp = tile_plan(s.R, s.C, s.D, p.batch, true, sms);
-    rc = L.tall ? launch_tile<true, true, true>(X, X, am_out, s, gram, gp, dev, sms, stream)
-                : launch_tile<false, false, true>(X, X, am_out, s, gram, gp, dev, sms, stream);
+    const TilePlan gp = tile_plan(s.R, s.C, s.D, p.batch, true, sms, ORTHO_EPILOGUE, true);
+    s.reverse = 1;
+    rc = L.tall ? launch_tile<true, true, true, true>(X, X, am_out, s, gram, gp, dev, sms, stream)
+                : launch_tile<false, false, true, true>(X, X, am_out, s, gram, gp, dev, sms, stream);
     if (rc != LMOE_OK) return rc;
     g.inject_stall = s.inject_stall = 0;
     s.D = L.side;
-    rc = launch_tile<false, false, true>(
+    s.reverse = 0;
+    rc = launch_tile<false, false, true, true>(
         A, A, bm_out, s, PolyEpi{am, adiag, bdiag, L.ldd, L.lda, astride, cb, cc},
-        tile_plan(s.R, s.C, s.D, p.batch, true, sms), dev, sms, stream);
+        tile_plan(s.R, s.C, s.D, p.batch, true, sms, ORTHO_EPILOGUE, true), dev, sms, stream);
     if (rc != LMOE_OK) return rc;
     TileArgs f = g;
     f.R = p.rows;

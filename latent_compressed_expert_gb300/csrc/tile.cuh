@@ -23,7 +23,9 @@ struct TileArgs {
   int R, C, D;          // output rows and columns, reduction length
   int batch;            // matrices
   int ks;               // slices of the reduction (batch is 1)
+  int split;            // tile_split_kernel: CTAs of a cluster
   int sym;
+  int reverse;          // last tiles first: they read what the launch before wrote last, out of L2
   int bn, stages;
   int bufs;             // buffers of an epilogue warp
   int p_rows;           // rows of P's K-major boxes (one SM: no more than R, rounded up to 8)
@@ -47,6 +49,7 @@ struct Tile {
 
 __device__ __forceinline__ Tile tile_at(const TileArgs& g, int64_t index, int TM) {
   Tile t;
+  if (g.reverse) index = g.tiles - 1 - index;
   t.z = static_cast<int>(index / g.per);
   const int local = static_cast<int>(index % g.per);
   t.diag = false;
@@ -194,6 +197,24 @@ __device__ __forceinline__ void tile_row16(const uint8_t* buf, int lane, uint32_
     w[4 * j + 3] = u.w;
   }
 }
+// One K-block's MMAs: 32 bytes of K-major rows, 16 rows of MN-major boxes, at a time.
+template <bool P_MN, bool Q_MN, bool PAIR>
+__device__ __forceinline__ void tile_mma(uint32_t d, uint32_t sp, uint32_t idesc, bool first) {
+  const uint32_t sq = sp + LINEAR_P_BYTES;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint64_t da = P_MN ? ptx::smem_desc_sw128_mn(sp + k * 2048, LINEAR_BOX_BYTES)
+                             : ptx::smem_desc_sw128(sp + k * 32);
+    const uint64_t db = Q_MN ? ptx::smem_desc_sw128_mn(sq + k * 2048, LINEAR_BOX_BYTES)
+                             : ptx::smem_desc_sw128(sq + k * 32);
+    const uint32_t add = first && k == 0 ? 0u : 1u;
+    if constexpr (PAIR)
+      ptx::umma_bf16_pair(d, da, db, idesc, add);
+    else
+      ptx::umma_bf16(d, da, db, idesc, add);
+  }
+}
+
 // Epi: a struct of arguments with
 //   struct State; begin, before a tile's chunks; load, which fetches what the first chunk, at column
 //   `col`, needs; chunk, given 32 of its row's values and the column of the chunk after it (or -1), for
@@ -316,51 +337,38 @@ tile_kernel(const __grid_constant__ TileMaps maps, const TileArgs g, const Epi e
       bool ok = !g.inject_stall || ptx::mbar_wait(drain, 0, abort_flag, limit);
       if (!ok) tile_fail(g, abort_flag, DEVERR_TIMEOUT_MMA);
       for (int64_t index = first; ok && index < g.tiles; index += step) {
-       const Tile t = tile_at(g, index, TM);
-       for (int k0 = 0; ok && k0 < t.nk; k0 += Epi::PART ? Epi::PART : t.nk, ++lt) {
-        const int acc = lt & 1;
-        if (!ptx::mbar_wait(&tempty[acc], ((lt >> 1) & 1) ^ 1, abort_flag, limit)) {
-          tile_fail(g, abort_flag, DEVERR_TIMEOUT_MMA);
-          ok = false;
-          break;
-        }
-        ptx::tc_fence_after();
-        const uint32_t d = tmem_base + static_cast<uint32_t>(acc * 256);
-        const int k1 = Epi::PART ? min(t.nk, k0 + Epi::PART) : t.nk;
-        for (int kb = k0; kb < k1; ++kb) {
-          if (!ptx::mbar_wait(&m.full[s], parity, abort_flag, limit)) {
+        const Tile t = tile_at(g, index, TM);
+        for (int k0 = 0; ok && k0 < t.nk; k0 += Epi::PART ? Epi::PART : t.nk, ++lt) {
+          const int acc = lt & 1;
+          if (!ptx::mbar_wait(&tempty[acc], ((lt >> 1) & 1) ^ 1, abort_flag, limit)) {
             tile_fail(g, abort_flag, DEVERR_TIMEOUT_MMA);
             ok = false;
             break;
           }
           ptx::tc_fence_after();
-          const uint32_t sp = ptx::smem_u32(m.base + s * stage_bytes);
-          const uint32_t sq = sp + LINEAR_P_BYTES;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint64_t da = P_MN ? ptx::smem_desc_sw128_mn(sp + k * 2048, LINEAR_BOX_BYTES)
-                                     : ptx::smem_desc_sw128(sp + k * 32);
-            const uint64_t db = Q_MN ? ptx::smem_desc_sw128_mn(sq + k * 2048, LINEAR_BOX_BYTES)
-                                     : ptx::smem_desc_sw128(sq + k * 32);
-            const uint32_t add = kb == k0 && k == 0 ? 0u : 1u;
+          const uint32_t d = tmem_base + static_cast<uint32_t>(acc * 256);
+          const int k1 = Epi::PART ? min(t.nk, k0 + Epi::PART) : t.nk;
+          for (int kb = k0; kb < k1; ++kb) {
+            if (!ptx::mbar_wait(&m.full[s], parity, abort_flag, limit)) {
+              tile_fail(g, abort_flag, DEVERR_TIMEOUT_MMA);
+              ok = false;
+              break;
+            }
+            ptx::tc_fence_after();
+            tile_mma<P_MN, Q_MN, PAIR>(d, ptx::smem_u32(m.base + s * stage_bytes), idesc, kb == k0);
             if constexpr (PAIR)
-              ptx::umma_bf16_pair(d, da, db, idesc, add);
+              ptx::umma_commit_pair(&m.empty[s], 0x3);
             else
-              ptx::umma_bf16(d, da, db, idesc, add);
+              ptx::umma_commit(&m.empty[s]);
+            if (++s == stages) s = 0, parity ^= 1u;
           }
-          if constexpr (PAIR)
-            ptx::umma_commit_pair(&m.empty[s], 0x3);
-          else
-            ptx::umma_commit(&m.empty[s]);
-          if (++s == stages) s = 0, parity ^= 1u;
+          if (ok) {
+            if constexpr (PAIR)
+              ptx::umma_commit_pair(&tfull[acc], 0x3);
+            else
+              ptx::umma_commit(&tfull[acc]);
+          }
         }
-        if (ok) {
-          if constexpr (PAIR)
-            ptx::umma_commit_pair(&tfull[acc], 0x3);
-          else
-            ptx::umma_commit(&tfull[acc]);
-        }
-       }
       }
       // all MMAs issued by this thread complete before TMEM is released
       if constexpr (PAIR)
@@ -480,6 +488,194 @@ tile_kernel(const __grid_constant__ TileMaps maps, const TileArgs g, const Epi e
   }
 }
 
+// ------------------------------------------------------------------------- split reductions
+// For products of few tiles and long reductions: one 128 x 128 tile per cluster of ks CTAs, which split
+// the reduction between them.  The tile's 16 units of 32 rows by 32 columns are dealt to the CTAs;
+// each writes its part of a unit into its owner's shared memory, and the owner's warps add the parts
+// up in rank order and go through the same epilogue.  (Owners that fetched the parts waited a latency
+// for each: 10 us where the whole product on one SM took 6.)
+constexpr int SPLIT_BN = 128;
+constexpr int SPLIT_UNITS = 4 * (SPLIT_BN / 32), SPLIT_UNIT = 32 * 32 * 4;
+// ks parts of each of a CTA's ceil(16 / ks) units: 16, or for 3, 5, 6 and 7 CTAs 18, 20, 18 and 21
+constexpr int split_parts(int ks) { return (SPLIT_UNITS + ks - 1) / ks * ks * SPLIT_UNIT; }
+constexpr int split_smem_bytes(int ks, int stages) {
+  return stages * tile_stage_bytes(false, SPLIT_BN) + TILE_BUFS + split_parts(ks) + LINEAR_MISC + 1024;
+}
+constexpr int split_stages(int ks) {
+  int st = LINEAR_MAX_STAGES;
+  while (split_smem_bytes(ks, st) > LINEAR_SMEM_MAX) --st;
+  return st;
+}
+static_assert(split_stages(7) >= 3 && split_stages(8) >= 4, "");
+
+template <bool P_MN, bool Q_MN, bool F16, class Epi>
+__global__ void __launch_bounds__(LINEAR_THREADS, 1)
+tile_split_kernel(const __grid_constant__ TileMaps maps, const TileArgs g, const Epi epi) {
+  const int stages = g.stages, ks = g.split;
+  constexpr int STAGE = tile_stage_bytes(false, SPLIT_BN);
+  extern __shared__ uint8_t smem_raw[];
+  const LinearSmem m = linear_smem(smem_raw, stages * STAGE + TILE_BUFS + split_parts(ks));
+  uint8_t* parts = m.base + stages * STAGE + TILE_BUFS;  // [unit of this CTA][rank][32][32], fp32
+  uint64_t* tfull = m.extra;
+  volatile int* abort_flag = m.abort_flag;
+  const int rank = static_cast<int>(ptx::cluster_ctarank());
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint64_t limit = g.timeout_ns;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < stages; ++s) {
+      ptx::mbar_init(&m.full[s], 1);
+      ptx::mbar_init(&m.empty[s], 1);
+    }
+    ptx::mbar_init(tfull, 1);
+    *abort_flag = 0;
+    ptx::fence_mbar_init();
+    ptx::prefetch_tmap(&maps.p);
+    ptx::prefetch_tmap(&maps.q);
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc(m.tmem_slot, SPLIT_BN);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem_base = *m.tmem_slot;
+  ptx::cluster_arrive();  // this CTA is there to be written to
+  pdl_wait();  // from here on: the previous kernel's outputs are visible
+  pdl_launch_dependents();
+  const Tile t = tile_at(g, ptx::cluster_id_x(), BLOCK_M);
+  const int kb0 = static_cast<int>(static_cast<int64_t>(t.nk) * rank / ks);
+  const int nk = static_cast<int>(static_cast<int64_t>(t.nk) * (rank + 1) / ks) - kb0;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ------------------------------------------------------------ TMA producer
+      int it = 0, s = 0;
+      uint32_t parity = 1;
+      const uint32_t bytes =
+          (P_MN ? LINEAR_P_BYTES : static_cast<uint32_t>(g.p_rows) * 128u) + SPLIT_BN * 128u;
+      for (; it < nk; ++it) {
+        if (!ptx::mbar_wait(&m.empty[s], parity, abort_flag, limit)) {
+          tile_fail(g, abort_flag, DEVERR_TIMEOUT_PRODUCER);
+          break;
+        }
+        uint8_t* sp = m.base + s * STAGE;
+        uint8_t* sq = sp + LINEAR_P_BYTES;
+        const int k = (kb0 + it) * BLOCK_K;
+        ptx::mbar_arrive_expect_tx(&m.full[s], bytes);
+#pragma unroll
+        for (int b = 0; b < (P_MN ? 2 : 1); ++b)
+          ptx::tma_load_3d(sp + b * LINEAR_BOX_BYTES, &maps.p, &m.full[s],
+                           P_MN ? t.row0 + 64 * b : k, P_MN ? k : t.row0, t.z);
+#pragma unroll
+        for (int b = 0; b < (Q_MN ? 2 : 1); ++b)
+          ptx::tma_load_3d(sq + b * LINEAR_BOX_BYTES, &maps.q, &m.full[s],
+                           Q_MN ? t.col0 + 64 * b : k, Q_MN ? k : t.col0, t.z);
+        if (++s == stages) s = 0, parity ^= 1u;
+      }
+      // every issued copy lands before the stages are written over or the CTA leaves
+      for (int j = it > stages ? it - stages : 0; j < it; ++j)
+        if (!linear_drain(&m.full[j % stages], (j / stages) & 1, limit)) {
+          tile_fail(g, abort_flag, DEVERR_TIMEOUT_DRAIN);
+          break;
+        }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      // ------------------------------------------------------------ MMA issuer
+      const uint32_t idesc = (F16 ? ptx::idesc_f16_f32(BLOCK_M, SPLIT_BN)
+                                  : ptx::idesc_bf16_f32(BLOCK_M, SPLIT_BN)) |
+                             (P_MN ? 1u << 15 : 0u) | (Q_MN ? 1u << 16 : 0u);
+      const bool stalled = g.inject_stall && !ptx::mbar_wait(tfull, 0, abort_flag, limit);
+      if (stalled) tile_fail(g, abort_flag, DEVERR_TIMEOUT_MMA);
+      int s = 0;
+      uint32_t parity = 0;
+      for (int it = 0; !stalled && it < nk; ++it) {
+        if (!ptx::mbar_wait(&m.full[s], parity, abort_flag, limit)) {
+          tile_fail(g, abort_flag, DEVERR_TIMEOUT_MMA);
+          break;
+        }
+        ptx::tc_fence_after();
+        tile_mma<P_MN, Q_MN, false>(tmem_base, ptx::smem_u32(m.base + s * STAGE), idesc, it == 0);
+        ptx::umma_commit(&m.empty[s]);
+        if (++s == stages) s = 0, parity ^= 1u;
+      }
+      ptx::umma_commit(tfull);  // the accumulator, and every MMA issued
+      if (!linear_drain(tfull, 0, limit)) tile_fail(g, abort_flag, DEVERR_TIMEOUT_DRAIN);
+    }
+  }
+  __syncwarp();
+  // ---------------------------------------------------------------- this CTA's part
+  ptx::cluster_wait();
+  if (warp >= 2) {
+    const int q = warp & 3, half = (warp - 2) >> 2;
+    const bool ok = ptx::mbar_wait(tfull, 0, abort_flag, limit);
+    if (__all_sync(0xffffffffu, ok)) {
+      ptx::tc_fence_after();
+#pragma unroll 1
+      for (int ch = half; ch < SPLIT_BN / 32; ch += 2) {
+        float v[32];
+        ptx::tmem_ld_32x32b_x32(tmem_base + (static_cast<uint32_t>(q * 32) << 16) + ch * 32, v);
+        const int u = ch * 4 + q;  // unit u is CTA u % ks's (u / ks)-th
+        const uint32_t to = ptx::mapa_shared(
+            ptx::smem_u32(parts + (u / ks * ks + rank) * SPLIT_UNIT + lane * 128), u % ks);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          ptx::st_cluster_f32x4(to + ((j ^ (lane & 7)) << 4), v[4 * j], v[4 * j + 1], v[4 * j + 2],
+                                v[4 * j + 3]);
+      }
+    } else if (lane == 0) {
+      tile_fail(g, abort_flag, DEVERR_TIMEOUT_EPILOGUE);
+    }
+  }
+  ptx::tc_fence_before();
+  ptx::cluster_sync();  // every part is with its unit's owner
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem_base, SPLIT_BN);
+  }
+  // ---------------------------------------------------------------- epilogue
+  if (warp >= 2 && *abort_flag == 0) {
+    TileCtx c;
+    c.maps = &maps;
+    c.t = t;
+    c.half = 0;
+    c.lane = lane;
+    c.bufs = 1;
+    c.second = 0;
+    c.buf = c.first_buf = m.base + stages * STAGE + (warp - 2) * TILE_BUF;
+    typename Epi::State st;
+    for (int i = warp - 2; rank + i * ks < SPLIT_UNITS; i += 8) {
+      const int u = rank + i * ks, col = t.col0 + u / 4 * 32;
+      c.warp_row = t.row0 + u % 4 * 32;
+      c.row = c.warp_row + lane;
+      if (c.warp_row >= g.R || col >= g.C) continue;
+      epi.begin(g, c, st);
+      epi.load(g, c, col, st);
+      float v[32];
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+#pragma unroll 1
+      for (int p = 0; p < ks; ++p) {  // in rank order
+        const uint8_t* from = parts + (i * ks + p) * SPLIT_UNIT + lane * 128;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float4 f = *reinterpret_cast<const float4*>(from + ((j ^ (lane & 7)) << 4));
+          v[4 * j] += f.x;
+          v[4 * j + 1] += f.y;
+          v[4 * j + 2] += f.z;
+          v[4 * j + 3] += f.w;
+        }
+      }
+      epi.chunk(g, c, col, st, v, -1);
+      epi.end(g, c, st);
+    }
+    if (lane == 0) ptx::bulk_wait_group_all();
+  }
+  __syncthreads();
+}
+
 // ------------------------------------------------------------------------- host side
 // An operand as stored: `rows` of `cols` elements ld apart, matrices `stride` apart.
 struct TileOperand {
@@ -495,33 +691,45 @@ inline bool tile_map(CUtensorMap* m, const TileOperand& o, int batch, bool mn, i
   return make_tmap_boxes(m, o.p, 3, dims, strides, box);
 }
 
-// Tiles of a product, by time: `bn` is 0 for the least of an estimate over SM pairs of 256 columns
-// and single SMs of 64 to 256, else given for one SM alone.  The estimate's constants are those of
-// the linear layers: FLOP/ns of an SM's MMAs, bytes/ns into an SM's stages, ns from a stage's load to
-// its being free again (an SM draws no more than its stages hold per round), ns per accumulator column
-// of a tile's epilogue.
+// Tiles of a product: the least of an estimate over SM pairs of 256 columns, single SMs of 64 to 256,
+// and (may_split) clusters that split the reduction of 128 x 128 tiles.  The estimate's constants, fitted
+// to measured times:
+//   RATE   FLOP/ns of an SM's MMAs
+//   FEED   bytes/ns into an SM's stages
+//   ROUND  ns from a stage's load to its being free again: an SM draws no more than its stages hold
+//          per round
+//   SPLIT  ns of a split's exchange of parts, and for each CTA that takes part (so that a split pays
+//          from about 16 K-blocks on: 896 x 896 over 3584 23 -> 14 us, over 320 6.4 -> 8)
+// and the epilogue's, ns a tile and for each of its columns.
+struct TileEpilogue {
+  double tile, column;
+};
 struct TilePlan {
   bool pair;
-  int bn;
+  int bn, split;        // split: CTAs of a cluster, 1 without
   double ns;
 };
-inline TilePlan tile_plan(int64_t R, int64_t C, int64_t D, int64_t batch, bool sym, int sms) {
-  constexpr double RATE = 12500.0, FEED = 150.0, ROUND = 2050.0, EPILOGUE = 11.0;
-  const double nk = static_cast<double>(ceil_div(D, BLOCK_K));
-  TilePlan best{false, 128, 1e300};
+inline TilePlan tile_plan(int64_t R, int64_t C, int64_t D, int64_t batch, bool sym, int sms,
+                          TileEpilogue e, bool may_split = false) {
+  constexpr double RATE = 12500.0, FEED = 150.0, ROUND = 2050.0, SPLIT = 1500.0, SPLIT_CTA = 900.0;
+  const int64_t nk = ceil_div(D, BLOCK_K);
   const int bufs = nk <= TILE_SHORT ? 2 : 1;
+  TilePlan best{false, 128, 1, 1e300};
+  auto tiles = [&](int tm, int bn) {
+    const int64_t mt = ceil_div(R, tm), nt = ceil_div(C, bn);
+    return batch * (sym ? mt * (mt + 1) / 2 : mt * nt);
+  };
   auto offer = [&](bool pair, int bn) {
-    const int64_t tm = pair ? 256 : 128, mt = ceil_div(R, tm), nt = ceil_div(C, bn);
-    const int64_t tiles = batch * (sym ? mt * (mt + 1) / 2 : mt * nt);
-    const int64_t units = pair ? sms / 2 : sms;
     const double mma = 2.0 * BLOCK_K * BLOCK_M * bn / RATE;
     const double feed = tile_stage_bytes(pair, bn) / FEED;
     const double round = ROUND / tile_stages(pair, bn, bufs);
-    const double block = mma > feed ? mma : feed;
-    double tile = nk * (block > round ? block : round);
-    if (tile < EPILOGUE * bn) tile = EPILOGUE * bn;
-    const double ns = static_cast<double>(ceil_div(tiles, units)) * tile + EPILOGUE * bn + 200.0;
-    if (ns < best.ns) best = {pair, bn, ns};
+    const double most = mma > feed ? mma : feed;
+    const double sums = static_cast<double>(nk) * (most > round ? most : round);
+    const double cols = static_cast<double>(C < bn ? ceil_div(C, 32) * 32 : bn);
+    const double out = e.tile + e.column * cols;
+    const int64_t rounds = ceil_div(tiles(pair ? 256 : 128, bn), pair ? sms / 2 : sms);
+    const double ns = sums + static_cast<double>(rounds - 1) * (sums > out ? sums : out) + out;
+    if (ns < best.ns) best = {pair, bn, 1, ns};
   };
   offer(true, 256);
   offer(false, 128);
@@ -529,21 +737,32 @@ inline TilePlan tile_plan(int64_t R, int64_t C, int64_t D, int64_t batch, bool s
     offer(false, 64);
     offer(false, 256);
   }
+  for (int ks = 2; may_split && ks <= 8 && ks <= nk; ++ks) {
+    if (tiles(BLOCK_M, SPLIT_BN) * ks > sms) break;
+    const double ns = static_cast<double>(ceil_div(nk, ks)) * ROUND / split_stages(ks) + SPLIT +
+                      SPLIT_CTA * ks + e.tile + e.column * 32.0;
+    if (ns < best.ns) best = {false, SPLIT_BN, ks, ns};
+  }
   return best;
 }
 
 // Fills the plan's part of g, encodes P and Q and launches.  maps: the epilogue's are already there.
-template <bool PAIR, bool P_MN, bool Q_MN, bool F16, class Epi>
+// split > 0: tile_split_kernel over clusters of that many CTAs.
+template <bool PAIR, bool SPLIT, bool P_MN, bool Q_MN, bool F16, class Epi>
 int launch_tile(const TileOperand& P, const TileOperand& Q, TileMaps& maps, TileArgs g,
-                const Epi& epi, int bn, int dev, int sms, cudaStream_t stream) {
+                const Epi& epi, int bn, int split, int dev, int sms, cudaStream_t stream) {
   static std::atomic<int> cache[LINEAR_MAX_DEVICES];
-  auto kernel = tile_kernel<PAIR, P_MN, Q_MN, F16, Epi>;
+  void (*kernel)(TileMaps, TileArgs, Epi);
+  if constexpr (SPLIT)
+    kernel = tile_split_kernel<P_MN, Q_MN, F16, Epi>;
+  else
+    kernel = tile_kernel<PAIR, P_MN, Q_MN, F16, Epi>;
   const int active = linear_kernel_setup(kernel, PAIR ? 2 : 1, dev, cache);
   if (active < 0) return LMOE_ERR_CUDA;
   constexpr int TM = PAIR ? 2 * BLOCK_M : BLOCK_M;
   g.bn = bn;
   g.bufs = g.D <= TILE_SHORT * BLOCK_K ? 2 : 1;
-  g.stages = tile_stages(PAIR, bn, g.bufs);
+  g.stages = SPLIT ? split_stages(split) : tile_stages(PAIR, bn, g.bufs);
   g.p_rows = PAIR || g.R >= BLOCK_M ? BLOCK_M : (g.R + 7) / 8 * 8;
   g.mt = static_cast<int>(ceil_div(g.R, TM));
   g.nt = static_cast<int>(ceil_div(g.C, bn));
@@ -558,30 +777,39 @@ int launch_tile(const TileOperand& P, const TileOperand& Q, TileMaps& maps, Tile
     return LMOE_ERR_CUDA;
   int64_t units = PAIR ? sms / 2 : sms;
   if (PAIR && active > 0 && units > active) units = active;
-  if (units > g.tiles) units = g.tiles;
+  if (SPLIT || units > g.tiles) units = g.tiles;
+  g.split = split;
+  const int cluster = SPLIT ? split : PAIR ? 2 : 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((PAIR ? 2 : 1) * units));
+  cfg.gridDim = dim3(static_cast<unsigned>(cluster * units));
   cfg.blockDim = dim3(LINEAR_THREADS);
-  cfg.dynamicSmemBytes = static_cast<size_t>(tile_smem_bytes(PAIR, bn, g.stages, g.bufs));
+  cfg.dynamicSmemBytes = static_cast<size_t>(
+      SPLIT ? split_smem_bytes(split, g.stages) : tile_smem_bytes(PAIR, bn, g.stages, g.bufs));
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = PAIR ? 2 : 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, maps, g, epi) == cudaSuccess ? LMOE_OK : LMOE_ERR_CUDA;
 }
-// The plan's choice between the two forms.
-template <bool P_MN, bool Q_MN, bool F16, class Epi>
+// The plan's choice between the forms (SPLITS: which may split).
+template <bool P_MN, bool Q_MN, bool F16, bool SPLITS = false, class Epi>
 int launch_tile(const TileOperand& P, const TileOperand& Q, TileMaps& maps, const TileArgs& g,
                 const Epi& epi, const TilePlan& plan, int dev, int sms, cudaStream_t stream) {
-  return plan.pair
-             ? launch_tile<true, P_MN, Q_MN, F16>(P, Q, maps, g, epi, plan.bn, dev, sms, stream)
-             : launch_tile<false, P_MN, Q_MN, F16>(P, Q, maps, g, epi, plan.bn, dev, sms, stream);
+  if constexpr (SPLITS) {
+    if (plan.split > 1)
+      return launch_tile<false, true, P_MN, Q_MN, F16>(P, Q, maps, g, epi, plan.bn, plan.split, dev,
+                                                       sms, stream);
+  }
+  return plan.pair ? launch_tile<true, false, P_MN, Q_MN, F16>(P, Q, maps, g, epi, plan.bn, 1, dev,
+                                                               sms, stream)
+                   : launch_tile<false, false, P_MN, Q_MN, F16>(P, Q, maps, g, epi, plan.bn, 1, dev,
+                                                                sms, stream);
 }
 
 }  // namespace lmoe

@@ -252,14 +252,16 @@ xent_dx_kernel(const float* __restrict__ sum, int ks, int64_t M, int K, __nv_bfl
 }
 
 // ------------------------------------------------------------------------- host side
+constexpr TileEpilogue XENT_EPILOGUE{500.0, 11.0};
+
 // Up to 128 rows the head's way from HBM is the time: tiles of 128 rows, of as many columns as
 // deals the vocabulary evenly to the SMs.
 static TilePlan lse_plan(int64_t M, int64_t V, int64_t K, int sms) {
-  if (M > BLOCK_M) return tile_plan(M, V, K, 1, false, sms);
-  TilePlan best{false, 256, 1e300};
+  if (M > BLOCK_M) return tile_plan(M, V, K, 1, false, sms, XENT_EPILOGUE);
+  TilePlan best{false, 256, 1, 1e300};
   for (int bn = 64; bn <= 256; bn += 32) {
     const double ns = static_cast<double>(ceil_div(ceil_div(V, bn), sms)) * (bn + 16);
-    if (ns < best.ns) best = {false, bn, ns};
+    if (ns < best.ns) best = {false, bn, 1, ns};
   }
   return best;
 }
@@ -397,7 +399,7 @@ static int xent_backward(const lmoe_linear_xent& p, const float* dloss, __nv_bfl
       if (c0 == 0) slices = L.slices;
       g.ks = slices < nkb ? slices : nkb;
       const TilePlan plan =
-          slices > 1 ? TilePlan{false, 256, 0.0} : tile_plan(p.M, p.K, cols, 1, false, sms);
+          slices > 1 ? TilePlan{false, 256, 1, 0.0} : tile_plan(p.M, p.K, cols, 1, false, sms, XENT_EPILOGUE);
       rc = launch_tile<false, true, false>(Dl, W, maps, g, XentDxEpi{sum, c0 > 0}, plan, dev, sms,
                                            stream);
       if (rc != LMOE_OK) return rc;
@@ -408,7 +410,7 @@ static int xent_backward(const lmoe_linear_xent& p, const float* dloss, __nv_bfl
       if (!make_tmap_out32(&maps.out0, out, dw_f32 ? 4 : 2, cols, p.K, p.K, 1, 0))
         return LMOE_ERR_CUDA;
       rc = launch_tile<true, true, false>(Dl, X, maps, xent_args(p, cols, p.K, p.M),
-                                          StoreEpi{dw_f32}, tile_plan(cols, p.K, p.M, 1, false, sms),
+                                          StoreEpi{dw_f32}, tile_plan(cols, p.K, p.M, 1, false, sms, XENT_EPILOGUE),
                                           dev, sms, stream);
       if (rc != LMOE_OK) return rc;
     }
