@@ -223,7 +223,7 @@ __device__ __forceinline__ void muon_factors(double square, float eps, float* s1
 }
 
 // Orthogonalises matrices of a side of at most MUON_SMALL_SIDE, each in one cluster, with one launch.
-// False: this form does not take them.
+// False: this form does not take them, or would take longer than `most_ns` by its estimate.
 constexpr int MUON_SMALL_SIDE = 128;
 struct MuonSmall {
   MuonIn in;
@@ -231,6 +231,7 @@ struct MuonSmall {
   int batch, steps;
   const float* coeffs;  // host
   uint32_t* err;
+  double most_ns;
 };
 bool launch_muon_small(const MuonSmall& a, cudaStream_t stream, int* rc);
 

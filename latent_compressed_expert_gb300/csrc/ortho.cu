@@ -317,10 +317,27 @@ static MuonLayout muon_layout(const lmoe_muon& p) {
 
 constexpr TileEpilogue ORTHO_EPILOGUE{800.0, 19.0};
 
+struct MuonPlans {
+  TilePlan gram, poly, apply;
+  double ns;  // of the whole call
+};
+static MuonPlans muon_plans(const lmoe_muon& p, const MuonLayout& L, int sms) {
+  constexpr double HBM = 5000.0, LAUNCH = 1500.0;  // bytes/ns of the mixed passes; ns beside a plan's
+  MuonPlans m{};
+  const int len = L.tall ? p.rows : p.cols;
+  m.gram = tile_plan(L.side, L.side, len, p.batch, true, sms, ORTHO_EPILOGUE, true);
+  m.poly = tile_plan(L.side, L.side, L.side, p.batch, true, sms, ORTHO_EPILOGUE, true);
+  m.apply = tile_plan(p.rows, p.cols, L.side, p.batch, false, sms, ORTHO_EPILOGUE, true);
+  const double n = static_cast<double>(p.batch) * p.rows * p.cols, apply = 8.0 * n / HBM;
+  m.ns = 10000.0 + 12.0 * n / HBM +
+         p.steps * (m.gram.ns + m.poly.ns + (m.apply.ns > apply ? m.apply.ns : apply) + 3.0 * LAUNCH);
+  return m;
+}
+
 template <bool TALL, bool LAST>
 static int muon_apply(const TileOperand& X, const TileOperand& B, TileMaps& maps, const TileArgs& g,
-                      const ApplyEpi<TALL, LAST>& epi, int dev, int sms, cudaStream_t stream) {
-  const TilePlan plan = tile_plan(g.R, g.C, g.D, g.batch, false, sms, ORTHO_EPILOGUE, true);
+                      const ApplyEpi<TALL, LAST>& epi, const TilePlan& plan, int dev, int sms,
+                      cudaStream_t stream) {
   if constexpr (TALL)
     return launch_tile<false, false, true, true>(X, B, maps, g, epi, plan, dev, sms, stream);
   else
@@ -382,7 +399,9 @@ static int muon_run(const lmoe_muon& p, bool update, uint8_t* ws, cudaStream_t s
             vec16(out.w.p, out.w.p && rows ? out.w.ld : 0, out.w.stride, 2) &&
             vec16(out.master.p, out.master.p && rows ? out.master.ld : 0, out.master.stride, 4);
 
-  if (launch_muon_small({in, out, p.batch, p.steps, p.coeffs, p.dev_flag}, stream, &rc)) return rc;
+  const MuonPlans plans = muon_plans(p, L, sms);
+  if (launch_muon_small({in, out, p.batch, p.steps, p.coeffs, p.dev_flag, plans.ns}, stream, &rc))
+    return rc;
   const dim3 grid(static_cast<unsigned>(L.parts), static_cast<unsigned>(p.batch));
   if (launch_pdl(muon_square_kernel, grid, 256, 0, stream, in) != cudaSuccess ||
       launch_pdl(muon_scale_kernel, grid, 256, 0, stream, in) != cudaSuccess)
@@ -405,17 +424,16 @@ static int muon_run(const lmoe_muon& p, bool update, uint8_t* ws, cudaStream_t s
     s.R = s.C = L.side;
     s.D = L.tall ? p.rows : p.cols;
     const GramEpi gram{adiag, L.ldd};
-    const TilePlan gp = tile_plan(s.R, s.C, s.D, p.batch, true, sms, ORTHO_EPILOGUE, true);
     s.reverse = 1;
-    rc = L.tall ? launch_tile<true, true, true, true>(X, X, am_out, s, gram, gp, dev, sms, stream)
-                : launch_tile<false, false, true, true>(X, X, am_out, s, gram, gp, dev, sms, stream);
+    rc = L.tall ? launch_tile<true, true, true, true>(X, X, am_out, s, gram, plans.gram, dev, sms, stream)
+                : launch_tile<false, false, true, true>(X, X, am_out, s, gram, plans.gram, dev, sms, stream);
     if (rc != LMOE_OK) return rc;
     g.inject_stall = s.inject_stall = 0;
     s.D = L.side;
     s.reverse = 0;
     rc = launch_tile<false, false, true, true>(
         A, A, bm_out, s, PolyEpi{am, adiag, bdiag, L.ldd, L.lda, astride, cb, cc},
-        tile_plan(s.R, s.C, s.D, p.batch, true, sms, ORTHO_EPILOGUE, true), dev, sms, stream);
+        plans.poly, dev, sms, stream);
     if (rc != LMOE_OK) return rc;
     TileArgs f = g;
     f.R = p.rows;
@@ -426,20 +444,20 @@ static int muon_run(const lmoe_muon& p, bool update, uint8_t* ws, cudaStream_t s
     if (k + 1 == p.steps) {
       rc = L.tall ? muon_apply<true, true>(X, B, maps, f,
                                            {hi[k & 1], lo, bdiag, L.ldx, xstride, L.ldd, ca, exact, keep_lo, out},
-                                           dev, sms, stream)
+                                           plans.apply, dev, sms, stream)
                   : muon_apply<false, true>(X, B, maps, f,
                                             {hi[k & 1], lo, bdiag, L.ldx, xstride, L.ldd, ca, exact, keep_lo, out},
-                                            dev, sms, stream);
+                                            plans.apply, dev, sms, stream);
     } else {
       if (!make_tmap_out32(&maps.out0, hi[~k & 1], 2, p.rows, p.cols, L.ldx, p.batch, xstride) ||
           !make_tmap_out32(&maps.out1, lo, 2, p.rows, p.cols, L.ldx, p.batch, xstride))
         return LMOE_ERR_CUDA;
       rc = L.tall ? muon_apply<true, false>(X, B, maps, f,
                                             {hi[k & 1], lo, bdiag, L.ldx, xstride, L.ldd, ca, exact, keep_lo, out},
-                                            dev, sms, stream)
+                                            plans.apply, dev, sms, stream)
                   : muon_apply<false, false>(X, B, maps, f,
                                              {hi[k & 1], lo, bdiag, L.ldx, xstride, L.ldd, ca, exact, keep_lo, out},
-                                             dev, sms, stream);
+                                             plans.apply, dev, sms, stream);
     }
     if (rc != LMOE_OK) return rc;
   }

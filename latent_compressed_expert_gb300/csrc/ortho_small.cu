@@ -438,19 +438,21 @@ static bool launch_small(const MuonSmall& s, int dev, cudaStream_t stream, int* 
   for (int i = 0; i < 3 * s.steps; ++i) a.coeffs[i] = s.coeffs[i];
   a.err = s.err;
   a.timeout_ns = wait_limit_ns();
-  // The least of an estimate over the splits: what a step costs at any width, the exchange of A among
-  // the CTAs, and the columns' way through the epilogue, for as many rounds of clusters as it takes.
+  // The least of an estimate over the splits, in ns, fitted to measured times: ten thousand for the
+  // first X; for a step what it costs at any width, the columns' way through the epilogue, and the
+  // exchange of A among the CTAs; all for as many rounds of clusters as it takes.  (128 x 1024, five
+  // steps: 8 CTAs of 128 columns 54 us, 4 of 256 65.)
   double best = 1e300;
   for (int W = 64; W <= SMALL_MAX_W; W += 64) {
     const int cn = static_cast<int>(ceil_div(a.len, W));
     if (cn > SMALL_MAX_CLUSTER) continue;
     const int active = small_active<TALL>(cn, dev);
     if (active < 1) continue;
-    const double ns = static_cast<double>(ceil_div(s.batch, active)) *
-                      (4000.0 + (cn > 1 ? 2500.0 + 50.0 * cn : 0.0) + 12.0 * W);
+    const double step = 4300.0 + 12.0 * W + (cn > 1 ? 1000.0 + 200.0 * cn : 0.0);
+    const double ns = static_cast<double>(ceil_div(s.batch, active)) * (10000.0 + s.steps * step);
     if (ns < best) best = ns, a.W = W, a.cn = cn;
   }
-  if (best == 1e300) return false;
+  if (best > s.most_ns) return false;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(s.batch * a.cn));
   cfg.blockDim = dim3(SMALL_THREADS);

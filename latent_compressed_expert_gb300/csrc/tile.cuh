@@ -114,7 +114,7 @@ constexpr int tile_stages(bool pair, int bn, int bufs) {
 // A chunk waits for the tensor store of the one before it to have read the buffer.  A second buffer
 // takes that wait away, and a stage: for reductions of at most this many K-blocks, where the epilogue
 // is the longer part.
-constexpr int TILE_SHORT = 16;
+constexpr int TILE_SHORT = 8;
 
 // A warp's 32 rows of 32 16-bit values (16 words a thread) into 2 KB of its buffer, as a tensor store
 // of the 64-byte swizzle reads them.
