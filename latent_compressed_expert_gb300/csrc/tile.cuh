@@ -111,11 +111,6 @@ constexpr int tile_stages(bool pair, int bn, int bufs) {
   while (tile_smem_bytes(pair, bn, st, bufs) > LINEAR_SMEM_MAX) --st;
   return st;
 }
-// A chunk waits for the tensor store of the one before it to have read the buffer.  A second buffer
-// takes that wait away, and a stage: for reductions of at most this many K-blocks, where the epilogue
-// is the longer part.
-constexpr int TILE_SHORT = 8;
-
 // A warp's 32 rows of 32 16-bit values (16 words a thread) into 2 KB of its buffer, as a tensor store
 // of the 64-byte swizzle reads them.
 __device__ __forceinline__ void tile_put16(uint8_t* buf, int lane, const uint32_t (&w)[16]) {
@@ -220,7 +215,9 @@ __device__ __forceinline__ void tile_mma(uint32_t d, uint32_t sp, uint32_t idesc
 //   `col`, needs; chunk, given 32 of its row's values and the column of the chunk after it (or -1), for
 //   which it fetches what that needs; end, after the chunks.  PART: K-blocks after which an accumulator is taken out of
 // TMEM and the sum goes on in registers, which round (the MMA cuts off what it adds below the last
-// bit, which makes long sums too small); 0: never.
+// bit, which makes long sums too small); 0: never.  SHORT: a chunk waits for the tensor store of the one
+// before it to have read the buffer; a second buffer takes that wait away, and a stage: for reductions of
+// at most this many K-blocks, where the epilogue is the longer part.
 template <bool PAIR, bool P_MN, bool Q_MN, bool F16, class Epi>
 __global__ void __launch_bounds__(LINEAR_THREADS, 1)
 tile_kernel(const __grid_constant__ TileMaps maps, const TileArgs g, const Epi epi) {
@@ -703,6 +700,7 @@ inline bool tile_map(CUtensorMap* m, const TileOperand& o, int batch, bool mn, i
 // and the epilogue's, ns a tile and for each of its columns.
 struct TileEpilogue {
   double tile, column;
+  int shortest;  // Epi::SHORT
 };
 struct TilePlan {
   bool pair;
@@ -713,7 +711,7 @@ inline TilePlan tile_plan(int64_t R, int64_t C, int64_t D, int64_t batch, bool s
                           TileEpilogue e, bool may_split = false) {
   constexpr double RATE = 12500.0, FEED = 150.0, ROUND = 2050.0, SPLIT = 1500.0, SPLIT_CTA = 900.0;
   const int64_t nk = ceil_div(D, BLOCK_K);
-  const int bufs = nk <= TILE_SHORT ? 2 : 1;
+  const int bufs = nk <= e.shortest ? 2 : 1;
   TilePlan best{false, 128, 1, 1e300};
   auto tiles = [&](int tm, int bn) {
     const int64_t mt = ceil_div(R, tm), nt = ceil_div(C, bn);
@@ -761,7 +759,7 @@ int launch_tile(const TileOperand& P, const TileOperand& Q, TileMaps& maps, Tile
   if (active < 0) return LMOE_ERR_CUDA;
   constexpr int TM = PAIR ? 2 * BLOCK_M : BLOCK_M;
   g.bn = bn;
-  g.bufs = g.D <= TILE_SHORT * BLOCK_K ? 2 : 1;
+  g.bufs = g.D <= Epi::SHORT * BLOCK_K ? 2 : 1;
   g.stages = SPLIT ? split_stages(split) : tile_stages(PAIR, bn, g.bufs);
   g.p_rows = PAIR || g.R >= BLOCK_M ? BLOCK_M : (g.R + 7) / 8 * 8;
   g.mt = static_cast<int>(ceil_div(g.R, TM));

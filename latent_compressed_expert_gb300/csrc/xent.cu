@@ -16,7 +16,7 @@ constexpr float LOG2E = 1.4426950408889634f;
 // infinite logit gives an infinite sum and rows of -inf a sum of 0.
 __device__ __forceinline__ float lse_base(float m) { return fabsf(m) < INFINITY ? m : 0.0f; }
 __device__ __forceinline__ float lse_factor(float m, float to) {
-  return m == to ? 1.0f : exp2f((m - to) * LOG2E);
+  return m == to ? 1.0f : ptx::exp2_approx((m - to) * LOG2E);
 }
 __device__ __forceinline__ void lse_join(float& m, float& s, float m2, float s2) {
   const float top = fmaxf(m, m2);
@@ -40,7 +40,7 @@ struct XentTarget {
 struct LseEpi {
   // 1024 features at a time: logits over 7168 in one chain of MMAs made losses 5.6e-6 too small in the
   // norm, over 3584 2.6e-6; the loss and lse are fp32 numbers
-  static constexpr int PART = 16;
+  static constexpr int PART = 16, SHORT = 0;
   XentTarget target;
   float2* part;    // [2 tile columns][M] (maximum, sum)
   float* picked;   // [M] the targets' logits
@@ -74,7 +74,7 @@ struct LseEpi {
     const float m = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), base = lse_base(m);
     float sum[4] = {st.s * lse_factor(st.m, m), 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int j = 0; j < 32; ++j) sum[j & 3] += exp2f((v[j] - base) * LOG2E);
+    for (int j = 0; j < 32; ++j) sum[j & 3] += ptx::exp2_approx((v[j] - base) * LOG2E);
     st.s = (sum[0] + sum[1]) + (sum[2] + sum[3]);
     st.m = m;
   }
@@ -117,7 +117,7 @@ lse_join_kernel(const float2* __restrict__ part, int parts, int M, XentTarget ta
 // ------------------------------------------------------------------------- backward
 // d of a piece of the vocabulary, from column `col0` on.
 struct XentGradEpi {
-  static constexpr int PART = 0;
+  static constexpr int PART = 0, SHORT = 8;
   XentTarget target;
   const float* lse;
   const float* dloss;
@@ -141,17 +141,18 @@ struct XentGradEpi {
   __device__ __forceinline__ void chunk(const TileArgs&, TileCtx& c, int col, State& st,
                                         float (&v)[32], int) const {
     uint32_t w[16];
+    const int at = st.target - col;
+    const bool none = st.target == INT32_MIN;  // 0, whatever its logits are
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
       float d[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const float p = exp2f((v[2 * j + h] - st.lse) * LOG2E);
-        d[h] = st.g * (p - (st.target == col + 2 * j + h ? 1.0f : 0.0f));
-        if (st.target == INT32_MIN) d[h] = 0.0f;  // whatever its logits are
+        const float p = ptx::exp2_approx((v[2 * j + h] - st.lse) * LOG2E);
+        d[h] = st.g * (2 * j + h == at ? p - 1.0f : p);
       }
       const __nv_bfloat162 b = __floats2bfloat162_rn(d[0], d[1]);
-      w[j] = *reinterpret_cast<const uint32_t*>(&b);
+      w[j] = none ? 0u : *reinterpret_cast<const uint32_t*>(&b);
     }
     tile_next_buf(c);
     tile_put16(c.buf, c.lane, w);
@@ -162,7 +163,7 @@ struct XentGradEpi {
 
 // dx's fp32 sums [ks][M, K] over the pieces.
 struct XentDxEpi {
-  static constexpr int PART = 0;
+  static constexpr int PART = 0, SHORT = 8;
   float* sum;
   int add;  // not the first piece
   struct State {
@@ -204,7 +205,7 @@ struct XentDxEpi {
 
 // A plain output, bf16 or fp32.
 struct StoreEpi {
-  static constexpr int PART = 0;
+  static constexpr int PART = 0, SHORT = 16;
   int f32;
   struct State {};
   __device__ __forceinline__ void begin(const TileArgs&, TileCtx&, State&) const {}
@@ -252,12 +253,14 @@ xent_dx_kernel(const float* __restrict__ sum, int ks, int64_t M, int K, __nv_bfl
 }
 
 // ------------------------------------------------------------------------- host side
-constexpr TileEpilogue XENT_EPILOGUE{500.0, 11.0};
+// ns of an epilogue that computes exponentials, of one that stores sums, and of one that stores dw.
+constexpr TileEpilogue EXP_EPILOGUE{500.0, 24.0, 8}, SUM_EPILOGUE{500.0, 11.0, 8},
+    STORE_EPILOGUE{500.0, 11.0, 16};
 
 // Up to 128 rows the head's way from HBM is the time: tiles of 128 rows, of as many columns as
 // deals the vocabulary evenly to the SMs.
 static TilePlan lse_plan(int64_t M, int64_t V, int64_t K, int sms) {
-  if (M > BLOCK_M) return tile_plan(M, V, K, 1, false, sms, XENT_EPILOGUE);
+  if (M > BLOCK_M) return tile_plan(M, V, K, 1, false, sms, EXP_EPILOGUE);
   TilePlan best{false, 256, 1, 1e300};
   for (int bn = 64; bn <= 256; bn += 32) {
     const double ns = static_cast<double>(ceil_div(ceil_div(V, bn), sms)) * (bn + 16);
@@ -399,7 +402,8 @@ static int xent_backward(const lmoe_linear_xent& p, const float* dloss, __nv_bfl
       if (c0 == 0) slices = L.slices;
       g.ks = slices < nkb ? slices : nkb;
       const TilePlan plan =
-          slices > 1 ? TilePlan{false, 256, 1, 0.0} : tile_plan(p.M, p.K, cols, 1, false, sms, XENT_EPILOGUE);
+          slices > 1 ? TilePlan{false, 256, 1, 0.0}
+                     : tile_plan(p.M, p.K, cols, 1, false, sms, SUM_EPILOGUE);
       rc = launch_tile<false, true, false>(Dl, W, maps, g, XentDxEpi{sum, c0 > 0}, plan, dev, sms,
                                            stream);
       if (rc != LMOE_OK) return rc;
@@ -410,7 +414,8 @@ static int xent_backward(const lmoe_linear_xent& p, const float* dloss, __nv_bfl
       if (!make_tmap_out32(&maps.out0, out, dw_f32 ? 4 : 2, cols, p.K, p.K, 1, 0))
         return LMOE_ERR_CUDA;
       rc = launch_tile<true, true, false>(Dl, X, maps, xent_args(p, cols, p.K, p.M),
-                                          StoreEpi{dw_f32}, tile_plan(cols, p.K, p.M, 1, false, sms, XENT_EPILOGUE),
+                                          StoreEpi{dw_f32},
+                                          tile_plan(cols, p.K, p.M, 1, false, sms, STORE_EPILOGUE),
                                           dev, sms, stream);
       if (rc != LMOE_OK) return rc;
     }
