@@ -652,7 +652,8 @@ typedef struct lmoe_muon {
   const void *grad;        /* of grad_type */
   int grad_type;           /* LMOE_BF16 or LMOE_F32 */
   long long ldg, grad_stride;
-  void *out;               /* bf16 (lmoe_orthogonalize); may be grad itself */
+  void *out;               /* bf16 (lmoe_orthogonalize); may be a bf16 grad itself,
+                              at its distances */
   long long ldo, out_stride;
   float *momentum;         /* fp32, in and out (lmoe_muon_update, as all that follows) */
   long long ldm, momentum_stride;
@@ -675,7 +676,7 @@ typedef struct lmoe_muon {
  * equal ones, do not average out), before its rounding to bf16.  The iterates must keep to fp16's
  * range: singular values of X up to 8 (from 1 at the start) and entries of b A + c A^2 up to
  * 255 are safe.  A matrix that is not finite gives NaN, in its own place in the batch only.
- * Outputs overlap no input, nor each other (out may be grad, which is read before it is written).
+ * Outputs overlap no input, nor each other (out may be grad).
  * Errors: INVALID_ARG (also coeffs, eps or rates that are not finite), UNSUPPORTED (rows or cols above
  * 2^20, rows cols above 2^32, batch above 65535), WORKSPACE_TOO_SMALL, CUDA. */
 size_t lmoe_muon_workspace_bytes(const lmoe_muon *p);

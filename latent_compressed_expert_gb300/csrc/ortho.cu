@@ -515,6 +515,11 @@ int lmoe_orthogonalize(const lmoe_muon* p, void* ws, size_t ws_bytes, void* stre
   if (!p->out || misaligned(p->out, 2) || !distances_ok(p, p->out, p->ldo, p->out_stride, true) ||
       p->out == ws || p->grad == ws)
     return LMOE_ERR_INVALID_ARG;
+  // over the gradient: the same places, or a matrix would be written before another is read
+  if (p->out == p->grad &&
+      (p->grad_type != LMOE_BF16 || (p->rows > 1 && p->ldo != p->ldg) ||
+       (p->batch > 1 && p->out_stride != p->grad_stride)))
+    return LMOE_ERR_INVALID_ARG;
   if ((rc = muon_common_ok(p, ws, ws_bytes)) != LMOE_OK) return rc;
   return muon_run(*p, false, static_cast<uint8_t*>(ws), static_cast<cudaStream_t>(stream));
 }

@@ -6,8 +6,12 @@
 // A thread of the epilogue holds one row of the output tile and 32 of its columns at a time, so
 // that sums along a row stay in registers; what it does with them is the kernel's Epi.
 //
-//   PAIR   256 x bn tiles over SM pairs (cta_group::2), else 128 x bn tiles on one SM each; both
-//          persistent with two accumulator sets, one written out while the next is computed.
+// Three forms, chosen by tile_plan:
+//   tile_kernel over SM pairs (cta_group::2), 256 x 256 tiles, persistent, two accumulator sets, one
+//          written out while the next is computed.  A pair draws 64 KB a K-block through L2 for the
+//          tensor cores' 335 ns: 4096 x 65536 logits over 7168 features run at 1.7 PFLOP/s.
+//   tile_kernel on single SMs, 128 x 64 .. 256: for fewer rows, and for matrices of a batch.
+//   tile_split_kernel, 128 x 128 tiles whose reduction a cluster splits: few tiles, long reductions.
 //   z      a matrix of the batch, or (ks > 1) a slice of the reduction of one product.
 //   sym    P and Q are the same matrix: only tiles on or above the diagonal are computed, and the
 //          epilogue writes each to both places.
@@ -86,13 +90,13 @@ __device__ __forceinline__ void tile_fail(const TileArgs& g, volatile int* abort
   atomicOr(g.err, code);
 }
 
-// What an epilogue is given of a tile: this thread's row of it is row0 + row.
+// What an epilogue is given of a tile.
 struct TileCtx {
   const TileMaps* maps;
   Tile t;
-  int row;        // of the output
-  int half;       // which of the two warps of this TMEM lane quarter: they take chunks in turn
-  int warp_row;   // the warp's first row
+  int row;             // of the output, this thread's
+  int half;            // which of the two warps of this TMEM lane quarter: they take chunks in turn
+  int warp_row;        // the warp's first row
   int lane;
   uint8_t* buf;        // this warp's TILE_BUF bytes for the chunk, 1024-byte aligned (tile_next_buf)
   int bufs;            // one, or two that the chunks take in turn, the second TILE_BUFS behind the
@@ -111,6 +115,7 @@ constexpr int tile_stages(bool pair, int bn, int bufs) {
   while (tile_smem_bytes(pair, bn, st, bufs) > LINEAR_SMEM_MAX) --st;
   return st;
 }
+
 // A warp's 32 rows of 32 16-bit values (16 words a thread) into 2 KB of its buffer, as a tensor store
 // of the 64-byte swizzle reads them.
 __device__ __forceinline__ void tile_put16(uint8_t* buf, int lane, const uint32_t (&w)[16]) {
@@ -192,6 +197,7 @@ __device__ __forceinline__ void tile_row16(const uint8_t* buf, int lane, uint32_
     w[4 * j + 3] = u.w;
   }
 }
+
 // One K-block's MMAs: 32 bytes of K-major rows, 16 rows of MN-major boxes, at a time.
 template <bool P_MN, bool Q_MN, bool PAIR>
 __device__ __forceinline__ void tile_mma(uint32_t d, uint32_t sp, uint32_t idesc, bool first) {
@@ -210,14 +216,18 @@ __device__ __forceinline__ void tile_mma(uint32_t d, uint32_t sp, uint32_t idesc
   }
 }
 
-// Epi: a struct of arguments with
-//   struct State; begin, before a tile's chunks; load, which fetches what the first chunk, at column
-//   `col`, needs; chunk, given 32 of its row's values and the column of the chunk after it (or -1), for
-//   which it fetches what that needs; end, after the chunks.  PART: K-blocks after which an accumulator is taken out of
-// TMEM and the sum goes on in registers, which round (the MMA cuts off what it adds below the last
-// bit, which makes long sums too small); 0: never.  SHORT: a chunk waits for the tensor store of the one
-// before it to have read the buffer; a second buffer takes that wait away, and a stage: for reductions of
-// at most this many K-blocks, where the epilogue is the longer part.
+// Epi: a struct of arguments with a State that a thread keeps over a tile's chunks, and
+//   begin   before a tile's chunks
+//   load    fetches what the first chunk, at column `col`, needs
+//   chunk   takes 32 values of the thread's row, from column `col` on, and fetches what the next chunk,
+//           at column `next`, needs (-1: there is none)
+//   end     after them
+//   PART    K-blocks after which an accumulator is taken out of TMEM and the sum goes on in registers,
+//           which round (the MMA cuts off what it adds below the last bit, which makes long sums too
+//           small); 0: never
+//   SHORT   reductions of at most this many K-blocks give an epilogue warp two buffers: a chunk else
+//           waits for the tensor store of the one before it to have read the buffer.  The second one
+//           costs a stage.
 template <bool PAIR, bool P_MN, bool Q_MN, bool F16, class Epi>
 __global__ void __launch_bounds__(LINEAR_THREADS, 1)
 tile_kernel(const __grid_constant__ TileMaps maps, const TileArgs g, const Epi epi) {

@@ -258,8 +258,11 @@ constexpr TileEpilogue EXP_EPILOGUE{500.0, 24.0, 8}, SUM_EPILOGUE{500.0, 11.0, 8
     STORE_EPILOGUE{500.0, 11.0, 16};
 
 // Up to 128 rows the head's way from HBM is the time: tiles of 128 rows, of as many columns as
-// deals the vocabulary evenly to the SMs.
+// deals the vocabulary evenly to the SMs.  From XENT_MANY rows on SM pairs are always the best, and the
+// parts of a row are those of 256 columns.
+constexpr int XENT_MANY = 1024;
 static TilePlan lse_plan(int64_t M, int64_t V, int64_t K, int sms) {
+  if (M > XENT_MANY) return {true, 256, 1, 0.0};
   if (M > BLOCK_M) return tile_plan(M, V, K, 1, false, sms, EXP_EPILOGUE);
   TilePlan best{false, 256, 1, 1e300};
   for (int bn = 64; bn <= 256; bn += 32) {
@@ -272,10 +275,10 @@ static TilePlan lse_plan(int64_t M, int64_t V, int64_t K, int sms) {
 struct XentLayout {
   size_t part, picked, total;
 };
-// The parts are those of the narrowest tiles, so that the size is the same on every device.
+// The parts are those of the narrowest tiles that the plan may take.
 static XentLayout xent_layout(const lmoe_linear_xent& p) {
   XentLayout L{};
-  L.picked = (static_cast<size_t>(ceil_div(p.V, 64)) * 2 * p.M * sizeof(float2) + 255) / 256 * 256;
+  L.picked = (static_cast<size_t>(ceil_div(p.V, p.M > XENT_MANY ? 256 : 64)) * 2 * p.M * sizeof(float2) + 255) / 256 * 256;
   L.total = L.picked + static_cast<size_t>(p.M) * sizeof(float);
   return L;
 }
