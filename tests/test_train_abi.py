@@ -1,6 +1,9 @@
 """Host side of the operators that close a training step (cross entropy of a linear head, Muon's update):
 size queries and refusals.  No call here launches a kernel."""
 import ctypes
+import os
+import shutil
+import subprocess
 
 import pytest
 import torch
@@ -199,3 +202,22 @@ def test_muon_workspace(lib):
         side = min(r, c)
         least = n * (6 * r * c + 4 * side * side)
         assert least <= q(batch=n, rows=r, cols=c) <= least + n * 8 * side + (1 << 16)
+
+
+@pytest.mark.parametrize("struct,cls", [("lmoe_linear_xent", lmoe.LinearXentDesc),
+                                        ("lmoe_muon", lmoe.MuonDesc)])
+def test_binding_structs_match_the_header(struct, cls, tmp_path):
+    cc = shutil.which("gcc") or shutil.which("cc")
+    if cc is None:
+        pytest.skip("no C compiler")
+    fields = [n for n, _ in cls._fields_]
+    body = "".join(f'  printf(" %zu", offsetof({struct}, {f}));\n' for f in fields)
+    src, exe = tmp_path / "layout.c", tmp_path / "layout"
+    src.write_text('#include <stddef.h>\n#include <stdio.h>\n#include "lmoe.h"\n'
+                   f'int main(void) {{\n  printf("%zu", sizeof({struct}));\n{body}'
+                   '  printf(" %d %d %d", LMOE_MUON_MAX_STEPS, LMOE_I32, LMOE_I64);\n  return 0;\n}\n')
+    include = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include")
+    subprocess.run([cc, "-I" + include, str(src), "-o", str(exe)], check=True)
+    out = subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout.split()
+    assert [int(v) for v in out] == [ctypes.sizeof(cls)] + [getattr(cls, f).offset for f in fields] + \
+        [lmoe.MUON_MAX_STEPS, lmoe.I32, lmoe.I64]
