@@ -28,6 +28,7 @@ struct TileArgs {
   int batch;            // matrices
   int ks;               // slices of the reduction (batch is 1)
   int split;            // tile_split_kernel: CTAs of a cluster
+  int two;              // P is the sum of two matrices, z = 0 and 1
   int sym;
   int reverse;          // last tiles first: they read what the launch before wrote last, out of L2
   int bn, stages;
@@ -74,7 +75,7 @@ __device__ __forceinline__ Tile tile_at(const TileArgs& g, int64_t index, int TM
     t.row0 = p.row0;
     t.col0 = p.col0;
   }
-  const int nkb = (g.D + BLOCK_K - 1) / BLOCK_K;
+  const int nkb = (g.D + BLOCK_K - 1) / BLOCK_K << g.two;
   t.kb0 = 0;
   t.nk = nkb;
   if (g.ks > 1) {
@@ -290,7 +291,6 @@ tile_kernel(const __grid_constant__ TileMaps maps, const TileArgs g, const Epi e
       for (int64_t index = first; ok && index < g.tiles; index += step) {
         const Tile t = tile_at(g, index, TM);
         const int prow = t.row0 + rank * BLOCK_M, qrow = t.col0 + rank * qn;
-        const int z = g.ks > 1 ? 0 : t.z;
         for (int kb = 0; kb < t.nk; ++kb, ++it) {
           if (!ptx::mbar_wait(&m.empty[s], parity, abort_flag, limit)) {
             tile_fail(g, abort_flag, DEVERR_TIMEOUT_PRODUCER);
@@ -301,8 +301,11 @@ tile_kernel(const __grid_constant__ TileMaps maps, const TileArgs g, const Epi e
           uint8_t* sq = sp + LINEAR_P_BYTES;
           const uint32_t fb = PAIR ? ptx::mapa_shared(ptx::smem_u32(&m.full[s]), 0) : 0u;
           if (lead) ptx::mbar_arrive_expect_tx(&m.full[s], (PAIR ? 2u : 1u) * bytes);
-          const int k = (t.kb0 + kb) * BLOCK_K;
-          auto load = [&](uint8_t* dst, const CUtensorMap* map, int c0, int c1) {
+          // a K-block's terms one after the other: Q's part is then the same
+          const int k = (t.kb0 + kb >> g.two) * BLOCK_K;
+          const int zq = g.ks > 1 || g.two ? 0 : t.z;
+          const int zp = g.two ? t.kb0 + kb & 1 : zq;
+          auto load = [&](uint8_t* dst, const CUtensorMap* map, int c0, int c1, int z) {
             if constexpr (PAIR)
               ptx::tma_load_3d_pair(dst, map, fb, c0, c1, z);
             else
@@ -311,15 +314,15 @@ tile_kernel(const __grid_constant__ TileMaps maps, const TileArgs g, const Epi e
           if constexpr (P_MN) {
 #pragma unroll
             for (int b = 0; b < BLOCK_M / 64; ++b)
-              load(sp + b * LINEAR_BOX_BYTES, &maps.p, prow + 64 * b, k);
+              load(sp + b * LINEAR_BOX_BYTES, &maps.p, prow + 64 * b, k, zp);
           } else {
-            load(sp, &maps.p, k, prow);
+            load(sp, &maps.p, k, prow, zp);
           }
           if constexpr (Q_MN) {
             for (int b = 0; b < qn / 64; ++b)
-              load(sq + b * LINEAR_BOX_BYTES, &maps.q, qrow + 64 * b, k);
+              load(sq + b * LINEAR_BOX_BYTES, &maps.q, qrow + 64 * b, k, zq);
           } else {
-            load(sq, &maps.q, k, qrow);
+            load(sq, &maps.q, k, qrow, zq);
           }
           if (++s == stages) s = 0, parity ^= 1u;
         }
@@ -780,7 +783,7 @@ int launch_tile(const TileOperand& P, const TileOperand& Q, TileMaps& maps, Tile
   g.per = static_cast<int>(per);
   g.tiles = per * (g.ks > 1 ? g.ks : g.batch);
   g.timeout_ns = wait_limit_ns();
-  if (!tile_map(&maps.p, P, g.batch, P_MN, g.p_rows) ||
+  if (!tile_map(&maps.p, P, g.two ? 2 : g.batch, P_MN, g.p_rows) ||
       !tile_map(&maps.q, Q, g.batch, Q_MN, PAIR ? bn / 2 : bn))
     return LMOE_ERR_CUDA;
   int64_t units = PAIR ? sms / 2 : sms;

@@ -115,12 +115,19 @@ lse_join_kernel(const float2* __restrict__ part, int parts, int M, XentTarget ta
 }
 
 // ------------------------------------------------------------------------- backward
-// d of a piece of the vocabulary, from column `col0` on.
+// d of a piece of the vocabulary, from column `col0` on, as bf16.
+// Of a row's d the target's element is by far the largest, and its rounding, up to 2^-8 of it, goes
+// into all of that row's dx and of the target's row of dw.  Over many rows such errors are as large as
+// the results' own rounding in the norm, over few rows up to twice that.  So up to XENT_TWO_TERMS rows,
+// where the head's way from HBM is the time in any case, d is two terms (2^-17); beyond, `rest` keeps
+// what the target's element lost, and dx gets that times the target's weights.
+template <bool TWO>
 struct XentGradEpi {
   static constexpr int PART = 0, SHORT = 8;
   XentTarget target;
   const float* lse;
   const float* dloss;
+  float* rest;     // [M] (one term)
   int col0;
   struct State {
     float lse, g;
@@ -140,23 +147,38 @@ struct XentGradEpi {
   __device__ __forceinline__ void load(const TileArgs&, TileCtx&, int, State&) const {}
   __device__ __forceinline__ void chunk(const TileArgs&, TileCtx& c, int col, State& st,
                                         float (&v)[32], int) const {
-    uint32_t w[16];
+    uint32_t w[16], low[TWO ? 16 : 1];
     const int at = st.target - col;
     const bool none = st.target == INT32_MIN;  // 0, whatever its logits are
+    auto value = [&](float l, bool hot) {
+      const float p = ptx::exp2_approx((l - st.lse) * LOG2E);
+      return st.g * (hot ? p - 1.0f : p);
+    };
+    if (!TWO && at >= 0 && at < 32) {
+      float l = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 32; ++j) l = j == at ? v[j] : l;
+      const float d = value(l, true);
+      rest[c.row] = d - __bfloat162float(__float2bfloat16_rn(d));
+    }
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
-      float d[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float p = ptx::exp2_approx((v[2 * j + h] - st.lse) * LOG2E);
-        d[h] = st.g * (2 * j + h == at ? p - 1.0f : p);
-      }
-      const __nv_bfloat162 b = __floats2bfloat162_rn(d[0], d[1]);
+      const float d0 = value(v[2 * j], 2 * j == at), d1 = value(v[2 * j + 1], 2 * j + 1 == at);
+      const __nv_bfloat162 b = __floats2bfloat162_rn(d0, d1);
       w[j] = none ? 0u : *reinterpret_cast<const uint32_t*>(&b);
+      if constexpr (TWO) {
+        const float2 f = __bfloat1622float2(b);
+        const __nv_bfloat162 r = __floats2bfloat162_rn(d0 - f.x, d1 - f.y);
+        low[j] = none ? 0u : *reinterpret_cast<const uint32_t*>(&r);
+      }
     }
     tile_next_buf(c);
     tile_put16(c.buf, c.lane, w);
-    tile_send(c.lane, [&] { ptx::tma_store_3d(&c.maps->out0, c.buf, col, c.warp_row, 0); });
+    if constexpr (TWO) tile_put16(c.buf + 2048, c.lane, low);
+    tile_send(c.lane, [&] {
+      ptx::tma_store_3d(&c.maps->out0, c.buf, col, c.warp_row, 0);
+      if (TWO) ptx::tma_store_3d(&c.maps->out0, c.buf + 2048, col, c.warp_row, 1);
+    });
   }
   __device__ __forceinline__ void end(const TileArgs&, TileCtx&, State&) const {}
 };
@@ -229,10 +251,12 @@ struct StoreEpi {
   __device__ __forceinline__ void end(const TileArgs&, TileCtx&, State&) const {}
 };
 
-// dx = the slices' sums added in order, rounded to bf16; a thread takes eight columns.
+// dx = the slices' sums added in order, and what the target's element of d lost times the target's
+// weights, rounded to bf16; a thread takes eight columns.
 __global__ void __launch_bounds__(256)
-xent_dx_kernel(const float* __restrict__ sum, int ks, int64_t M, int K, __nv_bfloat16* dx,
-               int64_t lddx) {
+xent_dx_kernel(const float* __restrict__ sum, int ks, int64_t M, int K, XentTarget target,
+               const float* __restrict__ rest, const __nv_bfloat16* __restrict__ w, int64_t ldw,
+               __nv_bfloat16* dx, int64_t lddx) {
   pdl_wait();
   pdl_launch_dependents();
   const int per = K / 8;
@@ -243,6 +267,17 @@ xent_dx_kernel(const float* __restrict__ sum, int ks, int64_t M, int K, __nv_bfl
   float a[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) a[j] = 0.0f;
+  const int t = rest ? target.of(static_cast<int>(row)) : -1;
+  if (t >= 0) {
+    const float lost = __ldg(rest + row);
+    const uint4 u = __ldg(reinterpret_cast<const uint4*>(w + t * ldw + col));
+    const uint32_t b[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      a[2 * j] = lost * __uint_as_float(b[j] << 16);
+      a[2 * j + 1] = lost * __uint_as_float(b[j] & 0xFFFF0000u);
+    }
+  }
   for (int s = 0; s < ks; ++s) {
     float f[8];
     linear_read8(sum + (s * M + row) * K + col, f);
@@ -288,10 +323,12 @@ static XentLayout xent_layout(const lmoe_linear_xent& p) {
 constexpr int64_t XENT_PIECE_BYTES = int64_t{256} << 20;
 constexpr int XENT_PIECE_MIN = 4096;
 constexpr int XENT_MAX_SLICES = 32;
+constexpr int XENT_TWO_TERMS = BLOCK_M;
 struct XentBwdLayout {
   int64_t piece, ldd;  // columns of a piece; distance between rows of d
   int slices;          // at most
-  size_t d, sum, total;
+  int terms;           // of d
+  size_t d, sum, rest, total;
 };
 static XentBwdLayout xent_bwd_layout(const lmoe_linear_xent& p) {
   XentBwdLayout L{};
@@ -305,9 +342,11 @@ static XentBwdLayout xent_bwd_layout(const lmoe_linear_xent& p) {
   if (s > ceil_div(L.piece, BLOCK_K) / 8) s = ceil_div(L.piece, BLOCK_K) / 8;
   if (s > XENT_MAX_SLICES) s = XENT_MAX_SLICES;
   L.slices = s < 1 ? 1 : static_cast<int>(s);
+  L.terms = p.M <= XENT_TWO_TERMS ? 2 : 1;
   L.d = 0;
-  L.sum = (static_cast<size_t>(p.M) * L.ldd * 2 + 255) / 256 * 256;
-  L.total = L.sum + static_cast<size_t>(L.slices) * p.M * p.K * sizeof(float);
+  L.sum = (static_cast<size_t>(p.M) * L.ldd * 2 * L.terms + 255) / 256 * 256;
+  L.rest = L.sum + static_cast<size_t>(L.slices) * p.M * p.K * sizeof(float);
+  L.total = L.rest + static_cast<size_t>(p.M) * sizeof(float);
   return L;
 }
 
@@ -376,6 +415,7 @@ static int xent_backward(const lmoe_linear_xent& p, const float* dloss, __nv_bfl
   if (linear_device(&dev, &sms) != LMOE_OK) return LMOE_ERR_CUDA;
   const XentBwdLayout L = xent_bwd_layout(p);
   float* sum = reinterpret_cast<float*>(ws + L.sum);
+  float* rest = L.terms > 1 ? nullptr : reinterpret_cast<float*>(ws + L.rest);
   const XentTarget target{p.target, p.target_type == LMOE_I64, p.V};
   const TileOperand X{p.x, p.M, p.K, p.ldx, 0};
   bool stall = inject_stall();
@@ -383,16 +423,24 @@ static int xent_backward(const lmoe_linear_xent& p, const float* dloss, __nv_bfl
   for (int64_t c0 = 0; c0 < p.V; c0 += L.piece) {
     const int cols = static_cast<int>(p.V - c0 < L.piece ? p.V - c0 : L.piece);
     const TileOperand W{static_cast<const __nv_bfloat16*>(p.w) + c0 * p.ldw, cols, p.K, p.ldw, 0};
-    const TileOperand Dl{ws + L.d, p.M, cols, L.ldd, 0};
+    const TileOperand Dl{ws + L.d, p.M, cols, L.ldd, p.M * L.ldd};
     {
       TileMaps maps{};
-      if (!make_tmap_out32(&maps.out0, ws + L.d, 2, p.M, cols, L.ldd, 1, 0)) return LMOE_ERR_CUDA;
+      if (!make_tmap_out32(&maps.out0, ws + L.d, 2, p.M, cols, L.ldd, L.terms,
+                           static_cast<uint64_t>(p.M) * L.ldd))
+        return LMOE_ERR_CUDA;
       TileArgs g = xent_args(p, p.M, cols, p.K);
       g.inject_stall = stall;
       stall = false;
-      rc = launch_tile<false, false, false>(
-          X, W, maps, g, XentGradEpi{target, p.lse, dloss, static_cast<int>(c0)},
-          lse_plan(p.M, cols, p.K, sms), dev, sms, stream);
+      const TilePlan plan = lse_plan(p.M, cols, p.K, sms);
+      const int at = static_cast<int>(c0);
+      rc = L.terms > 1
+               ? launch_tile<false, false, false>(
+                     X, W, maps, g, XentGradEpi<true>{target, p.lse, dloss, nullptr, at}, plan, dev,
+                     sms, stream)
+               : launch_tile<false, false, false>(
+                     X, W, maps, g, XentGradEpi<false>{target, p.lse, dloss, rest, at}, plan, dev,
+                     sms, stream);
       if (rc != LMOE_OK) return rc;
     }
     if (dx) {
@@ -401,12 +449,14 @@ static int xent_backward(const lmoe_linear_xent& p, const float* dloss, __nv_bfl
                            static_cast<uint64_t>(p.M) * p.K))
         return LMOE_ERR_CUDA;
       TileArgs g = xent_args(p, p.M, p.K, cols);
+      g.two = L.terms > 1;
       const int nkb = static_cast<int>(ceil_div(cols, BLOCK_K));
       if (c0 == 0) slices = L.slices;
       g.ks = slices < nkb ? slices : nkb;
       const TilePlan plan =
           slices > 1 ? TilePlan{false, 256, 1, 0.0}
-                     : tile_plan(p.M, p.K, cols, 1, false, sms, SUM_EPILOGUE);
+                     : tile_plan(p.M, p.K, static_cast<int64_t>(cols) * L.terms, 1, false, sms,
+                                 SUM_EPILOGUE);
       rc = launch_tile<false, true, false>(Dl, W, maps, g, XentDxEpi{sum, c0 > 0}, plan, dev, sms,
                                            stream);
       if (rc != LMOE_OK) return rc;
@@ -416,9 +466,11 @@ static int xent_backward(const lmoe_linear_xent& p, const float* dloss, __nv_bfl
       uint8_t* out = static_cast<uint8_t*>(dw) + c0 * p.K * (dw_f32 ? 4 : 2);
       if (!make_tmap_out32(&maps.out0, out, dw_f32 ? 4 : 2, cols, p.K, p.K, 1, 0))
         return LMOE_ERR_CUDA;
-      rc = launch_tile<true, true, false>(Dl, X, maps, xent_args(p, cols, p.K, p.M),
-                                          StoreEpi{dw_f32},
-                                          tile_plan(cols, p.K, p.M, 1, false, sms, STORE_EPILOGUE),
+      TileArgs g = xent_args(p, cols, p.K, p.M);
+      g.two = L.terms > 1;
+      rc = launch_tile<true, true, false>(Dl, X, maps, g, StoreEpi{dw_f32},
+                                          tile_plan(cols, p.K, p.M * L.terms, 1, false, sms,
+                                                    STORE_EPILOGUE),
                                           dev, sms, stream);
       if (rc != LMOE_OK) return rc;
     }
@@ -426,7 +478,8 @@ static int xent_backward(const lmoe_linear_xent& p, const float* dloss, __nv_bfl
   if (!dx) return LMOE_OK;
   const int64_t threads = static_cast<int64_t>(p.M) * (p.K / 8);
   return launch_pdl(xent_dx_kernel, static_cast<unsigned>(ceil_div(threads, 256)), 256, 0, stream,
-                    sum, slices, p.M, p.K, dx, lddx) == cudaSuccess
+                    sum, slices, p.M, p.K, target, rest,
+                    static_cast<const __nv_bfloat16*>(p.w), p.ldw, dx, lddx) == cudaSuccess
              ? LMOE_OK
              : LMOE_ERR_CUDA;
 }
