@@ -16,7 +16,7 @@
 
 namespace lmoe {
 
-constexpr int SMALL_THREADS = 256;
+constexpr int SMALL_THREADS = 512;  // sixteen warps, four to a quarter of the TMEM lanes
 constexpr int SMALL_MAX_W = 256, SMALL_MAX_CLUSTER = 16;
 constexpr int SMALL_BOX = MUON_SMALL_SIDE * 128;            // 128 rows of 64 columns
 constexpr int SMALL_OB = 2 * SMALL_BOX;                     // A or B as fp16
@@ -78,15 +78,17 @@ muon_small_kernel(const __grid_constant__ SmallArgs a) {
   float* be = d + MUON_SMALL_SIDE;                     // B's
   uint64_t* bar = reinterpret_cast<uint64_t*>(be + MUON_SMALL_SIDE);
   uint64_t* drain = bar + 1;
+  constexpr int WARPS = SMALL_THREADS / 32;
   double* sums = reinterpret_cast<double*>(bar + 2);   // the warps', then this CTA's
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sums + 9);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sums + WARPS + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  static_assert(2 * MUON_SMALL_SIDE * 4 + 11 * 8 + 8 <= SMALL_MISC - 1024, "fits");
+  static_assert(2 * MUON_SMALL_SIDE * 4 + (WARPS + 3) * 8 + 8 <= SMALL_MISC - 1024, "fits");
+  static_assert(WARPS * 4096 <= SMALL_EX, "a buffer for each warp on the way out");
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cn = a.cn, rank = cn > 1 ? static_cast<int>(ptx::cluster_ctarank()) : 0;
   const int64_t z = blockIdx.x / cn;
-  const int q = warp & 3, half = warp >> 2, row = q * 32 + lane;  // TMEM lanes of this warp
+  const int q = warp & 3, part = warp >> 2, row = q * 32 + lane;  // TMEM lanes of this warp
   const int W = a.W, s16 = a.s16;
   const int j0 = rank * W, mine = min(W, a.len - j0);  // columns of X here
   const uint64_t limit = a.timeout_ns;
@@ -153,18 +155,18 @@ muon_small_kernel(const __grid_constant__ SmallArgs a) {
   if (lane == 0) sums[warp] = sum;
   __syncthreads();
   if (tid == 0) {
-    for (int w = 1; w < SMALL_THREADS / 32; ++w) sum += sums[w];
-    sums[8] = sum;
+    for (int w = 1; w < WARPS; ++w) sum += sums[w];
+    sums[WARPS] = sum;
   }
   if (cn > 1)
     ptx::cluster_sync();
   else
     __syncthreads();
   if (tid == 0) {  // alone: the SM has few 64-bit units
-    sum = sums[8];
+    sum = sums[WARPS];
     if (cn > 1) {
       sum = 0.0;
-      const uint32_t at = ptx::smem_u32(sums + 8);
+      const uint32_t at = ptx::smem_u32(sums + WARPS);
       for (int p = 0; p < cn; ++p) sum += ptx::ld_cluster_f64(ptx::mapa_shared(at, p));
     }
     muon_factors(sum, a.in.eps, &d[0], &d[1]);
@@ -218,24 +220,22 @@ muon_small_kernel(const __grid_constant__ SmallArgs a) {
       ptx::umma_commit(bar);
     }
     done();
-#pragma unroll 1
-    for (int ch = half * 2; ch < half * 2 + 2; ++ch) {
-      const int col = ch * 32;
-      if (col >= s16) break;
+    const int scol = part * 32;  // this warp's 32 columns of A and B
+    if (scol < s16) {
       float v[32];
-      ptx::tmem_ld_32x32b_x32(tq + col, v);
+      ptx::tmem_ld_32x32b_x32(tq + scol, v);
       if (cn > 1) {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          *reinterpret_cast<float4*>(ex + row * 512 + (((ch * 8 + j) ^ (row & 31)) << 4)) =
+          *reinterpret_cast<float4*>(ex + row * 512 + (((part * 8 + j) ^ (row & 31)) << 4)) =
               make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
       } else {
-        if (col == q * 32) d[row] = take_out(v, lane) * TO_A;
+        if (part == q) d[row] = take_out(v, lane) * TO_A;
         uint32_t w[16];
 #pragma unroll
         for (int j = 0; j < 16; ++j)
           w[j] = pack_half2(v[2 * j] * (TO_A * A_SCALE), v[2 * j + 1] * (TO_A * A_SCALE));
-        small_put32(ob, row, col, w);
+        small_put32(ob, row, scol, w);
       }
     }
     if (cn > 1) {
@@ -286,26 +286,23 @@ muon_small_kernel(const __grid_constant__ SmallArgs a) {
       ptx::umma_commit(bar);
     }
     done();
-#pragma unroll 1
-    for (int ch = half * 2; ch < half * 2 + 2; ++ch) {
-      const int col = ch * 32;
-      if (col >= s16) break;
+    if (scol < s16) {
       float v[32];
-      ptx::tmem_ld_32x32b_x32(tq + 128 + col, v);
+      ptx::tmem_ld_32x32b_x32(tq + 128 + scol, v);
       uint32_t w[16];
-      small_row32(ob, row, col, w);
+      small_row32(ob, row, scol, w);
       const float di = d[row], pi = fmaf(cc, di, cb) * (B_SCALE / A_SCALE);
-      const float pj = cc * d[col + lane] * (B_SCALE / A_SCALE);
+      const float pj = cc * d[scol + lane] * (B_SCALE / A_SCALE);
 #pragma unroll
       for (int j = 0; j < 32; ++j) {
         const float2 o = unpack_half2(w[j / 2]);
         const float p = pi + __shfl_sync(0xffffffffu, pj, j);
         v[j] = fmaf(p, j & 1 ? o.y : o.x, cc * (B_SCALE * TO_A2) * v[j]);
       }
-      if (col == q * 32) be[row] = take_out(v, lane) * (1.0f / B_SCALE) + di * fmaf(cc, di, cb);
+      if (part == q) be[row] = take_out(v, lane) * (1.0f / B_SCALE) + di * fmaf(cc, di, cb);
 #pragma unroll
       for (int j = 0; j < 16; ++j) w[j] = pack_half2(v[2 * j], v[2 * j + 1]);
-      small_put32(ob, row, col, w);
+      small_put32(ob, row, scol, w);
     }
     all_sync();
     // ------------------------------------------------------------ X
@@ -321,7 +318,7 @@ muon_small_kernel(const __grid_constant__ SmallArgs a) {
     const float ph = ca + be[row], pl = (exact ? ph : ca) * (1.0f / LO_SCALE);
     float* buf = reinterpret_cast<float*>(ex + warp * 4096);
 #pragma unroll 1
-    for (int ch = half; ch < W / 32; ch += 2) {
+    for (int ch = part; ch < W / 32; ch += 4) {
       const int col = ch * 32;
       float v[32];
       ptx::tmem_ld_32x32b_x32(tq + 256 + col, v);
@@ -438,18 +435,18 @@ static bool launch_small(const MuonSmall& s, int dev, cudaStream_t stream, int* 
   for (int i = 0; i < 3 * s.steps; ++i) a.coeffs[i] = s.coeffs[i];
   a.err = s.err;
   a.timeout_ns = wait_limit_ns();
-  // The least of an estimate over the splits, in ns, fitted to measured times: ten thousand for the
+  // The least of an estimate over the splits, in ns, fitted to measured times: nine thousand for the
   // first X; for a step what it costs at any width, the columns' way through the epilogue, and the
   // exchange of A among the CTAs; all for as many rounds of clusters as it takes.  (128 x 1024, five
-  // steps: 8 CTAs of 128 columns 54 us, 4 of 256 65.)
+  // steps: 8 CTAs of 128 columns 50 us, 4 of 256 56.)
   double best = 1e300;
   for (int W = 64; W <= SMALL_MAX_W; W += 64) {
     const int cn = static_cast<int>(ceil_div(a.len, W));
     if (cn > SMALL_MAX_CLUSTER) continue;
     const int active = small_active<TALL>(cn, dev);
     if (active < 1) continue;
-    const double step = 4300.0 + 12.0 * W + (cn > 1 ? 1000.0 + 200.0 * cn : 0.0);
-    const double ns = static_cast<double>(ceil_div(s.batch, active)) * (10000.0 + s.steps * step);
+    const double step = 1200.0 + 19.0 * W + (cn > 1 ? 2800.0 + 180.0 * cn : 0.0);
+    const double ns = static_cast<double>(ceil_div(s.batch, active)) * (9000.0 + s.steps * step);
     if (ns < best) best = ns, a.W = W, a.cn = cn;
   }
   if (best > s.most_ns) return false;
