@@ -6,7 +6,8 @@ kernels behind the C ABI of include/lmoe.h, with a thin ctypes binding.
     y = layer.forward(x, residual=x)
     y = layer.forward_few(x, residual=x, tau=tau)   # up to eight tokens, one kernel
 
-and, for the rest of a decoder block's feed-forward half, ``lmoe.add_rmsnorm`` and ``lmoe.Linear``.
+and, for the rest of a decoder block's feed-forward half, ``lmoe.add_rmsnorm`` and ``lmoe.Linear``;
+for the ends of a training step, ``lmoe.LinearCrossEntropy`` and ``lmoe.Muon``.
 
 The seeded input generators live in ``synth``; the binding in ``lmoe`` loads the library
 lazily and raises if it has not been built.

@@ -15,8 +15,19 @@
 //     a multiple of the identity, and the rounding of its diagonal was most of the error (3e-3).
 //     With A = D + O:  A^2 = D^2 + D O + O D + O^2, of which only O^2 is a product.
 //   - In B X the diagonal's part takes hi, as the product does, while later steps can still amplify
-//     what the two would differ by, and X itself in the last two steps.
+//     what the two would differ by, and X itself in the last step but one.
 // The result is then 4e-4 to 1e-3 off in the norm, half of what its rounding to bf16 adds.
+//
+// What bounds it (five steps, fp32 gradients but for the first; tensor rate of measured burst):
+//   4096 x 7168, update   1.57-1.64 ms, 0.67-0.70: a step's products take 77 + 51 + 145 us; the
+//                         symmetric ones' 136 tiles are two rounds of 76 SM pairs, 0.89 full
+//   7168 x 3584           1.35 ms, 0.61: 81 + 46 + 129 us; 105 tiles are two rounds, 0.69 full
+//   64 x 512 x 3584       1.62-1.65 ms, 0.29: 8 bytes an element and step of X in the last product
+//                         (195 us of a step's 290, 4.8 TB/s; loads and stores add to its 62 us of MMAs
+//                         rather than hide behind them: sixteen epilogue warps, L2 prefetches and wider
+//                         stores changed nothing), and 230 us for two passes over the gradients
+//   896 x 3584, update    187-197 us; 64 x 256 x 512, update, 203-217; 7 x 1001 x 333 150-157: launches
+//                         of 5 us and more each, of which 3 us are from the first load to the last MMA
 #include "muon.cuh"
 #include "tile.cuh"
 
