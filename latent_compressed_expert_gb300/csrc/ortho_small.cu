@@ -24,7 +24,7 @@ constexpr int SMALL_MAX_W = 256, SMALL_MAX_CLUSTER = 16;
 constexpr int SMALL_BOX = MUON_SMALL_SIDE * 128;            // 128 rows of 64 columns
 constexpr int SMALL_OB = 2 * SMALL_BOX;                     // A or B as fp16
 constexpr int SMALL_EX = MUON_SMALL_SIDE * MUON_SMALL_SIDE * 4;  // A's part
-constexpr int SMALL_MISC = 3072;  // barriers, diagonals, and slack for the alignment to 1024
+constexpr int SMALL_MISC = 2048 + 1024;  // barriers and diagonals, and slack for the alignment
 constexpr int small_smem_bytes(int W) {
   return 2 * (W / 64) * SMALL_BOX + SMALL_OB + SMALL_EX + SMALL_MISC;
 }

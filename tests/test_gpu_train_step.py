@@ -199,3 +199,74 @@ def test_first_call_of_a_host_thread(ex):
         torch.cuda.synchronize()
         assert codes == [lmoe.LMOE_OK]
         assert torch.equal(out, ref)
+
+
+def test_first_calls_of_a_process_are_captured(ex):
+    """Set-up (a kernel's shared memory, how many clusters fit) does not disturb a capture."""
+    import subprocess
+    import sys
+    code = """
+import torch
+from latent_compressed_expert_gb300 import lmoe
+dev = torch.device("cuda:0")
+gen = torch.Generator(device=dev).manual_seed(3)
+draw = lambda *s: torch.randn(*s, generator=gen, device=dev)
+head, muon = lmoe.LinearCrossEntropy((draw(900, 64) * 0.2).bfloat16()), lmoe.Muon()
+cases = [(draw(m, 64).bfloat16(), torch.randint(0, 900, (m,), generator=gen, device=dev),
+          torch.full((m,), 1.0 / m, device=dev)) for m in (4, 1500)]
+mats = [draw(60, 500), draw(700, 900), draw(3, 1000, 130)]
+def everything():
+    out = []
+    for x, t, w in cases:
+        loss, lse = head.forward(x, t)
+        g = head.backward(x, t, lse, w)
+        out += [loss, lse, g["dx"], g["dw"]]
+    return out + [muon.orthogonalize(m) for m in mats]
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = everything()
+graph.replay()
+torch.cuda.synchronize()
+want = everything()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, want))
+assert head.device_error() == muon.device_error() == lmoe.LMOE_OK
+print("same")
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True,
+                       timeout=100)
+    assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]
+
+
+def test_calls_of_two_host_threads(ex):
+    """Two threads on streams of their own, on the same head, weights and Muon object at once."""
+    dev = torch.device("cuda:0")
+    gen = torch.Generator(device=dev).manual_seed(2)
+    draw = lambda *s: torch.randn(*s, generator=gen, device=dev)
+    head, muon = lmoe.LinearCrossEntropy((draw(3000, 128) * 0.1).bfloat16()), lmoe.Muon()
+    data = [(draw(m, 128).bfloat16(), torch.randint(0, 3000, (m,), generator=gen, device=dev),
+             torch.full((m,), 1.0 / m, device=dev), draw(*s))
+            for m, s in ((50, (100, 300)), (700, (400, 300)))]
+
+    def work(d, out):
+        x, t, w, g = d
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(10):
+                loss, lse = head.forward(x, t)
+                grads = head.backward(x, t, lse, w)
+                out[:] = [loss, lse, grads["dx"], grads["dw"], muon.orthogonalize(g)]
+            torch.cuda.current_stream().synchronize()
+
+    want, got = [[], []], [[], []]
+    for d, o in zip(data, want):
+        work(d, o)
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=work, args=a) for a in zip(data, got)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        assert len(b) == 5 and all(torch.equal(p, q) for p, q in zip(a, b))
