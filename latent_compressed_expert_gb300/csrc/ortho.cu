@@ -46,7 +46,7 @@ __device__ __forceinline__ void put_symmetric(const TileCtx& c, int col, const u
 
 // A: its diagonal, and the rest as fp16.
 struct GramEpi {
-  static constexpr int PART = 0, SHORT = 8;
+  static constexpr int PART = 0, PART_ONE = 0, SHORT = 8;
   float* diag;   // [batch][ld]
   int64_t ld;
   struct State {};
@@ -71,7 +71,7 @@ struct GramEpi {
 
 // B = b A + c A^2: its diagonal, and the rest as fp16.
 struct PolyEpi {
-  static constexpr int PART = 0, SHORT = 8;
+  static constexpr int PART = 0, PART_ONE = 0, SHORT = 8;
   const __half* a;     // A without its diagonal, [batch][rows][lda]
   const float* adiag;  // [batch][ld]
   float* bdiag;
@@ -122,7 +122,7 @@ struct PolyEpi {
 // 438 us, of which the product is 150: its loads waited for one another.)
 template <bool TALL, bool LAST>
 struct ApplyEpi {
-  static constexpr int PART = 0, SHORT = 8;
+  static constexpr int PART = 0, PART_ONE = 0, SHORT = 8;
   const __half *hi, *lo;  // [batch][rows][ldx]
   const float* bdiag;     // [batch][ld]
   int64_t ldx, stride, ld;

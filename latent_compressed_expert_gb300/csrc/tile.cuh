@@ -225,7 +225,7 @@ __device__ __forceinline__ void tile_mma(uint32_t d, uint32_t sp, uint32_t idesc
 //   end     after them
 //   PART    K-blocks after which an accumulator is taken out of TMEM and the sum goes on in registers,
 //           which round (the MMA cuts off what it adds below the last bit, which makes long sums too
-//           small); 0: never
+//           small), over SM pairs, and on one SM (PART_ONE); 0: never
 //   SHORT   reductions of at most this many K-blocks give an epilogue warp two buffers: a chunk else
 //           waits for the tensor store of the one before it to have read the buffer.  The second one
 //           costs a stage.
@@ -235,6 +235,7 @@ tile_kernel(const __grid_constant__ TileMaps maps, const TileArgs g, const Epi e
   const int bn = g.bn, stages = g.stages;
   constexpr int TM = PAIR ? 2 * BLOCK_M : BLOCK_M;
   constexpr int TMEM_COLS = 512;  // two accumulator sets, 256 columns apart
+  constexpr int PART = PAIR ? Epi::PART : Epi::PART_ONE;
   const int qn = PAIR ? bn / 2 : bn;  // columns of Q that this CTA stages
   const int stage_bytes = LINEAR_P_BYTES + qn * 128;
   extern __shared__ uint8_t smem_raw[];
@@ -348,7 +349,7 @@ tile_kernel(const __grid_constant__ TileMaps maps, const TileArgs g, const Epi e
       if (!ok) tile_fail(g, abort_flag, DEVERR_TIMEOUT_MMA);
       for (int64_t index = first; ok && index < g.tiles; index += step) {
         const Tile t = tile_at(g, index, TM);
-        for (int k0 = 0; ok && k0 < t.nk; k0 += Epi::PART ? Epi::PART : t.nk, ++lt) {
+        for (int k0 = 0; ok && k0 < t.nk; k0 += PART ? PART : t.nk, ++lt) {
           const int acc = lt & 1;
           if (!ptx::mbar_wait(&tempty[acc], ((lt >> 1) & 1) ^ 1, abort_flag, limit)) {
             tile_fail(g, abort_flag, DEVERR_TIMEOUT_MMA);
@@ -357,7 +358,7 @@ tile_kernel(const __grid_constant__ TileMaps maps, const TileArgs g, const Epi e
           }
           ptx::tc_fence_after();
           const uint32_t d = tmem_base + static_cast<uint32_t>(acc * 256);
-          const int k1 = Epi::PART ? min(t.nk, k0 + Epi::PART) : t.nk;
+          const int k1 = PART ? min(t.nk, k0 + PART) : t.nk;
           for (int kb = k0; kb < k1; ++kb) {
             if (!ptx::mbar_wait(&m.full[s], parity, abort_flag, limit)) {
               tile_fail(g, abort_flag, DEVERR_TIMEOUT_MMA);
@@ -434,8 +435,8 @@ tile_kernel(const __grid_constant__ TileMaps maps, const TileArgs g, const Epi e
         }
       };
       if (!arrived()) break;
-      if constexpr (Epi::PART > 0) {
-        if (c.t.nk > Epi::PART) {
+      if constexpr (PART > 0) {
+        if (c.t.nk > PART) {
           float sum[4][32];
 #pragma unroll
           for (int i = 0; i < 4; ++i)
@@ -456,7 +457,7 @@ tile_kernel(const __grid_constant__ TileMaps maps, const TileArgs g, const Epi e
               }
             }
             release();
-            if ((k0 += Epi::PART) >= c.t.nk) break;
+            if ((k0 += PART) >= c.t.nk) break;
             ++lt;
             if (!(ok = arrived())) break;
           }

@@ -45,9 +45,10 @@ struct XentTarget {
 
 // ------------------------------------------------------------------------- forward
 struct LseEpi {
-  // 1024 features at a time: logits over 7168 in one chain of MMAs made losses 5.6e-6 too small in the
-  // norm, over 3584 2.6e-6; the loss and lse are fp32 numbers
-  static constexpr int PART = 16, SHORT = 0;
+  // The loss and lse are fp32 numbers.  Logits over 7168 features in one chain of MMAs made losses 5.6e-6
+  // too small in the norm; 1024 at a time 7e-7, which is what fp32 products give, and 256 at a time,
+  // where the head's way from HBM leaves the time, 2e-7 (over SM pairs that would take 8 % longer).
+  static constexpr int PART = 16, PART_ONE = 4, SHORT = 0;
   XentTarget target;
   float2* part;    // [2 tile columns][M] (maximum, sum)
   float* picked;   // [M] the targets' logits
@@ -131,7 +132,7 @@ lse_join_kernel(const float2* __restrict__ part, int parts, int M, XentTarget ta
 // what the target's element lost, and dx gets that times the target's weights.
 template <bool TWO>
 struct XentGradEpi {
-  static constexpr int PART = 0, SHORT = 8;
+  static constexpr int PART = 0, PART_ONE = 0, SHORT = 8;
   XentTarget target;
   const float* lse;
   const float* dloss;
@@ -193,7 +194,7 @@ struct XentGradEpi {
 
 // dx's fp32 sums [ks][M, K] over the pieces.
 struct XentDxEpi {
-  static constexpr int PART = 0, SHORT = 8;
+  static constexpr int PART = 0, PART_ONE = 0, SHORT = 8;
   float* sum;
   int add;  // not the first piece
   struct State {
@@ -235,7 +236,7 @@ struct XentDxEpi {
 
 // A plain output, bf16 or fp32.
 struct StoreEpi {
-  static constexpr int PART = 0, SHORT = 16;
+  static constexpr int PART = 0, PART_ONE = 0, SHORT = 16;
   int f32;
   struct State {};
   __device__ __forceinline__ void begin(const TileArgs&, TileCtx&, State&) const {}
