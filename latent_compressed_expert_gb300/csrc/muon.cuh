@@ -97,15 +97,37 @@ struct MuonOut {
     }
     if (w.p) *reinterpret_cast<uint4*>(w.at(z, row, col)) = linear_pack8(x);
   }
-  __device__ __forceinline__ void put(int64_t z, int64_t row, int64_t col, float x) const {
+  // One column of up to 32 rows, any alignment: x from buf, a row every 32 words, the word's place in it
+  // XORed with the row.  Eight rows' weights are fetched together.
+  __device__ __forceinline__ void put_column(int64_t z, int64_t row0, int rows, int64_t col,
+                                             const float* buf, int word) const {
     if (o.p) {
-      *o.at(z, row, col) = __float2bfloat16_rn(x);
+#pragma unroll 8
+      for (int r = 0; r < rows; ++r)
+        *o.at(z, row0 + r, col) = __float2bfloat16_rn(buf[r * 32 + (word ^ r)]);
       return;
     }
-    const float old = master.p ? *master.at(z, row, col) : __bfloat162float(*w.at(z, row, col));
-    const float now = fmaf(-step, x, keep * old);
-    if (master.p) *master.at(z, row, col) = now;
-    if (w.p) *w.at(z, row, col) = __float2bfloat16_rn(now);
+#pragma unroll 1
+    for (int r0 = 0; r0 < rows; r0 += 8) {
+      float old[8];
+      if (master.p) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) old[i] = *master.at(z, row0 + min(r0 + i, rows - 1), col);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          old[i] = __bfloat162float(*w.at(z, row0 + min(r0 + i, rows - 1), col));
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = r0 + i;
+        if (r < rows) {
+          const float now = fmaf(-step, buf[r * 32 + (word ^ r)], keep * old[i]);
+          if (master.p) *master.at(z, row0 + r, col) = now;
+          if (w.p) *w.at(z, row0 + r, col) = __float2bfloat16_rn(now);
+        }
+      }
+    }
   }
 };
 
@@ -125,67 +147,125 @@ struct MuonIn {
   int64_t ldx, xstride;
 };
 
-// Eight columns of the gradient, those from cols on as 0.
-__device__ __forceinline__ void muon_grad8(const MuonIn& p, int64_t z, uint32_t row, int col,
-                                           float (&g)[8]) {
-  const int64_t off = z * p.stride + static_cast<int64_t>(row) * p.ldg + col;
-  if (p.vec) {
+// Which eight elements of a part of a matrix (rows from row0 and columns from col0 on, `rows` by `cols`) a
+// thread takes for its i-th turn: eight columns in 16-byte loads (vec, i by thread), or four pairs of
+// columns (i by warp: four pieces of 64 columns, of one row or of several, a pair for each thread), so that
+// a warp's loads of single elements lie side by side.
+template <bool VEC>
+struct MuonGroups {
+  int rows, cols, row0, col0;
+  int per;          // groups, or pieces, of a row
+  uint32_t turns;
+  __device__ __forceinline__ MuonGroups(int rows_, int cols_, int row0_, int col0_)
+      : rows(rows_), cols(cols_), row0(row0_), col0(col0_) {
+    per = (cols + (VEC ? 7 : 63)) / (VEC ? 8 : 64);
+    turns = VEC ? static_cast<uint32_t>(rows) * per : (static_cast<uint32_t>(rows) * per + 3) / 4;
+  }
+  // This thread's first turn, and how far apart its turns are, among `threads` threads.
+  static __device__ __forceinline__ uint32_t first(uint32_t thread) { return VEC ? thread : thread / 32; }
+  static __device__ __forceinline__ uint32_t step(uint32_t threads) { return VEC ? threads : threads / 32; }
+  // Pair k's row and first column in the matrix; false: there is none.
+  __device__ __forceinline__ bool at(uint32_t i, int k, int* row, int* col) const {
+    const uint32_t piece = VEC ? i : 4 * i + k;
+    const int r = static_cast<int>(piece / per);
+    const int c = (static_cast<int>(piece) - r * per) * (VEC ? 8 : 64) +
+                  (VEC ? 2 * k : 2 * static_cast<int>(threadIdx.x & 31));
+    *row = row0 + r;
+    *col = col0 + c;
+    return r < rows && c < cols;
+  }
+};
+
+// The matrix to be orthogonalised at the i-th turn's elements, 0 where there is none; STEP: after the
+// momentum's step.
+template <bool STEP, bool VEC>
+__device__ __forceinline__ void muon_input8(const MuonIn& p, int64_t z, const MuonGroups<VEC>& of,
+                                            uint32_t i, float (&u)[8]) {
+  float f[8];
+  float* m = p.m.p;
+  if constexpr (VEC) {
+    int row, col;
+    of.at(i, 0, &row, &col);
+    const int64_t off = z * p.stride + row * p.ldg + col;
     if (p.f32) {
-      linear_read8(static_cast<const float*>(p.grad) + off, g);
+      linear_read8(static_cast<const float*>(p.grad) + off, u);
     } else {
-      const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.grad) + off);
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+      const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.grad) + off);
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        g[2 * i] = __uint_as_float(w[i] << 16);
-        g[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+      for (int k = 0; k < 4; ++k) {
+        u[2 * k] = __uint_as_float(w[k] << 16);
+        u[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
       }
     }
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    g[i] = 0.0f;
-    if (col + i < p.cols)
-      g[i] = p.f32 ? static_cast<const float*>(p.grad)[off + i]
-                   : __bfloat162float(static_cast<const __nv_bfloat16*>(p.grad)[off + i]);
-  }
-}
-// The matrix to be orthogonalised there; STEP: after the momentum's step.
-template <bool STEP>
-__device__ __forceinline__ void muon_input8(const MuonIn& p, int64_t z, uint32_t row, int col,
-                                            float (&u)[8]) {
-  muon_grad8(p, z, row, col, u);
-  if (!p.m.p) return;
-  float* m = p.m.at(z, row, col);
-  float f[8];
-  if (p.vec) {
+    if (!m) return;
+    m = p.m.at(z, row, col);
     linear_read8(m, f);
-  } else {
+    if (STEP) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = col + i < p.cols ? m[i] : 0.0f;
-  }
-  if (STEP) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = fmaf(p.beta, f[i], u[i]);
-    if (p.vec) {
+      for (int k = 0; k < 8; ++k) f[k] = fmaf(p.beta, f[k], u[k]);
       float4* o = reinterpret_cast<float4*>(m);
       o[0] = make_float4(f[0], f[1], f[2], f[3]);
       o[1] = make_float4(f[4], f[5], f[6], f[7]);
+    }
+  } else {
+    // all loads at once: from the part's first element where there is none, which is then left out
+    int row[4], col[4], next[4];
+    bool live[8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      live[2 * k] = of.at(i, k, &row[k], &col[k]);
+      live[2 * k + 1] = live[2 * k] && col[k] + 1 < of.col0 + of.cols;
+      if (!live[2 * k]) row[k] = of.row0, col[k] = of.col0;
+      next[k] = live[2 * k + 1] ? 1 : 0;
+    }
+    if (p.f32) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float* g = static_cast<const float*>(p.grad) + z * p.stride + row[k] * p.ldg + col[k];
+        u[2 * k] = g[0];
+        u[2 * k + 1] = g[next[k]];
+      }
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (col + i < p.cols) m[i] = f[i];
+      for (int k = 0; k < 4; ++k) {
+        const __nv_bfloat16* g =
+            static_cast<const __nv_bfloat16*>(p.grad) + z * p.stride + row[k] * p.ldg + col[k];
+        u[2 * k] = __bfloat162float(g[0]);
+        u[2 * k + 1] = __bfloat162float(g[next[k]]);
+      }
+    }
+    if (m) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float* q = p.m.at(z, row[k], col[k]);
+        f[2 * k] = q[0];
+        f[2 * k + 1] = q[next[k]];
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (!live[k]) u[k] = f[k] = 0.0f;
+    if (!m) return;
+    if (STEP) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) f[k] = fmaf(p.beta, f[k], u[k]);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float* q = p.m.at(z, row[k], col[k]);
+        if (live[2 * k]) q[0] = f[2 * k];
+        if (live[2 * k + 1]) q[1] = f[2 * k + 1];
+      }
     }
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) u[i] = p.nesterov ? fmaf(p.beta, f[i], u[i]) : f[i];
+  for (int k = 0; k < 8; ++k) u[k] = p.nesterov ? fmaf(p.beta, f[k], u[k]) : f[k];
 }
 
-// A sum of squares.  Eight of them are added in fp32, and those sums to an fp32 pair (sum and what its
-// roundings lost); where the values are so far from 1 that their squares would leave fp32's range, they
-// are brought near it by a power of two and added in 64 bits.  (All in 64 bits, of which the GPU has few
-// units, took longer than the gradients' way from HBM.)
+// A sum of squares as an fp32 pair: the sum, and what its roundings and the squares' lost, so that the
+// order of adding (which the loads' alignment decides) shows in none of its bits that count.  Where values
+// are so far from 1 that their squares would leave fp32's range, they are added in 64 bits instead.  (All in
+// 64 bits, of which the GPU has few units, took longer than the gradients' way from HBM.)
 struct MuonSquares {
   float s = 0.0f, lost = 0.0f;
   double far = 0.0;
@@ -193,18 +273,21 @@ struct MuonSquares {
     float top = 0.0f;
 #pragma unroll
     for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(u[k]));
-    const bool high = top > 0x1p40f, low = top < 0x1p-40f;
-    const float up = high ? 0x1p-90f : low ? 0x1p90f : 1.0f;
-    float q = 0.0f;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) q = fmaf(u[k] * up, u[k] * up, q);
-    if (high || low) {
-      if (top > 0.0f) far += static_cast<double>(q) * (high ? 0x1p180 : 0x1p-180);
+    if (top > 0x1p40f || top < 0x1p-40f) {
+      if (top > 0.0f) {
+#pragma unroll 1
+        for (int k = 0; k < 8; ++k) far += static_cast<double>(u[k]) * static_cast<double>(u[k]);
+      } else {
+        s += u[0] + u[1] + u[2] + u[3] + u[4] + u[5] + u[6] + u[7];  // 0, or NaN
+      }
       return;
     }
-    const float t = s + q, b = t - s;
-    lost += (s - (t - b)) + (q - b);
-    s = t;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float q = u[k] * u[k], t = s + q, b = t - s;
+      lost += ((s - (t - b)) + (q - b)) + fmaf(u[k], u[k], -q);
+      s = t;
+    }
   }
   __device__ __forceinline__ double sum() const {
     return static_cast<double>(s) + static_cast<double>(lost) + far;

@@ -216,10 +216,7 @@ struct ApplyEpi {
       if (out.vec) {
         put_chunk(g, t, col, st, buf);
       } else if (col + t.lane < g.C) {
-        const int rows = min(32, g.R - t.warp_row);
-#pragma unroll 4
-        for (int r = 0; r < rows; ++r)
-          out.put(t.t.z, t.warp_row + r, col + t.lane, buf[r * 32 + (t.lane ^ r)]);
+        out.put_column(t.t.z, t.warp_row, min(32, g.R - t.warp_row), col + t.lane, buf, t.lane);
       }
       __syncwarp();
       if (next >= 0) load(g, t, next, st);
@@ -230,17 +227,18 @@ struct ApplyEpi {
 
 // ------------------------------------------------------------------------- the first X
 // Sums of squares of a matrix, blocks x of its groups of eight columns; the momentum's step.
+template <bool VEC>
 __global__ void __launch_bounds__(256) muon_square_kernel(const MuonIn p) {
   __shared__ double red[8];
   pdl_wait();
   pdl_launch_dependents();
   const int64_t z = blockIdx.y;
-  const uint32_t per = (p.cols + 7) / 8, groups = per * static_cast<uint32_t>(p.rows);
+  const MuonGroups<VEC> of(p.rows, p.cols, 0, 0);
+  const uint32_t at = blockIdx.x * 256 + threadIdx.x, all = p.parts * 256;
   MuonSquares squares;
-  for (uint32_t i = blockIdx.x * 256 + threadIdx.x; i < groups; i += p.parts * 256) {
-    const uint32_t row = i / per;
+  for (uint32_t i = of.first(at); i < of.turns; i += of.step(all)) {
     float u[8];
-    muon_input8<true>(p, z, row, static_cast<int>(i - row * per) * 8, u);
+    muon_input8<true, VEC>(p, z, of, i, u);
     squares.add8(u);
   }
   double sum = squares.sum();
@@ -255,6 +253,7 @@ __global__ void __launch_bounds__(256) muon_square_kernel(const MuonIn p) {
 }
 
 // X = U / (|U| + eps) as hi + lo.
+template <bool VEC>
 __global__ void __launch_bounds__(256) muon_scale_kernel(const MuonIn p) {
   __shared__ float factors[2];
   pdl_wait();
@@ -270,19 +269,30 @@ __global__ void __launch_bounds__(256) muon_scale_kernel(const MuonIn p) {
   }
   __syncthreads();
   const float s1 = factors[0], s2 = factors[1];
-  const uint32_t per = (p.cols + 7) / 8, groups = per * static_cast<uint32_t>(p.rows);
-  for (uint32_t i = blockIdx.x * 256 + threadIdx.x; i < groups; i += gridDim.x * 256) {
-    const uint32_t row = i / per;
-    const int col = static_cast<int>(i - row * per) * 8;
+  const MuonGroups<VEC> of(p.rows, p.cols, 0, 0);
+  const uint32_t at = blockIdx.x * 256 + threadIdx.x, all = gridDim.x * 256;
+  for (uint32_t i = of.first(at); i < of.turns; i += of.step(all)) {
     float u[8];
-    muon_input8<false>(p, z, row, col, u);
+    muon_input8<false, VEC>(p, z, of, i, u);
     uint32_t h[4], l[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k)
       split_half2(u[2 * k] * s1 * s2, u[2 * k + 1] * s1 * s2, &h[k], &l[k]);
-    const int64_t off = z * p.xstride + static_cast<int64_t>(row) * p.ldx + col;
-    *reinterpret_cast<uint4*>(p.hi + off) = make_uint4(h[0], h[1], h[2], h[3]);
-    *reinterpret_cast<uint4*>(p.lo + off) = make_uint4(l[0], l[1], l[2], l[3]);
+    int row, col;
+    if constexpr (VEC) {
+      of.at(i, 0, &row, &col);
+      const int64_t off = z * p.xstride + row * p.ldx + col;
+      *reinterpret_cast<uint4*>(p.hi + off) = make_uint4(h[0], h[1], h[2], h[3]);
+      *reinterpret_cast<uint4*>(p.lo + off) = make_uint4(l[0], l[1], l[2], l[3]);
+      continue;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {  // (the column behind an odd row's last is padding)
+      if (!of.at(i, k, &row, &col)) continue;
+      const int64_t off = z * p.xstride + row * p.ldx + col;
+      *reinterpret_cast<uint32_t*>(p.hi + off) = h[k];
+      *reinterpret_cast<uint32_t*>(p.lo + off) = l[k];
+    }
   }
 }
 
@@ -304,7 +314,7 @@ static MuonLayout muon_layout(const lmoe_muon& p) {
   L.side = L.tall ? p.cols : p.rows;
   L.ldx = ceil_div(p.cols, 8) * 8;
   L.lda = L.ldd = ceil_div(L.side, 8) * 8;
-  const int64_t blocks = ceil_div(static_cast<int64_t>(p.rows) * ceil_div(p.cols, 8), 256);
+  const int64_t blocks = ceil_div(static_cast<int64_t>(p.rows) * ceil_div(p.cols, 8), 128);
   const int64_t most = ceil_div(MUON_BLOCKS, p.batch);
   L.parts = static_cast<int>(blocks < most ? blocks : most);
   size_t off = 0;
@@ -414,8 +424,10 @@ static int muon_run(const lmoe_muon& p, bool update, uint8_t* ws, cudaStream_t s
   if (launch_muon_small({in, out, p.batch, p.steps, p.coeffs, p.dev_flag, plans.ns}, stream, &rc))
     return rc;
   const dim3 grid(static_cast<unsigned>(L.parts), static_cast<unsigned>(p.batch));
-  if (launch_pdl(muon_square_kernel, grid, 256, 0, stream, in) != cudaSuccess ||
-      launch_pdl(muon_scale_kernel, grid, 256, 0, stream, in) != cudaSuccess)
+  auto square = in.vec ? muon_square_kernel<true> : muon_square_kernel<false>;
+  auto scale = in.vec ? muon_scale_kernel<true> : muon_scale_kernel<false>;
+  if (launch_pdl(square, grid, 256, 0, stream, in) != cudaSuccess ||
+      launch_pdl(scale, grid, 256, 0, stream, in) != cudaSuccess)
     return LMOE_ERR_CUDA;
   TileArgs g{};
   g.batch = p.batch;

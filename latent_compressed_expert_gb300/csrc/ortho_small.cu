@@ -67,7 +67,7 @@ __device__ __forceinline__ void small_put32(uint8_t* base, int row, int col,
         make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
 }
 
-template <bool TALL>
+template <bool TALL, bool VEC>
 __global__ void __launch_bounds__(SMALL_THREADS, 1)
 muon_small_kernel(const __grid_constant__ SmallArgs a) {
   extern __shared__ uint8_t smem_raw[];
@@ -135,21 +135,13 @@ muon_small_kernel(const __grid_constant__ SmallArgs a) {
   };
 
   // -------------------------------------------------------------- the first X
-  const int per = TALL ? (a.side + 7) / 8 : (mine + 7) / 8;
-  const int groups = mine > 0 ? (TALL ? mine : a.side) * per : 0;
-  auto place = [&](int i, uint32_t* r, int* c) {  // of group i, in the caller's matrix
-    const int k = i / per;
-    *r = static_cast<uint32_t>(TALL ? j0 + k : k);
-    *c = (i - k * per) * 8 + (TALL ? 0 : j0);
-  };
+  const MuonGroups<VEC> of(TALL ? mine : a.side, TALL ? a.side : mine, TALL ? j0 : 0, TALL ? 0 : j0);
+  const uint32_t first = of.first(tid), stride = of.step(SMALL_THREADS);
   MuonSquares squares;
 #pragma unroll 2
-  for (int i = tid; i < groups; i += SMALL_THREADS) {
-    uint32_t r;
-    int c;
-    place(i, &r, &c);
+  for (uint32_t i = first; i < of.turns; i += stride) {
     float u[8];
-    muon_input8<true>(a.in, z, r, c, u);
+    muon_input8<true, VEC>(a.in, z, of, i, u);
     squares.add8(u);
   }
   double sum = squares.sum();
@@ -177,27 +169,36 @@ muon_small_kernel(const __grid_constant__ SmallArgs a) {
   __syncthreads();
   const float s1 = d[0], s2 = d[1];
 #pragma unroll 2
-  for (int i = tid; i < groups; i += SMALL_THREADS) {
-    uint32_t r;
-    int c;
-    place(i, &r, &c);
+  for (uint32_t i = first; i < of.turns; i += stride) {
     float u[8];
-    muon_input8<false>(a.in, z, r, c, u);
+    muon_input8<false, VEC>(a.in, z, of, i, u);
     uint32_t h[4], l[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k)
       split_half2(u[2 * k] * s1 * s2, u[2 * k + 1] * s1 * s2, &h[k], &l[k]);
-    if constexpr (!TALL) {
-      const uint32_t at = small_at(static_cast<int>(r), c - j0);
+    int r, c;
+    if (!TALL && VEC) {
+      of.at(i, 0, &r, &c);
+      const uint32_t at = small_at(r, c - j0);
       *reinterpret_cast<uint4*>(hi + at) = make_uint4(h[0], h[1], h[2], h[3]);
       *reinterpret_cast<uint4*>(lo + at) = make_uint4(l[0], l[1], l[2], l[3]);
-    } else {
-      const int j = static_cast<int>(r) - j0;
+      continue;
+    }
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const uint32_t at = small_at(c + k, j) + (j & 7) * 2;
-        *reinterpret_cast<uint16_t*>(hi + at) = static_cast<uint16_t>(h[k / 2] >> (16 * (k & 1)));
-        *reinterpret_cast<uint16_t*>(lo + at) = static_cast<uint16_t>(l[k / 2] >> (16 * (k & 1)));
+    for (int k = 0; k < 4; ++k) {
+      if (!of.at(i, k, &r, &c)) continue;
+      if (!TALL) {  // (the column behind an odd row's last is 0)
+        const uint32_t at = small_at(r, c - j0) + ((c - j0) & 7) * 2;
+        *reinterpret_cast<uint32_t*>(hi + at) = h[k];
+        *reinterpret_cast<uint32_t*>(lo + at) = l[k];
+        continue;
+      }
+      const int j = r - j0;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {  // (row `side` of X is 0 too)
+        const uint32_t at = small_at(c + e, j) + (j & 7) * 2;
+        *reinterpret_cast<uint16_t*>(hi + at) = static_cast<uint16_t>(h[k] >> (16 * e));
+        *reinterpret_cast<uint16_t*>(lo + at) = static_cast<uint16_t>(l[k] >> (16 * e));
       }
     }
   }
@@ -366,9 +367,7 @@ muon_small_kernel(const __grid_constant__ SmallArgs a) {
           a.out.put8(z, r0 + r, c0 + c8, x, old);
         }
       } else if (c0 + lane < cols) {
-        const int n = min(32, rows - r0);
-#pragma unroll 4
-        for (int r = 0; r < n; ++r) a.out.put(z, r0 + r, c0 + lane, buf[r * 32 + (lane ^ r)]);
+        a.out.put_column(z, r0, min(32, rows - r0), c0 + lane, buf, lane);
       }
       __syncwarp();
     }
@@ -392,7 +391,7 @@ muon_small_kernel(const __grid_constant__ SmallArgs a) {
 }
 
 // How many clusters of cn CTAs can be resident at once; 0: none, or not known.
-template <bool TALL>
+template <bool TALL, bool VEC>
 static int small_active(int cn, int dev) {
   static std::atomic<int> cache[LINEAR_MAX_DEVICES][SMALL_MAX_CLUSTER + 1];
   const bool cached = dev >= 0 && dev < LINEAR_MAX_DEVICES;
@@ -400,7 +399,7 @@ static int small_active(int cn, int dev) {
     const int v = cache[dev][cn].load(std::memory_order_acquire);
     if (v != 0) return v - 1;
   }
-  auto kernel = muon_small_kernel<TALL>;
+  auto kernel = muon_small_kernel<TALL, VEC>;
   int active = 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(cn));
@@ -425,7 +424,7 @@ static int small_active(int cn, int dev) {
   return active;
 }
 
-template <bool TALL>
+template <bool TALL, bool VEC>
 static bool launch_small(const MuonSmall& s, int dev, cudaStream_t stream, int* rc) {
   SmallArgs a;
   a.in = s.in;
@@ -446,7 +445,7 @@ static bool launch_small(const MuonSmall& s, int dev, cudaStream_t stream, int* 
   for (int W = 64; W <= SMALL_MAX_W; W += 64) {
     const int cn = static_cast<int>(ceil_div(a.len, W));
     if (cn > SMALL_MAX_CLUSTER) continue;
-    const int active = small_active<TALL>(cn, dev);
+    const int active = small_active<TALL, VEC>(cn, dev);
     if (active < 1) continue;
     const double step = 1200.0 + 19.0 * W + (cn > 1 ? 2800.0 + 180.0 * cn : 0.0);
     const double ns = static_cast<double>(ceil_div(s.batch, active)) * (9000.0 + s.steps * step);
@@ -467,7 +466,7 @@ static bool launch_small(const MuonSmall& s, int dev, cudaStream_t stream, int* 
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = a.cn > 1 ? 2 : 1;
-  *rc = cudaLaunchKernelEx(&cfg, muon_small_kernel<TALL>, a) == cudaSuccess ? LMOE_OK
+  *rc = cudaLaunchKernelEx(&cfg, muon_small_kernel<TALL, VEC>, a) == cudaSuccess ? LMOE_OK
                                                                             : LMOE_ERR_CUDA;
   return true;
 }
@@ -481,7 +480,11 @@ bool launch_muon_small(const MuonSmall& s, cudaStream_t stream, int* rc) {
     *rc = LMOE_ERR_CUDA;
     return true;
   }
-  return tall ? launch_small<true>(s, dev, stream, rc) : launch_small<false>(s, dev, stream, rc);
+  if (s.in.vec)
+    return tall ? launch_small<true, true>(s, dev, stream, rc)
+                : launch_small<false, true>(s, dev, stream, rc);
+  return tall ? launch_small<true, false>(s, dev, stream, rc)
+              : launch_small<false, false>(s, dev, stream, rc);
 }
 
 }  // namespace lmoe
