@@ -147,115 +147,76 @@ struct MuonIn {
   int64_t ldx, xstride;
 };
 
-// Which eight elements of a part of a matrix (rows from row0 and columns from col0 on, `rows` by `cols`) a
-// thread takes for its i-th turn: eight columns in 16-byte loads (vec, i by thread), or four pairs of
-// columns (i by warp: four pieces of 64 columns, of one row or of several, a pair for each thread), so that
-// a warp's loads of single elements lie side by side.
-template <bool VEC>
+// A part of a matrix (rows from row0 and columns from col0 on, `rows` by `cols`), taken in groups of eight
+// columns, one thread each.
 struct MuonGroups {
   int rows, cols, row0, col0;
-  int per;          // groups, or pieces, of a row
-  uint32_t turns;
+  int per;          // groups of a row
+  uint32_t count;
   __device__ __forceinline__ MuonGroups(int rows_, int cols_, int row0_, int col0_)
-      : rows(rows_), cols(cols_), row0(row0_), col0(col0_) {
-    per = (cols + (VEC ? 7 : 63)) / (VEC ? 8 : 64);
-    turns = VEC ? static_cast<uint32_t>(rows) * per : (static_cast<uint32_t>(rows) * per + 3) / 4;
+      : rows(rows_), cols(cols_), row0(row0_), col0(col0_), per((cols_ + 7) / 8) {
+    count = static_cast<uint32_t>(rows) * per;
   }
-  // This thread's first turn, and how far apart its turns are, among `threads` threads.
-  static __device__ __forceinline__ uint32_t first(uint32_t thread) { return VEC ? thread : thread / 32; }
-  static __device__ __forceinline__ uint32_t step(uint32_t threads) { return VEC ? threads : threads / 32; }
-  // Pair k's row and first column in the matrix; false: there is none.
-  __device__ __forceinline__ bool at(uint32_t i, int k, int* row, int* col) const {
-    const uint32_t piece = VEC ? i : 4 * i + k;
-    const int r = static_cast<int>(piece / per);
-    const int c = (static_cast<int>(piece) - r * per) * (VEC ? 8 : 64) +
-                  (VEC ? 2 * k : 2 * static_cast<int>(threadIdx.x & 31));
+  // Group i's place in the matrix.
+  __device__ __forceinline__ void at(uint32_t i, int* row, int* col) const {
+    const int r = static_cast<int>(i / per);
     *row = row0 + r;
-    *col = col0 + c;
-    return r < rows && c < cols;
+    *col = col0 + (static_cast<int>(i) - r * per) * 8;
   }
 };
 
-// The matrix to be orthogonalised at the i-th turn's elements, 0 where there is none; STEP: after the
-// momentum's step.
+// The matrix to be orthogonalised at a group's columns, 0 from the part's end on; STEP: after the
+// momentum's step.  VEC: in 16-byte loads and stores; else by elements, all loads of a group at once (each
+// waited for by itself they took most of a small matrix's time), from the part's last column where there is
+// none.
 template <bool STEP, bool VEC>
-__device__ __forceinline__ void muon_input8(const MuonIn& p, int64_t z, const MuonGroups<VEC>& of,
-                                            uint32_t i, float (&u)[8]) {
+__device__ __forceinline__ void muon_input8(const MuonIn& p, int64_t z, const MuonGroups& of, int row,
+                                            int col, float (&u)[8]) {
+  const int last = of.col0 + of.cols - 1 - col;  // of the group's columns
+  const int64_t off = z * p.stride + row * p.ldg + col;
+  const float* gf = static_cast<const float*>(p.grad) + off;
+  const __nv_bfloat16* gh = static_cast<const __nv_bfloat16*>(p.grad) + off;
+  float* m = p.m.p ? p.m.at(z, row, col) : nullptr;
   float f[8];
-  float* m = p.m.p;
-  if constexpr (VEC) {
-    int row, col;
-    of.at(i, 0, &row, &col);
-    const int64_t off = z * p.stride + row * p.ldg + col;
-    if (p.f32) {
-      linear_read8(static_cast<const float*>(p.grad) + off, u);
-    } else {
-      const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.grad) + off);
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  if (VEC && p.f32) {
+    linear_read8(gf, u);
+  } else if (VEC) {
+    const uint4 v = *reinterpret_cast<const uint4*>(gh);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        u[2 * k] = __uint_as_float(w[k] << 16);
-        u[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
-      }
+    for (int k = 0; k < 4; ++k) {
+      u[2 * k] = __uint_as_float(w[k] << 16);
+      u[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
     }
-    if (!m) return;
-    m = p.m.at(z, row, col);
-    linear_read8(m, f);
-    if (STEP) {
+  } else if (p.f32) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) f[k] = fmaf(p.beta, f[k], u[k]);
+    for (int k = 0; k < 8; ++k) u[k] = gf[min(k, last)];
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) u[k] = __bfloat162float(gh[min(k, last)]);
+  }
+  if (m && VEC) linear_read8(m, f);
+  if (m && !VEC) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) f[k] = m[min(k, last)];
+  }
+  if (!VEC) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k > last) u[k] = f[k] = 0.0f;
+  }
+  if (!m) return;
+  if (STEP) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) f[k] = fmaf(p.beta, f[k], u[k]);
+    if (VEC) {
       float4* o = reinterpret_cast<float4*>(m);
       o[0] = make_float4(f[0], f[1], f[2], f[3]);
       o[1] = make_float4(f[4], f[5], f[6], f[7]);
-    }
-  } else {
-    // all loads at once: from the part's first element where there is none, which is then left out
-    int row[4], col[4], next[4];
-    bool live[8];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      live[2 * k] = of.at(i, k, &row[k], &col[k]);
-      live[2 * k + 1] = live[2 * k] && col[k] + 1 < of.col0 + of.cols;
-      if (!live[2 * k]) row[k] = of.row0, col[k] = of.col0;
-      next[k] = live[2 * k + 1] ? 1 : 0;
-    }
-    if (p.f32) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float* g = static_cast<const float*>(p.grad) + z * p.stride + row[k] * p.ldg + col[k];
-        u[2 * k] = g[0];
-        u[2 * k + 1] = g[next[k]];
-      }
     } else {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const __nv_bfloat16* g =
-            static_cast<const __nv_bfloat16*>(p.grad) + z * p.stride + row[k] * p.ldg + col[k];
-        u[2 * k] = __bfloat162float(g[0]);
-        u[2 * k + 1] = __bfloat162float(g[next[k]]);
-      }
-    }
-    if (m) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float* q = p.m.at(z, row[k], col[k]);
-        f[2 * k] = q[0];
-        f[2 * k + 1] = q[next[k]];
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (!live[k]) u[k] = f[k] = 0.0f;
-    if (!m) return;
-    if (STEP) {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) f[k] = fmaf(p.beta, f[k], u[k]);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        float* q = p.m.at(z, row[k], col[k]);
-        if (live[2 * k]) q[0] = f[2 * k];
-        if (live[2 * k + 1]) q[1] = f[2 * k + 1];
-      }
+      for (int k = 0; k < 8; ++k)
+        if (k <= last) m[k] = f[k];
     }
   }
 #pragma unroll

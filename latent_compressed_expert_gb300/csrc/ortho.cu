@@ -233,12 +233,13 @@ __global__ void __launch_bounds__(256) muon_square_kernel(const MuonIn p) {
   pdl_wait();
   pdl_launch_dependents();
   const int64_t z = blockIdx.y;
-  const MuonGroups<VEC> of(p.rows, p.cols, 0, 0);
-  const uint32_t at = blockIdx.x * 256 + threadIdx.x, all = p.parts * 256;
+  const MuonGroups of(p.rows, p.cols, 0, 0);
   MuonSquares squares;
-  for (uint32_t i = of.first(at); i < of.turns; i += of.step(all)) {
+  for (uint32_t i = blockIdx.x * 256 + threadIdx.x; i < of.count; i += p.parts * 256) {
+    int row, col;
+    of.at(i, &row, &col);
     float u[8];
-    muon_input8<true, VEC>(p, z, of, i, u);
+    muon_input8<true, VEC>(p, z, of, row, col, u);
     squares.add8(u);
   }
   double sum = squares.sum();
@@ -269,30 +270,19 @@ __global__ void __launch_bounds__(256) muon_scale_kernel(const MuonIn p) {
   }
   __syncthreads();
   const float s1 = factors[0], s2 = factors[1];
-  const MuonGroups<VEC> of(p.rows, p.cols, 0, 0);
-  const uint32_t at = blockIdx.x * 256 + threadIdx.x, all = gridDim.x * 256;
-  for (uint32_t i = of.first(at); i < of.turns; i += of.step(all)) {
+  const MuonGroups of(p.rows, p.cols, 0, 0);
+  for (uint32_t i = blockIdx.x * 256 + threadIdx.x; i < of.count; i += gridDim.x * 256) {
+    int row, col;
+    of.at(i, &row, &col);
     float u[8];
-    muon_input8<false, VEC>(p, z, of, i, u);
+    muon_input8<false, VEC>(p, z, of, row, col, u);
     uint32_t h[4], l[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k)
       split_half2(u[2 * k] * s1 * s2, u[2 * k + 1] * s1 * s2, &h[k], &l[k]);
-    int row, col;
-    if constexpr (VEC) {
-      of.at(i, 0, &row, &col);
-      const int64_t off = z * p.xstride + row * p.ldx + col;
-      *reinterpret_cast<uint4*>(p.hi + off) = make_uint4(h[0], h[1], h[2], h[3]);
-      *reinterpret_cast<uint4*>(p.lo + off) = make_uint4(l[0], l[1], l[2], l[3]);
-      continue;
-    }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {  // (the column behind an odd row's last is padding)
-      if (!of.at(i, k, &row, &col)) continue;
-      const int64_t off = z * p.xstride + row * p.ldx + col;
-      *reinterpret_cast<uint32_t*>(p.hi + off) = h[k];
-      *reinterpret_cast<uint32_t*>(p.lo + off) = l[k];
-    }
+    const int64_t off = z * p.xstride + row * p.ldx + col;
+    *reinterpret_cast<uint4*>(p.hi + off) = make_uint4(h[0], h[1], h[2], h[3]);
+    *reinterpret_cast<uint4*>(p.lo + off) = make_uint4(l[0], l[1], l[2], l[3]);
   }
 }
 

@@ -135,13 +135,14 @@ muon_small_kernel(const __grid_constant__ SmallArgs a) {
   };
 
   // -------------------------------------------------------------- the first X
-  const MuonGroups<VEC> of(TALL ? mine : a.side, TALL ? a.side : mine, TALL ? j0 : 0, TALL ? 0 : j0);
-  const uint32_t first = of.first(tid), stride = of.step(SMALL_THREADS);
+  const MuonGroups of(TALL ? mine : a.side, TALL ? a.side : mine, TALL ? j0 : 0, TALL ? 0 : j0);
   MuonSquares squares;
 #pragma unroll 2
-  for (uint32_t i = first; i < of.turns; i += stride) {
+  for (uint32_t i = tid; i < of.count; i += SMALL_THREADS) {
+    int r, c;
+    of.at(i, &r, &c);
     float u[8];
-    muon_input8<true, VEC>(a.in, z, of, i, u);
+    muon_input8<true, VEC>(a.in, z, of, r, c, u);
     squares.add8(u);
   }
   double sum = squares.sum();
@@ -169,36 +170,26 @@ muon_small_kernel(const __grid_constant__ SmallArgs a) {
   __syncthreads();
   const float s1 = d[0], s2 = d[1];
 #pragma unroll 2
-  for (uint32_t i = first; i < of.turns; i += stride) {
+  for (uint32_t i = tid; i < of.count; i += SMALL_THREADS) {
+    int r, c;
+    of.at(i, &r, &c);
     float u[8];
-    muon_input8<false, VEC>(a.in, z, of, i, u);
+    muon_input8<false, VEC>(a.in, z, of, r, c, u);
     uint32_t h[4], l[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k)
       split_half2(u[2 * k] * s1 * s2, u[2 * k + 1] * s1 * s2, &h[k], &l[k]);
-    int r, c;
-    if (!TALL && VEC) {
-      of.at(i, 0, &r, &c);
+    if constexpr (!TALL) {
       const uint32_t at = small_at(r, c - j0);
       *reinterpret_cast<uint4*>(hi + at) = make_uint4(h[0], h[1], h[2], h[3]);
       *reinterpret_cast<uint4*>(lo + at) = make_uint4(l[0], l[1], l[2], l[3]);
-      continue;
-    }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if (!of.at(i, k, &r, &c)) continue;
-      if (!TALL) {  // (the column behind an odd row's last is 0)
-        const uint32_t at = small_at(r, c - j0) + ((c - j0) & 7) * 2;
-        *reinterpret_cast<uint32_t*>(hi + at) = h[k];
-        *reinterpret_cast<uint32_t*>(lo + at) = l[k];
-        continue;
-      }
+    } else {
       const int j = r - j0;
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {  // (row `side` of X is 0 too)
-        const uint32_t at = small_at(c + e, j) + (j & 7) * 2;
-        *reinterpret_cast<uint16_t*>(hi + at) = static_cast<uint16_t>(h[k] >> (16 * e));
-        *reinterpret_cast<uint16_t*>(lo + at) = static_cast<uint16_t>(l[k] >> (16 * e));
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t at = small_at(c + k, j) + (j & 7) * 2;
+        *reinterpret_cast<uint16_t*>(hi + at) = static_cast<uint16_t>(h[k / 2] >> (16 * (k & 1)));
+        *reinterpret_cast<uint16_t*>(lo + at) = static_cast<uint16_t>(l[k / 2] >> (16 * (k & 1)));
       }
     }
   }
