@@ -9,9 +9,10 @@
 
 namespace lmoe {
 
-// Scales of the fp16 operands, powers of two: X up to 2^8 and A up to 2^6 in magnitude fit, and what
-// is 2^-15 of 1 or more keeps all its bits.
-constexpr float X_SCALE = 256.0f, A_SCALE = 1024.0f, B_SCALE = 256.0f, LO_SCALE = 2048.0f;
+// Scales of the fp16 operands, powers of two: X up to 2^4 and A and B up to 2^6 and 2^7 in magnitude fit,
+// and what is 2^-25 of 1 or more in X, 2^-24 in A, keeps all its bits.  (X's second term, down to 2^-12 of
+// the first, needs no scale of its own then.)
+constexpr float X_SCALE = 2048.0f, A_SCALE = 1024.0f, B_SCALE = 256.0f;
 constexpr int EXACT_STEPS = 2;  // the last ones, in which B's diagonal takes X itself
 
 __device__ __forceinline__ uint32_t pack_half2(float a, float b) {
@@ -21,11 +22,11 @@ __device__ __forceinline__ uint32_t pack_half2(float a, float b) {
 __device__ __forceinline__ float2 unpack_half2(uint32_t w) {
   return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
-// Two values of X in units of X_SCALE as hi + lo / LO_SCALE.
+// Two values of X in units of X_SCALE as hi + lo.
 __device__ __forceinline__ void split_scaled(float a, float b, uint32_t* hi, uint32_t* lo) {
   *hi = pack_half2(a, b);
   const float2 h = unpack_half2(*hi);
-  *lo = pack_half2((a - h.x) * LO_SCALE, (b - h.y) * LO_SCALE);
+  *lo = pack_half2(a - h.x, b - h.y);
 }
 __device__ __forceinline__ void split_half2(float a, float b, uint32_t* hi, uint32_t* lo) {
   split_scaled(a * X_SCALE, b * X_SCALE, hi, lo);

@@ -78,15 +78,17 @@ struct PolyEpi {
   int64_t ld, lda, stride;
   float b, c;
   struct State {
+    TileFetch at;
     float d, dj;  // A's diagonal at this thread's row, and at column `lane` of the chunk
     uint4 next[4];
   };
   __device__ __forceinline__ void begin(const TileArgs& g, TileCtx& c_, State& st) const {
+    st.at = tile_fetch_at(lda, c_.warp_row, g.R, c_.lane);
     st.d = c_.row < g.R ? __ldg(adiag + c_.t.z * ld + c_.row) : 0.0f;
   }
   __device__ __forceinline__ void load(const TileArgs& g, TileCtx& t, int col,
                                        State& st) const {
-    tile_fetch16(a + t.t.z * stride, lda, t.warp_row, col, g.R, g.C, t.lane, st.next);
+    tile_fetch16(a + t.t.z * stride, st.at, lda, col, g.C, st.next);
     st.dj = col + t.lane < g.C ? __ldg(adiag + t.t.z * ld + col + t.lane) : 0.0f;
   }
   __device__ __forceinline__ void chunk(const TileArgs& g, TileCtx& t, int col, State& st,
@@ -131,20 +133,22 @@ struct ApplyEpi {
   int keep_lo;            // the next step is not the last
   MuonOut out;
   struct State {
+    TileFetch at;
     float d;  // B's diagonal at this thread's row, or (TALL) at column `lane` of the chunk
     uint4 h[4], l[LAST ? 1 : 4];
     MuonOut::Old old[LAST ? 4 : 1];
   };
   __device__ __forceinline__ void begin(const TileArgs& g, TileCtx& t, State& st) const {
+    st.at = tile_fetch_at(ldx, t.warp_row, g.R, t.lane);
     st.d = !TALL && t.row < g.R ? __ldg(bdiag + t.t.z * ld + t.row) : 0.0f;
   }
   __device__ __forceinline__ void load(const TileArgs& g, TileCtx& t, int col,
                                        State& st) const {
-    tile_fetch16(hi + t.t.z * stride, ldx, t.warp_row, col, g.R, g.C, t.lane, st.h);
+    tile_fetch16(hi + t.t.z * stride, st.at, ldx, col, g.C, st.h);
     if constexpr (TALL)
       st.d = col + t.lane < g.C ? __ldg(bdiag + t.t.z * ld + col + t.lane) : 0.0f;
     if constexpr (!LAST) {
-      tile_fetch16(lo + t.t.z * stride, ldx, t.warp_row, col, g.R, g.C, t.lane, st.l);
+      tile_fetch16(lo + t.t.z * stride, st.at, ldx, col, g.C, st.l);
     } else if (out.vec) {
       const int c8 = col + t.lane % 4 * 8;
 #pragma unroll
@@ -170,14 +174,14 @@ struct ApplyEpi {
   }
   __device__ __forceinline__ void chunk(const TileArgs& g, TileCtx& t, int col, State& st,
                                         float (&v)[32], int next) const {
-    // In units of X_SCALE, with d of B's diagonal and X = hi + lo / LO_SCALE:
-    //   a X + d (X or hi) = (a + d) hi + (a + (d or 0)) / LO_SCALE lo
+    // In units of X_SCALE, with d of B's diagonal and X = hi + lo:
+    //   a X + d (X or hi) = (a + d) hi + (a + (d or 0)) lo
     constexpr float TO_BX = LAST ? 1.0f / (B_SCALE * X_SCALE) : 1.0f / B_SCALE;
     uint32_t h[16], l[16];
     tile_next_buf(t);
     tile_spread16(t.buf, t.lane, st.h);
     if constexpr (!LAST) tile_spread16(t.buf + 2048, t.lane, st.l);
-    float ph = a + st.d, pl = (exact ? ph : a) * (1.0f / LO_SCALE);
+    float ph = a + st.d, pl = exact ? ph : a;
     if (LAST) ph *= 1.0f / X_SCALE;
     __syncwarp();
     tile_row16(t.buf, t.lane, h);

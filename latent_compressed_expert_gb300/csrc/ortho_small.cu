@@ -309,8 +309,8 @@ muon_small_kernel(const __grid_constant__ SmallArgs a) {
       ptx::umma_commit(bar);
     }
     done();
-    // as in ortho.cu: in units of X_SCALE, (a + d) hi + (a + (d or 0)) / LO_SCALE lo
-    const float ph = ca + be[row], pl = (exact ? ph : ca) * (1.0f / LO_SCALE);
+    // as in ortho.cu: in units of X_SCALE, (a + d) hi + (a + (d or 0)) lo
+    const float ph = ca + be[row], pl = exact ? ph : ca;
     float* buf = reinterpret_cast<float*>(ex + warp * 4096);
 #pragma unroll 1
     for (int ch = part; ch < W / 32; ch += 4) {

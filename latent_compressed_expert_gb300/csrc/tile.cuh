@@ -169,16 +169,23 @@ __device__ __forceinline__ void tile_next_buf(TileCtx& c) {
 // A warp's 32 rows of 32 16-bit values from memory: four threads take 16 bytes each of a row, so that a
 // load touches eight lines (a row for each thread touches 32 in each of four loads, which the L1's tags
 // take a cycle each for: 4 us of a 256 x 256 tile's epilogue).  Rows from R and columns from C on (C
-// rounded up to 8) are left alone.
-__device__ __forceinline__ void tile_fetch16(const void* base, int64_t ld, int row, int col, int R,
-                                             int C, int lane, uint4 (&v)[4]) {
-  const int c = col + lane % 4 * 8;
+// rounded up to 8) are left alone.  TileFetch: a thread's place, the same for all of a tile's chunks.
+struct TileFetch {
+  int64_t off;  // of its first row, and its columns of a chunk
+  int rows;     // of the output from there on
+  int col;
+};
+__device__ __forceinline__ TileFetch tile_fetch_at(int64_t ld, int row, int R, int lane) {
+  const int r = row + lane / 4, c = lane % 4 * 8;
+  return {r * ld + c, R - r, c};
+}
+__device__ __forceinline__ void tile_fetch16(const void* base, const TileFetch& at, int64_t ld, int col,
+                                             int C, uint4 (&v)[4]) {
+  if (col + at.col >= C) return;
+  const uint16_t* p = static_cast<const uint16_t*>(base) + at.off + col;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = row + 8 * i + lane / 4;
-    if (r < R && c < C)
-      v[i] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + r * ld + c);
-  }
+  for (int i = 0; i < 4; ++i)
+    if (8 * i < at.rows) v[i] = *reinterpret_cast<const uint4*>(p + 8 * i * ld);
 }
 // Through 2 KB of shared memory to a row for each thread, where tile_put16 puts its own.
 __device__ __forceinline__ void tile_spread16(uint8_t* buf, int lane, const uint4 (&v)[4]) {

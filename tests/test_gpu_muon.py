@@ -60,8 +60,8 @@ def _rounded(u, coeffs=MUON, steps=5, eps=1e-7):
     tall = x.shape[-2] > x.shape[-1]
     x = x.mT if tall else x
     for k, (a, b, c) in enumerate(_steps(coeffs, steps)):
-        hi = half(x, 256.0)
-        x = hi + half(x - hi, 256.0 * 2048.0) if k + 1 < steps else hi
+        hi = half(x, 2048.0)
+        x = hi + half(x - hi, 2048.0) if k + 1 < steps else hi
         p = hi @ hi.mT
         d = torch.diag_embed(p.diagonal(dim1=-2, dim2=-1))
         o = half(p - d, 1024.0)
