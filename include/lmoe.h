@@ -672,9 +672,10 @@ typedef struct lmoe_muon {
  * batch and 4 for each of its matrices' smaller side squared).  Any rows and cols and any alignment to
  * the element size; multiples of 8 columns in whole 16 bytes are read faster.  A size of 0 is a no-op.
  * Arithmetic: products of fp16 operands with fp32 sums, X as two fp16 terms and the diagonals of A and
- * of b A + c A^2 in fp32 beside them, the norm in 64 bits; X comes out within 1e-3 of itself or so (in
- * the norm, against the formulas in 64 bits; up to 1.3e-2 where the roundings of a few elements, or of
- * equal ones, do not average out), before its rounding to bf16.  The iterates must keep to fp16's
+ * of b A + c A^2 in fp32 beside them, the norm's sum of squares with the roundings' rests beside it; X
+ * comes out within 1e-3 of itself or so (in the norm, against the formulas in 64 bits; up to 1.3e-2
+ * where the roundings of a few elements, or of equal ones, do not average out), before its rounding to
+ * bf16.  The iterates must keep to fp16's
  * range: singular values of X up to 8 (from 1 at the start) and entries of b A + c A^2 up to
  * 255 are safe.  A matrix that is not finite gives NaN, in its own place in the batch only.
  * Outputs overlap no input, nor each other (out may be grad).
