@@ -124,12 +124,37 @@ lse_join_kernel(const float2* __restrict__ part, int parts, int M, XentTarget ta
 }
 
 // ------------------------------------------------------------------------- backward
+// The unit of d: the mantissa (1 to 2, so that it takes nothing from the range) of the first weight that is
+// a normal number, of 256 rows from all over the batch; 1 where there is none.  Called by whole warps.
+__device__ __forceinline__ float xent_unit(const float* dloss, int M, int lane) {
+  uint32_t bits[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int i = 32 * k + lane;
+    const int row = M <= 256 ? i : static_cast<int>(static_cast<int64_t>(i) * M >> 8);
+    bits[k] = row < M ? __float_as_uint(__ldg(dloss + row)) : 0u;
+  }
+  uint32_t unit = 0;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const uint32_t e = bits[k] >> 23 & 255u;
+    const uint32_t some = __ballot_sync(0xffffffffu, e != 0 && e != 255);
+    const uint32_t b = __shfl_sync(0xffffffffu, bits[k], some ? __ffs(some) - 1 : 0);
+    if (unit == 0 && some) unit = (b & 0x7FFFFFu) | 0x3F800000u;
+  }
+  return unit ? __uint_as_float(unit) : 1.0f;
+}
+
 // d of a piece of the vocabulary, from column `col0` on, as bf16.
 // Of a row's d the target's element is by far the largest, and its rounding, up to 2^-8 of it, goes
 // into all of that row's dx and of the target's row of dw.  Over many rows such errors are as large as
 // the results' own rounding in the norm, over few rows up to twice that.  So up to XENT_TWO_TERMS rows,
 // where the head's way from HBM is the time in any case, d is two terms (2^-17); beyond, `rest` keeps
-// what the target's element lost, and dx gets that times the target's weights.
+// what the target's element lost, and dx gets that times the target's weights.  (Two terms for 300 rows:
+// 116 -> 160 us, dw 2.4e-3 -> 1.7e-3 off in the norm, the part of its own rounding.)
+// A mean's rows all have one weight, and with it would all be off by the same part, in one direction.
+// So d is kept in units of the weights' mantissa (xent_unit), which the results are multiplied by: the
+// targets' elements, -1 for the most part, are then exact.
 template <bool TWO>
 struct XentGradEpi {
   static constexpr int PART = 0, PART_ONE = 0, SHORT = 8;
@@ -137,17 +162,21 @@ struct XentGradEpi {
   const float* lse;
   const float* dloss;
   float* rest;     // [M] (one term)
+  float* unit;     // out, for the kernels behind this one
   int col0;
   struct State {
+    float unit = 0.0f;
     float lse, g;
     int target;
   };
   __device__ __forceinline__ void begin(const TileArgs& g, TileCtx& c, State& st) const {
+    if (st.unit == 0.0f) st.unit = xent_unit(dloss, g.R, c.lane);  // once
+    if (c.row == 0 && c.t.col0 == 0 && c.half == 0) *unit = st.unit;
     st.target = c.row < g.R ? target.of(c.row) : -1;
     st.lse = st.g = 0.0f;
     if (st.target >= 0) {
       st.lse = __ldg(lse + c.row);
-      st.g = __ldg(dloss + c.row);
+      st.g = __fdiv_rn(__ldg(dloss + c.row), st.unit);
       st.target -= col0;
     } else {
       st.target = INT32_MIN;
@@ -234,15 +263,22 @@ struct XentDxEpi {
   __device__ __forceinline__ void end(const TileArgs&, TileCtx&, State&) const {}
 };
 
-// A plain output, bf16 or fp32.
+// An output times d's unit, bf16 or fp32.
 struct StoreEpi {
   static constexpr int PART = 0, PART_ONE = 0, SHORT = 16;
   int f32;
-  struct State {};
-  __device__ __forceinline__ void begin(const TileArgs&, TileCtx&, State&) const {}
+  const float* unit;
+  struct State {
+    float unit;
+  };
+  __device__ __forceinline__ void begin(const TileArgs&, TileCtx&, State& st) const {
+    st.unit = __ldg(unit);
+  }
   __device__ __forceinline__ void load(const TileArgs&, TileCtx&, int, State&) const {}
-  __device__ __forceinline__ void chunk(const TileArgs&, TileCtx& c, int col, State&,
+  __device__ __forceinline__ void chunk(const TileArgs&, TileCtx& c, int col, State& st,
                                         float (&v)[32], int) const {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] *= st.unit;
     tile_next_buf(c);
     if (f32) {
       tile_put32(c.buf, c.lane, v);
@@ -261,11 +297,11 @@ struct StoreEpi {
 };
 
 // dx = the slices' sums added in order, and what the target's element of d lost times the target's
-// weights, rounded to bf16; a thread takes eight columns.
+// weights, times d's unit and rounded to bf16; a thread takes eight columns.
 __global__ void __launch_bounds__(256)
 xent_dx_kernel(const float* __restrict__ sum, int ks, int64_t M, int K, XentTarget target,
-               const float* __restrict__ rest, const __nv_bfloat16* __restrict__ w, int64_t ldw,
-               __nv_bfloat16* dx, int64_t lddx) {
+               const float* __restrict__ rest, const float* __restrict__ unit,
+               const __nv_bfloat16* __restrict__ w, int64_t ldw, __nv_bfloat16* dx, int64_t lddx) {
   pdl_wait();
   pdl_launch_dependents();
   const int per = K / 8;
@@ -293,6 +329,9 @@ xent_dx_kernel(const float* __restrict__ sum, int ks, int64_t M, int K, XentTarg
 #pragma unroll
     for (int j = 0; j < 8; ++j) a[j] += f[j];
   }
+  const float u = __ldg(unit);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) a[j] *= u;
   *reinterpret_cast<uint4*>(dx + row * lddx + col) = linear_pack8(a);
 }
 
@@ -337,7 +376,7 @@ struct XentBwdLayout {
   int64_t piece, ldd;  // columns of a piece; distance between rows of d
   int slices;          // at most
   int terms;           // of d
-  size_t d, sum, rest, total;
+  size_t d, sum, rest, unit, total;
 };
 static XentBwdLayout xent_bwd_layout(const lmoe_linear_xent& p) {
   XentBwdLayout L{};
@@ -355,7 +394,8 @@ static XentBwdLayout xent_bwd_layout(const lmoe_linear_xent& p) {
   L.d = 0;
   L.sum = (static_cast<size_t>(p.M) * L.ldd * 2 * L.terms + 255) / 256 * 256;
   L.rest = L.sum + static_cast<size_t>(L.slices) * p.M * p.K * sizeof(float);
-  L.total = L.rest + static_cast<size_t>(p.M) * sizeof(float);
+  L.unit = L.rest + static_cast<size_t>(p.M) * sizeof(float);
+  L.total = L.unit + sizeof(float);
   return L;
 }
 
@@ -425,6 +465,7 @@ static int xent_backward(const lmoe_linear_xent& p, const float* dloss, __nv_bfl
   const XentBwdLayout L = xent_bwd_layout(p);
   float* sum = reinterpret_cast<float*>(ws + L.sum);
   float* rest = L.terms > 1 ? nullptr : reinterpret_cast<float*>(ws + L.rest);
+  float* unit = reinterpret_cast<float*>(ws + L.unit);
   const XentTarget target{p.target, p.target_type == LMOE_I64, p.V};
   const TileOperand X{p.x, p.M, p.K, p.ldx, 0};
   bool stall = inject_stall();
@@ -445,10 +486,10 @@ static int xent_backward(const lmoe_linear_xent& p, const float* dloss, __nv_bfl
       const int at = static_cast<int>(c0);
       rc = L.terms > 1
                ? launch_tile<false, false, false>(
-                     X, W, maps, g, XentGradEpi<true>{target, p.lse, dloss, nullptr, at}, plan, dev,
+                     X, W, maps, g, XentGradEpi<true>{target, p.lse, dloss, nullptr, unit, at}, plan, dev,
                      sms, stream)
                : launch_tile<false, false, false>(
-                     X, W, maps, g, XentGradEpi<false>{target, p.lse, dloss, rest, at}, plan, dev,
+                     X, W, maps, g, XentGradEpi<false>{target, p.lse, dloss, rest, unit, at}, plan, dev,
                      sms, stream);
       if (rc != LMOE_OK) return rc;
     }
@@ -477,7 +518,7 @@ static int xent_backward(const lmoe_linear_xent& p, const float* dloss, __nv_bfl
         return LMOE_ERR_CUDA;
       TileArgs g = xent_args(p, cols, p.K, p.M);
       g.two = L.terms > 1;
-      rc = launch_tile<true, true, false>(Dl, X, maps, g, StoreEpi{dw_f32},
+      rc = launch_tile<true, true, false>(Dl, X, maps, g, StoreEpi{dw_f32, unit},
                                           tile_plan(cols, p.K, p.M * L.terms, 1, false, sms,
                                                     STORE_EPILOGUE),
                                           dev, sms, stream);
@@ -487,7 +528,7 @@ static int xent_backward(const lmoe_linear_xent& p, const float* dloss, __nv_bfl
   if (!dx) return LMOE_OK;
   const int64_t threads = static_cast<int64_t>(p.M) * (p.K / 8);
   return launch_pdl(xent_dx_kernel, static_cast<unsigned>(ceil_div(threads, 256)), 256, 0, stream,
-                    sum, slices, p.M, p.K, target, rest,
+                    sum, slices, p.M, p.K, target, rest, unit,
                     static_cast<const __nv_bfloat16*>(p.w), p.ldw, dx, lddx) == cudaSuccess
              ? LMOE_OK
              : LMOE_ERR_CUDA;

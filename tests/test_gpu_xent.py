@@ -375,3 +375,33 @@ def test_stalled_wait_is_reported(dev, monkeypatch, M):
     torch.cuda.synchronize()
     assert head.device_error() == lmoe.LMOE_OK
     assert torch.equal(again[0], want[0]) and torch.equal(again[1], want[1])
+
+
+@pytest.mark.parametrize("M", [129, 300, 1000])
+@pytest.mark.parametrize("weight", [1 + 2.0 ** -8, 1 / 300, -3e-30])
+def test_one_weight_for_all_rows(dev, M, weight):
+    """A mean's 1 / rows, and rows without weight before them: what rounding the weight to bf16 would take
+    from every target's element (half a step, 2^-8 of it, for the first weight) is not lost.  In units of
+    the weight the target's element is p - 1, which for p < 2^-9 rounds to -1: off by p; the others, p,
+    by 2^-8 of p.  So both gradients are off by at most weight p |x| or |w| a row, the logits' errors, and
+    the products' sums (and the weight's unit taken out and put back, two roundings)."""
+    V, K = 20000, 64
+    head = lmoe.LinearCrossEntropy(_draw(dev, V, K, 1, 0.05))
+    x, t = _draw(dev, M, K, 2), _targets(dev, M, V, 3)
+    g = torch.full((M,), weight, device=dev)
+    g[: M // 2] = 0.0
+    _, lse = head.forward(x, t)
+    out = head.backward(x, t, lse, g, dw_dtype=torch.float32)
+    l, e = _logits(x, head.w)
+    on = ((t >= 0) & (t < V)).unsqueeze(1)
+    p = (l - lse.double().unsqueeze(1)).exp()
+    assert float(p.max()) < 2.0 ** -9
+    gd = torch.where(on, g.double().unsqueeze(1), 0.0)
+    d = gd * (p - (torch.arange(V, device=dev) == t.unsqueeze(1)).double())
+    ed = gd.abs() * p * (1 + 1.01 * e + EXP) + 4 * ULP * d.abs()
+    x64, w64 = x.double(), head.w.double()
+    ew = ed.T @ x64.abs() + 1.01 * (M + 1) * ULP * (d.abs().T @ x64.abs())
+    _within(out["dw"], d.T @ x64, 1.01 * ew, "dw")
+    ex = ed @ w64.abs() + 1.01 * (V + 1) * ULP * (d.abs() @ w64.abs())
+    want = d @ w64
+    _within(out["dx"], want, 1.01 * (ex + HALF * want.abs()), "dx")
