@@ -7,11 +7,12 @@
 // Backward: for one piece of the vocabulary after the other the logits are computed again, d goes
 // to scratch as bf16, and both products read it there.
 // What bounds them (times with inputs past L2; HBM and tensor rates of measured peaks):
-//   up to 128 rows the head's way from HBM: 1 row x 131072 tokens x 7168 279 us (6.73 TB/s, 0.99), 77
-//   x 32003 x 3584 43 us (0.78: 143 tiles for 152 SMs, and 8 us of launch, first load and join);
-//   from some hundred rows on the tensor cores: 4096 x 65536 x 7168 forward 2.27-2.34 ms (0.84-0.87 of
-//   the burst rate, 0.96-0.99 of the sustained one), backward 6.78-6.88 ms (0.86-0.87);
-//   between, rows that fill part of a tile: 300 x 50257 x 1024 backward 117 us, of which the products
+//   up to 128 rows the head's way from HBM: 1 row x 131072 tokens x 7168 279-288 us (6.5-6.7 TB/s,
+//   0.96-0.99), 77 x 32003 x 3584 43 us (0.78: 143 tiles for 152 SMs, and 8 us of launch, first load
+//   and join);
+//   from some hundred rows on the tensor cores: 4096 x 65536 x 7168 forward 2.27-2.39 ms (0.83-0.87 of
+//   the burst rate, 0.94-0.99 of the sustained one), backward 6.79-7.12 ms (0.83-0.87);
+//   between, rows that fill part of a tile: 300 x 50257 x 1024 backward 117-121 us, of which the products
 //   on whole tiles of 384 and 512 rows are 36 + 35 + 41 (profiled one by one).
 #include "tile.cuh"
 
