@@ -126,24 +126,32 @@ lse_join_kernel(const float2* __restrict__ part, int parts, int M, XentTarget ta
 
 // ------------------------------------------------------------------------- backward
 // The unit of d: the mantissa (1 to 2, so that it takes nothing from the range) of the first weight that is
-// a normal number, of 256 rows from all over the batch; 1 where there is none.  Called by whole warps.
-__device__ __forceinline__ float xent_unit(const float* dloss, int M, int lane) {
-  uint32_t bits[8];
-#pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const int i = 32 * k + lane;
-    const int row = M <= 256 ? i : static_cast<int>(static_cast<int64_t>(i) * M >> 8);
-    bits[k] = row < M ? __float_as_uint(__ldg(dloss + row)) : 0u;
+// a normal number of a row that has a target; 1 where there is none.  One block goes through the rows until
+// it finds it, 1024 at a time.  (Chosen from 256 rows' weights, targets or not, by each warp for itself it
+// was another one where a padded row's weight was read, or none of the few rows that have a weight.)
+constexpr int XENT_UNIT_THREADS = 1024;
+__global__ void __launch_bounds__(XENT_UNIT_THREADS)
+xent_unit_kernel(XentTarget target, const float* dloss, int M, float* unit) {
+  __shared__ int first;
+  if (threadIdx.x == 0) first = INT32_MAX;
+  pdl_wait();
+  pdl_launch_dependents();
+  for (int64_t row0 = 0; row0 < M; row0 += XENT_UNIT_THREADS) {
+    const int64_t row = row0 + threadIdx.x;
+    uint32_t bits = 0;
+    bool some = false;
+    if (row < M) {
+      bits = __float_as_uint(dloss[row]);
+      const uint32_t e = bits >> 23 & 255u;
+      some = target.of(static_cast<int>(row)) >= 0 && e != 0 && e != 255;
+    }
+    if (!__syncthreads_or(some)) continue;
+    if (some) atomicMin(&first, static_cast<int>(row));
+    __syncthreads();
+    if (row == first) *unit = __uint_as_float((bits & 0x7FFFFFu) | 0x3F800000u);
+    return;
   }
-  uint32_t unit = 0;
-#pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const uint32_t e = bits[k] >> 23 & 255u;
-    const uint32_t some = __ballot_sync(0xffffffffu, e != 0 && e != 255);
-    const uint32_t b = __shfl_sync(0xffffffffu, bits[k], some ? __ffs(some) - 1 : 0);
-    if (unit == 0 && some) unit = (b & 0x7FFFFFu) | 0x3F800000u;
-  }
-  return unit ? __uint_as_float(unit) : 1.0f;
+  if (threadIdx.x == 0) *unit = 1.0f;
 }
 
 // d of a piece of the vocabulary, from column `col0` on, as bf16.
@@ -154,7 +162,7 @@ __device__ __forceinline__ float xent_unit(const float* dloss, int M, int lane) 
 // what the target's element lost, and dx gets that times the target's weights.  (Two terms for 300 rows:
 // 116 -> 160 us, dw 2.4e-3 -> 1.7e-3 off in the norm, the part of its own rounding.)
 // A mean's rows all have one weight, and with it would all be off by the same part, in one direction.
-// So d is kept in units of the weights' mantissa (xent_unit), which the results are multiplied by: the
+// So d is kept in units of the weights' mantissa (xent_unit_kernel), which the results are multiplied by: the
 // targets' elements, -1 for the most part, are then exact.
 template <bool TWO>
 struct XentGradEpi {
@@ -163,21 +171,18 @@ struct XentGradEpi {
   const float* lse;
   const float* dloss;
   float* rest;     // [M] (one term)
-  float* unit;     // out, for the kernels behind this one
+  const float* unit;
   int col0;
   struct State {
-    float unit = 0.0f;
     float lse, g;
     int target;
   };
   __device__ __forceinline__ void begin(const TileArgs& g, TileCtx& c, State& st) const {
-    if (st.unit == 0.0f) st.unit = xent_unit(dloss, g.R, c.lane);  // once
-    if (c.row == 0 && c.t.col0 == 0 && c.half == 0) *unit = st.unit;
     st.target = c.row < g.R ? target.of(c.row) : -1;
     st.lse = st.g = 0.0f;
     if (st.target >= 0) {
       st.lse = __ldg(lse + c.row);
-      st.g = __fdiv_rn(__ldg(dloss + c.row), st.unit);
+      st.g = __fdiv_rn(__ldg(dloss + c.row), *unit);
       st.target -= col0;
     } else {
       st.target = INT32_MIN;
@@ -469,6 +474,9 @@ static int xent_backward(const lmoe_linear_xent& p, const float* dloss, __nv_bfl
   float* unit = reinterpret_cast<float*>(ws + L.unit);
   const XentTarget target{p.target, p.target_type == LMOE_I64, p.V};
   const TileOperand X{p.x, p.M, p.K, p.ldx, 0};
+  if (launch_pdl(xent_unit_kernel, 1u, XENT_UNIT_THREADS, 0, stream, target, dloss, p.M, unit) !=
+      cudaSuccess)
+    return LMOE_ERR_CUDA;
   bool stall = inject_stall();
   int slices = 1;
   for (int64_t c0 = 0; c0 < p.V; c0 += L.piece) {

@@ -405,3 +405,53 @@ def test_one_weight_for_all_rows(dev, M, weight):
     ex = ed @ w64.abs() + 1.01 * (V + 1) * ULP * (d.abs() @ w64.abs())
     want = d @ w64
     _within(out["dx"], want, 1.01 * (ex + HALF * want.abs()), "dx")
+
+
+def _check_one_weight(head, x, t, g):
+    """Rows of one weight, or none: the bounds derived at test_one_weight_for_all_rows."""
+    M, V = x.shape[0], head.V
+    _, lse = head.forward(x, t)
+    out = head.backward(x, t, lse, g, dw_dtype=torch.float32)
+    l, e = _logits(x, head.w)
+    on = ((t >= 0) & (t < V)).unsqueeze(1)
+    p = (l - lse.double().unsqueeze(1)).exp()
+    assert float(p.max()) < 2.0 ** -9
+    gd = torch.where(on, g.double().unsqueeze(1), 0.0)
+    d = gd * (p - (torch.arange(V, device=x.device) == t.unsqueeze(1)).double())
+    ed = gd.abs() * p * (1 + 1.01 * e + EXP) + 4 * ULP * d.abs()
+    x64, w64 = x.double(), head.w.double()
+    live = int((gd != 0).sum())  # the others add zeros
+    ew = ed.T @ x64.abs() + 1.01 * (live + 1) * ULP * (d.abs().T @ x64.abs())
+    _within(out["dw"], d.T @ x64, 1.01 * ew, "dw")
+    ex = ed @ w64.abs() + 1.01 * (V + 1) * ULP * (d.abs() @ w64.abs())
+    want = d @ w64
+    _within(out["dx"], want, 1.01 * (ex + HALF * want.abs()), "dx")
+
+
+@pytest.mark.parametrize("other", [1.0, float("nan"), float("inf"), 0.0])
+@pytest.mark.parametrize("M", [129, 300, 3000])
+def test_weights_of_rows_without_a_target_do_not_count(dev, M, other):
+    """The one weight of the rows that have a target is not rounded, whatever the others' is."""
+    head = lmoe.LinearCrossEntropy(_draw(dev, 8000, 64, 1, 0.05))
+    x, t = _draw(dev, M, 64, 2), _targets(dev, M, 8000, 3, ignored=0.5)
+    t[0] = -100
+    weight = torch.full((M,), 1 / 300, device=dev)
+    weight[t < 0] = other
+    got = head.forward(x, t)
+    clean = head.backward(x, t, got[1], torch.full((M,), 1 / 300, device=dev))
+    out = head.backward(x, t, got[1], weight)
+    assert torch.equal(out["dx"], clean["dx"]) and torch.equal(out["dw"], clean["dw"])
+    if other == 1.0:
+        _check_one_weight(head, x, t, weight)
+
+
+@pytest.mark.parametrize("M,rows", [(4096, range(5, 4096, 200)), (4096, [4095]), (1000, [999]),
+                                    (70000, [3, 69999])])
+def test_few_rows_of_one_weight_among_many_without(dev, M, rows):
+    """Wherever they lie."""
+    V = 8000 if M < 10000 else 3000
+    head = lmoe.LinearCrossEntropy(_draw(dev, V, 64, 1, 0.02))
+    x, t = _draw(dev, M, 64, 2), _targets(dev, M, V, 3, ignored=0.0)
+    g = torch.zeros(M, device=dev)
+    g[list(rows)] = 1 / 300
+    _check_one_weight(head, x, t, g)
