@@ -590,8 +590,8 @@ int lmoe_linear_backward(const lmoe_linear *p, const void *dy, long long lddy, v
  * Per row of x, with the V logits l = x . w^T in fp32:
  *   lse = log sum exp l;   loss = lse - l[target]
  * The logits are not kept: no buffer of M x V elements is written or needed.  A row whose target is
- * outside 0 .. V - 1 (an ignored token) has loss 0 and takes no part in the gradients; its lse is
- * computed all the same.  The loss is the target's negative log-probability: with one row the call
+ * outside 0 .. V - 1 (an ignored token) has loss 0 and takes no part in the gradients, whatever its
+ * x, lse and dloss hold (NaN, infinities); its lse is computed all the same.  The loss is the target's negative log-probability: with one row the call
  * scores a sampled token. */
 typedef struct lmoe_linear_xent {
   int M, V, K;            /* rows of x, tokens of the vocabulary, features */

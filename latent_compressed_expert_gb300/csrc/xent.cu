@@ -125,33 +125,61 @@ lse_join_kernel(const float2* __restrict__ part, int parts, int M, XentTarget ta
 }
 
 // ------------------------------------------------------------------------- backward
-// The unit of d: the mantissa (1 to 2, so that it takes nothing from the range) of the first weight that is
-// a normal number of a row that has a target; 1 where there is none.  One block goes through the rows until
-// it finds it, 1024 at a time.  (Chosen from 256 rows' weights, targets or not, by each warp for itself it
-// was another one where a padded row's weight was read, or none of the few rows that have a weight.)
-constexpr int XENT_UNIT_THREADS = 1024;
-__global__ void __launch_bounds__(XENT_UNIT_THREADS)
-xent_unit_kernel(XentTarget target, const float* dloss, int M, float* unit) {
+// What the products need of all rows beforehand, in one launch.
+// Block 0: the unit of d, the mantissa (1 to 2, so that it takes nothing from the range) of the first weight
+// that is a normal number of a row that has a target; 1 where there is none.  It goes through the rows until
+// it finds it.  (Chosen from 256 rows' weights, targets or not, by each warp for itself it was another one
+// where a padded row's weight was read, or none of the few rows that have a weight.)
+// All blocks (`rows` not null): x with zeros in the rows without a target, which dw = d^T x reads: d is 0
+// there, but a padded row may hold anything, and 0 times NaN is not 0.  A warp takes 1024 columns of a row
+// at a time.  (4096 x 7168, 118 MB there and back: 20 us of 7 ms.)
+constexpr int XENT_PREPARE_THREADS = 256;
+__global__ void __launch_bounds__(XENT_PREPARE_THREADS)
+xent_prepare_kernel(XentTarget target, const float* dloss, int M, float* unit, const __nv_bfloat16* x,
+                    int64_t ldx, int K, __nv_bfloat16* rows, int64_t ldrows) {
   __shared__ int first;
   if (threadIdx.x == 0) first = INT32_MAX;
   pdl_wait();
   pdl_launch_dependents();
-  for (int64_t row0 = 0; row0 < M; row0 += XENT_UNIT_THREADS) {
-    const int64_t row = row0 + threadIdx.x;
-    uint32_t bits = 0;
-    bool some = false;
-    if (row < M) {
-      bits = __float_as_uint(dloss[row]);
-      const uint32_t e = bits >> 23 & 255u;
-      some = target.of(static_cast<int>(row)) >= 0 && e != 0 && e != 255;
+  if (blockIdx.x == 0) {
+    int64_t row0 = 0;
+    for (; row0 < M; row0 += XENT_PREPARE_THREADS) {
+      const int64_t row = row0 + threadIdx.x;
+      uint32_t bits = 0;
+      bool some = false;
+      if (row < M) {
+        bits = __float_as_uint(dloss[row]);
+        const uint32_t e = bits >> 23 & 255u;
+        some = target.of(static_cast<int>(row)) >= 0 && e != 0 && e != 255;
+      }
+      if (!__syncthreads_or(some)) continue;
+      if (some) atomicMin(&first, static_cast<int>(row));
+      __syncthreads();
+      if (row == first) *unit = __uint_as_float((bits & 0x7FFFFFu) | 0x3F800000u);
+      break;
     }
-    if (!__syncthreads_or(some)) continue;
-    if (some) atomicMin(&first, static_cast<int>(row));
-    __syncthreads();
-    if (row == first) *unit = __uint_as_float((bits & 0x7FFFFFu) | 0x3F800000u);
-    return;
+    if (row0 >= M && threadIdx.x == 0) *unit = 1.0f;
   }
-  if (threadIdx.x == 0) *unit = 1.0f;
+  if (!rows) return;
+  const int lane = threadIdx.x & 31, per = K / 8, parts = (per + 127) / 128;
+  const int64_t items = static_cast<int64_t>(M) * parts;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * (XENT_PREPARE_THREADS / 32);
+  for (int64_t i = blockIdx.x * (XENT_PREPARE_THREADS / 32) + (threadIdx.x >> 5); i < items; i += step) {
+    const int64_t row = i / parts;
+    const int c = static_cast<int>(i - row * parts) * 128 + lane;
+    const bool on = target.of(static_cast<int>(row)) >= 0;
+    const uint4* from = reinterpret_cast<const uint4*>(x + row * ldx);
+    uint4* to = reinterpret_cast<uint4*>(rows + row * ldrows);
+    uint4 v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      v[k] = make_uint4(0u, 0u, 0u, 0u);
+      if (on && c + 32 * k < per) v[k] = from[c + 32 * k];
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (c + 32 * k < per) to[c + 32 * k] = v[k];
+  }
 }
 
 // d of a piece of the vocabulary, from column `col0` on, as bf16.
@@ -162,8 +190,8 @@ xent_unit_kernel(XentTarget target, const float* dloss, int M, float* unit) {
 // what the target's element lost, and dx gets that times the target's weights.  (Two terms for 300 rows:
 // 116 -> 160 us, dw 2.4e-3 -> 1.7e-3 off in the norm, the part of its own rounding.)
 // A mean's rows all have one weight, and with it would all be off by the same part, in one direction.
-// So d is kept in units of the weights' mantissa (xent_unit_kernel), which the results are multiplied by: the
-// targets' elements, -1 for the most part, are then exact.
+// So d is kept in units of the weights' mantissa (xent_prepare_kernel), which the results are multiplied
+// by: the targets' elements, -1 for the most part, are then exact.
 template <bool TWO>
 struct XentGradEpi {
   static constexpr int PART = 0, PART_ONE = 0, SHORT = 8;
@@ -303,7 +331,8 @@ struct StoreEpi {
 };
 
 // dx = the slices' sums added in order, and what the target's element of d lost times the target's
-// weights, times d's unit and rounded to bf16; a thread takes eight columns.
+// weights, times d's unit and rounded to bf16; 0 in the rows without a target, whatever w holds.  A thread
+// takes eight columns.
 __global__ void __launch_bounds__(256)
 xent_dx_kernel(const float* __restrict__ sum, int ks, int64_t M, int K, XentTarget target,
                const float* __restrict__ rest, const float* __restrict__ unit,
@@ -318,8 +347,12 @@ xent_dx_kernel(const float* __restrict__ sum, int ks, int64_t M, int K, XentTarg
   float a[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) a[j] = 0.0f;
-  const int t = rest ? target.of(static_cast<int>(row)) : -1;
-  if (t >= 0) {
+  const int t = target.of(static_cast<int>(row));
+  if (t < 0) {
+    *reinterpret_cast<uint4*>(dx + row * lddx + col) = make_uint4(0u, 0u, 0u, 0u);
+    return;
+  }
+  if (rest) {
     const float lost = __ldg(rest + row);
     const uint4 u = __ldg(reinterpret_cast<const uint4*>(w + t * ldw + col));
     const uint32_t b[4] = {u.x, u.y, u.z, u.w};
@@ -474,8 +507,17 @@ static int xent_backward(const lmoe_linear_xent& p, const float* dloss, __nv_bfl
   float* unit = reinterpret_cast<float*>(ws + L.unit);
   const XentTarget target{p.target, p.target_type == LMOE_I64, p.V};
   const TileOperand X{p.x, p.M, p.K, p.ldx, 0};
-  if (launch_pdl(xent_unit_kernel, 1u, XENT_UNIT_THREADS, 0, stream, target, dloss, p.M, unit) !=
-      cudaSuccess)
+  // dw's x: in dx until that is written, at the end, or where dx's sums would be
+  __nv_bfloat16* rows = !dw ? nullptr : dx ? dx : reinterpret_cast<__nv_bfloat16*>(sum);
+  const int64_t ldrows = dx ? lddx : p.K;
+  int64_t blocks = 1;
+  if (dw) {
+    blocks = ceil_div(p.M * ceil_div(p.K, 1024), XENT_PREPARE_THREADS / 32);
+    if (blocks > 8 * sms) blocks = 8 * sms;
+  }
+  if (launch_pdl(xent_prepare_kernel, static_cast<unsigned>(blocks), XENT_PREPARE_THREADS, 0, stream,
+                 target, dloss, p.M, unit, static_cast<const __nv_bfloat16*>(p.x), p.ldx, p.K, rows,
+                 ldrows) != cudaSuccess)
     return LMOE_ERR_CUDA;
   bool stall = inject_stall();
   int slices = 1;
@@ -527,7 +569,8 @@ static int xent_backward(const lmoe_linear_xent& p, const float* dloss, __nv_bfl
         return LMOE_ERR_CUDA;
       TileArgs g = xent_args(p, cols, p.K, p.M);
       g.two = L.terms > 1;
-      rc = launch_tile<true, true, false>(Dl, X, maps, g, StoreEpi{dw_f32, unit},
+      rc = launch_tile<true, true, false>(Dl, TileOperand{rows, p.M, p.K, ldrows, 0}, maps, g,
+                                          StoreEpi{dw_f32, unit},
                                           tile_plan(cols, p.K, p.M * L.terms, 1, false, sms,
                                                     STORE_EPILOGUE),
                                           dev, sms, stream);

@@ -817,7 +817,7 @@ class LinearCrossEntropy:
                  want_dw: bool = True, stream=None) -> dict:
         """Gradients for the x, target and lse of a ``forward``: dloss [M] fp32, the gradient of each
         row's loss -> dx [M, K] bf16, dw [V, K] (fp32, or bf16 with dw_dtype).  Rows without a target
-        have none."""
+        have none, whatever x, lse and dloss hold there."""
         if stream is not None:
             with torch.cuda.stream(stream):
                 return self.backward(x, target, lse, dloss, dw_dtype, want_dx, want_dw)

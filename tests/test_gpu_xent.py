@@ -455,3 +455,31 @@ def test_few_rows_of_one_weight_among_many_without(dev, M, rows):
     g = torch.zeros(M, device=dev)
     g[list(rows)] = 1 / 300
     _check_one_weight(head, x, t, g)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("M,K", [(1, 8), (40, 64), (128, 1032), (300, 64), (1100, 200)])
+def test_rows_without_a_target_take_no_part(dev, M, K, bad):
+    """Whatever is in them (a padded batch): the other rows' gradients and dw keep their bits, their own
+    dx is 0; with weights that are not finite too, for which the formulas give the others NaN."""
+    V = 700
+    head = lmoe.LinearCrossEntropy(_draw(dev, V, K, 1, 0.2))
+    x, t, g = _draw(dev, M, K, 2), _targets(dev, M, V, 3, ignored=0.3), _weights_of_rows(dev, M, 4)
+    t[0] = -100
+    off = t < 0
+    _, lse = head.forward(x, t)
+    want = head.backward(x, t, lse, g)
+    xx, gg = x.clone(), g.clone()
+    xx[off] = bad
+    xx[0, 1:] = 1.0
+    gg[off] = bad
+    _, lse2 = head.forward(xx, t)
+    assert torch.equal(lse2[~off], lse[~off])
+    for dw in (torch.float32, BF):
+        out = head.backward(xx, t, lse2, gg, dw_dtype=dw)
+        assert torch.equal(out["dx"], want["dx"]) and torch.equal(out["dw"], want["dw"].to(dw))
+        assert not out["dx"][off].any()
+    assert torch.equal(head.backward(xx, t, lse2, gg, want_dx=False)["dw"], want["dw"])
+    head.w = head.w.clone()
+    head.w[5, 3] = bad
+    assert not head.backward(x, t, lse, g)["dx"][off].any()
