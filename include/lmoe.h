@@ -591,8 +591,8 @@ int lmoe_linear_backward(const lmoe_linear *p, const void *dy, long long lddy, v
  *   lse = log sum exp l;   loss = lse - l[target]
  * The logits are not kept: no buffer of M x V elements is written or needed.  A row whose target is
  * outside 0 .. V - 1 (an ignored token) has loss 0 and takes no part in the gradients, whatever its
- * x, lse and dloss hold (NaN, infinities); its lse is computed all the same.  The loss is the target's negative log-probability: with one row the call
- * scores a sampled token. */
+ * x, lse and dloss hold (NaN, infinities); its lse is computed all the same.  The loss is the target's
+ * negative log-probability: with one row the call scores a sampled token. */
 typedef struct lmoe_linear_xent {
   int M, V, K;            /* rows of x, tokens of the vocabulary, features */
   const void *x;          /* [M, K] bf16, rows ldx elements apart */
@@ -622,8 +622,9 @@ int lmoe_linear_xent_forward(const lmoe_linear_xent *p, void *ws, size_t ws_byte
  *   dloss, so that a weight that all rows share is not rounded;
  *   dx [M, K] bf16 = d . w, rows lddx elements apart;  dw [V, K] = d^T . x, dw_type LMOE_BF16 or
  *   LMOE_F32 (the sum over the rows without a second rounding).
- * Either may be NULL (not wanted).  The logits are computed again, a piece of the vocabulary at a
- * time: ws, lmoe_linear_xent_backward_workspace_bytes(p) of device scratch, 16-byte aligned, holds d
+ * Either may be NULL (not wanted).  The logits are computed again, bit for bit as by the forward (of
+ * which lse is to be: p - 1 of a target that is nearly certain is then off by lse's rounding only), a
+ * piece of the vocabulary at a time: ws, lmoe_linear_xent_backward_workspace_bytes(p) of device scratch, 16-byte aligned, holds d
  * of one piece (256 MB, or 4096 tokens) and dx in fp32.  M == 0 zeroes dw.  Alignment and overlaps as
  * above.  Errors: as above. */
 size_t lmoe_linear_xent_backward_workspace_bytes(const lmoe_linear_xent *p);

@@ -194,7 +194,7 @@ xent_prepare_kernel(XentTarget target, const float* dloss, int M, float* unit, c
 // by: the targets' elements, -1 for the most part, are then exact.
 template <bool TWO>
 struct XentGradEpi {
-  static constexpr int PART = 0, PART_ONE = 0, SHORT = 8;
+  static constexpr int PART = LseEpi::PART, PART_ONE = LseEpi::PART_ONE, SHORT = 8;
   XentTarget target;
   const float* lse;
   const float* dloss;
@@ -222,20 +222,20 @@ struct XentGradEpi {
     uint32_t w[16], low[TWO ? 16 : 1];
     const int at = st.target - col;
     const bool none = st.target == INT32_MIN;  // 0, whatever its logits are
-    auto value = [&](float l, bool hot) {
-      const float p = ptx::exp2_approx((l - st.lse) * LOG2E);
-      return st.g * (hot ? p - 1.0f : p);
-    };
-    if (!TWO && at >= 0 && at < 32) {
+    float hot = 0.0f;  // the target's element
+    if (at >= 0 && at < 32) {
       float l = 0.0f;
 #pragma unroll
       for (int j = 0; j < 32; ++j) l = j == at ? v[j] : l;
-      const float d = value(l, true);
-      rest[c.row] = d - __bfloat162float(__float2bfloat16_rn(d));
+      hot = st.g * expm1f(l - st.lse);
+      if (!TWO) rest[c.row] = hot - __bfloat162float(__float2bfloat16_rn(hot));
     }
+    auto value = [&](int j) {
+      return j == at ? hot : st.g * ptx::exp2_approx((v[j] - st.lse) * LOG2E);
+    };
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
-      const float d0 = value(v[2 * j], 2 * j == at), d1 = value(v[2 * j + 1], 2 * j + 1 == at);
+      const float d0 = value(2 * j), d1 = value(2 * j + 1);
       const __nv_bfloat162 b = __floats2bfloat162_rn(d0, d1);
       w[j] = none ? 0u : *reinterpret_cast<const uint32_t*>(&b);
       if constexpr (TWO) {
@@ -394,6 +394,12 @@ static TilePlan lse_plan(int64_t M, int64_t V, int64_t K, int sms) {
   return best;
 }
 
+// The logits' tiles in the backward: the widths that suit a piece of `cols` columns, but one SM or a pair as
+// the forward took for all V.
+static TilePlan xent_logits_plan(const lmoe_linear_xent& p, int64_t cols, int sms) {
+  return lse_plan(p.M, p.M > BLOCK_M ? p.V : cols, p.K, sms);
+}
+
 struct XentLayout {
   size_t part, picked, total;
 };
@@ -533,7 +539,7 @@ static int xent_backward(const lmoe_linear_xent& p, const float* dloss, __nv_bfl
       TileArgs g = xent_args(p, p.M, cols, p.K);
       g.inject_stall = stall;
       stall = false;
-      const TilePlan plan = lse_plan(p.M, cols, p.K, sms);
+      const TilePlan plan = xent_logits_plan(p, cols, sms);
       const int at = static_cast<int>(c0);
       rc = L.terms > 1
                ? launch_tile<false, false, false>(

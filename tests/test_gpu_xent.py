@@ -483,3 +483,44 @@ def test_rows_without_a_target_take_no_part(dev, M, K, bad):
     head.w = head.w.clone()
     head.w[5, 3] = bad
     assert not head.backward(x, t, lse, g)["dx"][off].any()
+
+
+@pytest.mark.parametrize("M", [1, 100, 300, 2049])
+@pytest.mark.parametrize("dw", [torch.float32, BF])
+def test_rows_that_are_nearly_certain(dev, M, dw):
+    """Targets of probability 1 - 1e-3 down to 1 - 1e-9, whose gradient is what is left of it.  A target's
+    logit here is a sum of 7168 terms of one sign, which the tensor cores may make 1e-4 too small and
+    more; lse is made of the same number, so that p - 1 is only off by lse's own rounding, 2^-20 (lse is
+    below 32), the additions to the sum behind it, 2^-24 each, and what the logits' errors e change
+    in the other tokens' probabilities.  e: sums within one accumulator are cut off by 2^-23 at most for
+    each of 64 products of 16 features, then added in fp32."""
+    V, K = 2500, 7168
+    gen = torch.Generator(device=dev).manual_seed(3)
+    x = _draw(dev, M, K, 2)
+    t = torch.randperm(V, generator=gen, device=dev)[:M]
+    size = 14 + 16 * torch.rand(M, 1, generator=gen, device=dev)
+    w = _draw(dev, V, K, 1, 0.3 * K ** -0.5)
+    w[t] = (size / x.float().square().sum(1, keepdim=True) * x.float()).to(BF)
+    head = lmoe.LinearCrossEntropy(w)
+    g = 0.5 + torch.rand(M, generator=gen, device=dev)
+    _, lse = head.forward(x, t)
+    out = head.backward(x, t, lse, g, dw_dtype=dw)
+    x64, w64 = x.double(), w.double()
+    l = x64 @ w64.T
+    p = torch.softmax(l, 1)
+    hot = torch.arange(V, device=dev) == t.unsqueeze(1)
+    gd = g.double().unsqueeze(1)
+    left = torch.where(hot, 0.0, p).sum(1, keepdim=True)  # 1 - p of the target
+    d = gd * torch.where(hot, -left, p)
+    e = (64 + 7) * ULP * (x64.abs() @ w64.abs().T).amax(1, keepdim=True)
+    off = 2.0 ** -20 + (128 + V / 1024) * 2.0 ** -24
+    ed = gd * torch.where(hot, off + (2 * e + 2.0 ** -20) * left, (2 * e + off + EXP) * p)
+    half = HALF * HALF if M <= 128 else HALF
+    sums = 2 if M <= 128 else 1
+    ew = (ed + half * d.abs()).T @ x64.abs() + 1.01 * sums * M * ULP * (d.abs().T @ x64.abs())
+    want = d.T @ x64
+    _within(out["dw"], want, 1.01 * (ew + (HALF if dw is BF else ULP) * want.abs()), (M, "dw"))
+    ex = (ed + half * torch.where(hot, 0.0, d).abs()) @ w64.abs() + \
+        1.01 * sums * V * ULP * (d.abs() @ w64.abs())
+    want = d @ w64
+    _within(out["dx"], want, 1.01 * (ex + HALF * want.abs()), (M, "dx"))
