@@ -119,9 +119,10 @@ lse_join_kernel(const float2* __restrict__ part, int parts, int M, XentTarget ta
   __syncthreads();
   if (w != 0 || row >= M) return;
   for (int i = 1; i < JOIN_WARPS; ++i) lse_join(m, s, red[i][lane].x, red[i][lane].y);
-  const float l = lse_base(m) + logf(s);
-  if (lse) lse[row] = l;
-  if (loss) loss[row] = target.of(row) >= 0 ? l - picked[row] : 0.0f;
+  // the loss not from lse, whose rounding (5e-7 near 12) is all of a likely token's loss
+  const float base = lse_base(m), l = logf(s);
+  if (lse) lse[row] = base + l;
+  if (loss) loss[row] = target.of(row) >= 0 ? l + (base - picked[row]) : 0.0f;
 }
 
 // ------------------------------------------------------------------------- backward

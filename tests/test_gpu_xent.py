@@ -524,3 +524,30 @@ def test_rows_that_are_nearly_certain(dev, M, dw):
         1.01 * sums * V * ULP * (d.abs() @ w64.abs())
     want = d @ w64
     _within(out["dx"], want, 1.01 * (ex + HALF * want.abs()), (M, "dx"))
+
+
+@pytest.mark.parametrize("base", [0.0, 12.0, 200.0, -3008.0])
+@pytest.mark.parametrize("M", [5, 300, 1100])
+def test_small_losses_have_no_steps_of_lse(dev, M, base):
+    """Logits that fp32 holds exactly, all shifted by `base`: the loss does not see it.  The sum of 40
+    tokens' exponentials takes at most 8 + 4 additions, 2^-24 of 1 or so each, and exponentials 2^-21 of
+    themselves and 2^-24 of their argument (at most 30); the logarithm 2^-22 of its value."""
+    V, K = 40, 8
+    w = torch.zeros(V, K, device=dev)
+    w[:, 0] = 1.0
+    w[:, 1] = -torch.arange(V, device=dev) / 2.0   # tokens' distances from the first
+    w[0, 1] = 4.0
+    x = torch.zeros(M, K, device=dev)
+    x[:, 0] = base
+    x[:, 1] = (1 + torch.arange(M, device=dev) % 6) / 2.0
+    l = (x.double() @ w.double().T)
+    t = torch.arange(M, device=dev) // 6 % 5  # the likely one, and others
+    t = torch.where(t > 1, 0, t)
+    head = lmoe.LinearCrossEntropy(w.to(BF))
+    loss, lse = head.forward(x.to(BF), t)
+    want = -torch.log_softmax(l, 1).gather(1, t.unsqueeze(1)).squeeze(1)
+    rest = torch.expm1(-torch.log_softmax(l, 1).amax(1)).abs()
+    bound = 12 * 2.0 ** -24 * (1 + rest) + rest * (2.0 ** -21 + 30 * 2.0 ** -22) + \
+        2.0 ** -22 * want + 2.0 ** -23 * want
+    _within(loss, want, 1.01 * bound, "loss")
+    _within(lse, torch.logsumexp(l, 1), 1.01 * bound + ULP * l.abs().amax(1), "lse")
