@@ -621,12 +621,12 @@ int lmoe_linear_xent_forward(const lmoe_linear_xent *p, void *ws, size_t ws_byte
  *   terms up to 128 rows; beyond, dx takes the target's element unrounded) in units of the rows'
  *   dloss, so that a weight that all rows share is not rounded;
  *   dx [M, K] bf16 = d . w, rows lddx elements apart;  dw [V, K] = d^T . x, dw_type LMOE_BF16 or
- *   LMOE_F32 (the sum over the rows without a second rounding).
+ *   LMOE_F32 (the sum over the rows without a second rounding, added up in fp32).
  * Either may be NULL (not wanted).  The logits are computed again, bit for bit as by the forward (of
  * which lse is to be: p - 1 of a target that is nearly certain is then off by lse's rounding only), a
- * piece of the vocabulary at a time: ws, lmoe_linear_xent_backward_workspace_bytes(p) of device scratch, 16-byte aligned, holds d
- * of one piece (256 MB, or 4096 tokens) and dx in fp32.  M == 0 zeroes dw.  Alignment and overlaps as
- * above.  Errors: as above. */
+ * piece of the vocabulary at a time: ws, lmoe_linear_xent_backward_workspace_bytes(p) of device
+ * scratch, 16-byte aligned, holds d of one piece (256 MB, or 4096 tokens) and dx in fp32.  M == 0 zeroes
+ * dw.  Alignment and overlaps as above.  Errors: as above. */
 size_t lmoe_linear_xent_backward_workspace_bytes(const lmoe_linear_xent *p);
 int lmoe_linear_xent_backward(const lmoe_linear_xent *p, const float *dloss, void *dx,
                               long long lddx, void *dw, int dw_type, void *ws, size_t ws_bytes,

@@ -236,13 +236,16 @@ __device__ __forceinline__ void tile_mma(uint32_t d, uint32_t sp, uint32_t idesc
 //   SHORT   reductions of at most this many K-blocks give an epilogue warp two buffers: a chunk else
 //           waits for the tensor store of the one before it to have read the buffer.  The second one
 //           costs a stage.
-template <bool PAIR, bool P_MN, bool Q_MN, bool F16, class Epi>
+// PARTS: the reduction is longer than that.  (The epilogue's code stands there once for each chunk in registers,
+// which reductions without parts need not pay for: gradients of 300 x 50257 x 1024 with an fp32 dw took 151 us
+// in one kernel for both, 141 so.)
+template <bool PAIR, bool P_MN, bool Q_MN, bool F16, bool PARTS, class Epi>
 __global__ void __launch_bounds__(LINEAR_THREADS, 1)
 tile_kernel(const __grid_constant__ TileMaps maps, const TileArgs g, const Epi epi) {
   const int bn = g.bn, stages = g.stages;
   constexpr int TM = PAIR ? 2 * BLOCK_M : BLOCK_M;
   constexpr int TMEM_COLS = 512;  // two accumulator sets, 256 columns apart
-  constexpr int PART = PAIR ? Epi::PART : Epi::PART_ONE;
+  constexpr int PART = !PARTS ? 0 : PAIR ? Epi::PART : Epi::PART_ONE;
   const int qn = PAIR ? bn / 2 : bn;  // columns of Q that this CTA stages
   const int stage_bytes = LINEAR_P_BYTES + qn * 128;
   extern __shared__ uint8_t smem_raw[];
@@ -442,51 +445,48 @@ tile_kernel(const __grid_constant__ TileMaps maps, const TileArgs g, const Epi e
         }
       };
       if (!arrived()) break;
-      if constexpr (PART > 0) {
-        if (c.t.nk > PART) {
-          float sum[4][32];
+      if constexpr (PARTS) {
+        float sum[4][32];
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int j = 0; j < 32; ++j) sum[i][j] = 0.0f;
-          bool ok = true;
-          for (int k0 = 0;;) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              if (half + 2 * i >= chunks) continue;
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                float v[16];
-                ptx::tmem_ld_32x32b_x16(
-                    tb + static_cast<uint32_t>((half + 2 * i) * TILE_CHUNK + 16 * h), v);
-#pragma unroll
-                for (int j = 0; j < 16; ++j) sum[i][16 * h + j] += v[j];
-              }
-            }
-            release();
-            if ((k0 += PART) >= c.t.nk) break;
-            ++lt;
-            if (!(ok = arrived())) break;
-          }
-          if (!ok) break;
+          for (int j = 0; j < 32; ++j) sum[i][j] = 0.0f;
+        bool ok = true;
+        for (int k0 = 0;;) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int ch = half + 2 * i, col = c.t.col0 + ch * TILE_CHUNK;
-            if (ch < chunks)
-              epi.chunk(g, c, col, st, sum[i], ch + 2 < chunks ? col + 2 * TILE_CHUNK : -1);
+            if (half + 2 * i >= chunks) continue;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              float v[16];
+              ptx::tmem_ld_32x32b_x16(
+                  tb + static_cast<uint32_t>((half + 2 * i) * TILE_CHUNK + 16 * h), v);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) sum[i][16 * h + j] += v[j];
+            }
           }
-          if (half < chunks) epi.end(g, c, st);
-          continue;
+          release();
+          if ((k0 += PART) >= c.t.nk) break;
+          ++lt;
+          if (!(ok = arrived())) break;
         }
-      }
-      if (half >= chunks) release();
+        if (!ok) break;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int ch = half + 2 * i, col = c.t.col0 + ch * TILE_CHUNK;
+          if (ch < chunks)
+            epi.chunk(g, c, col, st, sum[i], ch + 2 < chunks ? col + 2 * TILE_CHUNK : -1);
+        }
+      } else {
+        if (half >= chunks) release();
 #pragma unroll 1
-      for (int ch = half; ch < chunks; ch += 2) {
-        float v[32];
-        ptx::tmem_ld_32x32b_x32(tb + static_cast<uint32_t>(ch * TILE_CHUNK), v);
-        if (ch + 2 >= chunks) release();
-        const int col = c.t.col0 + ch * TILE_CHUNK;
-        epi.chunk(g, c, col, st, v, ch + 2 < chunks ? col + 2 * TILE_CHUNK : -1);
+        for (int ch = half; ch < chunks; ch += 2) {
+          float v[32];
+          ptx::tmem_ld_32x32b_x32(tb + static_cast<uint32_t>(ch * TILE_CHUNK), v);
+          if (ch + 2 >= chunks) release();
+          const int col = c.t.col0 + ch * TILE_CHUNK;
+          epi.chunk(g, c, col, st, v, ch + 2 < chunks ? col + 2 * TILE_CHUNK : -1);
+        }
       }
       if (half < chunks) epi.end(g, c, st);
     }
@@ -770,13 +770,20 @@ inline TilePlan tile_plan(int64_t R, int64_t C, int64_t D, int64_t batch, bool s
 template <bool PAIR, bool SPLIT, bool P_MN, bool Q_MN, bool F16, class Epi>
 int launch_tile(const TileOperand& P, const TileOperand& Q, TileMaps& maps, TileArgs g,
                 const Epi& epi, int bn, int split, int dev, int sms, cudaStream_t stream) {
-  static std::atomic<int> cache[LINEAR_MAX_DEVICES];
+  static std::atomic<int> caches[2][LINEAR_MAX_DEVICES];
+  constexpr int PART = PAIR ? Epi::PART : Epi::PART_ONE;
   void (*kernel)(TileMaps, TileArgs, Epi);
-  if constexpr (SPLIT)
+  bool parts = false;
+  if constexpr (SPLIT) {
     kernel = tile_split_kernel<P_MN, Q_MN, F16, Epi>;
-  else
-    kernel = tile_kernel<PAIR, P_MN, Q_MN, F16, Epi>;
-  const int active = linear_kernel_setup(kernel, PAIR ? 2 : 1, dev, cache);
+  } else {
+    kernel = tile_kernel<PAIR, P_MN, Q_MN, F16, false, Epi>;
+    if constexpr (PART > 0) {
+      parts = ceil_div(g.D, BLOCK_K) << g.two > PART;
+      if (parts) kernel = tile_kernel<PAIR, P_MN, Q_MN, F16, true, Epi>;
+    }
+  }
+  const int active = linear_kernel_setup(kernel, PAIR ? 2 : 1, dev, caches[parts]);
   if (active < 0) return LMOE_ERR_CUDA;
   constexpr int TM = PAIR ? 2 * BLOCK_M : BLOCK_M;
   g.bn = bn;

@@ -131,9 +131,9 @@ lse_join_kernel(const float2* __restrict__ part, int parts, int M, XentTarget ta
 // that is a normal number of a row that has a target; 1 where there is none.  It goes through the rows until
 // it finds it.  (Chosen from 256 rows' weights, targets or not, by each warp for itself it was another one
 // where a padded row's weight was read, or none of the few rows that have a weight.)
-// All blocks (`rows` not null): x with zeros in the rows without a target, which dw = d^T x reads: d is 0
+// The others, if any: x with zeros in the rows without a target, which dw = d^T x reads: d is 0
 // there, but a padded row may hold anything, and 0 times NaN is not 0.  A warp takes 1024 columns of a row
-// at a time.  (4096 x 7168, 118 MB there and back: 20 us of 7 ms.)
+// at a time.
 constexpr int XENT_PREPARE_THREADS = 256;
 __global__ void __launch_bounds__(XENT_PREPARE_THREADS)
 xent_prepare_kernel(XentTarget target, const float* dloss, int M, float* unit, const __nv_bfloat16* x,
@@ -160,26 +160,25 @@ xent_prepare_kernel(XentTarget target, const float* dloss, int M, float* unit, c
       break;
     }
     if (row0 >= M && threadIdx.x == 0) *unit = 1.0f;
+    return;
   }
-  if (!rows) return;
   const int lane = threadIdx.x & 31, per = K / 8, parts = (per + 127) / 128;
   const int64_t items = static_cast<int64_t>(M) * parts;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * (XENT_PREPARE_THREADS / 32);
-  for (int64_t i = blockIdx.x * (XENT_PREPARE_THREADS / 32) + (threadIdx.x >> 5); i < items; i += step) {
+  constexpr int WARPS = XENT_PREPARE_THREADS / 32;
+  const int64_t step = static_cast<int64_t>(gridDim.x - 1) * WARPS;
+  for (int64_t i = (blockIdx.x - 1) * WARPS + (threadIdx.x >> 5); i < items; i += step) {
     const int64_t row = i / parts;
     const int c = static_cast<int>(i - row * parts) * 128 + lane;
-    const bool on = target.of(static_cast<int>(row)) >= 0;
     const uint4* from = reinterpret_cast<const uint4*>(x + row * ldx);
     uint4* to = reinterpret_cast<uint4*>(rows + row * ldrows);
     uint4 v[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      v[k] = make_uint4(0u, 0u, 0u, 0u);
-      if (on && c + 32 * k < per) v[k] = from[c + 32 * k];
-    }
+    for (int k = 0; k < 4; ++k)
+      if (c + 32 * k < per) v[k] = from[c + 32 * k];
+    const bool on = target.of(static_cast<int>(row)) >= 0;
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-      if (c + 32 * k < per) to[c + 32 * k] = v[k];
+      if (c + 32 * k < per) to[c + 32 * k] = on ? v[k] : make_uint4(0u, 0u, 0u, 0u);
   }
 }
 
@@ -298,10 +297,13 @@ struct XentDxEpi {
   __device__ __forceinline__ void end(const TileArgs&, TileCtx&, State&) const {}
 };
 
-// An output times d's unit, bf16 or fp32.
+// dw: the sums times d's unit, bf16 or fp32.  An fp32 dw's sums are taken out of TMEM every 512 rows, as the
+// linear layers' are: what the MMA cuts off made those of 65536 rows of one sign 1.5e-4 too small.  (A bf16 dw
+// stays in TMEM: that is a sixth of its own rounding at 2^18 rows.  So do dx's sums, a chain over a slice of a
+// piece at a time.)
+template <bool F32>
 struct StoreEpi {
-  static constexpr int PART = 0, PART_ONE = 0, SHORT = 16;
-  int f32;
+  static constexpr int PART = F32 ? LINEAR_DW_PART : 0, PART_ONE = PART, SHORT = 16;
   const float* unit;
   struct State {
     float unit;
@@ -315,7 +317,7 @@ struct StoreEpi {
 #pragma unroll
     for (int j = 0; j < 32; ++j) v[j] *= st.unit;
     tile_next_buf(c);
-    if (f32) {
+    if constexpr (F32) {
       tile_put32(c.buf, c.lane, v);
     } else {
       uint32_t w[16];
@@ -517,12 +519,9 @@ static int xent_backward(const lmoe_linear_xent& p, const float* dloss, __nv_bfl
   // dw's x: in dx until that is written, at the end, or where dx's sums would be
   __nv_bfloat16* rows = !dw ? nullptr : dx ? dx : reinterpret_cast<__nv_bfloat16*>(sum);
   const int64_t ldrows = dx ? lddx : p.K;
-  int64_t blocks = 1;
-  if (dw) {
-    blocks = ceil_div(p.M * ceil_div(p.K, 1024), XENT_PREPARE_THREADS / 32);
-    if (blocks > 8 * sms) blocks = 8 * sms;
-  }
-  if (launch_pdl(xent_prepare_kernel, static_cast<unsigned>(blocks), XENT_PREPARE_THREADS, 0, stream,
+  int64_t blocks = dw ? ceil_div(p.M * ceil_div(p.K, 1024), XENT_PREPARE_THREADS / 32) : 0;
+  if (blocks > 8 * sms) blocks = 8 * sms;
+  if (launch_pdl(xent_prepare_kernel, static_cast<unsigned>(1 + blocks), XENT_PREPARE_THREADS, 0, stream,
                  target, dloss, p.M, unit, static_cast<const __nv_bfloat16*>(p.x), p.ldx, p.K, rows,
                  ldrows) != cudaSuccess)
     return LMOE_ERR_CUDA;
@@ -576,11 +575,12 @@ static int xent_backward(const lmoe_linear_xent& p, const float* dloss, __nv_bfl
         return LMOE_ERR_CUDA;
       TileArgs g = xent_args(p, cols, p.K, p.M);
       g.two = L.terms > 1;
-      rc = launch_tile<true, true, false>(Dl, TileOperand{rows, p.M, p.K, ldrows, 0}, maps, g,
-                                          StoreEpi{dw_f32, unit},
-                                          tile_plan(cols, p.K, p.M * L.terms, 1, false, sms,
-                                                    STORE_EPILOGUE),
-                                          dev, sms, stream);
+      const TileOperand XT{rows, p.M, p.K, ldrows, 0};
+      const TilePlan plan = tile_plan(cols, p.K, p.M * L.terms, 1, false, sms, STORE_EPILOGUE);
+      rc = dw_f32 ? launch_tile<true, true, false>(Dl, XT, maps, g, StoreEpi<true>{unit}, plan, dev, sms,
+                                                   stream)
+                  : launch_tile<true, true, false>(Dl, XT, maps, g, StoreEpi<false>{unit}, plan, dev, sms,
+                                                   stream);
       if (rc != LMOE_OK) return rc;
     }
   }

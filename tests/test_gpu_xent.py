@@ -468,7 +468,6 @@ def test_rows_without_a_target_take_no_part(dev, M, K, bad):
     t[0] = -100
     off = t < 0
     _, lse = head.forward(x, t)
-    want = head.backward(x, t, lse, g)
     xx, gg = x.clone(), g.clone()
     xx[off] = bad
     xx[0, 1:] = 1.0
@@ -476,10 +475,12 @@ def test_rows_without_a_target_take_no_part(dev, M, K, bad):
     _, lse2 = head.forward(xx, t)
     assert torch.equal(lse2[~off], lse[~off])
     for dw in (torch.float32, BF):
+        want = head.backward(x, t, lse, g, dw_dtype=dw)
         out = head.backward(xx, t, lse2, gg, dw_dtype=dw)
-        assert torch.equal(out["dx"], want["dx"]) and torch.equal(out["dw"], want["dw"].to(dw))
+        assert torch.equal(out["dx"], want["dx"]) and torch.equal(out["dw"], want["dw"])
         assert not out["dx"][off].any()
-    assert torch.equal(head.backward(xx, t, lse2, gg, want_dx=False)["dw"], want["dw"])
+        alone = head.backward(xx, t, lse2, gg, dw_dtype=dw, want_dx=False)
+        assert torch.equal(alone["dw"], want["dw"])
     head.w = head.w.clone()
     head.w[5, 3] = bad
     assert not head.backward(x, t, lse, g)["dx"][off].any()
@@ -551,3 +552,22 @@ def test_small_losses_have_no_steps_of_lse(dev, M, base):
         2.0 ** -22 * want + 2.0 ** -23 * want
     _within(loss, want, 1.01 * bound, "loss")
     _within(lse, torch.logsumexp(l, 1), 1.01 * bound + ULP * l.abs().amax(1), "lse")
+
+
+@pytest.mark.parametrize("M,K", [(300, 136), (70000, 8), (65536, 264)])
+def test_fp32_dw_of_many_rows(dev, M, K):
+    """A head of zeros over 128 tokens: d is 2^-7, or that less 1, for all rows, which bf16 holds, and x is
+    positive.  The tensor cores cut off less than 2^-23 of what has been summed in each step of 16 rows; over
+    the 512 rows that stay in TMEM that is 32 * 2^-23, and their sums are added in fp32, 2^-24 each (a sum of
+    both signs: of the larger part).  Multiplying by the unit, 1, changes nothing."""
+    V = 128
+    head = lmoe.LinearCrossEntropy(torch.zeros(V, K, dtype=BF, device=dev))
+    gen = torch.Generator(device=dev).manual_seed(1)
+    x = torch.exp2(-8 * torch.rand(M, K, generator=gen, device=dev)).to(BF)
+    t = torch.arange(M, device=dev) % 64
+    _, lse = head.forward(x, t)
+    out = head.backward(x, t, lse, torch.ones(M, device=dev), want_dx=False)
+    sums = torch.zeros(V, K, dtype=torch.float64, device=dev).index_add_(0, t, x.double())
+    all_rows = x.double().sum(0) / V
+    bound = (32 * 2.0 ** -23 + (M // 512 + 1) * 2.0 ** -24 + 2.0 ** -23) * (sums + all_rows)
+    _within(out["dw"], all_rows - sums, bound, (M, K))
