@@ -32,6 +32,8 @@ __device__ __forceinline__ void lse_join(float& m, float& s, float m2, float s2)
   m = top;
 }
 
+constexpr int XENT_MOST = 1 << 30;  // of rows, tokens and features
+
 struct XentTarget {
   const void* p;
   int wide;  // int64, else int32
@@ -192,8 +194,11 @@ xent_prepare_kernel(XentTarget target, const float* dloss, int M, float* unit, c
 // A mean's rows all have one weight, and with it would all be off by the same part, in one direction.
 // So d is kept in units of the weights' mantissa (xent_prepare_kernel), which the results are multiplied
 // by: the targets' elements, -1 for the most part, are then exact.
+// NONE: a row without a target, in the place of a target's column; no distance to a column wraps.
 template <bool TWO>
 struct XentGradEpi {
+  static constexpr int NONE = INT32_MIN / 2;
+  static_assert(int64_t{NONE} - XENT_MOST >= INT32_MIN && NONE <= -XENT_MOST, "");
   static constexpr int PART = LseEpi::PART, PART_ONE = LseEpi::PART_ONE, SHORT = 8;
   XentTarget target;
   const float* lse;
@@ -213,7 +218,7 @@ struct XentGradEpi {
       st.g = __fdiv_rn(__ldg(dloss + c.row), *unit);
       st.target -= col0;
     } else {
-      st.target = INT32_MIN;
+      st.target = NONE;
     }
   }
   __device__ __forceinline__ void load(const TileArgs&, TileCtx&, int, State&) const {}
@@ -221,7 +226,7 @@ struct XentGradEpi {
                                         float (&v)[32], int) const {
     uint32_t w[16], low[TWO ? 16 : 1];
     const int at = st.target - col;
-    const bool none = st.target == INT32_MIN;  // 0, whatever its logits are
+    const bool none = st.target == NONE;  // 0, whatever its logits are
     float hot = 0.0f;  // the target's element
     if (at >= 0 && at < 32) {
       float l = 0.0f;
@@ -450,8 +455,8 @@ static XentBwdLayout xent_bwd_layout(const lmoe_linear_xent& p) {
 static int xent_sizes_ok(const lmoe_linear_xent* p) {
   if (!p || p->M < 0 || p->V < 1 || p->K < 1) return LMOE_ERR_INVALID_ARG;
   if (p->target_type != LMOE_I32 && p->target_type != LMOE_I64) return LMOE_ERR_INVALID_ARG;
-  constexpr int MOST = 1 << 30;
-  if (p->K % 8 || p->M > MOST || p->V > MOST || p->K > MOST) return LMOE_ERR_UNSUPPORTED;
+  if (p->K % 8 || p->M > XENT_MOST || p->V > XENT_MOST || p->K > XENT_MOST)
+    return LMOE_ERR_UNSUPPORTED;
   if (ceil_div(p->M, 64) * ceil_div(p->V, 64) > (1 << 27) ||
       ceil_div(p->M, 64) * ceil_div(p->K, 64) > (1 << 27) ||
       ceil_div(p->V, 64) * ceil_div(p->K, 64) > (1 << 27))
