@@ -84,12 +84,12 @@ struct PolyEpi {
   };
   __device__ __forceinline__ void begin(const TileArgs& g, TileCtx& c_, State& st) const {
     st.at = tile_fetch_at(lda, c_.warp_row, g.R, c_.lane);
-    st.d = c_.row < g.R ? __ldg(adiag + c_.t.z * ld + c_.row) : 0.0f;
+    st.d = c_.row < g.R ? adiag[c_.t.z * ld + c_.row] : 0.0f;
   }
   __device__ __forceinline__ void load(const TileArgs& g, TileCtx& t, int col,
                                        State& st) const {
     tile_fetch16(a + t.t.z * stride, st.at, lda, col, g.C, st.next);
-    st.dj = col + t.lane < g.C ? __ldg(adiag + t.t.z * ld + col + t.lane) : 0.0f;
+    st.dj = col + t.lane < g.C ? adiag[t.t.z * ld + col + t.lane] : 0.0f;
   }
   __device__ __forceinline__ void chunk(const TileArgs& g, TileCtx& t, int col, State& st,
                                         float (&v)[32], int next) const {
@@ -140,13 +140,13 @@ struct ApplyEpi {
   };
   __device__ __forceinline__ void begin(const TileArgs& g, TileCtx& t, State& st) const {
     st.at = tile_fetch_at(ldx, t.warp_row, g.R, t.lane);
-    st.d = !TALL && t.row < g.R ? __ldg(bdiag + t.t.z * ld + t.row) : 0.0f;
+    st.d = !TALL && t.row < g.R ? bdiag[t.t.z * ld + t.row] : 0.0f;
   }
   __device__ __forceinline__ void load(const TileArgs& g, TileCtx& t, int col,
                                        State& st) const {
     tile_fetch16(hi + t.t.z * stride, st.at, ldx, col, g.C, st.h);
     if constexpr (TALL)
-      st.d = col + t.lane < g.C ? __ldg(bdiag + t.t.z * ld + col + t.lane) : 0.0f;
+      st.d = col + t.lane < g.C ? bdiag[t.t.z * ld + col + t.lane] : 0.0f;
     if constexpr (!LAST) {
       tile_fetch16(lo + t.t.z * stride, st.at, ldx, col, g.C, st.l);
     } else if (out.vec) {

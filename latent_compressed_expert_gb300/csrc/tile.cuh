@@ -16,7 +16,9 @@
 //   sym    P and Q are the same matrix: only tiles on or above the diagonal are computed, and the
 //          epilogue writes each to both places.
 // TMA fills what lies outside an operand with zeros, so no size is a multiple of a tile.  Every wait
-// is bounded, as in linear.cuh.
+// is bounded, as in linear.cuh.  What another launch may have written is read with plain loads: a grid may be
+// resident while the one before it still runs (programmatic launches), which the read-only path (__ldg,
+// __restrict__) does not allow for.
 #pragma once
 
 #include "linear.cuh"

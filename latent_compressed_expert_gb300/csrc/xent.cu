@@ -40,8 +40,7 @@ struct XentTarget {
   int V;
   // the row's target, -1 where it has none
   __device__ __forceinline__ int of(int row) const {
-    const long long t = wide ? __ldg(static_cast<const long long*>(p) + row)
-                             : __ldg(static_cast<const int*>(p) + row);
+    const long long t = wide ? static_cast<const long long*>(p)[row] : static_cast<const int*>(p)[row];
     return t >= 0 && t < V ? static_cast<int>(t) : -1;
   }
 };
@@ -101,9 +100,8 @@ struct LseEpi {
 // are joined in order.
 constexpr int JOIN_WARPS = 32;
 __global__ void __launch_bounds__(JOIN_WARPS * 32)
-lse_join_kernel(const float2* __restrict__ part, int parts, int M, XentTarget target,
-                const float* __restrict__ picked, float* __restrict__ loss,
-                float* __restrict__ lse) {
+lse_join_kernel(const float2* part, int parts, int M, XentTarget target, const float* picked,
+                float* loss, float* lse) {
   __shared__ float2 red[JOIN_WARPS][32];
   pdl_wait();
   pdl_launch_dependents();
@@ -113,7 +111,7 @@ lse_join_kernel(const float2* __restrict__ part, int parts, int M, XentTarget ta
   if (row < M) {
 #pragma unroll 8
     for (int p = w; p < parts; p += JOIN_WARPS) {
-      const float2 v = __ldg(part + static_cast<int64_t>(p) * M + row);
+      const float2 v = part[static_cast<int64_t>(p) * M + row];
       lse_join(m, s, v.x, v.y);
     }
   }
@@ -214,8 +212,8 @@ struct XentGradEpi {
     st.target = c.row < g.R ? target.of(c.row) : -1;
     st.lse = st.g = 0.0f;
     if (st.target >= 0) {
-      st.lse = __ldg(lse + c.row);
-      st.g = __fdiv_rn(__ldg(dloss + c.row), *unit);
+      st.lse = lse[c.row];
+      st.g = __fdiv_rn(dloss[c.row], *unit);
       st.target -= col0;
     } else {
       st.target = NONE;
@@ -314,7 +312,7 @@ struct StoreEpi {
     float unit;
   };
   __device__ __forceinline__ void begin(const TileArgs&, TileCtx&, State& st) const {
-    st.unit = __ldg(unit);
+    st.unit = *unit;
   }
   __device__ __forceinline__ void load(const TileArgs&, TileCtx&, int, State&) const {}
   __device__ __forceinline__ void chunk(const TileArgs&, TileCtx& c, int col, State& st,
@@ -342,9 +340,9 @@ struct StoreEpi {
 // weights, times d's unit and rounded to bf16; 0 in the rows without a target, whatever w holds.  A thread
 // takes eight columns.
 __global__ void __launch_bounds__(256)
-xent_dx_kernel(const float* __restrict__ sum, int ks, int64_t M, int K, XentTarget target,
-               const float* __restrict__ rest, const float* __restrict__ unit,
-               const __nv_bfloat16* __restrict__ w, int64_t ldw, __nv_bfloat16* dx, int64_t lddx) {
+xent_dx_kernel(const float* sum, int ks, int64_t M, int K, XentTarget target, const float* rest,
+               const float* unit, const __nv_bfloat16* w, int64_t ldw, __nv_bfloat16* dx,
+               int64_t lddx) {
   pdl_wait();
   pdl_launch_dependents();
   const int per = K / 8;
@@ -361,8 +359,8 @@ xent_dx_kernel(const float* __restrict__ sum, int ks, int64_t M, int K, XentTarg
     return;
   }
   if (rest) {
-    const float lost = __ldg(rest + row);
-    const uint4 u = __ldg(reinterpret_cast<const uint4*>(w + t * ldw + col));
+    const float lost = rest[row];
+    const uint4 u = *reinterpret_cast<const uint4*>(w + t * ldw + col);
     const uint32_t b[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -376,7 +374,7 @@ xent_dx_kernel(const float* __restrict__ sum, int ks, int64_t M, int K, XentTarg
 #pragma unroll
     for (int j = 0; j < 8; ++j) a[j] += f[j];
   }
-  const float u = __ldg(unit);
+  const float u = *unit;
 #pragma unroll
   for (int j = 0; j < 8; ++j) a[j] *= u;
   *reinterpret_cast<uint4*>(dx + row * lddx + col) = linear_pack8(a);
