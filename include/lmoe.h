@@ -625,8 +625,9 @@ int lmoe_linear_xent_forward(const lmoe_linear_xent *p, void *ws, size_t ws_byte
  * Either may be NULL (not wanted).  The logits are computed again, bit for bit as by the forward (of
  * which lse is to be: p - 1 of a target that is nearly certain is then off by lse's rounding only), a
  * piece of the vocabulary at a time: ws, lmoe_linear_xent_backward_workspace_bytes(p) of device
- * scratch, 16-byte aligned, holds d of one piece (256 MB, or 4096 tokens) and dx in fp32.  M == 0 zeroes
- * dw.  Alignment and overlaps as above.  Errors: as above. */
+ * scratch, 16-byte aligned, holds d of one piece (at most 256 MB, or 4096 tokens) and dx in fp32: one copy,
+ * or up to 32 while its tiles are fewer than the GPU's SMs.  M == 0 zeroes dw.  Alignment and overlaps as
+ * above.  Errors: as above. */
 size_t lmoe_linear_xent_backward_workspace_bytes(const lmoe_linear_xent *p);
 int lmoe_linear_xent_backward(const lmoe_linear_xent *p, const float *dloss, void *dx,
                               long long lddx, void *dw, int dw_type, void *ws, size_t ws_bytes,
@@ -671,7 +672,7 @@ typedef struct lmoe_muon {
 } lmoe_muon;
 
 /* ws: lmoe_muon_workspace_bytes(p) of device scratch, 16-byte aligned (6 bytes for each element of the
- * batch and 4 for each of its matrices' smaller side squared).  Any rows and cols and any alignment to
+ * batch and 4 for each of its matrices' smaller side squared, columns rounded up to 8).  Any rows and cols and any alignment to
  * the element size; multiples of 8 columns in whole 16 bytes are read faster.  A size of 0 is a no-op.
  * Arithmetic: products of fp16 operands with fp32 sums, X as two fp16 terms and the diagonals of A and
  * of b A + c A^2 in fp32 beside them, the norm's sum of squares with the roundings' rests beside it; X

@@ -417,7 +417,7 @@ static XentLayout xent_layout(const lmoe_linear_xent& p) {
   return L;
 }
 
-// Backward: a piece's d is about 256 MB (it is written once and read twice), and at least 4096
+// Backward: a piece's d is at most 256 MB (it is written once and read twice), but at least 4096
 // columns, which the products that read it need to be worth their sums' way through memory.
 constexpr int64_t XENT_PIECE_BYTES = int64_t{256} << 20;
 constexpr int XENT_PIECE_MIN = 4096;
@@ -431,7 +431,8 @@ struct XentBwdLayout {
 };
 static XentBwdLayout xent_bwd_layout(const lmoe_linear_xent& p) {
   XentBwdLayout L{};
-  L.piece = XENT_PIECE_BYTES / 2 / p.M / 256 * 256;
+  L.terms = p.M <= XENT_TWO_TERMS ? 2 : 1;
+  L.piece = XENT_PIECE_BYTES / 2 / L.terms / p.M / 256 * 256;
   if (L.piece < XENT_PIECE_MIN) L.piece = XENT_PIECE_MIN;
   if (L.piece > p.V) L.piece = p.V;
   L.ldd = ceil_div(L.piece, 8) * 8;
@@ -441,7 +442,6 @@ static XentBwdLayout xent_bwd_layout(const lmoe_linear_xent& p) {
   if (s > ceil_div(L.piece, BLOCK_K) / 8) s = ceil_div(L.piece, BLOCK_K) / 8;
   if (s > XENT_MAX_SLICES) s = XENT_MAX_SLICES;
   L.slices = s < 1 ? 1 : static_cast<int>(s);
-  L.terms = p.M <= XENT_TWO_TERMS ? 2 : 1;
   L.d = 0;
   L.sum = (static_cast<size_t>(p.M) * L.ldd * 2 * L.terms + 255) / 256 * 256;
   L.rest = L.sum + static_cast<size_t>(L.slices) * p.M * p.K * sizeof(float);

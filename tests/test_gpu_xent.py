@@ -571,3 +571,16 @@ def test_fp32_dw_of_many_rows(dev, M, K):
     all_rows = x.double().sum(0) / V
     bound = (32 * 2.0 ** -23 + (M // 512 + 1) * 2.0 ** -24 + 2.0 ** -23) * (sums + all_rows)
     _within(out["dw"], all_rows - sums, bound, (M, K))
+
+
+@pytest.mark.parametrize("M,V,K", [(300, 447232 + 100, 64), (1000, 200000, 256), (128, (1 << 19) + 70, 8),
+                                   (5, 300001, 16), (129, (1 << 20) + 40, 8)])
+def test_pieces_and_slices(dev, M, V, K):
+    """Vocabularies of several pieces whose dx is summed in slices: a last piece of fewer K-blocks than
+    slices, and (up to 128 rows) two terms of d.  Targets on both sides of the pieces' edges."""
+    head = lmoe.LinearCrossEntropy(_draw(dev, V, K, V + K, 3 * K ** -0.5))
+    x, t = _draw(dev, M, K, M), _targets(dev, M, V, 5)
+    edges = torch.tensor([V - 1, V - 41, 447231, 447232, 134143, 134144, 262144, 524287], device=dev)
+    t[:min(M, 8)] = edges[:M].clamp(max=V - 1)
+    _, lse = _check_forward(head, x, t, (M, V, K))
+    _check_backward(head, x, t, lse, _weights_of_rows(dev, M, 9), (M, V, K))

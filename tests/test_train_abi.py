@@ -121,6 +121,25 @@ def test_xent_workspaces(lib):
     assert b(M=1, V=1 << 18, K=7168, ldx=7168, ldw=7168) <= 4 * (1 << 18) + 64 * 7168 * 4
 
 
+@pytest.mark.parametrize("M,V,K", [(1, 1 << 28, 8), (16, 1 << 24, 8), (128, 1 << 20, 8),
+                                   (128, 1 << 20, 7168), (129, 1 << 21, 64), (4096, 1 << 17, 7168),
+                                   (40000, 1 << 17, 64)])
+def test_xent_backward_workspace_is_what_the_header_says(lib, M, V, K):
+    """d of a piece of the vocabulary in at most 256 MB, or of 4096 tokens, in as many terms as it has;
+    up to 32 copies of dx in fp32 while its tiles of 128 x 256 are fewer than 152; vectors."""
+    b = lib.lmoe_linear_xent_backward_workspace_bytes(ctypes.byref(_xent(M=M, V=V, K=K, ldx=K, ldw=K)))
+    copies = max(1, min(32, 152 // (-(-M // 128) * -(-K // 256))))
+    assert b <= max(256 << 20, 2 * M * 4096) + copies * 4 * M * K + 4 * M + 1024
+
+
+def test_muon_workspace_is_what_the_header_says(lib):
+    for n, r, c in ((3, 5000, 1), (3, 1, 5000), (2, 70, 129), (1, 4097, 333)):
+        eight = lambda v: -(-v // 8) * 8
+        side = min(r, c)
+        q = lib.lmoe_muon_workspace_bytes(ctypes.byref(_muon(batch=n, rows=r, cols=c)))
+        assert q <= n * (6 * r * eight(c) + 4 * side * eight(side) + 8 * eight(side)) + (1 << 16)
+
+
 @no_gpu
 def test_xent_without_a_description(lib):
     assert lib.lmoe_linear_xent_forward(None, None, 0, None) == ARG
