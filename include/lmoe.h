@@ -618,8 +618,9 @@ int lmoe_linear_xent_forward(const lmoe_linear_xent *p, void *ws, size_t ws_byte
 /* Its gradients, from dloss [M] fp32, the gradient of each row's loss (1 / rows for their mean), and
  * the forward's lse; loss is not read:
  *   d = dloss (exp(l - lse) - onehot(target)), rounded to bf16 as the products' operand (two bf16
- *   terms up to 128 rows; beyond, dx takes the target's element unrounded) in units of the rows'
- *   dloss, so that a weight that all rows share is not rounded;
+ *   terms up to 128 rows; beyond, dx takes the target's element unrounded, others, such as that of a
+ *   token that is wrongly taken for certain, as rounded) in units of the rows' dloss, so that a weight
+ *   that all rows share is not rounded;
  *   dx [M, K] bf16 = d . w, rows lddx elements apart;  dw [V, K] = d^T . x, dw_type LMOE_BF16 or
  *   LMOE_F32 (the sum over the rows without a second rounding, added up in fp32).
  * Either may be NULL (not wanted).  The logits are computed again, bit for bit as by the forward (of

@@ -183,12 +183,14 @@ xent_prepare_kernel(XentTarget target, const float* dloss, int M, float* unit, c
 }
 
 // d of a piece of the vocabulary, from column `col0` on, as bf16.
-// Of a row's d the target's element is by far the largest, and its rounding, up to 2^-8 of it, goes
-// into all of that row's dx and of the target's row of dw.  Over many rows such errors are as large as
-// the results' own rounding in the norm, over few rows up to twice that.  So up to XENT_TWO_TERMS rows,
-// where the head's way from HBM is the time in any case, d is two terms (2^-17); beyond, `rest` keeps
-// what the target's element lost, and dx gets that times the target's weights.  (Two terms for 300 rows:
-// 116 -> 160 us, dw 2.4e-3 -> 1.7e-3 off in the norm, the part of its own rounding.)
+// Unless the model is sure of another token, the target's element is by far the largest of a row's d, and its
+// rounding, up to 2^-8 of it, goes into all of that row's dx and of the target's row of dw.  Over many rows
+// such errors are as large as the results' own rounding in the norm, over few rows up to twice that.  So up
+// to XENT_TWO_TERMS rows, where the head's way from HBM is the time in any case, d is two terms (2^-17);
+// beyond, `rest` keeps what the target's element lost, and dx gets that times the target's weights.  (Two terms
+// for 300 rows: 116 -> 160 us, dw 2.4e-3 -> 1.7e-3 off in the norm, the part of its own rounding.)  A token that
+// the model is wrongly sure of has an element as large as the target's, whose rounding stays in dx: with p near 1
+// 1.2e-3 of it in the norm, where dx's own rounding is 1.7e-3.
 // A mean's rows all have one weight, and with it would all be off by the same part, in one direction.
 // So d is kept in units of the weights' mantissa (xent_prepare_kernel), which the results are multiplied
 // by: the targets' elements, -1 for the most part, are then exact.

@@ -584,3 +584,37 @@ def test_pieces_and_slices(dev, M, V, K):
     t[:min(M, 8)] = edges[:M].clamp(max=V - 1)
     _, lse = _check_forward(head, x, t, (M, V, K))
     _check_backward(head, x, t, lse, _weights_of_rows(dev, M, 9), (M, V, K))
+
+
+def test_gradients_of_rows_that_are_not_finite(dev):
+    """Each row's infinities and NaN stay in its own dx; dw, which sums over the rows, is NaN as the formulas
+    give it."""
+    M, V, K = 140, 700, 64
+    w = _draw(dev, V, K, 1, 0.2)
+    w[:, 0] = 1.0
+    x, t = _draw(dev, M, K, 2), _targets(dev, M, V, 3, ignored=0.0)
+    head, g = lmoe.LinearCrossEntropy(w), _weights_of_rows(dev, M, 4)
+    for rows in (M, 100):
+        x0, t0, g0 = x[:rows], t[:rows], g[:rows]
+        clean = head.backward(x0, t0, head.forward(x0, t0)[1], g0)
+        xx = x0.clone()
+        xx[5, 3], xx[6, 0], xx[7, 0] = float("nan"), float("inf"), float("-inf")
+        out = head.backward(xx, t0, head.forward(xx, t0)[1], g0)
+        others = [i for i in range(rows) if i not in (5, 6, 7)]
+        assert torch.equal(out["dx"][others], clean["dx"][others])
+        assert torch.isnan(out["dx"][5:8]).all() and torch.isnan(out["dw"]).all()
+
+
+@pytest.mark.parametrize("M", [100, 129, 700])
+def test_certain_of_a_wrong_token(dev, M):
+    """The element of the token that has the probability is then as large as the target's; its rounding to
+    bf16 counts in dx (beyond 128 rows) as the bounds say."""
+    V, K = 900, 512
+    x = _draw(dev, M, K, 2)
+    w = _draw(dev, V, K, 1, 0.02)
+    sure = torch.arange(M, device=dev)
+    w[sure] = (12 / K * x.float()).to(BF)
+    head, t = lmoe.LinearCrossEntropy(w), (sure + 7) % V
+    _, lse = _check_forward(head, x, t, M)
+    for dw in (torch.float32, BF):
+        _check_backward(head, x, t, lse, _weights_of_rows(dev, M, 4), M, dw_dtype=dw)
