@@ -673,15 +673,20 @@ typedef struct lmoe_muon {
 } lmoe_muon;
 
 /* ws: lmoe_muon_workspace_bytes(p) of device scratch, 16-byte aligned (6 bytes for each element of the
- * batch and 4 for each of its matrices' smaller side squared, columns rounded up to 8).  Any rows and cols and any alignment to
- * the element size; multiples of 8 columns in whole 16 bytes are read faster.  A size of 0 is a no-op.
- * Arithmetic: products of fp16 operands with fp32 sums, X as two fp16 terms and the diagonals of A and
- * of b A + c A^2 in fp32 beside them, the norm's sum of squares with the roundings' rests beside it; X
- * comes out within 1e-3 of itself or so (in the norm, against the formulas in 64 bits; up to 1.3e-2
- * where the roundings of a few elements, or of equal ones, do not average out), before its rounding to
- * bf16.  The iterates must keep to fp16's
- * range: singular values of X up to 8 (from 1 at the start) and entries of b A + c A^2 up to
- * 255 are safe.  A matrix that is not finite gives NaN, in its own place in the batch only.
+ * batch and 4 for each of its matrices' smaller side squared, columns rounded up to 8).  Any rows and cols
+ * and any alignment to the element size; multiples of 8 columns in whole 16 bytes are read faster.  A size
+ * of 0 is a no-op.
+ * Arithmetic: products of fp16 operands with fp32 sums, X as two fp16 terms and the diagonals of A and of
+ * b A + c A^2 in fp32 beside them, the norm's sum of squares with the roundings' rests beside it.
+ * After five steps of Muon's coefficients X is within 1e-3 of itself or so (in the norm, against the
+ * formulas in 64 bits; up to 1.3e-2 where the roundings of a few elements, or of equal ones, do not
+ * average out), before its rounding to bf16.  These steps do not contract near 1, so that more of them add
+ * to it: 3e-3 after eight, 5e-3 after twelve, for a well-conditioned U; 14 of (1.5, -0.5, 0), which do,
+ * 4e-4. Steps with a > 1 grow what is small by a each: from some ten of Muon's on, the roundings of a U of
+ * low rank have become singular values of X of their own, as they would in fp32.
+ * The iterates must keep to fp16's range: singular values of X up to 8 (from 1 at the start) and entries
+ * of b A + c A^2 up to 255 are safe.  A matrix that is not finite gives NaN, in its own place in the batch
+ * only.
  * Outputs overlap no input, nor each other (out may be grad).
  * Errors: INVALID_ARG (also coeffs, eps or rates that are not finite), UNSUPPORTED (rows or cols above
  * 2^20, rows cols above 2^32, batch above 65535), WORKSPACE_TOO_SMALL, CUDA. */

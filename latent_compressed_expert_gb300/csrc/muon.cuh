@@ -9,9 +9,10 @@
 
 namespace lmoe {
 
-// Scales of the fp16 operands, powers of two: X up to 2^4 and A and B up to 2^6 and 2^7 in magnitude fit,
-// and what is 2^-25 of 1 or more in X, 2^-24 in A, keeps all its bits.  (X's second term, down to 2^-12 of
-// the first, needs no scale of its own then.)
+// Scales of the fp16 operands (65504 at most), powers of two: X below 2^5 in magnitude fits, A below 2^6 and B
+// below 2^8 off their diagonals, which are kept apart in fp32.  (Singular values of X up to 8 make A's
+// eigenvalues 0 .. 64, and entries off the diagonal half of that at most: 32.)  What is 2^-25 of 1 or more in X,
+// 2^-24 in A, keeps all its bits.  (X's second term, down to 2^-12 of the first, needs no scale of its own then.)
 constexpr float X_SCALE = 2048.0f, A_SCALE = 1024.0f, B_SCALE = 256.0f;
 constexpr int EXACT_STEPS = 2;  // the last ones, in which B's diagonal takes X itself
 

@@ -238,9 +238,9 @@ __device__ __forceinline__ void tile_mma(uint32_t d, uint32_t sp, uint32_t idesc
 //   SHORT   reductions of at most this many K-blocks give an epilogue warp two buffers: a chunk else
 //           waits for the tensor store of the one before it to have read the buffer.  The second one
 //           costs a stage.
-// PARTS: the reduction is longer than that.  (The epilogue's code stands there once for each chunk in registers,
-// which reductions without parts need not pay for: gradients of 300 x 50257 x 1024 with an fp32 dw took 151 us
-// in one kernel for both, 141 so.)
+// PARTS: the reduction is longer than that.  (The epilogue's code stands there once for each chunk in
+// registers, which reductions without parts need not pay for: gradients of 300 x 50257 x 1024 with an fp32 dw
+// took 151 us in one kernel for both, 141 so.)
 template <bool PAIR, bool P_MN, bool Q_MN, bool F16, bool PARTS, class Epi>
 __global__ void __launch_bounds__(LINEAR_THREADS, 1)
 tile_kernel(const __grid_constant__ TileMaps maps, const TileArgs g, const Epi epi) {

@@ -354,3 +354,27 @@ def test_stalled_wait_is_reported(dev, monkeypatch, shape):
     assert torch.equal(m.orthogonalize(g), want)
     torch.cuda.synchronize()
     assert m.device_error() == lmoe.LMOE_OK
+
+
+@pytest.mark.parametrize("steps,coeffs,worst", [(5, MUON, 1e-3), (8, MUON, 3e-3), (12, MUON, 5e-3),
+                                                (14, (1.5, -0.5, 0.0), 4e-4)])
+def test_accuracy_that_the_header_names(dev, steps, coeffs, worst):
+    """Well-conditioned matrices (their smaller side's singular values within a factor of ten), by either
+    form, tall and wide.  "Or so" is a quarter."""
+    m = lmoe.Muon(steps=steps, coeffs=coeffs)
+    for rows, cols in ((96, 160), (160, 96), (128, 1024), (512, 768), (1000, 333)):
+        g = _draw(dev, rows, cols, seed=steps + rows)
+        _check(m.orthogonalize(g), g, coeffs, steps, tag=(steps, rows, cols), worst=1.25 * worst)
+
+
+@pytest.mark.parametrize("rows,cols", [(2, 16), (16, 2), (200, 300), (300, 200)])
+def test_singular_values_up_to_eight(dev, rows, cols):
+    """What the header calls safe: one singular value, brought to 8, of two equal rows (or columns), where A
+    has 32 off its diagonal, and by 8 (1 - 1/2 + 1/4) to 6."""
+    coeffs = [(8.0, 0.0, 0.0), (1.0, -1 / 128, 1 / 16384)]
+    m = lmoe.Muon(steps=2, coeffs=coeffs)
+    g = torch.zeros(rows, cols, device=dev)
+    (g if rows < cols else g.mT)[:2] = _draw(dev, 1, max(rows, cols), seed=rows)
+    out = m.orthogonalize(g)
+    _check(out, g, coeffs, 2, tag=(rows, cols), worst=1.3e-2)
+    assert abs(float(_norm(out)) - 6) <= 6 * (HALF + 1.3e-2)
