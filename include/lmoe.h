@@ -668,7 +668,7 @@ typedef struct lmoe_muon {
   long long ldw, w_stride;
   float *master;           /* fp32, in and out, or NULL */
   long long ldmaster, master_stride;
-  float rate, weight_decay, scale;
+  float rate, weight_decay, scale;  /* as beta, part of the call: a captured one replays them as they were */
   uint32_t *dev_flag;      /* as in lmoe_linear */
 } lmoe_muon;
 

@@ -388,8 +388,9 @@ constexpr TileEpilogue EXP_EPILOGUE{500.0, 24.0, 8}, SUM_EPILOGUE{500.0, 11.0, 8
     STORE_EPILOGUE{500.0, 11.0, 16};
 
 // Up to 128 rows the head's way from HBM is the time: tiles of 128 rows, of as many columns as
-// deals the vocabulary evenly to the SMs.  From XENT_MANY rows on SM pairs are always the best, and the
-// parts of a row are those of 256 columns.
+// deals the vocabulary evenly to the SMs.  Beyond XENT_MANY rows SM pairs, whose parts, of 256 columns, take a
+// quarter of the scratch that tiles of 64 might need (16384 rows over 2^18 tokens: 268 MB).  Vocabularies of
+// a few tiles would be quicker on single SMs (1100 x 1000 x 7168: 31 us by tile_plan's estimate against 45).
 constexpr int XENT_MANY = 1024;
 static TilePlan lse_plan(int64_t M, int64_t V, int64_t K, int sms) {
   if (M > XENT_MANY) return {true, 256, 1, 0.0};
@@ -414,7 +415,8 @@ struct XentLayout {
 // The parts are those of the narrowest tiles that the plan may take.
 static XentLayout xent_layout(const lmoe_linear_xent& p) {
   XentLayout L{};
-  L.picked = (static_cast<size_t>(ceil_div(p.V, p.M > XENT_MANY ? 256 : 64)) * 2 * p.M * sizeof(float2) + 255) / 256 * 256;
+  const int64_t tiles = ceil_div(p.V, p.M > XENT_MANY ? 256 : 64);
+  L.picked = (static_cast<size_t>(tiles) * 2 * p.M * sizeof(float2) + 255) / 256 * 256;
   L.total = L.picked + static_cast<size_t>(p.M) * sizeof(float);
   return L;
 }

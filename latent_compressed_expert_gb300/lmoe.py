@@ -912,7 +912,8 @@ class Muon:
         """One step, in place: momentum (fp32) = beta momentum + grad, then
         w = w (1 - rate weight_decay) - rate scale X, X the orthogonalisation of grad + beta momentum
         (or of momentum, without nesterov).  w is bf16; with an fp32 ``master`` that is what is updated,
-        and w, or None, receives its rounding."""
+        and w, or None, receives its rounding.  Rate and scale are numbers of the call: a graph that has
+        captured it replays them, and is captured anew where a schedule changes them."""
         if stream is not None:
             with torch.cuda.stream(stream):
                 return self.update(w, grad, momentum, rate, scale, master)
