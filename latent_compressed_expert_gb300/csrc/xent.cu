@@ -7,13 +7,14 @@
 // Backward: for one piece of the vocabulary after the other the logits are computed again, d goes
 // to scratch as bf16, and both products read it there.
 // What bounds them (times with inputs past L2; HBM and tensor rates of measured peaks):
-//   up to 128 rows the head's way from HBM: 1 row x 131072 tokens x 7168 279-288 us (6.5-6.7 TB/s,
-//   0.96-0.99), 77 x 32003 x 3584 43 us (0.78: 143 tiles for 152 SMs, and 8 us of launch, first load
+//   up to 128 rows the head's way from HBM: 1 row x 131072 tokens x 7168 279-289 us (6.5-6.7 TB/s,
+//   0.96-0.99), 77 x 32003 x 3584 43-45 us (0.75-0.78: 143 tiles for 152 SMs, and 8 us of launch, first load
 //   and join);
-//   from some hundred rows on the tensor cores: 4096 x 65536 x 7168 forward 2.27-2.39 ms (0.83-0.87 of
-//   the burst rate, 0.94-0.99 of the sustained one), backward 6.79-7.12 ms (0.83-0.87);
-//   between, rows that fill part of a tile: 300 x 50257 x 1024 backward 117-121 us, of which the products
-//   on whole tiles of 384 and 512 rows are 36 + 35 + 41 (profiled one by one).
+//   from some hundred rows on the tensor cores: 4096 x 65536 x 7168 forward 2.22-2.42 ms (0.82-0.89 of
+//   the burst rate), backward 6.86-7.09 ms (0.83-0.86; with an fp32 dw 7.05-7.16);
+//   between, rows that fill part of a tile: 300 x 50257 x 1024 backward 119-124 us, of which logits and dx,
+//   on three tiles of 128 rows, are 40 + 37, dw, whose tiles' stores take longer than their products, 42 and
+//   what is prepared 6 (profiled one by one).
 #include "tile.cuh"
 
 namespace lmoe {
