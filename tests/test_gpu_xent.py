@@ -618,3 +618,51 @@ def test_certain_of_a_wrong_token(dev, M):
     _, lse = _check_forward(head, x, t, M)
     for dw in (torch.float32, BF):
         _check_backward(head, x, t, lse, _weights_of_rows(dev, M, 4), M, dw_dtype=dw)
+
+
+@pytest.mark.parametrize("M", [1, 128])
+def test_logits_do_not_depend_on_the_tiles(dev, M):
+    """Tiles are as wide as the vocabulary asks for, and the backward's pieces have widths of their own.  With
+    all other tokens' probability 0, lse is the remaining token's logit, to the last bit."""
+    K = 7168
+    x = _draw(dev, M, K, 2)
+    x[:, 0] = 3e4
+    one = _draw(dev, 1, K, 3, 5 * K ** -0.5)
+    one[:, 0] = 0.0
+    want = None
+    for V in (1, 70, 4000, 12000, 22000, 40000):  # 64 to 256 columns
+        for at in (0, V // 2, V - 1):
+            w = torch.zeros(V, K, dtype=BF, device=dev)
+            w[:, 0] = -3e4
+            w[at] = one
+            _, lse = lmoe.LinearCrossEntropy(w).forward(x, torch.full((M,), at, device=dev))
+            want = lse if want is None else want
+            assert torch.equal(lse, want), (V, at)
+    l, e = _logits(x, one)
+    _within(want, l.squeeze(1), e.squeeze(1), "logit")
+
+
+@pytest.mark.parametrize("M", [40, 300])
+@pytest.mark.parametrize("parts", ["both", "dx", "dw"])
+def test_rows_of_dx_at_a_distance(dev, M, parts):
+    """Through the C entry: dx with gaps between its rows, which stay as they were, and rows behind the last."""
+    V, K, ld = 700, 72, 104
+    head = lmoe.LinearCrossEntropy(_draw(dev, V, K, 1, 0.2))
+    x, t, g = _draw(dev, M, K, 2, ld=K + 16), _targets(dev, M, V, 3), _weights_of_rows(dev, M, 4)
+    _, lse = head.forward(x, t)
+    want = head.backward(x, t, lse, g)
+    dx = torch.full((M + 2, ld), 7.0, dtype=BF, device=dev)
+    dw = torch.full((V + 2, K), 7.0, device=dev)
+    lib, d = lmoe.load(), head._desc(x, t, None, lse.data_ptr())
+    nb = lib.lmoe_linear_xent_backward_workspace_bytes(d)
+    ws = torch.full((nb + 256,), 0xA5, dtype=torch.uint8, device=dev)
+    rc = lib.lmoe_linear_xent_backward(
+        d, g.data_ptr(), None if parts == "dw" else dx.data_ptr(), ld,
+        None if parts == "dx" else dw.data_ptr(), lmoe.F32, ws.data_ptr(), nb,
+        torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert rc == lmoe.LMOE_OK and head.device_error() == lmoe.LMOE_OK
+    assert (ws[nb:] == 0xA5).all() and (dx[:, K:] == 7).all() and (dx[M:] == 7).all()
+    assert (dw[V:] == 7).all()
+    assert torch.equal(dx[:M, :K], want["dx"]) if parts != "dw" else (dx == 7).all()
+    assert torch.equal(dw[:V], want["dw"]) if parts != "dx" else (dw == 7).all()
